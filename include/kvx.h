@@ -36,6 +36,17 @@
  *                    TransferEngine API ("RDMA point-to-point communication
  *                    for LLM systems", Perplexity)
  *
+ * and what a decoding server does with the pages next, over the same pool and
+ * address table:
+ *
+ *   kvx_append_tokens  new tokens' queries and keys normed and rotated, keys
+ *                    and values written into their pages, in one pass
+ *   kvx_attend       attention of one new token per sequence over its pages,
+ *                    with a sliding window and sinks, and the attention
+ *                    weights added up per token
+ *   kvx_evict        the tokens of a sequence with the most added-up weight
+ *                    chosen and copied into fresh pages
+ *
  * Conventions for every call:
  *   - Array arguments are DEVICE pointers, allocated and owned by the caller.
  *     The library allocates nothing; scratch memory is the caller's `ws`
@@ -105,6 +116,7 @@ typedef enum kvx_status {
 #define KVX_S_CAPACITY   512u  /* a plan output exceeds its capacity, or the slab 2^63 bytes */
 #define KVX_S_TIMEOUT    1024u /* a copy kernel's bounded wait on its own bulk copy gave up
                                   (the GPU did not deliver the bytes; the copy is incomplete) */
+#define KVX_S_ALIGN      2048u /* a cache segment's address is no multiple of 16 bytes */
 
 /* READ splitting: planned descriptors are split into pieces of at most
  * MAX_RDMA_READ_BYTES = 32 MiB. */
@@ -511,6 +523,177 @@ kvx_status kvx_pack_noalloc(const uint8_t *pool, uint64_t pool_bytes,
                             const kvx_desc *descs, const uint64_t *num_descs,
                             uint64_t desc_capacity, uint8_t *slab, uint64_t slab_bytes,
                             uint32_t *status, void *stream);
+
+/* ------------------------------------------------- the cache's operators */
+
+/* Element types of the cache operators. */
+#define KVX_F32  0u
+#define KVX_BF16 1u
+#define KVX_F16  2u
+#define KVX_E4M3 3u /* 8 bits, finite (largest value 448), stored as value / scale */
+
+/*
+ * One layer's paged cache inside a pool, as the transfer lays it out: block b
+ * holds page_tokens tokens, and head h's K and V segments of block b start at
+ * byte addr[b*L + first_lane + 2*h] and addr[b*L + first_lane + 2*h + 1] of
+ * the pool, wherever those are.  Token i of a segment is dim elements at
+ * byte i * token_stride (dim * element size when a head's tokens lie
+ * together; heads times that when a token's heads do).  A host struct, read
+ * during the call; pool and addr are device pointers.
+ *
+ * Rules (else KVX_EINVAL): dim a multiple of 16, at most 256; dtype KVX_BF16,
+ * KVX_F16 or KVX_E4M3; page_tokens, heads, B > 0; the lanes first_lane ..
+ * first_lane + 2*heads - 1 within L; token_stride a multiple of 16 bytes and
+ * at least a row; pool 16-byte aligned; k_scale and v_scale (the values that a
+ * stored 1 stands for) finite and > 0, and 1 unless dtype is KVX_E4M3.
+ * On the device: a segment whose address is not a multiple of 16 raises
+ * KVX_S_ALIGN, one that leaves the pool (all page_tokens rows of it counted)
+ * or whose block id is >= B raises KVX_S_BOUNDS; it is neither read nor
+ * written.
+ */
+typedef struct kvx_cache {
+    uint8_t *pool;
+    uint64_t pool_bytes;
+    const uint64_t *addr;  /* [B][L] */
+    uint32_t B, L;
+    uint32_t first_lane;   /* lane of head 0's K */
+    uint32_t heads;
+    uint32_t dim;
+    uint32_t dtype;
+    uint32_t page_tokens;
+    uint32_t reserved;     /* 0 */
+    uint64_t token_stride; /* bytes */
+    float k_scale, v_scale;
+} kvx_cache;
+
+/*
+ * Append T new tokens: norm and rotate their queries and keys, write the
+ * queries to q_out and keys and values into their places in the cache.  For
+ * each token t and each head x of q (or k), with weight w:
+ *     y = x / sqrt(mean(x^2) + eps) * w          (y = x where w is NULL)
+ * and, with (c, s) = cos_sin[positions[t]], the first rot_dim values of y are
+ * rotated in pairs (y_a, y_b) -> (y_a c_i - y_b s_i, y_b c_i + y_a s_i),
+ * i < rot_dim / 2: a = i and b = i + rot_dim/2, or with interleaved != 0
+ * a = 2i and b = 2i + 1.  Everything is computed in 32 bits and rounded once,
+ * to the nearest even; KVX_E4M3 stores value / scale and limits it to +-448
+ * (a NaN stays NaN).
+ *
+ *   q, k, v        [T][q_heads|heads|heads][dim] of `dtype` (KVX_BF16 or
+ *                  KVX_F16; the cache's type is the same one or KVX_E4M3); a
+ *                  token's heads are contiguous, tokens q_stride, k_stride,
+ *                  v_stride elements apart (parts of one projection's output).
+ *   q_weight, k_weight  [dim] of `dtype`, or NULL.
+ *   cos_sin        [max_pos][rot_dim] float: rot_dim/2 cosines, then as many
+ *                  sines; rot_dim a multiple of 16, at most dim, or 0 for no
+ *                  rotation (cos_sin and positions are then not read).
+ *   positions      [T] uint32; one >= max_pos raises KVX_S_BOUNDS and the
+ *                  token is left out.
+ *   slots          [T] int64: block * page_tokens + place in the block.  A
+ *                  negative slot writes nothing into the cache (its query is
+ *                  computed all the same); one beyond the cache's blocks
+ *                  raises KVX_S_BOUNDS likewise.  Two tokens with the same
+ *                  slot leave either one's bytes.
+ *   q_out          [T][q_heads][dim] of `dtype`, tokens q_out_stride elements
+ *                  apart.  It may be q itself (with the same stride).
+ * Pointers and strides of q, k, v, q_out, the weights and cos_sin keep 16-byte
+ * alignment (else KVX_EINVAL).  One launch; T == 0 enqueues nothing.
+ */
+kvx_status kvx_append_tokens(const kvx_cache *cache, const void *q,
+                             uint64_t q_stride, const void *k,
+                             uint64_t k_stride, const void *v,
+                             uint64_t v_stride, uint32_t dtype, uint32_t T,
+                             uint32_t q_heads, const void *q_weight,
+                             const void *k_weight, float eps,
+                             const float *cos_sin, uint32_t rot_dim,
+                             uint32_t max_pos, uint32_t interleaved,
+                             const uint32_t *positions, const int64_t *slots,
+                             void *q_out, uint64_t q_out_stride,
+                             uint32_t *status, void *stream);
+
+/* Scratch of kvx_attend; 0 for arguments it refuses.  with_scores: whether
+ * scores will be passed. */
+size_t kvx_attend_workspace_size(const kvx_cache *cache, uint32_t num_seqs,
+                                 uint32_t q_heads, uint32_t blocks_per_seq,
+                                 uint32_t window, uint32_t sinks,
+                                 uint32_t with_scores);
+
+/*
+ * Attention of one new token per sequence over its cached tokens.  Sequence n
+ * has lens[n] tokens, token j in block blocks[n][j / page_tokens].  Visible are
+ * j < lens[n] with window == 0, or j >= lens[n] - window, or j < sinks.  For query
+ * head x of KV head h (q_heads / heads consecutive ones share a KV head):
+ *     logit_j = scale * q . k_j,  lse = log(sum_j exp(logit_j)),
+ *     out = sum_j exp(logit_j - lse) v_j
+ * over the visible tokens.  A sequence without any (lens[n] == 0), like a head
+ * whose logits are all -infinity, gets zeros and lse = -infinity.
+ * Logits, softmax and sums are held in 32 bits; the weights that multiply V
+ * go into the tensor cores as the sum of two 16-bit values.
+ *
+ *   q              [num_seqs][q_heads][dim] of `dtype` (KVX_BF16 or KVX_F16;
+ *                  the cache's type is the same one or KVX_E4M3), sequences
+ *                  q_stride elements apart, 16-byte aligned as in
+ *                  kvx_append_tokens.  q_heads a multiple of heads, at most
+ *                  128 per KV head.
+ *   blocks         [num_seqs][blocks_per_seq] uint32; blocks_per_seq *
+ *                  page_tokens < 2^31.  Entries of pages that hold no visible
+ *                  token are not read.
+ *   lens           [num_seqs] uint32; one that exceeds its pages raises
+ *                  KVX_S_BOUNDS and counts as full pages.
+ *   out            [num_seqs][q_heads][dim] of `dtype`, out_stride apart.
+ *   lse            [num_seqs][q_heads] float (natural logarithm), or NULL.
+ *   scores         [num_seqs][heads][scores_stride] float, or NULL: the sum
+ *                  over the KV head's query heads of exp(logit_j - lse) is
+ *                  added to element j of every visible token, in a fixed
+ *                  order.  scores_stride >= blocks_per_seq * page_tokens.
+ * Results depend on nothing but the arguments and the device's SM count: no
+ * atomics.  One launch, or two where a sequence may be split or scores are
+ * added; num_seqs == 0 enqueues nothing.
+ */
+kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t q_stride,
+                      uint32_t dtype, uint32_t num_seqs, uint32_t q_heads,
+                      const uint32_t *blocks, uint32_t blocks_per_seq,
+                      const uint32_t *lens, float scale, uint32_t window,
+                      uint32_t sinks, void *out, uint64_t out_stride,
+                      float *lse, float *scores, uint64_t scores_stride,
+                      uint32_t *status, void *ws, size_t ws_bytes,
+                      void *stream);
+
+/* Scratch of kvx_evict; 0 for arguments it refuses. */
+size_t kvx_evict_workspace_size(const kvx_cache *cache, uint32_t num_seqs,
+                                uint32_t blocks_per_seq, uint32_t budget);
+
+/*
+ * Cut every sequence to at most `budget` tokens per KV head, by its scores
+ * (kvx_attend's).  A sequence of n = lens[s] <= budget tokens is kept whole.
+ * Of a longer one each head keeps its first S = min(sinks, budget) tokens, its
+ * last R = min(recent, budget - S), and of the others the budget - S - R
+ * with the highest scores; of equal scores the token at the lower index, and a
+ * NaN counts as -infinity.  The kept tokens' K and V rows are copied, in
+ * their order, to tokens 0, 1, ... of the sequence's pages dst_blocks[s],
+ * which must be none of the blocks read here (the pages read may be shared
+ * with other sequences, and stay as they are).
+ *
+ *   blocks, blocks_per_seq, lens  as for kvx_attend.
+ *   scores         [num_seqs][heads][scores_stride] float, scores_stride >=
+ *                  blocks_per_seq * page_tokens.
+ *   dst_blocks     [num_seqs][dst_per_seq] uint32, dst_per_seq *
+ *                  page_tokens >= budget.
+ *   kept           [num_seqs][heads][budget] uint32 out: the kept tokens'
+ *                  indices, ascending; 0xFFFFFFFF after the last.
+ *   kept_scores    [num_seqs][heads][budget] float out: their scores; 0 after
+ *                  the last.
+ *   new_lens       [num_seqs] uint32 out: min(lens[s], budget).
+ * Rows are copied as stored, whatever the type.  num_seqs == 0 enqueues
+ * nothing; budget == 0 is refused (KVX_EINVAL).
+ */
+kvx_status kvx_evict(const kvx_cache *cache, uint32_t num_seqs,
+                     const uint32_t *blocks, uint32_t blocks_per_seq,
+                     const uint32_t *lens, const float *scores,
+                     uint64_t scores_stride, uint32_t budget, uint32_t sinks,
+                     uint32_t recent, const uint32_t *dst_blocks,
+                     uint32_t dst_per_seq, uint32_t *kept, float *kept_scores,
+                     uint32_t *new_lens, uint32_t *status, void *ws,
+                     size_t ws_bytes, void *stream);
 
 /*
  * Diagnostic, no counterpart in the paper: shows that the library's bounded

@@ -1,0 +1,4 @@
+// kvx_attend for f16 queries over an e4m3 cache.
+#include "kvx_attend.cuh"
+
+template bool kvx::attend::launch<__half, 1>(const kvx::attend::Args &, uint32_t, uint32_t, cudaStream_t);

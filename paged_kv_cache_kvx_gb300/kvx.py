@@ -8,6 +8,8 @@ There is no fallback: if the library is missing, loading raises.
 ``Transfer`` bundles the buffers of one block-prefix transfer (allocated with
 torch, sized from the library's capacity and workspace queries) and runs the
 five calls in order on one stream, with no host synchronisation in between.
+``Cache`` describes one layer's paged cache in a pool and runs the operators
+that a decoding server applies to it: append, attend, evict.
 """
 from __future__ import annotations
 
@@ -29,6 +31,8 @@ assert GROUP_DTYPE.itemsize == 48 and DESC_DTYPE.itemsize == 32
 KVX_OK, KVX_EINVAL, KVX_ECAPACITY, KVX_ECUDA = 0, 1, 3, 4
 S_LANES, S_ARRAYS, S_COVERAGE, S_ZERO_COUNT, S_ZERO_LEN = 1, 2, 4, 8, 16
 S_SPAN, S_STRIDE1, S_BOUNDS, S_DESC, S_CAPACITY, S_TIMEOUT = 32, 64, 128, 256, 512, 1024
+S_ALIGN = 2048
+KVX_F32, KVX_BF16, KVX_F16, KVX_E4M3 = 0, 1, 2, 3
 MAX_READ_BYTES = 32 * 1024 * 1024
 
 _ERR = {KVX_EINVAL: "KVX_EINVAL", KVX_ECAPACITY: "KVX_ECAPACITY", KVX_ECUDA: "KVX_ECUDA"}
@@ -38,6 +42,17 @@ _P = ctypes.c_void_p
 _U32 = ctypes.c_uint32
 _U64 = ctypes.c_uint64
 _SZ = ctypes.c_size_t
+_F = ctypes.c_float
+
+
+class CacheStruct(ctypes.Structure):
+    """struct kvx_cache (include/kvx.h)"""
+    _fields_ = [("pool", _P), ("pool_bytes", _U64), ("addr", _P), ("B", _U32), ("L", _U32), ("first_lane", _U32),
+                ("heads", _U32), ("dim", _U32), ("dtype", _U32), ("page_tokens", _U32), ("reserved", _U32),
+                ("token_stride", _U64), ("k_scale", _F), ("v_scale", _F)]
+
+
+assert ctypes.sizeof(CacheStruct) == 72
 
 _SIGS = {
     "kvx_run_capacity": (_U64, [_U32, _U32]),
@@ -65,6 +80,14 @@ _SIGS = {
                                        _U64, _P, _P, _U64, _P, _P, _SZ, _P]),
     "kvx_paged_writes": (ctypes.c_int, [_U64, _P, _U64, _P, _U64, _U64, _P, _U64, _P, _U64, _U64,
                                         _U64, _P, _P, _SZ, _P]),
+    "kvx_append_tokens": (ctypes.c_int, [_P, _P, _U64, _P, _U64, _P, _U64, _U32, _U32, _U32, _P, _P, _F, _P, _U32,
+                                         _U32, _U32, _P, _P, _P, _U64, _P, _P]),
+    "kvx_attend_workspace_size": (_SZ, [_P, _U32, _U32, _U32, _U32, _U32, _U32]),
+    "kvx_attend": (ctypes.c_int, [_P, _P, _U64, _U32, _U32, _U32, _P, _U32, _P, _F, _U32, _U32, _P, _U64, _P, _P,
+                                  _U64, _P, _P, _SZ, _P]),
+    "kvx_evict_workspace_size": (_SZ, [_P, _U32, _U32, _U32]),
+    "kvx_evict": (ctypes.c_int, [_P, _U32, _P, _U32, _P, _P, _U64, _U32, _U32, _U32, _P, _U32, _P, _P, _P, _P, _P,
+                                 _SZ, _P]),
     "kvx_selftest_timeouts": (ctypes.c_int, [_P, _P]),
     "kvx_launch_count": (_U64, []),
     "kvx_version": (_U32, []),
@@ -259,6 +282,41 @@ def kvx_paged_writes(page_len, src, src_bytes, src_indices, src_stride, src_offs
                                   dst_offset, num_pages, _ptr(status), _ptr(ws),
                                   0 if ws is None else ws.numel(), _stream(stream)),
            "kvx_paged_writes")
+
+
+def kvx_append_tokens(cache, q, q_stride, k, k_stride, v, v_stride, dtype, T, q_heads, q_weight, k_weight, eps, cos_sin,
+                      rot_dim, max_pos, interleaved, positions, slots, q_out, q_out_stride, status, stream=None):
+    """cache: a CacheStruct (by reference, as everywhere below)."""
+    _check(lib().kvx_append_tokens(ctypes.byref(cache), _ptr(q), q_stride, _ptr(k), k_stride, _ptr(v), v_stride, dtype,
+                                   T, q_heads, _ptr(q_weight), _ptr(k_weight), eps, _ptr(cos_sin), rot_dim, max_pos,
+                                   interleaved, _ptr(positions), _ptr(slots), _ptr(q_out), q_out_stride, _ptr(status),
+                                   _stream(stream)), "kvx_append_tokens")
+
+
+def kvx_attend_workspace_size(cache, num_seqs: int, q_heads: int, blocks_per_seq: int, window: int = 0, sinks: int = 0,
+                              with_scores: bool = False) -> int:
+    return int(lib().kvx_attend_workspace_size(ctypes.byref(cache), num_seqs, q_heads, blocks_per_seq, window, sinks,
+                                               int(with_scores)))
+
+
+def kvx_attend(cache, q, q_stride, dtype, num_seqs, q_heads, blocks, blocks_per_seq, lens, scale, window, sinks, out,
+               out_stride, lse, scores, scores_stride, status, ws, stream=None):
+    _check(lib().kvx_attend(ctypes.byref(cache), _ptr(q), q_stride, dtype, num_seqs, q_heads, _ptr(blocks),
+                            blocks_per_seq, _ptr(lens), scale, window, sinks, _ptr(out), out_stride, _ptr(lse),
+                            _ptr(scores), scores_stride, _ptr(status), _ptr(ws), ws.numel(), _stream(stream)),
+           "kvx_attend")
+
+
+def kvx_evict_workspace_size(cache, num_seqs: int, blocks_per_seq: int, budget: int) -> int:
+    return int(lib().kvx_evict_workspace_size(ctypes.byref(cache), num_seqs, blocks_per_seq, budget))
+
+
+def kvx_evict(cache, num_seqs, blocks, blocks_per_seq, lens, scores, scores_stride, budget, sinks, recent, dst_blocks,
+              dst_per_seq, kept, kept_scores, new_lens, status, ws, stream=None):
+    _check(lib().kvx_evict(ctypes.byref(cache), num_seqs, _ptr(blocks), blocks_per_seq, _ptr(lens), _ptr(scores),
+                           scores_stride, budget, sinks, recent, _ptr(dst_blocks), dst_per_seq, _ptr(kept),
+                           _ptr(kept_scores), _ptr(new_lens), _ptr(status), _ptr(ws), ws.numel(), _stream(stream)),
+           "kvx_evict")
 
 
 def kvx_selftest_timeouts(status, stream=None):
@@ -458,6 +516,126 @@ class Transfer:
 
     def read_local(self) -> np.ndarray:
         return _u64_np(self.local)[: self.B * self.L].reshape(self.B, self.L).copy()
+
+
+_DTYPES = {torch.bfloat16: KVX_BF16, torch.float16: KVX_F16, torch.float8_e4m3fn: KVX_E4M3}
+_IDS = (torch.int32, torch.uint32)
+
+
+def _need(ok, what):
+    if not ok:
+        raise KvxError(what)
+
+
+def _heads(t, name, dim, dtype=None):
+    """A [tokens, heads, dim] activation whose tokens' heads are contiguous."""
+    _need(t.dim() == 3 and t.size(2) == dim and (t.numel() == 0 or (t.stride(2) == 1 and (t.size(1) == 1 or
+          t.stride(1) == dim))), "%s: [tokens, heads, %d] with a token's heads contiguous" % (name, dim))
+    _need(t.dtype in (torch.bfloat16, torch.float16) and dtype in (None, t.dtype), "%s: wrong type %s" % (name, t.dtype))
+    # a single token's stride says nothing
+    return t.stride(0) if t.size(0) > 1 else t.size(1) * dim
+
+
+def _table(t, name, dtypes, shape):
+    _need(t.dtype in dtypes and t.is_contiguous() and tuple(t.shape) == tuple(shape),
+          "%s: contiguous %s of %s" % (name, list(shape), " or ".join(str(d) for d in dtypes)))
+
+
+class Cache:
+    """One layer's paged cache in a pool (struct kvx_cache): block b's K and V
+    segments of head h start at the bytes addr[b, first_lane + 2*h] and
+    addr[b, first_lane + 2*h + 1], so the address table of a transfer serves as it is.
+    The object keeps the pool and the table alive and owns one status word;
+    workspaces are the caller's (attend_workspace, evict_workspace: uint8
+    tensors, one per stream that calls concurrently)."""
+
+    def __init__(self, pool, addr, heads: int, dim: int, dtype, page_tokens: int, first_lane: int = 0,
+                 token_stride: int | None = None, k_scale: float = 1.0, v_scale: float = 1.0):
+        _need(pool.dtype == torch.uint8 and pool.is_contiguous(), "pool: contiguous uint8")
+        _need(addr.dim() == 2 and addr.dtype in (torch.int64, torch.uint64) and addr.is_contiguous(),
+              "addr: contiguous [blocks, lanes] of 64-bit byte offsets")
+        _need(dtype in _DTYPES, "dtype: one of %s" % ", ".join(str(d) for d in _DTYPES))
+        self.pool, self.addr, self.dim, self.heads, self.dtype = pool, addr, int(dim), int(heads), dtype
+        self.page_tokens = int(page_tokens)
+        row = self.dim * dtype.itemsize
+        self.c = CacheStruct(pool=pool.data_ptr(), pool_bytes=pool.numel(), addr=addr.data_ptr(), B=addr.size(0),
+                             L=addr.size(1), first_lane=first_lane, heads=heads, dim=dim, dtype=_DTYPES[dtype],
+                             page_tokens=page_tokens, token_stride=row if token_stride is None else token_stride,
+                             k_scale=k_scale, v_scale=v_scale)
+        self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
+
+    def append(self, q, k, v, positions, slots, q_out, q_weight=None, k_weight=None, eps: float = 1e-6, cos_sin=None,
+               interleaved: bool = False, stream=None):
+        """kvx_append_tokens: q [T, q_heads, dim], k and v [T, heads, dim] (views of
+        one projection's output will do); positions int32 [T]; slots int64 [T];
+        cos_sin float [max_pos, rot_dim]; q_out as q, or q itself."""
+        T, dim = q.size(0), self.dim
+        strides = [_heads(t, name, dim, q.dtype) for t, name in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out"))]
+        _need(k.shape == v.shape == (T, self.heads, dim) and q_out.shape == q.shape, "q, k, v, q_out: shapes differ")
+        _table(slots, "slots", (torch.int64,), (T,))
+        for w in (q_weight, k_weight):
+            if w is not None:
+                _table(w, "weight", (q.dtype,), (dim,))
+        max_pos = rot = 0
+        if cos_sin is not None:
+            max_pos, rot = cos_sin.shape
+            _table(cos_sin, "cos_sin", (torch.float32,), (max_pos, rot))
+            _table(positions, "positions", _IDS, (T,))
+        kvx_append_tokens(self.c, q, strides[0], k, strides[1], v, strides[2], _DTYPES[q.dtype], T, q.size(1), q_weight,
+                          k_weight, eps, cos_sin, rot, max_pos, int(interleaved), positions, slots, q_out, strides[3],
+                          self.status, stream)
+
+    def attend_workspace(self, num_seqs: int, q_heads: int, blocks_per_seq: int, window: int = 0, sinks: int = 0,
+                         scores: bool = False):
+        n = kvx_attend_workspace_size(self.c, num_seqs, q_heads, blocks_per_seq, window, sinks, scores)
+        _need(n > 0, "attend: refused sizes")
+        return torch.empty(n, dtype=torch.uint8, device=self.pool.device)
+
+    def attend(self, q, blocks, lens, out, ws, scale: float | None = None, window: int = 0, sinks: int = 0, lse=None,
+               scores=None, stream=None):
+        """kvx_attend: q and out [num_seqs, q_heads, dim]; blocks int32 [num_seqs,
+        blocks_per_seq]; lens int32 [num_seqs]; lse float [num_seqs, q_heads];
+        scores float [num_seqs, heads, stride], added to.  scale defaults to
+        1/sqrt(dim)."""
+        N, dim = q.size(0), self.dim
+        qs, os_ = _heads(q, "q", dim), _heads(out, "out", dim, q.dtype)
+        _need(out.shape == q.shape, "out: not q's shape")
+        _need(blocks.dim() == 2, "blocks: [num_seqs, blocks_per_seq]")
+        _table(blocks, "blocks", _IDS, (N, blocks.size(1)))
+        _table(lens, "lens", _IDS, (N,))
+        if lse is not None:
+            _table(lse, "lse", (torch.float32,), (N, q.size(1)))
+        if scores is not None:
+            _table(scores, "scores", (torch.float32,), (N, self.heads, scores.size(-1)))
+        kvx_attend(self.c, q, qs, _DTYPES[q.dtype], N, q.size(1), blocks, blocks.size(1), lens,
+                   dim ** -0.5 if scale is None else scale, window, sinks, out, os_, lse, scores,
+                   0 if scores is None else scores.size(-1), self.status, ws, stream)
+
+    def evict_workspace(self, num_seqs: int, blocks_per_seq: int, budget: int):
+        n = kvx_evict_workspace_size(self.c, num_seqs, blocks_per_seq, budget)
+        _need(n > 0, "evict: refused sizes")
+        return torch.empty(n, dtype=torch.uint8, device=self.pool.device)
+
+    def evict(self, blocks, lens, scores, dst_blocks, kept, kept_scores, new_lens, ws, sinks: int = 0, recent: int = 0,
+              stream=None):
+        """kvx_evict: kept int32 and kept_scores float [num_seqs, heads, budget];
+        dst_blocks int32 [num_seqs, dst_per_seq]; new_lens int32 [num_seqs]."""
+        N = lens.size(0)
+        _need(blocks.dim() == 2 and dst_blocks.dim() == 2 and kept.dim() == 3, "evict: blocks and dst_blocks are "
+              "[num_seqs, pages], kept is [num_seqs, heads, budget]")
+        _table(blocks, "blocks", _IDS, (N, blocks.size(1)))
+        _table(lens, "lens", _IDS, (N,))
+        _table(scores, "scores", (torch.float32,), (N, self.heads, scores.size(-1)))
+        _table(dst_blocks, "dst_blocks", _IDS, (N, dst_blocks.size(1)))
+        budget = kept.size(2)
+        _table(kept, "kept", _IDS, (N, self.heads, budget))
+        _table(kept_scores, "kept_scores", (torch.float32,), (N, self.heads, budget))
+        _table(new_lens, "new_lens", _IDS, (N,))
+        kvx_evict(self.c, N, blocks, blocks.size(1), lens, scores, scores.size(-1), budget, sinks, recent, dst_blocks,
+                  dst_blocks.size(1), kept, kept_scores, new_lens, self.status, ws, stream)
+
+    def read_status(self) -> int:
+        return int(_u32_np(self.status)[0])
 
 
 def overlapped_steps(transfers, pool, slab, dst_pool, n, main, ctl, side):

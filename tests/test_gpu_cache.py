@@ -1,0 +1,522 @@
+"""The cache operators on the GPU against plain 64-bit statements of them (cache_ref.py).
+
+Tolerances come from the number formats: half a step of the output's type, plus the error that 32-bit arithmetic can
+gather on the way (bounded from the inputs' magnitudes)."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import cache_ref as R
+from paged_kv_cache_kvx_gb300 import kvx
+
+pytestmark = pytest.mark.gpu
+BF, FP, E4 = torch.bfloat16, torch.float16, torch.float8_e4m3fn
+
+
+def near(got, want, dtype, extra=0.0, scale=1.0):
+    """|got - want| within half a step of dtype (stored values times scale) plus `extra`, element by element."""
+    got, want = got.double().cpu(), want.double()
+    tol = R.HALF[dtype] * want.abs() * (1 + 2 ** -6) + R.TINY[dtype] * scale + extra
+    bad = ~((got - want).abs() <= tol)
+    assert not bad.any(), (int(bad.sum()), float((got - want).abs()[bad].max()), bad.nonzero()[0].tolist())
+
+
+# ------------------------------------------------------------------ append
+
+APPEND = [  # act, store, T, q_heads, heads, dim, page, rot, interleaved, token_major, norm
+    (BF, BF, 1, 8, 2, 128, 16, 128, False, False, True),
+    (BF, BF, 37, 32, 8, 128, 16, 128, False, False, True),
+    (BF, E4, 37, 6, 3, 128, 7, 64, False, True, True),
+    (FP, FP, 50, 4, 4, 96, 24, 64, True, True, True),
+    (FP, E4, 9, 5, 1, 256, 1, 256, False, False, True),
+    (BF, BF, 11, 12, 2, 64, 4, 16, True, False, True),
+    (FP, FP, 5, 1, 1, 16, 2, 16, False, False, True),
+    (BF, BF, 5, 3, 1, 80, 16, 0, False, False, True),
+    (BF, BF, 6, 0, 2, 112, 16, 112, False, False, False),
+    (FP, FP, 700, 16, 16, 128, 256, 32, False, True, False),
+]
+
+
+def run_append(act, store, T, HQ, H, D, page, rot, interleaved, token_major, norm, seed=3, in_place=False):
+    gen = torch.Generator().manual_seed(seed)
+    blocks = -(-T // page) + 2
+    lay = R.Layout(blocks, H, D, page, store, seed, token_major=token_major)
+    ks, vs = (0.13, 0.041) if store == E4 else (1.0, 1.0)
+    k0, v0 = (R.randn((blocks, H, page, D), torch.float32, gen).to(store) for _ in range(2))
+    host = lay.pool(k0, v0)
+    pool = host.cuda()
+    cache = lay.cache(pool, k_scale=ks, v_scale=vs)
+    qkv = R.randn((T, (HQ + 2 * H) * D + 8), act, gen, 1.7)
+    dev = qkv.cuda()
+    cut = lambda x: [y.unflatten(1, (-1, D)) if y.numel() else y.view(T, 0, D) for y in  # noqa: E731
+                     x[:, :(HQ + 2 * H) * D].split([HQ * D, H * D, H * D], dim=1)]
+    q, k, v = cut(qkv)
+    dq, dk, dv = cut(dev)
+    wq, wk = ((1 + 0.2 * torch.randn(D, generator=gen)).to(act) for _ in range(2)) if norm else (None, None)
+    most = 500
+    table = None
+    pos = torch.randint(0, most, (T,), generator=gen, dtype=torch.int32)
+    if rot:
+        ang = torch.arange(most).double()[:, None] * 100.0 ** (-torch.arange(rot // 2).double() / rot)
+        table = torch.cat([ang.cos(), ang.sin()], 1).float()
+    slots = torch.randperm(blocks * page, generator=gen)[:T].clone()
+    if T > 4:
+        slots[T // 2] = -1
+        slots[1] = -(2 ** 40)
+    out = dq if in_place else torch.empty(T, HQ, D, dtype=act, device="cuda")
+    cu = lambda x: None if x is None else x.cuda()  # noqa: E731
+    cache.append(dq, dk, dv, pos.cuda(), slots.cuda(), out, q_weight=cu(wq), k_weight=cu(wk), eps=1e-5,
+                 cos_sin=cu(table), interleaved=interleaved)
+    torch.cuda.synchronize()
+    assert cache.read_status() == 0
+    # 32-bit steps on the way: the sum of squares enters by its root
+    steps = (D / 8 + 24) * R.U
+    want, size = R.norm_rotate(q, wq, 1e-5, table, pos, interleaved)
+    near(out, want, act, steps * size)
+    wk_, size = R.norm_rotate(k, wk, 1e-5, table, pos, interleaved)
+    got_k, got_v = lay.values(pool.cpu())
+    want_k, want_v, extra = k0.double(), v0.double(), torch.zeros(k0.shape, dtype=torch.float64)
+    has = slots >= 0
+    b, o = slots[has] // page, slots[has] % page
+    lim = 448.0 if store == E4 else math.inf
+    want_k[b, :, o], want_v[b, :, o] = (wk_[has] / ks).clamp(-lim, lim), (v.double()[has] / vs).clamp(-lim, lim)
+    extra[b, :, o] = (steps * size)[has] / ks
+    near(got_k.float(), want_k, store, extra)
+    near(got_v.float(), want_v, store, 4 * R.U * want_v.abs())
+    untouched = torch.ones(k0.shape[:3], dtype=torch.bool)
+    untouched[b, :, o] = False
+    assert torch.equal(got_k.view(torch.uint8).view(*k0.shape[:3], -1)[untouched], k0.view(torch.uint8).view(*k0.shape[:3], -1)[untouched])
+    # nothing outside the segments changed
+    clean = lay.pool(got_k, got_v)
+    assert torch.equal(clean, pool.cpu())
+
+
+@pytest.mark.parametrize("case", APPEND, ids=str)
+def test_append(case):
+    run_append(*case)
+
+
+def test_append_in_place():
+    run_append(BF, BF, 37, 32, 8, 128, 16, 128, False, False, True, in_place=True)
+
+
+def test_append_special_values():
+    """NaN and infinities pass through; 8-bit storage limits infinities to 448 and keeps NaN."""
+    for store in (BF, E4):
+        lay = R.Layout(2, 1, 64, 4, store, 1)
+        z = torch.zeros(2, 1, 4, 64).to(store)
+        pool = lay.pool(z, z).cuda()
+        cache = lay.cache(pool)
+        k = torch.ones(1, 1, 64, dtype=BF)
+        k[0, 0, 5], k[0, 0, 6], k[0, 0, 7] = math.nan, math.inf, -math.inf
+        v = k.clone()
+        q = torch.ones(1, 1, 64, dtype=BF)
+        out = torch.empty_like(q).cuda()
+        cache.append(q.cuda(), k.cuda(), v.cuda(), None, torch.tensor([2]).cuda(), out)
+        got_k, got_v = lay.values(pool.cpu())
+        for got in (got_k, got_v):
+            x = got[0, 0, 2].float()
+            assert math.isnan(x[5])
+            assert x[6] == (448 if store == E4 else math.inf) and x[7] == -x[6]
+            assert (x[8:] == 1).all() and (x[:5] == 1).all()
+        assert (out.cpu() == 1).all() and cache.read_status() == 0
+
+
+def test_append_bad_places():
+    """A slot beyond the blocks, a segment off its alignment or outside the pool, a position beyond the table: a status
+    bit, and only the good tokens are written."""
+    H, D, page, T = 1, 64, 4, 4
+    for fault in ("slot", "align", "pool", "position"):
+        lay = R.Layout(3, H, D, page, BF, 5)
+        z = torch.zeros(3, H, page, D, dtype=BF)
+        slots = torch.tensor([0, 5, 9, 1])
+        pos = torch.tensor([0, 1, 2, 3], dtype=torch.int32)
+        bit = kvx.S_BOUNDS
+        if fault == "slot":
+            slots[2] = 12
+        elif fault == "align":
+            lay.addr[2, lay.first_lane] += 8
+            bit = kvx.S_ALIGN
+        elif fault == "pool":
+            lay.addr[2, lay.first_lane] = lay.pool_bytes - (page * D * 2 - 16)
+        else:
+            pos[2] = 8
+        pool = torch.zeros(lay.pool_bytes, dtype=torch.uint8, device="cuda")
+        cache = lay.cache(pool)
+        x = torch.ones(T, H, D, dtype=BF, device="cuda")
+        out = torch.zeros(T, H, D, dtype=BF, device="cuda")
+        table = torch.cat([torch.ones(8, 32), torch.zeros(8, 32)], 1).cuda()
+        cache.append(x, x, x, pos.cuda(), slots.cuda(), out, cos_sin=table)
+        torch.cuda.synchronize()
+        assert cache.read_status() == bit, fault
+        got = pool.cpu().view(BF)
+        rows = {(int(s) // page, int(s) % page, kv) for i, s in enumerate(slots) for kv in (0, 1) if i != 2}
+        if fault in ("align", "pool"):
+            rows.add((2, 1, 1))
+        at = lay.rows()
+        total = sum(int((got[at[b, 0, kv, o] // 2:at[b, 0, kv, o] // 2 + D] == 1).all()) for b, o, kv in rows)
+        assert total == len(rows) and int((got == 1).sum()) == len(rows) * D, fault
+        assert (out[[0, 1, 3]] == 1).all()
+
+
+def test_append_nothing():
+    lay = R.Layout(2, 1, 64, 4, BF, 1)
+    cache = lay.cache(torch.zeros(lay.pool_bytes, dtype=torch.uint8, device="cuda"))
+    x = torch.ones(0, 1, 64, dtype=BF, device="cuda")
+    before = kvx.kvx_launch_count()
+    cache.append(x, x, x, None, torch.zeros(0, dtype=torch.int64, device="cuda"), x)
+    assert kvx.kvx_launch_count() == before
+
+
+# ------------------------------------------------------------------ attend
+
+LENS = [0, 1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 500, 1111]
+ATTEND = [  # act, store, q_heads, heads, dim, page, window, sinks, scores, token_major, lens
+    (BF, BF, 8, 2, 128, 16, 0, 0, False, False, LENS),
+    (BF, BF, 8, 2, 128, 16, 0, 0, True, False, LENS),
+    (FP, FP, 6, 2, 64, 24, 0, 0, True, True, LENS),
+    (BF, E4, 16, 2, 128, 64, 0, 0, True, False, LENS),
+    (FP, E4, 3, 3, 64, 1, 0, 0, False, True, LENS),
+    (BF, BF, 9, 1, 128, 2, 0, 0, True, False, LENS),
+    (BF, BF, 32, 2, 64, 16, 0, 0, True, False, LENS),
+    (FP, FP, 20, 1, 128, 256, 0, 0, True, False, LENS),
+    (BF, BF, 5, 1, 256, 16, 0, 0, True, False, LENS),
+    (FP, E4, 24, 2, 256, 32, 0, 0, True, True, LENS),
+    (BF, BF, 4, 1, 16, 3, 0, 0, True, False, LENS),
+    (FP, FP, 4, 2, 80, 16, 0, 0, False, False, LENS),
+    (BF, E4, 4, 2, 96, 16, 0, 0, False, False, LENS),
+    (BF, E4, 4, 2, 208, 16, 0, 0, False, False, LENS),
+    (BF, BF, 8, 2, 128, 16, 1, 0, True, False, LENS),
+    (BF, BF, 8, 2, 128, 16, 64, 4, True, False, LENS),
+    (FP, FP, 8, 1, 64, 5, 100, 33, True, False, LENS),
+    (BF, E4, 8, 1, 128, 16, 1, 200, True, False, LENS),
+    (BF, BF, 128, 1, 64, 16, 7, 1, True, False, [700, 3, 20]),
+    (BF, BF, 8, 2, 128, 16, 0, 0, True, False, [9000]),
+    (FP, E4, 16, 1, 128, 16, 0, 0, True, False, [0, 20000, 1]),
+]
+
+
+def make_attend(act, store, HQ, H, D, page, window, sinks, scores, token_major, lens, seed=5, extra_pages=1, poison=True):
+    gen = torch.Generator().manual_seed(seed)
+    N = len(lens)
+    per = -(-max(lens) // page) + extra_pages
+    need = [-(-n // page) for n in lens]
+    blocks = sum(need) + 1
+    lay = R.Layout(blocks, H, D, page, store, seed, token_major=token_major)
+    k, v = (R.randn((blocks, H, page, D), torch.float32, gen).to(store) for _ in range(2))
+    ids = torch.randperm(blocks, generator=gen)
+    table = torch.full((N, per), 2 ** 31 - 1, dtype=torch.int32)  # pages without a token: ids that do not exist
+    at = 0
+    for n, m in enumerate(need):
+        table[n, :m] = ids[at:at + m].int()
+        at += m
+    if poison:  # what no sequence sees holds NaN and infinities
+        used = torch.zeros(blocks, page, dtype=torch.bool)
+        for n in range(N):
+            pos = torch.from_numpy(R.seen(lens[n], window, sinks))
+            used[table[n].long()[pos // page], pos % page] = True
+        bad = ~used[:, None, :, None].expand_as(k)
+        kb, vb = k.view(torch.uint8).clone(), v.view(torch.uint8).clone()
+        rep = bad.repeat_interleave(store.itemsize, dim=3)
+        kb[rep], vb[rep] = 0x7F, 0xFF  # NaN in every type (0x7F7F in bf16 and fp16 are large or NaN)
+        k, v = kb.view(store), vb.view(store)
+    q = R.randn((N, HQ, D), act, gen, 1.5)
+    sc = torch.rand(N, H, per * page + 3, generator=gen) if scores else None
+    return lay, k, v, q, table, sc
+
+
+def run_attend(case, stream=None, ks=None, scale=None):
+    act, store, HQ, H, D, page, window, sinks, scores, token_major, lens = case
+    lay, k, v, q, table, sc = make_attend(*case)
+    ks, vs = ks or ((0.4, 0.07) if store == E4 else (1.0, 1.0))
+    scale = D ** -0.5 if scale is None else scale
+    pool = lay.pool(k, v).cuda()
+    cache = lay.cache(pool, k_scale=ks, v_scale=vs)
+    N, per = table.shape
+    wide = torch.zeros(N, HQ * D + 16, dtype=act)
+    wide[:, :HQ * D] = q.flatten(1)
+    wide = wide.cuda()
+    out, lse = torch.empty(N, HQ, D, dtype=act, device="cuda"), torch.empty(N, HQ, device="cuda")
+    ln = torch.tensor(lens, dtype=torch.int32).cuda()
+    ws = cache.attend_workspace(N, HQ, per, window=window, sinks=sinks, scores=scores)
+    ws.fill_(0xFF)  # scratch: whatever it holds
+    dsc = None if sc is None else sc.cuda()
+    tb = table.cuda()
+    torch.cuda.synchronize()
+    cache.attend(wide[:, :HQ * D].unflatten(1, (HQ, D)), tb, ln, out, ws, scale=scale, window=window, sinks=sinks, lse=lse,
+                 scores=dsc, stream=stream)
+    torch.cuda.synchronize()
+    assert cache.read_status() == 0
+    kz, vz = (torch.nan_to_num(x.float(), 0, 0, 0) for x in (k, v))
+    want, wlse, weights, off, off_lse = R.attend(q, kz, vz, table, lens, scale, window, sinks, ks, vs)
+    near(out, want, act, off)
+    none = torch.isinf(wlse)
+    assert torch.equal(torch.isinf(lse.cpu()) & (lse.cpu() < 0), none)
+    d = (lse.cpu().double() - wlse)[~none].abs()
+    assert (d <= off_lse[~none]).all(), float((d / off_lse[~none]).max())
+    if scores:
+        new = dsc.cpu().double()
+        for n, (pos, w) in enumerate(weights):
+            full = sc[n].double()
+            add = w.view(H, HQ // H, -1).sum(1)
+            full[:, pos] += add
+            tol = torch.zeros_like(full)
+            tol[:, pos] = add * (2 * off_lse[n].max() + (HQ // H + 8) * R.U) + 2 * R.U * full[:, pos]
+            assert ((new[n] - full).abs() <= tol).all(), (n, float((new[n] - full).abs().max()))
+    return out, lse, dsc
+
+
+@pytest.mark.parametrize("case", ATTEND, ids=lambda c: "-".join(str(x) for x in c[:10]).replace("torch.", ""))
+def test_attend(case):
+    run_attend(case)
+
+
+def test_attend_repeats_bit_for_bit_and_on_another_stream():
+    case = (BF, BF, 16, 2, 128, 16, 0, 0, True, False, [4000, 10, 777])
+    a = run_attend(case)
+    b = run_attend(case, stream=torch.cuda.Stream())
+    for x, y in zip(a, b):
+        assert torch.equal(x, y)
+
+
+def test_attend_large_queries_over_an_8_bit_cache():
+    """bf16 queries beyond fp16's range, and logits far apart."""
+    lay, k, v, q, table, _ = make_attend(BF, E4, 8, 1, 128, 16, 0, 0, False, False, [100, 5000], poison=False)
+    for size in (2.0 ** 100, 2.0 ** -100):
+        big = (q.float() * size).to(BF)
+        pool = lay.pool(k, v).cuda()
+        cache = lay.cache(pool)
+        out, lse = torch.empty_like(big).cuda(), torch.empty(2, 8, device="cuda")
+        ws = cache.attend_workspace(2, 8, table.shape[1])
+        lens = torch.tensor([100, 5000], dtype=torch.int32).cuda()
+        cache.attend(big.cuda(), table.cuda(), lens, out, ws, scale=1.0 / size / 11, lse=lse)
+        torch.cuda.synchronize()
+        want, wlse, _, off, off_lse = R.attend(big, k.float(), v.float(), table, [100, 5000], 1.0 / size / 11, 0, 0)
+        near(out, want, BF, off)
+        assert ((lse.cpu().double() - wlse).abs() <= off_lse).all()
+
+
+def test_attend_infinite_and_nan_logits():
+    """All logits -infinity: as an empty row.  A NaN among the visible keys: NaN."""
+    lay, k, v, q, table, sc = make_attend(BF, BF, 2, 1, 64, 16, 0, 0, True, False, [40, 40, 40, 1000], poison=False)
+    q = q.abs() + 0.1
+    kb = k.clone()
+    for n in (0, 3):
+        for p in range(40 if n == 0 else 1000):
+            kb[table[n, p // 16].item(), 0, p % 16, 3] = -math.inf
+    kb[table[1, 1].item(), 0, 2, 5] = math.nan
+    kb[table[2, 0].item(), 0, 0, 5] = -math.inf  # one of many
+    pool = lay.pool(kb, v).cuda()
+    cache = lay.cache(pool)
+    out, lse = torch.empty_like(q).cuda(), torch.empty(4, 2, device="cuda")
+    dsc = sc.cuda()
+    ws = cache.attend_workspace(4, 2, table.shape[1], scores=True)
+    lens = torch.tensor([40, 40, 40, 1000], dtype=torch.int32).cuda()
+    cache.attend(q.cuda(), table.cuda(), lens, out, ws, lse=lse, scores=dsc)
+    torch.cuda.synchronize()
+    assert cache.read_status() == 0
+    for n in (0, 3):
+        assert (out[n] == 0).all() and (lse[n] == -math.inf).all() and torch.equal(dsc[n].cpu(), sc[n])
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+    assert torch.isfinite(out[2]).all() and torch.isfinite(lse[2]).all()
+    kz = kb.float()
+    kz[table[2, 0].item(), 0, 0, 5] = -1e30
+    want, wlse, _, _, _ = R.attend(q[2:3], kz, v.float(), table[2:3], [40], 64 ** -0.5, 0, 0)
+    assert (out[2].cpu().double() - want[0]).abs().max() < 2 ** -7 * want.abs().max()
+    assert dsc[2, 0, 0].item() == sc[2, 0, 0].item()
+
+
+def test_attend_bad_pages():
+    """Block ids and segments that do not exist, and lengths beyond the pages: a status bit, no access outside."""
+    base = (BF, BF, 4, 1, 64, 16, 0, 0, False, False, [200, 200])
+    for fault, bit in (("block", kvx.S_BOUNDS), ("align", kvx.S_ALIGN), ("pool", kvx.S_BOUNDS), ("len", kvx.S_BOUNDS)):
+        lay, k, v, q, table, _ = make_attend(*base, extra_pages=0)
+        lens = [200, 200]
+        hit = table[1, 3].item()
+        if fault == "block":
+            table[1, 3] = lay.blocks
+        elif fault == "align":
+            lay.addr[hit, lay.first_lane + 1] += 8
+        elif fault == "pool":
+            lay.addr[hit, lay.first_lane] = lay.pool_bytes - 16 * 64 * 2 + 16
+        else:
+            lens[1] = 10 ** 9
+        pool = lay.pool(k, v) if fault in ("block", "len") else torch.zeros(lay.pool_bytes, dtype=torch.uint8)
+        cache = lay.cache(pool.cuda())
+        out = torch.empty_like(q).cuda()
+        ws = cache.attend_workspace(2, 4, table.shape[1])
+        cache.attend(q.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), out, ws)
+        torch.cuda.synchronize()
+        assert cache.read_status() == bit, fault
+        if fault in ("block", "len"):  # the other sequence is answered
+            want, _, _, off, _ = R.attend(q[:1], torch.nan_to_num(k.float(), 0, 0, 0), torch.nan_to_num(v.float(), 0, 0, 0),
+                                          table[:1], [200], 0.125, 0, 0)
+            near(out[:1], want, BF, off)
+
+
+def test_attend_in_a_graph_follows_new_lengths():
+    case = (BF, BF, 8, 2, 128, 16, 0, 0, False, False, [900, 300, 50])
+    lay, k, v, q, table, _ = make_attend(*case, poison=False)
+    cache = lay.cache(lay.pool(k, v).cuda())
+    dq, tb, lens = q.cuda(), table.cuda(), torch.tensor([1, 2, 3], dtype=torch.int32).cuda()
+    out = torch.empty_like(dq)
+    ws = cache.attend_workspace(3, 8, table.shape[1])
+    cache.attend(dq, tb, lens, out, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.attend(dq, tb, lens, out, ws)
+    for now in ([900, 300, 50], [0, 299, 50], [5, 5, 5]):
+        lens.copy_(torch.tensor(now, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        want, _, _, off, _ = R.attend(q, k.float(), v.float(), table, now, 128 ** -0.5, 0, 0)
+        near(out, want, BF, off)
+    assert cache.read_status() == 0
+
+
+def test_cache_beyond_32_bits():
+    """Pages more than 4 GiB apart: append into, attend over and evict between them."""
+    H, D, page = 1, 64, 16
+    pool = torch.zeros(9 << 30, dtype=torch.uint8, device="cuda")
+    seg = page * D * 2
+    at = [16, (4 << 30) + 32, (9 << 30) - 2 * seg, 5 << 30, (8 << 30) + 64, 1 << 20]
+    addr = torch.tensor([[a, a + seg] for a in at])
+    cache = kvx.Cache(pool, addr.cuda(), heads=H, dim=D, dtype=BF, page_tokens=page)
+    gen = torch.Generator().manual_seed(1)
+    T = 40
+    k, v, q = (R.randn((T, H, D), BF, gen) for _ in range(3))
+    slots = torch.tensor([[2, 0, 1][t // page] * page + t % page for t in range(T)])
+    out = torch.empty(T, H, D, dtype=BF, device="cuda")
+    cache.append(q.cuda(), k.cuda(), v.cuda(), None, slots.cuda(), out)
+    table = torch.tensor([[2, 0, 1]], dtype=torch.int32)
+    o1 = torch.empty(1, H, D, dtype=BF, device="cuda")
+    sc = torch.zeros(1, H, 3 * page, device="cuda")
+    lens = torch.tensor([T], dtype=torch.int32).cuda()
+    cache.attend(q[:1].cuda(), table.cuda(), lens, o1, cache.attend_workspace(1, 1, 3, scores=True), scores=sc)
+    kv = torch.zeros(2, 3, H, page, D, dtype=BF)
+    for x, y in ((0, k), (1, v)):
+        kv[x].permute(0, 2, 1, 3).reshape(-1, H, D)[:T] = 0
+        kv[x] = torch.nn.functional.pad(y, (0, 0, 0, 0, 0, 3 * page - T)).view(3, page, H, D).permute(0, 2, 1, 3)
+    want, _, weights, off, _ = R.attend(q[:1], kv[0], kv[1], torch.tensor([[0, 1, 2]]), [T], D ** -0.5, 0, 0)
+    near(o1, want, BF, off)
+    budget = 20
+    kept = torch.empty(1, H, budget, dtype=torch.int32, device="cuda")
+    ksc = torch.empty(1, H, budget, device="cuda")
+    nl = torch.empty(1, dtype=torch.int32, device="cuda")
+    dst = torch.tensor([[4, 3]], dtype=torch.int32).cuda()
+    cache.evict(table.cuda(), lens, sc, dst, kept, ksc, nl, cache.evict_workspace(1, 3, budget), sinks=2, recent=4)
+    torch.cuda.synchronize()
+    pos = R.evict_positions(sc.cpu()[0, 0].tolist(), T, budget, 2, 4)
+    assert kept.cpu()[0, 0].tolist() == pos and nl.item() == budget and cache.read_status() == 0
+    for r, p in enumerate(pos):
+        for lane, x in ((0, k), (1, v)):
+            a = at[[4, 3][r // page]] + lane * seg + r % page * D * 2
+            assert torch.equal(pool[a:a + D * 2].cpu().view(BF), x[p, 0])
+    assert cache.read_status() == 0
+
+
+# ------------------------------------------------------------------ evict
+
+def scores_of(kind, shape, gen):
+    if kind == "ties":
+        return torch.randint(0, 5, shape, generator=gen).float()
+    if kind == "equal":
+        return torch.full(shape, 0.25)
+    x = torch.randn(shape, generator=gen).mul(3).exp()
+    if kind == "special":
+        r = torch.randint(0, 12, shape, generator=gen)
+        for i, y in enumerate((math.nan, math.inf, -math.inf, 0.0, -0.0, -1.5, 1e-42)):
+            x[r == i] = y
+    return x
+
+
+EVICT = [  # store, heads, dim, page, lens, budget, sinks, recent, kind, token_major
+    (BF, 2, 128, 16, [0, 1, 99, 100, 101, 400], 100, 4, 16, "random", False),
+    (BF, 2, 128, 16, [0, 1, 99, 100, 101, 400], 100, 4, 16, "ties", True),
+    (E4, 3, 64, 24, [900, 5, 1000], 333, 0, 0, "special", False),
+    (FP, 1, 96, 7, [700], 1, 0, 0, "special", True),
+    (FP, 1, 80, 7, [700, 20], 10, 10, 99, "random", False),
+    (BF, 1, 64, 16, [700, 20], 10, 3, 99, "random", False),
+    (E4, 1, 16, 1, [77, 300], 50, 100, 0, "equal", False),
+    (BF, 1, 256, 16, [3000], 2999, 1, 1, "equal", False),
+    (E4, 2, 208, 16, [12345, 4096, 4097], 1025, 4, 100, "random", True),
+    (FP, 1, 16, 64, [100000], 5000, 4, 1000, "random", False),
+    (FP, 1, 16, 64, [70001], 30000, 0, 0, "ties", False),
+]
+
+
+@pytest.mark.parametrize("case", EVICT, ids=str)
+def test_evict(case):
+    store, H, D, page, lens, budget, sinks, recent, kind, token_major = case
+    gen = torch.Generator().manual_seed(11)
+    N = len(lens)
+    per, dper = -(-max(lens) // page) + 1, -(-budget // page)
+    need = [-(-n // page) for n in lens]
+    blocks = sum(need) + N * dper + 1
+    lay = R.Layout(blocks, H, D, page, store, 4, token_major=token_major)
+    raw = torch.randint(0, 256, (2, blocks, H, page, D * store.itemsize), generator=gen, dtype=torch.uint8)
+    k, v = raw.view(store)
+    host = lay.pool(k, v)
+    ids = torch.randperm(blocks, generator=gen).int()
+    table = torch.full((N, per), -1, dtype=torch.int32)
+    at = 0
+    for n, m in enumerate(need):
+        table[n, :m] = ids[at:at + m]
+        at += m
+    dst = ids[at:at + N * dper].view(N, dper)
+    sc = scores_of(kind, (N, H, per * page + 1), gen)
+    pool = host.cuda()
+    cache = lay.cache(pool)
+    kept = torch.empty(N, H, budget, dtype=torch.int32, device="cuda")
+    ksc = torch.empty(N, H, budget, device="cuda")
+    nl = torch.empty(N, dtype=torch.int32, device="cuda")
+    ws = cache.evict_workspace(N, per, budget)
+    ws.fill_(0xFF)
+    cache.evict(table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), sc.cuda(), dst.cuda(), kept, ksc, nl, ws,
+                sinks=sinks, recent=recent)
+    torch.cuda.synchronize()
+    assert cache.read_status() == 0
+    assert nl.cpu().tolist() == [min(n, budget) for n in lens]
+    want = host.clone()
+    src_rows, rows = lay.rows(), lay.rows()
+    for n in range(N):
+        for h in range(H):
+            pos = R.evict_positions(sc[n, h].tolist(), lens[n], budget, sinks, recent)
+            m = len(pos)
+            got = kept[n, h].cpu().tolist()
+            assert got[:m] == pos and got[m:] == [-1] * (budget - m), (n, h)
+            ws_ = ksc[n, h].cpu()
+            assert torch.equal(ws_[:m].view(torch.int32), sc[n, h][pos].view(torch.int32)) and (ws_[m:] == 0).all()
+            p, r = np.array(pos, dtype=np.int64), np.arange(m)
+            for kv in (0, 1):
+                s = src_rows[table[n].numpy()[p // page], h, kv, p % page]
+                d = rows[dst[n].numpy()[r // page], h, kv, r % page]
+                b = np.arange(lay.row)
+                want[torch.from_numpy((d[:, None] + b).reshape(-1))] = host[torch.from_numpy((s[:, None] + b).reshape(-1))]
+    assert torch.equal(pool.cpu(), want)
+
+
+def test_evict_bad_pages():
+    for fault, bit in (("src", kvx.S_BOUNDS), ("dst", kvx.S_BOUNDS), ("align", kvx.S_ALIGN), ("len", kvx.S_BOUNDS)):
+        lay = R.Layout(9, 1, 64, 16, BF, 4)
+        table, dst = torch.tensor([[0, 1, 2, 3]], dtype=torch.int32), torch.tensor([[4, 5]], dtype=torch.int32)
+        length = 60
+        if fault == "src":
+            table[0, 3] = 9
+        elif fault == "dst":
+            dst[0, 1] = -1
+        elif fault == "align":
+            lay.addr[5, lay.first_lane + 1] += 4
+        else:
+            length = 2 ** 31 - 1
+        pool = torch.zeros(lay.pool_bytes, dtype=torch.uint8, device="cuda")
+        cache = lay.cache(pool)
+        kept = torch.empty(1, 1, 30, dtype=torch.int32, device="cuda")
+        ksc, nl = torch.empty(1, 1, 30, device="cuda"), torch.empty(1, dtype=torch.int32, device="cuda")
+        cache.evict(table.cuda(), torch.tensor([length], dtype=torch.int32).cuda(), torch.arange(64.0).view(1, 1, 64).cuda(),
+                    dst.cuda(), kept, ksc, nl, cache.evict_workspace(1, 4, 30), sinks=24)  # keeps 0-23 and the last six
+        torch.cuda.synchronize()
+        assert cache.read_status() == bit, fault
