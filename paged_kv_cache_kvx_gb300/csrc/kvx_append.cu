@@ -3,11 +3,10 @@
 //
 // Per head x:  y = x / sqrt(sum(x^2)/D + eps) * w, then the pairs (y_a, y_b)
 // of the first rot_dim values turn by the token's angles.  A head is one row
-// of up to 32 lanes, eight values (16 bytes) a lane, so the sum is a few
-// shuffles and the pair's other half is in the lane itself (interleaved) or in
-// the lane rot_dim/16 away.  All in 32 bits, rounded once when stored: a
-// 16-bit norm rounded before the rotation would add an error as large as the
-// result's own rounding.
+// of up to 32 lanes with eight values each, as two runs of four that hold whole
+// pairs: a lane turns its own values, and only the sum of squares crosses lanes.
+// All in 32 bits, rounded once when stored: a 16-bit norm rounded before the
+// rotation would add an error as large as the result's own rounding.
 //
 // Bound by HBM for prompts (each value read once and written once; the table's
 // row of cosines and sines is read once per block of a token's heads) and by
@@ -40,20 +39,14 @@ struct AppendArgs {
 };
 
 template <class T>
-__device__ __forceinline__ void unpack8(const uint4 &r, float *x) {
-    const uint32_t w[4] = {r.x, r.y, r.z, r.w};
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const float2 f = Pair<T>::unpack(w[i]);
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
-    }
+__device__ __forceinline__ void unpack4(const uint2 &r, float *x) {
+    const float2 a = Pair<T>::unpack(r.x), b = Pair<T>::unpack(r.y);
+    x[0] = a.x, x[1] = a.y, x[2] = b.x, x[3] = b.y;
 }
 
 template <class T>
-__device__ __forceinline__ uint4 pack8(const float *x) {
-    return make_uint4(Pair<T>::pack(x[0], x[1]), Pair<T>::pack(x[2], x[3]), Pair<T>::pack(x[4], x[5]),
-                      Pair<T>::pack(x[6], x[7]));
+__device__ __forceinline__ uint2 pack4(const float *x) {
+    return make_uint2(Pair<T>::pack(x[0], x[1]), Pair<T>::pack(x[2], x[3]));
 }
 
 __device__ __forceinline__ uint32_t e4m3x4(const float *x, float inv) {
@@ -62,20 +55,32 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *x, float inv) {
     return lo | hi << 16;
 }
 
+// A lane's eight values of a row: four from each of two places.
+struct Eight {
+    uint2 a, b;
+};
+template <class T>
+__device__ __forceinline__ Eight load8(const T *row, uint32_t da, uint32_t db) {
+    return Eight{*reinterpret_cast<const uint2 *>(row + da), *reinterpret_cast<const uint2 *>(row + db)};
+}
+
 // Lanes of a row: a power of two with 8 * LANES >= dim.
 template <class T, bool FP8, int LANES>
-__global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ AppendArgs a) {
+__global__ void __launch_bounds__(kThreads, 4) k_append(const __grid_constant__ AppendArgs a) {
     constexpr uint32_t kRows = kThreads / LANES;
     const uint64_t t = blockIdx.x;
-    const uint32_t li = threadIdx.x % LANES, d0 = li * 8;
+    const uint32_t li = threadIdx.x % LANES;
+    // the lanes of this row, whose shuffles other rows take no part in
+    const uint32_t mask = LANES == 32 ? 0xFFFFFFFFu : ((1u << LANES % 32) - 1) << (threadIdx.x % 32 / LANES * LANES);
     const uint32_t dim = a.c.dim, heads = a.c.heads, rows = a.q_heads + 2 * heads;
-    const uint32_t step = gridDim.y * kRows;
-    const bool in = d0 < dim;
+    const bool in = li * 8 < dim;
     uint32_t bad = 0;
 
-    const T *q = static_cast<const T *>(a.q) + t * a.q_stride + d0;
-    const T *k = static_cast<const T *>(a.k) + t * a.k_stride + d0;
-    const T *v = static_cast<const T *>(a.v) + t * a.v_stride + d0;
+    // values da .. da+3 and db .. db+3: rotated halves hold each other's
+    // partners, neighbours are partners anyway
+    const bool turns = li * 8 < a.rot, halves = turns && !a.interleaved;
+    const uint32_t da = halves ? li * 4 : li * 8, db = halves ? da + a.rot / 2 : da + 4;
+
     const int64_t slot = a.slots[t];
     uint32_t block = 0, place = 0;
     bool write = slot >= 0;
@@ -90,93 +95,78 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ App
         }
     }
 
-    // the token's angles for this lane's values: value e turns by c[e], with
-    // its partner's sign in s[e]
-    const bool turns = d0 < a.rot;
-    const uint32_t half = a.rot / 2;
-    float c[8], s[8];
-    uint32_t partner = threadIdx.x & 31;
+    float4 c = make_float4(1, 1, 1, 1), s = make_float4(0, 0, 0, 0);
     if (a.rot) {
         const uint32_t pos = a.positions[t];
         if (pos >= a.max_pos) {  // the same for the whole block
             if (threadIdx.x == 0) raise(a.status, bad | KVX_S_BOUNDS);
             return;
         }
-        const float *row = a.cos_sin + (uint64_t)pos * a.rot;
-        if (turns && !a.interleaved) {
-            const bool low = d0 < half;
-            const uint32_t i = low ? d0 : d0 - half;
-            partner = low ? partner + half / 8 : partner - half / 8;
-#pragma unroll
-            for (int j = 0; j < 8; j += 4) {
-                const float4 cv = __ldg(reinterpret_cast<const float4 *>(row + i + j));
-                const float4 sv = __ldg(reinterpret_cast<const float4 *>(row + half + i + j));
-                c[j] = cv.x, c[j + 1] = cv.y, c[j + 2] = cv.z, c[j + 3] = cv.w;
-                s[j] = low ? -sv.x : sv.x, s[j + 1] = low ? -sv.y : sv.y;
-                s[j + 2] = low ? -sv.z : sv.z, s[j + 3] = low ? -sv.w : sv.w;
-            }
-        } else if (turns) {
-            const float4 cv = __ldg(reinterpret_cast<const float4 *>(row + d0 / 2));
-            const float4 sv = __ldg(reinterpret_cast<const float4 *>(row + half + d0 / 2));
-            c[0] = c[1] = cv.x, c[2] = c[3] = cv.y, c[4] = c[5] = cv.z, c[6] = c[7] = cv.w;
-            s[0] = -sv.x, s[1] = sv.x, s[2] = -sv.y, s[3] = sv.y;
-            s[4] = -sv.z, s[5] = sv.z, s[6] = -sv.w, s[7] = sv.w;
+        if (turns) {
+            const float *row = a.cos_sin + (uint64_t)pos * a.rot + li * 4;
+            c = __ldg(reinterpret_cast<const float4 *>(row));
+            s = __ldg(reinterpret_cast<const float4 *>(row + a.rot / 2));
         }
     }
-    uint4 wq = make_uint4(0, 0, 0, 0), wk = wq;
-    if (in && a.q_weight) wq = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q_weight) + d0));
-    if (in && a.k_weight) wk = __ldg(reinterpret_cast<const uint4 *>(static_cast<const T *>(a.k_weight) + d0));
+    Eight wq = {}, wk = {};
+    if (in && a.q_weight) wq = load8(static_cast<const T *>(a.q_weight), da, db);
+    if (in && a.k_weight) wk = load8(static_cast<const T *>(a.k_weight), da, db);
 
-    const uint32_t first = blockIdx.y * kRows + threadIdx.x / LANES;
-    // every lane of a warp makes the same number of turns: the shuffles below
-    // are warp-wide
-    for (uint32_t r0 = first - first % (32 / LANES); r0 < rows; r0 += kUnroll * step) {
-        const uint32_t rg = r0 + first % (32 / LANES);
-        uint4 raw[kUnroll];
+    const T *q = static_cast<const T *>(a.q) + t * a.q_stride;
+    const T *k = static_cast<const T *>(a.k) + t * a.k_stride;
+    const T *v = static_cast<const T *>(a.v) + t * a.v_stride;
+    const uint32_t step = gridDim.y * kRows;
+    for (uint32_t r0 = blockIdx.y * kRows + threadIdx.x / LANES; r0 < rows; r0 += kUnroll * step) {
+        Eight raw[kUnroll] = {};
 #pragma unroll
         for (int u = 0; u < kUnroll; u++) {
-            const uint32_t r = rg + u * step;
-            raw[u] = make_uint4(0, 0, 0, 0);
-            if (in && r < rows) {
-                const T *src = r < a.q_heads ? q + (uint64_t)r * dim
+            const uint32_t r = r0 + u * step;
+            if (in && r < rows)
+                raw[u] = load8(r < a.q_heads           ? q + (uint64_t)r * dim
                                : r < a.q_heads + heads ? k + (uint64_t)(r - a.q_heads) * dim
-                                                       : v + (uint64_t)(r - a.q_heads - heads) * dim;
-                raw[u] = *reinterpret_cast<const uint4 *>(src);
-            }
+                                                       : v + (uint64_t)(r - a.q_heads - heads) * dim,
+                               da, db);
         }
 #pragma unroll
         for (int u = 0; u < kUnroll; u++) {
-            const uint32_t r = rg + u * step;
-            if (r0 + u * step >= rows) break;  // the same for the whole warp
+            const uint32_t r = r0 + u * step;
+            if (r >= rows) break;
             const bool is_q = r < a.q_heads, is_v = r >= a.q_heads + heads;
             float x[8];
-            unpack8<T>(raw[u], x);
-            float ss = 0;
+            unpack4<T>(raw[u].a, x);
+            unpack4<T>(raw[u].b, x + 4);
+            if (!is_v) {
+                if (is_q ? a.q_weight : a.k_weight) {
+                    float ss = 0;
 #pragma unroll
-            for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
+                    for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-            for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
-            if (!is_v && (is_q ? a.q_weight : a.k_weight)) {
-                const float inv = rsqrtf(ss / (float)dim + a.eps);
-                float w[8];
-                unpack8<T>(is_q ? wq : wk, w);
+                    for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
+                    const float inv = rsqrtf(ss / (float)dim + a.eps);
+                    float w[8];
+                    unpack4<T>(is_q ? wq.a : wk.a, w);
+                    unpack4<T>(is_q ? wq.b : wk.b, w + 4);
 #pragma unroll
-                for (int e = 0; e < 8; e++) x[e] = x[e] * inv * w[e];
-            }
-            if (a.rot) {
-                float y[8];
+                    for (int e = 0; e < 8; e++) x[e] = x[e] * inv * w[e];
+                }
+                if (turns) {
+                    const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
 #pragma unroll
-                for (int e = 0; e < 8; e++)
-                    y[e] = a.interleaved ? x[e ^ 1] : __shfl_sync(0xFFFFFFFFu, x[e], partner);
-                if (turns && !is_v) {
-#pragma unroll
-                    for (int e = 0; e < 8; e++) x[e] = fmaf(y[e], s[e], x[e] * c[e]);
+                    for (int i = 0; i < 4; i++) {  // pair i: values i and i+4, or 2i and 2i+1
+                        const float ya = a.interleaved ? x[2 * i] : x[i], yb = a.interleaved ? x[2 * i + 1] : x[i + 4];
+                        const float za = fmaf(-yb, sn[i], ya * cc[i]), zb = fmaf(ya, sn[i], yb * cc[i]);
+                        if (a.interleaved)
+                            x[2 * i] = za, x[2 * i + 1] = zb;
+                        else
+                            x[i] = za, x[i + 4] = zb;
+                    }
                 }
             }
-            if (!in || r >= rows) continue;
+            if (!in) continue;
             if (is_q) {
-                T *o = static_cast<T *>(a.q_out) + t * a.q_out_stride + (uint64_t)r * dim + d0;
-                *reinterpret_cast<uint4 *>(o) = pack8<T>(x);
+                T *o = static_cast<T *>(a.q_out) + t * a.q_out_stride + (uint64_t)r * dim;
+                *reinterpret_cast<uint2 *>(o + da) = pack4<T>(x);
+                *reinterpret_cast<uint2 *>(o + db) = pack4<T>(x + 4);
             } else if (write) {
                 const uint32_t h = is_v ? r - a.q_heads - heads : r - a.q_heads;
                 const uint64_t at = __ldg(a.c.lane_addr(block, h, is_v));
@@ -184,9 +174,11 @@ __global__ void __launch_bounds__(kThreads) k_append(const __grid_constant__ App
                     uint8_t *o = a.c.pool + at + place * a.c.token_stride;
                     if constexpr (FP8) {
                         const float inv = 1.0f / (is_v ? a.c.v_scale : a.c.k_scale);
-                        *reinterpret_cast<uint2 *>(o + d0) = make_uint2(e4m3x4(x, inv), e4m3x4(x + 4, inv));
+                        *reinterpret_cast<uint32_t *>(o + da) = e4m3x4(x, inv);
+                        *reinterpret_cast<uint32_t *>(o + db) = e4m3x4(x + 4, inv);
                     } else {
-                        *reinterpret_cast<uint4 *>(o + 2 * d0) = pack8<T>(x);
+                        *reinterpret_cast<uint2 *>(o + 2 * da) = pack4<T>(x);
+                        *reinterpret_cast<uint2 *>(o + 2 * db) = pack4<T>(x + 4);
                     }
                 }
             }

@@ -1,170 +1,156 @@
 // kvx_attend: attention of one new token per sequence over a paged cache.
 //
-// Two launches.  k_attend (kvx_attend.cuh) walks equal shares of all
-// sequences' tiles, one per block; a unit (the query heads of one KV head of
-// one sequence) that lies in one share is finished there, one that is cut by
-// share borders leaves partial outputs with their bases m and sums l.  k_finish
-// joins those,
+// k_attend (kvx_attend.cuh) walks equal shares of all sequences' tiles, one
+// per block; a unit (the query heads of one KV head of one sequence) that
+// lies in one share is finished there, one that is cut by share borders leaves
+// partial outputs with their bases m and sums l.  k_join puts those together,
 //     M = max m_c,  L = sum l_c 2^(m_c - M),  out = sum o_c 2^(m_c - M) / L
-// in the order of the blocks, and adds the attention weights 2^(logit - lse)
-// to the scores: a weight needs the sum over all keys, so the logits pass
-// through the workspace (4 bytes per key and query head, beside 2*dim*size
-// bytes of key and value per KV head).  It starts beside k_attend's last
-// blocks (programmatic dependency) and waits for their results.
+// in a fixed order.  k_scores adds the attention weights 2^(logit - lse) to the
+// scores: a weight needs the sum over all keys, so the logits pass through the
+// workspace (4 bytes per key and query head, beside 2*dim*size bytes of key
+// and value per KV head).  Each starts beside the last blocks of the kernel
+// before it (programmatic dependency) and waits for its results.
 #include "kvx_attend.cuh"
 
 namespace kvx {
 namespace attend {
 
 // instantiated in kvx_attend_<types>.cu, a file each so that they compile in parallel
-extern template bool launch<__nv_bfloat16, 2>(const Args &, uint32_t, uint32_t, cudaStream_t);
-extern template bool launch<__nv_bfloat16, 1>(const Args &, uint32_t, uint32_t, cudaStream_t);
-extern template bool launch<__half, 2>(const Args &, uint32_t, uint32_t, cudaStream_t);
-extern template bool launch<__half, 1>(const Args &, uint32_t, uint32_t, cudaStream_t);
+extern template bool launch<__nv_bfloat16, 2>(Args &, uint64_t, uint32_t, uint32_t, cudaStream_t);
+extern template bool launch<__nv_bfloat16, 1>(Args &, uint64_t, uint32_t, uint32_t, cudaStream_t);
+extern template bool launch<__half, 2>(Args &, uint64_t, uint32_t, uint32_t, cudaStream_t);
+extern template bool launch<__half, 1>(Args &, uint64_t, uint32_t, uint32_t, cudaStream_t);
 
 namespace {
 
 constexpr uint32_t kMaxGroup = 128;
-constexpr uint32_t kScoreKeys = 1024;  // of a block that adds weights
+constexpr int kJoinWarps = 4;
+constexpr int kJoinUnroll = 8;  // parts whose loads a warp has in flight
+constexpr int kScoreThreads = 128;
+constexpr uint32_t kScoreKeys = 4 * kScoreThreads;  // of a block that adds weights
 
-// The blocks of k_attend that hold a unit's parts: first .. last, the first
-// one's part in its first or second slot.
-struct Parts {
-    uint64_t first, last;
-    bool second;
-    __device__ __forceinline__ uint64_t slot(uint64_t c) const { return 2 * c + (c == first && second); }
-};
-
-__device__ __forceinline__ Parts parts_of(uint64_t tile, uint32_t nt, uint64_t share) {
-    return Parts{tile / share, (tile + nt - 1) / share, tile % share != 0};
+// Block (c, hh) joins query head hh of the unit whose first part block c of
+// k_attend did; its other parts are the first ones of blocks c+1 .. last.
+template <class T>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant__ Args a, uint32_t dp,
+                                                          uint32_t unit_heads) {
+    __shared__ float sh_m[kJoinWarps], sh_l[kJoinWarps];
+    __shared__ float4 sh_o[kJoinWarps][32];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t heads = a.group < unit_heads ? a.group : unit_heads;
+    const uint32_t first = blockIdx.x / heads, hh = blockIdx.x % heads;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint4 cut = __ldcg(a.cut + first);
+    if (cut.x == kNone) return;
+    const uint32_t per_head = (a.group + unit_heads - 1) / unit_heads;
+    const uint32_t in = cut.y % per_head * unit_heads + hh, qh = cut.y / per_head * a.group + in;
+    if (in >= a.group) return;
+    const uint32_t n = cut.x, last = cut.z;
+    auto slot = [&](uint32_t c) { return (uint64_t)(2 * c + (c == first && cut.w)) * unit_heads + hh; };
+    // each warp takes every fourth part; a lane four of 128 values at a time
+    for (uint32_t d0 = 0; d0 < dp; d0 += 128) {
+        const uint32_t d = d0 + lane * 4;
+        float4 v = make_float4(0, 0, 0, 0);
+        float top = -INFINITY, sum = 0;
+        for (uint32_t c0 = first + warp; c0 <= last; c0 += kJoinWarps * kJoinUnroll) {
+            float2 ml[kJoinUnroll];
+            float4 x[kJoinUnroll];
+            float higher = top;
+#pragma unroll
+            for (int u = 0; u < kJoinUnroll; u++) {
+                const uint32_t c = c0 + u * kJoinWarps;
+                ml[u] = make_float2(-INFINITY, 0);
+                x[u] = make_float4(0, 0, 0, 0);
+                if (c <= last) ml[u] = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + slot(c));
+                if (c <= last && d < dp) x[u] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot(c) * dp + d));
+            }
+#pragma unroll
+            for (int u = 0; u < kJoinUnroll; u++) higher = fmaxf(higher, ml[u].x);
+            float f = top == -INFINITY ? 1.0f : exp2f(top - higher);
+            top = higher;
+            sum *= f, v.x *= f, v.y *= f, v.z *= f, v.w *= f;
+#pragma unroll
+            for (int u = 0; u < kJoinUnroll; u++) {
+                f = ml[u].x == -INFINITY ? 1.0f : exp2f(ml[u].x - top);  // 1: zeros, or a NaN
+                sum += ml[u].y * f;
+                v.x += x[u].x * f, v.y += x[u].y * f, v.z += x[u].z * f, v.w += x[u].w * f;
+            }
+        }
+        sh_o[warp][lane] = v;
+        if (lane == 0) sh_m[warp] = top, sh_l[warp] = sum;
+        __syncthreads();
+        if (warp == 0) {
+            for (int w = 1; w < kJoinWarps; w++) top = fmaxf(top, sh_m[w]);
+            v = make_float4(0, 0, 0, 0);
+            sum = 0;
+#pragma unroll
+            for (int w = 0; w < kJoinWarps; w++) {
+                const float f = sh_m[w] == -INFINITY ? 1.0f : exp2f(sh_m[w] - top);
+                const float4 x = sh_o[w][lane];
+                v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
+                sum += sh_l[w] * f;
+            }
+            const float inv = sum == 0 ? 0.0f : a.c.v_scale / sum;
+            if (d < a.c.dim) {
+                T *to = static_cast<T *>(a.out) + (uint64_t)n * a.out_stride + (uint64_t)qh * a.c.dim + d;
+                *reinterpret_cast<uint2 *>(to) =
+                    make_uint2(Pair<T>::pack(v.x * inv, v.y * inv), Pair<T>::pack(v.z * inv, v.w * inv));
+            }
+            if (d == 0) {
+                const float lse2 = sum == 0 ? -INFINITY : top + log2f(sum);
+                if (a.lse) a.lse[(uint64_t)n * a.q_heads + qh] = lse2 * 0.6931471805599453f;
+                if (a.lse2) a.lse2[(uint64_t)n * a.q_heads + qh] = lse2;
+            }
+        }
+        __syncthreads();
+    }
 }
 
-// Blocks 0 .. num_seqs*q_heads-1 join a query head each; the others add the
-// weights of kScoreKeys keys of a KV head.
-template <class T>
-__global__ void __launch_bounds__(kThreads) k_finish(const __grid_constant__ Args a, uint32_t dp, uint32_t unit_heads,
-                                                     uint32_t chunks) {
-    __shared__ uint64_t sh_sum[kWarps];
+// Adds the weights of kScoreKeys keys of a KV head, four keys a thread.
+__global__ void __launch_bounds__(kScoreThreads) k_scores(const __grid_constant__ Args a, uint32_t chunks) {
     __shared__ float sh_lse[kMaxGroup];
-    __shared__ float4 sh_o[kWarps][32];
-    __shared__ float sh_l[kWarps];
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t joins = a.num_seqs * a.q_heads;
-    const bool join = blockIdx.x < joins;
-    const uint32_t r = join ? 0 : blockIdx.x - joins;
-    const uint32_t n = join ? blockIdx.x / a.q_heads : r / chunks / a.c.heads;
-    const uint32_t head = join ? blockIdx.x % a.q_heads / a.group : r / chunks % a.c.heads;
-
-    uint64_t mine = 0, mine_before = 0;
-    for (uint32_t i = threadIdx.x; i < a.num_seqs; i += kThreads) {
-        const uint32_t k = tiles(seen(a, a.lens[i]).n);
-        mine += k;
-        if (i < n) mine_before += k;
-    }
-    const uint64_t share = share_of(block_sum(mine, sh_sum) * a.units, a.grid);
-    const uint64_t before = block_sum(mine_before, sh_sum) * a.units;
+    const uint32_t row = blockIdx.x / chunks, n = row / a.c.heads, head = row % a.c.heads;
+    const uint32_t i0 = blockIdx.x % chunks * kScoreKeys + threadIdx.x;
     const Seen sv = seen(a, a.lens[n]);
-    const uint32_t nt = tiles(sv.n);
-    const uint32_t per_head = (a.group + unit_heads - 1) / unit_heads;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    if (!nt) return;
-
-    if (join) {
-        const uint32_t qh = blockIdx.x % a.q_heads, in = qh % a.group;
-        const Parts p = parts_of(before + (uint64_t)(head * per_head + in / unit_heads) * nt, nt, share);
-        if (p.first == p.last) return;
-        const uint32_t hh = in % unit_heads;
-        float top = -INFINITY;
-        for (uint64_t c = p.first; c <= p.last; c++)
-            top = fmaxf(top, __ldcg(a.part_ml + (p.slot(c) * unit_heads + hh) * 2));
-        // warp w takes parts w, w+4, ...; a lane four of 128 values at a time
-        for (uint32_t d0 = 0; d0 < dp; d0 += 128) {
-            const uint32_t d = d0 + lane * 4;
-            float4 v = make_float4(0, 0, 0, 0);
-            float sum = 0;
-#pragma unroll 4
-            for (uint64_t c = p.first + warp; c <= p.last; c += kWarps) {
-                const uint64_t s = p.slot(c) * unit_heads + hh;
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + s);
-                const float4 x = d < dp ? __ldcg(reinterpret_cast<const float4 *>(a.part_o + s * dp + d))
-                                        : make_float4(0, 0, 0, 0);
-                const float f = ml.x == -INFINITY ? 1.0f : exp2f(ml.x - top);
-                sum += ml.y * f;
-                v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
-            }
-            sh_o[warp][lane] = v;
-            if (lane == 0) sh_l[warp] = sum;
-            __syncthreads();
-            if (warp == 0) {
-                sum = sh_l[0];
-#pragma unroll
-                for (int w = 1; w < kWarps; w++) {
-                    const float4 x = sh_o[w][lane];
-                    v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-                    sum += sh_l[w];
-                }
-                const float inv = sum == 0 ? 0.0f : a.c.v_scale / sum;
-                if (d < a.c.dim) {
-                    T *to = static_cast<T *>(a.out) + (uint64_t)n * a.out_stride + (uint64_t)qh * a.c.dim + d;
-                    *reinterpret_cast<uint2 *>(to) =
-                        make_uint2(Pair<T>::pack(v.x * inv, v.y * inv), Pair<T>::pack(v.z * inv, v.w * inv));
-                }
-                if (d == 0 && a.lse)
-                    a.lse[(uint64_t)n * a.q_heads + qh] =
-                        sum == 0 ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
-            }
-            __syncthreads();
-        }
-        return;
-    }
-
-    const uint32_t i0 = r % chunks * kScoreKeys;
-    if (i0 >= sv.n) return;
-    for (uint32_t in = warp; in < a.group; in += kWarps) {
-        const Parts p = parts_of(before + (uint64_t)(head * per_head + in / unit_heads) * nt, nt, share);
-        float lse2;
-        if (p.first == p.last) {
-            lse2 = __ldcg(a.lse2 + (uint64_t)n * a.q_heads + head * a.group + in);
-        } else {
-            const uint32_t hh = in % unit_heads;
-            float top = -INFINITY, sum = 0;
-            for (uint64_t c = p.first + lane; c <= p.last; c += 32)
-                top = fmaxf(top, __ldcg(a.part_ml + (p.slot(c) * unit_heads + hh) * 2));
-#pragma unroll
-            for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-            for (uint64_t c = p.first + lane; c <= p.last; c += 32) {
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + p.slot(c) * unit_heads + hh);
-                sum += ml.y * (ml.x == -INFINITY ? 1.0f : exp2f(ml.x - top));
-            }
-#pragma unroll
-            for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(0xFFFFFFFFu, sum, o);
-            lse2 = sum == 0 ? -INFINITY : top + log2f(sum);
-        }
-        // a head without a finite logit gives no weight: exp2(-inf - inf) = 0
-        if (lane == 0) sh_lse[in] = lse2 == -INFINITY ? INFINITY : lse2;
+    if (i0 - threadIdx.x >= sv.n) return;
+    for (uint32_t i = threadIdx.x; i < a.group; i += kScoreThreads) {
+        const float lse2 = __ldcg(a.lse2 + (uint64_t)n * a.q_heads + head * a.group + i);
+        sh_lse[i] = lse2 == -INFINITY ? INFINITY : lse2;  // no finite logit, no weight: 2^(-inf - inf) = 0
     }
     __syncthreads();
     const uint32_t gp = (a.group + 1) & ~1u;
-    const uint64_t row = (uint64_t)n * a.c.heads + head;
-    for (uint32_t i = i0 + threadIdx.x; i < sv.n && i < i0 + kScoreKeys; i += kThreads) {
-        const float2 *x = reinterpret_cast<const float2 *>(a.logits + (row * a.logits_keys + i) * gp);
-        float *to = a.scores + row * a.scores_stride + (i < sv.sinks ? i : i + sv.shift);
-        const float old = *to;
-        float w = 0;
-        for (uint32_t k = 0; k < a.group; k += 2) {
-            const float2 v = __ldcg(x + k / 2);
-            w += exp2f(v.x - sh_lse[k]);
-            if (k + 1 < a.group) w += exp2f(v.y - sh_lse[k + 1]);
+    const float2 *x = reinterpret_cast<const float2 *>(a.logits + ((uint64_t)row * a.logits_keys + i0) * gp);
+    float *to = a.scores + (uint64_t)row * a.scores_stride;
+    float old[4], w[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        const uint32_t i = i0 + u * kScoreThreads;
+        old[u] = i < sv.n ? to[i < sv.sinks ? i : i + sv.shift] : 0;
+    }
+    for (uint32_t k = 0; k < a.group; k += 2) {
+        const float l0 = sh_lse[k], l1 = k + 1 < a.group ? sh_lse[k + 1] : INFINITY;
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            if (i0 + u * kScoreThreads >= sv.n) continue;
+            const float2 v = __ldcg(x + (uint64_t)u * kScoreThreads * (gp / 2) + k / 2);
+            w[u] += exp2f(v.x - l0);
+            if (k + 1 < a.group) w[u] += exp2f(v.y - l1);
         }
-        *to = old + w;
+    }
+#pragma unroll
+    for (int u = 0; u < 4; u++) {
+        const uint32_t i = i0 + u * kScoreThreads;
+        if (i < sv.n) to[i < sv.sinks ? i : i + sv.shift] = old[u] + w[u];
     }
 }
 
 struct Plan {
-    uint32_t dp, nt, unit_heads, units, max_len, grid, chunks;
+    uint32_t dp, nt, unit_heads, units, max_len, tile, chunks;
     uint64_t max_seen, parts;
     bool split;
-    size_t part_o, part_ml, lse2, logits;  // elements
+    size_t part_o, part_ml, cut, lse2, logits;  // elements
 };
 
 // Sizes that follow from the host's arguments; false where they are refused.
@@ -183,23 +169,28 @@ bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t bloc
     p.unit_heads = 8 * p.nt;
     p.units = c->heads * (uint32_t)ceil_div(group, p.unit_heads);
     p.max_seen = !window ? max_len : (uint64_t)window + sinks < max_len ? (uint64_t)window + sinks : max_len;
-    const uint64_t unit_tiles = ceil_div(p.max_seen, kTile);
+    // Up to kWhole keys a unit is left to one block: splitting it would save
+    // less than the second launch costs.
+    p.tile = p.max_seen <= kWhole ? kWhole : kStep;
+    const uint64_t unit_tiles = ceil_div(p.max_seen, p.tile);
     const uint64_t all = unit_tiles * p.units * num_seqs;
     p.parts = all < kMaxBlocks ? all : kMaxBlocks;
     p.split = unit_tiles > 1;
     p.part_o = p.split ? 2 * p.parts * p.unit_heads * p.dp : 0;
     p.part_ml = p.split ? 2 * p.parts * p.unit_heads * 2 : 0;
+    p.cut = p.split ? p.parts : 0;
     p.lse2 = scores ? (size_t)num_seqs * q_heads : 0;
     p.logits = scores ? (size_t)num_seqs * c->heads * p.max_seen * ((group + 1) & ~1u) : 0;
     p.chunks = scores ? (uint32_t)ceil_div(p.max_seen, kScoreKeys) : 0;
-    return (uint64_t)num_seqs * (q_heads + (uint64_t)c->heads * p.chunks) < (1ull << 31);
+    return (uint64_t)num_seqs * c->heads * p.chunks < (1ull << 31);
 }
 
 size_t carve(const Plan &p, void *ws, Args *a) {
     Carver w(ws);
     float *po = w.take<float>(p.part_o), *pm = w.take<float>(p.part_ml);
+    uint4 *ct = w.take<uint4>(p.cut);
     float *ls = w.take<float>(p.lse2), *lg = w.take<float>(p.logits);
-    if (a) a->part_o = po, a->part_ml = pm, a->lse2 = p.lse2 ? ls : nullptr, a->logits = p.logits ? lg : nullptr;
+    if (a) a->part_o = po, a->part_ml = pm, a->cut = p.cut ? ct : nullptr, a->lse2 = p.lse2 ? ls : nullptr, a->logits = p.logits ? lg : nullptr;
     return w.off;
 }
 
@@ -241,33 +232,37 @@ extern "C" kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t
     a.logits_keys = p.max_seen;
     a.scale2 = scale * cache->k_scale * 1.4426950408889634f;
     a.num_seqs = num_seqs, a.q_heads = q_heads, a.group = q_heads / cache->heads, a.units = p.units;
-    a.blocks_per_seq = blocks_per_seq, a.max_len = p.max_len, a.window = window, a.sinks = sinks;
-    const uint64_t room = (uint64_t)sm_count() * 2;
-    a.grid = (uint32_t)(p.parts < room ? p.parts : room);
-    if (!a.grid) a.grid = 1;  // nothing to see anywhere: the zeros still have to be written
+    a.blocks_per_seq = blocks_per_seq, a.max_len = p.max_len, a.window = window, a.sinks = sinks, a.tile = p.tile;
     const cudaStream_t s = as_stream(stream);
     const uint32_t es = elem_size(cache->dtype);
     const bool ok = dtype == KVX_BF16
-                        ? (es == 2 ? launch<__nv_bfloat16, 2>(a, cache->dim, p.nt, s)
-                                   : launch<__nv_bfloat16, 1>(a, cache->dim, p.nt, s))
-                        : (es == 2 ? launch<__half, 2>(a, cache->dim, p.nt, s) : launch<__half, 1>(a, cache->dim, p.nt, s));
+                        ? (es == 2 ? launch<__nv_bfloat16, 2>(a, p.parts, cache->dim, p.nt, s)
+                                   : launch<__nv_bfloat16, 1>(a, p.parts, cache->dim, p.nt, s))
+                        : (es == 2 ? launch<__half, 2>(a, p.parts, cache->dim, p.nt, s)
+                                   : launch<__half, 1>(a, p.parts, cache->dim, p.nt, s));
     if (!ok) return KVX_ECUDA;
     KVX_LAUNCHED();
-    if (!p.split && !scores) return KVX_OK;
 
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_seqs * (q_heads + cache->heads * p.chunks));
-    cfg.blockDim = dim3(attend::kThreads);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = dtype == KVX_BF16
-                              ? cudaLaunchKernelEx(&cfg, k_finish<__nv_bfloat16>, a, p.dp, p.unit_heads, p.chunks)
-                              : cudaLaunchKernelEx(&cfg, k_finish<__half>, a, p.dp, p.unit_heads, p.chunks);
-    if (e != cudaSuccess) return KVX_ECUDA;
-    KVX_LAUNCHED();
+    if (p.split) {
+        cfg.gridDim = dim3(a.grid * (a.group < p.unit_heads ? a.group : p.unit_heads));
+        cfg.blockDim = dim3(32 * kJoinWarps);
+        const cudaError_t e = dtype == KVX_BF16 ? cudaLaunchKernelEx(&cfg, k_join<__nv_bfloat16>, a, p.dp, p.unit_heads)
+                                                : cudaLaunchKernelEx(&cfg, k_join<__half>, a, p.dp, p.unit_heads);
+        if (e != cudaSuccess) return KVX_ECUDA;
+        KVX_LAUNCHED();
+    }
+    if (p.chunks) {
+        cfg.gridDim = dim3(num_seqs * cache->heads * p.chunks);
+        cfg.blockDim = dim3(kScoreThreads);
+        if (cudaLaunchKernelEx(&cfg, k_scores, a, p.chunks) != cudaSuccess) return KVX_ECUDA;
+        KVX_LAUNCHED();
+    }
     return KVX_OK;
 }

@@ -3,7 +3,7 @@
 // point and the joining kernel.
 #pragma once
 
-#include <cuda_fp8.h>
+#include <type_traits>
 
 #include "kvx_cache.cuh"
 
@@ -12,7 +12,8 @@ namespace attend {
 
 constexpr int kWarps = 4;
 constexpr int kThreads = 32 * kWarps;
-constexpr uint32_t kTile = 16 * kWarps;  // keys of a block's step; the unit in which work is shared out
+constexpr uint32_t kStep = 16 * kWarps;  // keys of a block's step
+constexpr uint32_t kWhole = 256;         // keys up to which no unit is split
 constexpr uint32_t kMaxBlocks = 512;     // of the splitting grid: bounds the partial results in the workspace
 
 struct Args {
@@ -30,12 +31,14 @@ struct Args {
     // workspace
     float *part_o;   // [2 * blocks of the grid][heads of a unit][padded dim]: unnormalised outputs
     float *part_ml;  // [2 * blocks of the grid][heads of a unit][2]: base and sum
-    float *lse2;     // [num_seqs][q_heads]: log2 of the sum, of the units one block did
+    uint4 *cut;      // [blocks of the grid]: the unit whose first part the block did: sequence, unit, last block; or none
+    float *lse2;     // [num_seqs][q_heads]: log2 of the sum of the exponentials
     float *logits;   // [num_seqs][heads][visible][group rounded up to even], in powers of two
     uint64_t logits_keys;
     float scale2;    // scale * k_scale * log2(e)
     uint32_t num_seqs, q_heads, group, units;  // units: pieces of a sequence's heads that blocks take
     uint32_t blocks_per_seq, max_len, window, sinks, grid;
+    uint32_t tile;   // keys of a tile, in which work is shared out
 };
 
 // Visible tokens of a sequence: logical index i is token i below `sinks`, and
@@ -54,27 +57,10 @@ __device__ __forceinline__ Seen seen(const Args &a, uint32_t len) {
     return v;
 }
 
-__device__ __forceinline__ uint32_t tiles(uint32_t keys) { return (keys + kTile - 1) / kTile; }
-
-// Sum over the block, the same in every thread; sh holds a value per warp.
-__device__ __forceinline__ uint64_t block_sum(uint64_t v, uint64_t *sh) {
-#pragma unroll
-    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xFFFFFFFFu, v, o);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) sh[threadIdx.x >> 5] = v;
-    __syncthreads();
-    v = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; w++) v += sh[w];
-    return v;
-}
-
-// Tiles in a block's share.  Blocks take equal stretches of the tiles of all
-// units in order, so that a batch of any lengths keeps every SM busy to the
-// end.
-__device__ __forceinline__ uint64_t share_of(uint64_t total, uint32_t grid) {
-    const uint64_t s = (total + grid - 1) / grid;
-    return s ? s : 1;
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // ----------------------------------------------------------- tensor cores
@@ -103,10 +89,16 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
-// Two stored 8-bit values as two fp16 ones, exactly.
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)two, __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
+// The low or the high two of four stored 8-bit values as two fp16 ones, exactly.
+__device__ __forceinline__ uint32_t e4m3_lo(uint32_t four) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(r) : "r"(four));
+    return r;
+}
+__device__ __forceinline__ uint32_t e4m3_hi(uint32_t four) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(r) : "r"(four));
+    return r;
 }
 
 template <int BYTES>
@@ -137,8 +129,14 @@ struct Shape {
     static constexpr int kVElems = kVBytes / ES;
     static constexpr int kQVecs = kKChunks * (ES == 1 ? 2 : 1);           // 16-byte vectors of q per lane
     static constexpr int kStage = 2 * 16 * DP * ES;                       // bytes of a warp's 16 keys, K and V
-    static constexpr int kFit = 98304 / (kStage * kWarps);                 // stages of two blocks an SM
-    static constexpr int kStages = kFit < 3 ? 3 : kFit > 6 ? 6 : kFit;
+    // Blocks an SM has registers for, and stages that as many rings have room for.
+    static constexpr int kBlocks = DP == 256 ? (ES == 1 ? 2 : 1) : NT == 2 && DP == 128 ? 2 : 3;
+    static constexpr int kFit = 196608 / kBlocks / (kStage * kWarps);
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
+    static_assert(kStages >= 2, "");
+    // A unit's look-ups, first copies, query and output take about as long as
+    // a block takes for 32 KB: they count as so many tiles when work is shared out.
+    static constexpr uint32_t kExtra = DP * ES >= 256 ? 1 : 256 / (DP * ES);
     static constexpr int kORow = DP + 4;                                  // floats of a row when warps are joined
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kJoin = kWarps * kHeads * kORow * 4;
@@ -165,7 +163,7 @@ struct Shape {
 // rate to consume the measured bandwidth, and operands come to registers
 // without a transposition through shared memory that a larger tile would need.
 template <class T, int DP, int ES, int NT>
-__global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ Args a) {
+__global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_attend(const __grid_constant__ Args a) {
     using S = Shape<DP, ES, NT>;
     // the type in which the products are taken: 8-bit values are exact in fp16
     using C = typename std::conditional<ES == 1, __half, T>::type;
@@ -179,85 +177,98 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t g = lane >> 2, t4 = lane & 3;
     uint8_t *ring = smem + warp * (S::kStages * S::kStage);
+    // A V row's pieces lie together, as they arrive (scattered ones held the
+    // copies to three quarters of the bandwidth), in an order that keeps the
+    // eight or sixteen lanes that read at a time on different banks.
+    const uint32_t vslot = (t4 * 8 + (g ^ (S::kVBytes == 16 ? 2 * t4 : t4 / 2 * 4))) * S::kVBytes;
     uint4 *qs = reinterpret_cast<uint4 *>(smem + (S::kRing > S::kJoin ? S::kRing : S::kJoin));
     uint32_t bad = 0;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // ---- the block's share
+    // ---- the block's share: blocks take equal stretches of the tiles of all
+    // units in order, so that a batch of any lengths keeps every SM busy to
+    // the end.  Each thread counts the tiles of some sequences in a row.
+    const uint32_t per = (a.num_seqs + kThreads - 1) / kThreads;
+    const uint32_t n0 = threadIdx.x * per, n1 = n0 + per < a.num_seqs ? n0 + per : a.num_seqs;
+    auto unit_tiles = [&](uint32_t keys) { return (keys + a.tile - 1) / a.tile; };
     uint64_t mine = 0;
-    for (uint32_t n = threadIdx.x; n < a.num_seqs; n += kThreads) {
-        const uint32_t len = a.lens[n];
+    bool none = false;
+    for (uint32_t n = n0; n < n1; n++) {
+        const uint32_t len = a.lens[n], keys = seen(a, len).n;
         if (blockIdx.x == 0 && len > a.max_len) bad |= KVX_S_BOUNDS;
-        mine += tiles(seen(a, len).n);
+        if (keys)
+            mine += unit_tiles(keys) + S::kExtra;
+        else
+            none |= n % gridDim.x == blockIdx.x;
     }
-    const uint64_t total = block_sum(mine, sh_sum) * a.units;
-    const uint64_t share = share_of(total, a.grid);
+    uint64_t upto = warp_incl_sum(mine), total = 0;
+    if (lane == 31) sh_sum[warp] = upto;
+    none = __syncthreads_or(none);
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+        if (w < (int)warp) upto += sh_sum[w];
+        total += sh_sum[w];
+    }
+    total *= a.units;
+    const uint64_t share = (total + a.grid - 1) / a.grid;
     uint64_t at = blockIdx.x * share;
-    const uint64_t end = at + share < total ? at + share : total;
-
-    // sequences without a visible token
-    for (uint32_t n = blockIdx.x; n < a.num_seqs; n += gridDim.x) {
-        if (seen(a, a.lens[n]).n) continue;
-        for (uint32_t i = threadIdx.x; i < a.q_heads * a.c.dim; i += kThreads)
-            static_cast<T *>(a.out)[n * a.out_stride + i] = T(0.0f);
-        if (a.lse)
-            for (uint32_t i = threadIdx.x; i < a.q_heads; i += kThreads) a.lse[(uint64_t)n * a.q_heads + i] = -INFINITY;
+    const uint64_t begin = at, end = at + share < total ? at + share : total;
+    if (at < end && (upto - mine) * a.units <= at && at < upto * a.units) {  // one thread
+        uint64_t before = (upto - mine) * a.units;
+        uint32_t n = n0;
+        for (;; n++) {
+            const uint32_t keys = seen(a, a.lens[n]).n;
+            const uint64_t m = keys ? (uint64_t)(unit_tiles(keys) + S::kExtra) * a.units : 0;
+            if (at < before + m) break;
+            before += m;
+        }
+        sh_n = n;
+        sh_first = before;
     }
+    if (none)  // sequences without a visible token
+        for (uint32_t n = blockIdx.x; n < a.num_seqs; n += gridDim.x) {
+            if (seen(a, a.lens[n]).n) continue;
+            for (uint32_t i = threadIdx.x; i < a.q_heads * a.c.dim; i += kThreads)
+                static_cast<T *>(a.out)[n * a.out_stride + i] = T(0.0f);
+            for (uint32_t i = threadIdx.x; i < a.q_heads; i += kThreads)
+                if (a.lse) a.lse[(uint64_t)n * a.q_heads + i] = -INFINITY;
+        }
     if (at >= end) {
+        if (a.cut && threadIdx.x == 0) a.cut[blockIdx.x].x = kNone;
         raise(a.status, bad);
         return;
     }
-
-    // ---- the sequence of the first tile
-    {
-        uint64_t before = 0;
-        for (uint32_t n0 = 0;; n0 += kThreads) {
-            const uint32_t n = n0 + threadIdx.x;
-            const uint64_t m = n < a.num_seqs ? tiles(seen(a, a.lens[n]).n) : 0;
-            uint64_t incl = warp_incl_sum(m);
-            __syncthreads();
-            if (lane == 31) sh_sum[warp] = incl;
-            if (threadIdx.x == 0) sh_n = kNone;
-            __syncthreads();
-            uint64_t sum = 0;
-#pragma unroll
-            for (int w = 0; w < kWarps; w++) {
-                if (w < (int)warp) incl += sh_sum[w];
-                sum += sh_sum[w];
-            }
-            incl += before;
-            if (m && (incl - m) * a.units <= at && at < incl * a.units) {
-                sh_n = n;
-                sh_first = incl - m;
-            }
-            __syncthreads();
-            if (sh_n != kNone) break;
-            before += sum;
-        }
-    }
+    __syncthreads();
     uint32_t n = sh_n;
-    uint64_t seq_tile = at - sh_first * a.units;  // within the sequence's units
+    uint64_t seq_tile = at - sh_first;  // within the sequence's units
     Seen sv = seen(a, a.lens[n]);
-    uint32_t nt = tiles(sv.n);
-    const uint64_t begin = at;
+    uint32_t nt = unit_tiles(sv.n), len_u = nt + S::kExtra;
     const uint32_t units_per_head = (a.group + S::kHeads - 1) / S::kHeads;
 
     // ---- one piece of a unit after the other
-    while (at < end) {
-        while (seq_tile >= (uint64_t)nt * a.units) {
-            seq_tile -= (uint64_t)nt * a.units;
+    for (uint64_t next; at < end; seq_tile += next - at, at = next) {
+        while (seq_tile >= (uint64_t)len_u * a.units) {
+            seq_tile -= (uint64_t)len_u * a.units;
             do sv = seen(a, a.lens[++n]);
             while (!sv.n);
-            nt = tiles(sv.n);
+            nt = unit_tiles(sv.n);
+            len_u = nt + S::kExtra;
         }
-        const uint32_t unit = (uint32_t)(seq_tile / nt), tile0 = (uint32_t)(seq_tile - (uint64_t)unit * nt);
-        const uint32_t ntile = (uint32_t)((uint64_t)(nt - tile0) < end - at ? nt - tile0 : end - at);
+        const uint32_t unit = (uint32_t)(seq_tile / len_u), from = (uint32_t)(seq_tile - (uint64_t)unit * len_u);
+        const uint32_t to = (uint32_t)(len_u - from < end - at ? len_u : from + (end - at));
+        next = at + (to - from);
+        // the kExtra that stand for the unit's overhead come first
+        const uint32_t tile0 = from > S::kExtra ? from - S::kExtra : 0, tile1 = to > S::kExtra ? to - S::kExtra : 0;
+        const bool whole = tile0 == 0 && tile1 == nt;
+        if (a.cut && threadIdx.x == 0 && next == end)
+            a.cut[blockIdx.x] = make_uint4(tile0 == 0 && tile1 && !whole ? n : kNone, unit,
+                                           (uint32_t)((at - from + len_u - 1) / share), at != begin);
+        if (tile0 == tile1) continue;
         const uint32_t head = unit / units_per_head, qh0 = unit % units_per_head * S::kHeads;
         const uint32_t nheads = a.group - qh0 < S::kHeads ? a.group - qh0 : S::kHeads;
         const uint32_t q0 = head * a.group + qh0;
-        const uint32_t k0 = tile0 * kTile;
-        const uint32_t k1 = (tile0 + ntile) * kTile < sv.n ? (tile0 + ntile) * kTile : sv.n;
+        const uint32_t k0 = tile0 * a.tile, k1 = tile1 * a.tile < sv.n ? tile1 * a.tile : sv.n;
 
         // -- this lane looks up key lane%16's K (lanes 0-15) or V segment
         const uint32_t *seq_blocks = a.blocks + (uint64_t)n * a.blocks_per_seq;
@@ -281,46 +292,57 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
             return seg + place * a.c.token_stride;
         };
         const uint32_t warp_keys = k1 - k0;
-        const uint32_t steps = warp_keys > warp * 16 ? (warp_keys - warp * 16 + kTile - 1) / kTile : 0;
-        // -- asynchronous copies of tile j's pieces into its stage
+        const uint32_t steps = warp_keys > warp * 16 ? (warp_keys - warp * 16 + kStep - 1) / kStep : 0;
+        // -- asynchronous copies of tile j's pieces into its stage: where a row
+        // or a piece does not exist, zeros (a copy of no bytes reads nothing)
         auto fetch = [&](uint32_t j, uint64_t row) {
-            uint8_t *st = ring + (j % S::kStages) * S::kStage + lane * 16;
-            const uint32_t dst = smem_u32(st);
+            const uint32_t kdst = smem_u32(ring + (j % S::kStages) * S::kStage + lane * 16);
+            const uint32_t vdst = smem_u32(ring + (j % S::kStages) * S::kStage + S::kStage / 2 + vslot);
+            const uint8_t *p[6];
+            uint32_t n[6];
 #pragma unroll
-            for (int r = 0; r < 2; r++) {
-                const uint64_t src = __shfl_sync(0xFFFFFFFFu, row, g + 8 * r);
-                const bool none = src == ~0ull;
-                const uint8_t *p = a.c.pool + (none ? 0 : src) + t4 * 16;
-#pragma unroll
-                for (int c = 0; c < S::kKChunks; c++) {
-                    const bool in = !none && c * 64 + t4 * 16 < a.c.row_bytes;
-                    copy_async<16>(dst + (c * 2 + r) * 512, in ? p + c * 64 : a.c.pool, in ? 16 : 0);
-                }
+            for (int r = 0; r < 6; r++) {
+                const uint32_t from = r < 2 ? g + 8 * r : 16 + 2 * t4 + (r & 1) + 8 * ((r - 2) >> 1);
+                const uint64_t src = __shfl_sync(0xFFFFFFFFu, row, from);
+                n[r] = src == ~0ull ? 0 : r < 2 ? 16 : S::kVBytes;
+                p[r] = a.c.pool + (src == ~0ull ? 0 : src) + (r < 2 ? t4 * 16 : g * S::kVBytes);
             }
-            const uint32_t vdst = smem_u32(ring + (j % S::kStages) * S::kStage + S::kStage / 2 + lane * S::kVBytes);
+            if (a.c.row_bytes == DP * ES) {
 #pragma unroll
-            for (int r = 0; r < 4; r++) {
-                const uint64_t src = __shfl_sync(0xFFFFFFFFu, row, 16 + 2 * t4 + (r & 1) + 8 * (r >> 1));
-                const bool none = src == ~0ull;
-                const uint8_t *p = a.c.pool + (none ? 0 : src) + g * S::kVBytes;
+                for (int r = 0; r < 2; r++)
 #pragma unroll
-                for (int c = 0; c < S::kVParts; c++) {
-                    const bool in = !none && c * 8 * S::kVBytes + g * S::kVBytes < a.c.row_bytes;
-                    copy_async<S::kVBytes>(vdst + (c * 4 + r) * 32 * S::kVBytes,
-                                           in ? p + c * 8 * S::kVBytes : a.c.pool, in ? S::kVBytes : 0);
-                }
+                    for (int c = 0; c < S::kKChunks; c++) copy_async<16>(kdst + (c * 2 + r) * 512, p[r] + c * 64, n[r]);
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+#pragma unroll
+                    for (int c = 0; c < S::kVParts; c++)
+                        copy_async<S::kVBytes>(vdst + (c * 4 + r) * 32 * S::kVBytes, p[2 + r] + c * 8 * S::kVBytes, n[2 + r]);
+            } else {
+#pragma unroll
+                for (int r = 0; r < 2; r++)
+#pragma unroll
+                    for (int c = 0; c < S::kKChunks; c++)
+                        copy_async<16>(kdst + (c * 2 + r) * 512, p[r] + c * 64,
+                                       c * 64 + t4 * 16 < a.c.row_bytes ? n[r] : 0);
+#pragma unroll
+                for (int r = 0; r < 4; r++)
+#pragma unroll
+                    for (int c = 0; c < S::kVParts; c++)
+                        copy_async<S::kVBytes>(vdst + (c * 4 + r) * 32 * S::kVBytes, p[2 + r] + c * 8 * S::kVBytes,
+                                               (c * 8 + g) * S::kVBytes < a.c.row_bytes ? n[2 + r] : 0);
             }
         };
 
-        // look-ups run ahead of the copies: the block of one tile, the address
-        // of the tile before it
-        uint32_t b1 = kNone, p1 = 0, b2 = kNone, p2 = 0;
+        // look-ups run ahead of the copies: the address of one tile, the block of
+        // the next and of the one after, whose address is fetched into L2
+        uint32_t b1 = kNone, p1 = 0, b2 = kNone, p2 = 0, b3 = kNone, p3 = 0;
         uint64_t row = ~0ull, seg1 = ~0ull;
         {
             uint32_t b0, p0 = 0;
             b0 = find_block(0, p0);
             b1 = find_block(1, p1);
             b2 = find_block(2, p2);
+            b3 = find_block(3, p3);
             const uint64_t seg0 = find_addr(b0);
             seg1 = find_addr(b1);
             row = resolve(seg0, p0, b0);
@@ -330,7 +352,10 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
             b1 = b2;
             p1 = p2;
             seg1 = find_addr(b1);
-            b2 = find_block(j + 3, p2);
+            b2 = b3;
+            p2 = p3;
+            if (b2 != kNone) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.lane_addr(b2, head, kv)));
+            b3 = find_block(j + 4, p3);
         };
 #pragma unroll
         for (int j = 0; j < S::kStages - 1; j++) {
@@ -384,11 +409,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
         }
         __syncthreads();
 
-        // Weights are taken as 2^(logit - base), the base lying kBoost below
-        // the running maximum m: in fp16, whose smallest step is 2^-24, small
-        // weights keep ten bits more beside a large one.
-        constexpr float kBoost = std::is_same<C, __half>::value ? 10.0f : 0.0f;
-        float scale2[NT][2], m[NT][2], base[NT][2], l[NT][2];
+        // Weights are taken as 2^(logit - base).  The base follows the running
+        // maximum only when a logit exceeds it by more than kSlack + kBoost:
+        // sums and outputs are divided by the same power in the end, and the
+        // few octaves above 1 do not matter to 32-bit sums.  It lies kBoost
+        // below that maximum, so that in fp16, whose smallest step is 2^-24,
+        // small weights keep some bits more beside a large one.
+        constexpr float kSlack = 8.0f, kBoost = std::is_same<C, __half>::value ? 7.0f : 0.0f;
+        float scale2[NT][2], limit[NT][2], base[NT][2], l[NT][2];  // limit: base + kBoost + kSlack
         constexpr int kOTiles = DP / 16;
         float o[kOTiles][NT][4];
 #pragma unroll
@@ -396,7 +424,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
 #pragma unroll
             for (int i = 0; i < 2; i++) {
                 scale2[x][i] = a.scale2 * sh_qscale[x * 8 + 2 * t4 + i];
-                m[x][i] = -INFINITY, base[x][i] = 0, l[x][i] = 0;
+                limit[x][i] = -INFINITY, base[x][i] = 0, l[x][i] = 0;
             }
 #pragma unroll
         for (int j = 0; j < kOTiles; j++)
@@ -416,7 +444,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
             const uint8_t *st = ring + (j % S::kStages) * S::kStage;
 
             // S^T = K Q^T
-            float s[NT][4] = {};
+            float s[NT][4] = {}, s2[NT][4] = {};  // two chains of products
 #pragma unroll
             for (int c = 0; c < S::kKChunks; c++) {
                 const uint4 r0 = *reinterpret_cast<const uint4 *>(st + (c * 2) * 512 + lane * 16);
@@ -426,18 +454,17 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
                     for (int x = 0; x < NT; x++) {
                         const uint4 qv = qs[(x * S::kQVecs + c) * 32 + lane];
                         mma<C>(s[x], r0.x, r1.x, r0.y, r1.y, qv.x, qv.y);
-                        mma<C>(s[x], r0.z, r1.z, r0.w, r1.w, qv.z, qv.w);
+                        mma<C>(s2[x], r0.z, r1.z, r0.w, r1.w, qv.z, qv.w);
                     }
                 } else {
 #pragma unroll
                     for (int w = 0; w < 4; w++) {
                         const uint32_t w0 = word(r0, w), w1 = word(r1, w);
-                        const uint32_t a0 = e4m3x2_to_f16x2(w0 & 0xFFFF), a2 = e4m3x2_to_f16x2(w0 >> 16);
-                        const uint32_t a1 = e4m3x2_to_f16x2(w1 & 0xFFFF), a3 = e4m3x2_to_f16x2(w1 >> 16);
+                        const uint32_t a0 = e4m3_lo(w0), a1 = e4m3_lo(w1), a2 = e4m3_hi(w0), a3 = e4m3_hi(w1);
 #pragma unroll
                         for (int x = 0; x < NT; x++) {
                             const uint4 qv = qs[(x * S::kQVecs + c * 2 + w / 2) * 32 + lane];
-                            mma<C>(s[x], a0, a1, a2, a3, w % 2 ? qv.z : qv.x, w % 2 ? qv.w : qv.y);
+                            mma<C>(w % 2 ? s2[x] : s[x], a0, a1, a2, a3, w % 2 ? qv.z : qv.x, w % 2 ? qv.w : qv.y);
                         }
                     }
                 }
@@ -450,9 +477,9 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
             for (int x = 0; x < NT; x++) {
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
-                    s[x][i] *= scale2[x][i & 1];
+                    s[x][i] = (s[x][i] + s2[x][i]) * scale2[x][i & 1];
                     if ((i < 2 ? i0 : i1) >= k1) s[x][i] = -INFINITY;
-                    higher |= s[x][i] > m[x][i & 1];
+                    higher |= s[x][i] > limit[x][i & 1];
                 }
                 if (a.logits) {
                     const uint32_t gp = (a.group + 1) & ~1u, hh = qh0 + x * 8 + 2 * t4;
@@ -463,8 +490,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
                     }
                 }
             }
-            // A new maximum is rare after the first tiles: only then are the
-            // sums so far scaled to it.
             if (__any_sync(0xFFFFFFFFu, higher)) {
                 float f[NT][2];
 #pragma unroll
@@ -474,10 +499,12 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
                         float top = fmaxf(s[x][i], s[x][i + 2]);
 #pragma unroll
                         for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
-                        top = fmaxf(top, m[x][i]);
-                        f[x][i] = m[x][i] == -INFINITY ? 1.0f : exp2f(m[x][i] - top);
-                        m[x][i] = top;
-                        base[x][i] = top == -INFINITY ? 0.0f : top - kBoost;  // exp2(-inf - 0) = 0, not NaN
+                        f[x][i] = 1.0f;
+                        if (top - kBoost > base[x][i] || (limit[x][i] == -INFINITY && top > -INFINITY)) {
+                            if (limit[x][i] > -INFINITY) f[x][i] = exp2_fast(base[x][i] - (top - kBoost));
+                            base[x][i] = top - kBoost;
+                            limit[x][i] = top + kSlack;
+                        }
                         l[x][i] *= f[x][i];
                     }
 #pragma unroll
@@ -496,7 +523,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
             for (int x = 0; x < NT; x++)
 #pragma unroll
                 for (int r = 0; r < 2; r++) {
-                    const float p0 = exp2f(s[x][2 * r] - base[x][0]), p1 = exp2f(s[x][2 * r + 1] - base[x][1]);
+                    const float p0 = exp2_fast(s[x][2 * r] - base[x][0]), p1 = exp2_fast(s[x][2 * r + 1] - base[x][1]);
                     l[x][0] += p0;
                     l[x][1] += p1;
                     const uint32_t hi = Pair<C>::pack(p0, p1);
@@ -506,7 +533,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
                 }
 
             // O^T += V^T P^T
-            const uint8_t *sv_ = st + S::kStage / 2 + lane * S::kVBytes;
+            const uint8_t *sv_ = st + S::kStage / 2 + vslot;
 #pragma unroll
             for (int c = 0; c < S::kVParts; c++) {
                 uint32_t v[4][S::kVBytes / 4];
@@ -537,8 +564,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
                         for (int y = 0; y < 2; y++) {
                             const uint32_t e = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
                             const uint32_t f = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
-                            const uint32_t a0 = e4m3x2_to_f16x2(e & 0xFFFF), a1 = e4m3x2_to_f16x2(e >> 16);
-                            const uint32_t a2 = e4m3x2_to_f16x2(f & 0xFFFF), a3 = e4m3x2_to_f16x2(f >> 16);
+                            const uint32_t a0 = e4m3_lo(e), a1 = e4m3_hi(e), a2 = e4m3_lo(f), a3 = e4m3_hi(f);
                             constexpr int per = S::kVBytes / 2;  // output tiles of a part
 #pragma unroll
                             for (int x = 0; x < NT; x++) {
@@ -560,7 +586,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
 #pragma unroll
                 for (int k = 4; k < 32; k <<= 1) l[x][i] += __shfl_xor_sync(0xFFFFFFFFu, l[x][i], k);
                 if (g == 0) {
-                    sh_ml[warp][x * 8 + 2 * t4 + i][0] = m[x][i] == -INFINITY ? -INFINITY : base[x][i];
+                    sh_ml[warp][x * 8 + 2 * t4 + i][0] = limit[x][i] == -INFINITY ? -INFINITY : base[x][i];
                     sh_ml[warp][x * 8 + 2 * t4 + i][1] = l[x][i];
                 }
             }
@@ -574,7 +600,7 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
                 float top = sh_ml[0][hh][0];
 #pragma unroll
                 for (int w = 1; w < kWarps; w++) top = fmaxf(top, sh_ml[w][hh][0]);
-                const float f = m[x][i] == -INFINITY ? 0.0f : exp2f(base[x][i] - top);
+                const float f = limit[x][i] == -INFINITY ? 1.0f : exp2f(base[x][i] - top);  // 1: zeros, or a NaN
                 float *to = join + (warp * S::kHeads + hh) * S::kORow;
 #pragma unroll
                 for (int c = 0; c < S::kVParts; c++)
@@ -586,7 +612,6 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
                     }
             }
         __syncthreads();
-        const bool whole = ntile == nt;
         const uint32_t slot = 2 * blockIdx.x + (at != begin);
         for (uint32_t i = threadIdx.x * 4; i < nheads * DP; i += kThreads * 4) {
             const uint32_t hh = i / DP, d = i % DP;
@@ -624,18 +649,14 @@ __global__ void __launch_bounds__(kThreads, 2) k_attend(const __grid_constant__ 
             }
         }
         __syncthreads();  // the ring takes the next piece's copies
-        at += ntile;
-        seq_tile += ntile;
     }
     raise(a.status, bad);
 }
 
-// Launches one variant; false where the launch failed.
-template <class T, int ES>
-bool launch(const Args &a, uint32_t dim, uint32_t nt, cudaStream_t s);
-
+// Launches one variant over at most `parts` blocks, and leaves their number in
+// a.grid; false where that failed.
 template <class T, int DP, int ES, int NT>
-bool launch_one(const Args &a, cudaStream_t s) {
+bool launch_one(Args &a, uint64_t parts, cudaStream_t s) {
     using S = Shape<DP, ES, NT>;
     static bool done[64];
     int dev = 0;
@@ -646,15 +667,18 @@ bool launch_one(const Args &a, cudaStream_t s) {
             return false;
         if (dev >= 0 && dev < 64) done[dev] = true;
     }
+    const uint64_t room = (uint64_t)sm_count() * S::kBlocks;
+    a.grid = (uint32_t)(parts < room ? parts : room);
+    if (!a.grid) a.grid = 1;  // nothing to see anywhere: the zeros still have to be written
     k_attend<T, DP, ES, NT><<<a.grid, kThreads, S::kSmem, s>>>(a);
     return true;
 }
 
 template <class T, int ES>
-bool launch(const Args &a, uint32_t dim, uint32_t nt, cudaStream_t s) {
-    if (dim <= 64) return nt == 1 ? launch_one<T, 64, ES, 1>(a, s) : launch_one<T, 64, ES, 2>(a, s);
-    if (dim <= 128) return nt == 1 ? launch_one<T, 128, ES, 1>(a, s) : launch_one<T, 128, ES, 2>(a, s);
-    return launch_one<T, 256, ES, 1>(a, s);
+bool launch(Args &a, uint64_t parts, uint32_t dim, uint32_t nt, cudaStream_t s) {
+    if (dim <= 64) return nt == 1 ? launch_one<T, 64, ES, 1>(a, parts, s) : launch_one<T, 64, ES, 2>(a, parts, s);
+    if (dim <= 128) return nt == 1 ? launch_one<T, 128, ES, 1>(a, parts, s) : launch_one<T, 128, ES, 2>(a, parts, s);
+    return launch_one<T, 256, ES, 1>(a, parts, s);
 }
 
 }  // namespace attend

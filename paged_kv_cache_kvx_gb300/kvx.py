@@ -519,7 +519,7 @@ class Transfer:
 
 
 _DTYPES = {torch.bfloat16: KVX_BF16, torch.float16: KVX_F16, torch.float8_e4m3fn: KVX_E4M3}
-_IDS = (torch.int32, torch.uint32)
+_ACTS, _IDS, _SLOTS, _FLOAT = (torch.bfloat16, torch.float16), (torch.int32, torch.uint32), (torch.int64,), (torch.float32,)
 
 
 def _need(ok, what):
@@ -527,18 +527,20 @@ def _need(ok, what):
         raise KvxError(what)
 
 
-def _heads(t, name, dim, dtype=None):
-    """A [tokens, heads, dim] activation whose tokens' heads are contiguous."""
-    _need(t.dim() == 3 and t.size(2) == dim and (t.numel() == 0 or (t.stride(2) == 1 and (t.size(1) == 1 or
-          t.stride(1) == dim))), "%s: [tokens, heads, %d] with a token's heads contiguous" % (name, dim))
-    _need(t.dtype in (torch.bfloat16, torch.float16) and dtype in (None, t.dtype), "%s: wrong type %s" % (name, t.dtype))
-    # a single token's stride says nothing
-    return t.stride(0) if t.size(0) > 1 else t.size(1) * dim
+def _heads(t, name, shape, dtype):
+    """The distance between tokens, in elements, of an activation [tokens, heads,
+    dim] whose tokens' heads are contiguous."""
+    dim = shape[2]
+    if t.shape == shape and t.dtype is dtype:
+        token, head, one = t.stride()
+        if (one == 1 and (head == dim or shape[1] < 2)) or t.numel() == 0:
+            return token if shape[0] > 1 else shape[1] * dim  # a single token's stride says nothing
+    raise KvxError("%s: %s %s with a token's heads contiguous" % (name, dtype, list(shape)))
 
 
 def _table(t, name, dtypes, shape):
-    _need(t.dtype in dtypes and t.is_contiguous() and tuple(t.shape) == tuple(shape),
-          "%s: contiguous %s of %s" % (name, list(shape), " or ".join(str(d) for d in dtypes)))
+    if not (t.shape == shape and t.dtype in dtypes and t.is_contiguous()):
+        raise KvxError("%s: contiguous %s of %s" % (name, list(shape), " or ".join(str(d) for d in dtypes)))
 
 
 class Cache:
@@ -569,21 +571,24 @@ class Cache:
         """kvx_append_tokens: q [T, q_heads, dim], k and v [T, heads, dim] (views of
         one projection's output will do); positions int32 [T]; slots int64 [T];
         cos_sin float [max_pos, rot_dim]; q_out as q, or q itself."""
-        T, dim = q.size(0), self.dim
-        strides = [_heads(t, name, dim, q.dtype) for t, name in ((q, "q"), (k, "k"), (v, "v"), (q_out, "q_out"))]
-        _need(k.shape == v.shape == (T, self.heads, dim) and q_out.shape == q.shape, "q, k, v, q_out: shapes differ")
-        _table(slots, "slots", (torch.int64,), (T,))
-        for w in (q_weight, k_weight):
-            if w is not None:
-                _table(w, "weight", (q.dtype,), (dim,))
+        _need(q.dim() == 3, "q: [tokens, q_heads, dim]")
+        (T, q_heads, _), act, dim = q.shape, q.dtype, self.dim
+        _need(act in _ACTS, "q: bfloat16 or float16")
+        kv = (T, self.heads, dim)
+        qs, ks, vs = _heads(q, "q", (T, q_heads, dim), act), _heads(k, "k", kv, act), _heads(v, "v", kv, act)
+        os_ = _heads(q_out, "q_out", (T, q_heads, dim), act)
+        _table(slots, "slots", _SLOTS, (T,))
+        if q_weight is not None:
+            _table(q_weight, "q_weight", (act,), (dim,))
+        if k_weight is not None:
+            _table(k_weight, "k_weight", (act,), (dim,))
         max_pos = rot = 0
         if cos_sin is not None:
             max_pos, rot = cos_sin.shape
-            _table(cos_sin, "cos_sin", (torch.float32,), (max_pos, rot))
+            _table(cos_sin, "cos_sin", _FLOAT, (max_pos, rot))
             _table(positions, "positions", _IDS, (T,))
-        kvx_append_tokens(self.c, q, strides[0], k, strides[1], v, strides[2], _DTYPES[q.dtype], T, q.size(1), q_weight,
-                          k_weight, eps, cos_sin, rot, max_pos, int(interleaved), positions, slots, q_out, strides[3],
-                          self.status, stream)
+        kvx_append_tokens(self.c, q, qs, k, ks, v, vs, _DTYPES[act], T, q_heads, q_weight, k_weight, eps, cos_sin, rot,
+                          max_pos, 1 if interleaved else 0, positions, slots, q_out, os_, self.status, stream)
 
     def attend_workspace(self, num_seqs: int, q_heads: int, blocks_per_seq: int, window: int = 0, sinks: int = 0,
                          scores: bool = False):
@@ -597,19 +602,19 @@ class Cache:
         blocks_per_seq]; lens int32 [num_seqs]; lse float [num_seqs, q_heads];
         scores float [num_seqs, heads, stride], added to.  scale defaults to
         1/sqrt(dim)."""
-        N, dim = q.size(0), self.dim
-        qs, os_ = _heads(q, "q", dim), _heads(out, "out", dim, q.dtype)
-        _need(out.shape == q.shape, "out: not q's shape")
-        _need(blocks.dim() == 2, "blocks: [num_seqs, blocks_per_seq]")
-        _table(blocks, "blocks", _IDS, (N, blocks.size(1)))
+        _need(q.dim() == 3 and blocks.dim() == 2, "q: [num_seqs, q_heads, dim], blocks: [num_seqs, blocks_per_seq]")
+        (N, q_heads, _), act, dim, per, stride = q.shape, q.dtype, self.dim, blocks.shape[1], 0
+        _need(act in _ACTS, "q: bfloat16 or float16")
+        qs, os_ = _heads(q, "q", (N, q_heads, dim), act), _heads(out, "out", (N, q_heads, dim), act)
+        _table(blocks, "blocks", _IDS, (N, per))
         _table(lens, "lens", _IDS, (N,))
         if lse is not None:
-            _table(lse, "lse", (torch.float32,), (N, q.size(1)))
+            _table(lse, "lse", _FLOAT, (N, q_heads))
         if scores is not None:
-            _table(scores, "scores", (torch.float32,), (N, self.heads, scores.size(-1)))
-        kvx_attend(self.c, q, qs, _DTYPES[q.dtype], N, q.size(1), blocks, blocks.size(1), lens,
-                   dim ** -0.5 if scale is None else scale, window, sinks, out, os_, lse, scores,
-                   0 if scores is None else scores.size(-1), self.status, ws, stream)
+            stride = scores.shape[-1]
+            _table(scores, "scores", _FLOAT, (N, self.heads, stride))
+        kvx_attend(self.c, q, qs, _DTYPES[act], N, q_heads, blocks, per, lens, dim ** -0.5 if scale is None else scale,
+                   window, sinks, out, os_, lse, scores, stride, self.status, ws, stream)
 
     def evict_workspace(self, num_seqs: int, blocks_per_seq: int, budget: int):
         n = kvx_evict_workspace_size(self.c, num_seqs, blocks_per_seq, budget)
@@ -620,19 +625,18 @@ class Cache:
               stream=None):
         """kvx_evict: kept int32 and kept_scores float [num_seqs, heads, budget];
         dst_blocks int32 [num_seqs, dst_per_seq]; new_lens int32 [num_seqs]."""
-        N = lens.size(0)
         _need(blocks.dim() == 2 and dst_blocks.dim() == 2 and kept.dim() == 3, "evict: blocks and dst_blocks are "
               "[num_seqs, pages], kept is [num_seqs, heads, budget]")
-        _table(blocks, "blocks", _IDS, (N, blocks.size(1)))
+        (N, per), dper, heads, budget, stride = blocks.shape, dst_blocks.shape[1], self.heads, kept.shape[2], scores.shape[-1]
+        _table(blocks, "blocks", _IDS, (N, per))
         _table(lens, "lens", _IDS, (N,))
-        _table(scores, "scores", (torch.float32,), (N, self.heads, scores.size(-1)))
-        _table(dst_blocks, "dst_blocks", _IDS, (N, dst_blocks.size(1)))
-        budget = kept.size(2)
-        _table(kept, "kept", _IDS, (N, self.heads, budget))
-        _table(kept_scores, "kept_scores", (torch.float32,), (N, self.heads, budget))
+        _table(scores, "scores", _FLOAT, (N, heads, stride))
+        _table(dst_blocks, "dst_blocks", _IDS, (N, dper))
+        _table(kept, "kept", _IDS, (N, heads, budget))
+        _table(kept_scores, "kept_scores", _FLOAT, (N, heads, budget))
         _table(new_lens, "new_lens", _IDS, (N,))
-        kvx_evict(self.c, N, blocks, blocks.size(1), lens, scores, scores.size(-1), budget, sinks, recent, dst_blocks,
-                  dst_blocks.size(1), kept, kept_scores, new_lens, self.status, ws, stream)
+        kvx_evict(self.c, N, blocks, per, lens, scores, stride, budget, sinks, recent, dst_blocks, dper, kept, kept_scores,
+                  new_lens, self.status, ws, stream)
 
     def read_status(self) -> int:
         return int(_u32_np(self.status)[0])
