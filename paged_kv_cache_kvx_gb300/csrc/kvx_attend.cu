@@ -29,31 +29,20 @@ constexpr int kJoinUnroll = 8;  // parts whose loads a warp has in flight
 constexpr int kScoreThreads = 128;
 constexpr uint32_t kScoreKeys = 4 * kScoreThreads;  // of a block that adds weights
 
-// Block (c, hh) joins query head hh of the unit whose first part block c of
-// k_attend did; its other parts are the first ones of blocks c+1 .. last.
 template <class T>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant__ Args a, uint32_t dp,
-                                                          uint32_t unit_heads) {
-    __shared__ float sh_m[kJoinWarps], sh_l[kJoinWarps];
-    __shared__ float4 sh_o[kJoinWarps][32];
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t heads = a.group < unit_heads ? a.group : unit_heads;
-    const uint32_t first = blockIdx.x / heads, hh = blockIdx.x % heads;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    const uint4 cut = __ldcg(a.cut + first);
-    if (cut.x == kNone) return;
-    const uint32_t per_head = (a.group + unit_heads - 1) / unit_heads;
-    const uint32_t in = cut.y % per_head * unit_heads + hh, qh = cut.y / per_head * a.group + in;
-    if (in >= a.group) return;
-    const uint32_t n = cut.x, last = cut.z;
-    auto slot = [&](uint32_t c) { return (uint64_t)(2 * c + (c == first && cut.w)) * unit_heads + hh; };
+__device__ __forceinline__ void join_unit(const Args &a, uint32_t dp, uint32_t unit_heads, const uint4 &cut,
+                                          uint32_t first, uint32_t hh, uint32_t qh, uint32_t lane, uint32_t warp,
+                                          float *sh_m, float *sh_l, float4 (*sh_o)[32]) {
+    const uint32_t n = cut.x, step = cut.w >> 31 ? a.chunks : 1, parts = (cut.z - first) / step + 1;
+    auto slot = [&](uint32_t i) {
+        return (uint64_t)(i ? 2 * (first + i * step) : cut.w & 0x7FFFFFFFu) * unit_heads + hh;
+    };
     // each warp takes every fourth part; a lane four of 128 values at a time
     for (uint32_t d0 = 0; d0 < dp; d0 += 128) {
         const uint32_t d = d0 + lane * 4;
         float4 v = make_float4(0, 0, 0, 0);
         float top = -INFINITY, sum = 0;
-        for (uint32_t c0 = first + warp; c0 <= last; c0 += kJoinWarps * kJoinUnroll) {
+        for (uint32_t c0 = warp; c0 < parts; c0 += kJoinWarps * kJoinUnroll) {
             float2 ml[kJoinUnroll];
             float4 x[kJoinUnroll];
             float higher = top;
@@ -62,8 +51,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
                 const uint32_t c = c0 + u * kJoinWarps;
                 ml[u] = make_float2(-INFINITY, 0);
                 x[u] = make_float4(0, 0, 0, 0);
-                if (c <= last) ml[u] = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + slot(c));
-                if (c <= last && d < dp) x[u] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot(c) * dp + d));
+                if (c < parts) ml[u] = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + slot(c));
+                if (c < parts && d < dp) x[u] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot(c) * dp + d));
             }
 #pragma unroll
             for (int u = 0; u < kJoinUnroll; u++) higher = fmaxf(higher, ml[u].x);
@@ -104,6 +93,32 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
             }
         }
         __syncthreads();
+    }
+}
+
+// Block (r, hh) joins query head hh of the units whose first part lies in share
+// r: the other parts are the first ones of the chunks after it.
+template <class T>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant__ Args a, uint32_t dp,
+                                                          uint32_t unit_heads) {
+    __shared__ float sh_m[kJoinWarps], sh_l[kJoinWarps];
+    __shared__ float4 sh_o[kJoinWarps][32];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t heads = a.group < unit_heads ? a.group : unit_heads;
+    const uint32_t hh = blockIdx.x % heads, per_head = (a.group + unit_heads - 1) / unit_heads;
+    const uint32_t chunk0 = blockIdx.x / heads * a.chunks;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    uint4 cuts[kChunks];
+#pragma unroll
+    for (int i = 0; i < (int)kChunks; i++)
+        cuts[i] = i < a.chunks ? __ldcg(a.cut + chunk0 + i) : make_uint4(kNone, 0, 0, 0);
+#pragma unroll 1
+    for (uint32_t i = 0; i < a.chunks; i++) {
+        const uint4 cut = i == 0 ? cuts[0] : i == 1 ? cuts[1] : i == 2 ? cuts[2] : cuts[3];
+        if (cut.x == kNone) continue;
+        const uint32_t in = cut.y % per_head * unit_heads + hh, qh = cut.y / per_head * a.group + in;
+        if (in < a.group) join_unit<T>(a, dp, unit_heads, cut, chunk0 + i, hh, qh, lane, warp, sh_m, sh_l, sh_o);
     }
 }
 
@@ -148,7 +163,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_scores(const __grid_constant_
 
 struct Plan {
     uint32_t dp, nt, unit_heads, units, max_len, tile, chunks;
-    uint64_t max_seen, parts;
+    uint64_t max_seen, most, parts;  // most: tiles there can be; parts: chunks
     bool split;
     size_t part_o, part_ml, cut, lse2, logits;  // elements
 };
@@ -174,7 +189,8 @@ bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t bloc
     p.tile = p.max_seen <= kWhole ? kWhole : kStep;
     const uint64_t unit_tiles = ceil_div(p.max_seen, p.tile);
     const uint64_t all = unit_tiles * p.units * num_seqs;
-    p.parts = all < kMaxBlocks ? all : kMaxBlocks;
+    p.most = all;
+    p.parts = (all < kMaxBlocks ? all : kMaxBlocks) * kChunks;
     p.split = unit_tiles > 1;
     p.part_o = p.split ? 2 * p.parts * p.unit_heads * p.dp : 0;
     p.part_ml = p.split ? 2 * p.parts * p.unit_heads * 2 : 0;
@@ -236,10 +252,10 @@ extern "C" kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t
     const cudaStream_t s = as_stream(stream);
     const uint32_t es = elem_size(cache->dtype);
     const bool ok = dtype == KVX_BF16
-                        ? (es == 2 ? launch<__nv_bfloat16, 2>(a, p.parts, cache->dim, p.nt, s)
-                                   : launch<__nv_bfloat16, 1>(a, p.parts, cache->dim, p.nt, s))
-                        : (es == 2 ? launch<__half, 2>(a, p.parts, cache->dim, p.nt, s)
-                                   : launch<__half, 1>(a, p.parts, cache->dim, p.nt, s));
+                        ? (es == 2 ? launch<__nv_bfloat16, 2>(a, p.most, cache->dim, p.nt, s)
+                                   : launch<__nv_bfloat16, 1>(a, p.most, cache->dim, p.nt, s))
+                        : (es == 2 ? launch<__half, 2>(a, p.most, cache->dim, p.nt, s)
+                                   : launch<__half, 1>(a, p.most, cache->dim, p.nt, s));
     if (!ok) return KVX_ECUDA;
     KVX_LAUNCHED();
 
@@ -251,7 +267,7 @@ extern "C" kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (p.split) {
-        cfg.gridDim = dim3(a.grid * (a.group < p.unit_heads ? a.group : p.unit_heads));
+        cfg.gridDim = dim3(a.regions * (a.group < p.unit_heads ? a.group : p.unit_heads));
         cfg.blockDim = dim3(32 * kJoinWarps);
         const cudaError_t e = dtype == KVX_BF16 ? cudaLaunchKernelEx(&cfg, k_join<__nv_bfloat16>, a, p.dp, p.unit_heads)
                                                 : cudaLaunchKernelEx(&cfg, k_join<__half>, a, p.dp, p.unit_heads);

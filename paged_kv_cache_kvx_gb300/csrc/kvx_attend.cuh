@@ -10,11 +10,13 @@
 namespace kvx {
 namespace attend {
 
-constexpr int kWarps = 4;
-constexpr int kThreads = 32 * kWarps;
-constexpr uint32_t kStep = 16 * kWarps;  // keys of a block's step
-constexpr uint32_t kWhole = 256;         // keys up to which no unit is split
-constexpr uint32_t kMaxBlocks = 512;     // of the splitting grid: bounds the partial results in the workspace
+constexpr int kWarps = 4;                       // that compute; one more looks up and copies
+constexpr int kThreads = 32 * (kWarps + 1);
+constexpr uint32_t kStep = 16 * kWarps;         // keys of a block's step, and of a tile in which work is shared out
+constexpr uint32_t kWhole = 256;                // keys up to which no unit is split
+constexpr uint32_t kChunks = 4;                 // pieces of a block's share: one it begins with, others anyone takes
+constexpr uint32_t kMaxBlocks = 512;            // blocks at a time: bounds the partial results in the workspace
+constexpr int kPieces = 8;                      // descriptors that the looking-up warp may be ahead
 
 struct Args {
     CacheView c;
@@ -29,16 +31,18 @@ struct Args {
     uint64_t scores_stride;
     uint32_t *status;
     // workspace
-    float *part_o;   // [2 * blocks of the grid][heads of a unit][padded dim]: unnormalised outputs
-    float *part_ml;  // [2 * blocks of the grid][heads of a unit][2]: base and sum
-    uint4 *cut;      // [blocks of the grid]: the unit whose first part the block did: sequence, unit, last block; or none
+    float *part_o;   // [2 * chunks][heads of a unit][padded dim]: unnormalised outputs
+    float *part_ml;  // [2 * chunks][heads of a unit][2]: base and sum
+    uint4 *cut;      // [chunks]: the unit whose first part lies in the chunk: sequence (or none), unit, last chunk, slot
     float *lse2;     // [num_seqs][q_heads]: log2 of the sum of the exponentials
     float *logits;   // [num_seqs][heads][visible][group rounded up to even], in powers of two
     uint64_t logits_keys;
     float scale2;    // scale * k_scale * log2(e)
     uint32_t num_seqs, q_heads, group, units;  // units: pieces of a sequence's heads that blocks take
-    uint32_t blocks_per_seq, max_len, window, sinks, grid;
-    uint32_t tile;   // keys of a tile, in which work is shared out
+    uint32_t blocks_per_seq, max_len, window, sinks;
+    uint32_t tile;     // keys of a tile, in which work is shared out
+    uint32_t regions;  // shares
+    uint32_t chunks;   // per share: 1, or kChunks
 };
 
 // Visible tokens of a sequence: logical index i is token i below `sinks`, and
@@ -134,29 +138,344 @@ struct Shape {
     static constexpr int kFit = 196608 / kBlocks / (kStage * kWarps);
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static_assert(kStages >= 2, "");
-    // A unit's look-ups, first copies, query and output take about as long as
-    // a block takes for 32 KB: they count as so many tiles when work is shared out.
-    static constexpr uint32_t kExtra = DP * ES >= 256 ? 1 : 256 / (DP * ES);
-    static constexpr int kORow = DP + 4;                                  // floats of a row when warps are joined
+    // What a unit costs beside its keys (its query, its output) counts as so
+    // many tiles when work is shared out: about 16 KB of copies.
+    static constexpr uint32_t kExtra = DP * ES >= 128 ? 1 : 2;
     static constexpr int kRing = kWarps * kStages * kStage;
-    static constexpr int kJoin = kWarps * kHeads * kORow * 4;
     static constexpr int kQ = NT * kQVecs * 32 * 16;
-    static constexpr int kSmem = (kRing > kJoin ? kRing : kJoin) + kQ;
+    static constexpr int kJoin = (DP / 16 + 1) * NT * 32 * 16;
+    static constexpr int kQBufs = kBlocks == 3 ? 2 : 1;
+    static constexpr int kSmem = kRing + kQBufs * kQ + kJoin;
 };
 
-// One block walks its share of the tiles.  For 16 keys at a time a warp
-// computes, with the KV head's query heads as the columns,
+// 64-bit division takes several times as long as 32-bit division.
+__device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
+    return (a | b) >> 32 ? a / b : (uint64_t)((uint32_t)a / (uint32_t)b);
+}
+
+// How the tiles of all units, in order, are shared out.  Shares are equal, and
+// each is cut into a large chunk and kChunks - 1 small ones of about a
+// twentieth: SMs differ in bandwidth by a sixth, and the small chunks go to
+// those that are done first.
+struct Sharing {
+    uint64_t total, share;
+    uint32_t big, small, chunks;
+    __device__ __forceinline__ Sharing(uint64_t tiles, uint32_t regions, uint32_t per) : total(tiles), chunks(per) {
+        share = quotient(tiles + regions - 1, regions);
+        small = per > 1 && share >= 16 ? (uint32_t)quotient(share + 10, 20) : 0;
+        big = (uint32_t)(share - (per - 1) * (uint64_t)small);
+    }
+    __device__ __forceinline__ uint64_t first(uint32_t chunk) const {
+        const uint32_t r = chunk / chunks, k = chunk % chunks;
+        const uint64_t t = r * share + (k ? big + (uint64_t)(k - 1) * small : 0);
+        return t < total ? t : total;
+    }
+    __device__ __forceinline__ uint32_t chunk_of(uint64_t tile) const {
+        const uint64_t r = quotient(tile, share), in = tile - r * share;
+        return (uint32_t)(r * chunks + (in < big ? 0 : 1 + quotient(in - big, small)));
+    }
+};
+
+// A part of a unit that one block works on.
+struct Piece {
+    uint32_t n;       // sequence; kNone ends the stream
+    uint32_t head;    // KV head
+    uint32_t qh0;     // first of the unit's query heads within the group
+    uint32_t nheads;
+    uint32_t k0, k1;  // visible keys, by logical index
+    uint32_t slot;    // of the partial result; kNone: the piece is the whole unit
+    uint32_t pad;
+};
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+// Arrives when this thread's copies so far are complete.
+__device__ __forceinline__ void mbar_arrive_copies(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Loads into a register that is not touched again before its use: a branch or
+// a copy around them would wait for them.
+__device__ __forceinline__ void load_early(uint32_t &v, const uint32_t *p, bool go) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.nc.u32 %0, [%1];\n\t}"
+                 : "+r"(v)
+                 : "l"(p), "r"((uint32_t)go));
+}
+__device__ __forceinline__ void load_early(uint64_t &v, const uint64_t *p, bool go) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.nc.u64 %0, [%1];\n\t}"
+                 : "+l"(v)
+                 : "l"(p), "r"((uint32_t)go));
+}
+
+// Asks for a block of this grid that has not begun, to do its work in its
+// place; the answer arrives in 16 bytes of shared memory.
+__device__ __forceinline__ void ask_for_block(uint4 *answer, uint64_t *bar) {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                     smem_u32(answer)),
+                 "r"(smem_u32(bar))
+                 : "memory");
+}
+// The block's index; kNone when none is left.
+__device__ __forceinline__ uint32_t block_given(const uint4 *answer) {
+    uint32_t id;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
+        "ld.shared.b128 h, [%1];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "mov.u32 %0, 0xFFFFFFFF;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
+        : "=r"(id)
+        : "r"(smem_u32(answer))
+        : "memory");
+    return id;
+}
+
+// The looking-up warp.  It runs ahead of the computing warps, over pieces and
+// chunks without a pause: the block ids of one step are loaded while the
+// segment addresses of the step before are, and the rows of the one before that
+// are handed to the warps.
+template <class T, int DP, int ES, int NT>
+__device__ __forceinline__ void look_up(const Args &a, const Sharing &sharing, uint32_t per, uint32_t lane,
+                                        uint4 *qbuf, const uint64_t *upto, uint64_t (*rows)[32], uint64_t *ready,
+                                        uint64_t *taken, uint64_t *pfull, uint64_t *pempty, Piece *pieces, uint4 *sh_given, uint64_t *given,
+                                        uint32_t &bad) {
+    using S = Shape<DP, ES, NT>;
+    const uint32_t g = lane >> 2, t4 = lane & 3, kv = lane >> 4;
+    const uint32_t units_per_head = (a.group + S::kHeads - 1) / S::kHeads;
+    auto unit_len = [&](uint32_t keys) { return keys ? (keys + a.tile - 1) / a.tile + S::kExtra : 0; };
+    bool alive = true;  // no wait has run out
+
+    // -- where the walk is
+    uint32_t block = blockIdx.x, asked = 0;  // the block whose chunk this is
+    uint64_t at = 0, end = 0;                // tiles of the chunk still to come
+    bool in_chunk = false, at_begin = false;
+    uint32_t chunk = 0, n = 0, len_u = 0;
+    uint64_t seq_tile = 0;
+    Seen sv = {};
+    uint32_t np = 0;                   // pieces so far
+    uint32_t k = 0, k1 = 0, head = 0;  // the piece's keys still to come
+    bool fresh = false;                // its first step is still to come
+
+    auto begin_chunk = [&]() {
+        // blocks 0 .. regions-1 stand for the large chunks, in order
+        const uint32_t rest = block - a.regions, small = a.chunks - 1;
+        chunk = block < a.regions ? block * a.chunks : rest / small * a.chunks + 1 + rest % small;
+        if (block < a.regions)  // and see to the sequences without a visible token
+            for (uint32_t i = block; i < a.num_seqs; i += a.regions)
+                if (!seen(a, a.lens[i]).n) {
+                    for (uint32_t d = lane; d < a.q_heads * a.c.dim; d += 32)
+                        static_cast<T *>(a.out)[i * a.out_stride + d] = T(0.0f);
+                    for (uint32_t d = lane; d < a.q_heads; d += 32)
+                        if (a.lse) a.lse[(uint64_t)i * a.q_heads + d] = -INFINITY;
+                }
+        at = sharing.first(chunk);
+        end = sharing.first(chunk + 1);
+        at_begin = true;
+        if (a.cut && at >= end && lane == 0) a.cut[chunk].x = kNone;
+        if (a.chunks > 1 && lane == 0) ask_for_block(sh_given, given);
+        if (at >= end) return;
+        // its sequence: by the threads' counts, then one by one
+        const uint32_t i = __popc(__ballot_sync(0xFFFFFFFFu, upto[lane] * a.units <= at));
+        uint64_t before = i ? upto[i - 1] * a.units : 0;
+        for (n = i * kWarps * per;; n++) {
+            sv = seen(a, a.lens[n]);
+            len_u = unit_len(sv.n);
+            if (at < before + (uint64_t)len_u * a.units) break;
+            before += (uint64_t)len_u * a.units;
+        }
+        seq_tile = at - before;
+    };
+
+    // Moves on to the next piece with keys; false at the end of all work.
+    auto next_piece = [&]() -> bool {
+        for (;;) {
+            if (at >= end) {
+                if (in_chunk) {
+                    if (a.chunks == 1) return false;
+                    if (!mbar_wait(given, asked++ & 1)) return alive = false;
+                    block = block_given(sh_given);
+                    __syncwarp();
+                    if (block == kNone) return false;
+                }
+                in_chunk = true;
+                begin_chunk();
+                continue;
+            }
+            while (seq_tile >= (uint64_t)len_u * a.units) {
+                seq_tile -= (uint64_t)len_u * a.units;
+                do sv = seen(a, a.lens[++n]);
+                while (!sv.n);
+                len_u = unit_len(sv.n);
+            }
+            const uint32_t unit = (uint32_t)quotient(seq_tile, len_u), from = (uint32_t)(seq_tile - (uint64_t)unit * len_u);
+            const uint32_t to = (uint32_t)(len_u - from < end - at ? len_u : from + (end - at));
+            // the kExtra that stand for the unit's overhead come first
+            const uint32_t nt = len_u - S::kExtra;
+            const uint32_t tile0 = from > S::kExtra ? from - S::kExtra : 0, tile1 = to > S::kExtra ? to - S::kExtra : 0;
+            const bool whole = tile0 == 0 && tile1 == nt;
+            const uint32_t slot = 2 * chunk + !at_begin;
+            const uint32_t gaps = sharing.small ? 0 : 1u << 31;  // the small chunks are empty
+            if (a.cut && lane == 0 && at + (to - from) == end)
+                a.cut[chunk] = make_uint4(tile0 == 0 && tile1 && !whole ? n : kNone, unit,
+                                          sharing.chunk_of(at - from + len_u - 1), slot | gaps);
+            at += to - from;
+            seq_tile += to - from;
+            at_begin = false;
+            if (tile0 == tile1) continue;
+            head = unit / units_per_head;
+            k = tile0 * a.tile;
+            k1 = tile1 * a.tile < sv.n ? tile1 * a.tile : sv.n;
+            fresh = true;
+            if (np >= kPieces && !mbar_wait(&pempty[np % kPieces], (np / kPieces & 1) ^ 1)) return alive = false;
+            if (lane == 0) {
+                const uint32_t qh0 = unit % units_per_head * S::kHeads;
+                const uint32_t nheads = a.group - qh0 < S::kHeads ? a.group - qh0 : S::kHeads;
+                pieces[np % kPieces] = Piece{n, head, qh0, nheads, k, k1, whole ? kNone : slot, 0};
+            }
+            np++;
+            __syncwarp();
+            return true;
+        }
+    };
+
+    // Two steps on their way: the block ids of one are loaded while the segment
+    // addresses of the one before are.  Loaded registers are used up where they
+    // are (a copy of one would wait for it), so lane i < 16 holds key i of each
+    // warp's 16 keys for K, lane 16 + i for V.
+    struct Step {
+        uint32_t place[kWarps], valid;  // place in the page; a bit per warp: the block exists
+        uint32_t table, piece, warps;   // lane of the address table; warps with keys, 0 at the end
+        bool fresh;                     // the piece's first step
+    };
+    uint32_t ids[kWarps] = {};
+    uint64_t segs[kWarps] = {};
+    auto find_blocks = [&]() -> Step {
+        Step s = {};
+        if (k >= k1 && !next_piece()) return s;
+        s.warps = k1 - k < kStep ? (k1 - k + 15) / 16 : kWarps;
+        s.piece = np - 1;
+        s.fresh = fresh;
+        s.table = a.c.first_lane + 2 * head + kv;
+        const uint32_t *seq_blocks = a.blocks + (uint64_t)n * a.blocks_per_seq;
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            const uint32_t i = k + w * 16 + (lane & 15);
+            const uint32_t pos = i < sv.sinks ? i : i + sv.shift, page = a.c.page.div(pos);
+            s.place[w] = pos - page * a.c.page.d;
+            s.valid |= (uint32_t)(i < k1) << w;
+            load_early(ids[w], seq_blocks + page, i < k1);
+        }
+        fresh = false;
+        k = k1 - k < kStep ? k1 : k + kStep;
+        return s;
+    };
+    auto find_addrs = [&](Step &s) {
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            const uint32_t id = ids[w], there = s.valid >> w & 1, known = id < a.c.B;
+            load_early(segs[w], a.c.addr + (uint64_t)id * a.c.L + s.table, there & known);
+            bad |= there & ~known ? KVX_S_BOUNDS : 0;
+            s.valid &= ~((known ^ 1) << w);
+        }
+    };
+
+    uint32_t handed[kWarps] = {};  // tiles handed to each warp so far
+    auto announce = [&](uint32_t p) {
+        mbar_arrive_copies(&pfull[p % kPieces]);
+        if (lane == 0) mbar_arrive(&pfull[p % kPieces]);
+    };
+    auto issue = [&](const Step &s, const uint64_t (&row)[kWarps]) {
+        if (s.fresh) {  // the piece's query heads, as the second operand's lanes hold them
+            const uint32_t p = s.piece;
+            const uint32_t q_of = p - S::kQBufs;  // the piece whose query was there before
+            if (p >= S::kQBufs && !mbar_wait(&pempty[q_of % kPieces], q_of / kPieces & 1)) {
+                alive = false;
+                return;
+            }
+            const Piece pc = pieces[p % kPieces];
+            const T *q = static_cast<const T *>(a.q) + (uint64_t)pc.n * a.q_stride +
+                         (uint64_t)(pc.head * a.group + pc.qh0) * a.c.dim;
+            const uint32_t dst = smem_u32(qbuf + p % S::kQBufs * (S::kQ / 16) + lane);
+#pragma unroll
+            for (int x = 0; x < NT; x++)
+#pragma unroll
+                for (int i = 0; i < S::kQVecs; i++) {
+                    const uint32_t d = ES == 2 ? i * 32 + t4 * 8 : (i / 2) * 64 + t4 * 16 + (i & 1) * 8;
+                    const bool in = x * 8 + g < pc.nheads && d < a.c.dim;
+                    copy_async<16>(dst + (x * S::kQVecs + i) * 512, in ? q + (uint64_t)(x * 8 + g) * a.c.dim + d : q,
+                                   in ? 16 : 0);
+                }
+            announce(p);
+        }
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            if (w >= s.warps) break;
+            if (handed[w] && !mbar_wait(&taken[w], (handed[w] & 1) ^ 1)) {
+                alive = false;
+                return;
+            }
+            rows[w][lane] = row[w];
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ready[w]);
+            handed[w]++;
+        }
+    };
+
+    Step next = find_blocks(), now = next;
+    find_addrs(now);
+    if (now.warps) next = find_blocks();
+    while (alive && now.warps) {
+        uint64_t row[kWarps];
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            row[w] = reinterpret_cast<uint64_t>(a.c.pool) | 1;  // no such row
+            if ((now.valid >> w & 1) && a.c.ok(segs[w], bad)) row[w] += segs[w] + now.place[w] * a.c.token_stride - 1;
+        }
+        const Step s = now;
+        now = next;
+        find_addrs(now);
+        if (now.warps) next = find_blocks();
+        issue(s, row);
+    }
+    if (alive) {  // the end of the stream
+        if (np >= kPieces && !mbar_wait(&pempty[np % kPieces], (np / kPieces & 1) ^ 1)) alive = false;
+        if (lane == 0) pieces[np % kPieces].n = kNone;
+        __syncwarp();
+        if (alive) announce(np);
+    }
+    if (!alive) bad |= KVX_S_TIMEOUT;
+    asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// A block walks chunks of its share of the tiles.  Its last warp looks the
+// pages up and copies keys, values and queries into rings in shared memory;
+// the others compute, 16 keys of a step each.  For those a warp computes, with
+// the KV head's query heads as the columns,
 //     S^T = K Q^T   (16 keys x 8 heads per mma.m16n8k16)
 //     O^T += V^T P^T
-// where P = exp2(S - running maximum).  Contracting over a permuted order of
-// the head's values, and of the keys, lets every lane take its operands of
-// both products from 16-byte pieces of the rows as they lie in memory: lane
-// (g, t) = (lane / 4, lane % 4) holds pieces t, t+4, ... of the rows of keys
-// g and g+8 for K, and piece g of the rows of keys 2t, 2t+1, 2t+8, 2t+9 for V
-// (whose pairs of keys one byte permutation brings together).  So each lane
-// fetches exactly the pieces it will use, with asynchronous copies into its
-// own places of a ring in shared memory: no lane waits for another's copies,
-// reads are free of bank conflicts, and pages, strides and gaps cost nothing.
+// where P = 2^(S - base).  Contracting over a permuted order of the head's
+// values, and of the keys, lets every lane take its operands of both products
+// from 16-byte pieces of the rows as they lie in memory: lane (g, t) =
+// (lane / 4, lane % 4) holds pieces t, t+4, ... of the rows of keys g and g+8
+// for K, and piece g of the rows of keys 2t, 2t+1, 2t+8, 2t+9 for V (whose
+// pairs of keys one byte permutation brings together).  So rows are copied
+// piece by piece to where their lanes read them, free of bank conflicts, and
+// pages, strides and gaps cost nothing.  A unit's four partial results pass
+// from warp to warp through a buffer of the same lanes' places, so that no
+// warp waits for a slower one before it goes on to the next piece.
 //
 // Bound by HBM: per key 2*DP*ES bytes for 4*group*DP operations.  mma.sync
 // suffices: with 16 columns in use the SMs need well under a fifth of its
@@ -167,247 +486,156 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
     using S = Shape<DP, ES, NT>;
     // the type in which the products are taken: 8-bit values are exact in fp16
     using C = typename std::conditional<ES == 1, __half, T>::type;
-    extern __shared__ __align__(16) uint8_t smem[];
-    __shared__ uint64_t sh_sum[kWarps];
-    __shared__ uint64_t sh_first;                   // tiles of the sequences before the first one
-    __shared__ uint32_t sh_n;
-    __shared__ float sh_ml[kWarps][S::kHeads][2];
-    __shared__ float sh_qscale[S::kHeads];          // power of two taken out of a head's query
+    constexpr bool kConvertQ = !std::is_same<C, T>::value;
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t sh_sum[kWarps + 1], sh_upto[32];
+    __shared__ uint64_t full[kWarps][S::kStages];   // a warp's tiles
+    __shared__ __align__(16) uint64_t rows[kWarps][32];  // and its next one's rows: addresses of 16 of K and 16 of V
+    __shared__ uint64_t ready[kWarps], taken[kWarps];
+    __shared__ uint64_t pfull[kPieces], pempty[kPieces];                      // pieces
+    __shared__ uint64_t passed[kWarps], joined, converted[2], given;
+    __shared__ Piece pieces[kPieces];
+    __shared__ uint4 sh_given;
+    __shared__ float sh_qscale[2][S::kHeads];  // power of two taken out of a head's query
 
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const uint32_t g = lane >> 2, t4 = lane & 3;
-    uint8_t *ring = smem + warp * (S::kStages * S::kStage);
+    uint4 *qbuf = reinterpret_cast<uint4 *>(smem + S::kRing);
     // A V row's pieces lie together, as they arrive (scattered ones held the
     // copies to three quarters of the bandwidth), in an order that keeps the
     // eight or sixteen lanes that read at a time on different banks.
     const uint32_t vslot = (t4 * 8 + (g ^ (S::kVBytes == 16 ? 2 * t4 : t4 / 2 * 4))) * S::kVBytes;
-    uint4 *qs = reinterpret_cast<uint4 *>(smem + (S::kRing > S::kJoin ? S::kRing : S::kJoin));
     uint32_t bad = 0;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
-    // ---- the block's share: blocks take equal stretches of the tiles of all
-    // units in order, so that a batch of any lengths keeps every SM busy to
-    // the end.  Each thread counts the tiles of some sequences in a row.
-    const uint32_t per = (a.num_seqs + kThreads - 1) / kThreads;
-    const uint32_t n0 = threadIdx.x * per, n1 = n0 + per < a.num_seqs ? n0 + per : a.num_seqs;
-    auto unit_tiles = [&](uint32_t keys) { return (keys + a.tile - 1) / a.tile; };
+    // ---- the tiles of all units: each thread counts those of some sequences in a row
+    const uint32_t per = (a.num_seqs + kWarps * 32 - 1) / (kWarps * 32);
+    auto unit_len = [&](uint32_t keys) { return keys ? (keys + a.tile - 1) / a.tile + S::kExtra : 0; };
     uint64_t mine = 0;
-    bool none = false;
-    for (uint32_t n = n0; n < n1; n++) {
-        const uint32_t len = a.lens[n], keys = seen(a, len).n;
-        if (blockIdx.x == 0 && len > a.max_len) bad |= KVX_S_BOUNDS;
-        if (keys)
-            mine += unit_tiles(keys) + S::kExtra;
-        else
-            none |= n % gridDim.x == blockIdx.x;
-    }
-    uint64_t upto = warp_incl_sum(mine), total = 0;
-    if (lane == 31) sh_sum[warp] = upto;
-    none = __syncthreads_or(none);
-#pragma unroll
-    for (int w = 0; w < kWarps; w++) {
-        if (w < (int)warp) upto += sh_sum[w];
-        total += sh_sum[w];
-    }
-    total *= a.units;
-    const uint64_t share = (total + a.grid - 1) / a.grid;
-    uint64_t at = blockIdx.x * share;
-    const uint64_t begin = at, end = at + share < total ? at + share : total;
-    if (at < end && (upto - mine) * a.units <= at && at < upto * a.units) {  // one thread
-        uint64_t before = (upto - mine) * a.units;
-        uint32_t n = n0;
-        for (;; n++) {
-            const uint32_t keys = seen(a, a.lens[n]).n;
-            const uint64_t m = keys ? (uint64_t)(unit_tiles(keys) + S::kExtra) * a.units : 0;
-            if (at < before + m) break;
-            before += m;
+    if (warp < kWarps) {
+        const uint32_t n0 = threadIdx.x * per, n1 = n0 + per < a.num_seqs ? n0 + per : a.num_seqs;
+        for (uint32_t n = n0; n < n1; n++) {
+            const uint32_t len = a.lens[n];
+            if (len > a.max_len) bad |= KVX_S_BOUNDS;
+            mine += unit_len(seen(a, len).n);
         }
-        sh_n = n;
-        sh_first = before;
-    }
-    if (none)  // sequences without a visible token
-        for (uint32_t n = blockIdx.x; n < a.num_seqs; n += gridDim.x) {
-            if (seen(a, a.lens[n]).n) continue;
-            for (uint32_t i = threadIdx.x; i < a.q_heads * a.c.dim; i += kThreads)
-                static_cast<T *>(a.out)[n * a.out_stride + i] = T(0.0f);
-            for (uint32_t i = threadIdx.x; i < a.q_heads; i += kThreads)
-                if (a.lse) a.lse[(uint64_t)n * a.q_heads + i] = -INFINITY;
+    } else if (lane == 0) {
+        for (int w = 0; w < kWarps; w++) {
+            for (int i = 0; i < S::kStages; i++) mbar_init(&full[w][i], 32);
+            mbar_init(&ready[w], 1);
+            mbar_init(&taken[w], 1);
+            mbar_init(&passed[w], 1);
         }
-    if (at >= end) {
-        if (a.cut && threadIdx.x == 0) a.cut[blockIdx.x].x = kNone;
+        for (int i = 0; i < kPieces; i++) {
+            mbar_init(&pfull[i], 33);
+            mbar_init(&pempty[i], kWarps);
+        }
+        mbar_init(&joined, 1);
+        mbar_init(&converted[0], NT);
+        mbar_init(&converted[1], NT);
+        mbar_init(&given, 1);
+        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    }
+    {
+        uint64_t upto = warp_incl_sum(mine);
+        if (lane == 31) sh_sum[warp] = upto;
+        __syncthreads();
+        for (uint32_t w = 0; w < warp && w < kWarps; w++) upto += sh_sum[w];
+        if (warp < kWarps && threadIdx.x % kWarps == kWarps - 1) sh_upto[threadIdx.x / kWarps] = upto;
+        __syncthreads();
+    }
+    const Sharing sharing(sh_upto[31] * a.units, a.regions, a.chunks);
+
+    if (warp == kWarps) {
+        look_up<T, DP, ES, NT>(a, sharing, per, lane, qbuf, sh_upto, rows, ready, taken, pfull, pempty, pieces, &sh_given,
+                               &given, bad);
         raise(a.status, bad);
         return;
     }
-    __syncthreads();
-    uint32_t n = sh_n;
-    uint64_t seq_tile = at - sh_first;  // within the sequence's units
-    Seen sv = seen(a, a.lens[n]);
-    uint32_t nt = unit_tiles(sv.n), len_u = nt + S::kExtra;
-    const uint32_t units_per_head = (a.group + S::kHeads - 1) / S::kHeads;
+    raise(a.status, bad);
 
-    // ---- one piece of a unit after the other
-    for (uint64_t next; at < end; seq_tile += next - at, at = next) {
-        while (seq_tile >= (uint64_t)len_u * a.units) {
-            seq_tile -= (uint64_t)len_u * a.units;
-            do sv = seen(a, a.lens[++n]);
-            while (!sv.n);
-            nt = unit_tiles(sv.n);
-            len_u = nt + S::kExtra;
-        }
-        const uint32_t unit = (uint32_t)(seq_tile / len_u), from = (uint32_t)(seq_tile - (uint64_t)unit * len_u);
-        const uint32_t to = (uint32_t)(len_u - from < end - at ? len_u : from + (end - at));
-        next = at + (to - from);
-        // the kExtra that stand for the unit's overhead come first
-        const uint32_t tile0 = from > S::kExtra ? from - S::kExtra : 0, tile1 = to > S::kExtra ? to - S::kExtra : 0;
-        const bool whole = tile0 == 0 && tile1 == nt;
-        if (a.cut && threadIdx.x == 0 && next == end)
-            a.cut[blockIdx.x] = make_uint4(tile0 == 0 && tile1 && !whole ? n : kNone, unit,
-                                           (uint32_t)((at - from + len_u - 1) / share), at != begin);
-        if (tile0 == tile1) continue;
-        const uint32_t head = unit / units_per_head, qh0 = unit % units_per_head * S::kHeads;
-        const uint32_t nheads = a.group - qh0 < S::kHeads ? a.group - qh0 : S::kHeads;
-        const uint32_t q0 = head * a.group + qh0;
-        const uint32_t k0 = tile0 * a.tile, k1 = tile1 * a.tile < sv.n ? tile1 * a.tile : sv.n;
-
-        // -- this lane looks up key lane%16's K (lanes 0-15) or V segment
-        const uint32_t *seq_blocks = a.blocks + (uint64_t)n * a.blocks_per_seq;
-        const uint32_t kv = lane >> 4;
-        auto find_block = [&](uint32_t j, uint32_t &place) -> uint32_t {
-            const uint32_t i = k0 + (j * kWarps + warp) * 16 + (lane & 15);
-            if (i >= k1) return kNone;
-            const uint32_t pos = i < sv.sinks ? i : i + sv.shift;
-            const uint32_t page = a.c.page.div(pos);
-            place = pos - page * a.c.page.d;
-            const uint32_t b = __ldg(seq_blocks + page);
-            if (b < a.c.B) return b;
-            bad |= KVX_S_BOUNDS;
-            return kNone;
-        };
-        auto find_addr = [&](uint32_t b) -> uint64_t {
-            return b == kNone ? ~0ull : __ldg(a.c.lane_addr(b, head, kv));
-        };
-        auto resolve = [&](uint64_t seg, uint32_t place, uint32_t b) -> uint64_t {
-            if (b == kNone || !a.c.ok(seg, bad)) return ~0ull;
-            return seg + place * a.c.token_stride;
-        };
-        const uint32_t warp_keys = k1 - k0;
-        const uint32_t steps = warp_keys > warp * 16 ? (warp_keys - warp * 16 + kStep - 1) / kStep : 0;
-        // -- asynchronous copies of tile j's pieces into its stage: where a row
-        // or a piece does not exist, zeros (a copy of no bytes reads nothing)
-        auto fetch = [&](uint32_t j, uint64_t row) {
-            const uint32_t kdst = smem_u32(ring + (j % S::kStages) * S::kStage + lane * 16);
-            const uint32_t vdst = smem_u32(ring + (j % S::kStages) * S::kStage + S::kStage / 2 + vslot);
-            const uint8_t *p[6];
-            uint32_t n[6];
+    // ---- a computing warp: one piece after the other
+    uint8_t *ring = smem + warp * (S::kStages * S::kStage);
+    uint32_t copied = 0;  // tiles whose copies this warp has issued: up to kStages ahead, of later pieces too
+    const bool cover = a.c.row_bytes == DP * ES;
+    // Takes the next tile's rows and copies this lane's pieces of them: where a
+    // row or a piece does not exist, zeros (a copy of no bytes reads nothing).
+    auto copy_tile = [&]() {
+        const uint64_t *from = rows[warp];
+        const ulonglong2 v0 = *reinterpret_cast<const ulonglong2 *>(from + 16 + 2 * t4);
+        const ulonglong2 v1 = *reinterpret_cast<const ulonglong2 *>(from + 24 + 2 * t4);
+        const uint64_t row[6] = {from[g], from[g + 8], v0.x, v0.y, v1.x, v1.y};
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&taken[warp]);
+        const uint32_t stage = copied % S::kStages;
+        uint8_t *st = ring + stage * S::kStage;
+        const uint32_t kdst = smem_u32(st + lane * 16), vdst = smem_u32(st + S::kStage / 2 + vslot);
 #pragma unroll
-            for (int r = 0; r < 6; r++) {
-                const uint32_t from = r < 2 ? g + 8 * r : 16 + 2 * t4 + (r & 1) + 8 * ((r - 2) >> 1);
-                const uint64_t src = __shfl_sync(0xFFFFFFFFu, row, from);
-                n[r] = src == ~0ull ? 0 : r < 2 ? 16 : S::kVBytes;
-                p[r] = a.c.pool + (src == ~0ull ? 0 : src) + (r < 2 ? t4 * 16 : g * S::kVBytes);
-            }
-            if (a.c.row_bytes == DP * ES) {
+        for (int r = 0; r < 6; r++) {
+            const uint32_t bytes = row[r] & 1 ? 0 : r < 2 ? 16 : S::kVBytes;
+            const uint8_t *p = reinterpret_cast<const uint8_t *>(row[r] & ~1ull) + (r < 2 ? t4 * 16 : g * S::kVBytes);
+            if (r < 2) {
 #pragma unroll
-                for (int r = 0; r < 2; r++)
-#pragma unroll
-                    for (int c = 0; c < S::kKChunks; c++) copy_async<16>(kdst + (c * 2 + r) * 512, p[r] + c * 64, n[r]);
-#pragma unroll
-                for (int r = 0; r < 4; r++)
-#pragma unroll
-                    for (int c = 0; c < S::kVParts; c++)
-                        copy_async<S::kVBytes>(vdst + (c * 4 + r) * 32 * S::kVBytes, p[2 + r] + c * 8 * S::kVBytes, n[2 + r]);
+                for (int c = 0; c < S::kKChunks; c++)
+                    copy_async<16>(kdst + (c * 2 + r) * 512, p + c * 64,
+                                   cover || c * 64 + t4 * 16 < a.c.row_bytes ? bytes : 0);
             } else {
 #pragma unroll
-                for (int r = 0; r < 2; r++)
-#pragma unroll
-                    for (int c = 0; c < S::kKChunks; c++)
-                        copy_async<16>(kdst + (c * 2 + r) * 512, p[r] + c * 64,
-                                       c * 64 + t4 * 16 < a.c.row_bytes ? n[r] : 0);
-#pragma unroll
-                for (int r = 0; r < 4; r++)
-#pragma unroll
-                    for (int c = 0; c < S::kVParts; c++)
-                        copy_async<S::kVBytes>(vdst + (c * 4 + r) * 32 * S::kVBytes, p[2 + r] + c * 8 * S::kVBytes,
-                                               (c * 8 + g) * S::kVBytes < a.c.row_bytes ? n[2 + r] : 0);
+                for (int c = 0; c < S::kVParts; c++)
+                    copy_async<S::kVBytes>(vdst + (c * 4 + r - 2) * 32 * S::kVBytes, p + c * 8 * S::kVBytes,
+                                           cover || (c * 8 + g) * S::kVBytes < a.c.row_bytes ? bytes : 0);
             }
-        };
-
-        // look-ups run ahead of the copies: the address of one tile, the block of
-        // the next and of the one after, whose address is fetched into L2
-        uint32_t b1 = kNone, p1 = 0, b2 = kNone, p2 = 0, b3 = kNone, p3 = 0;
-        uint64_t row = ~0ull, seg1 = ~0ull;
-        {
-            uint32_t b0, p0 = 0;
-            b0 = find_block(0, p0);
-            b1 = find_block(1, p1);
-            b2 = find_block(2, p2);
-            b3 = find_block(3, p3);
-            const uint64_t seg0 = find_addr(b0);
-            seg1 = find_addr(b1);
-            row = resolve(seg0, p0, b0);
         }
-        auto advance = [&](uint32_t j) {  // after tile j's copies were issued
-            row = resolve(seg1, p1, b1);
-            b1 = b2;
-            p1 = p2;
-            seg1 = find_addr(b1);
-            b2 = b3;
-            p2 = p3;
-            if (b2 != kNone) asm volatile("prefetch.global.L2 [%0];" ::"l"(a.c.lane_addr(b2, head, kv)));
-            b3 = find_block(j + 4, p3);
-        };
+        mbar_arrive_copies(&full[warp][stage]);
+        copied++;
+    };
+    float4 *join = reinterpret_cast<float4 *>(smem + S::kRing + S::kQBufs * S::kQ) + lane;
+    uint32_t tile = 0, joins = 0, passes = 0;  // tiles taken, pieces joined, and results taken over so far
+    for (uint32_t p = 0;; p++) {
+        if (!mbar_wait(&pfull[p % kPieces], p / kPieces & 1)) break;
+        const Piece pc = pieces[p % kPieces];
+        if (pc.n == kNone) return;
+        uint4 *qs = qbuf + p % S::kQBufs * (S::kQ / 16);
+        if constexpr (kConvertQ) {
+            // bf16's range does not fit fp16: a head's largest power of two is
+            // taken out first (exact, but for values 2^-14 of the largest and
+            // below, which lose the bits under 2^-24 of it)
+            if (warp < NT) {
+                uint4 *mine_q = qs + warp * S::kQVecs * 32 + lane;
+                float top = 0;
 #pragma unroll
-        for (int j = 0; j < S::kStages - 1; j++) {
-            if (j < steps) {
-                fetch(j, row);
-                advance(j);
-            }
-            copies_commit();
-        }
-
-        // -- the query heads, as the second operand's lanes hold them
-        __syncthreads();  // the last piece's reads of qs and sh_ml are done
-        for (uint32_t hh = warp; hh < S::kHeads; hh += kWarps) {
-            const uint32_t d0 = lane * 8;
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (hh < nheads && d0 < a.c.dim)
-                raw = *reinterpret_cast<const uint4 *>(static_cast<const T *>(a.q) + (uint64_t)n * a.q_stride +
-                                                       (uint64_t)(q0 + hh) * a.c.dim + d0);
-            float unit2 = 1.0f;
-            if constexpr (ES == 1 && std::is_same<T, __nv_bfloat16>::value) {
-                // bf16's range does not fit fp16: the head's largest power of
-                // two is taken out first (exact, but for values 2^-14 of the
-                // largest and below, which lose the bits under 2^-24 of it)
-                float x[8], top = 0;
+                for (int i = 0; i < S::kQVecs; i++) {
+                    const uint4 raw = mine_q[i * 32];
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    const float2 f = Pair<T>::unpack(word(raw, i));
-                    x[2 * i] = f.x, x[2 * i + 1] = f.y;
-                    top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    for (int k = 0; k < 4; k++) {
+                        const float2 f = Pair<T>::unpack(word(raw, k));
+                        top = fmaxf(top, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
                 }
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2));
+                int e = 0;
+                if (top > 0 && top < INFINITY) frexpf(top, &e);
+                e = e < -120 ? -120 : e > 120 ? 120 : e;
+                const float inv = ldexpf(1.0f, -e);
 #pragma unroll
-                for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
-                float inv = 1.0f;
-                if (top > 0 && top < INFINITY) {
-                    int e;
-                    frexpf(top, &e);
-                    e = e < -120 ? -120 : e > 120 ? 120 : e;
-                    unit2 = ldexpf(1.0f, e);
-                    inv = ldexpf(1.0f, -e);
+                for (int i = 0; i < S::kQVecs; i++) {
+                    const uint4 raw = mine_q[i * 32];
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const float2 f = Pair<T>::unpack(word(raw, k));
+                        w[k] = Pair<C>::pack(f.x * inv, f.y * inv);
+                    }
+                    mine_q[i * 32] = make_uint4(w[0], w[1], w[2], w[3]);
                 }
-                raw = make_uint4(Pair<C>::pack(x[0] * inv, x[1] * inv), Pair<C>::pack(x[2] * inv, x[3] * inv),
-                                 Pair<C>::pack(x[4] * inv, x[5] * inv), Pair<C>::pack(x[6] * inv, x[7] * inv));
+                if (t4 == 0) sh_qscale[p & 1][warp * 8 + g] = ldexpf(1.0f, e);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&converted[p & 1]);
             }
-            if (d0 < DP) {
-                // piece (c, t) of a K row is 16 bytes: 8 or 16 values
-                constexpr int per = 16 / ES;
-                const uint32_t c = d0 / (4 * per), tt = d0 % (4 * per) / per, hf = d0 % per / 8;
-                qs[((hh >> 3) * S::kQVecs + c * (per / 8) + hf) * 32 + (hh & 7) * 4 + tt] = raw;
-            }
-            if (lane == 0) sh_qscale[hh] = unit2;
+            if (!mbar_wait(&converted[p & 1], p / 2 & 1)) break;
         }
-        __syncthreads();
 
         // Weights are taken as 2^(logit - base).  The base follows the running
         // maximum only when a logit exceeds it by more than kSlack + kBoost:
@@ -423,7 +651,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
         for (int x = 0; x < NT; x++)
 #pragma unroll
             for (int i = 0; i < 2; i++) {
-                scale2[x][i] = a.scale2 * sh_qscale[x * 8 + 2 * t4 + i];
+                scale2[x][i] = a.scale2;
+                if constexpr (kConvertQ) scale2[x][i] *= sh_qscale[p & 1][x * 8 + 2 * t4 + i];
                 limit[x][i] = -INFINITY, base[x][i] = 0, l[x][i] = 0;
             }
 #pragma unroll
@@ -432,16 +661,27 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
             for (int x = 0; x < NT; x++)
 #pragma unroll
                 for (int i = 0; i < 4; i++) o[j][x][i] = 0;
+        float *logits = nullptr;
+        const uint32_t gp = (a.group + 1) & ~1u;
+        if (a.logits)
+            logits = a.logits + ((uint64_t)pc.n * a.c.heads + pc.head) * a.logits_keys * gp + pc.qh0 + 2 * t4;
 
-        for (uint32_t j = 0; j < steps; j++) {
-            const uint32_t jf = j + S::kStages - 1;
-            if (jf < steps) {
-                fetch(jf, row);
-                advance(jf);
+        bool ok = true;
+        for (uint32_t k = pc.k0 + warp * 16; k < pc.k1; k += kStep, tile++) {
+            if (copied == tile) {
+                if (!mbar_wait(&ready[warp], copied & 1)) {
+                    ok = false;
+                    break;
+                }
+                copy_tile();
             }
-            copies_commit();
-            copies_wait<S::kStages - 1>();
-            const uint8_t *st = ring + (j % S::kStages) * S::kStage;
+            while (copied < tile + S::kStages && __all_sync(0xFFFFFFFFu, mbar_test(&ready[warp], copied & 1))) copy_tile();
+            const uint32_t stage = tile % S::kStages;
+            if (!mbar_wait(&full[warp][stage], tile / S::kStages & 1)) {
+                ok = false;
+                break;
+            }
+            const uint8_t *st = ring + stage * S::kStage;
 
             // S^T = K Q^T
             float s[NT][4] = {}, s2[NT][4] = {};  // two chains of products
@@ -471,23 +711,20 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
             }
 
             // logits in powers of two, masked beyond the last key
-            const uint32_t i0 = k0 + (j * kWarps + warp) * 16 + g, i1 = i0 + 8;
+            const uint32_t i0 = k + g, i1 = i0 + 8;
             bool higher = false;
 #pragma unroll
             for (int x = 0; x < NT; x++) {
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     s[x][i] = (s[x][i] + s2[x][i]) * scale2[x][i & 1];
-                    if ((i < 2 ? i0 : i1) >= k1) s[x][i] = -INFINITY;
+                    if ((i < 2 ? i0 : i1) >= pc.k1) s[x][i] = -INFINITY;
                     higher |= s[x][i] > limit[x][i & 1];
                 }
-                if (a.logits) {
-                    const uint32_t gp = (a.group + 1) & ~1u, hh = qh0 + x * 8 + 2 * t4;
-                    if (hh < a.group) {
-                        float *to = a.logits + ((uint64_t)n * a.c.heads + head) * a.logits_keys * gp + hh;
-                        if (i0 < k1) *reinterpret_cast<float2 *>(to + (uint64_t)i0 * gp) = make_float2(s[x][0], s[x][1]);
-                        if (i1 < k1) *reinterpret_cast<float2 *>(to + (uint64_t)i1 * gp) = make_float2(s[x][2], s[x][3]);
-                    }
+                if (logits && x * 8 + 2 * t4 < pc.nheads) {
+                    float2 *to = reinterpret_cast<float2 *>(logits + x * 8 + (uint64_t)i0 * gp);
+                    if (i0 < pc.k1) to[0] = make_float2(s[x][0], s[x][1]);
+                    if (i1 < pc.k1) to[4 * gp] = make_float2(s[x][2], s[x][3]);
                 }
             }
             if (__any_sync(0xFFFFFFFFu, higher)) {
@@ -576,87 +813,119 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
                 }
             }
         }
-        copies_wait<0>();
+        if (!ok) break;
+        if (lane == 0) mbar_arrive(&pempty[p % kPieces]);  // its query and descriptor are done with
 
-        // ---- the warps' results joined
+        // ---- the warps' results: each adds its own to the next one's
+        const uint32_t active = pc.k1 - pc.k0 < kStep ? (pc.k1 - pc.k0 + 15) / 16 : kWarps;
+        if (warp >= active) {
+            joins += active > 1;
+            continue;
+        }
+        float m[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; x++)
 #pragma unroll
             for (int i = 0; i < 2; i++) {
 #pragma unroll
                 for (int k = 4; k < 32; k <<= 1) l[x][i] += __shfl_xor_sync(0xFFFFFFFFu, l[x][i], k);
-                if (g == 0) {
-                    sh_ml[warp][x * 8 + 2 * t4 + i][0] = limit[x][i] == -INFINITY ? -INFINITY : base[x][i];
-                    sh_ml[warp][x * 8 + 2 * t4 + i][1] = l[x][i];
+                m[x][i] = limit[x][i] == -INFINITY ? -INFINITY : base[x][i];
+            }
+        if (warp + 1 < active) {
+            if (!mbar_wait(&passed[warp + 1], passes++ & 1)) break;
+#pragma unroll
+            for (int x = 0; x < NT; x++) {
+                const float4 ml = join[(kOTiles * NT + x) * 32];
+                float f[2], fj[2];
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const float mj = i ? ml.y : ml.x, top = fmaxf(m[x][i], mj);
+                    f[i] = m[x][i] == -INFINITY ? 1.0f : exp2f(m[x][i] - top);  // 1: zeros, or a NaN
+                    fj[i] = mj == -INFINITY ? 1.0f : exp2f(mj - top);
+                    l[x][i] = l[x][i] * f[i] + (i ? ml.w : ml.z) * fj[i];
+                    m[x][i] = top;
+                }
+#pragma unroll
+                for (int k = 0; k < kOTiles; k++) {
+                    const float4 v = join[(k * NT + x) * 32];
+                    o[k][x][0] = o[k][x][0] * f[0] + v.x * fj[0];
+                    o[k][x][1] = o[k][x][1] * f[1] + v.y * fj[1];
+                    o[k][x][2] = o[k][x][2] * f[0] + v.z * fj[0];
+                    o[k][x][3] = o[k][x][3] * f[1] + v.w * fj[1];
                 }
             }
-        __syncthreads();  // also: every warp's ring is free
-        float *join = reinterpret_cast<float *>(smem);
+        } else if (active > 1 && joins) {  // the first to write: the last piece's results have been read
+            if (!mbar_wait(&joined, joins - 1 & 1)) break;
+        }
+        joins += active > 1;
+        if (warp > 0) {
+#pragma unroll
+            for (int x = 0; x < NT; x++) {
+                join[(kOTiles * NT + x) * 32] = make_float4(m[x][0], m[x][1], l[x][0], l[x][1]);
+#pragma unroll
+                for (int k = 0; k < kOTiles; k++)
+                    join[(k * NT + x) * 32] = make_float4(o[k][x][0], o[k][x][1], o[k][x][2], o[k][x][3]);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&passed[warp]);
+            continue;
+        }
+        __syncwarp();
+        if (lane == 0 && active > 1) mbar_arrive(&joined);
+
+        // ---- the unit's output, or its part for k_join
 #pragma unroll
         for (int x = 0; x < NT; x++)
 #pragma unroll
             for (int i = 0; i < 2; i++) {
                 const uint32_t hh = x * 8 + 2 * t4 + i;
-                float top = sh_ml[0][hh][0];
+                if (hh >= pc.nheads) continue;
+                const uint32_t qh = pc.head * a.group + pc.qh0 + hh;
+                if (pc.slot != kNone) {
+                    float *to = a.part_o + ((uint64_t)pc.slot * S::kHeads + hh) * DP;
 #pragma unroll
-                for (int w = 1; w < kWarps; w++) top = fmaxf(top, sh_ml[w][hh][0]);
-                const float f = limit[x][i] == -INFINITY ? 1.0f : exp2f(base[x][i] - top);  // 1: zeros, or a NaN
-                float *to = join + (warp * S::kHeads + hh) * S::kORow;
+                    for (int c = 0; c < S::kVParts; c++)
+#pragma unroll
+                        for (int e = 0; e < S::kVElems; e += 4) {
+                            const int k = (c * S::kVElems + e) / 2;
+                            *reinterpret_cast<float4 *>(to + (c * 8 + g) * S::kVElems + e) =
+                                make_float4(o[k][x][i], o[k][x][i + 2], o[k + 1][x][i], o[k + 1][x][i + 2]);
+                        }
+                    if (g == 0)
+                        *reinterpret_cast<float2 *>(a.part_ml + ((uint64_t)pc.slot * S::kHeads + hh) * 2) =
+                            make_float2(m[x][i], l[x][i]);
+                    continue;
+                }
+                const float inv = l[x][i] == 0 ? 0.0f : a.c.v_scale / l[x][i];
+                T *to = static_cast<T *>(a.out) + (uint64_t)pc.n * a.out_stride + (uint64_t)qh * a.c.dim;
 #pragma unroll
                 for (int c = 0; c < S::kVParts; c++)
 #pragma unroll
-                    for (int e = 0; e < S::kVElems / 2; e++) {
-                        const int k = c * (S::kVElems / 2) + e;
-                        *reinterpret_cast<float2 *>(to + (c * 8 + g) * S::kVElems + 2 * e) =
-                            make_float2(o[k][x][i] * f, o[k][x][i + 2] * f);
+                    for (int e = 0; e < S::kVElems; e += 8) {
+                        const int k = (c * S::kVElems + e) / 2;
+                        const uint32_t d = (c * 8 + g) * S::kVElems + e;
+                        if (d < a.c.dim)
+                            *reinterpret_cast<uint4 *>(to + d) =
+                                make_uint4(Pair<T>::pack(o[k][x][i] * inv, o[k][x][i + 2] * inv),
+                                           Pair<T>::pack(o[k + 1][x][i] * inv, o[k + 1][x][i + 2] * inv),
+                                           Pair<T>::pack(o[k + 2][x][i] * inv, o[k + 2][x][i + 2] * inv),
+                                           Pair<T>::pack(o[k + 3][x][i] * inv, o[k + 3][x][i + 2] * inv));
                     }
-            }
-        __syncthreads();
-        const uint32_t slot = 2 * blockIdx.x + (at != begin);
-        for (uint32_t i = threadIdx.x * 4; i < nheads * DP; i += kThreads * 4) {
-            const uint32_t hh = i / DP, d = i % DP;
-            float top = sh_ml[0][hh][0];
-#pragma unroll
-            for (int w = 1; w < kWarps; w++) top = fmaxf(top, sh_ml[w][hh][0]);
-            float sum = 0;
-            float4 v = make_float4(0, 0, 0, 0);
-#pragma unroll
-            for (int w = 0; w < kWarps; w++) {
-                const float mw = sh_ml[w][hh][0];
-                // (a NaN among the logits leaves the maximum alone but not the sum)
-                sum += sh_ml[w][hh][1] * (mw == -INFINITY ? 1.0f : exp2f(mw - top));
-                const float4 x = *reinterpret_cast<const float4 *>(join + (w * S::kHeads + hh) * S::kORow + d);
-                v.x += x.x, v.y += x.y, v.z += x.z, v.w += x.w;
-            }
-            if (!whole) {
-                *reinterpret_cast<float4 *>(a.part_o + ((uint64_t)slot * S::kHeads + hh) * DP + d) = v;
-                if (d == 0) {
-                    a.part_ml[((uint64_t)slot * S::kHeads + hh) * 2] = top;
-                    a.part_ml[((uint64_t)slot * S::kHeads + hh) * 2 + 1] = sum;
+                if (g == 0) {
+                    const float lse2 = l[x][i] == 0 ? -INFINITY : m[x][i] + log2f(l[x][i]);
+                    if (a.lse) a.lse[(uint64_t)pc.n * a.q_heads + qh] = lse2 * 0.6931471805599453f;
+                    if (a.lse2) a.lse2[(uint64_t)pc.n * a.q_heads + qh] = lse2;
                 }
-                continue;
             }
-            const float inv = sum == 0 ? 0.0f : a.c.v_scale / sum;
-            if (d < a.c.dim) {
-                T *to = static_cast<T *>(a.out) + (uint64_t)n * a.out_stride + (uint64_t)(q0 + hh) * a.c.dim + d;
-                *reinterpret_cast<uint2 *>(to) =
-                    make_uint2(Pair<T>::pack(v.x * inv, v.y * inv), Pair<T>::pack(v.z * inv, v.w * inv));
-            }
-            if (d == 0) {
-                const float lse2 = sum == 0 ? -INFINITY : top + log2f(sum);
-                if (a.lse) a.lse[(uint64_t)n * a.q_heads + q0 + hh] = lse2 * 0.6931471805599453f;
-                if (a.lse2) a.lse2[(uint64_t)n * a.q_heads + q0 + hh] = lse2;
-            }
-        }
-        __syncthreads();  // the ring takes the next piece's copies
     }
-    raise(a.status, bad);
+    raise(a.status, KVX_S_TIMEOUT);  // a wait ran out
+    asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Launches one variant over at most `parts` blocks, and leaves their number in
-// a.grid; false where that failed.
+// Launches one variant over shares for at most `most` blocks and leaves their
+// number and that of a share's chunks in a; false where that failed.
 template <class T, int DP, int ES, int NT>
-bool launch_one(Args &a, uint64_t parts, cudaStream_t s) {
+bool launch_one(Args &a, uint64_t most, cudaStream_t s) {
     using S = Shape<DP, ES, NT>;
     static bool done[64];
     int dev = 0;
@@ -667,18 +936,21 @@ bool launch_one(Args &a, uint64_t parts, cudaStream_t s) {
             return false;
         if (dev >= 0 && dev < 64) done[dev] = true;
     }
-    const uint64_t room = (uint64_t)sm_count() * S::kBlocks;
-    a.grid = (uint32_t)(parts < room ? parts : room);
-    if (!a.grid) a.grid = 1;  // nothing to see anywhere: the zeros still have to be written
-    k_attend<T, DP, ES, NT><<<a.grid, kThreads, S::kSmem, s>>>(a);
+    uint64_t room = (uint64_t)sm_count() * S::kBlocks;
+    if (room > kMaxBlocks) room = kMaxBlocks;
+    a.regions = (uint32_t)(most < room ? most : room);
+    if (!a.regions) a.regions = 1;  // nothing to see anywhere: the zeros still have to be written
+    // A grid that fits on the device has no block to take over.
+    a.chunks = most > 16 * room ? kChunks : 1;
+    k_attend<T, DP, ES, NT><<<a.regions * a.chunks, kThreads, S::kSmem, s>>>(a);
     return true;
 }
 
 template <class T, int ES>
-bool launch(Args &a, uint64_t parts, uint32_t dim, uint32_t nt, cudaStream_t s) {
-    if (dim <= 64) return nt == 1 ? launch_one<T, 64, ES, 1>(a, parts, s) : launch_one<T, 64, ES, 2>(a, parts, s);
-    if (dim <= 128) return nt == 1 ? launch_one<T, 128, ES, 1>(a, parts, s) : launch_one<T, 128, ES, 2>(a, parts, s);
-    return launch_one<T, 256, ES, 1>(a, parts, s);
+bool launch(Args &a, uint64_t most, uint32_t dim, uint32_t nt, cudaStream_t s) {
+    if (dim <= 64) return nt == 1 ? launch_one<T, 64, ES, 1>(a, most, s) : launch_one<T, 64, ES, 2>(a, most, s);
+    if (dim <= 128) return nt == 1 ? launch_one<T, 128, ES, 1>(a, most, s) : launch_one<T, 128, ES, 2>(a, most, s);
+    return launch_one<T, 256, ES, 1>(a, most, s);
 }
 
 }  // namespace attend
