@@ -24,35 +24,46 @@ extern template bool launch<__half, 1>(Args &, uint64_t, uint32_t, uint32_t, cud
 namespace {
 
 constexpr uint32_t kMaxGroup = 128;
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = 16;
 constexpr int kJoinUnroll = 8;  // parts whose loads a warp has in flight
 constexpr int kScoreThreads = 128;
 constexpr uint32_t kScoreKeys = 4 * kScoreThreads;  // of a block that adds weights
 
+// Block c joins the query heads of the unit whose first part block c of
+// k_attend did; its other parts are the first ones of blocks c+1 .. last.  The
+// warps are dealt out to the heads, and those of a head to its parts.
 template <class T>
-__device__ __forceinline__ void join_unit(const Args &a, uint32_t dp, uint32_t unit_heads, const uint4 &cut,
-                                          uint32_t first, uint32_t hh, uint32_t qh, uint32_t lane, uint32_t warp,
-                                          float *sh_m, float *sh_l, float4 (*sh_o)[32]) {
-    const uint32_t n = cut.x, step = cut.w >> 31 ? a.chunks : 1, parts = (cut.z - first) / step + 1;
-    auto slot = [&](uint32_t i) {
-        return (uint64_t)(i ? 2 * (first + i * step) : cut.w & 0x7FFFFFFFu) * unit_heads + hh;
-    };
-    // each warp takes every fourth part; a lane four of 128 values at a time
+__global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant__ Args a, uint32_t dp,
+                                                          uint32_t unit_heads) {
+    __shared__ float sh_m[kJoinWarps], sh_l[kJoinWarps];
+    __shared__ float4 sh_o[kJoinWarps][32];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t heads = a.group < unit_heads ? a.group : unit_heads, deal = kJoinWarps / heads;
+    const uint32_t hh = warp / deal, turn = warp % deal, per_head = (a.group + unit_heads - 1) / unit_heads;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint4 cut = __ldcg(a.cut + blockIdx.x);
+    if (cut.x == kNone) return;
+    const uint32_t n = cut.x, parts = cut.z - blockIdx.x + 1;
+    const uint32_t in = cut.y % per_head * unit_heads + hh, qh = cut.y / per_head * a.group + in;
+    const bool has = hh < heads && in < a.group;
+    auto slot = [&](uint32_t i) { return (uint64_t)(i ? 2 * (blockIdx.x + i) : cut.w) * unit_heads + hh; };
+    // a lane takes four of 128 values at a time
     for (uint32_t d0 = 0; d0 < dp; d0 += 128) {
         const uint32_t d = d0 + lane * 4;
         float4 v = make_float4(0, 0, 0, 0);
         float top = -INFINITY, sum = 0;
-        for (uint32_t c0 = warp; c0 < parts; c0 += kJoinWarps * kJoinUnroll) {
+        for (uint32_t i0 = turn; has && i0 < parts; i0 += deal * kJoinUnroll) {
             float2 ml[kJoinUnroll];
             float4 x[kJoinUnroll];
             float higher = top;
 #pragma unroll
             for (int u = 0; u < kJoinUnroll; u++) {
-                const uint32_t c = c0 + u * kJoinWarps;
+                const uint32_t i = i0 + u * deal;
                 ml[u] = make_float2(-INFINITY, 0);
                 x[u] = make_float4(0, 0, 0, 0);
-                if (c < parts) ml[u] = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + slot(c));
-                if (c < parts && d < dp) x[u] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot(c) * dp + d));
+                if (i < parts) ml[u] = __ldcg(reinterpret_cast<const float2 *>(a.part_ml) + slot(i));
+                if (i < parts && d < dp) x[u] = __ldcg(reinterpret_cast<const float4 *>(a.part_o + slot(i) * dp + d));
             }
 #pragma unroll
             for (int u = 0; u < kJoinUnroll; u++) higher = fmaxf(higher, ml[u].x);
@@ -66,59 +77,34 @@ __device__ __forceinline__ void join_unit(const Args &a, uint32_t dp, uint32_t u
                 v.x += x[u].x * f, v.y += x[u].y * f, v.z += x[u].z * f, v.w += x[u].w * f;
             }
         }
-        sh_o[warp][lane] = v;
-        if (lane == 0) sh_m[warp] = top, sh_l[warp] = sum;
-        __syncthreads();
-        if (warp == 0) {
-            for (int w = 1; w < kJoinWarps; w++) top = fmaxf(top, sh_m[w]);
+        if (deal > 1) {
+            __syncthreads();  // the last round's results have been read
+            sh_o[warp][lane] = v;
+            if (lane == 0) sh_m[warp] = top, sh_l[warp] = sum;
+            __syncthreads();
+            if (turn || !has) continue;
+            for (uint32_t w = 1; w < deal; w++) top = fmaxf(top, sh_m[warp + w]);
             v = make_float4(0, 0, 0, 0);
             sum = 0;
-#pragma unroll
-            for (int w = 0; w < kJoinWarps; w++) {
-                const float f = sh_m[w] == -INFINITY ? 1.0f : exp2f(sh_m[w] - top);
-                const float4 x = sh_o[w][lane];
+            for (uint32_t w = 0; w < deal; w++) {
+                const float f = sh_m[warp + w] == -INFINITY ? 1.0f : exp2f(sh_m[warp + w] - top);
+                const float4 x = sh_o[warp + w][lane];
                 v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
-                sum += sh_l[w] * f;
-            }
-            const float inv = sum == 0 ? 0.0f : a.c.v_scale / sum;
-            if (d < a.c.dim) {
-                T *to = static_cast<T *>(a.out) + (uint64_t)n * a.out_stride + (uint64_t)qh * a.c.dim + d;
-                *reinterpret_cast<uint2 *>(to) =
-                    make_uint2(Pair<T>::pack(v.x * inv, v.y * inv), Pair<T>::pack(v.z * inv, v.w * inv));
-            }
-            if (d == 0) {
-                const float lse2 = sum == 0 ? -INFINITY : top + log2f(sum);
-                if (a.lse) a.lse[(uint64_t)n * a.q_heads + qh] = lse2 * 0.6931471805599453f;
-                if (a.lse2) a.lse2[(uint64_t)n * a.q_heads + qh] = lse2;
+                sum += sh_l[warp + w] * f;
             }
         }
-        __syncthreads();
-    }
-}
-
-// Block (r, hh) joins query head hh of the units whose first part lies in share
-// r: the other parts are the first ones of the chunks after it.
-template <class T>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant__ Args a, uint32_t dp,
-                                                          uint32_t unit_heads) {
-    __shared__ float sh_m[kJoinWarps], sh_l[kJoinWarps];
-    __shared__ float4 sh_o[kJoinWarps][32];
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t heads = a.group < unit_heads ? a.group : unit_heads;
-    const uint32_t hh = blockIdx.x % heads, per_head = (a.group + unit_heads - 1) / unit_heads;
-    const uint32_t chunk0 = blockIdx.x / heads * a.chunks;
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    uint4 cuts[kChunks];
-#pragma unroll
-    for (int i = 0; i < (int)kChunks; i++)
-        cuts[i] = i < a.chunks ? __ldcg(a.cut + chunk0 + i) : make_uint4(kNone, 0, 0, 0);
-#pragma unroll 1
-    for (uint32_t i = 0; i < a.chunks; i++) {
-        const uint4 cut = i == 0 ? cuts[0] : i == 1 ? cuts[1] : i == 2 ? cuts[2] : cuts[3];
-        if (cut.x == kNone) continue;
-        const uint32_t in = cut.y % per_head * unit_heads + hh, qh = cut.y / per_head * a.group + in;
-        if (in < a.group) join_unit<T>(a, dp, unit_heads, cut, chunk0 + i, hh, qh, lane, warp, sh_m, sh_l, sh_o);
+        if (!has) continue;
+        const float inv = sum == 0 ? 0.0f : a.c.v_scale / sum;
+        if (d < a.c.dim) {
+            T *to = static_cast<T *>(a.out) + (uint64_t)n * a.out_stride + (uint64_t)qh * a.c.dim + d;
+            *reinterpret_cast<uint2 *>(to) =
+                make_uint2(Pair<T>::pack(v.x * inv, v.y * inv), Pair<T>::pack(v.z * inv, v.w * inv));
+        }
+        if (d == 0) {
+            const float lse2 = sum == 0 ? -INFINITY : top + log2f(sum);
+            if (a.lse) a.lse[(uint64_t)n * a.q_heads + qh] = lse2 * 0.6931471805599453f;
+            if (a.lse2) a.lse2[(uint64_t)n * a.q_heads + qh] = lse2;
+        }
     }
 }
 
@@ -163,7 +149,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_scores(const __grid_constant_
 
 struct Plan {
     uint32_t dp, nt, unit_heads, units, max_len, tile, chunks;
-    uint64_t max_seen, most, parts;  // most: tiles there can be; parts: chunks
+    uint64_t max_seen, parts;  // parts: blocks that the workspace has room for
     bool split;
     size_t part_o, part_ml, cut, lse2, logits;  // elements
 };
@@ -189,8 +175,7 @@ bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t bloc
     p.tile = p.max_seen <= kWhole ? kWhole : kStep;
     const uint64_t unit_tiles = ceil_div(p.max_seen, p.tile);
     const uint64_t all = unit_tiles * p.units * num_seqs;
-    p.most = all;
-    p.parts = (all < kMaxBlocks ? all : kMaxBlocks) * kChunks;
+    p.parts = all < kMaxBlocks ? all : kMaxBlocks;
     p.split = unit_tiles > 1;
     p.part_o = p.split ? 2 * p.parts * p.unit_heads * p.dp : 0;
     p.part_ml = p.split ? 2 * p.parts * p.unit_heads * 2 : 0;
@@ -252,10 +237,10 @@ extern "C" kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t
     const cudaStream_t s = as_stream(stream);
     const uint32_t es = elem_size(cache->dtype);
     const bool ok = dtype == KVX_BF16
-                        ? (es == 2 ? launch<__nv_bfloat16, 2>(a, p.most, cache->dim, p.nt, s)
-                                   : launch<__nv_bfloat16, 1>(a, p.most, cache->dim, p.nt, s))
-                        : (es == 2 ? launch<__half, 2>(a, p.most, cache->dim, p.nt, s)
-                                   : launch<__half, 1>(a, p.most, cache->dim, p.nt, s));
+                        ? (es == 2 ? launch<__nv_bfloat16, 2>(a, p.parts, cache->dim, p.nt, s)
+                                   : launch<__nv_bfloat16, 1>(a, p.parts, cache->dim, p.nt, s))
+                        : (es == 2 ? launch<__half, 2>(a, p.parts, cache->dim, p.nt, s)
+                                   : launch<__half, 1>(a, p.parts, cache->dim, p.nt, s));
     if (!ok) return KVX_ECUDA;
     KVX_LAUNCHED();
 
@@ -267,7 +252,7 @@ extern "C" kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (p.split) {
-        cfg.gridDim = dim3(a.regions * (a.group < p.unit_heads ? a.group : p.unit_heads));
+        cfg.gridDim = dim3(a.grid);
         cfg.blockDim = dim3(32 * kJoinWarps);
         const cudaError_t e = dtype == KVX_BF16 ? cudaLaunchKernelEx(&cfg, k_join<__nv_bfloat16>, a, p.dp, p.unit_heads)
                                                 : cudaLaunchKernelEx(&cfg, k_join<__half>, a, p.dp, p.unit_heads);

@@ -14,8 +14,7 @@ constexpr int kWarps = 4;                       // that compute; one more looks 
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr uint32_t kStep = 16 * kWarps;         // keys of a block's step, and of a tile in which work is shared out
 constexpr uint32_t kWhole = 256;                // keys up to which no unit is split
-constexpr uint32_t kChunks = 4;                 // pieces of a block's share: one it begins with, others anyone takes
-constexpr uint32_t kMaxBlocks = 512;            // blocks at a time: bounds the partial results in the workspace
+constexpr uint32_t kMaxBlocks = 512;            // bounds the partial results in the workspace
 constexpr int kPieces = 8;                      // descriptors that the looking-up warp may be ahead
 
 struct Args {
@@ -31,9 +30,9 @@ struct Args {
     uint64_t scores_stride;
     uint32_t *status;
     // workspace
-    float *part_o;   // [2 * chunks][heads of a unit][padded dim]: unnormalised outputs
-    float *part_ml;  // [2 * chunks][heads of a unit][2]: base and sum
-    uint4 *cut;      // [chunks]: the unit whose first part lies in the chunk: sequence (or none), unit, last chunk, slot
+    float *part_o;   // [2 * blocks][heads of a unit][padded dim]: unnormalised outputs
+    float *part_ml;  // [2 * blocks][heads of a unit][2]: base and sum
+    uint4 *cut;      // [blocks]: the unit whose first part the block did: sequence (or none), unit, last block, slot
     float *lse2;     // [num_seqs][q_heads]: log2 of the sum of the exponentials
     float *logits;   // [num_seqs][heads][visible][group rounded up to even], in powers of two
     uint64_t logits_keys;
@@ -41,8 +40,7 @@ struct Args {
     uint32_t num_seqs, q_heads, group, units;  // units: pieces of a sequence's heads that blocks take
     uint32_t blocks_per_seq, max_len, window, sinks;
     uint32_t tile;     // keys of a tile, in which work is shared out
-    uint32_t regions;  // shares
-    uint32_t chunks;   // per share: 1, or kChunks
+    uint32_t grid;     // blocks
 };
 
 // Visible tokens of a sequence: logical index i is token i below `sinks`, and
@@ -153,29 +151,6 @@ __device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
     return (a | b) >> 32 ? a / b : (uint64_t)((uint32_t)a / (uint32_t)b);
 }
 
-// How the tiles of all units, in order, are shared out.  Shares are equal, and
-// each is cut into a large chunk and kChunks - 1 small ones of about a
-// twentieth: SMs differ in bandwidth by a sixth, and the small chunks go to
-// those that are done first.
-struct Sharing {
-    uint64_t total, share;
-    uint32_t big, small, chunks;
-    __device__ __forceinline__ Sharing(uint64_t tiles, uint32_t regions, uint32_t per) : total(tiles), chunks(per) {
-        share = quotient(tiles + regions - 1, regions);
-        small = per > 1 && share >= 16 ? (uint32_t)quotient(share + 10, 20) : 0;
-        big = (uint32_t)(share - (per - 1) * (uint64_t)small);
-    }
-    __device__ __forceinline__ uint64_t first(uint32_t chunk) const {
-        const uint32_t r = chunk / chunks, k = chunk % chunks;
-        const uint64_t t = r * share + (k ? big + (uint64_t)(k - 1) * small : 0);
-        return t < total ? t : total;
-    }
-    __device__ __forceinline__ uint32_t chunk_of(uint64_t tile) const {
-        const uint64_t r = quotient(tile, share), in = tile - r * share;
-        return (uint32_t)(r * chunks + (in < big ? 0 : 1 + quotient(in - big, small)));
-    }
-};
-
 // A part of a unit that one block works on.
 struct Piece {
     uint32_t n;       // sequence; kNone ends the stream
@@ -218,39 +193,14 @@ __device__ __forceinline__ void load_early(uint64_t &v, const uint64_t *p, bool 
                  : "l"(p), "r"((uint32_t)go));
 }
 
-// Asks for a block of this grid that has not begun, to do its work in its
-// place; the answer arrives in 16 bytes of shared memory.
-__device__ __forceinline__ void ask_for_block(uint4 *answer, uint64_t *bar) {
-    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-    mbar_arrive_expect_tx(bar, 16);
-    asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
-                     smem_u32(answer)),
-                 "r"(smem_u32(bar))
-                 : "memory");
-}
-// The block's index; kNone when none is left.
-__device__ __forceinline__ uint32_t block_given(const uint4 *answer) {
-    uint32_t id;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t.reg .b128 h;\n\t"
-        "ld.shared.b128 h, [%1];\n\t"
-        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
-        "mov.u32 %0, 0xFFFFFFFF;\n\t"
-        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %0, h;\n\t}"
-        : "=r"(id)
-        : "r"(smem_u32(answer))
-        : "memory");
-    return id;
-}
-
-// The looking-up warp.  It runs ahead of the computing warps, over pieces and
-// chunks without a pause: the block ids of one step are loaded while the
-// segment addresses of the step before are, and the rows of the one before that
-// are handed to the warps.
+// The looking-up warp.  It runs ahead of the computing warps, over pieces
+// without a pause: the block ids of one step are loaded while the segment
+// addresses of the step before are, and the rows of the one before that are
+// handed to the warps.
 template <class T, int DP, int ES, int NT>
-__device__ __forceinline__ void look_up(const Args &a, const Sharing &sharing, uint32_t per, uint32_t lane,
+__device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t per, uint32_t lane,
                                         uint4 *qbuf, const uint64_t *upto, uint64_t (*rows)[32], uint64_t *ready,
-                                        uint64_t *taken, uint64_t *pfull, uint64_t *pempty, Piece *pieces, uint4 *sh_given, uint64_t *given,
+                                        uint64_t *taken, uint64_t *pfull, uint64_t *pempty, Piece *pieces,
                                         uint32_t &bad) {
     using S = Shape<DP, ES, NT>;
     const uint32_t g = lane >> 2, t4 = lane & 3, kv = lane >> 4;
@@ -258,36 +208,28 @@ __device__ __forceinline__ void look_up(const Args &a, const Sharing &sharing, u
     auto unit_len = [&](uint32_t keys) { return keys ? (keys + a.tile - 1) / a.tile + S::kExtra : 0; };
     bool alive = true;  // no wait has run out
 
-    // -- where the walk is
-    uint32_t block = blockIdx.x, asked = 0;  // the block whose chunk this is
-    uint64_t at = 0, end = 0;                // tiles of the chunk still to come
-    bool in_chunk = false, at_begin = false;
-    uint32_t chunk = 0, n = 0, len_u = 0;
-    uint64_t seq_tile = 0;
+    // the sequences without a visible token
+    for (uint32_t i = blockIdx.x; i < a.num_seqs; i += gridDim.x)
+        if (!seen(a, a.lens[i]).n) {
+            for (uint32_t d = lane; d < a.q_heads * a.c.dim; d += 32)
+                static_cast<T *>(a.out)[i * a.out_stride + d] = T(0.0f);
+            for (uint32_t d = lane; d < a.q_heads; d += 32)
+                if (a.lse) a.lse[(uint64_t)i * a.q_heads + d] = -INFINITY;
+        }
+
+    // -- where the walk is: tiles at .. end-1 are still to come
+    const uint64_t share = quotient(total + a.grid - 1, a.grid), begin = blockIdx.x * share;
+    const uint64_t end = begin + share < total ? begin + share : total;
+    uint64_t at = begin, seq_tile = 0;  // seq_tile: within the sequence
+    uint32_t n = 0, len_u = 0;
     Seen sv = {};
     uint32_t np = 0;                   // pieces so far
     uint32_t k = 0, k1 = 0, head = 0;  // the piece's keys still to come
     bool fresh = false;                // its first step is still to come
-
-    auto begin_chunk = [&]() {
-        // blocks 0 .. regions-1 stand for the large chunks, in order
-        const uint32_t rest = block - a.regions, small = a.chunks - 1;
-        chunk = block < a.regions ? block * a.chunks : rest / small * a.chunks + 1 + rest % small;
-        if (block < a.regions)  // and see to the sequences without a visible token
-            for (uint32_t i = block; i < a.num_seqs; i += a.regions)
-                if (!seen(a, a.lens[i]).n) {
-                    for (uint32_t d = lane; d < a.q_heads * a.c.dim; d += 32)
-                        static_cast<T *>(a.out)[i * a.out_stride + d] = T(0.0f);
-                    for (uint32_t d = lane; d < a.q_heads; d += 32)
-                        if (a.lse) a.lse[(uint64_t)i * a.q_heads + d] = -INFINITY;
-                }
-        at = sharing.first(chunk);
-        end = sharing.first(chunk + 1);
-        at_begin = true;
-        if (a.cut && at >= end && lane == 0) a.cut[chunk].x = kNone;
-        if (a.chunks > 1 && lane == 0) ask_for_block(sh_given, given);
-        if (at >= end) return;
-        // its sequence: by the threads' counts, then one by one
+    if (at >= end) {
+        if (a.cut && lane == 0) a.cut[blockIdx.x].x = kNone;
+    } else {
+        // the first sequence: by the threads' counts, then one by one
         const uint32_t i = __popc(__ballot_sync(0xFFFFFFFFu, upto[lane] * a.units <= at));
         uint64_t before = i ? upto[i - 1] * a.units : 0;
         for (n = i * kWarps * per;; n++) {
@@ -297,23 +239,11 @@ __device__ __forceinline__ void look_up(const Args &a, const Sharing &sharing, u
             before += (uint64_t)len_u * a.units;
         }
         seq_tile = at - before;
-    };
+    }
 
     // Moves on to the next piece with keys; false at the end of all work.
     auto next_piece = [&]() -> bool {
-        for (;;) {
-            if (at >= end) {
-                if (in_chunk) {
-                    if (a.chunks == 1) return false;
-                    if (!mbar_wait(given, asked++ & 1)) return alive = false;
-                    block = block_given(sh_given);
-                    __syncwarp();
-                    if (block == kNone) return false;
-                }
-                in_chunk = true;
-                begin_chunk();
-                continue;
-            }
+        while (at < end) {
             while (seq_tile >= (uint64_t)len_u * a.units) {
                 seq_tile -= (uint64_t)len_u * a.units;
                 do sv = seen(a, a.lens[++n]);
@@ -326,14 +256,13 @@ __device__ __forceinline__ void look_up(const Args &a, const Sharing &sharing, u
             const uint32_t nt = len_u - S::kExtra;
             const uint32_t tile0 = from > S::kExtra ? from - S::kExtra : 0, tile1 = to > S::kExtra ? to - S::kExtra : 0;
             const bool whole = tile0 == 0 && tile1 == nt;
-            const uint32_t slot = 2 * chunk + !at_begin;
-            const uint32_t gaps = sharing.small ? 0 : 1u << 31;  // the small chunks are empty
+            // of a block's pieces at most the first and the last are parts
+            const uint32_t slot = 2 * blockIdx.x + (at != begin);
             if (a.cut && lane == 0 && at + (to - from) == end)
-                a.cut[chunk] = make_uint4(tile0 == 0 && tile1 && !whole ? n : kNone, unit,
-                                          sharing.chunk_of(at - from + len_u - 1), slot | gaps);
+                a.cut[blockIdx.x] = make_uint4(tile0 == 0 && tile1 && !whole ? n : kNone, unit,
+                                               (uint32_t)quotient(at - from + len_u - 1, share), slot);
             at += to - from;
             seq_tile += to - from;
-            at_begin = false;
             if (tile0 == tile1) continue;
             head = unit / units_per_head;
             k = tile0 * a.tile;
@@ -349,6 +278,7 @@ __device__ __forceinline__ void look_up(const Args &a, const Sharing &sharing, u
             __syncwarp();
             return true;
         }
+        return false;
     };
 
     // Two steps on their way: the block ids of one are loaded while the segment
@@ -460,10 +390,10 @@ __device__ __forceinline__ void look_up(const Args &a, const Sharing &sharing, u
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// A block walks chunks of its share of the tiles.  Its last warp looks the
-// pages up and copies keys, values and queries into rings in shared memory;
-// the others compute, 16 keys of a step each.  For those a warp computes, with
-// the KV head's query heads as the columns,
+// The tiles of all units, in order, are shared out equally, one share a block.
+// A block's last warp walks the share and looks the pages up; the others copy
+// keys and values into rings of their own and compute, 16 keys of a step each.
+// For those a warp computes, with the KV head's query heads as the columns,
 //     S^T = K Q^T   (16 keys x 8 heads per mma.m16n8k16)
 //     O^T += V^T P^T
 // where P = 2^(S - base).  Contracting over a permuted order of the head's
@@ -493,9 +423,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
     __shared__ __align__(16) uint64_t rows[kWarps][32];  // and its next one's rows: addresses of 16 of K and 16 of V
     __shared__ uint64_t ready[kWarps], taken[kWarps];
     __shared__ uint64_t pfull[kPieces], pempty[kPieces];                      // pieces
-    __shared__ uint64_t passed[kWarps], joined, converted[2], given;
+    __shared__ uint64_t passed[kWarps], joined, converted[2];
     __shared__ Piece pieces[kPieces];
-    __shared__ uint4 sh_given;
     __shared__ float sh_qscale[2][S::kHeads];  // power of two taken out of a head's query
 
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -534,8 +463,6 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
         mbar_init(&joined, 1);
         mbar_init(&converted[0], NT);
         mbar_init(&converted[1], NT);
-        mbar_init(&given, 1);
-        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     }
     {
         uint64_t upto = warp_incl_sum(mine);
@@ -545,11 +472,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
         if (warp < kWarps && threadIdx.x % kWarps == kWarps - 1) sh_upto[threadIdx.x / kWarps] = upto;
         __syncthreads();
     }
-    const Sharing sharing(sh_upto[31] * a.units, a.regions, a.chunks);
 
     if (warp == kWarps) {
-        look_up<T, DP, ES, NT>(a, sharing, per, lane, qbuf, sh_upto, rows, ready, taken, pfull, pempty, pieces, &sh_given,
-                               &given, bad);
+        look_up<T, DP, ES, NT>(a, sh_upto[31] * a.units, per, lane, qbuf, sh_upto, rows, ready, taken, pfull, pempty,
+                               pieces, bad);
         raise(a.status, bad);
         return;
     }
@@ -922,8 +848,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Launches one variant over shares for at most `most` blocks and leaves their
-// number and that of a share's chunks in a; false where that failed.
+// Launches one variant over at most `most` blocks and leaves their number in
+// a.grid; false where that failed.
 template <class T, int DP, int ES, int NT>
 bool launch_one(Args &a, uint64_t most, cudaStream_t s) {
     using S = Shape<DP, ES, NT>;
@@ -938,11 +864,9 @@ bool launch_one(Args &a, uint64_t most, cudaStream_t s) {
     }
     uint64_t room = (uint64_t)sm_count() * S::kBlocks;
     if (room > kMaxBlocks) room = kMaxBlocks;
-    a.regions = (uint32_t)(most < room ? most : room);
-    if (!a.regions) a.regions = 1;  // nothing to see anywhere: the zeros still have to be written
-    // A grid that fits on the device has no block to take over.
-    a.chunks = most > 16 * room ? kChunks : 1;
-    k_attend<T, DP, ES, NT><<<a.regions * a.chunks, kThreads, S::kSmem, s>>>(a);
+    a.grid = (uint32_t)(most < room ? most : room);
+    if (!a.grid) a.grid = 1;  // nothing to see anywhere: the zeros still have to be written
+    k_attend<T, DP, ES, NT><<<a.grid, kThreads, S::kSmem, s>>>(a);
     return true;
 }
 
