@@ -203,7 +203,7 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
                                         uint64_t *taken, uint64_t *pfull, uint64_t *pempty, Piece *pieces,
                                         uint32_t &bad) {
     using S = Shape<DP, ES, NT>;
-    const uint32_t g = lane >> 2, t4 = lane & 3, kv = lane >> 4;
+    const uint32_t g = lane >> 2, t4 = lane & 3;
     const uint32_t units_per_head = (a.group + S::kHeads - 1) / S::kHeads;
     auto unit_len = [&](uint32_t keys) { return keys ? (keys + a.tile - 1) / a.tile + S::kExtra : 0; };
     bool alive = true;  // no wait has run out
@@ -281,53 +281,66 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
         return false;
     };
 
-    // Two steps on their way: the block ids of one are loaded while the segment
-    // addresses of the one before are.  Loaded registers are used up where they
-    // are (a copy of one would wait for it), so lane i < 16 holds key i of each
-    // warp's 16 keys for K, lane 16 + i for V.
+    // Three steps on their way: the block ids of one are loaded, the table
+    // entries of the one before brought into L2, the segment addresses of the
+    // one before that loaded.  Loaded registers are used up where they are (a
+    // copy of one would wait for it).  A lane has the step's keys `lane` and
+    // `lane` + 32.
     struct Step {
-        uint32_t place[kWarps], valid;  // place in the page; a bit per warp: the block exists
-        uint32_t table, piece, warps;   // lane of the address table; warps with keys, 0 at the end
-        bool fresh;                     // the piece's first step
+        uint32_t place[2], valid;      // place in the page; a bit per key: its block exists
+        uint32_t table, piece, warps;  // lane of the address table; warps with keys, 0 at the end
+        bool fresh;                    // the piece's first step
     };
-    uint32_t ids[kWarps] = {};
-    uint64_t segs[kWarps] = {};
+    uint32_t ids[2] = {};
+    const uint64_t *entry[2];
+    uint64_t segs[2][2] = {};  // of K and V
     auto find_blocks = [&]() -> Step {
         Step s = {};
         if (k >= k1 && !next_piece()) return s;
         s.warps = k1 - k < kStep ? (k1 - k + 15) / 16 : kWarps;
         s.piece = np - 1;
         s.fresh = fresh;
-        s.table = a.c.first_lane + 2 * head + kv;
+        s.table = a.c.first_lane + 2 * head;
         const uint32_t *seq_blocks = a.blocks + (uint64_t)n * a.blocks_per_seq;
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) {
-            const uint32_t i = k + w * 16 + (lane & 15);
+        for (int u = 0; u < 2; u++) {
+            const uint32_t i = k + u * 32 + lane;
             const uint32_t pos = i < sv.sinks ? i : i + sv.shift, page = a.c.page.div(pos);
-            s.place[w] = pos - page * a.c.page.d;
-            s.valid |= (uint32_t)(i < k1) << w;
-            load_early(ids[w], seq_blocks + page, i < k1);
+            s.place[u] = pos - page * a.c.page.d;
+            s.valid |= (uint32_t)(i < k1) << u;
+            load_early(ids[u], seq_blocks + page, i < k1);
         }
         fresh = false;
         k = k1 - k < kStep ? k1 : k + kStep;
         return s;
     };
-    auto find_addrs = [&](Step &s) {
+    auto find_entries = [&](Step &s) {
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) {
-            const uint32_t id = ids[w], there = s.valid >> w & 1, known = id < a.c.B;
-            load_early(segs[w], a.c.addr + (uint64_t)id * a.c.L + s.table, there & known);
+        for (int u = 0; u < 2; u++) {
+            const uint32_t id = ids[u], there = s.valid >> u & 1, known = id < a.c.B;
+            entry[u] = a.c.addr + (there & known ? (uint64_t)id * a.c.L + s.table : 0);
             bad |= there & ~known ? KVX_S_BOUNDS : 0;
-            s.valid &= ~((known ^ 1) << w);
+            s.valid &= ~((known ^ 1) << u);
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(entry[u]));
         }
     };
+    auto find_addrs = [&](const Step &s) {
+#pragma unroll
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int kv = 0; kv < 2; kv++) load_early(segs[u][kv], entry[u] + kv, s.valid >> u & 1);
+    };
 
-    uint32_t handed[kWarps] = {};  // tiles handed to each warp so far
+    const uint64_t no_row = reinterpret_cast<uint64_t>(a.c.pool) | 1;
+    const uint64_t room = a.c.pool_bytes - a.c.span;  // a segment's largest offset, where any fits
+    const bool fits = a.c.pool_bytes >= a.c.span;
+    const uint32_t stride = (uint32_t)a.c.token_stride;
+    uint32_t handed = 0;  // tiles handed to warp lane%4 so far
     auto announce = [&](uint32_t p) {
         mbar_arrive_copies(&pfull[p % kPieces]);
         if (lane == 0) mbar_arrive(&pfull[p % kPieces]);
     };
-    auto issue = [&](const Step &s, const uint64_t (&row)[kWarps]) {
+    auto issue = [&](const Step &s, const uint64_t (&row)[2][2]) {
         if (s.fresh) {  // the piece's query heads, as the second operand's lanes hold them
             const uint32_t p = s.piece;
             const uint32_t q_of = p - S::kQBufs;  // the piece whose query was there before
@@ -350,34 +363,49 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
                 }
             announce(p);
         }
-#pragma unroll
-        for (int w = 0; w < kWarps; w++) {
-            if (w >= s.warps) break;
-            if (handed[w] && !mbar_wait(&taken[w], (handed[w] & 1) ^ 1)) {
-                alive = false;
-                return;
-            }
-            rows[w][lane] = row[w];
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&ready[w]);
-            handed[w]++;
+        const uint32_t w = lane % kWarps;
+        const bool mine = w < s.warps;
+        const bool free = !mine || !handed || mbar_wait(&taken[w], (handed & 1) ^ 1);
+        if (!__all_sync(0xFFFFFFFFu, free)) {
+            alive = false;
+            return;
         }
+        handed += mine;
+#pragma unroll
+        for (int u = 0; u < 2; u++) {
+            if (2 * u + lane / 16 >= s.warps) continue;
+            rows[2 * u + lane / 16][lane % 16] = row[u][0];
+            rows[2 * u + lane / 16][16 + lane % 16] = row[u][1];
+        }
+        __syncwarp();
+        if (lane < s.warps) mbar_arrive(&ready[lane]);
     };
 
-    Step next = find_blocks(), now = next;
+    // (find_blocks() is not asked again after it has said that there is no more)
+    Step now = find_blocks(), held = {}, next = {};
+    find_entries(now);
+    if (now.warps) held = find_blocks();
     find_addrs(now);
-    if (now.warps) next = find_blocks();
+    find_entries(held);
+    if (held.warps) next = find_blocks();
     while (alive && now.warps) {
-        uint64_t row[kWarps];
+        uint64_t row[2][2];
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) {
-            row[w] = reinterpret_cast<uint64_t>(a.c.pool) | 1;  // no such row
-            if ((now.valid >> w & 1) && a.c.ok(segs[w], bad)) row[w] += segs[w] + now.place[w] * a.c.token_stride - 1;
-        }
+        for (int u = 0; u < 2; u++)
+#pragma unroll
+            for (int kv = 0; kv < 2; kv++) {
+                const uint64_t seg = segs[u][kv];
+                const bool there = now.valid >> u & 1, good = fits && seg <= room && !((uint32_t)seg & 15);
+                row[u][kv] = no_row;
+                if (there && good) row[u][kv] = no_row - 1 + seg + (uint64_t)now.place[u] * stride;
+                if (there && !good) a.c.ok(seg, bad);
+            }
         const Step s = now;
-        now = next;
+        now = held;
         find_addrs(now);
-        if (now.warps) next = find_blocks();
+        held = next;
+        find_entries(held);
+        if (held.warps) next = find_blocks();
         issue(s, row);
     }
     if (alive) {  // the end of the stream

@@ -9,20 +9,19 @@
 
 namespace kvx {
 
-// Exact division of n < 2^31 by a fixed d >= 1: with s = 31 + ceil(log2 d)
-// and m = ceil(2^s / d), m*d - 2^s < d <= 2^(s-31), so n*m / 2^s exceeds n/d
-// by less than 1/d and the quotient's floor is right.
+// Exact division of n < 2^31 by a fixed 1 <= d < 2^31: with l = ceil(log2 d) and
+// m = ceil(2^(31+l) / d), m*d - 2^(31+l) < d <= 2^l, so n*m / 2^(31+l) exceeds
+// n/d by less than 1/d and its floor is the quotient.  2^31 <= m < 2^32.
 struct FastDiv {
-    uint64_t mul;
-    uint32_t shift, d;
+    uint32_t mul, shift, d;
     FastDiv() = default;
-    explicit FastDiv(uint32_t div) : d(div) {
-        uint32_t l = 0;
-        while ((1ull << l) < div) l++;
-        shift = 31 + l;
-        mul = ((1ull << shift) - 1) / div + 1;  // shift <= 62: d < 2^31
+    explicit FastDiv(uint32_t div) : shift(0), d(div) {
+        while ((1ull << shift) < div) shift++;
+        mul = (uint32_t)(((1ull << (31 + shift)) - 1) / div + 1);
     }
-    __host__ __device__ __forceinline__ uint32_t div(uint32_t n) const { return (uint32_t)((n * mul) >> shift); }
+    __host__ __device__ __forceinline__ uint32_t div(uint32_t n) const {
+        return (uint32_t)(((uint64_t)(n << 1) * mul) >> 32) >> shift;
+    }
 };
 
 struct CacheView {
