@@ -21,8 +21,9 @@
 namespace kvx {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kUnroll = 3;  // rows whose loads a lane has in flight
+constexpr int kThreads = 32;
+constexpr int kMinBlocks = 32;  // an SM
+constexpr int kUnroll = 2;  // rows that a lane works on at a time, with as many on their way
 
 struct AppendArgs {
     CacheView c;
@@ -34,8 +35,8 @@ struct AppendArgs {
     const int64_t *slots;
     void *q_out;
     uint32_t *status;
-    float eps;
-    uint32_t q_heads, rot, max_pos, interleaved;
+    float eps, inv_dim, inv_k_scale, inv_v_scale;
+    uint32_t q_heads, rot, max_pos;
 };
 
 template <class T>
@@ -59,142 +60,187 @@ __device__ __forceinline__ uint32_t e4m3x4(const float *x, float inv) {
 struct Eight {
     uint2 a, b;
 };
-template <class T>
-__device__ __forceinline__ Eight load8(const T *row, uint32_t da, uint32_t db) {
-    return Eight{*reinterpret_cast<const uint2 *>(row + da), *reinterpret_cast<const uint2 *>(row + db)};
-}
 
-// Lanes of a row: a power of two with 8 * LANES >= dim.
-template <class T, bool FP8, int LANES>
-__global__ void __launch_bounds__(kThreads, 4) k_append(const __grid_constant__ AppendArgs a) {
-    constexpr uint32_t kRows = kThreads / LANES;
-    const uint64_t t = blockIdx.x;
-    const uint32_t li = threadIdx.x % LANES;
-    // the lanes of this row, whose shuffles other rows take no part in
-    const uint32_t mask = LANES == 32 ? 0xFFFFFFFFu : ((1u << LANES % 32) - 1) << (threadIdx.x % 32 / LANES * LANES);
-    const uint32_t dim = a.c.dim, heads = a.c.heads, rows = a.q_heads + 2 * heads;
-    const bool in = li * 8 < dim;
-    uint32_t bad = 0;
+// One token's part that a lane works on.
+struct Lane {
+    uint32_t da, db;           // its values: da .. da+3 and db .. db+3
+    bool in, turns;            // within the head; among the rotated values
+    float4 c, s;               // its pairs' angles
+    uint32_t first, at, step;  // rows of a section: the warp's first, the lane's among those, to the warp's next
+};
 
-    // values da .. da+3 and db .. db+3: rotated halves hold each other's
-    // partners, neighbours are partners anyway
-    const bool turns = li * 8 < a.rot, halves = turns && !a.interleaved;
-    const uint32_t da = halves ? li * 4 : li * 8, db = halves ? da + a.rot / 2 : da + 4;
+enum Kind { kQuery, kKey, kValue };
 
-    const int64_t slot = a.slots[t];
-    uint32_t block = 0, place = 0;
-    bool write = slot >= 0;
-    if (write) {
-        const uint64_t b = (uint64_t)slot < (1ull << 31) ? a.c.page.div((uint32_t)slot) : (uint64_t)slot / a.c.page.d;
-        place = (uint32_t)((uint64_t)slot - b * a.c.page.d);
-        if (b >= a.c.B) {
-            bad |= KVX_S_BOUNDS;
-            write = false;
-        } else {
-            block = (uint32_t)b;
-        }
-    }
-
-    float4 c = make_float4(1, 1, 1, 1), s = make_float4(0, 0, 0, 0);
-    if (a.rot) {
-        const uint32_t pos = a.positions[t];
-        if (pos >= a.max_pos) {  // the same for the whole block
-            if (threadIdx.x == 0) raise(a.status, bad | KVX_S_BOUNDS);
-            return;
-        }
-        if (turns) {
-            const float *row = a.cos_sin + (uint64_t)pos * a.rot + li * 4;
-            c = __ldg(reinterpret_cast<const float4 *>(row));
-            s = __ldg(reinterpret_cast<const float4 *>(row + a.rot / 2));
-        }
-    }
-    Eight wq = {}, wk = {};
-    if (in && a.q_weight) wq = load8(static_cast<const T *>(a.q_weight), da, db);
-    if (in && a.k_weight) wk = load8(static_cast<const T *>(a.k_weight), da, db);
-
-    const T *q = static_cast<const T *>(a.q) + t * a.q_stride;
-    const T *k = static_cast<const T *>(a.k) + t * a.k_stride;
-    const T *v = static_cast<const T *>(a.v) + t * a.v_stride;
-    const uint32_t step = gridDim.y * kRows;
-    for (uint32_t r0 = blockIdx.y * kRows + threadIdx.x / LANES; r0 < rows; r0 += kUnroll * step) {
-        Eight raw[kUnroll] = {};
+// All of a token's rows of one kind.  Loads run a round ahead.
+template <class T, bool FP8, int LANES, bool NEIGHBOURS, Kind KIND>
+struct Section {
+    const AppendArgs &a;
+    const Lane &l;
+    const T *src;
+    uint32_t rows;
+    Eight raw[kUnroll];
+    __device__ __forceinline__ Section(const AppendArgs &args, const Lane &lane, const T *from, uint32_t n)
+        : a(args), l(lane), src(from), rows(n) {}
+    __device__ __forceinline__ void load(uint32_t r0) {
 #pragma unroll
         for (int u = 0; u < kUnroll; u++) {
-            const uint32_t r = r0 + u * step;
-            if (in && r < rows)
-                raw[u] = load8(r < a.q_heads           ? q + (uint64_t)r * dim
-                               : r < a.q_heads + heads ? k + (uint64_t)(r - a.q_heads) * dim
-                                                       : v + (uint64_t)(r - a.q_heads - heads) * dim,
-                               da, db);
+            const uint32_t r = r0 + l.at + u * l.step;
+            raw[u] = Eight{};
+            if (l.in && r < rows) {
+                const T *row = src + r * a.c.dim;
+                raw[u].a = *reinterpret_cast<const uint2 *>(row + l.da);
+                raw[u].b = *reinterpret_cast<const uint2 *>(row + l.db);
+            }
         }
+    }
+    // entry: the block's address-table entries from head 0's K on, or NULL
+    __device__ __forceinline__ void run(const void *weight, T *q_out, const uint64_t *entry, uint64_t place, uint64_t room,
+                                        uint32_t &bad) {
+        float w[8];
 #pragma unroll
-        for (int u = 0; u < kUnroll; u++) {
-            const uint32_t r = r0 + u * step;
-            if (r >= rows) break;
-            const bool is_q = r < a.q_heads, is_v = r >= a.q_heads + heads;
-            float x[8];
-            unpack4<T>(raw[u].a, x);
-            unpack4<T>(raw[u].b, x + 4);
-            if (!is_v) {
-                if (is_q ? a.q_weight : a.k_weight) {
+        for (int e = 0; e < 8; e++) w[e] = 1.0f;
+        if (KIND != kValue && weight && l.in) {
+            unpack4<T>(*reinterpret_cast<const uint2 *>(static_cast<const T *>(weight) + l.da), w);
+            unpack4<T>(*reinterpret_cast<const uint2 *>(static_cast<const T *>(weight) + l.db), w + 4);
+        }
+        const bool norm = KIND != kValue && weight;
+#pragma unroll 1
+        for (uint32_t r0 = l.first; r0 < rows; r0 += kUnroll * l.step) {  // the same turns for a whole warp
+            Eight cur[kUnroll];
+            uint64_t seg[kUnroll];
+#pragma unroll
+            for (int u = 0; u < kUnroll; u++) {
+                cur[u] = raw[u];
+                const uint32_t r = r0 + l.at + u * l.step;
+                if (KIND != kQuery && entry && r < rows) seg[u] = __ldg(entry + 2 * r + (KIND == kValue));
+            }
+            load(r0 + kUnroll * l.step);
+#pragma unroll
+            for (int u = 0; u < kUnroll; u++) {
+                const uint32_t r = r0 + l.at + u * l.step;
+                float x[8];
+                unpack4<T>(cur[u].a, x);
+                unpack4<T>(cur[u].b, x + 4);
+                if (norm) {
                     float ss = 0;
 #pragma unroll
                     for (int e = 0; e < 8; e++) ss = fmaf(x[e], x[e], ss);
 #pragma unroll
-                    for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(mask, ss, o);
-                    const float inv = rsqrtf(ss / (float)dim + a.eps);
-                    float w[8];
-                    unpack4<T>(is_q ? wq.a : wk.a, w);
-                    unpack4<T>(is_q ? wq.b : wk.b, w + 4);
+                    for (int o = LANES / 2; o; o >>= 1) ss += __shfl_xor_sync(0xFFFFFFFFu, ss, o);
+                    const float inv = rsqrtf(fmaf(ss, a.inv_dim, a.eps));
 #pragma unroll
-                    for (int e = 0; e < 8; e++) x[e] = x[e] * inv * w[e];
+                    for (int e = 0; e < 8; e++) x[e] *= inv * w[e];
                 }
-                if (turns) {
-                    const float cc[4] = {c.x, c.y, c.z, c.w}, sn[4] = {s.x, s.y, s.z, s.w};
+                if (KIND != kValue && l.turns) {
+                    const float cc[4] = {l.c.x, l.c.y, l.c.z, l.c.w}, sn[4] = {l.s.x, l.s.y, l.s.z, l.s.w};
 #pragma unroll
                     for (int i = 0; i < 4; i++) {  // pair i: values i and i+4, or 2i and 2i+1
-                        const float ya = a.interleaved ? x[2 * i] : x[i], yb = a.interleaved ? x[2 * i + 1] : x[i + 4];
-                        const float za = fmaf(-yb, sn[i], ya * cc[i]), zb = fmaf(ya, sn[i], yb * cc[i]);
-                        if (a.interleaved)
-                            x[2 * i] = za, x[2 * i + 1] = zb;
-                        else
-                            x[i] = za, x[i + 4] = zb;
+                        constexpr int other = NEIGHBOURS ? 1 : 4;
+                        const int j = NEIGHBOURS ? 2 * i : i;
+                        const float ya = x[j], yb = x[j + other];
+                        x[j] = fmaf(-yb, sn[i], ya * cc[i]);
+                        x[j + other] = fmaf(ya, sn[i], yb * cc[i]);
                     }
                 }
-            }
-            if (!in) continue;
-            if (is_q) {
-                T *o = static_cast<T *>(a.q_out) + t * a.q_out_stride + (uint64_t)r * dim;
-                *reinterpret_cast<uint2 *>(o + da) = pack4<T>(x);
-                *reinterpret_cast<uint2 *>(o + db) = pack4<T>(x + 4);
-            } else if (write) {
-                const uint32_t h = is_v ? r - a.q_heads - heads : r - a.q_heads;
-                const uint64_t at = __ldg(a.c.lane_addr(block, h, is_v));
-                if (a.c.ok(at, bad)) {
-                    uint8_t *o = a.c.pool + at + place * a.c.token_stride;
+                if (!l.in || r >= rows) continue;
+                if constexpr (KIND == kQuery) {
+                    T *o = q_out + r * a.c.dim;
+                    *reinterpret_cast<uint2 *>(o + l.da) = pack4<T>(x);
+                    *reinterpret_cast<uint2 *>(o + l.db) = pack4<T>(x + 4);
+                } else if (entry) {
+                    if (seg[u] > room || ((uint32_t)seg[u] & 15)) {
+                        a.c.ok(seg[u], bad);
+                        continue;
+                    }
+                    uint8_t *o = a.c.pool + (seg[u] + place);
                     if constexpr (FP8) {
-                        const float inv = 1.0f / (is_v ? a.c.v_scale : a.c.k_scale);
-                        *reinterpret_cast<uint32_t *>(o + da) = e4m3x4(x, inv);
-                        *reinterpret_cast<uint32_t *>(o + db) = e4m3x4(x + 4, inv);
+                        const float inv = KIND == kValue ? a.inv_v_scale : a.inv_k_scale;
+                        *reinterpret_cast<uint32_t *>(o + l.da) = e4m3x4(x, inv);
+                        *reinterpret_cast<uint32_t *>(o + l.db) = e4m3x4(x + 4, inv);
+                    } else if constexpr (KIND == kValue) {
+                        *reinterpret_cast<uint2 *>(o + 2 * l.da) = cur[u].a;
+                        *reinterpret_cast<uint2 *>(o + 2 * l.db) = cur[u].b;
                     } else {
-                        *reinterpret_cast<uint2 *>(o + 2 * da) = pack4<T>(x);
-                        *reinterpret_cast<uint2 *>(o + 2 * db) = pack4<T>(x + 4);
+                        *reinterpret_cast<uint2 *>(o + 2 * l.da) = pack4<T>(x);
+                        *reinterpret_cast<uint2 *>(o + 2 * l.db) = pack4<T>(x + 4);
                     }
                 }
             }
         }
     }
+};
+
+// Lanes of a row: a power of two with 8 * LANES >= dim.
+template <class T, bool FP8, int LANES, bool NEIGHBOURS>
+__global__ void __launch_bounds__(kThreads, kMinBlocks) k_append(const __grid_constant__ AppendArgs a) {
+    constexpr uint32_t kRows = kThreads / LANES, kWarpRows = 32 / LANES;
+    const uint64_t t = blockIdx.x;
+    const uint32_t li = threadIdx.x % LANES, heads = a.c.heads;
+    uint32_t bad = 0;
+    Lane l;
+    l.in = li * 8 < a.c.dim;
+    l.turns = li * 8 < a.rot;
+    // rotated halves hold each other's partners, neighbours are partners anyway
+    const bool halves = l.turns && !NEIGHBOURS;
+    l.da = halves ? li * 4 : li * 8;
+    l.db = halves ? l.da + a.rot / 2 : l.da + 4;
+    l.step = gridDim.y * kRows;
+    l.at = threadIdx.x / LANES % kWarpRows;
+    l.first = blockIdx.y * kRows + threadIdx.x / LANES - l.at;
+
+    // Two rounds of latency to the first store: the values, the slot and the
+    // position, then the angles and the segments' addresses.
+    Section<T, FP8, LANES, NEIGHBOURS, kQuery> q(a, l, static_cast<const T *>(a.q) + t * a.q_stride, a.q_heads);
+    Section<T, FP8, LANES, NEIGHBOURS, kKey> k(a, l, static_cast<const T *>(a.k) + t * a.k_stride, heads);
+    Section<T, FP8, LANES, NEIGHBOURS, kValue> v(a, l, static_cast<const T *>(a.v) + t * a.v_stride, heads);
+    q.load(l.first);
+    const int64_t slot = a.slots[t];
+    const uint32_t pos = a.rot ? a.positions[t] : 0;
+    if (a.rot && pos >= a.max_pos) {  // the same for the whole block
+        if (threadIdx.x == 0) raise(a.status, KVX_S_BOUNDS);
+        return;
+    }
+    if (l.turns) {
+        const float *row = a.cos_sin + (uint64_t)pos * a.rot + li * 4;
+        l.c = __ldg(reinterpret_cast<const float4 *>(row));
+        l.s = __ldg(reinterpret_cast<const float4 *>(row + a.rot / 2));
+    }
+    const uint64_t *entry = nullptr;
+    uint64_t place = 0;
+    if (slot >= 0) {
+        const uint64_t b = (uint64_t)slot < (1ull << 31) ? a.c.page.div((uint32_t)slot) : (uint64_t)slot / a.c.page.d;
+        place = ((uint64_t)slot - b * a.c.page.d) * a.c.token_stride;
+        if (b < a.c.B)
+            entry = a.c.lane_addr((uint32_t)b, 0, 0);
+        else
+            bad |= KVX_S_BOUNDS;
+    }
+    const uint64_t room = a.c.pool_bytes - a.c.span;  // a segment's largest offset, where any fits
+    if (entry && a.c.pool_bytes < a.c.span) {
+        bad |= KVX_S_BOUNDS;
+        entry = nullptr;
+    }
+    k.load(l.first);
+    q.run(a.q_weight, static_cast<T *>(a.q_out) + t * a.q_out_stride, nullptr, 0, 0, bad);
+    v.load(l.first);
+    k.run(a.k_weight, nullptr, entry, place, room, bad);
+    v.run(nullptr, nullptr, entry, place, room, bad);
     raise(a.status, bad);
 }
 
-template <class T, bool FP8>
-void launch(const AppendArgs &a, dim3 grid, cudaStream_t s) {
+template <class T, bool FP8, bool NEIGHBOURS>
+void launch_one(const AppendArgs &a, dim3 grid, cudaStream_t s) {
     if (a.c.dim <= 64)
-        k_append<T, FP8, 8><<<grid, kThreads, 0, s>>>(a);
+        k_append<T, FP8, 8, NEIGHBOURS><<<grid, kThreads, 0, s>>>(a);
     else if (a.c.dim <= 128)
-        k_append<T, FP8, 16><<<grid, kThreads, 0, s>>>(a);
+        k_append<T, FP8, 16, NEIGHBOURS><<<grid, kThreads, 0, s>>>(a);
     else
-        k_append<T, FP8, 32><<<grid, kThreads, 0, s>>>(a);
+        k_append<T, FP8, 32, NEIGHBOURS><<<grid, kThreads, 0, s>>>(a);
+}
+
+template <class T, bool FP8>
+void launch(const AppendArgs &a, dim3 grid, bool neighbours, cudaStream_t s) {
+    neighbours ? launch_one<T, FP8, true>(a, grid, s) : launch_one<T, FP8, false>(a, grid, s);
 }
 
 }  // namespace
@@ -219,18 +265,25 @@ extern "C" kvx_status kvx_append_tokens(const kvx_cache *cache, const void *q, u
     if (!T) return KVX_OK;
     if (!k || !v || !slots || (q_heads && (!q || !q_out))) return KVX_EINVAL;
     AppendArgs a = {cache_view(cache), q, k, v, q_stride, k_stride, v_stride, q_out_stride, q_weight, k_weight,
-                    cos_sin, positions, slots, q_out, status, eps, q_heads, rot_dim, max_pos, interleaved};
+                    cos_sin, positions, slots, q_out, status, eps, 1.0f / cache->dim, 1.0f / cache->k_scale,
+                    1.0f / cache->v_scale, q_heads, rot_dim, max_pos};
     const uint32_t lanes = cache->dim <= 64 ? 8 : cache->dim <= 128 ? 16 : 32;
     const uint32_t per_block = kThreads / lanes, rows = q_heads + 2 * cache->heads;
-    // A token's rows over several blocks while that fills the device's first wave (8 blocks an SM).
-    const uint64_t most = ceil_div(rows, per_block), room = ceil_div(8 * (uint64_t)sm_count(), T);
-    const dim3 grid(T, (uint32_t)(most < room ? most : room));
+    // A token's rows go to several blocks while those fit on the device
+    // together.  Beyond that, to two where the last wave is short of blocks: a
+    // block's start costs as much as about kStart of its rounds.
+    const uint64_t most = ceil_div(rows, per_block), fit = (uint64_t)kMinBlocks * sm_count();
+    uint64_t parts = T < fit ? fit / T : 1;
+    constexpr uint64_t kStart = 4;
+    if (parts == 1 && ceil_div(2 * (uint64_t)T, fit) * (kStart + ceil_div(most, 2)) < ceil_div(T, fit) * (kStart + most))
+        parts = 2;
+    const dim3 grid(T, (uint32_t)(most < parts ? most : parts));
     if (dtype == KVX_BF16)
-        cache->dtype == KVX_E4M3 ? launch<__nv_bfloat16, true>(a, grid, as_stream(stream))
-                                 : launch<__nv_bfloat16, false>(a, grid, as_stream(stream));
+        cache->dtype == KVX_E4M3 ? launch<__nv_bfloat16, true>(a, grid, interleaved != 0, as_stream(stream))
+                                 : launch<__nv_bfloat16, false>(a, grid, interleaved != 0, as_stream(stream));
     else
-        cache->dtype == KVX_E4M3 ? launch<__half, true>(a, grid, as_stream(stream))
-                                 : launch<__half, false>(a, grid, as_stream(stream));
+        cache->dtype == KVX_E4M3 ? launch<__half, true>(a, grid, interleaved != 0, as_stream(stream))
+                                 : launch<__half, false>(a, grid, interleaved != 0, as_stream(stream));
     KVX_LAUNCHED();
     return KVX_OK;
 }

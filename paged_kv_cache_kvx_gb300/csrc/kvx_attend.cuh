@@ -137,8 +137,8 @@ struct Shape {
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static_assert(kStages >= 2, "");
     // What a unit costs beside its keys (its query, its output) counts as so
-    // many tiles when work is shared out: about 16 KB of copies.
-    static constexpr uint32_t kExtra = DP * ES >= 128 ? 1 : 2;
+    // many tiles when work is shared out: about 32 KB of copies.
+    static constexpr uint32_t kExtra = DP * ES >= 256 ? 1 : 256 / (DP * ES);
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kQ = NT * kQVecs * 32 * 16;
     static constexpr int kJoin = (DP / 16 + 1) * NT * 32 * 16;
