@@ -17,6 +17,10 @@ namespace {
 constexpr int kSelThreads = 1024;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
+constexpr uint32_t kHeld = 51200;  // keys that a block keeps in shared memory
+constexpr int kSelUnroll = 8;
+// Keys that no score has: a token that is not there, and one that stays in any case.
+constexpr uint32_t kAbsent = 0, kStays = 0xFFFFFFFFu;
 constexpr int kRows = 64;  // tokens whose K and V rows a block of k_gather copies
 constexpr int kGatherThreads = 256;
 
@@ -40,7 +44,8 @@ __device__ __forceinline__ uint32_t key_of(float f) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ EvictArgs a) {
+__global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ EvictArgs a, uint32_t held) {
+    extern __shared__ __align__(16) uint32_t keys[];  // [held], of the first tokens; held is a multiple of four
     __shared__ uint32_t hist[kBins];
     __shared__ uint32_t sh_scan[33];
     __shared__ uint32_t sh_digit, sh_left;
@@ -74,32 +79,71 @@ __global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ 
     const uint32_t hi = len - recent;  // tokens lo .. hi-1 compete for `take` places
     const uint32_t take = a.budget - lo - recent;
 
+    auto make_key = [&](uint32_t i, float v) { return i >= lo && i < hi ? key_of(v) : kStays; };
+    // Keys of tokens i .. i+3, i a multiple of four.
+    auto keys_at = [&](uint32_t i) -> uint4 {
+        if (i < held) return *reinterpret_cast<const uint4 *>(keys + i);
+        uint32_t k[4];
+#pragma unroll
+        for (int u = 0; u < 4; u++) k[u] = i + u < len ? make_key(i + u, __ldg(x + i + u)) : kAbsent;
+        return make_uint4(k[0], k[1], k[2], k[3]);
+    };
+
+    for (uint32_t i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
+    __syncthreads();
+    const uint32_t padded = (len + 3) & ~3u;
+    for (uint32_t i0 = threadIdx.x; i0 < padded; i0 += kSelUnroll * kSelThreads) {
+        float v[kSelUnroll];
+#pragma unroll
+        for (int u = 0; u < kSelUnroll; u++) v[u] = i0 + u * kSelThreads < len ? __ldg(x + i0 + u * kSelThreads) : 0;
+#pragma unroll
+        for (int u = 0; u < kSelUnroll; u++) {
+            const uint32_t i = i0 + u * kSelThreads;
+            if (i >= padded) break;
+            const uint32_t k = i < len ? make_key(i, v[u]) : kAbsent;
+            if (i < held) keys[i] = k;
+            if (k != kAbsent && k != kStays) atomicAdd(&hist[k >> 21], 1u);
+        }
+    }
+    __syncthreads();
+
     // the threshold: the take-th largest key, and how many of its equals stay
-    uint32_t cut = 0, left = take;
+    uint32_t cut = take ? 0 : kStays - 1, left = take;
     if (take) {
 #pragma unroll 1
         for (int pass = 0; pass < 3; pass++) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-            const uint32_t bins = pass == 2 ? 1024 : 2048;
-            const uint32_t known = pass == 0 ? 0 : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
-            for (uint32_t i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
-            __syncthreads();
-            for (uint32_t i = lo + threadIdx.x; i < hi; i += kSelThreads) {
-                const uint32_t k = key_of(__ldg(x + i));
-                if ((k & known) == cut) atomicAdd(&hist[k >> shift & (bins - 1)], 1u);
+            if (pass) {
+                const uint32_t bins = pass == 2 ? 1024 : 2048, known = pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+                for (uint32_t i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
+                __syncthreads();
+                auto add = [&](uint32_t k) {  // (no cut begins like kStays)
+                    if ((k & known) == cut) atomicAdd(&hist[k >> shift & (bins - 1)], 1u);
+                };
+#pragma unroll 2
+                for (uint32_t i = 4 * threadIdx.x; i < padded; i += 4 * kSelThreads) {
+                    const uint4 k = keys_at(i);
+                    add(k.x), add(k.y), add(k.z), add(k.w);
+                }
+                __syncthreads();
             }
-            __syncthreads();
-            // two bins a thread, from the largest down
-            const uint32_t b1 = kBins - 1 - 2 * threadIdx.x, b0 = b1 - 1;
-            const uint32_t h1 = hist[b1], h0 = hist[b0];
-            uint32_t total;
-            const uint32_t above = block_excl_sum<uint32_t>(h1 + h0, sh_scan, &total);
-            if (above < left && above + h1 >= left) {
-                sh_digit = b1;
-                sh_left = left - above;
-            } else if (above + h1 < left && above + h1 + h0 >= left) {
-                sh_digit = b0;
-                sh_left = left - above - h1;
+            // some bins a thread, from the largest down
+            constexpr int kPer = kBins / kSelThreads;
+            const uint32_t top = kBins - 1 - kPer * threadIdx.x;
+            uint32_t sum = 0, total;
+#pragma unroll
+            for (int i = 0; i < kPer; i++) sum += hist[top - i];
+            uint32_t above = block_excl_sum<uint32_t>(sum, sh_scan, &total);
+            if (above < left && above + sum >= left) {
+                for (uint32_t b = top;; b--) {
+                    const uint32_t h = hist[b];
+                    if (above + h >= left) {
+                        sh_digit = b;
+                        sh_left = left - above;
+                        break;
+                    }
+                    above += h;
+                }
             }
             __syncthreads();
             cut |= sh_digit << shift;
@@ -109,40 +153,51 @@ __global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ 
     }
 
     // every warp counts its stretch, then writes it at its place
-    const uint32_t per = ((len + kSelWarps - 1) / kSelWarps + 31) & ~31u;
-    const uint32_t from = warp * per < len ? warp * per : len, to = from + per < len ? from + per : len;
-    auto classify = [&](uint32_t i, bool &over, bool &tie) {
-        const uint32_t k = i < to ? key_of(__ldg(x + i)) : 0;
-        const bool competes = i >= lo && i < hi;
-        over = i < to && (!competes || (take && k > cut));
-        tie = i < to && competes && take && k == cut;
-    };
+    const uint32_t per = (padded + 128 * kSelWarps - 1) / (128 * kSelWarps) * 128;
+    const uint32_t from = warp * per < padded ? warp * per : padded, to = from + per < padded ? from + per : padded;
     uint32_t n_over = 0, n_ties = 0;
-    for (uint32_t i0 = from; i0 < to; i0 += 32) {
-        bool over, tie;
-        classify(i0 + lane, over, tie);
-        n_over += __popc(__ballot_sync(0xFFFFFFFFu, over));
-        n_ties += __popc(__ballot_sync(0xFFFFFFFFu, tie));
+#pragma unroll 2
+    for (uint32_t i = from + 4 * lane; i < to; i += 128) {
+        const uint4 k = keys_at(i);
+        n_over += (k.x > cut) + (k.y > cut) + (k.z > cut) + (k.w > cut);
+        n_ties += (k.x == cut) + (k.y == cut) + (k.z == cut) + (k.w == cut);
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        n_over += __shfl_xor_sync(0xFFFFFFFFu, n_over, o);
+        n_ties += __shfl_xor_sync(0xFFFFFFFFu, n_ties, o);
     }
     if (lane == 0) sh_over[warp] = n_over, sh_ties[warp] = n_ties;
     __syncthreads();
-    uint32_t over_before = 0, ties_before = 0;
-    for (uint32_t w = 0; w < warp; w++) over_before += sh_over[w], ties_before += sh_ties[w];
-    for (uint32_t i0 = from; i0 < to; i0 += 32) {
-        const uint32_t i = i0 + lane;
-        bool over, tie;
-        classify(i, over, tie);
-        const uint32_t mo = __ballot_sync(0xFFFFFFFFu, over), mt = __ballot_sync(0xFFFFFFFFu, tie);
-        const uint32_t below = (1u << lane) - 1;
-        const uint32_t ties = ties_before + __popc(mt & below);
-        if (over || (tie && ties < left)) {
-            const uint32_t at = over_before + __popc(mo & below) + (ties < left ? ties : left);
-            kept[at] = i;
-            ks[at] = __ldg(x + i);
-        }
-        over_before += __popc(mo);
-        ties_before += __popc(mt);
+    uint32_t over = lane < warp ? sh_over[lane] : 0, ties = lane < warp ? sh_ties[lane] : 0;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        over += __shfl_xor_sync(0xFFFFFFFFu, over, o);
+        ties += __shfl_xor_sync(0xFFFFFFFFu, ties, o);
     }
+    for (uint32_t i0 = from; i0 < to; i0 += 128) {
+        const uint32_t i = i0 + 4 * lane;
+        uint4 k = make_uint4(kAbsent, kAbsent, kAbsent, kAbsent);
+        if (i < to) k = keys_at(i);
+        const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
+        uint32_t both = 0;  // over the threshold, and equal to it, in halves
+#pragma unroll
+        for (int u = 0; u < 4; u++) both += (kk[u] > cut) + ((uint32_t)(kk[u] == cut) << 16);
+        const uint32_t incl = warp_incl_sum(both), before = incl - both;
+        uint32_t o = over + (before & 0xFFFF), t = ties + (before >> 16);
+#pragma unroll
+        for (int u = 0; u < 4; u++) {
+            if (kk[u] > cut || (kk[u] == cut && t < left)) kept[o + (t < left ? t : left)] = i + u;
+            o += kk[u] > cut;
+            t += kk[u] == cut;
+        }
+        const uint32_t all = __shfl_sync(0xFFFFFFFFu, incl, 31);
+        over += all & 0xFFFF;
+        ties += all >> 16;
+    }
+    __syncthreads();
+#pragma unroll 4
+    for (uint32_t i = threadIdx.x; i < keep; i += kSelThreads) ks[i] = __ldg(x + __ldcg(kept + i));
 }
 
 // Copies kRows tokens' K and V rows: a thread looks up each row's two places,
@@ -231,7 +286,16 @@ extern "C" kvx_status kvx_evict(const kvx_cache *cache, uint32_t num_seqs, const
     EvictArgs a = {cache_view(cache), blocks, lens, scores, scores_stride, dst_blocks, kept, kept_scores, new_lens,
                    status, num_seqs, blocks_per_seq, dst_per_seq, (uint32_t)max_len, budget, sinks, recent};
     const cudaStream_t s = as_stream(stream);
-    k_select<<<num_seqs * cache->heads, kSelThreads, 0, s>>>(a);
+    const uint32_t held = max_len < kHeld ? ((uint32_t)max_len + 3) & ~3u : kHeld;
+    static bool done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return KVX_ECUDA;
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+        if (cudaFuncSetAttribute(k_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4) != cudaSuccess)
+            return KVX_ECUDA;
+        if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+    k_select<<<num_seqs * cache->heads, kSelThreads, held * 4, s>>>(a, held);
     KVX_LAUNCHED();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((uint32_t)ceil_div(budget, kRows) * cache->heads * num_seqs);
