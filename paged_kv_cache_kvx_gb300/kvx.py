@@ -126,8 +126,15 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# torch's own way to the current stream's handle, without the Stream object
+# around it (2.8 us a call less); the public way where it is missing.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
@@ -530,17 +537,19 @@ def _need(ok, what):
 def _heads(t, name, shape, dtype):
     """The distance between tokens, in elements, of an activation [tokens, heads,
     dim] whose tokens' heads are contiguous."""
-    dim = shape[2]
     if t.shape == shape and t.dtype is dtype:
         token, head, one = t.stride()
-        if (one == 1 and (head == dim or shape[1] < 2)) or t.numel() == 0:
-            return token if shape[0] > 1 else shape[1] * dim  # a single token's stride says nothing
+        tokens, heads, dim = shape
+        if (one == 1 and (head == dim or heads < 2)) or not tokens or not heads:
+            return token if tokens > 1 else heads * dim  # a single token's stride says nothing
     raise KvxError("%s: %s %s with a token's heads contiguous" % (name, dtype, list(shape)))
 
 
 def _table(t, name, dtypes, shape):
-    if not (t.shape == shape and t.dtype in dtypes and t.is_contiguous()):
-        raise KvxError("%s: contiguous %s of %s" % (name, list(shape), " or ".join(str(d) for d in dtypes)))
+    """The pointer of a contiguous tensor of the given shape and one of the types."""
+    if t.shape == shape and t.dtype in dtypes and t.is_contiguous():
+        return t.data_ptr()
+    raise KvxError("%s: contiguous %s of %s" % (name, list(shape), " or ".join(str(d) for d in dtypes)))
 
 
 class Cache:
@@ -565,6 +574,7 @@ class Cache:
                              page_tokens=page_tokens, token_stride=row if token_stride is None else token_stride,
                              k_scale=k_scale, v_scale=v_scale)
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
+        self._ref, self._status = ctypes.byref(self.c), self.status.data_ptr()
 
     def append(self, q, k, v, positions, slots, q_out, q_weight=None, k_weight=None, eps: float = 1e-6, cos_sin=None,
                interleaved: bool = False, stream=None):
@@ -574,21 +584,21 @@ class Cache:
         _need(q.dim() == 3, "q: [tokens, q_heads, dim]")
         (T, q_heads, _), act, dim = q.shape, q.dtype, self.dim
         _need(act in _ACTS, "q: bfloat16 or float16")
-        kv = (T, self.heads, dim)
-        qs, ks, vs = _heads(q, "q", (T, q_heads, dim), act), _heads(k, "k", kv, act), _heads(v, "v", kv, act)
-        os_ = _heads(q_out, "q_out", (T, q_heads, dim), act)
-        _table(slots, "slots", _SLOTS, (T,))
-        if q_weight is not None:
-            _table(q_weight, "q_weight", (act,), (dim,))
-        if k_weight is not None:
-            _table(k_weight, "k_weight", (act,), (dim,))
-        max_pos = rot = 0
+        queries, keys = (T, q_heads, dim), (T, self.heads, dim)
+        qs, os_ = _heads(q, "q", queries, act), _heads(q_out, "q_out", queries, act)
+        ks, vs = _heads(k, "k", keys, act), _heads(v, "v", keys, act)
+        wq = None if q_weight is None else _table(q_weight, "q_weight", (act,), (dim,))
+        wk = None if k_weight is None else _table(k_weight, "k_weight", (act,), (dim,))
+        angles = pos = None
+        most = rot = 0
         if cos_sin is not None:
-            max_pos, rot = cos_sin.shape
-            _table(cos_sin, "cos_sin", _FLOAT, (max_pos, rot))
-            _table(positions, "positions", _IDS, (T,))
-        kvx_append_tokens(self.c, q, qs, k, ks, v, vs, _DTYPES[act], T, q_heads, q_weight, k_weight, eps, cos_sin, rot,
-                          max_pos, 1 if interleaved else 0, positions, slots, q_out, os_, self.status, stream)
+            most, rot = cos_sin.shape
+            angles = _table(cos_sin, "cos_sin", _FLOAT, (most, rot))
+            pos = _table(positions, "positions", _IDS, (T,))
+        _check(lib().kvx_append_tokens(self._ref, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[act], T,
+                                       q_heads, wq, wk, eps, angles, rot, most, 1 if interleaved else 0, pos,
+                                       _table(slots, "slots", _SLOTS, (T,)), q_out.data_ptr(), os_, self._status,
+                                       _stream(stream)), "kvx_append_tokens")
 
     def attend_workspace(self, num_seqs: int, q_heads: int, blocks_per_seq: int, window: int = 0, sinks: int = 0,
                          scores: bool = False):
@@ -605,16 +615,17 @@ class Cache:
         _need(q.dim() == 3 and blocks.dim() == 2, "q: [num_seqs, q_heads, dim], blocks: [num_seqs, blocks_per_seq]")
         (N, q_heads, _), act, dim, per, stride = q.shape, q.dtype, self.dim, blocks.shape[1], 0
         _need(act in _ACTS, "q: bfloat16 or float16")
-        qs, os_ = _heads(q, "q", (N, q_heads, dim), act), _heads(out, "out", (N, q_heads, dim), act)
-        _table(blocks, "blocks", _IDS, (N, per))
-        _table(lens, "lens", _IDS, (N,))
+        queries, sums, weights = (N, q_heads, dim), None, None
         if lse is not None:
-            _table(lse, "lse", _FLOAT, (N, q_heads))
+            sums = _table(lse, "lse", _FLOAT, (N, q_heads))
         if scores is not None:
             stride = scores.shape[-1]
-            _table(scores, "scores", _FLOAT, (N, self.heads, stride))
-        kvx_attend(self.c, q, qs, _DTYPES[act], N, q_heads, blocks, per, lens, dim ** -0.5 if scale is None else scale,
-                   window, sinks, out, os_, lse, scores, stride, self.status, ws, stream)
+            weights = _table(scores, "scores", _FLOAT, (N, self.heads, stride))
+        _check(lib().kvx_attend(self._ref, q.data_ptr(), _heads(q, "q", queries, act), _DTYPES[act], N, q_heads,
+                                _table(blocks, "blocks", _IDS, (N, per)), per, _table(lens, "lens", _IDS, (N,)),
+                                dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
+                                _heads(out, "out", queries, act), sums, weights, stride, self._status, ws.data_ptr(),
+                                ws.numel(), _stream(stream)), "kvx_attend")
 
     def evict_workspace(self, num_seqs: int, blocks_per_seq: int, budget: int):
         n = kvx_evict_workspace_size(self.c, num_seqs, blocks_per_seq, budget)
@@ -628,15 +639,13 @@ class Cache:
         _need(blocks.dim() == 2 and dst_blocks.dim() == 2 and kept.dim() == 3, "evict: blocks and dst_blocks are "
               "[num_seqs, pages], kept is [num_seqs, heads, budget]")
         (N, per), dper, heads, budget, stride = blocks.shape, dst_blocks.shape[1], self.heads, kept.shape[2], scores.shape[-1]
-        _table(blocks, "blocks", _IDS, (N, per))
-        _table(lens, "lens", _IDS, (N,))
-        _table(scores, "scores", _FLOAT, (N, heads, stride))
-        _table(dst_blocks, "dst_blocks", _IDS, (N, dper))
-        _table(kept, "kept", _IDS, (N, heads, budget))
-        _table(kept_scores, "kept_scores", _FLOAT, (N, heads, budget))
-        _table(new_lens, "new_lens", _IDS, (N,))
-        kvx_evict(self.c, N, blocks, per, lens, scores, stride, budget, sinks, recent, dst_blocks, dper, kept, kept_scores,
-                  new_lens, self.status, ws, stream)
+        _check(lib().kvx_evict(self._ref, N, _table(blocks, "blocks", _IDS, (N, per)), per, _table(lens, "lens", _IDS, (N,)),
+                               _table(scores, "scores", _FLOAT, (N, heads, stride)), stride, budget, sinks, recent,
+                               _table(dst_blocks, "dst_blocks", _IDS, (N, dper)), dper,
+                               _table(kept, "kept", _IDS, (N, heads, budget)),
+                               _table(kept_scores, "kept_scores", _FLOAT, (N, heads, budget)),
+                               _table(new_lens, "new_lens", _IDS, (N,)), self._status, ws.data_ptr(), ws.numel(),
+                               _stream(stream)), "kvx_evict")
 
     def read_status(self) -> int:
         return int(_u32_np(self.status)[0])
