@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kScoreThreads) k_scores(const __grid_constant_
 #pragma unroll
     for (int u = 0; u < 4; u++) {
         const uint32_t i = i0 + u * kScoreThreads;
-        old[u] = i < sv.n ? to[i < sv.sinks ? i : i + sv.shift] : 0;
+        old[u] = i < sv.n ? to[sv.token(i)] : 0;
     }
     for (uint32_t k = 0; k < a.group; k += 2) {
         const float l0 = sh_lse[k], l1 = k + 1 < a.group ? sh_lse[k + 1] : INFINITY;
@@ -143,12 +143,13 @@ __global__ void __launch_bounds__(kScoreThreads) k_scores(const __grid_constant_
 #pragma unroll
     for (int u = 0; u < 4; u++) {
         const uint32_t i = i0 + u * kScoreThreads;
-        if (i < sv.n) to[i < sv.sinks ? i : i + sv.shift] = old[u] + w[u];
+        const uint32_t pos = sv.token(i);
+        if (i < sv.n && (pos < sv.sinks || pos >= sv.recent)) to[pos] = old[u] + w[u];
     }
 }
 
 struct Plan {
-    uint32_t dp, nt, unit_heads, units, max_len, tile, chunks;
+    uint32_t dp, nt, unit_heads, units, max_len, tile, chunks, align;
     uint64_t max_seen, parts;  // parts: blocks that the workspace has room for
     bool split;
     size_t part_o, part_ml, cut, lse2, logits;  // elements
@@ -169,7 +170,9 @@ bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t bloc
     p.nt = group > 8 && p.dp < 256 ? 2 : 1;
     p.unit_heads = 8 * p.nt;
     p.units = c->heads * (uint32_t)ceil_div(group, p.unit_heads);
-    p.max_seen = !window ? max_len : (uint64_t)window + sinks < max_len ? (uint64_t)window + sinks : max_len;
+    p.align = c->page_tokens % 16 ? 1 : 16;
+    const uint64_t shown = (uint64_t)window + sinks + 2 * (p.align - 1);  // with what alignment adds
+    p.max_seen = window && shown < max_len ? shown : max_len;
     // Up to kWhole keys a unit is left to one block: splitting it would save
     // less than the second launch costs.
     p.tile = p.max_seen <= kWhole ? kWhole : kStep;
@@ -233,7 +236,7 @@ extern "C" kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t
     a.logits_keys = p.max_seen;
     a.scale2 = scale * cache->k_scale * 1.4426950408889634f;
     a.num_seqs = num_seqs, a.q_heads = q_heads, a.group = q_heads / cache->heads, a.units = p.units;
-    a.blocks_per_seq = blocks_per_seq, a.max_len = p.max_len, a.window = window, a.sinks = sinks, a.tile = p.tile;
+    a.blocks_per_seq = blocks_per_seq, a.max_len = p.max_len, a.window = window, a.sinks = sinks, a.tile = p.tile, a.align = p.align;
     const cudaStream_t s = as_stream(stream);
     const uint32_t es = elem_size(cache->dtype);
     const bool ok = dtype == KVX_BF16

@@ -41,20 +41,26 @@ struct Args {
     uint32_t blocks_per_seq, max_len, window, sinks;
     uint32_t tile;     // keys of a tile, in which work is shared out
     uint32_t grid;     // blocks
+    uint32_t align;    // 16 where pages are whole tiles of 16 tokens, else 1
 };
 
-// Visible tokens of a sequence: logical index i is token i below `sinks`, and
-// token i + shift from there on.
+// The tokens of a sequence that are looked at: logical index i is token i below
+// `turn`, and token i + shift from there on.  With align == 16 both are
+// multiples of 16, so that 16 indices from a multiple of 16 on are tokens of
+// one page; tokens from `sinks` to `recent`-1 may then be among them, unseen.
 struct Seen {
-    uint32_t n, sinks, shift;
+    uint32_t n, turn, shift, sinks, recent;
+    __device__ __forceinline__ uint32_t token(uint32_t i) const { return i < turn ? i : i + shift; }
 };
 
 __device__ __forceinline__ Seen seen(const Args &a, uint32_t len) {
     Seen v;
     if (len > a.max_len) len = a.max_len;
     v.sinks = a.sinks < len ? a.sinks : len;
-    v.shift = 0;
-    if (a.window && len - v.sinks > a.window) v.shift = len - a.window - v.sinks;
+    v.recent = a.window && len - v.sinks > a.window ? len - a.window : v.sinks;
+    v.turn = (v.sinks + a.align - 1) & ~(a.align - 1);
+    const uint32_t from = v.recent & ~(a.align - 1);
+    v.shift = v.turn < from ? from - v.turn : 0;
     v.n = len - v.shift;
     return v;
 }
@@ -131,14 +137,14 @@ struct Shape {
     static constexpr int kVElems = kVBytes / ES;
     static constexpr int kQVecs = kKChunks * (ES == 1 ? 2 : 1);           // 16-byte vectors of q per lane
     static constexpr int kStage = 2 * 16 * DP * ES;                       // bytes of a warp's 16 keys, K and V
-    // Blocks an SM has registers for, and stages that as many rings have room for.
+    // Blocks that an SM has registers for.  Two stages a warp: with three to six
+    // the copies in flight got in each other's way (16 query heads to a KV head,
+    // 128 values: 104 us where two stages take 94; 8-bit, 8 heads: 98 and 93).
     static constexpr int kBlocks = DP == 256 ? (ES == 1 ? 2 : 1) : NT == 2 && DP == 128 ? 2 : 3;
-    static constexpr int kFit = 196608 / kBlocks / (kStage * kWarps);
-    static constexpr int kStages = kFit > 6 ? 6 : kFit;
-    static_assert(kStages >= 2, "");
+    static constexpr int kStages = 2;
     // What a unit costs beside its keys (its query, its output) counts as so
-    // many tiles when work is shared out: about 32 KB of copies.
-    static constexpr uint32_t kExtra = DP * ES >= 256 ? 1 : 256 / (DP * ES);
+    // many tiles when work is shared out: about 64 KB of copies.
+    static constexpr uint32_t kExtra = DP * ES >= 512 ? 1 : 512 / (DP * ES);
     static constexpr int kRing = kWarps * kStages * kStage;
     static constexpr int kQ = NT * kQVecs * 32 * 16;
     static constexpr int kJoin = (DP / 16 + 1) * NT * 32 * 16;
@@ -159,7 +165,7 @@ struct Piece {
     uint32_t nheads;
     uint32_t k0, k1;  // visible keys, by logical index
     uint32_t slot;    // of the partial result; kNone: the piece is the whole unit
-    uint32_t pad;
+    uint32_t turn, shift, sinks, recent;  // of the sequence's Seen
 };
 
 __device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
@@ -197,10 +203,10 @@ __device__ __forceinline__ void load_early(uint64_t &v, const uint64_t *p, bool 
 // without a pause: the block ids of one step are loaded while the segment
 // addresses of the step before are, and the rows of the one before that are
 // handed to the warps.
-template <class T, int DP, int ES, int NT>
+template <class T, int DP, int ES, int NT, bool PAGED16>
 __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t per, uint32_t lane,
-                                        uint4 *qbuf, const uint64_t *upto, uint64_t (*rows)[32], uint64_t *ready,
-                                        uint64_t *taken, uint64_t *pfull, uint64_t *pempty, Piece *pieces,
+                                        uint4 *qbuf, const uint64_t *upto, uint64_t (*rows)[32], uint64_t (*ready)[2],
+                                        uint64_t (*taken)[2], uint64_t *pfull, uint64_t *pempty, Piece *pieces,
                                         uint32_t &bad) {
     using S = Shape<DP, ES, NT>;
     const uint32_t g = lane >> 2, t4 = lane & 3;
@@ -272,7 +278,7 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
             if (lane == 0) {
                 const uint32_t qh0 = unit % units_per_head * S::kHeads;
                 const uint32_t nheads = a.group - qh0 < S::kHeads ? a.group - qh0 : S::kHeads;
-                pieces[np % kPieces] = Piece{n, head, qh0, nheads, k, k1, whole ? kNone : slot, 0};
+                pieces[np % kPieces] = Piece{n,  head, qh0, nheads, k, k1, whole ? kNone : slot, sv.turn, sv.shift, sv.sinks, sv.recent};
             }
             np++;
             __syncwarp();
@@ -284,39 +290,50 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
     // Three steps on their way: the block ids of one are loaded, the table
     // entries of the one before brought into L2, the segment addresses of the
     // one before that loaded.  Loaded registers are used up where they are (a
-    // copy of one would wait for it).  A lane has the step's keys `lane` and
-    // `lane` + 32.
+    // copy of one would wait for it).
+    //   PAGED16: 16 tiles of 16 keys; lane 2*i + kv has tile i's K or V segment.
+    //   Otherwise 4 tiles; a lane has both segments of keys `lane` and `lane` + 32.
+    constexpr int kKeys = PAGED16 ? 1 : 2, kSegs = PAGED16 ? 1 : 2;
+    constexpr uint32_t kReach = PAGED16 ? 16 * 16 : kStep;  // keys of a step
     struct Step {
-        uint32_t place[2], valid;      // place in the page; a bit per key: its block exists
+        uint32_t place[kKeys], valid;  // place in the page; a bit per key: its block exists
+        uint32_t mask, left;           // PAGED16: rows of the tile that are seen; a bit per tile with keys
         uint32_t table, piece, warps;  // lane of the address table; warps with keys, 0 at the end
         bool fresh;                    // the piece's first step
     };
-    uint32_t ids[2] = {};
-    const uint64_t *entry[2];
-    uint64_t segs[2][2] = {};  // of K and V
+    uint32_t ids[kKeys] = {};
+    const uint64_t *entry[kKeys];
+    uint64_t segs[kKeys][kSegs] = {};
     auto find_blocks = [&]() -> Step {
         Step s = {};
         if (k >= k1 && !next_piece()) return s;
         s.warps = k1 - k < kStep ? (k1 - k + 15) / 16 : kWarps;
         s.piece = np - 1;
         s.fresh = fresh;
-        s.table = a.c.first_lane + 2 * head;
+        s.table = a.c.first_lane + 2 * head + (PAGED16 ? lane & 1 : 0);
         const uint32_t *seq_blocks = a.blocks + (uint64_t)n * a.blocks_per_seq;
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-            const uint32_t i = k + u * 32 + lane;
-            const uint32_t pos = i < sv.sinks ? i : i + sv.shift, page = a.c.page.div(pos);
+        for (int u = 0; u < kKeys; u++) {
+            const uint32_t i = k + (PAGED16 ? lane / 2 * 16 : u * 32 + lane);
+            const uint32_t pos = sv.token(i), page = a.c.page.div(pos);
             s.place[u] = pos - page * a.c.page.d;
             s.valid |= (uint32_t)(i < k1) << u;
             load_early(ids[u], seq_blocks + page, i < k1);
+            if constexpr (PAGED16) {
+                auto bits = [](uint32_t count) { return count < 16 ? (1u << count) - 1 : 0xFFFFu; };
+                s.mask = bits(i < k1 ? k1 - i : 0);
+                if (sv.recent > sv.sinks)
+                    s.mask &= ~bits(sv.recent > pos ? sv.recent - pos : 0) | bits(sv.sinks > pos ? sv.sinks - pos : 0);
+            }
         }
+        s.left = k1 - k < kReach ? (1u << (k1 - k + 15) / 16) - 1 : 0xFFFFu;
         fresh = false;
-        k = k1 - k < kStep ? k1 : k + kStep;
+        k = k1 - k < kReach ? k1 : k + kReach;
         return s;
     };
     auto find_entries = [&](Step &s) {
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
+        for (int u = 0; u < kKeys; u++) {
             const uint32_t id = ids[u], there = s.valid >> u & 1, known = id < a.c.B;
             entry[u] = a.c.addr + (there & known ? (uint64_t)id * a.c.L + s.table : 0);
             bad |= there & ~known ? KVX_S_BOUNDS : 0;
@@ -326,21 +343,21 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
     };
     auto find_addrs = [&](const Step &s) {
 #pragma unroll
-        for (int u = 0; u < 2; u++)
+        for (int u = 0; u < kKeys; u++)
 #pragma unroll
-            for (int kv = 0; kv < 2; kv++) load_early(segs[u][kv], entry[u] + kv, s.valid >> u & 1);
+            for (int kv = 0; kv < kSegs; kv++) load_early(segs[u][kv], entry[u] + kv, s.valid >> u & 1);
     };
 
     const uint64_t no_row = reinterpret_cast<uint64_t>(a.c.pool) | 1;
     const uint64_t room = a.c.pool_bytes - a.c.span;  // a segment's largest offset, where any fits
     const bool fits = a.c.pool_bytes >= a.c.span;
     const uint32_t stride = (uint32_t)a.c.token_stride;
-    uint32_t handed = 0;  // tiles handed to warp lane%4 so far
+    uint32_t handed = 0;  // hand-overs to warp lane%4 so far
     auto announce = [&](uint32_t p) {
         mbar_arrive_copies(&pfull[p % kPieces]);
         if (lane == 0) mbar_arrive(&pfull[p % kPieces]);
     };
-    auto issue = [&](const Step &s, const uint64_t (&row)[2][2]) {
+    auto issue = [&](const Step &s, const uint64_t (&row)[kKeys][kSegs]) {
         if (s.fresh) {  // the piece's query heads, as the second operand's lanes hold them
             const uint32_t p = s.piece;
             const uint32_t q_of = p - S::kQBufs;  // the piece whose query was there before
@@ -363,22 +380,32 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
                 }
             announce(p);
         }
-        const uint32_t w = lane % kWarps;
+        // one buffer of rows a warp, or two of up to four tiles each
+        const uint32_t w = lane % kWarps, buffer = PAGED16 ? handed & 1 : 0;
+        const uint32_t turn = PAGED16 ? handed >> 1 : handed;
         const bool mine = w < s.warps;
-        const bool free = !mine || !handed || mbar_wait(&taken[w], (handed & 1) ^ 1);
+        const bool free = !mine || !turn || mbar_wait(&taken[w][buffer], (turn & 1) ^ 1);
         if (!__all_sync(0xFFFFFFFFu, free)) {
             alive = false;
             return;
         }
         handed += mine;
+        if constexpr (PAGED16) {
+            const uint32_t i = lane / 2, to = __shfl_sync(0xFFFFFFFFu, buffer, i % kWarps);
+            const bool last = i / kWarps == 3 || !(s.left >> (i + kWarps) & 1);
+            if (s.left >> i & 1)
+                reinterpret_cast<uint4 *>(rows[i % kWarps])[(to * 4 + i / kWarps) * 2 + (lane & 1)] =
+                    make_uint4((uint32_t)row[0][0], (uint32_t)(row[0][0] >> 32), row[0][0] & 1 ? 0 : s.mask, last);
+        } else {
 #pragma unroll
-        for (int u = 0; u < 2; u++) {
-            if (2 * u + lane / 16 >= s.warps) continue;
-            rows[2 * u + lane / 16][lane % 16] = row[u][0];
-            rows[2 * u + lane / 16][16 + lane % 16] = row[u][1];
+            for (int u = 0; u < kKeys; u++) {
+                if (2 * u + lane / 16 >= s.warps) continue;
+                rows[2 * u + lane / 16][lane % 16] = row[u][0];
+                rows[2 * u + lane / 16][16 + lane % 16] = row[u][kSegs - 1];
+            }
         }
         __syncwarp();
-        if (lane < s.warps) mbar_arrive(&ready[lane]);
+        if (lane < s.warps) mbar_arrive(&ready[lane][buffer]);
     };
 
     // (find_blocks() is not asked again after it has said that there is no more)
@@ -389,11 +416,11 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
     find_entries(held);
     if (held.warps) next = find_blocks();
     while (alive && now.warps) {
-        uint64_t row[2][2];
+        uint64_t row[kKeys][kSegs];
 #pragma unroll
-        for (int u = 0; u < 2; u++)
+        for (int u = 0; u < kKeys; u++)
 #pragma unroll
-            for (int kv = 0; kv < 2; kv++) {
+            for (int kv = 0; kv < kSegs; kv++) {
                 const uint64_t seg = segs[u][kv];
                 const bool there = now.valid >> u & 1, good = fits && seg <= room && !((uint32_t)seg & 15);
                 row[u][kv] = no_row;
@@ -439,7 +466,7 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
 // suffices: with 16 columns in use the SMs need well under a fifth of its
 // rate to consume the measured bandwidth, and operands come to registers
 // without a transposition through shared memory that a larger tile would need.
-template <class T, int DP, int ES, int NT>
+template <class T, int DP, int ES, int NT, bool PAGED16>
 __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_attend(const __grid_constant__ Args a) {
     using S = Shape<DP, ES, NT>;
     // the type in which the products are taken: 8-bit values are exact in fp16
@@ -448,8 +475,12 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t sh_sum[kWarps + 1], sh_upto[32];
     __shared__ uint64_t full[kWarps][S::kStages];   // a warp's tiles
-    __shared__ __align__(16) uint64_t rows[kWarps][32];  // and its next one's rows: addresses of 16 of K and 16 of V
-    __shared__ uint64_t ready[kWarps], taken[kWarps];
+    // Where its next ones' rows are.  PAGED16: two buffers of four tiles, for
+    // each the first row's address, which rows are seen, and whether the tile
+    // is the buffer's last, for K and for V.  Otherwise one tile: addresses of
+    // its 16 rows of K and of V, with bit 0 set where there is none.
+    __shared__ __align__(16) uint64_t rows[kWarps][32];
+    __shared__ uint64_t ready[kWarps][2], taken[kWarps][2];
     __shared__ uint64_t pfull[kPieces], pempty[kPieces];                      // pieces
     __shared__ uint64_t passed[kWarps], joined, converted[2];
     __shared__ Piece pieces[kPieces];
@@ -480,8 +511,10 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
     } else if (lane == 0) {
         for (int w = 0; w < kWarps; w++) {
             for (int i = 0; i < S::kStages; i++) mbar_init(&full[w][i], 32);
-            mbar_init(&ready[w], 1);
-            mbar_init(&taken[w], 1);
+            for (int i = 0; i < 2; i++) {
+                mbar_init(&ready[w][i], 1);
+                mbar_init(&taken[w][i], 1);
+            }
             mbar_init(&passed[w], 1);
         }
         for (int i = 0; i < kPieces; i++) {
@@ -502,7 +535,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
     }
 
     if (warp == kWarps) {
-        look_up<T, DP, ES, NT>(a, sh_upto[31] * a.units, per, lane, qbuf, sh_upto, rows, ready, taken, pfull, pempty,
+        look_up<T, DP, ES, NT, PAGED16>(a, sh_upto[31] * a.units, per, lane, qbuf, sh_upto, rows, ready, taken, pfull, pempty,
                                pieces, bad);
         raise(a.status, bad);
         return;
@@ -511,38 +544,73 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
 
     // ---- a computing warp: one piece after the other
     uint8_t *ring = smem + warp * (S::kStages * S::kStage);
-    uint32_t copied = 0;  // tiles whose copies this warp has issued: up to kStages ahead, of later pieces too
+    uint32_t copied = 0;   // tiles whose copies this warp has issued: up to kStages ahead, of later pieces too
+    uint32_t buffers = 0, in_buffer = 0;  // buffers of rows used up, tiles of the present one taken
     const bool cover = a.c.row_bytes == DP * ES;
+    const uint32_t stride = (uint32_t)a.c.token_stride;
     // Takes the next tile's rows and copies this lane's pieces of them: where a
     // row or a piece does not exist, zeros (a copy of no bytes reads nothing).
     auto copy_tile = [&]() {
-        const uint64_t *from = rows[warp];
-        const ulonglong2 v0 = *reinterpret_cast<const ulonglong2 *>(from + 16 + 2 * t4);
-        const ulonglong2 v1 = *reinterpret_cast<const ulonglong2 *>(from + 24 + 2 * t4);
-        const uint64_t row[6] = {from[g], from[g + 8], v0.x, v0.y, v1.x, v1.y};
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&taken[warp]);
+        const uint8_t *row[6];
+        uint32_t there[6];
+        bool done = true;
+        if constexpr (PAGED16) {
+            const uint4 *from = reinterpret_cast<const uint4 *>(rows[warp]) + ((buffers & 1) * 4 + in_buffer) * 2;
+            const uint4 kr = from[0], vr = from[1];
+            const uint8_t *kp = reinterpret_cast<const uint8_t *>(((uint64_t)kr.y << 32 | kr.x) & ~1ull);
+            const uint8_t *vp = reinterpret_cast<const uint8_t *>(((uint64_t)vr.y << 32 | vr.x) & ~1ull);
+            row[0] = kp + (uint64_t)g * stride;
+            row[1] = row[0] + 8ull * stride;
+            row[2] = vp + 2ull * t4 * stride;
+            row[3] = row[2] + stride;
+            row[4] = row[2] + 8ull * stride;
+            row[5] = row[3] + 8ull * stride;
+#pragma unroll
+            for (int r = 0; r < 6; r++)
+                there[r] = r < 2 ? kr.z >> (g + 8 * r) & 1 : vr.z >> (2 * t4 + (r & 1) + 8 * ((r - 2) >> 1)) & 1;
+            done = kr.w;
+        } else {
+            const uint64_t *from = rows[warp];
+            const ulonglong2 v0 = *reinterpret_cast<const ulonglong2 *>(from + 16 + 2 * t4);
+            const ulonglong2 v1 = *reinterpret_cast<const ulonglong2 *>(from + 24 + 2 * t4);
+            const uint64_t at[6] = {from[g], from[g + 8], v0.x, v0.y, v1.x, v1.y};
+#pragma unroll
+            for (int r = 0; r < 6; r++) {
+                row[r] = reinterpret_cast<const uint8_t *>(at[r] & ~1ull);
+                there[r] = ~(uint32_t)at[r] & 1;
+            }
+        }
+        in_buffer++;
+        if (done) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&taken[warp][PAGED16 ? buffers & 1 : 0]);
+            buffers++;
+            in_buffer = 0;
+        }
         const uint32_t stage = copied % S::kStages;
         uint8_t *st = ring + stage * S::kStage;
         const uint32_t kdst = smem_u32(st + lane * 16), vdst = smem_u32(st + S::kStage / 2 + vslot);
 #pragma unroll
         for (int r = 0; r < 6; r++) {
-            const uint32_t bytes = row[r] & 1 ? 0 : r < 2 ? 16 : S::kVBytes;
-            const uint8_t *p = reinterpret_cast<const uint8_t *>(row[r] & ~1ull) + (r < 2 ? t4 * 16 : g * S::kVBytes);
             if (r < 2) {
 #pragma unroll
                 for (int c = 0; c < S::kKChunks; c++)
-                    copy_async<16>(kdst + (c * 2 + r) * 512, p + c * 64,
-                                   cover || c * 64 + t4 * 16 < a.c.row_bytes ? bytes : 0);
+                    copy_async<16>(kdst + (c * 2 + r) * 512, row[r] + t4 * 16 + c * 64,
+                                   there[r] && (cover || c * 64 + t4 * 16 < a.c.row_bytes) ? 16 : 0);
             } else {
 #pragma unroll
                 for (int c = 0; c < S::kVParts; c++)
-                    copy_async<S::kVBytes>(vdst + (c * 4 + r - 2) * 32 * S::kVBytes, p + c * 8 * S::kVBytes,
-                                           cover || (c * 8 + g) * S::kVBytes < a.c.row_bytes ? bytes : 0);
+                    copy_async<S::kVBytes>(vdst + (c * 4 + r - 2) * 32 * S::kVBytes, row[r] + (c * 8 + g) * S::kVBytes,
+                                           there[r] && (cover || (c * 8 + g) * S::kVBytes < a.c.row_bytes) ? S::kVBytes : 0);
             }
         }
         mbar_arrive_copies(&full[warp][stage]);
         copied++;
+    };
+    // Whether the next tile's rows are there; the barrier is asked once a buffer.
+    auto rows_there = [&]() {
+        const uint32_t parity = (PAGED16 ? buffers >> 1 : buffers) & 1;
+        return in_buffer || __all_sync(0xFFFFFFFFu, mbar_test(&ready[warp][PAGED16 ? buffers & 1 : 0], parity));
     };
     float4 *join = reinterpret_cast<float4 *>(smem + S::kRing + S::kQBufs * S::kQ) + lane;
     uint32_t tile = 0, joins = 0, passes = 0;  // tiles taken, pieces joined, and results taken over so far
@@ -623,13 +691,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
         bool ok = true;
         for (uint32_t k = pc.k0 + warp * 16; k < pc.k1; k += kStep, tile++) {
             if (copied == tile) {
-                if (!mbar_wait(&ready[warp], copied & 1)) {
+                const uint32_t parity = (PAGED16 ? buffers >> 1 : buffers) & 1;
+                if (!in_buffer && !mbar_wait(&ready[warp][PAGED16 ? buffers & 1 : 0], parity)) {
                     ok = false;
                     break;
                 }
                 copy_tile();
             }
-            while (copied < tile + S::kStages && __all_sync(0xFFFFFFFFu, mbar_test(&ready[warp], copied & 1))) copy_tile();
+            while (copied < tile + S::kStages && rows_there()) copy_tile();
             const uint32_t stage = tile % S::kStages;
             if (!mbar_wait(&full[warp][stage], tile / S::kStages & 1)) {
                 ok = false;
@@ -666,13 +735,19 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
 
             // logits in powers of two, masked beyond the last key
             const uint32_t i0 = k + g, i1 = i0 + 8;
+            bool hide0 = i0 >= pc.k1, hide1 = i1 >= pc.k1;
+            if (PAGED16 && a.window) {
+                const uint32_t p0 = i0 < pc.turn ? i0 : i0 + pc.shift, p1 = p0 + 8;  // in one page
+                hide0 |= p0 >= pc.sinks && p0 < pc.recent;
+                hide1 |= p1 >= pc.sinks && p1 < pc.recent;
+            }
             bool higher = false;
 #pragma unroll
             for (int x = 0; x < NT; x++) {
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
                     s[x][i] = (s[x][i] + s2[x][i]) * scale2[x][i & 1];
-                    if ((i < 2 ? i0 : i1) >= pc.k1) s[x][i] = -INFINITY;
+                    if (i < 2 ? hide0 : hide1) s[x][i] = -INFINITY;
                     higher |= s[x][i] > limit[x][i & 1];
                 }
                 if (logits && x * 8 + 2 * t4 < pc.nheads) {
@@ -878,15 +953,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
 
 // Launches one variant over at most `most` blocks and leaves their number in
 // a.grid; false where that failed.
-template <class T, int DP, int ES, int NT>
-bool launch_one(Args &a, uint64_t most, cudaStream_t s) {
+template <class T, int DP, int ES, int NT, bool PAGED16>
+bool launch_kernel(Args &a, uint64_t most, cudaStream_t s) {
     using S = Shape<DP, ES, NT>;
     static bool done[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
     if (dev < 0 || dev >= 64 || !done[dev]) {
-        if (cudaFuncSetAttribute(k_attend<T, DP, ES, NT>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) !=
-            cudaSuccess)
+        if (cudaFuncSetAttribute(k_attend<T, DP, ES, NT, PAGED16>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 S::kSmem) != cudaSuccess)
             return false;
         if (dev >= 0 && dev < 64) done[dev] = true;
     }
@@ -894,8 +969,13 @@ bool launch_one(Args &a, uint64_t most, cudaStream_t s) {
     if (room > kMaxBlocks) room = kMaxBlocks;
     a.grid = (uint32_t)(most < room ? most : room);
     if (!a.grid) a.grid = 1;  // nothing to see anywhere: the zeros still have to be written
-    k_attend<T, DP, ES, NT><<<a.grid, kThreads, S::kSmem, s>>>(a);
+    k_attend<T, DP, ES, NT, PAGED16><<<a.grid, kThreads, S::kSmem, s>>>(a);
     return true;
+}
+
+template <class T, int DP, int ES, int NT>
+bool launch_one(Args &a, uint64_t most, cudaStream_t s) {
+    return a.align == 16 ? launch_kernel<T, DP, ES, NT, true>(a, most, s) : launch_kernel<T, DP, ES, NT, false>(a, most, s);
 }
 
 template <class T, int ES>
