@@ -146,6 +146,11 @@ struct Shape {
     // many tiles when work is shared out: about 64 KB of copies.
     static constexpr uint32_t kExtra = DP * ES >= 512 ? 1 : 512 / (DP * ES);
     static constexpr int kRing = kWarps * kStages * kStage;
+    // Where the rings of an SM hold more than 160 KB (16-bit, 128 values, three
+    // blocks) the next tile's copies go out when the present one's have
+    // arrived: 86 us against 88 at once (16,000 tokens x 8 heads x 8
+    // sequences); smaller rings want both on their way (8-bit: 92 us and 96).
+    static constexpr bool kLate = kRing * kBlocks > 160 * 1024;
     static constexpr int kQ = NT * kQVecs * 32 * 16;
     static constexpr int kJoin = (DP / 16 + 1) * NT * 32 * 16;
     static constexpr int kQBufs = kBlocks == 3 ? 2 : 1;
@@ -698,12 +703,15 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
                 }
                 copy_tile();
             }
-            while (copied < tile + S::kStages && rows_there()) copy_tile();
+            if (!S::kLate)
+                while (copied < tile + S::kStages && rows_there()) copy_tile();
             const uint32_t stage = tile % S::kStages;
             if (!mbar_wait(&full[warp][stage], tile / S::kStages & 1)) {
                 ok = false;
                 break;
             }
+            if (S::kLate)
+                while (copied < tile + S::kStages && rows_there()) copy_tile();
             const uint8_t *st = ring + stage * S::kStage;
 
             // S^T = K Q^T
