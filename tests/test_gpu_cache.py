@@ -520,3 +520,18 @@ def test_evict_bad_pages():
                     dst.cuda(), kept, ksc, nl, cache.evict_workspace(1, 4, 30), sinks=24)  # keeps 0-23 and the last six
         torch.cuda.synchronize()
         assert cache.read_status() == bit, fault
+
+
+# ------------------------------------------------------------------ together
+
+def test_decoding_on_a_transferred_prefix():
+    """The example: transfer, append, attend, evict and attend again; its last attention is off by at most half a step of
+    bf16 in values below 2 (256 random values averaged), and the steps of 32-bit sums."""
+    import importlib.util
+    import os
+
+    from conftest import ROOT
+    spec = importlib.util.spec_from_file_location("example", os.path.join(ROOT, "examples", "decode_received_prefix.py"))
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    assert example.main(verbose=False) <= 2 * 2 ** -8 + 2 ** -12
