@@ -64,7 +64,10 @@
  *     or asserts.  Thread blocks wait on one another only at the grid
  *     barriers of cooperative launches (encode, verify-encode, plan), each
  *     bounded by one second of wall time, after which the kernel ORs
- *     KVX_S_TIMEOUT and returns: bad input cannot hang or fault the GPU;
+ *     KVX_S_TIMEOUT and returns, and at the hardware barrier of a cluster
+ *     (kvx_evict), whose blocks are always resident together; waits within a
+ *     block for copies (copies, kvx_attend) are bounded likewise: bad input
+ *     cannot hang or fault the GPU;
  *     every global access is checked against the capacities passed in.
  *   - Co-scheduling: the grid of a cooperative launch is sized to fit on
  *     the device, but while other kernels occupy SMs (the library's own
@@ -646,8 +649,9 @@ size_t kvx_attend_workspace_size(const kvx_cache *cache, uint32_t num_seqs,
  *                  added to element j of every visible token, in a fixed
  *                  order.  scores_stride >= blocks_per_seq * page_tokens.
  * Results depend on nothing but the arguments and the device's SM count: no
- * atomics.  One launch, or two where a sequence may be split or scores are
- * added; num_seqs == 0 enqueues nothing.
+ * atomics.  One launch, another where blocks_per_seq and the window let a
+ * sequence show more than 256 tokens (it may be split over blocks and is then
+ * joined), another where scores are added; num_seqs == 0 enqueues nothing.
  */
 kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t q_stride,
                       uint32_t dtype, uint32_t num_seqs, uint32_t q_heads,
@@ -658,7 +662,8 @@ kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t q_stride,
                       uint32_t *status, void *ws, size_t ws_bytes,
                       void *stream);
 
-/* Scratch of kvx_evict; 0 for arguments it refuses. */
+/* Scratch of kvx_evict; 0 for arguments it refuses.  (The present kernels keep
+ * what they need in shared memory: it is a small constant.) */
 size_t kvx_evict_workspace_size(const kvx_cache *cache, uint32_t num_seqs,
                                 uint32_t blocks_per_seq, uint32_t budget);
 

@@ -1,23 +1,29 @@
 // kvx_evict: sequences cut to a budget of tokens per KV head, by the attention
 // weight that each token has gathered.
 //
-// k_select, a block per (sequence, head), finds the M-th largest score among
-// the tokens that have to compete with a radix select over order-preserving
-// 32-bit keys (digits of 11, 11 and 10 bits from the top: a histogram of the
-// scores that share the digits found so far, then the digit in which the M-th
-// lies), so the threshold is exact and nothing is sorted.  What is over it, the
-// first of its equals, the sinks and the last tokens are then written in order:
-// each warp counts its own stretch, a scan over the warps gives their places.
-// k_gather copies the kept rows.
+// k_select, a block per (sequence, head) or a cluster of up to eight, finds the
+// M-th largest score among the tokens that have to compete with a radix select
+// over order-preserving 32-bit keys (digits of 11, 11 and 10 bits from the top:
+// a histogram of the scores that share the digits found so far, then the digit
+// in which the M-th lies), so the threshold is exact and nothing is sorted.
+// Each block keeps its part of the keys in shared memory, so the scores are
+// read once; the blocks of a cluster add up each other's histograms through
+// distributed shared memory.  What is over the threshold, the first of its
+// equals, the sinks and the last tokens are then written in order: each warp
+// counts its own stretch, sums over the warps and blocks before it give its
+// places.  Bound by the latency of these steps and, with many heads, by their
+// instructions.  k_gather copies the kept rows, at the rate of a plain copy.
 #include "kvx_cache.cuh"
 
 namespace kvx {
 namespace {
 
-constexpr int kSelThreads = 1024;
-constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kBins = 2048;
-constexpr uint32_t kHeld = 51200;  // keys that a block keeps in shared memory
+constexpr uint32_t kHeld = 49152;  // keys that a block keeps in shared memory
+constexpr uint32_t kMaxCluster = 8;
+constexpr uint32_t kShare = 2048;  // tokens for which a block of a cluster pays
+constexpr uint32_t kShort = 16384; // tokens up to which a smaller block is faster
+constexpr int kDigits = 3;
 constexpr int kSelUnroll = 8;
 // Keys that no score has: a token that is not there, and one that stays in any case.
 constexpr uint32_t kAbsent = 0, kStays = 0xFFFFFFFFu;
@@ -44,33 +50,77 @@ __device__ __forceinline__ uint32_t key_of(float f) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
+__device__ __forceinline__ uint32_t cluster_rank() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ uint32_t cluster_size() {
+    uint32_t r;
+    asm("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+    return r;
+}
+__device__ __forceinline__ void cluster_arrive() {
+    __syncwarp();  // the whole warp together, whatever came before
+    asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+    __syncwarp();
+    asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Two words of another block's shared memory, at the place that p has in this one's.
+__device__ __forceinline__ uint2 ld_peer(const uint32_t *p, uint32_t rank) {
+    uint2 v;
+    asm volatile(
+        "{\n\t.reg .u32 a;\n\tmapa.shared::cluster.u32 a, %2, %3;\n\tld.shared::cluster.v2.u32 {%0, %1}, [a];\n\t}"
+        : "=r"(v.x), "=r"(v.y)
+        : "r"(smem_u32(p)), "r"(rank)
+        : "memory");
+    return v;
+}
+
+// Which part of a sequence a block has: tokens first .. first + n - 1.
+struct Part {
+    uint32_t first, n;
+    __device__ __forceinline__ Part(uint32_t len, uint32_t rank, uint32_t size) {
+        const uint32_t each = (len + 4 * size - 1) / (4 * size) * 4;  // whole groups of four keys
+        first = rank * each < len ? rank * each : len;
+        n = len - first < each ? len - first : each;
+    }
+};
+
+template <int kSelThreads, bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ EvictArgs a, uint32_t held) {
-    extern __shared__ __align__(16) uint32_t keys[];  // [held], of the first tokens; held is a multiple of four
-    __shared__ uint32_t hist[kBins];
+    constexpr int kSelWarps = kSelThreads / 32, kHists = CLUSTER ? kDigits : 1;
+    extern __shared__ __align__(16) uint32_t keys[];  // [held], of the part's first tokens; held is a multiple of four
+    __shared__ __align__(16) uint32_t hist[kHists][kBins];  // one a digit in a cluster: peers may still read the last one
     __shared__ uint32_t sh_scan[33];
     __shared__ uint32_t sh_digit, sh_left;
     __shared__ uint32_t sh_over[kSelWarps], sh_ties[kSelWarps];
+    __shared__ __align__(8) uint32_t sh_all[2];  // the block's counts
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t n = blockIdx.x / a.c.heads;
+    const uint32_t rank = CLUSTER ? cluster_rank() : 0, size = CLUSTER ? cluster_size() : 1;
+    const uint32_t row = blockIdx.x / size, n = row / a.c.heads;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     uint32_t len = a.lens[n];
     if (len > a.max_len) {
         if (threadIdx.x == 0) raise(a.status, KVX_S_BOUNDS);
         len = a.max_len;
     }
-    const float *x = a.scores + blockIdx.x * a.scores_stride;
-    uint32_t *kept = a.kept + (uint64_t)blockIdx.x * a.budget;
-    float *ks = a.kept_scores + (uint64_t)blockIdx.x * a.budget;
+    const Part part(len, rank, size);
+    const float *x = a.scores + row * a.scores_stride + part.first;  // the part's
+    uint32_t *kept = a.kept + (uint64_t)row * a.budget;
+    float *ks = a.kept_scores + (uint64_t)row * a.budget;
     const uint32_t keep = len < a.budget ? len : a.budget;
-    if (threadIdx.x == 0 && blockIdx.x % a.c.heads == 0) a.new_lens[n] = keep;
-    for (uint32_t i = keep + threadIdx.x; i < a.budget; i += kSelThreads) {
+    if (threadIdx.x == 0 && rank == 0 && row % a.c.heads == 0) a.new_lens[n] = keep;
+    for (uint32_t i = keep + rank * kSelThreads + threadIdx.x; i < a.budget; i += size * kSelThreads) {
         kept[i] = kNone;
         ks[i] = 0.0f;
     }
-    if (len <= a.budget) {
-        for (uint32_t i = threadIdx.x; i < len; i += kSelThreads) {
-            kept[i] = i;
-            ks[i] = x[i];
+    if (len <= a.budget) {  // the same for the whole cluster
+        for (uint32_t i = threadIdx.x; i < part.n; i += kSelThreads) {
+            kept[part.first + i] = part.first + i;
+            ks[part.first + i] = x[i];
         }
         return;
     }
@@ -79,30 +129,33 @@ __global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ 
     const uint32_t hi = len - recent;  // tokens lo .. hi-1 compete for `take` places
     const uint32_t take = a.budget - lo - recent;
 
-    auto make_key = [&](uint32_t i, float v) { return i >= lo && i < hi ? key_of(v) : kStays; };
-    // Keys of tokens i .. i+3, i a multiple of four.
+    auto make_key = [&](uint32_t i, float v) {
+        const uint32_t token = part.first + i;
+        return token >= lo && token < hi ? key_of(v) : kStays;
+    };
+    // Keys of the part's tokens i .. i+3, i a multiple of four.
     auto keys_at = [&](uint32_t i) -> uint4 {
         if (i < held) return *reinterpret_cast<const uint4 *>(keys + i);
         uint32_t k[4];
 #pragma unroll
-        for (int u = 0; u < 4; u++) k[u] = i + u < len ? make_key(i + u, __ldg(x + i + u)) : kAbsent;
+        for (int u = 0; u < 4; u++) k[u] = i + u < part.n ? make_key(i + u, __ldg(x + i + u)) : kAbsent;
         return make_uint4(k[0], k[1], k[2], k[3]);
     };
 
-    for (uint32_t i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
+    for (uint32_t i = threadIdx.x; i < kHists * kBins; i += kSelThreads) hist[i / kBins][i % kBins] = 0;
     __syncthreads();
-    const uint32_t padded = (len + 3) & ~3u;
+    const uint32_t padded = (part.n + 3) & ~3u;
     for (uint32_t i0 = threadIdx.x; i0 < padded; i0 += kSelUnroll * kSelThreads) {
         float v[kSelUnroll];
 #pragma unroll
-        for (int u = 0; u < kSelUnroll; u++) v[u] = i0 + u * kSelThreads < len ? __ldg(x + i0 + u * kSelThreads) : 0;
+        for (int u = 0; u < kSelUnroll; u++) v[u] = i0 + u * kSelThreads < part.n ? __ldg(x + i0 + u * kSelThreads) : 0;
 #pragma unroll
         for (int u = 0; u < kSelUnroll; u++) {
             const uint32_t i = i0 + u * kSelThreads;
             if (i >= padded) break;
-            const uint32_t k = i < len ? make_key(i, v[u]) : kAbsent;
+            const uint32_t k = i < part.n ? make_key(i, v[u]) : kAbsent;
             if (i < held) keys[i] = k;
-            if (k != kAbsent && k != kStays) atomicAdd(&hist[k >> 21], 1u);
+            if (k != kAbsent && k != kStays) atomicAdd(&hist[0][k >> 21], 1u);
         }
     }
     __syncthreads();
@@ -111,38 +164,52 @@ __global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ 
     uint32_t cut = take ? 0 : kStays - 1, left = take;
     if (take) {
 #pragma unroll 1
-        for (int pass = 0; pass < 3; pass++) {
+        for (int pass = 0; pass < kDigits; pass++) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
+            uint32_t *counts = hist[CLUSTER ? pass : 0];
             if (pass) {
+                if (!CLUSTER) {
+                    for (uint32_t i = threadIdx.x; i < kBins; i += kSelThreads) counts[i] = 0;
+                    __syncthreads();
+                }
                 const uint32_t bins = pass == 2 ? 1024 : 2048, known = pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
-                for (uint32_t i = threadIdx.x; i < kBins; i += kSelThreads) hist[i] = 0;
-                __syncthreads();
                 auto add = [&](uint32_t k) {  // (no cut begins like kStays)
-                    if ((k & known) == cut) atomicAdd(&hist[k >> shift & (bins - 1)], 1u);
+                    if ((k & known) == cut) atomicAdd(&counts[k >> shift & (bins - 1)], 1u);
                 };
 #pragma unroll 2
                 for (uint32_t i = 4 * threadIdx.x; i < padded; i += 4 * kSelThreads) {
                     const uint4 k = keys_at(i);
                     add(k.x), add(k.y), add(k.z), add(k.w);
                 }
+            }
+            if (CLUSTER) {
+                cluster_arrive();
+                cluster_wait();
+            } else {
                 __syncthreads();
             }
-            // some bins a thread, from the largest down
+            // some bins a thread, from the largest down, of all blocks
             constexpr int kPer = kBins / kSelThreads;
-            const uint32_t top = kBins - 1 - kPer * threadIdx.x;
-            uint32_t sum = 0, total;
+            const uint32_t bin = kBins - kPer * (threadIdx.x + 1);
+            uint32_t h[kPer] = {}, sum = 0;
 #pragma unroll
-            for (int i = 0; i < kPer; i++) sum += hist[top - i];
-            uint32_t above = block_excl_sum<uint32_t>(sum, sh_scan, &total);
-            if (above < left && above + sum >= left) {
-                for (uint32_t b = top;; b--) {
-                    const uint32_t h = hist[b];
-                    if (above + h >= left) {
-                        sh_digit = b;
-                        sh_left = left - above;
-                        break;
+            for (int i = 0; i < kPer; i += 2) {
+                if (CLUSTER) {
+                    for (uint32_t r = 0; r < size; r++) {
+                        const uint2 p = ld_peer(counts + bin + i, r);
+                        h[i] += p.x, h[i + 1] += p.y;
                     }
-                    above += h;
+                } else {
+                    h[i] = counts[bin + i], h[i + 1] = counts[bin + i + 1];
+                }
+                sum += h[i] + h[i + 1];
+            }
+            uint32_t total, above = block_excl_sum<uint32_t>(sum, sh_scan, &total);
+            if (above < left && above + sum >= left) {
+#pragma unroll
+                for (int i = kPer - 1; i >= 0; i--) {
+                    if (above < left && above + h[i] >= left) sh_digit = bin + i, sh_left = left - above;
+                    above += h[i];
                 }
             }
             __syncthreads();
@@ -169,12 +236,30 @@ __global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ 
     }
     if (lane == 0) sh_over[warp] = n_over, sh_ties[warp] = n_ties;
     __syncthreads();
-    uint32_t over = lane < warp ? sh_over[lane] : 0, ties = lane < warp ? sh_ties[lane] : 0;
+    // what comes before the warp: in blocks before this one, and in this one
+    uint2 peer = make_uint2(0, 0);
+    if constexpr (CLUSTER) {
+        if (warp == 0) {
+            uint32_t o = lane < kSelWarps ? sh_over[lane] : 0, t = lane < kSelWarps ? sh_ties[lane] : 0;
+#pragma unroll
+            for (int d = 16; d; d >>= 1) {
+                o += __shfl_xor_sync(0xFFFFFFFFu, o, d);
+                t += __shfl_xor_sync(0xFFFFFFFFu, t, d);
+            }
+            if (lane == 0) sh_all[0] = o, sh_all[1] = t;
+        }
+        cluster_arrive();
+        cluster_wait();
+        if (lane < rank) peer = ld_peer(sh_all, lane);
+    }
+    uint32_t over = peer.x + (lane < warp ? sh_over[lane] : 0), ties = peer.y + (lane < warp ? sh_ties[lane] : 0);
 #pragma unroll
     for (int o = 16; o; o >>= 1) {
         over += __shfl_xor_sync(0xFFFFFFFFu, over, o);
         ties += __shfl_xor_sync(0xFFFFFFFFu, ties, o);
     }
+    if (CLUSTER) cluster_arrive();  // done with the peers' memory
+    if (threadIdx.x == 0) sh_scan[0] = over + (ties < left ? ties : left);  // the block's first place
     for (uint32_t i0 = from; i0 < to; i0 += 128) {
         const uint32_t i = i0 + 4 * lane;
         uint4 k = make_uint4(kAbsent, kAbsent, kAbsent, kAbsent);
@@ -187,7 +272,7 @@ __global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ 
         uint32_t o = over + (before & 0xFFFF), t = ties + (before >> 16);
 #pragma unroll
         for (int u = 0; u < 4; u++) {
-            if (kk[u] > cut || (kk[u] == cut && t < left)) kept[o + (t < left ? t : left)] = i + u;
+            if (kk[u] > cut || (kk[u] == cut && t < left)) kept[o + (t < left ? t : left)] = part.first + i + u;
             o += kk[u] > cut;
             t += kk[u] == cut;
         }
@@ -195,9 +280,12 @@ __global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ 
         over += all & 0xFFFF;
         ties += all >> 16;
     }
+    if (threadIdx.x == kSelThreads - 1) sh_scan[1] = over + (ties < left ? ties : left);  // and the one after its last
     __syncthreads();
 #pragma unroll 4
-    for (uint32_t i = threadIdx.x; i < keep; i += kSelThreads) ks[i] = __ldg(x + __ldcg(kept + i));
+    for (uint32_t i = sh_scan[0] + threadIdx.x; i < sh_scan[1]; i += kSelThreads)
+        ks[i] = __ldg(x + (__ldcg(kept + i) - part.first));
+    if (CLUSTER) cluster_wait();  // no peer reads this block's memory any more
 }
 
 // Copies kRows tokens' K and V rows: a thread looks up each row's two places,
@@ -256,10 +344,38 @@ __global__ void __launch_bounds__(kGatherThreads) k_gather(const __grid_constant
     }
 }
 
+template <int THREADS, bool CLUSTER>
+bool launch_select(const EvictArgs &a, uint32_t rows, uint32_t size, uint32_t held, cudaStream_t s) {
+    static bool done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+        if (cudaFuncSetAttribute(k_select<THREADS, CLUSTER>, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4) !=
+            cudaSuccess)
+            return false;
+        if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+    if (!CLUSTER) {
+        k_select<THREADS, CLUSTER><<<rows, THREADS, held * 4, s>>>(a, held);
+        return true;
+    }
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(rows * size);
+    cfg.blockDim = dim3(THREADS);
+    cfg.dynamicSmemBytes = held * 4;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = size, attr[0].val.clusterDim.y = 1, attr[0].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, k_select<THREADS, CLUSTER>, a, held) == cudaSuccess;
+}
+
 bool sizes_ok(const kvx_cache *c, uint32_t num_seqs, uint32_t blocks_per_seq, uint32_t budget) {
     if (!cache_ok(c) || !budget || budget >= (1u << 31)) return false;
     if ((uint64_t)blocks_per_seq * c->page_tokens >= (1ull << 31)) return false;
-    return ceil_div(budget, kRows) * c->heads * (uint64_t)num_seqs < (1ull << 31);
+    return (ceil_div(budget, kRows) + kMaxCluster) * c->heads * (uint64_t)num_seqs < (1ull << 31);
 }
 
 }  // namespace
@@ -286,16 +402,24 @@ extern "C" kvx_status kvx_evict(const kvx_cache *cache, uint32_t num_seqs, const
     EvictArgs a = {cache_view(cache), blocks, lens, scores, scores_stride, dst_blocks, kept, kept_scores, new_lens,
                    status, num_seqs, blocks_per_seq, dst_per_seq, (uint32_t)max_len, budget, sinks, recent};
     const cudaStream_t s = as_stream(stream);
-    const uint32_t held = max_len < kHeld ? ((uint32_t)max_len + 3) & ~3u : kHeld;
-    static bool done[64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return KVX_ECUDA;
-    if (dev < 0 || dev >= 64 || !done[dev]) {
-        if (cudaFuncSetAttribute(k_select, cudaFuncAttributeMaxDynamicSharedMemorySize, kHeld * 4) != cudaSuccess)
-            return KVX_ECUDA;
-        if (dev >= 0 && dev < 64) done[dev] = true;
-    }
-    k_select<<<num_seqs * cache->heads, kSelThreads, held * 4, s>>>(a, held);
+    const uint32_t rows = num_seqs * cache->heads;
+    // Where there are fewer (sequence, head) pairs than SMs, blocks share one's
+    // tokens, kShare each at the least: 1 sequence of 131,071 tokens, 8 heads
+    // 111 us in one block each, 30 us in eight.  More blocks than SMs are slower
+    // (24 sequences of up to 40,000 tokens, 8 heads: 149 us, in clusters 159
+    // and more).
+    uint32_t size = 1;
+    while (size < kMaxCluster && 2 * size * (uint64_t)rows <= (uint64_t)sm_count() &&
+           max_len >= 2 * size * (uint64_t)kShare)
+        size *= 2;
+    const uint64_t each = ceil_div(max_len, 4 * size) * 4;
+    const uint32_t held = each < kHeld ? (uint32_t)each : kHeld;
+    // 64 sequences of 4000 tokens, 8 heads: 99 us in blocks of 512 threads, 111
+    // in blocks of 1024; up to 40,000 tokens: 157 and 149.
+    if (!(size > 1            ? launch_select<1024, true>(a, rows, size, held, s)
+          : max_len <= kShort ? launch_select<512, false>(a, rows, 1, held, s)
+                              : launch_select<1024, false>(a, rows, 1, held, s)))
+        return KVX_ECUDA;
     KVX_LAUNCHED();
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((uint32_t)ceil_div(budget, kRows) * cache->heads * num_seqs);

@@ -445,6 +445,10 @@ EVICT = [  # store, heads, dim, page, lens, budget, sinks, recent, kind, token_m
     (E4, 2, 208, 16, [12345, 4096, 4097], 1025, 4, 100, "random", True),
     (FP, 1, 16, 64, [100000], 5000, 4, 1000, "random", False),
     (FP, 1, 16, 64, [70001], 30000, 0, 0, "ties", False),
+    # more (sequence, head) pairs than half the SMs: a block each, its keys in shared memory and beyond it
+    (FP, 2, 16, 64, [17000, 18001] + [9] * 40, 2000, 4, 100, "special", False),
+    (FP, 1, 16, 64, [50001] + [10] * 80, 20000, 4, 100, "random", False),
+    (FP, 1, 16, 64, [60000] + [70] * 80, 50, 50, 100, "ties", False),
 ]
 
 
