@@ -24,8 +24,8 @@ extern template bool launch<__half, 1>(Args &, uint64_t, uint32_t, uint32_t, cud
 namespace {
 
 constexpr uint32_t kMaxGroup = 128;
-constexpr int kJoinWarps = 16;
-constexpr int kJoinUnroll = 8;  // parts whose loads a warp has in flight
+constexpr int kJoinWarps = 8;
+constexpr int kJoinUnroll = 4;  // parts whose loads a warp has in flight
 constexpr int kScoreThreads = 128;
 constexpr uint32_t kScoreKeys = 4 * kScoreThreads;  // of a block that adds weights
 
@@ -38,19 +38,21 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
     __shared__ float sh_m[kJoinWarps], sh_l[kJoinWarps];
     __shared__ float4 sh_o[kJoinWarps][32];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t heads = a.group < unit_heads ? a.group : unit_heads, deal = kJoinWarps / heads;
-    const uint32_t hh = warp / deal, turn = warp % deal, per_head = (a.group + unit_heads - 1) / unit_heads;
+    const uint32_t heads = a.group < unit_heads ? a.group : unit_heads;
+    const uint32_t deal = heads < kJoinWarps ? kJoinWarps / heads : 1, turn = warp % deal;
+    const uint32_t per_head = (a.group + unit_heads - 1) / unit_heads;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint4 cut = __ldcg(a.cut + blockIdx.x);
     if (cut.x == kNone) return;
     const uint32_t n = cut.x, parts = cut.z - blockIdx.x + 1;
-    const uint32_t in = cut.y % per_head * unit_heads + hh, qh = cut.y / per_head * a.group + in;
-    const bool has = hh < heads && in < a.group;
-    auto slot = [&](uint32_t i) { return (uint64_t)(i ? 2 * (blockIdx.x + i) : cut.w) * unit_heads + hh; };
-    // a lane takes four of 128 values at a time
-    for (uint32_t d0 = 0; d0 < dp; d0 += 128) {
-        const uint32_t d = d0 + lane * 4;
+    // Four of 128 values a lane, one head after the other where there are more
+    // heads than warps; every warp makes the same turns.
+    for (uint32_t h0 = 0, d0 = 0; h0 < heads; d0 += 128, h0 += d0 < dp ? 0 : kJoinWarps / deal, d0 = d0 < dp ? d0 : 0) {
+        const uint32_t d = d0 + lane * 4, hh = h0 + warp / deal;
+        const uint32_t in = cut.y % per_head * unit_heads + hh, qh = cut.y / per_head * a.group + in;
+        const bool has = hh < heads && in < a.group;
+        auto slot = [&](uint32_t i) { return (uint64_t)(i ? 2 * (blockIdx.x + i) : cut.w) * unit_heads + hh; };
         float4 v = make_float4(0, 0, 0, 0);
         float top = -INFINITY, sum = 0;
         for (uint32_t i0 = turn; has && i0 < parts; i0 += deal * kJoinUnroll) {
@@ -67,12 +69,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
             }
 #pragma unroll
             for (int u = 0; u < kJoinUnroll; u++) higher = fmaxf(higher, ml[u].x);
-            float f = top == -INFINITY ? 1.0f : exp2f(top - higher);
+            float f = top == -INFINITY ? 1.0f : exp2_fast(top - higher);
             top = higher;
             sum *= f, v.x *= f, v.y *= f, v.z *= f, v.w *= f;
 #pragma unroll
             for (int u = 0; u < kJoinUnroll; u++) {
-                f = ml[u].x == -INFINITY ? 1.0f : exp2f(ml[u].x - top);  // 1: zeros, or a NaN
+                f = ml[u].x == -INFINITY ? 1.0f : exp2_fast(ml[u].x - top);  // 1: zeros, or a NaN
                 sum += ml[u].y * f;
                 v.x += x[u].x * f, v.y += x[u].y * f, v.z += x[u].z * f, v.w += x[u].w * f;
             }
@@ -87,7 +89,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
             v = make_float4(0, 0, 0, 0);
             sum = 0;
             for (uint32_t w = 0; w < deal; w++) {
-                const float f = sh_m[warp + w] == -INFINITY ? 1.0f : exp2f(sh_m[warp + w] - top);
+                const float f = sh_m[warp + w] == -INFINITY ? 1.0f : exp2_fast(sh_m[warp + w] - top);
                 const float4 x = sh_o[warp + w][lane];
                 v.x += x.x * f, v.y += x.y * f, v.z += x.z * f, v.w += x.w * f;
                 sum += sh_l[warp + w] * f;
