@@ -630,7 +630,9 @@ size_t kvx_attend_workspace_size(const kvx_cache *cache, uint32_t num_seqs,
  * over the visible tokens.  A sequence without any (lens[n] == 0), like a head
  * whose logits are all -infinity, gets zeros and lse = -infinity.
  * Logits, softmax and sums are held in 32 bits; the weights that multiply V
- * go into the tensor cores as the sum of two 16-bit values.
+ * go into the tensor cores as the sum of two 16-bit values.  Over a
+ * KVX_E4M3 cache products are taken in fp16, bf16 queries scaled by a power of
+ * two per head (values under 2^-14 of a head's largest then lose low bits).
  *
  *   q              [num_seqs][q_heads][dim] of `dtype` (KVX_BF16 or KVX_F16;
  *                  the cache's type is the same one or KVX_E4M3), sequences

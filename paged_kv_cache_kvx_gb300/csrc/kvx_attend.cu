@@ -31,7 +31,10 @@ constexpr uint32_t kScoreKeys = 4 * kScoreThreads;  // of a block that adds weig
 
 // Block c joins the query heads of the unit whose first part block c of
 // k_attend did; its other parts are the first ones of blocks c+1 .. last.  The
-// warps are dealt out to the heads, and those of a head to its parts.
+// warps are dealt out to the heads, and those of a head to its parts.  Bound by
+// a chain of three loads: about 4 us behind k_attend, whatever the sizes; blocks
+// of sixteen warps with eight parts in flight did not fit on the SMs together
+// and took 3 us more.
 template <class T>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant__ Args a, uint32_t dp,
                                                           uint32_t unit_heads) {
@@ -110,7 +113,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
     }
 }
 
-// Adds the weights of kScoreKeys keys of a KV head, four keys a thread.
+// Adds the weights of kScoreKeys keys of a KV head, four keys a thread.  Bound
+// by HBM, logits in and scores in and out: 32 sequences of up to 6001 tokens, 8
+// heads of 5 query heads, about 7 us.
 __global__ void __launch_bounds__(kScoreThreads) k_scores(const __grid_constant__ Args a, uint32_t chunks) {
     __shared__ float sh_lse[kMaxGroup];
     const uint32_t row = blockIdx.x / chunks, n = row / a.c.heads, head = row % a.c.heads;
@@ -162,7 +167,7 @@ bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t bloc
           uint32_t sinks, bool scores, Plan &p) {
     if (!cache_ok(c) || !q_heads || q_heads % c->heads || q_heads / c->heads > kMaxGroup) return false;
     const uint64_t max_len = (uint64_t)blocks_per_seq * c->page_tokens;
-    if (max_len >= (1ull << 31) || num_seqs >= (1u << 24) || (uint64_t)num_seqs * q_heads >= (1ull << 30)) return false;
+    if (q_heads > 65536u || max_len >= (1ull << 31) || num_seqs >= (1u << 24) || (uint64_t)num_seqs * q_heads >= (1ull << 30)) return false;
     const uint32_t group = q_heads / c->heads;
     p.max_len = (uint32_t)max_len;
     p.dp = c->dim <= 64 ? 64 : c->dim <= 128 ? 128 : 256;

@@ -1,6 +1,6 @@
 // The attention kernels of kvx_attend, as templates on the element types and
 // the head size; kvx_attend_*.cu instantiate them, kvx_attend.cu has the entry
-// point and the joining kernel.
+// point, the joining kernel and the one that adds weights.
 #pragma once
 
 #include <type_traits>
@@ -10,7 +10,7 @@
 namespace kvx {
 namespace attend {
 
-constexpr int kWarps = 4;                       // that compute; one more looks up and copies
+constexpr int kWarps = 4;                       // that copy and compute; one more looks pages up
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr uint32_t kStep = 16 * kWarps;         // keys of a block's step, and of a tile in which work is shared out
 constexpr uint32_t kWhole = 256;                // keys up to which no unit is split
@@ -34,7 +34,7 @@ struct Args {
     float *part_ml;  // [2 * blocks][heads of a unit][2]: base and sum
     uint4 *cut;      // [blocks]: the unit whose first part the block did: sequence (or none), unit, last block, slot
     float *lse2;     // [num_seqs][q_heads]: log2 of the sum of the exponentials
-    float *logits;   // [num_seqs][heads][visible][group rounded up to even], in powers of two
+    float *logits;   // [num_seqs][heads][logits_keys][group rounded up to even], in powers of two
     uint64_t logits_keys;
     float scale2;    // scale * k_scale * log2(e)
     uint32_t num_seqs, q_heads, group, units;  // units: pieces of a sequence's heads that blocks take
@@ -76,7 +76,7 @@ __device__ __forceinline__ float exp2_fast(float x) {
 template <class T>
 __device__ __forceinline__ void mma(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                     uint32_t b1) {
-    if constexpr (sizeof(Pair<T>) && std::is_same<T, __nv_bfloat16>::value)
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
         asm volatile(
             "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
             "{%0,%1,%2,%3};"
@@ -115,11 +115,6 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, uint32
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
     else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void copies_wait() {
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
@@ -283,7 +278,8 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
             if (lane == 0) {
                 const uint32_t qh0 = unit % units_per_head * S::kHeads;
                 const uint32_t nheads = a.group - qh0 < S::kHeads ? a.group - qh0 : S::kHeads;
-                pieces[np % kPieces] = Piece{n,  head, qh0, nheads, k, k1, whole ? kNone : slot, sv.turn, sv.shift, sv.sinks, sv.recent};
+                pieces[np % kPieces] = Piece{n,  head, qh0, nheads, k, k1, whole ? kNone : slot,
+                                             sv.turn, sv.shift, sv.sinks, sv.recent};
             }
             np++;
             __syncwarp();
@@ -467,10 +463,13 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
 // from warp to warp through a buffer of the same lanes' places, so that no
 // warp waits for a slower one before it goes on to the next piece.
 //
-// Bound by HBM: per key 2*DP*ES bytes for 4*group*DP operations.  mma.sync
-// suffices: with 16 columns in use the SMs need well under a fifth of its
-// rate to consume the measured bandwidth, and operands come to registers
-// without a transposition through shared memory that a larger tile would need.
+// Bound by HBM: per key 2*DP*ES bytes for 4*group*DP operations.  One sequence
+// of 131,071 tokens, 8 KV heads of 128 values, bf16: 86 us at 6.3 TB/s (7.1
+// between the first and the last copy) with 13 % of the tensor pipe's cycles
+// in use; 8-bit with 8 query heads to a KV head: 22 %.  So mma.sync suffices:
+// its operands come to registers from rows as they lie, where a larger tile of
+// the tensor cores' would want them transposed and regrouped first, for 4 to 16
+// query heads that fill a fraction of it.
 template <class T, int DP, int ES, int NT, bool PAGED16>
 __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_attend(const __grid_constant__ Args a) {
     using S = Shape<DP, ES, NT>;
@@ -807,17 +806,17 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
                 }
 
             // O^T += V^T P^T
-            const uint8_t *sv_ = st + S::kStage / 2 + vslot;
+            const uint8_t *sv = st + S::kStage / 2 + vslot;
 #pragma unroll
             for (int c = 0; c < S::kVParts; c++) {
                 uint32_t v[4][S::kVBytes / 4];
 #pragma unroll
                 for (int r = 0; r < 4; r++) {
                     if constexpr (S::kVBytes == 16) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(sv_ + (c * 4 + r) * 512);
+                        const uint4 x = *reinterpret_cast<const uint4 *>(sv + (c * 4 + r) * 512);
                         v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
                     } else {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(sv_ + (c * 4 + r) * 256);
+                        const uint2 x = *reinterpret_cast<const uint2 *>(sv + (c * 4 + r) * 256);
                         v[r][0] = x.x, v[r][1] = x.y;
                     }
                 }

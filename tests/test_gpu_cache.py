@@ -273,6 +273,67 @@ def test_attend(case):
     run_attend(case)
 
 
+@pytest.mark.parametrize("page", [16, 5])
+def test_attend_many_short_sequences(page):
+    """More sequences than threads of a block, several to a block, with empty ones between and a few that are split."""
+    rng = np.random.default_rng(page)
+    lens = rng.integers(0, 70, size=700).tolist()
+    for n in (0, 3, 350, 699):
+        lens[n] = [0, 1500, 700, 300][(0, 3, 350, 699).index(n)]
+    run_attend((BF, BF, 3, 1, 64, page, 0, 0, True, False, lens))
+    run_attend((FP, E4, 2, 1, 128, page, 9, 2, False, True, lens))
+
+
+def test_attend_without_pages_or_sequences():
+    lay = R.Layout(2, 2, 64, 16, BF, 1)
+    cache = lay.cache(torch.zeros(lay.pool_bytes, dtype=torch.uint8, device="cuda"))
+    q = torch.ones(3, 4, 64, dtype=BF, device="cuda")
+    out, lse = torch.full_like(q, 7), torch.zeros(3, 4, device="cuda")
+    lens = torch.zeros(3, dtype=torch.int32, device="cuda")
+    ws = cache.attend_workspace(3, 4, 0, scores=True)
+    cache.attend(q, torch.empty(3, 0, dtype=torch.int32, device="cuda"), lens, out, ws, lse=lse,
+                 scores=torch.empty(3, 2, 0, device="cuda"))
+    assert (out == 0).all() and (lse == -math.inf).all() and cache.read_status() == 0
+    before = kvx.kvx_launch_count()
+    cache.attend(q[:0], torch.empty(0, 4, dtype=torch.int32, device="cuda"), lens[:0], out[:0], ws)
+    assert kvx.kvx_launch_count() == before
+
+
+def test_attend_writes_into_a_strided_output():
+    """out as a part of a wider row; what lies between stays."""
+    lay, k, v, q, table, _ = make_attend(BF, BF, 8, 2, 128, 16, 0, 0, False, False, [900, 30, 0], poison=False)
+    cache = lay.cache(lay.pool(k, v).cuda())
+    wide = torch.full((3, 8 * 128 + 24), 5.0, dtype=BF, device="cuda")
+    out = wide[:, 8:8 + 8 * 128].unflatten(1, (8, 128))
+    lens = torch.tensor([900, 30, 0], dtype=torch.int32).cuda()
+    cache.attend(q.cuda(), table.cuda(), lens, out, cache.attend_workspace(3, 8, table.shape[1]))
+    want, _, _, off, _ = R.attend(q, k.float(), v.float(), table, [900, 30, 0], 128 ** -0.5, 0, 0)
+    near(out, want, BF, off)
+    assert (wide[:, :8] == 5).all() and (wide[:, 8 + 8 * 128:] == 5).all()
+
+
+def test_operators_on_two_streams_at_once():
+    """Calls on two streams, each with its own workspace and outputs, give what they give alone."""
+    cases = [(BF, BF, 16, 2, 128, 16, 0, 0, True, False, [5000, 10, 777]), (BF, BF, 8, 2, 64, 24, 50, 3, True, False, [900] * 9)]
+    alone = [run_attend(c) for c in cases]
+    streams = [torch.cuda.Stream() for _ in cases]
+    work = []
+    for c in cases:
+        lay, k, v, q, table, sc = make_attend(*c)
+        cache = lay.cache(lay.pool(k, v).cuda())
+        N, per = table.shape
+        work.append((cache, q.cuda(), table.cuda(), torch.tensor(c[10], dtype=torch.int32).cuda(), torch.empty_like(q).cuda(),
+                     cache.attend_workspace(N, q.shape[1], per, window=c[6], sinks=c[7], scores=True),
+                     torch.empty(N, q.shape[1], device="cuda"), sc.cuda()))
+    torch.cuda.synchronize()
+    for turn in range(20):
+        for c, s, (cache, q, table, lens, out, ws, lse, sc) in zip(cases, streams, work):
+            cache.attend(q, table, lens, out, ws, window=c[6], sinks=c[7], lse=lse, scores=sc if turn == 0 else None, stream=s)
+    torch.cuda.synchronize()
+    for a, (cache, q, table, lens, out, ws, lse, sc) in zip(alone, work):
+        assert torch.equal(a[0], out) and torch.equal(a[1], lse) and torch.equal(a[2], sc) and cache.read_status() == 0
+
+
 def test_attend_repeats_bit_for_bit_and_on_another_stream():
     case = (BF, BF, 16, 2, 128, 16, 0, 0, True, False, [4000, 10, 777])
     a = run_attend(case)
