@@ -185,6 +185,8 @@ bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t bloc
     p.tile = p.max_seen <= kWhole ? kWhole : kStep;
     const uint64_t unit_tiles = ceil_div(p.max_seen, p.tile);
     const uint64_t all = unit_tiles * p.units * num_seqs;
+    // the kernel counts tiles, and what units cost beside them, in 32 bits
+    if ((unit_tiles + kMaxExtra) * p.units * num_seqs >= 1ull << 31) return false;
     p.parts = all < kMaxBlocks ? all : kMaxBlocks;
     p.split = unit_tiles > 1;
     p.part_o = p.split ? 2 * p.parts * p.unit_heads * p.dp : 0;

@@ -14,6 +14,7 @@ constexpr int kWarps = 4;                       // that copy and compute; one mo
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr uint32_t kStep = 16 * kWarps;         // keys of a block's step, and of a tile in which work is shared out
 constexpr uint32_t kWhole = 256;                // keys up to which no unit is split
+constexpr uint32_t kMaxExtra = 8;               // Shape::kExtra at the most
 constexpr uint32_t kMaxBlocks = 512;            // bounds the partial results in the workspace
 constexpr int kPieces = 8;                      // descriptors that the looking-up warp may be ahead
 
@@ -140,6 +141,7 @@ struct Shape {
     // What a unit costs beside its keys (its query, its output) counts as so
     // many tiles when work is shared out: about 64 KB of copies.
     static constexpr uint32_t kExtra = DP * ES >= 512 ? 1 : 512 / (DP * ES);
+    static_assert(kExtra <= kMaxExtra);
     static constexpr int kRing = kWarps * kStages * kStage;
     // Where the rings of an SM hold more than 160 KB (16-bit, 128 values, three
     // blocks) the next tile's copies go out when the present one's have
@@ -152,9 +154,14 @@ struct Shape {
     static constexpr int kSmem = kRing + kQBufs * kQ + kJoin;
 };
 
-// 64-bit division takes several times as long as 32-bit division.
-__device__ __forceinline__ uint64_t quotient(uint64_t a, uint64_t b) {
-    return (a | b) >> 32 ? a / b : (uint64_t)((uint32_t)a / (uint32_t)b);
+// a / b, b > 0.  Small quotients go through the reciprocal, a third of a
+// division's latency: a < 2^22 is exact as a float, and a * (1/b) is off by
+// less than one.
+__device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t b) {
+    if (a >= 1u << 22) return a / b;
+    uint32_t q = (uint32_t)__fmul_rz((float)a, __frcp_rz((float)b));
+    q += a - q * b >= b;
+    return q;
 }
 
 // A part of a unit that one block works on.
@@ -204,8 +211,8 @@ __device__ __forceinline__ void load_early(uint64_t &v, const uint64_t *p, bool 
 // addresses of the step before are, and the rows of the one before that are
 // handed to the warps.
 template <class T, int DP, int ES, int NT, bool PAGED16>
-__device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t per, uint32_t lane,
-                                        uint4 *qbuf, const uint64_t *upto, uint64_t (*rows)[32], uint64_t (*ready)[2],
+__device__ __forceinline__ void look_up(const Args &a, uint32_t total, uint32_t per, uint32_t lane,
+                                        uint4 *qbuf, const uint32_t *upto, uint64_t (*rows)[32], uint64_t (*ready)[2],
                                         uint64_t (*taken)[2], uint64_t *pfull, uint64_t *pempty, Piece *pieces,
                                         uint32_t &bad) {
     using S = Shape<DP, ES, NT>;
@@ -214,19 +221,11 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
     auto unit_len = [&](uint32_t keys) { return keys ? (keys + a.tile - 1) / a.tile + S::kExtra : 0; };
     bool alive = true;  // no wait has run out
 
-    // the sequences without a visible token
-    for (uint32_t i = blockIdx.x; i < a.num_seqs; i += gridDim.x)
-        if (!seen(a, a.lens[i]).n) {
-            for (uint32_t d = lane; d < a.q_heads * a.c.dim; d += 32)
-                static_cast<T *>(a.out)[i * a.out_stride + d] = T(0.0f);
-            for (uint32_t d = lane; d < a.q_heads; d += 32)
-                if (a.lse) a.lse[(uint64_t)i * a.q_heads + d] = -INFINITY;
-        }
-
     // -- where the walk is: tiles at .. end-1 are still to come
-    const uint64_t share = quotient(total + a.grid - 1, a.grid), begin = blockIdx.x * share;
-    const uint64_t end = begin + share < total ? begin + share : total;
-    uint64_t at = begin, seq_tile = 0;  // seq_tile: within the sequence
+    const uint32_t share = quotient(total + a.grid - 1, a.grid);
+    const uint32_t begin = blockIdx.x * share < total ? blockIdx.x * share : total;
+    const uint32_t end = total - begin > share ? begin + share : total;
+    uint32_t at = begin, seq_tile = 0;  // seq_tile: within the sequence
     uint32_t n = 0, len_u = 0;
     Seen sv = {};
     uint32_t np = 0;                   // pieces so far
@@ -237,12 +236,12 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
     } else {
         // the first sequence: by the threads' counts, then one by one
         const uint32_t i = __popc(__ballot_sync(0xFFFFFFFFu, upto[lane] * a.units <= at));
-        uint64_t before = i ? upto[i - 1] * a.units : 0;
+        uint32_t before = i ? upto[i - 1] * a.units : 0;
         for (n = i * kWarps * per;; n++) {
             sv = seen(a, a.lens[n]);
             len_u = unit_len(sv.n);
-            if (at < before + (uint64_t)len_u * a.units) break;
-            before += (uint64_t)len_u * a.units;
+            if (at - before < len_u * a.units) break;
+            before += len_u * a.units;
         }
         seq_tile = at - before;
     }
@@ -250,14 +249,14 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
     // Moves on to the next piece with keys; false at the end of all work.
     auto next_piece = [&]() -> bool {
         while (at < end) {
-            while (seq_tile >= (uint64_t)len_u * a.units) {
-                seq_tile -= (uint64_t)len_u * a.units;
+            while (seq_tile >= len_u * a.units) {
+                seq_tile -= len_u * a.units;
                 do sv = seen(a, a.lens[++n]);
                 while (!sv.n);
                 len_u = unit_len(sv.n);
             }
-            const uint32_t unit = (uint32_t)quotient(seq_tile, len_u), from = (uint32_t)(seq_tile - (uint64_t)unit * len_u);
-            const uint32_t to = (uint32_t)(len_u - from < end - at ? len_u : from + (end - at));
+            const uint32_t unit = quotient(seq_tile, len_u), from = seq_tile - unit * len_u;
+            const uint32_t to = len_u - from < end - at ? len_u : from + (end - at);
             // the kExtra that stand for the unit's overhead come first
             const uint32_t nt = len_u - S::kExtra;
             const uint32_t tile0 = from > S::kExtra ? from - S::kExtra : 0, tile1 = to > S::kExtra ? to - S::kExtra : 0;
@@ -266,7 +265,7 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
             const uint32_t slot = 2 * blockIdx.x + (at != begin);
             if (a.cut && lane == 0 && at + (to - from) == end)
                 a.cut[blockIdx.x] = make_uint4(tile0 == 0 && tile1 && !whole ? n : kNone, unit,
-                                               (uint32_t)quotient(at - from + len_u - 1, share), slot);
+                                               quotient(at - from + len_u - 1, share), slot);
             at += to - from;
             seq_tile += to - from;
             if (tile0 == tile1) continue;
@@ -409,13 +408,14 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
         if (lane < s.warps) mbar_arrive(&ready[lane][buffer]);
     };
 
-    // (find_blocks() is not asked again after it has said that there is no more)
+    // (find_blocks() is not asked again after it has said that there is no
+    // more; the first step's rows are handed over before the third is looked for)
     Step now = find_blocks(), held = {}, next = {};
     find_entries(now);
-    if (now.warps) held = find_blocks();
     find_addrs(now);
+    if (now.warps) held = find_blocks();
     find_entries(held);
-    if (held.warps) next = find_blocks();
+    bool first = true;
     while (alive && now.warps) {
         uint64_t row[kKeys][kSegs];
 #pragma unroll
@@ -431,10 +431,12 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
         const Step s = now;
         now = held;
         find_addrs(now);
+        issue(s, row);
+        if (first && now.warps) next = find_blocks();
+        first = false;
         held = next;
         find_entries(held);
         if (held.warps) next = find_blocks();
-        issue(s, row);
     }
     if (alive) {  // the end of the stream
         if (np >= kPieces && !mbar_wait(&pempty[np % kPieces], (np / kPieces & 1) ^ 1)) alive = false;
@@ -443,6 +445,15 @@ __device__ __forceinline__ void look_up(const Args &a, uint64_t total, uint32_t 
         if (alive) announce(np);
     }
     if (!alive) bad |= KVX_S_TIMEOUT;
+
+    // the sequences without a visible token
+    for (uint32_t i = blockIdx.x; i < a.num_seqs; i += gridDim.x)
+        if (!seen(a, a.lens[i]).n) {
+            for (uint32_t d = lane; d < a.q_heads * a.c.dim; d += 32)
+                static_cast<T *>(a.out)[i * a.out_stride + d] = T(0.0f);
+            for (uint32_t d = lane; d < a.q_heads; d += 32)
+                if (a.lse) a.lse[(uint64_t)i * a.q_heads + d] = -INFINITY;
+        }
     asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
@@ -477,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
     using C = typename std::conditional<ES == 1, __half, T>::type;
     constexpr bool kConvertQ = !std::is_same<C, T>::value;
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ uint64_t sh_sum[kWarps + 1], sh_upto[32];
+    __shared__ uint32_t sh_sum[kWarps + 1], sh_upto[32];
     __shared__ uint64_t full[kWarps][S::kStages];   // a warp's tiles
     // Where its next ones' rows are.  PAGED16: two buffers of four tiles, for
     // each the first row's address, which rows are seen, and whether the tile
@@ -504,7 +515,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
     // ---- the tiles of all units: each thread counts those of some sequences in a row
     const uint32_t per = (a.num_seqs + kWarps * 32 - 1) / (kWarps * 32);
     auto unit_len = [&](uint32_t keys) { return keys ? (keys + a.tile - 1) / a.tile + S::kExtra : 0; };
-    uint64_t mine = 0;
+    uint32_t mine = 0;
     if (warp < kWarps) {
         const uint32_t n0 = threadIdx.x * per, n1 = n0 + per < a.num_seqs ? n0 + per : a.num_seqs;
         for (uint32_t n = n0; n < n1; n++) {
@@ -530,7 +541,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
         mbar_init(&converted[1], NT);
     }
     {
-        uint64_t upto = warp_incl_sum(mine);
+        uint32_t upto = warp_incl_sum(mine);
         if (lane == 31) sh_sum[warp] = upto;
         __syncthreads();
         for (uint32_t w = 0; w < warp && w < kWarps; w++) upto += sh_sum[w];
