@@ -172,9 +172,8 @@ bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t bloc
     p.max_len = (uint32_t)max_len;
     p.dp = c->dim <= 64 ? 64 : c->dim <= 128 ? 128 : 256;
     // 16 columns where the group needs them: keys and values are then read
-    // once for 16 heads.  At 256 values a head their accumulators would not
-    // leave registers enough, and the heads are taken eight at a time.
-    p.nt = group > 8 && p.dp < 256 ? 2 : 1;
+    // once for 16 heads.
+    p.nt = group > 8 ? 2 : 1;
     p.unit_heads = 8 * p.nt;
     p.units = c->heads * (uint32_t)ceil_div(group, p.unit_heads);
     p.align = c->page_tokens % 16 ? 1 : 16;

@@ -136,7 +136,7 @@ struct Shape {
     // Blocks that an SM has registers for.  Two stages a warp: with three to six
     // the copies in flight got in each other's way (16 query heads to a KV head,
     // 128 values: 104 us where two stages take 94; 8-bit, 8 heads: 98 and 93).
-    static constexpr int kBlocks = DP == 256 ? (ES == 1 ? 2 : 1) : NT == 2 && DP == 128 ? 2 : 3;
+    static constexpr int kBlocks = DP == 256 ? (ES == 1 && NT == 1 ? 2 : 1) : NT == 2 && DP == 128 ? 2 : 3;
     static constexpr int kStages = 2;
     // What a unit costs beside its keys (its query, its output) counts as so
     // many tiles when work is shared out: about 64 KB of copies.
@@ -1000,7 +1000,7 @@ template <class T, int ES>
 bool launch(Args &a, uint64_t most, uint32_t dim, uint32_t nt, cudaStream_t s) {
     if (dim <= 64) return nt == 1 ? launch_one<T, 64, ES, 1>(a, most, s) : launch_one<T, 64, ES, 2>(a, most, s);
     if (dim <= 128) return nt == 1 ? launch_one<T, 128, ES, 1>(a, most, s) : launch_one<T, 128, ES, 2>(a, most, s);
-    return launch_one<T, 256, ES, 1>(a, most, s);
+    return nt == 1 ? launch_one<T, 256, ES, 1>(a, most, s) : launch_one<T, 256, ES, 2>(a, most, s);
 }
 
 }  // namespace attend

@@ -195,6 +195,10 @@ ATTEND = [  # act, store, q_heads, heads, dim, page, window, sinks, scores, toke
     (BF, BF, 128, 1, 64, 16, 7, 1, True, False, [700, 3, 20]),
     (BF, BF, 8, 2, 128, 16, 0, 0, True, False, [9000]),
     (FP, E4, 16, 1, 128, 16, 0, 0, True, False, [0, 20000, 1]),
+    (BF, BF, 16, 1, 256, 16, 0, 0, True, False, LENS),
+    (FP, FP, 11, 1, 208, 24, 100, 33, True, True, LENS),
+    (BF, E4, 26, 2, 224, 5, 0, 0, False, False, LENS),
+    (BF, E4, 16, 1, 256, 16, 0, 0, True, False, [9000, 0, 5]),
 ]
 
 
