@@ -12,7 +12,7 @@
 // equals, the sinks and the last tokens are then written in order: each warp
 // counts its own stretch, sums over the warps and blocks before it give its
 // places.  Bound by the latency of these steps and, with many heads, by their
-// instructions: 24 sequences of up to 40,000 tokens, 8 heads, in 25 us.
+// instructions: 24 sequences of up to 40,000 tokens, 8 heads, in 22 us.
 // k_gather copies the kept rows, 0.8 GB read and written for those in 116 us,
 // 6.9 TB/s: at HBM's rate.
 #include "kvx_cache.cuh"
@@ -24,9 +24,9 @@ constexpr int kBins = 2048;
 constexpr uint32_t kHeld = 49152;  // keys that a block keeps in shared memory
 constexpr uint32_t kMaxCluster = 8;
 constexpr uint32_t kShare = 2048;  // tokens for which a block of a cluster pays
-constexpr uint32_t kShort = 16384; // tokens up to which a smaller block is faster
+constexpr uint32_t kTiny = 2048, kShort = 8192;  // tokens up to which smaller blocks are faster
 constexpr int kDigits = 3;
-constexpr int kSelUnroll = 8;
+constexpr int kSelUnroll = 2;  // groups of four tokens
 // Keys that no score has: a token that is not there, and one that stays in any case.
 constexpr uint32_t kAbsent = 0, kStays = 0xFFFFFFFFu;
 constexpr int kRows = 64;  // tokens whose K and V rows a block of k_gather copies
@@ -42,14 +42,14 @@ struct EvictArgs {
     float *kept_scores;
     uint32_t *new_lens, *status;
     uint32_t num_seqs, blocks_per_seq, dst_per_seq, max_len, budget, sinks, recent;
+    bool aligned;  // rows of scores to 16 bytes
 };
 
 // Larger key = larger score; -0 = +0, and a NaN ranks with -infinity.
 __device__ __forceinline__ uint32_t key_of(float f) {
-    uint32_t u = __float_as_uint(f);
-    if (f != f) u = 0xFF800000u;
-    if (u == 0x80000000u) u = 0;
-    return u & 0x80000000u ? ~u : u | 0x80000000u;
+    const float g = f != f ? -INFINITY : f + 0.0f;
+    const int u = __float_as_int(g);
+    return (uint32_t)(u ^ (u >> 31 | (int)0x80000000));
 }
 
 __device__ __forceinline__ uint32_t cluster_rank() {
@@ -92,7 +92,8 @@ struct Part {
 };
 
 template <int kSelThreads, bool CLUSTER>
-__global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ EvictArgs a, uint32_t held) {
+__global__ void __launch_bounds__(kSelThreads, kSelThreads == 1024 ? 1 : 1536 / kSelThreads)
+k_select(const __grid_constant__ EvictArgs a, uint32_t held) {
     constexpr int kSelWarps = kSelThreads / 32, kHists = CLUSTER ? kDigits : 1;
     extern __shared__ __align__(16) uint32_t keys[];  // [held], of the part's first tokens; held is a multiple of four
     __shared__ __align__(16) uint32_t hist[kHists][kBins];  // one a digit in a cluster: peers may still read the last one
@@ -131,38 +132,53 @@ __global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ 
     const uint32_t hi = len - recent;  // tokens lo .. hi-1 compete for `take` places
     const uint32_t take = a.budget - lo - recent;
 
-    auto make_key = [&](uint32_t i, float v) {
-        const uint32_t token = part.first + i;
-        return token >= lo && token < hi ? key_of(v) : kStays;
+    // Scores of the part's tokens i .. i+3, i a multiple of four; where rows
+    // are aligned what follows the last token is read too, but for nothing.
+    auto load = [&](uint32_t i) -> float4 {
+        if (a.aligned) return __ldg(reinterpret_cast<const float4 *>(x + i));
+        const uint32_t last = part.n - 1;
+        return make_float4(__ldg(x + i), __ldg(x + (i + 1 < last ? i + 1 : last)),
+                           __ldg(x + (i + 2 < last ? i + 2 : last)), __ldg(x + (i + 3 < last ? i + 3 : last)));
+    };
+    auto make_key = [&](uint32_t i, float v) -> uint32_t {
+        const uint32_t key = part.first + i - lo < hi - lo ? key_of(v) : kStays;
+        return i < part.n ? key : kAbsent;
+    };
+    auto make_keys = [&](uint32_t i, float4 v) {
+        return make_uint4(make_key(i, v.x), make_key(i + 1, v.y), make_key(i + 2, v.z), make_key(i + 3, v.w));
     };
     // Keys of the part's tokens i .. i+3, i a multiple of four.
     auto keys_at = [&](uint32_t i) -> uint4 {
         if (i < held) return *reinterpret_cast<const uint4 *>(keys + i);
-        uint32_t k[4];
-#pragma unroll
-        for (int u = 0; u < 4; u++) k[u] = i + u < part.n ? make_key(i + u, __ldg(x + i + u)) : kAbsent;
-        return make_uint4(k[0], k[1], k[2], k[3]);
+        return make_keys(i, load(i));
     };
 
-    for (uint32_t i = threadIdx.x; i < kHists * kBins; i += kSelThreads) hist[i / kBins][i % kBins] = 0;
+    for (uint32_t i = threadIdx.x; i < kHists * kBins / 4; i += kSelThreads)
+        reinterpret_cast<uint4 *>(hist[0])[i] = make_uint4(0, 0, 0, 0);
     __syncthreads();
     const uint32_t padded = (part.n + 3) & ~3u;
-    for (uint32_t i0 = threadIdx.x; i0 < padded; i0 += kSelUnroll * kSelThreads) {
-        float v[kSelUnroll];
-#pragma unroll
-        for (int u = 0; u < kSelUnroll; u++) v[u] = i0 + u * kSelThreads < part.n ? __ldg(x + i0 + u * kSelThreads) : 0;
+    for (uint32_t i0 = 4 * threadIdx.x; i0 < padded; i0 += kSelUnroll * 4 * kSelThreads) {
+        float4 v[kSelUnroll];
 #pragma unroll
         for (int u = 0; u < kSelUnroll; u++) {
-            const uint32_t i = i0 + u * kSelThreads;
+            const uint32_t i = i0 + u * 4 * kSelThreads;
+            if (i < padded) v[u] = load(i);
+        }
+#pragma unroll
+        for (int u = 0; u < kSelUnroll; u++) {
+            const uint32_t i = i0 + u * 4 * kSelThreads;
             if (i >= padded) break;
-            const uint32_t k = i < part.n ? make_key(i, v[u]) : kAbsent;
-            if (i < held) keys[i] = k;
-            if (k != kAbsent && k != kStays) atomicAdd(&hist[0][k >> 21], 1u);
+            const uint4 k = make_keys(i, v[u]);
+            if (i < held) *reinterpret_cast<uint4 *>(keys + i) = k;
+            auto add = [&](uint32_t key) {
+                if (key - 1 < kStays - 1) atomicAdd(&hist[0][key >> 21], 1u);
+            };
+            add(k.x), add(k.y), add(k.z), add(k.w);
         }
     }
     __syncthreads();
 
-    // the threshold: the take-th largest key, and how many of its equals stay
+    // the threshold: what is over `cut` stays, and `left` of what equals it
     uint32_t cut = take ? 0 : kStays - 1, left = take;
     if (take) {
 #pragma unroll 1
@@ -174,9 +190,9 @@ __global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ 
                     for (uint32_t i = threadIdx.x; i < kBins; i += kSelThreads) counts[i] = 0;
                     __syncthreads();
                 }
-                const uint32_t bins = pass == 2 ? 1024 : 2048, known = pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
+                const uint32_t rest = pass == 1 ? 1u << 21 : 1u << 10;
                 auto add = [&](uint32_t k) {  // (no cut begins like kStays)
-                    if ((k & known) == cut) atomicAdd(&counts[k >> shift & (bins - 1)], 1u);
+                    if ((k ^ cut) < rest) atomicAdd(&counts[(k ^ cut) >> shift], 1u);
                 };
 #pragma unroll 2
                 for (uint32_t i = 4 * threadIdx.x; i < padded; i += 4 * kSelThreads) {
@@ -210,14 +226,20 @@ __global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ 
             if (above < left && above + sum >= left) {
 #pragma unroll
                 for (int i = kPer - 1; i >= 0; i--) {
-                    if (above < left && above + h[i] >= left) sh_digit = bin + i, sh_left = left - above;
+                    if (above < left && above + h[i] >= left)
+                        sh_digit = bin + i, sh_left = left - above, sh_all[0] = above + h[i] == left;
                     above += h[i];
                 }
             }
             __syncthreads();
             cut |= sh_digit << shift;
             left = sh_left;
+            const bool all = sh_all[0];
             __syncthreads();
+            if (all) {  // all that share these digits stay: the rest does not matter
+                cut--, left = 0;
+                break;
+            }
         }
     }
 
@@ -261,32 +283,36 @@ __global__ void __launch_bounds__(kSelThreads) k_select(const __grid_constant__ 
         ties += __shfl_xor_sync(0xFFFFFFFFu, ties, o);
     }
     if (CLUSTER) cluster_arrive();  // done with the peers' memory
-    if (threadIdx.x == 0) sh_scan[0] = over + (ties < left ? ties : left);  // the block's first place
-    for (uint32_t i0 = from; i0 < to; i0 += 128) {
-        const uint32_t i = i0 + 4 * lane;
-        uint4 k = make_uint4(kAbsent, kAbsent, kAbsent, kAbsent);
-        if (i < to) k = keys_at(i);
-        const uint32_t kk[4] = {k.x, k.y, k.z, k.w};
-        uint32_t both = 0;  // over the threshold, and equal to it, in halves
+    const uint32_t below = (1u << lane) - 1;
+    auto write = [&](auto TIES) {
+        for (uint32_t i0 = from; i0 < to; i0 += 128) {
 #pragma unroll
-        for (int u = 0; u < 4; u++) both += (kk[u] > cut) + ((uint32_t)(kk[u] == cut) << 16);
-        const uint32_t incl = warp_incl_sum(both), before = incl - both;
-        uint32_t o = over + (before & 0xFFFF), t = ties + (before >> 16);
-#pragma unroll
-        for (int u = 0; u < 4; u++) {
-            if (kk[u] > cut || (kk[u] == cut && t < left)) kept[o + (t < left ? t : left)] = part.first + i + u;
-            o += kk[u] > cut;
-            t += kk[u] == cut;
+            for (int u = 0; u < 4; u++) {
+                const uint32_t i = i0 + u * 32 + lane;
+                uint32_t k = kAbsent;
+                if (i < to) k = i < held ? keys[i] : make_key(i, __ldg(x + (i < part.n ? i : part.n - 1)));
+                const uint32_t more = __ballot_sync(0xFFFFFFFFu, k > cut);
+                uint32_t place = over + __popc(more & below);
+                bool stays = k > cut;
+                if (TIES.value) {
+                    const uint32_t same = __ballot_sync(0xFFFFFFFFu, k == cut);
+                    const uint32_t t = ties + __popc(same & below);
+                    stays |= k == cut && t < left;
+                    place += t < left ? t : left;
+                    ties += __popc(same);
+                }
+                over += __popc(more);
+                if (stays) {
+                    kept[place] = part.first + i;
+                    ks[place] = __ldg(x + i);
+                }
+            }
         }
-        const uint32_t all = __shfl_sync(0xFFFFFFFFu, incl, 31);
-        over += all & 0xFFFF;
-        ties += all >> 16;
-    }
-    if (threadIdx.x == kSelThreads - 1) sh_scan[1] = over + (ties < left ? ties : left);  // and the one after its last
-    __syncthreads();
-#pragma unroll 4
-    for (uint32_t i = sh_scan[0] + threadIdx.x; i < sh_scan[1]; i += kSelThreads)
-        ks[i] = __ldg(x + (__ldcg(kept + i) - part.first));
+    };
+    if (left)
+        write(std::true_type());
+    else
+        write(std::false_type());
     if (CLUSTER) cluster_wait();  // no peer reads this block's memory any more
 }
 
@@ -402,25 +428,31 @@ extern "C" kvx_status kvx_evict(const kvx_cache *cache, uint32_t num_seqs, const
         return KVX_EINVAL;
     if (!ws || ws_bytes < kvx_evict_workspace_size(cache, num_seqs, blocks_per_seq, budget)) return KVX_EINVAL;
     EvictArgs a = {cache_view(cache), blocks, lens, scores, scores_stride, dst_blocks, kept, kept_scores, new_lens,
-                   status, num_seqs, blocks_per_seq, dst_per_seq, (uint32_t)max_len, budget, sinks, recent};
+                   status, num_seqs, blocks_per_seq, dst_per_seq, (uint32_t)max_len, budget, sinks, recent,
+                   (uintptr_t)scores % 16 == 0 && scores_stride % 4 == 0};
     const cudaStream_t s = as_stream(stream);
     const uint32_t rows = num_seqs * cache->heads;
     // Where there are fewer (sequence, head) pairs than SMs, blocks share one's
-    // tokens, kShare each at the least: 1 sequence of 131,071 tokens, 8 heads
-    // 111 us in one block each, 30 us in eight.  More blocks than SMs are slower
-    // (24 sequences of up to 40,000 tokens, 8 heads: 149 us, in clusters 159
-    // and more).
+    // tokens, kShare each at the least: 8 sequences of 16,000 tokens, 8 heads 43 us
+    // in one block each, 37 us in clusters of two; more blocks than SMs are slower
+    // (40 sequences of 20,000 tokens: 145 and 164 us).  Clusters of eight do not
+    // all fit at once above half the SMs (2 sequences of 20,000 tokens: 36 us, in
+    // fours 26) and want longer shares (1 sequence of 30,000 tokens, 8 heads: 18
+    // and 17; of 131,071 tokens: 27 and 30).
+    const uint32_t sms = (uint32_t)sm_count();
     uint32_t size = 1;
-    while (size < kMaxCluster && 2 * size * (uint64_t)rows <= (uint64_t)sm_count() &&
-           max_len >= 2 * size * (uint64_t)kShare)
-        size *= 2;
+    while (size < 4 && 2 * size * (uint64_t)rows <= sms && max_len >= 2 * size * (uint64_t)kShare) size *= 2;
+    if (size == 4 && 16 * (uint64_t)rows <= sms && max_len >= 32 * (uint64_t)kShare) size = kMaxCluster;
     const uint64_t each = ceil_div(max_len, 4 * size) * 4;
     const uint32_t held = each < kHeld ? (uint32_t)each : kHeld;
-    // 64 sequences of 4000 tokens, 8 heads: 99 us in blocks of 512 threads, 111
-    // in blocks of 1024; up to 40,000 tokens: 157 and 149.
-    if (!(size > 1            ? launch_select<1024, true>(a, rows, size, held, s)
-          : max_len <= kShort ? launch_select<512, false>(a, rows, 1, held, s)
-                              : launch_select<1024, false>(a, rows, 1, held, s)))
+    // Threads of a block: 512 and 1024 take 98 and 106 us for 64 sequences of 4000
+    // tokens, 8 heads, 67 and 71 for 32 of 8000, 227 and 190 for 32 of 16,000; 256
+    // where blocks of 512 would not fit at once: 128 sequences of 1000 tokens 40
+    // us, 512 threads 43, but 1 sequence of 1500 tokens 8.7 and 7.6.
+    if (!(size > 1                             ? launch_select<1024, true>(a, rows, size, held, s)
+          : max_len <= kTiny && rows > 3 * sms ? launch_select<256, false>(a, rows, 1, held, s)
+          : max_len <= kShort                  ? launch_select<512, false>(a, rows, 1, held, s)
+                                               : launch_select<1024, false>(a, rows, 1, held, s)))
         return KVX_ECUDA;
     KVX_LAUNCHED();
     cudaLaunchConfig_t cfg = {};

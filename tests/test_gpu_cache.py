@@ -514,11 +514,15 @@ EVICT = [  # store, heads, dim, page, lens, budget, sinks, recent, kind, token_m
     (FP, 2, 16, 64, [17000, 18001] + [9] * 40, 2000, 4, 100, "special", False),
     (FP, 1, 16, 64, [50001] + [10] * 80, 20000, 4, 100, "random", False),
     (FP, 1, 16, 64, [60000] + [70] * 80, 50, 50, 100, "ties", False),
+    # short and many, and of medium length
+    (FP, 2, 16, 16, [2000, 301, 0, 77, 1999] + [60] * 235, 50, 3, 11, "special", False),
+    (BF, 2, 64, 16, [8000, 7001] + [30] * 78, 1000, 3, 11, "ties", False),
 ]
 
 
+@pytest.mark.parametrize("pad", [1, 4])  # of a row of scores, which is then aligned or not
 @pytest.mark.parametrize("case", EVICT, ids=str)
-def test_evict(case):
+def test_evict(case, pad):
     store, H, D, page, lens, budget, sinks, recent, kind, token_major = case
     gen = torch.Generator().manual_seed(11)
     N = len(lens)
@@ -536,7 +540,7 @@ def test_evict(case):
         table[n, :m] = ids[at:at + m]
         at += m
     dst = ids[at:at + N * dper].view(N, dper)
-    sc = scores_of(kind, (N, H, per * page + 1), gen)
+    sc = scores_of(kind, (N, H, per * page + pad), gen)
     pool = host.cuda()
     cache = lay.cache(pool)
     kept = torch.empty(N, H, budget, dtype=torch.int32, device="cuda")
