@@ -125,7 +125,7 @@ __device__ __forceinline__ uint32_t word(const uint4 &v, int i) {
 
 // Shapes of the kernel for a stored type of ES bytes, heads padded to DP
 // values and NT * 8 query heads at a time.
-template <int DP, int ES, int NT>
+template <int DP, int ES, int NT, bool PAGED16>
 struct Shape {
     static constexpr int kHeads = 8 * NT;
     static constexpr int kKChunks = DP * ES / 64;                         // 64-byte parts of a K row
@@ -133,7 +133,14 @@ struct Shape {
     static constexpr int kVParts = DP * ES / 8 / kVBytes;
     static constexpr int kVElems = kVBytes / ES;
     static constexpr int kQVecs = kKChunks * (ES == 1 ? 2 : 1);           // 16-byte vectors of q per lane
-    static constexpr int kStage = 2 * 16 * DP * ES;                       // bytes of a warp's 16 keys, K and V
+    // Tiles of 16 keys that a warp takes together.  In 8 bits a tile's bytes are
+    // few beside its latencies, which two share: 8 heads of 64 values 118 us in
+    // tiles of their own, 103 in pairs (16,000 tokens x 16 KV heads x 16
+    // sequences); 16 heads of 128 125 and 110, of 256 81 and 75; but 8 heads of
+    // 128 89 and 91, their copies in each other's way.
+    static constexpr int kTiles = PAGED16 && ES == 1 && (DP == 64 || NT == 2) ? 2 : 1;
+    static constexpr int kTile = 2 * 16 * DP * ES;                        // bytes of a tile, K and V
+    static constexpr int kStage = kTiles * kTile;
     // Blocks that an SM has registers for.  Two stages a warp: with three to six
     // the copies in flight got in each other's way (16 query heads to a KV head,
     // 128 values: 104 us where two stages take 94; 8-bit, 8 heads: 98 and 93).
@@ -216,7 +223,7 @@ __device__ __forceinline__ void look_up(const Args &a, uint32_t per, uint32_t le
                                         uint4 *qbuf, const uint32_t *upto, uint64_t (*rows)[32], uint64_t (*ready)[2],
                                         uint64_t (*taken)[2], uint64_t *pfull, uint64_t *pempty, Piece *pieces,
                                         uint32_t &bad) {
-    using S = Shape<DP, ES, NT>;
+    using S = Shape<DP, ES, NT, PAGED16>;
     const uint32_t g = lane >> 2, t4 = lane & 3;
     const uint32_t units_per_head = (a.group + S::kHeads - 1) / S::kHeads;
     auto unit_len = [&](uint32_t keys) { return keys ? (keys + a.tile - 1) / a.tile + S::kExtra : 0; };
@@ -501,8 +508,8 @@ __device__ __forceinline__ void look_up(const Args &a, uint32_t per, uint32_t le
 // the tensor cores' would want them transposed and regrouped first, for 4 to 16
 // query heads that fill a fraction of it.
 template <class T, int DP, int ES, int NT, bool PAGED16>
-__global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_attend(const __grid_constant__ Args a) {
-    using S = Shape<DP, ES, NT>;
+__global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT, PAGED16>::kBlocks)) k_attend(const __grid_constant__ Args a) {
+    using S = Shape<DP, ES, NT, PAGED16>;
     // the type in which the products are taken: 8-bit values are exact in fp16
     using C = typename std::conditional<ES == 1, __half, T>::type;
     constexpr bool kConvertQ = !std::is_same<C, T>::value;
@@ -587,63 +594,70 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
     uint32_t buffers = 0, in_buffer = 0;  // buffers of rows used up, tiles of the present one taken
     const bool cover = a.c.row_bytes == DP * ES;
     const uint32_t stride = (uint32_t)a.c.token_stride;
-    // Takes the next tile's rows and copies this lane's pieces of them: where a
-    // row or a piece does not exist, zeros (a copy of no bytes reads nothing).
-    auto copy_tile = [&]() {
-        const uint8_t *row[6];
-        uint32_t there[6];
-        bool done = true;
-        if constexpr (PAGED16) {
-            const uint4 *from = reinterpret_cast<const uint4 *>(rows[warp]) + ((buffers & 1) * 4 + in_buffer) * 2;
-            const uint4 kr = from[0], vr = from[1];
-            const uint8_t *kp = reinterpret_cast<const uint8_t *>(((uint64_t)kr.y << 32 | kr.x) & ~1ull);
-            const uint8_t *vp = reinterpret_cast<const uint8_t *>(((uint64_t)vr.y << 32 | vr.x) & ~1ull);
-            row[0] = kp + (uint64_t)g * stride;
-            row[1] = row[0] + 8ull * stride;
-            row[2] = vp + 2ull * t4 * stride;
-            row[3] = row[2] + stride;
-            row[4] = row[2] + 8ull * stride;
-            row[5] = row[3] + 8ull * stride;
+    // Takes the next tiles' rows and copies this lane's pieces of them: where a
+    // row, a piece or the second tile does not exist, zeros (a copy of no bytes
+    // reads nothing).
+    auto copy_tiles = [&]() {
+        uint8_t *st = ring + copied % S::kStages * S::kStage;
+        bool done = false;
 #pragma unroll
-            for (int r = 0; r < 6; r++)
-                there[r] = r < 2 ? kr.z >> (g + 8 * r) & 1 : vr.z >> (2 * t4 + (r & 1) + 8 * ((r - 2) >> 1)) & 1;
-            done = kr.w;
-        } else {
-            const uint64_t *from = rows[warp];
-            const ulonglong2 v0 = *reinterpret_cast<const ulonglong2 *>(from + 16 + 2 * t4);
-            const ulonglong2 v1 = *reinterpret_cast<const ulonglong2 *>(from + 24 + 2 * t4);
-            const uint64_t at[6] = {from[g], from[g + 8], v0.x, v0.y, v1.x, v1.y};
+        for (int h = 0; h < S::kTiles; h++, st += S::kTile) {
+            const uint8_t *row[6];
+            uint32_t there[6];
+            const bool none = done;  // the buffer has no second tile
+            if constexpr (PAGED16) {
+                const uint4 *from = reinterpret_cast<const uint4 *>(rows[warp]) + ((buffers & 1) * 4 + in_buffer) * 2;
+                uint4 kr = make_uint4((uint32_t)(uintptr_t)a.c.pool, (uint32_t)((uintptr_t)a.c.pool >> 32), 0, 0), vr = kr;
+                if (!none) kr = from[0], vr = from[1];
+                const uint8_t *kp = reinterpret_cast<const uint8_t *>(((uint64_t)kr.y << 32 | kr.x) & ~1ull);
+                const uint8_t *vp = reinterpret_cast<const uint8_t *>(((uint64_t)vr.y << 32 | vr.x) & ~1ull);
+                row[0] = kp + (uint64_t)g * stride;
+                row[1] = row[0] + 8ull * stride;
+                row[2] = vp + 2ull * t4 * stride;
+                row[3] = row[2] + stride;
+                row[4] = row[2] + 8ull * stride;
+                row[5] = row[3] + 8ull * stride;
+#pragma unroll
+                for (int r = 0; r < 6; r++)
+                    there[r] = r < 2 ? kr.z >> (g + 8 * r) & 1 : vr.z >> (2 * t4 + (r & 1) + 8 * ((r - 2) >> 1)) & 1;
+                done = kr.w;
+            } else {
+                const uint64_t *from = rows[warp];
+                const ulonglong2 v0 = *reinterpret_cast<const ulonglong2 *>(from + 16 + 2 * t4);
+                const ulonglong2 v1 = *reinterpret_cast<const ulonglong2 *>(from + 24 + 2 * t4);
+                const uint64_t at[6] = {from[g], from[g + 8], v0.x, v0.y, v1.x, v1.y};
+#pragma unroll
+                for (int r = 0; r < 6; r++) {
+                    row[r] = reinterpret_cast<const uint8_t *>(at[r] & ~1ull);
+                    there[r] = ~(uint32_t)at[r] & 1;
+                }
+                done = true;
+            }
+            if (!none) in_buffer++;
+            if (done && !none) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&taken[warp][PAGED16 ? buffers & 1 : 0]);
+                buffers++;
+                in_buffer = 0;
+            }
+            done |= none;
+            const uint32_t kdst = smem_u32(st + lane * 16), vdst = smem_u32(st + S::kTile / 2 + vslot);
 #pragma unroll
             for (int r = 0; r < 6; r++) {
-                row[r] = reinterpret_cast<const uint8_t *>(at[r] & ~1ull);
-                there[r] = ~(uint32_t)at[r] & 1;
+                if (r < 2) {
+#pragma unroll
+                    for (int c = 0; c < S::kKChunks; c++)
+                        copy_async<16>(kdst + (c * 2 + r) * 512, row[r] + t4 * 16 + c * 64,
+                                       there[r] && (cover || c * 64 + t4 * 16 < a.c.row_bytes) ? 16 : 0);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < S::kVParts; c++)
+                        copy_async<S::kVBytes>(vdst + (c * 4 + r - 2) * 32 * S::kVBytes, row[r] + (c * 8 + g) * S::kVBytes,
+                                               there[r] && (cover || (c * 8 + g) * S::kVBytes < a.c.row_bytes) ? S::kVBytes : 0);
+                }
             }
         }
-        in_buffer++;
-        if (done) {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&taken[warp][PAGED16 ? buffers & 1 : 0]);
-            buffers++;
-            in_buffer = 0;
-        }
-        const uint32_t stage = copied % S::kStages;
-        uint8_t *st = ring + stage * S::kStage;
-        const uint32_t kdst = smem_u32(st + lane * 16), vdst = smem_u32(st + S::kStage / 2 + vslot);
-#pragma unroll
-        for (int r = 0; r < 6; r++) {
-            if (r < 2) {
-#pragma unroll
-                for (int c = 0; c < S::kKChunks; c++)
-                    copy_async<16>(kdst + (c * 2 + r) * 512, row[r] + t4 * 16 + c * 64,
-                                   there[r] && (cover || c * 64 + t4 * 16 < a.c.row_bytes) ? 16 : 0);
-            } else {
-#pragma unroll
-                for (int c = 0; c < S::kVParts; c++)
-                    copy_async<S::kVBytes>(vdst + (c * 4 + r - 2) * 32 * S::kVBytes, row[r] + (c * 8 + g) * S::kVBytes,
-                                           there[r] && (cover || (c * 8 + g) * S::kVBytes < a.c.row_bytes) ? S::kVBytes : 0);
-            }
-        }
-        mbar_arrive_copies(&full[warp][stage]);
+        mbar_arrive_copies(&full[warp][copied % S::kStages]);
         copied++;
     };
     // Whether the next tile's rows are there; the barrier is asked once a buffer.
@@ -728,74 +742,93 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
             logits = a.logits + ((uint64_t)pc.n * a.c.heads + pc.head) * a.logits_keys * gp + pc.qh0 + 2 * t4;
 
         bool ok = true;
-        for (uint32_t k = pc.k0 + warp * 16; k < pc.k1; k += kStep, tile++) {
+        for (uint32_t k = pc.k0 + warp * 16; k < pc.k1; k += S::kTiles * kStep, tile++) {
             if (copied == tile) {
                 const uint32_t parity = (PAGED16 ? buffers >> 1 : buffers) & 1;
                 if (!in_buffer && !mbar_wait(&ready[warp][PAGED16 ? buffers & 1 : 0], parity)) {
                     ok = false;
                     break;
                 }
-                copy_tile();
+                copy_tiles();
             }
             if (!S::kLate)
-                while (copied < tile + S::kStages && rows_there()) copy_tile();
+                while (copied < tile + S::kStages && rows_there()) copy_tiles();
             const uint32_t stage = tile % S::kStages;
             if (!mbar_wait(&full[warp][stage], tile / S::kStages & 1)) {
                 ok = false;
                 break;
             }
             if (S::kLate)
-                while (copied < tile + S::kStages && rows_there()) copy_tile();
+                while (copied < tile + S::kStages && rows_there()) copy_tiles();
             const uint8_t *st = ring + stage * S::kStage;
 
-            // S^T = K Q^T
-            float s[NT][4] = {}, s2[NT][4] = {};  // two chains of products
+            // S^T = K Q^T, in two chains of products at the least
+            constexpr int KT = S::kTiles;
+            float s[KT][NT][4] = {}, s2[NT][4] = {};
 #pragma unroll
             for (int c = 0; c < S::kKChunks; c++) {
-                const uint4 r0 = *reinterpret_cast<const uint4 *>(st + (c * 2) * 512 + lane * 16);
-                const uint4 r1 = *reinterpret_cast<const uint4 *>(st + (c * 2 + 1) * 512 + lane * 16);
+                uint4 r0[KT], r1[KT];
+#pragma unroll
+                for (int h = 0; h < KT; h++) {
+                    r0[h] = *reinterpret_cast<const uint4 *>(st + h * S::kTile + (c * 2) * 512 + lane * 16);
+                    r1[h] = *reinterpret_cast<const uint4 *>(st + h * S::kTile + (c * 2 + 1) * 512 + lane * 16);
+                }
                 if constexpr (ES == 2) {
 #pragma unroll
                     for (int x = 0; x < NT; x++) {
                         const uint4 qv = qs[(x * S::kQVecs + c) * 32 + lane];
-                        mma<C>(s[x], r0.x, r1.x, r0.y, r1.y, qv.x, qv.y);
-                        mma<C>(s2[x], r0.z, r1.z, r0.w, r1.w, qv.z, qv.w);
+#pragma unroll
+                        for (int h = 0; h < KT; h++) {
+                            mma<C>(s[h][x], r0[h].x, r1[h].x, r0[h].y, r1[h].y, qv.x, qv.y);
+                            mma<C>(KT > 1 ? s[h][x] : s2[x], r0[h].z, r1[h].z, r0[h].w, r1[h].w, qv.z, qv.w);
+                        }
                     }
                 } else {
 #pragma unroll
                     for (int w = 0; w < 4; w++) {
-                        const uint32_t w0 = word(r0, w), w1 = word(r1, w);
-                        const uint32_t a0 = e4m3_lo(w0), a1 = e4m3_lo(w1), a2 = e4m3_hi(w0), a3 = e4m3_hi(w1);
+                        uint32_t k0[KT], k1[KT], k2[KT], k3[KT];
+#pragma unroll
+                        for (int h = 0; h < KT; h++) {
+                            const uint32_t w0 = word(r0[h], w), w1 = word(r1[h], w);
+                            k0[h] = e4m3_lo(w0), k1[h] = e4m3_lo(w1), k2[h] = e4m3_hi(w0), k3[h] = e4m3_hi(w1);
+                        }
 #pragma unroll
                         for (int x = 0; x < NT; x++) {
                             const uint4 qv = qs[(x * S::kQVecs + c * 2 + w / 2) * 32 + lane];
-                            mma<C>(w % 2 ? s2[x] : s[x], a0, a1, a2, a3, w % 2 ? qv.z : qv.x, w % 2 ? qv.w : qv.y);
+#pragma unroll
+                            for (int h = 0; h < KT; h++)
+                                mma<C>(KT == 1 && w % 2 ? s2[x] : s[h][x], k0[h], k1[h], k2[h], k3[h], w % 2 ? qv.z : qv.x,
+                                       w % 2 ? qv.w : qv.y);
                         }
                     }
                 }
             }
 
             // logits in powers of two, masked beyond the last key
-            const uint32_t i0 = k + g, i1 = i0 + 8;
-            bool hide0 = i0 >= pc.k1, hide1 = i1 >= pc.k1;
-            if (PAGED16 && a.window) {
-                const uint32_t p0 = i0 < pc.turn ? i0 : i0 + pc.shift, p1 = p0 + 8;  // in one page
-                hide0 |= p0 >= pc.sinks && p0 < pc.recent;
-                hide1 |= p1 >= pc.sinks && p1 < pc.recent;
-            }
             bool higher = false;
 #pragma unroll
-            for (int x = 0; x < NT; x++) {
-#pragma unroll
-                for (int i = 0; i < 4; i++) {
-                    s[x][i] = (s[x][i] + s2[x][i]) * scale2[x][i & 1];
-                    if (i < 2 ? hide0 : hide1) s[x][i] = -INFINITY;
-                    higher |= s[x][i] > limit[x][i & 1];
+            for (int h = 0; h < KT; h++) {
+                const uint32_t i0 = k + h * kStep + g, i1 = i0 + 8;
+                bool hide0 = i0 >= pc.k1, hide1 = i1 >= pc.k1;
+                if (PAGED16 && a.window) {
+                    const uint32_t p0 = i0 < pc.turn ? i0 : i0 + pc.shift, p1 = p0 + 8;  // in one page
+                    hide0 |= p0 >= pc.sinks && p0 < pc.recent;
+                    hide1 |= p1 >= pc.sinks && p1 < pc.recent;
                 }
-                if (logits && x * 8 + 2 * t4 < pc.nheads) {
-                    float2 *to = reinterpret_cast<float2 *>(logits + x * 8 + (uint64_t)i0 * gp);
-                    if (i0 < pc.k1) to[0] = make_float2(s[x][0], s[x][1]);
-                    if (i1 < pc.k1) to[4 * gp] = make_float2(s[x][2], s[x][3]);
+#pragma unroll
+                for (int x = 0; x < NT; x++) {
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        if (KT == 1) s[h][x][i] += s2[x][i];
+                        s[h][x][i] *= scale2[x][i & 1];
+                        if (i < 2 ? hide0 : hide1) s[h][x][i] = -INFINITY;
+                        higher |= s[h][x][i] > limit[x][i & 1];
+                    }
+                    if (logits && x * 8 + 2 * t4 < pc.nheads) {
+                        float2 *to = reinterpret_cast<float2 *>(logits + x * 8 + (uint64_t)i0 * gp);
+                        if (i0 < pc.k1) to[0] = make_float2(s[h][x][0], s[h][x][1]);
+                        if (i1 < pc.k1) to[4 * gp] = make_float2(s[h][x][2], s[h][x][3]);
+                    }
                 }
             }
             if (__any_sync(0xFFFFFFFFu, higher)) {
@@ -804,7 +837,9 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
                 for (int x = 0; x < NT; x++)
 #pragma unroll
                     for (int i = 0; i < 2; i++) {
-                        float top = fmaxf(s[x][i], s[x][i + 2]);
+                        float top = fmaxf(s[0][x][i], s[0][x][i + 2]);
+#pragma unroll
+                        for (int h = 1; h < KT; h++) top = fmaxf(top, fmaxf(s[h][x][i], s[h][x][i + 2]));
 #pragma unroll
                         for (int k = 4; k < 32; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, k));
                         f[x][i] = 1.0f;
@@ -826,58 +861,63 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
             // P^T as the sum of two 16-bit values (2^-17 of the weight for
             // bf16): one alone would add an error of the size of the output's
             // own rounding
-            uint32_t ph[NT][2], pl[NT][2];
+            uint32_t ph[KT][NT][2], pl[KT][NT][2];
 #pragma unroll
-            for (int x = 0; x < NT; x++)
+            for (int h = 0; h < KT; h++)
 #pragma unroll
-                for (int r = 0; r < 2; r++) {
-                    const float p0 = exp2_fast(s[x][2 * r] - base[x][0]), p1 = exp2_fast(s[x][2 * r + 1] - base[x][1]);
-                    l[x][0] += p0;
-                    l[x][1] += p1;
-                    const uint32_t hi = Pair<C>::pack(p0, p1);
-                    const float2 h = Pair<C>::unpack(hi);
-                    ph[x][r] = transpose8(hi);
-                    pl[x][r] = transpose8(Pair<C>::pack(p0 - h.x, p1 - h.y));
-                }
+                for (int x = 0; x < NT; x++)
+#pragma unroll
+                    for (int r = 0; r < 2; r++) {
+                        const float p0 = exp2_fast(s[h][x][2 * r] - base[x][0]), p1 = exp2_fast(s[h][x][2 * r + 1] - base[x][1]);
+                        l[x][0] += p0;
+                        l[x][1] += p1;
+                        const uint32_t hi = Pair<C>::pack(p0, p1);
+                        const float2 f = Pair<C>::unpack(hi);
+                        ph[h][x][r] = transpose8(hi);
+                        pl[h][x][r] = transpose8(Pair<C>::pack(p0 - f.x, p1 - f.y));
+                    }
 
             // O^T += V^T P^T
-            const uint8_t *sv = st + S::kStage / 2 + vslot;
 #pragma unroll
-            for (int c = 0; c < S::kVParts; c++) {
-                uint32_t v[4][S::kVBytes / 4];
+            for (int h = 0; h < KT; h++) {
+                const uint8_t *sv = st + h * S::kTile + S::kTile / 2 + vslot;
 #pragma unroll
-                for (int r = 0; r < 4; r++) {
-                    if constexpr (S::kVBytes == 16) {
-                        const uint4 x = *reinterpret_cast<const uint4 *>(sv + (c * 4 + r) * 512);
-                        v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
-                    } else {
-                        const uint2 x = *reinterpret_cast<const uint2 *>(sv + (c * 4 + r) * 256);
-                        v[r][0] = x.x, v[r][1] = x.y;
-                    }
-                }
+                for (int c = 0; c < S::kVParts; c++) {
+                    uint32_t v[4][S::kVBytes / 4];
 #pragma unroll
-                for (int w = 0; w < S::kVBytes / 4; w++) {
-                    if constexpr (ES == 2) {
-                        const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410);
-                        const uint32_t a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
-                        const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410);
-                        const uint32_t a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
-#pragma unroll
-                        for (int x = 0; x < NT; x++) {
-                            mma<C>(o[c * 4 + w][x], a0, a1, a2, a3, ph[x][0], ph[x][1]);
-                            mma<C>(o[c * 4 + w][x], a0, a1, a2, a3, pl[x][0], pl[x][1]);
+                    for (int r = 0; r < 4; r++) {
+                        if constexpr (S::kVBytes == 16) {
+                            const uint4 x = *reinterpret_cast<const uint4 *>(sv + (c * 4 + r) * 512);
+                            v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
+                        } else {
+                            const uint2 x = *reinterpret_cast<const uint2 *>(sv + (c * 4 + r) * 256);
+                            v[r][0] = x.x, v[r][1] = x.y;
                         }
-                    } else {
+                    }
 #pragma unroll
-                        for (int y = 0; y < 2; y++) {
-                            const uint32_t e = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
-                            const uint32_t f = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
-                            const uint32_t a0 = e4m3_lo(e), a1 = e4m3_hi(e), a2 = e4m3_lo(f), a3 = e4m3_hi(f);
-                            constexpr int per = S::kVBytes / 2;  // output tiles of a part
+                    for (int w = 0; w < S::kVBytes / 4; w++) {
+                        if constexpr (ES == 2) {
+                            const uint32_t a0 = __byte_perm(v[0][w], v[1][w], 0x5410);
+                            const uint32_t a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
+                            const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410);
+                            const uint32_t a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
 #pragma unroll
                             for (int x = 0; x < NT; x++) {
-                                mma<C>(o[c * per + 2 * w + y][x], a0, a1, a2, a3, ph[x][0], ph[x][1]);
-                                mma<C>(o[c * per + 2 * w + y][x], a0, a1, a2, a3, pl[x][0], pl[x][1]);
+                                mma<C>(o[c * 4 + w][x], a0, a1, a2, a3, ph[h][x][0], ph[h][x][1]);
+                                mma<C>(o[c * 4 + w][x], a0, a1, a2, a3, pl[h][x][0], pl[h][x][1]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int y = 0; y < 2; y++) {
+                                const uint32_t e = __byte_perm(v[0][w], v[1][w], y ? 0x7362 : 0x5140);
+                                const uint32_t f = __byte_perm(v[2][w], v[3][w], y ? 0x7362 : 0x5140);
+                                const uint32_t a0 = e4m3_lo(e), a1 = e4m3_hi(e), a2 = e4m3_lo(f), a3 = e4m3_hi(f);
+                                constexpr int per = S::kVBytes / 2;  // output tiles of a part
+#pragma unroll
+                                for (int x = 0; x < NT; x++) {
+                                    mma<C>(o[c * per + 2 * w + y][x], a0, a1, a2, a3, ph[h][x][0], ph[h][x][1]);
+                                    mma<C>(o[c * per + 2 * w + y][x], a0, a1, a2, a3, pl[h][x][0], pl[h][x][1]);
+                                }
                             }
                         }
                     }
@@ -997,7 +1037,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT>::kBlocks)) k_atte
 // a.grid; false where that failed.
 template <class T, int DP, int ES, int NT, bool PAGED16>
 bool launch_kernel(Args &a, uint64_t most, cudaStream_t s) {
-    using S = Shape<DP, ES, NT>;
+    using S = Shape<DP, ES, NT, PAGED16>;
     static bool done[64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;

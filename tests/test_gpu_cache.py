@@ -199,6 +199,10 @@ ATTEND = [  # act, store, q_heads, heads, dim, page, window, sinks, scores, toke
     (FP, FP, 11, 1, 208, 24, 100, 33, True, True, LENS),
     (BF, E4, 26, 2, 224, 5, 0, 0, False, False, LENS),
     (BF, E4, 16, 1, 256, 16, 0, 0, True, False, [9000, 0, 5]),
+    (BF, E4, 4, 1, 64, 16, 0, 0, True, False, LENS),
+    (FP, E4, 8, 2, 48, 32, 70, 5, True, True, LENS),
+    (BF, E4, 12, 1, 128, 16, 100, 33, True, False, LENS),
+    (FP, E4, 9, 1, 64, 48, 0, 0, False, False, [5000, 0, 33, 700]),
 ]
 
 
