@@ -27,7 +27,8 @@ constexpr uint32_t kMaxGroup = 128;
 constexpr int kJoinWarps = 8;
 constexpr int kJoinUnroll = 4;  // parts whose loads a warp has in flight
 constexpr int kScoreThreads = 128;
-constexpr uint32_t kScoreKeys = 4 * kScoreThreads;  // of a block that adds weights
+constexpr int kScoreUnroll = 8;  // keys of a thread
+constexpr uint32_t kScoreKeys = kScoreUnroll * kScoreThreads;  // of a block that adds weights
 
 // Block c joins the query heads of the unit whose first part block c of
 // k_attend did; its other parts are the first ones of blocks c+1 .. last.  The
@@ -113,44 +114,49 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
     }
 }
 
-// Adds the weights of kScoreKeys keys of a KV head, four keys a thread.  Bound
-// by HBM, logits in and scores in and out: 32 sequences of up to 6001 tokens, 8
-// heads of 5 query heads, about 7 us.
+// Adds the weights of kScoreKeys keys of a KV head.  Bound by HBM, logits in and
+// scores in and out, and by the chain of their loads: 16 sequences of 16,000
+// tokens, 4 heads of 5 query heads, take 101 us with weights and 85 without (with
+// four keys a thread in place of eight 103).
 __global__ void __launch_bounds__(kScoreThreads) k_scores(const __grid_constant__ Args a, uint32_t chunks) {
     __shared__ float sh_lse[kMaxGroup];
     const uint32_t row = blockIdx.x / chunks, n = row / a.c.heads, head = row % a.c.heads;
     const uint32_t i0 = blockIdx.x % chunks * kScoreKeys + threadIdx.x;
     const Seen sv = seen(a, a.lens[n]);
-    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const uint32_t gp = (a.group + 1) & ~1u;
+    float *to = a.scores + (uint64_t)row * a.scores_stride;
+    const float2 *x[kScoreUnroll];  // the keys' logits, two query heads a load
+    float old[kScoreUnroll], w[kScoreUnroll] = {};
     if (i0 - threadIdx.x >= sv.n) return;
-    for (uint32_t i = threadIdx.x; i < a.group; i += kScoreThreads) {
-        const float lse2 = __ldcg(a.lse2 + (uint64_t)n * a.q_heads + head * a.group + i);
+#pragma unroll
+    for (int u = 0; u < kScoreUnroll; u++) {
+        const uint32_t i = i0 + u * kScoreThreads < sv.n ? i0 + u * kScoreThreads : sv.n - 1;
+        x[u] = reinterpret_cast<const float2 *>(a.logits + ((uint64_t)row * a.logits_keys + i) * gp);
+        old[u] = to[sv.token(i)];  // (of earlier calls: nothing that runs now writes it)
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    float2 next[kScoreUnroll];
+#pragma unroll
+    for (int u = 0; u < kScoreUnroll; u++) next[u] = x[u][0];
+    for (uint32_t i = threadIdx.x; i < gp; i += kScoreThreads) {
+        const float lse2 = i < a.group ? a.lse2[(uint64_t)n * a.q_heads + head * a.group + i] : -INFINITY;
         sh_lse[i] = lse2 == -INFINITY ? INFINITY : lse2;  // no finite logit, no weight: 2^(-inf - inf) = 0
     }
     __syncthreads();
-    const uint32_t gp = (a.group + 1) & ~1u;
-    const float2 *x = reinterpret_cast<const float2 *>(a.logits + ((uint64_t)row * a.logits_keys + i0) * gp);
-    float *to = a.scores + (uint64_t)row * a.scores_stride;
-    float old[4], w[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int u = 0; u < 4; u++) {
-        const uint32_t i = i0 + u * kScoreThreads;
-        old[u] = i < sv.n ? to[sv.token(i)] : 0;
-    }
     for (uint32_t k = 0; k < a.group; k += 2) {
-        const float l0 = sh_lse[k], l1 = k + 1 < a.group ? sh_lse[k + 1] : INFINITY;
+        const float l0 = sh_lse[k], l1 = sh_lse[k + 1];
+        const bool both = k + 1 < a.group;
 #pragma unroll
-        for (int u = 0; u < 4; u++) {
-            if (i0 + u * kScoreThreads >= sv.n) continue;
-            const float2 v = __ldcg(x + (uint64_t)u * kScoreThreads * (gp / 2) + k / 2);
+        for (int u = 0; u < kScoreUnroll; u++) {
+            const float2 v = next[u];
+            if (k + 2 < a.group) next[u] = x[u][k / 2 + 1];
             w[u] += exp2f(v.x - l0);
-            if (k + 1 < a.group) w[u] += exp2f(v.y - l1);
+            if (both) w[u] += exp2f(v.y - l1);
         }
     }
 #pragma unroll
-    for (int u = 0; u < 4; u++) {
-        const uint32_t i = i0 + u * kScoreThreads;
-        const uint32_t pos = sv.token(i);
+    for (int u = 0; u < kScoreUnroll; u++) {
+        const uint32_t i = i0 + u * kScoreThreads, pos = sv.token(i);
         if (i < sv.n && (pos < sv.sinks || pos >= sv.recent)) to[pos] = old[u] + w[u];
     }
 }
