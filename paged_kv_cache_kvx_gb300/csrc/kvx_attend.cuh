@@ -14,7 +14,7 @@ constexpr int kWarps = 4;                       // that copy and compute; one mo
 constexpr int kThreads = 32 * (kWarps + 1);
 constexpr uint32_t kStep = 16 * kWarps;         // keys of a block's step, and of a tile in which work is shared out
 constexpr uint32_t kWhole = 256;                // keys up to which no unit is split
-constexpr uint32_t kMaxExtra = 8;               // Shape::kExtra at the most
+constexpr uint32_t kMaxExtra = 6;               // Shape::kExtra at the most
 constexpr uint32_t kFew = 32;                   // sequences that the looking-up warp counts by itself
 constexpr uint32_t kMaxBlocks = 512;            // bounds the partial results in the workspace
 constexpr int kPieces = 8;                      // descriptors that the looking-up warp may be ahead
@@ -147,8 +147,9 @@ struct Shape {
     static constexpr int kBlocks = DP == 256 ? (ES == 1 && NT == 1 ? 2 : 1) : NT == 2 && DP == 128 ? 2 : 3;
     static constexpr int kStages = 2;
     // What a unit costs beside its keys (its query, its output) counts as so
-    // many tiles when work is shared out: about 64 KB of copies.
-    static constexpr uint32_t kExtra = DP * ES >= 512 ? 1 : 512 / (DP * ES);
+    // many tiles when work is shared out: about 48 KB of copies (96 sequences up
+    // to 8192 tokens, 8-bit: 60 us with 32 KB, 56 with 48, 57 with 64, 60 with 96).
+    static constexpr uint32_t kExtra = DP * ES >= 384 ? 1 : 384 / (DP * ES);
     static_assert(kExtra <= kMaxExtra);
     static constexpr int kRing = kWarps * kStages * kStage;
     // Where the rings of an SM hold more than 160 KB (16-bit, 128 values, three
