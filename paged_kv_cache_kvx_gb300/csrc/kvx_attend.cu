@@ -30,10 +30,11 @@ constexpr int kScoreThreads = 128;
 constexpr int kScoreUnroll = 8;  // keys of a thread
 constexpr uint32_t kScoreKeys = kScoreUnroll * kScoreThreads;  // of a block that adds weights
 
-// Block c joins the query heads of the unit whose first part block c of
+// Blocks (c, ..) join the query heads of the unit whose first part block c of
 // k_attend did; its other parts are the first ones of blocks c+1 .. last.  The
 // warps are dealt out to the heads, and those of a head to its parts.  Bound by
-// a chain of three loads: about 4 us behind k_attend, whatever the sizes; blocks
+// a chain of three loads, about 4 us behind k_attend, and rounds of them where a
+// unit has more parts than its blocks have loads in flight for; blocks
 // of sixteen warps with eight parts in flight did not fit on the SMs together
 // and took 3 us more.
 template <class T>
@@ -42,20 +43,22 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
     __shared__ float sh_m[kJoinWarps], sh_l[kJoinWarps];
     __shared__ float4 sh_o[kJoinWarps][32];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t heads = a.group < unit_heads ? a.group : unit_heads;
-    const uint32_t deal = heads < kJoinWarps ? kJoinWarps / heads : 1, turn = warp % deal;
+    const uint32_t all = a.group < unit_heads ? a.group : unit_heads, each = (all + gridDim.y - 1) / gridDim.y;
+    const uint32_t first = blockIdx.y * each;  // this block's heads
+    const uint32_t heads = first + each < all ? each : all > first ? all - first : 0;
+    const uint32_t deal = heads < kJoinWarps && heads ? kJoinWarps / heads : 1, turn = warp % deal;
     const uint32_t per_head = (a.group + unit_heads - 1) / unit_heads;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint4 cut = __ldcg(a.cut + blockIdx.x);
-    if (cut.x == kNone) return;
+    if (cut.x == kNone || !heads) return;
     const uint32_t n = cut.x, parts = cut.z - blockIdx.x + 1;
     // Four of 128 values a lane, one head after the other where there are more
     // heads than warps; every warp makes the same turns.
     for (uint32_t h0 = 0, d0 = 0; h0 < heads; d0 += 128, h0 += d0 < dp ? 0 : kJoinWarps / deal, d0 = d0 < dp ? d0 : 0) {
-        const uint32_t d = d0 + lane * 4, hh = h0 + warp / deal;
+        const uint32_t d = d0 + lane * 4, hh = first + h0 + warp / deal;
         const uint32_t in = cut.y % per_head * unit_heads + hh, qh = cut.y / per_head * a.group + in;
-        const bool has = hh < heads && in < a.group;
+        const bool has = hh < first + heads && in < a.group;
         auto slot = [&](uint32_t i) { return (uint64_t)(i ? 2 * (blockIdx.x + i) : cut.w) * unit_heads + hh; };
         float4 v = make_float4(0, 0, 0, 0);
         float top = -INFINITY, sum = 0;
@@ -269,7 +272,15 @@ extern "C" kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     if (p.split) {
-        cfg.gridDim = dim3(a.grid);
+        // A cut unit's heads go to several blocks where it has more parts than
+        // one block has loads in flight for: 1 sequence of 16,000 tokens, 32
+        // query heads to its KV head 45 us in one, 21 in six; 8 sequences, 4
+        // heads, 85.3 in one, 85.9 in two, as blocks without a cut cost too.
+        const uint64_t heads = a.group < p.unit_heads ? a.group : p.unit_heads;
+        const uint64_t parts = ceil_div(a.grid, (uint64_t)num_seqs * p.units) * heads;
+        const uint64_t want = ceil_div(parts, kJoinWarps * kJoinUnroll), fit = 12ull * sm_count() / a.grid;
+        const uint64_t y = want < heads ? want : heads;
+        cfg.gridDim = dim3(a.grid, (uint32_t)(y < fit ? y : fit ? fit : 1));
         cfg.blockDim = dim3(32 * kJoinWarps);
         const cudaError_t e = dtype == KVX_BF16 ? cudaLaunchKernelEx(&cfg, k_join<__nv_bfloat16>, a, p.dp, p.unit_heads)
                                                 : cudaLaunchKernelEx(&cfg, k_join<__half>, a, p.dp, p.unit_heads);
