@@ -641,8 +641,8 @@ size_t kvx_attend_workspace_size(const kvx_cache *cache, uint32_t num_seqs,
  *                  128 per KV head.
  *   blocks         [num_seqs][blocks_per_seq] uint32; blocks_per_seq *
  *                  page_tokens < 2^31, and heads * num_seqs times that at most
- *                  about 2^37 in all (else KVX_EINVAL).  Entries of pages that hold no visible
- *                  token are not read.
+ *                  about 2^37 in all (else KVX_EINVAL).  Entries of pages
+ *                  that hold no visible token are not read.
  *   lens           [num_seqs] uint32; one that exceeds its pages raises
  *                  KVX_S_BOUNDS and counts as full pages.
  *   out            [num_seqs][q_heads][dim] of `dtype`, out_stride apart.

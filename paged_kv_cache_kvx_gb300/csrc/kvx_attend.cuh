@@ -141,9 +141,9 @@ struct Shape {
     static constexpr int kTiles = PAGED16 && ES == 1 && (DP == 64 || NT == 2) ? 2 : 1;
     static constexpr int kTile = 2 * 16 * DP * ES;                        // bytes of a tile, K and V
     static constexpr int kStage = kTiles * kTile;
-    // Blocks that an SM has registers for.  Two stages a warp: with three to six
-    // the copies in flight got in each other's way (16 query heads to a KV head,
-    // 128 values: 104 us where two stages take 94; 8-bit, 8 heads: 98 and 93).
+    // Blocks that an SM has registers for.  Two stages a warp: with more the
+    // copies in flight got in each other's way (8-bit, 8 heads of 128: 94 us with
+    // three, 96 with four, 89 with two; 16-bit, 8 heads of 64: 90, 91 and 87).
     static constexpr int kBlocks = DP == 256 ? (ES == 1 && NT == 1 ? 2 : 1) : NT == 2 && DP == 128 ? 2 : 3;
     static constexpr int kStages = 2;
     // What a unit costs beside its keys (its query, its output) counts as so
@@ -154,8 +154,9 @@ struct Shape {
     static constexpr int kRing = kWarps * kStages * kStage;
     // Where the rings of an SM hold more than 160 KB (16-bit, 128 values, three
     // blocks) the next tile's copies go out when the present one's have
-    // arrived: 86 us against 88 at once (16,000 tokens x 8 heads x 8
-    // sequences); smaller rings want both on their way (8-bit: 92 us and 96).
+    // arrived: 85 us against 88 at once (16,000 tokens x 8 heads x 8
+    // sequences); smaller rings want both on their way (16 heads of 64: 95 us
+    // against 99 for 16,000 tokens x 8 KV heads x 8 sequences).
     static constexpr bool kLate = kRing * kBlocks > 160 * 1024;
     static constexpr int kQ = NT * kQVecs * 32 * 16;
     static constexpr int kJoin = (DP / 16 + 1) * NT * 32 * 16;
@@ -502,9 +503,9 @@ __device__ __forceinline__ void look_up(const Args &a, uint32_t per, uint32_t le
 // warp waits for a slower one before it goes on to the next piece.
 //
 // Bound by HBM: per key 2*DP*ES bytes for 4*group*DP operations.  One sequence
-// of 131,071 tokens, 8 KV heads of 128 values, bf16: 86 us at 6.3 TB/s (7.1
-// between the first and the last copy) with 13 % of the tensor pipe's cycles
-// in use; 8-bit with 8 query heads to a KV head: 22 %.  So mma.sync suffices:
+// of 131,071 tokens, 8 KV heads of 128 values, bf16: 85 us at 6.3 TB/s (7.1
+// between the first and the last copy) with 12 % of the tensor pipe's cycles
+// in use; 8-bit with 8 query heads to a KV head: 20 %.  So mma.sync suffices:
 // its operands come to registers from rows as they lie, where a larger tile of
 // the tensor cores' would want them transposed and regrouped first, for 4 to 16
 // query heads that fill a fraction of it.
