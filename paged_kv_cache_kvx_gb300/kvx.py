@@ -87,7 +87,7 @@ _SIGS = {
     "kvx_attend_workspace_size": (_SZ, [_P, _U32, _U32, _U32, _U32, _U32, _U32]),
     "kvx_attend": (ctypes.c_int, [_P] * 9 + [_F] + [_P] * 11),
     "kvx_evict_workspace_size": (_SZ, [_P, _U32, _U32, _U32]),
-    "kvx_evict": (ctypes.c_int, [_P] * 18),
+    "kvx_evict": (ctypes.c_int, [_P] * 19),
     "kvx_selftest_timeouts": (ctypes.c_int, [_P, _P]),
     "kvx_launch_count": (_U64, []),
     "kvx_version": (_U32, []),

@@ -155,3 +155,22 @@ def test_prepared_copies_reject_bad_arguments():
 def test_noalloc_pack_rejects_slabs_beyond_its_scratch():
     L = _lib()
     assert L.kvx_pack_noalloc(P, 1 << 40, P, P, 10, P, 1 << 34, P, None) == ECAPACITY
+
+
+def test_binding_declares_every_parameter():
+    """ctypes passes an argument beyond the declared ones as a 32-bit int, which cuts a stream's handle in half: each
+    entry point's argtypes are as many as its prototype has parameters, floats for floats and nothing narrower."""
+    import ctypes
+    from paged_kv_cache_kvx_gb300 import kvx
+    src = open(os.path.join(ROOT, "include", "kvx.h")).read()
+    src = re.sub(r"/\*.*?\*/", "", src, flags=re.S)
+    takes = {name: [] if args.strip() == "void" else [" ".join(a.split()) for a in args.split(",")]
+             for name, args in re.findall(r"\b(kvx_[a-z_0-9]+)\s*\(([^()]*)\)\s*;", src)}
+    assert sorted(takes) == _declared()
+    for name, (_, args) in kvx._SIGS.items():
+        assert len(args) == len(takes[name]), name
+        for ctype, param in zip(args, takes[name]):
+            is_float = param.startswith("float ") and "*" not in param
+            wide = "*" in param or param.startswith(("uint64_t", "int64_t", "size_t"))
+            assert (ctype is ctypes.c_float) == is_float, (name, param)
+            assert ctypes.sizeof(ctype) >= (8 if wide else 4), (name, param)

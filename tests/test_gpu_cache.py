@@ -599,6 +599,91 @@ def test_evict_bad_pages():
         assert cache.read_status() == bit, fault
 
 
+def small_evict(lens=(300, 7, 100), budget=48, H=2, seed=9):
+    """A cache, its eviction's arguments on the GPU with fresh outputs, and scores by which heads keep different tokens."""
+    gen = torch.Generator().manual_seed(seed)
+    N, page, D = len(lens), 16, 64
+    per, dper = -(-max(lens) // page), -(-budget // page)
+    lay = R.Layout(N * (per + dper), H, D, page, BF, seed)
+    k, v = (R.randn((lay.blocks, H, page, D), BF, gen) for _ in range(2))
+    pool = lay.pool(k, v).cuda()
+    ids = torch.randperm(lay.blocks, generator=gen).int()
+    table, dst = ids[:N * per].view(N, per), ids[N * per:].view(N, dper)
+    a = dict(blocks=table.cuda(), lens=torch.tensor(lens, dtype=torch.int32).cuda(),
+             scores=scores_of("random", (N, H, per * page), gen).cuda(), dst_blocks=dst.cuda(),
+             kept=torch.full((N, H, budget), -7, dtype=torch.int32, device="cuda"),
+             kept_scores=torch.full((N, H, budget), -7.0, device="cuda"),
+             new_lens=torch.full((N,), -7, dtype=torch.int32, device="cuda"), sinks=4, recent=8)
+    cache = lay.cache(pool)
+    a["ws"] = cache.evict_workspace(N, per, budget)
+    return lay, cache, pool, k, v, a
+
+
+def check_evict(lay, cache, pool, k, v, a, lens):
+    """What an eviction of small_evict's has left, for the lengths that it was called with."""
+    assert cache.read_status() == 0
+    budget, host = a["kept"].shape[2], pool.cpu()
+    got_k, got_v = lay.values(host)
+    assert a["new_lens"].tolist() == [min(n, budget) for n in lens]
+    for n, length in enumerate(lens):
+        for h in range(lay.heads):
+            pos = R.evict_positions(a["scores"][n, h].tolist(), length, budget, a["sinks"], a["recent"])
+            assert a["kept"][n, h].tolist() == pos + [-1] * (budget - len(pos)), (n, h)
+            assert torch.equal(a["kept_scores"][n, h, :len(pos)], a["scores"][n, h, pos])
+            for r, p in enumerate(pos):
+                s, d = a["blocks"][n, p // lay.page].item(), a["dst_blocks"][n, r // lay.page].item()
+                assert torch.equal(got_k[d, h, r % lay.page], k[s, h, p % lay.page])
+                assert torch.equal(got_v[d, h, r % lay.page], v[s, h, p % lay.page])
+
+
+@pytest.mark.parametrize("how", ["current", "argument"])
+def test_append_and_evict_on_a_side_stream(how):
+    """Both run behind what their stream does first: inputs that are filled there, after a while."""
+    s = torch.cuda.Stream()
+    lay, cache, pool, k, v, a = small_evict()
+    scores = a["scores"].clone()
+    a["scores"].zero_()
+    T = 5
+    ka = torch.zeros(T, lay.heads, lay.dim, dtype=BF, device="cuda")
+    qa, kb = torch.ones_like(ka), R.randn((T, lay.heads, lay.dim), BF, torch.Generator().manual_seed(2)).cuda()
+    slots = a["blocks"][0, 0].long() * lay.page + torch.arange(T, device="cuda")
+    out = torch.zeros_like(qa)
+    busy = torch.empty(1 << 28, device="cuda")
+    torch.cuda.synchronize()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(8):
+            busy.fill_(1.0)
+        a["scores"].copy_(scores)
+        ka.copy_(kb)
+    arg = dict(stream=s) if how == "argument" else {}
+    with torch.cuda.stream(s if how == "current" else torch.cuda.current_stream()):
+        cache.append(qa, ka, ka, None, slots, out, **arg)
+        cache.evict(**a, **arg)
+    torch.cuda.synchronize()
+    b = a["blocks"][0, 0].item()
+    k[b, :, :T] = v[b, :, :T] = kb.transpose(0, 1).cpu()
+    assert torch.equal(out, qa)
+    check_evict(lay, cache, pool, k, v, a, [300, 7, 100])
+
+
+def test_evict_in_a_graph_follows_new_lengths():
+    lay, cache, pool, k, v, a = small_evict()
+    cache.evict(**a)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.evict(**a)
+    for now in ([300, 7, 100], [48, 49, 304], [0, 1, 250]):
+        a["lens"].copy_(torch.tensor(now, dtype=torch.int32))
+        for x in ("kept", "kept_scores", "new_lens"):
+            a[x].fill_(-7)
+        a["scores"].copy_(a["scores"].roll(1, 2))
+        graph.replay()
+        torch.cuda.synchronize()
+        check_evict(lay, cache, pool, k, v, a, now)
+
+
 # ------------------------------------------------------------------ together
 
 def test_decoding_on_a_transferred_prefix():
