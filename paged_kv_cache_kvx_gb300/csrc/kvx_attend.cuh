@@ -525,7 +525,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT, PAGED16>::kBlocks
     __shared__ __align__(16) uint64_t rows[kWarps][32];
     __shared__ uint64_t ready[kWarps][2], taken[kWarps][2];
     __shared__ uint64_t pfull[kPieces], pempty[kPieces];                      // pieces
-    __shared__ uint64_t passed[kWarps], joined, converted[2];
+    __shared__ uint64_t passed[kWarps], converted[2];
+    __shared__ uint64_t joined[kPieces];  // the first warp has the piece's results: the join buffer is free again
     __shared__ Piece pieces[kPieces];
     __shared__ float sh_qscale[2][S::kHeads];  // power of two taken out of a head's query
 
@@ -568,8 +569,8 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT, PAGED16>::kBlocks
             for (int i = 0; i < kPieces; i++) {
                 mbar_init(&pfull[i], 33);
                 mbar_init(&pempty[i], kWarps);
+                mbar_init(&joined[i], 1);
             }
-            mbar_init(&joined, 1);
             mbar_init(&converted[0], NT);
             mbar_init(&converted[1], NT);
         }
@@ -668,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT, PAGED16>::kBlocks
         return in_buffer || __all_sync(0xFFFFFFFFu, mbar_test(&ready[warp][PAGED16 ? buffers & 1 : 0], parity));
     };
     float4 *join = reinterpret_cast<float4 *>(smem + S::kRing + S::kQBufs * S::kQ) + lane;
-    uint32_t tile = 0, joins = 0, passes = 0;  // tiles taken, pieces joined, and results taken over so far
+    uint32_t tile = 0, passes = 0;  // tiles taken, and results taken over so far
     for (uint32_t p = 0;; p++) {
         if (!mbar_wait(&pfull[p % kPieces], p / kPieces & 1)) break;
         const Piece pc = pieces[p % kPieces];
@@ -931,10 +932,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT, PAGED16>::kBlocks
 
         // ---- the warps' results: each adds its own to the next one's
         const uint32_t active = pc.k1 - pc.k0 < kStep ? (pc.k1 - pc.k0 + 15) / 16 : kWarps;
-        if (warp >= active) {
-            joins += active > 1;
-            continue;
-        }
+        if (warp >= active) continue;
         float m[NT][2];
 #pragma unroll
         for (int x = 0; x < NT; x++)
@@ -967,10 +965,16 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT, PAGED16>::kBlocks
                     o[k][x][3] = o[k][x][3] * f[1] + v.w * fj[1];
                 }
             }
-        } else if (active > 1 && joins) {  // the first to write: the last piece's results have been read
-            if (!mbar_wait(&joined, joins - 1 & 1)) break;
+        } else if (active > 1 && p) {
+            // The first to write: the last piece's results have been read.  A
+            // barrier for each place of `pieces`, for warps without keys pass a
+            // piece by and may be two ahead of the first one, or behind it: a
+            // single barrier's parity would stand for two phases.  Of one place
+            // the last phase but this is over, as the first warp has handed
+            // back the descriptor that was here before this piece's, and the
+            // next one is after this piece.
+            if (!mbar_wait(&joined[(p - 1) % kPieces], (p - 1) / kPieces & 1)) break;
         }
-        joins += active > 1;
         if (warp > 0) {
 #pragma unroll
             for (int x = 0; x < NT; x++) {
@@ -984,7 +988,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT, PAGED16>::kBlocks
             continue;
         }
         __syncwarp();
-        if (lane == 0 && active > 1) mbar_arrive(&joined);
+        if (lane == 0) mbar_arrive(&joined[p % kPieces]);
 
         // ---- the unit's output, or its part for k_join
 #pragma unroll

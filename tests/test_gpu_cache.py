@@ -292,6 +292,17 @@ def test_attend_many_short_sequences(page):
     run_attend((FP, E4, 2, 1, 128, page, 9, 2, False, True, lens))
 
 
+@pytest.mark.parametrize("kind", [(BF, BF, 2, 1, 128), (FP, FP, 16, 1, 64), (FP, E4, 2, 1, 128), (BF, E4, 9, 1, 64),
+                                  (BF, BF, 3, 1, 256)], ids=str)
+def test_attend_units_that_some_warps_pass_by(kind):
+    """Units of four warps' keys beside some of one to three warps', many to a block: the warps without keys are ahead
+    of the others, whose results pass through one buffer."""
+    rng = np.random.default_rng(4)
+    lens = np.where(rng.random(2600) < 0.5, rng.integers(49, 130, 2600), rng.integers(1, 49, 2600))
+    lens[::3], lens[1::3] = np.maximum(lens[::3], 49), np.minimum(lens[1::3], 48)
+    run_attend((*kind, 16, 0, 0, False, False, lens.tolist()))
+
+
 def test_attend_without_pages_or_sequences():
     lay = R.Layout(2, 2, 64, 16, BF, 1)
     cache = lay.cache(torch.zeros(lay.pool_bytes, dtype=torch.uint8, device="cuda"))
