@@ -51,7 +51,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const uint4 cut = __ldcg(a.cut + blockIdx.x);
-    if (cut.x == kNone || !heads) return;
+    if (!joinable(cut, blockIdx.x, a.num_seqs, a.units, a.grid) || !heads) return;
     const uint32_t n = cut.x, parts = cut.z - blockIdx.x + 1;
     // Four of 128 values a lane, one head after the other where there are more
     // heads than warps; every warp makes the same turns.

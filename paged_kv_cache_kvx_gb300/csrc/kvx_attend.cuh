@@ -46,6 +46,13 @@ struct Args {
     uint32_t align;    // 16 where pages are whole tiles of 16 tokens, else 1
 };
 
+// Whether block `block`'s entry of Args::cut names a unit and parts that exist:
+// k_join indexes with it, and a block whose wait ran out leaves kNone there.
+__host__ __device__ __forceinline__ bool joinable(const uint4 &cut, uint32_t block, uint32_t num_seqs, uint32_t units,
+                                                  uint32_t grid) {
+    return cut.x < num_seqs && cut.y < units && cut.z >= block && cut.z < grid && cut.w < 2 * grid;
+}
+
 // The tokens of a sequence that are looked at: logical index i is token i below
 // `turn`, and token i + shift from there on.  With align == 16 both are
 // multiples of 16, so that 16 indices from a multiple of 16 on are tokens of
@@ -252,9 +259,8 @@ __device__ __forceinline__ void look_up(const Args &a, uint32_t per, uint32_t le
     uint32_t np = 0;                   // pieces so far
     uint32_t k = 0, k1 = 0, head = 0;  // the piece's keys still to come
     bool fresh = false;                // its first step is still to come
-    if (at >= end) {
-        if (a.cut && lane == 0) a.cut[blockIdx.x].x = kNone;
-    } else {
+    if (a.cut && lane == 0) a.cut[blockIdx.x].x = kNone;  // before any wait: one that runs out leaves it so
+    if (at < end) {
         // the first sequence: a lane's, or by the threads' counts and then one by one
         const uint32_t i = __popc(__ballot_sync(0xFFFFFFFFu, sum * a.units <= at));
         uint32_t before = __shfl_sync(0xFFFFFFFFu, sum - mine, i) * a.units;

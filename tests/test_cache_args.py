@@ -202,3 +202,49 @@ def test_address_arithmetic_on_the_host(tmp_path):
                     "-o", str(exe), str(src)], check=True, capture_output=True, text=True)
     out = subprocess.run([str(exe)], capture_output=True, text=True)
     assert out.stdout.strip() == "ok", out.stdout
+
+
+JOIN_CHECK = r"""
+#include <cstdio>
+#include <random>
+#include "kvx_attend.cuh"
+using namespace kvx;
+using namespace kvx::attend;
+#define NEED(x) do { if (!(x)) { printf("line %d: %s\n", __LINE__, #x); return 1; } } while (0)
+int main() {
+    std::mt19937_64 r(1);
+    const uint32_t seqs = 5, units = 8, grid = 456;
+    NEED(joinable(make_uint4(4, 7, 455, 911), 0, seqs, units, grid));
+    NEED(joinable(make_uint4(0, 0, 8, 14), 7, seqs, units, grid));
+    // what a workspace holds before its first use, and what a call with other sizes leaves there
+    NEED(!joinable(make_uint4(kNone, 0, 8, 14), 7, seqs, units, grid));
+    NEED(!joinable(make_uint4(kNone, kNone, kNone, kNone), 7, seqs, units, grid));
+    NEED(!joinable(make_uint4(0, 0, 0, 0), 7, seqs, units, grid));
+    NEED(!joinable(make_uint4(5, 0, 8, 14), 7, seqs, units, grid));
+    NEED(!joinable(make_uint4(0, 8, 8, 14), 7, seqs, units, grid));
+    NEED(!joinable(make_uint4(0, 0, 456, 14), 7, seqs, units, grid));
+    NEED(!joinable(make_uint4(0, 0, 8, 912), 7, seqs, units, grid));
+    for (int i = 0; i < 1000000; i++) {
+        const uint32_t block = r() % grid;
+        uint32_t w[4];
+        for (uint32_t &x : w) x = (uint32_t)(r() >> (32 + r() % 32));
+        const uint4 cut = make_uint4(w[0], w[1], w[2], w[3]);
+        if (!joinable(cut, block, seqs, units, grid)) continue;
+        const uint64_t parts = (uint64_t)cut.z - block + 1;
+        NEED(cut.x < seqs && cut.y < units && parts <= grid - block && cut.w < 2 * grid && 2 * (block + parts - 1) < 2 * grid);
+    }
+    puts("ok");
+}
+"""
+
+
+def test_join_entries_are_checked_on_the_host(tmp_path):
+    """The entries by which a cut unit's parts are joined are indexed with only where they name parts that exist."""
+    from paged_kv_cache_kvx_gb300 import build
+    src = tmp_path / "join_check.cu"
+    src.write_text(JOIN_CHECK)
+    exe = tmp_path / "join_check"
+    subprocess.run([build.nvcc(), *build.ARCH, "-std=c++17", "-I" + os.path.join(ROOT, "include"), "-I" + build.CSRC,
+                    "-o", str(exe), str(src)], check=True, capture_output=True, text=True)
+    out = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert out.stdout.strip() == "ok", out.stdout
