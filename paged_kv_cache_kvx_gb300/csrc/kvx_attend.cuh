@@ -934,6 +934,7 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT, PAGED16>::kBlocks
             }
         }
         if (!ok) break;
+        __syncwarp();  // a lane without keys may still be reading the descriptor
         if (lane == 0) mbar_arrive(&pempty[p % kPieces]);  // its query and descriptor are done with
 
         // ---- the warps' results: each adds its own to the next one's
