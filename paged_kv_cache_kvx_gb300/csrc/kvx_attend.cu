@@ -130,7 +130,12 @@ __global__ void __launch_bounds__(kScoreThreads) k_scores(const __grid_constant_
     float *to = a.scores + (uint64_t)row * a.scores_stride;
     const float2 *x[kScoreUnroll];  // the keys' logits, two query heads a load
     float old[kScoreUnroll], w[kScoreUnroll] = {};
-    if (i0 - threadIdx.x >= sv.n) return;
+    if (i0 - threadIdx.x >= sv.n) {
+        // The grid must not end before those that it depends on, even where no
+        // sequence shows a token: one block that waits is enough for that.
+        if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
+        return;
+    }
 #pragma unroll
     for (int u = 0; u < kScoreUnroll; u++) {
         const uint32_t i = i0 + u * kScoreThreads < sv.n ? i0 + u * kScoreThreads : sv.n - 1;

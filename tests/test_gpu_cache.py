@@ -457,6 +457,30 @@ def test_attend_in_a_graph_follows_new_lengths():
     assert cache.read_status() == 0
 
 
+def test_attend_with_scores_over_empty_sequences_in_a_graph():
+    """No sequence has a token: what follows on the stream finds the zeros and -infinities all the same."""
+    N, HQ, H, D, per = 3000, 32, 2, 128, 20
+    lay = R.Layout(2, H, D, 16, BF, 1)
+    cache = lay.cache(torch.zeros(lay.pool_bytes, dtype=torch.uint8, device="cuda"))
+    q = torch.ones(N, HQ, D, dtype=BF, device="cuda")
+    table, lens = torch.zeros(N, per, dtype=torch.int32, device="cuda"), torch.zeros(N, dtype=torch.int32, device="cuda")
+    out, lse, sc = torch.empty_like(q), torch.empty(N, HQ, device="cuda"), torch.rand(N, H, per * 16, device="cuda")
+    before, ws = sc.clone(), cache.attend_workspace(N, HQ, per, scores=True)
+    cache.attend(q, table, lens, out, ws, lse=lse, scores=sc)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out.fill_(math.nan)
+        lse.fill_(math.nan)
+        cache.attend(q, table, lens, out, ws, lse=lse, scores=sc)
+        got, sums = out.clone(), lse.clone()
+    for _ in range(20):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert (got == 0).all() and (sums == -math.inf).all()
+    assert torch.equal(sc, before) and cache.read_status() == 0
+
+
 def test_cache_beyond_32_bits():
     """Pages more than 4 GiB apart: append into, attend over and evict between them."""
     H, D, page = 1, 64, 16
