@@ -690,7 +690,9 @@ size_t kvx_evict_workspace_size(const kvx_cache *cache, uint32_t num_seqs,
  *                  indices, ascending; 0xFFFFFFFF after the last.
  *   kept_scores    [num_seqs][heads][budget] float out: their scores; 0 after
  *                  the last.
- *   new_lens       [num_seqs] uint32 out: min(lens[s], budget).
+ *   new_lens       [num_seqs] uint32 out: min(lens[s], budget), where a length
+ *                  beyond its pages counts as full pages.  It may be lens
+ *                  itself: lengths are then cut in place.
  * Rows are copied as stored, whatever the type.  num_seqs == 0 enqueues
  * nothing; budget == 0 is refused (KVX_EINVAL).
  */

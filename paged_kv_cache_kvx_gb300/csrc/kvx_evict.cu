@@ -115,7 +115,6 @@ k_select(const __grid_constant__ EvictArgs a, uint32_t held) {
     uint32_t *kept = a.kept + (uint64_t)row * a.budget;
     float *ks = a.kept_scores + (uint64_t)row * a.budget;
     const uint32_t keep = len < a.budget ? len : a.budget;
-    if (threadIdx.x == 0 && rank == 0 && row % a.c.heads == 0) a.new_lens[n] = keep;
     for (uint32_t i = keep + rank * kSelThreads + threadIdx.x; i < a.budget; i += size * kSelThreads) {
         kept[i] = kNone;
         ks[i] = 0.0f;
@@ -323,9 +322,13 @@ __global__ void __launch_bounds__(kGatherThreads) k_gather(const __grid_constant
     const uint32_t per = (a.budget + kRows - 1) / kRows;
     const uint32_t nh = blockIdx.x / per, r0 = blockIdx.x % per * kRows;
     const uint32_t n = nh / a.c.heads, h = nh % a.c.heads;
-    const uint32_t len = a.lens[n] < a.max_len ? a.lens[n] : a.max_len;
-    const uint32_t keep = len < a.budget ? len : a.budget;
+    const uint32_t len = a.lens[n];
+    uint32_t keep = len < a.max_len ? len : a.max_len;
+    if (keep > a.budget) keep = a.budget;
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    // Here, when every block of k_select has read its length, so that lengths
+    // may be cut in place: `keep` is the same from the old one and the new one.
+    if (threadIdx.x == 0 && h == 0 && r0 == 0) a.new_lens[n] = keep;
     if (r0 >= keep) return;
     const uint32_t rows = keep - r0 < kRows ? keep - r0 : kRows;
     if (threadIdx.x < 2 * rows) {

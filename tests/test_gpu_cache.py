@@ -719,6 +719,25 @@ def test_evict_in_a_graph_follows_new_lengths():
         check_evict(lay, cache, pool, k, v, a, now)
 
 
+@pytest.mark.parametrize("shape", [([300, 7, 100], 48, 2), ([30000, 5, 100, 20001], 1000, 8), ([900, 20, 49] * 100, 48, 2)],
+                         ids=["few", "clusters", "many"])
+def test_evict_cuts_lengths_in_place(shape):
+    """new_lens may be lens: every head goes by the length that was there."""
+    lens, budget, heads = shape
+    for turn in range(5):
+        lay, cache, pool, k, v, a = small_evict(lens, budget, heads, seed=20 + turn)
+        a["new_lens"] = a["lens"]
+        cache.evict(**a)
+        torch.cuda.synchronize()
+        if turn == 0:
+            check_evict(lay, cache, pool, k, v, a, lens)
+        assert a["lens"].tolist() == [min(n, budget) for n in lens]
+        for n, length in enumerate(lens):
+            for h in range(heads):
+                pos = R.evict_positions(a["scores"][n, h].tolist(), length, budget, 4, 8)
+                assert a["kept"][n, h].tolist() == pos + [-1] * (budget - len(pos)), (turn, n, h)
+
+
 # ------------------------------------------------------------------ together
 
 def test_decoding_on_a_transferred_prefix():
