@@ -630,7 +630,10 @@ size_t kvx_attend_workspace_size(const kvx_cache *cache, uint32_t num_seqs,
  * over the visible tokens.  A sequence without any (lens[n] == 0), like a head
  * whose logits are all -infinity, gets zeros and lse = -infinity.
  * Logits, softmax and sums are held in 32 bits; the weights that multiply V
- * go into the tensor cores as the sum of two 16-bit values.  Over a
+ * go into the tensor cores as the sum of two 16-bit values.  An infinite value
+ * in V makes its column of the output infinite, as in the formula (NaN where
+ * the weight there counts as 0: in fp16 one under 2^-32 of a head's largest
+ * may).  Over a
  * KVX_E4M3 cache products are taken in fp16, bf16 queries scaled by a power of
  * two per head (values under 2^-14 of a head's largest then lose low bits).
  *

@@ -106,6 +106,18 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
     return y;
 }
 
+// Two stored 16-bit values, of infinite ones (and of bf16 ones of 2^120 and
+// more) that magnitude: what the second parts of weights multiply.
+template <class T>
+__device__ __forceinline__ uint32_t finite2(uint32_t v) {
+    uint32_t r;
+    if constexpr (std::is_same<T, __nv_bfloat16>::value)
+        asm("min.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7B807B80u));
+    else
+        asm("min.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(0x7BFF7BFFu));
+    return r;
+}
+
 // The low or the high two of four stored 8-bit values as two fp16 ones, exactly.
 __device__ __forceinline__ uint32_t e4m3_lo(uint32_t four) {
     uint32_t r;
@@ -910,10 +922,14 @@ __global__ void __launch_bounds__(kThreads, (Shape<DP, ES, NT, PAGED16>::kBlocks
                             const uint32_t a1 = __byte_perm(v[0][w], v[1][w], 0x7632);
                             const uint32_t a2 = __byte_perm(v[2][w], v[3][w], 0x5410);
                             const uint32_t a3 = __byte_perm(v[2][w], v[3][w], 0x7632);
+                            // A weight's second part may be zero or negative:
+                            // times an infinite value it would turn the
+                            // infinity of the first into NaN.
+                            const uint32_t f0 = finite2<C>(a0), f1 = finite2<C>(a1), f2 = finite2<C>(a2), f3 = finite2<C>(a3);
 #pragma unroll
                             for (int x = 0; x < NT; x++) {
                                 mma<C>(o[c * 4 + w][x], a0, a1, a2, a3, ph[h][x][0], ph[h][x][1]);
-                                mma<C>(o[c * 4 + w][x], a0, a1, a2, a3, pl[h][x][0], pl[h][x][1]);
+                                mma<C>(o[c * 4 + w][x], f0, f1, f2, f3, pl[h][x][0], pl[h][x][1]);
                             }
                         } else {
 #pragma unroll

@@ -408,6 +408,48 @@ def test_attend_infinite_and_nan_logits():
     assert dsc[2, 0, 0].item() == sc[2, 0, 0].item()
 
 
+@pytest.mark.parametrize("kind", [(BF, 2, 1, 64, 16), (FP, 2, 1, 64, 16), (BF, 8, 2, 128, 16), (FP, 8, 1, 128, 5),
+                                  (BF, 16, 1, 128, 16), (FP, 12, 1, 64, 16), (BF, 4, 1, 256, 16), (FP, 16, 1, 256, 24)], ids=str)
+def test_attend_infinite_values(kind):
+    """An infinite value makes its column of the output infinite, whatever the weight's bits; two of opposite signs, and a
+    NaN, make it NaN.  The other columns are as without them."""
+    act, HQ, H, D, page = kind
+    lens = [2, 40, 1000, 5000, 3]
+    lay, k, v, q, table, _ = make_attend(act, act, HQ, H, D, page, 0, 0, False, False, lens, poison=False)
+    q = q / 4  # weights of every size, none beyond 2^-30
+    kb, vb = k.clone(), v.clone()
+    kb[table[0, 0].item(), :, 1] = kb[table[0, 0].item(), :, 0]  # two equal keys: weights of 0.5 each
+    put = lambda n, pos, h, d, x: vb[table[n, pos // page].item(), h].__setitem__((pos % page, d), x)  # noqa: E731
+    want = {}  # (sequence, KV head, column) -> sign, or None for NaN
+    for n, length in enumerate(lens):
+        for h in range(H):
+            for d in range(10):
+                sign = 1 if (d + h) % 2 else -1
+                put(n, (d * 977 + 13 * h) % length, h, 3 * d + h, sign * math.inf)
+                want[n, h, 3 * d + h] = sign
+            put(n, 0, h, D - 1, math.inf), put(n, length - 1, h, D - 1, -math.inf)
+            put(n, length // 2, h, D - 3, math.nan)
+            want[n, h, D - 1] = want[n, h, D - 3] = None
+            for pos in range(length):  # every value of a column
+                put(n, pos, h, D - 5, math.inf)
+            want[n, h, D - 5] = 1
+    cache = lay.cache(lay.pool(kb, vb).cuda())
+    out, lse = torch.empty_like(q).cuda(), torch.empty(len(lens), HQ, device="cuda")
+    cache.attend(q.cuda(), table.cuda(), torch.tensor(lens, dtype=torch.int32).cuda(), out,
+                 cache.attend_workspace(len(lens), HQ, table.shape[1]), lse=lse)
+    torch.cuda.synchronize()
+    out = out.cpu()
+    assert torch.isfinite(lse).all() and cache.read_status() == 0
+    finite = torch.ones_like(out, dtype=torch.bool)
+    for (n, h, d), sign in want.items():
+        heads = slice(h * (HQ // H), (h + 1) * (HQ // H))
+        got = out[n, heads, d]
+        assert torch.isnan(got).all() if sign is None else (got == sign * math.inf).all(), (n, h, d, sign, got)
+        finite[n, heads, d] = False
+    ref, _, _, off, _ = R.attend(q, kb.float(), torch.nan_to_num(vb.float(), 0, 0, 0), table, lens, D ** -0.5, 0, 0)
+    near(torch.where(finite, out, 0), torch.where(finite, ref, 0), act, off)
+
+
 def test_attend_bad_pages():
     """Block ids and segments that do not exist, and lengths beyond the pages: a status bit, no access outside."""
     base = (BF, BF, 4, 1, 64, 16, 0, 0, False, False, [200, 200])
