@@ -124,6 +124,33 @@ def test_append_special_values():
         assert (out.cpu() == 1).all() and cache.read_status() == 0
 
 
+def test_append_divides_by_the_scale():
+    """8-bit storage rounds value / scale, not value * (1 / scale): values next to a tie, where the two differ, and scales
+    whose reciprocal is infinite."""
+    values = torch.arange(1, 2048).to(BF).unique().float()
+    values = values[torch.randperm(len(values), generator=torch.Generator().manual_seed(1))]
+    ties = torch.tensor([(8 + i + 0.5) / 8 * 2.0 ** e for e in range(-5, 8) for i in range(8)])
+    scale = (values[:, None] / ties).flatten()  # value / scale is a tie, or rounds to one
+    x = values[:, None].expand(-1, len(ties)).flatten()
+    by_value, by_inverse = (x / scale).to(E4).float(), (x * (1 / scale)).to(E4).float()
+    apart = (by_value != by_inverse).nonzero().flatten()
+    assert len(apart) > 100  # the case has what it is about
+    picked = [(x[i].item(), scale[i].item(), by_value[i].item()) for i in apart[:24].tolist()]
+    picked += [(0.0, 1e-39, 0.0), (1.0, 1e-39, 448.0), (-1.0, 2.0 ** -149, -448.0), (2.0 ** -126, 2.0 ** -128, 4.0),
+               (2.0 ** -126, 2.0 ** -127, 2.0), (2.0 ** 127, 2.0 ** 127, 1.0), (1.5 * 2.0 ** 126, 2.0 ** 126, 1.5)]
+    for value, by, want in picked:
+        lay = R.Layout(1, 1, 16, 1, E4, 1)
+        pool = torch.full((lay.pool_bytes,), 0x55, dtype=torch.uint8, device="cuda")
+        cache = lay.cache(pool, k_scale=by, v_scale=by)
+        k = torch.full((1, 1, 16), value).to(BF).cuda()
+        assert k[0, 0, 0].item() == value
+        cache.append(torch.empty(1, 0, 16, dtype=BF, device="cuda"), k, k, None, torch.tensor([0]).cuda(),
+                     torch.empty(1, 0, 16, dtype=BF, device="cuda"))
+        for got in lay.values(pool.cpu()):
+            assert (got.float() == want).all(), (value, by, want, got.float())
+        assert cache.read_status() == 0
+
+
 def test_append_bad_places():
     """A slot beyond the blocks, a segment off its alignment or outside the pool, a position beyond the table: a status
     bit, and only the good tokens are written."""
