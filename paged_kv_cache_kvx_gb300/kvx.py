@@ -129,6 +129,7 @@ def _ptr(t):
 # torch's own way to the current stream's handle, without the Stream object
 # around it (2.8 us a call less); the public way where it is missing.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream(stream):
@@ -534,22 +535,33 @@ def _need(ok, what):
         raise KvxError(what)
 
 
-def _heads(t, name, shape, dtype):
+def _on(device):
+    return "cuda:%d" % device if device >= 0 else "the CPU"
+
+
+def _heads(t, name, shape, dtype, device):
     """The distance between tokens, in elements, of an activation [tokens, heads,
     dim] whose tokens' heads are contiguous."""
-    if t.shape == shape and t.dtype is dtype:
+    if t.shape == shape and t.dtype is dtype and t.get_device() == device:
         token, head, one = t.stride()
         tokens, heads, dim = shape
         if (one == 1 and (head == dim or heads < 2)) or not tokens or not heads:
             return token if tokens > 1 else heads * dim  # a single token's stride says nothing
-    raise KvxError("%s: %s %s with a token's heads contiguous" % (name, dtype, list(shape)))
+    raise KvxError("%s: %s %s with a token's heads contiguous, on %s" % (name, dtype, list(shape), _on(device)))
 
 
-def _table(t, name, dtypes, shape):
+def _table(t, name, dtypes, shape, device):
     """The pointer of a contiguous tensor of the given shape and one of the types."""
-    if t.shape == shape and t.dtype in dtypes and t.is_contiguous():
+    if t.shape == shape and t.dtype in dtypes and t.is_contiguous() and t.get_device() == device:
         return t.data_ptr()
-    raise KvxError("%s: contiguous %s of %s" % (name, list(shape), " or ".join(str(d) for d in dtypes)))
+    raise KvxError("%s: contiguous %s of %s, on %s" % (name, list(shape), " or ".join(str(d) for d in dtypes), _on(device)))
+
+
+def _scratch(t, device):
+    """A workspace's pointer."""
+    if t.dtype is torch.uint8 and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
+    raise KvxError("ws: contiguous uint8, on %s" % _on(device))
 
 
 class Cache:
@@ -558,13 +570,15 @@ class Cache:
     addr[b, first_lane + 2*h + 1], so the address table of a transfer serves as it is.
     The object keeps the pool and the table alive and owns one status word;
     workspaces are the caller's (attend_workspace, evict_workspace: uint8
-    tensors, one per stream that calls concurrently)."""
+    tensors, one per stream that calls concurrently).  Every tensor of a call is
+    on the pool's GPU, which is the current device."""
 
     def __init__(self, pool, addr, heads: int, dim: int, dtype, page_tokens: int, first_lane: int = 0,
                  token_stride: int | None = None, k_scale: float = 1.0, v_scale: float = 1.0):
         _need(pool.dtype == torch.uint8 and pool.is_contiguous(), "pool: contiguous uint8")
         _need(addr.dim() == 2 and addr.dtype in (torch.int64, torch.uint64) and addr.is_contiguous(),
               "addr: contiguous [blocks, lanes] of 64-bit byte offsets")
+        _need(addr.get_device() == pool.get_device(), "addr: on %s, as the pool" % _on(pool.get_device()))
         _need(dtype in _DTYPES, "dtype: one of %s" % ", ".join(str(d) for d in _DTYPES))
         self.pool, self.addr, self.dim, self.heads, self.dtype = pool, addr, int(dim), int(heads), dtype
         self.page_tokens = int(page_tokens)
@@ -574,7 +588,16 @@ class Cache:
                              page_tokens=page_tokens, token_stride=row if token_stride is None else token_stride,
                              k_scale=k_scale, v_scale=v_scale)
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
-        self._ref, self._status = ctypes.byref(self.c), self.status.data_ptr()
+        self._ref, self._status, self._device = ctypes.byref(self.c), self.status.data_ptr(), pool.get_device()
+
+    def _stream(self, stream):
+        """A call's stream: the given one, or the current one of the pool's GPU."""
+        _need(self._device >= 0, "pool: on a GPU")
+        if _current_device() != self._device:
+            raise KvxError("the pool is on cuda:%d, the current device is cuda:%d" % (self._device, _current_device()))
+        if stream is None and _raw_stream is not None:
+            return _raw_stream(self._device)
+        return _stream(stream)
 
     def append(self, q, k, v, positions, slots, q_out, q_weight=None, k_weight=None, eps: float = 1e-6, cos_sin=None,
                interleaved: bool = False, stream=None):
@@ -582,23 +605,23 @@ class Cache:
         one projection's output will do); positions int32 [T]; slots int64 [T];
         cos_sin float [max_pos, rot_dim]; q_out as q, or q itself."""
         _need(q.dim() == 3, "q: [tokens, q_heads, dim]")
-        (T, q_heads, _), act, dim = q.shape, q.dtype, self.dim
+        (T, q_heads, _), act, dim, dev = q.shape, q.dtype, self.dim, self._device
         _need(act in _ACTS, "q: bfloat16 or float16")
         queries, keys = (T, q_heads, dim), (T, self.heads, dim)
-        qs, os_ = _heads(q, "q", queries, act), _heads(q_out, "q_out", queries, act)
-        ks, vs = _heads(k, "k", keys, act), _heads(v, "v", keys, act)
-        wq = None if q_weight is None else _table(q_weight, "q_weight", (act,), (dim,))
-        wk = None if k_weight is None else _table(k_weight, "k_weight", (act,), (dim,))
+        qs, os_ = _heads(q, "q", queries, act, dev), _heads(q_out, "q_out", queries, act, dev)
+        ks, vs = _heads(k, "k", keys, act, dev), _heads(v, "v", keys, act, dev)
+        wq = None if q_weight is None else _table(q_weight, "q_weight", (act,), (dim,), dev)
+        wk = None if k_weight is None else _table(k_weight, "k_weight", (act,), (dim,), dev)
         angles = pos = None
         most = rot = 0
         if cos_sin is not None:
             most, rot = cos_sin.shape
-            angles = _table(cos_sin, "cos_sin", _FLOAT, (most, rot))
-            pos = _table(positions, "positions", _IDS, (T,))
+            angles = _table(cos_sin, "cos_sin", _FLOAT, (most, rot), dev)
+            pos = _table(positions, "positions", _IDS, (T,), dev)
         _check(lib().kvx_append_tokens(self._ref, q.data_ptr(), qs, k.data_ptr(), ks, v.data_ptr(), vs, _DTYPES[act], T,
                                        q_heads, wq, wk, eps, angles, rot, most, 1 if interleaved else 0, pos,
-                                       _table(slots, "slots", _SLOTS, (T,)), q_out.data_ptr(), os_, self._status,
-                                       _stream(stream)), "kvx_append_tokens")
+                                       _table(slots, "slots", _SLOTS, (T,), dev), q_out.data_ptr(), os_, self._status,
+                                       self._stream(stream)), "kvx_append_tokens")
 
     def attend_workspace(self, num_seqs: int, q_heads: int, blocks_per_seq: int, window: int = 0, sinks: int = 0,
                          scores: bool = False):
@@ -613,19 +636,19 @@ class Cache:
         scores float [num_seqs, heads, stride], added to.  scale defaults to
         1/sqrt(dim)."""
         _need(q.dim() == 3 and blocks.dim() == 2, "q: [num_seqs, q_heads, dim], blocks: [num_seqs, blocks_per_seq]")
-        (N, q_heads, _), act, dim, per, stride = q.shape, q.dtype, self.dim, blocks.shape[1], 0
+        (N, q_heads, _), act, dim, dev, per, stride = q.shape, q.dtype, self.dim, self._device, blocks.shape[1], 0
         _need(act in _ACTS, "q: bfloat16 or float16")
         queries, sums, weights = (N, q_heads, dim), None, None
         if lse is not None:
-            sums = _table(lse, "lse", _FLOAT, (N, q_heads))
+            sums = _table(lse, "lse", _FLOAT, (N, q_heads), dev)
         if scores is not None:
             stride = scores.shape[-1]
-            weights = _table(scores, "scores", _FLOAT, (N, self.heads, stride))
-        _check(lib().kvx_attend(self._ref, q.data_ptr(), _heads(q, "q", queries, act), _DTYPES[act], N, q_heads,
-                                _table(blocks, "blocks", _IDS, (N, per)), per, _table(lens, "lens", _IDS, (N,)),
+            weights = _table(scores, "scores", _FLOAT, (N, self.heads, stride), dev)
+        _check(lib().kvx_attend(self._ref, q.data_ptr(), _heads(q, "q", queries, act, dev), _DTYPES[act], N, q_heads,
+                                _table(blocks, "blocks", _IDS, (N, per), dev), per, _table(lens, "lens", _IDS, (N,), dev),
                                 dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
-                                _heads(out, "out", queries, act), sums, weights, stride, self._status, ws.data_ptr(),
-                                ws.numel(), _stream(stream)), "kvx_attend")
+                                _heads(out, "out", queries, act, dev), sums, weights, stride, self._status,
+                                _scratch(ws, dev), ws.numel(), self._stream(stream)), "kvx_attend")
 
     def evict_workspace(self, num_seqs: int, blocks_per_seq: int, budget: int):
         n = kvx_evict_workspace_size(self.c, num_seqs, blocks_per_seq, budget)
@@ -639,13 +662,15 @@ class Cache:
         _need(blocks.dim() == 2 and dst_blocks.dim() == 2 and kept.dim() == 3, "evict: blocks and dst_blocks are "
               "[num_seqs, pages], kept is [num_seqs, heads, budget]")
         (N, per), dper, heads, budget, stride = blocks.shape, dst_blocks.shape[1], self.heads, kept.shape[2], scores.shape[-1]
-        _check(lib().kvx_evict(self._ref, N, _table(blocks, "blocks", _IDS, (N, per)), per, _table(lens, "lens", _IDS, (N,)),
-                               _table(scores, "scores", _FLOAT, (N, heads, stride)), stride, budget, sinks, recent,
-                               _table(dst_blocks, "dst_blocks", _IDS, (N, dper)), dper,
-                               _table(kept, "kept", _IDS, (N, heads, budget)),
-                               _table(kept_scores, "kept_scores", _FLOAT, (N, heads, budget)),
-                               _table(new_lens, "new_lens", _IDS, (N,)), self._status, ws.data_ptr(), ws.numel(),
-                               _stream(stream)), "kvx_evict")
+        dev = self._device
+        _check(lib().kvx_evict(self._ref, N, _table(blocks, "blocks", _IDS, (N, per), dev), per,
+                               _table(lens, "lens", _IDS, (N,), dev),
+                               _table(scores, "scores", _FLOAT, (N, heads, stride), dev), stride, budget, sinks, recent,
+                               _table(dst_blocks, "dst_blocks", _IDS, (N, dper), dev), dper,
+                               _table(kept, "kept", _IDS, (N, heads, budget), dev),
+                               _table(kept_scores, "kept_scores", _FLOAT, (N, heads, budget), dev),
+                               _table(new_lens, "new_lens", _IDS, (N,), dev), self._status, _scratch(ws, dev), ws.numel(),
+                               self._stream(stream)), "kvx_evict")
 
     def read_status(self) -> int:
         return int(_u32_np(self.status)[0])

@@ -153,6 +153,72 @@ def test_cache_checks_its_tensors():
             c.evict(**(ok | bad))
 
 
+def call_args(dev):
+    """Valid arguments of the three calls, on a device, and the cache's own."""
+    T, D = 3, 64
+    pool, addr = torch.zeros(1 << 16, dtype=torch.uint8, device=dev), torch.zeros(4, 4, dtype=torch.int64, device=dev)
+    q, k = torch.zeros(T, 4, D, dtype=torch.bfloat16, device=dev), torch.zeros(T, 2, D, dtype=torch.bfloat16, device=dev)
+    ids = lambda *s: torch.zeros(*s, dtype=torch.int32, device=dev)  # noqa: E731
+    z = lambda *s: torch.zeros(*s, device=dev)  # noqa: E731
+    ws = torch.empty(1 << 20, dtype=torch.uint8, device=dev)
+    append = dict(q=q, k=k, v=k.clone(), positions=ids(T), slots=ids(T).long() - 1, q_out=q.clone(), cos_sin=z(8, D),
+                  q_weight=q[0, 0].clone(), k_weight=q[0, 0].clone())
+    attend = dict(q=q, blocks=ids(T, 5), lens=ids(T), out=q.clone(), ws=ws, lse=z(T, 4), scores=z(T, 2, 20))
+    evict = dict(blocks=ids(T, 5), lens=ids(T), scores=z(T, 2, 20), dst_blocks=ids(T, 5), kept=ids(T, 2, 8),
+                 kept_scores=z(T, 2, 8), new_lens=ids(T), ws=ws)
+    return pool, addr, dict(append=append, attend=attend, evict=evict)
+
+
+def make_cache(pool, addr):
+    return kvx.Cache(pool, addr, heads=2, dim=64, dtype=torch.bfloat16, page_tokens=4)
+
+
+def test_cache_wants_a_gpu():
+    """Valid arguments in host memory are refused by the binding, before the library sees their pointers."""
+    pool, addr, calls = call_args("cpu")
+    c, before = make_cache(pool, addr), kvx.kvx_launch_count()
+    for name, args in calls.items():
+        with pytest.raises(kvx.KvxError, match="on a GPU"):
+            getattr(c, name)(**args)
+    assert kvx.kvx_launch_count() == before
+
+
+def test_cache_refuses_tensors_of_another_device():
+    """A cache whose pool is on another device than the call's tensors: each is named."""
+    pool, addr, calls = call_args("cpu")
+    c = make_cache(pool, addr)
+    c._device = 0  # as if the pool were on the first GPU
+    for name, first in (("append", "q"), ("attend", "lse"), ("evict", "blocks")):
+        with pytest.raises(kvx.KvxError, match=r"^%s: .*on cuda:0" % first):
+            getattr(c, name)(**calls[name])
+
+
+@pytest.mark.parametrize("name", ["attend", "evict"])
+def test_cache_checks_its_workspace(name):
+    pool, addr, calls = call_args("cpu")
+    c, ws = make_cache(pool, addr), calls[name]["ws"]
+    for bad in (ws.view(torch.float32), ws[::2], ws.view(torch.int8)):
+        with pytest.raises(kvx.KvxError, match="^ws: "):
+            getattr(c, name)(**(calls[name] | dict(ws=bad)))
+
+
+@pytest.mark.gpu
+@pytest.mark.parametrize("name", ["append", "attend", "evict"])
+def test_cache_refuses_each_host_tensor(name):
+    pool, addr, calls = call_args("cuda")
+    c, args = make_cache(pool, addr), calls[name]
+    getattr(c, name)(**args)
+    before = kvx.kvx_launch_count()
+    for arg, t in args.items():
+        with pytest.raises(kvx.KvxError, match="^%s: .*on cuda:0" % arg):
+            getattr(c, name)(**(args | {arg: t.cpu()}))
+    with pytest.raises(kvx.KvxError, match="^addr: "):
+        make_cache(pool, addr.cpu())
+    assert kvx.kvx_launch_count() == before
+    torch.cuda.synchronize()
+    assert c.read_status() == 0
+
+
 HOST_CHECK = r"""
 #include <cstdio>
 #include <random>
