@@ -613,8 +613,14 @@ kvx_status kvx_append_tokens(const kvx_cache *cache, const void *q,
                              void *q_out, uint64_t q_out_stride,
                              uint32_t *status, void *stream);
 
-/* Scratch of kvx_attend; 0 for arguments it refuses.  with_scores: whether
- * scores will be passed. */
+/* Scratch of kvx_attend, 16-byte aligned (else KVX_EINVAL); 0 for arguments it
+ * refuses.  with_scores: whether scores will be passed.  Without, it is at most
+ * 17 MB (partial results of sequences split over blocks).  With, it
+ * also holds every logit, whatever the lengths will be:
+ *     num_seqs * heads * T * group * 4 bytes
+ * (group = q_heads / heads rounded up to even; T = blocks_per_seq *
+ * page_tokens, or with a window at most window + sinks + 30): 2.1 GB for 64
+ * sequences, 131,072 tokens, 64 query heads. */
 size_t kvx_attend_workspace_size(const kvx_cache *cache, uint32_t num_seqs,
                                  uint32_t q_heads, uint32_t blocks_per_seq,
                                  uint32_t window, uint32_t sinks,

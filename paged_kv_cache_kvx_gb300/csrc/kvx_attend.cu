@@ -247,7 +247,7 @@ extern "C" kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t
     if (scores && scores_stride < p.max_len) return KVX_EINVAL;
     if (!num_seqs) return KVX_OK;
     if (!q || !out || !lens || (p.max_len && !blocks)) return KVX_EINVAL;
-    if (!ws || ws_bytes < carve(p, nullptr, nullptr)) return KVX_EINVAL;
+    if (!ws || !aligned16(ws) || ws_bytes < carve(p, nullptr, nullptr)) return KVX_EINVAL;
 
     Args a = {};
     a.c = cache_view(cache);

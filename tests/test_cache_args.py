@@ -83,6 +83,12 @@ def test_attend_refuses(bad):
     assert attend(**bad) == EINVAL
 
 
+@pytest.mark.parametrize("ws", [P + 1, P + 4, P + 8])
+def test_attend_refuses_an_unaligned_workspace(ws):
+    """It is cut into arrays of 16-byte vectors."""
+    assert attend(n=1, ws=ws) == EINVAL
+
+
 def test_attend_workspace_is_checked_to_the_byte():
     c = cache()
     for scores in (0, 1):
