@@ -455,10 +455,10 @@ k_copy_vec(const uint8_t *pool_r, uint8_t *pool_w, const uint8_t *slab_r, uint8_
     __shared__ uint64_t s_delta[kThreads];
     __shared__ uint8_t s_ok[kThreads];
     __shared__ uint16_t s_first[kBuckets];  // per 64-byte bucket: the last span starting at or before it
-    if (ctl->bad || ctl->key != key || __ldcg(&ctl->users) != bulk_blocks) return;
+    const bool go = !ctl->bad && ctl->key == key && __ldcg(&ctl->users) == bulk_blocks;
     const uint64_t n = *num_descs < desc_cap ? *num_descs : desc_cap;
     const uint64_t used = ctl->used < slab_bytes ? ctl->used : slab_bytes;
-    const uint32_t nlist = ctl->n_vec;
+    const uint32_t nlist = go ? ctl->n_vec : 0;
     for (uint32_t li = blockIdx.x; li < nlist; li += gridDim.x) {
         const uint64_t t = vec_tiles[li];
         uint64_t lo = t * kTileBytes;
@@ -550,6 +550,9 @@ k_copy_vec(const uint8_t *pool_r, uint8_t *pool_w, const uint8_t *slab_r, uint8_
             k += nb;
         }
     }
+    // The grid must not end before the bulk kernel that it runs beside, or what
+    // follows on the stream could: one block that waits is enough for that.
+    if (blockIdx.x == 0) asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <bool PACK>

@@ -132,3 +132,31 @@ def test_overlapped_transfers_bit_exact():
         g.replay()
     torch.cuda.synchronize()
     check()
+
+
+@pytest.mark.parametrize("make", [lambda: W.bump("bulk", 400, 288, 4096, seed=2),
+                                  lambda: W.worst(blocks=61, slots=18, npos=128, seed=3)], ids=["bulk", "vector"])
+def test_what_follows_a_copy_finds_its_bytes(make):
+    """Kernels behind a pack on the stream read the whole slab, whichever of the copy's two kernels ends last."""
+    wl = make()
+    tr = kvx.Transfer(wl.blocks, wl.seg_len, wl.numa, wl.pool_bytes)
+    tr.set_addr(wl.addr)
+    pool = torch.empty(wl.pool_bytes, dtype=torch.uint8, device="cuda")
+    W.fill_pool_torch(pool, wl.seed)
+    slab = torch.zeros(tr.slab_bytes, dtype=torch.uint8, device="cuda")
+    tr.encode()
+    tr.plan()
+    tr.pack(pool, slab)
+    torch.cuda.synchronize()
+    assert tr.read_status() == 0
+    want = slab.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        slab.zero_()
+        tr.pack(pool, slab)
+        got = slab.clone()
+    for _ in range(10):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+    assert tr.read_status() == 0
