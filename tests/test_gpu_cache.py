@@ -330,6 +330,23 @@ def test_attend_units_that_some_warps_pass_by(kind):
     run_attend((*kind, 16, 0, 0, False, False, lens.tolist()))
 
 
+@pytest.mark.parametrize("count", [31, 32, 33, 127, 128, 129])
+def test_attend_counts_of_sequences(count):
+    """Up to 32 sequences are counted by one warp, more by all threads, beyond 128 several by each."""
+    rng = np.random.default_rng(count)
+    lens = rng.integers(1, 90, size=count)
+    lens[rng.integers(0, count, size=3)] = 0
+    lens[rng.integers(0, count, size=2)] = [1500, 400]
+    run_attend((BF, BF, 4, 2, 64, 16, 0, 0, True, False, lens.tolist()))
+    run_attend((FP, E4, 3, 1, 128, 5, 300, 2, True, False, lens.tolist()))
+
+
+@pytest.mark.parametrize("case", [(BF, BF, 3, 3, 128, 16, 0, 0, True, False, LENS), (FP, E4, 2, 2, 64, 24, 90, 3, True, True, LENS),
+                                  (FP, FP, 1, 1, 256, 16, 0, 0, True, False, [0, 3000, 1])], ids=str)
+def test_attend_one_query_head_to_a_kv_head_with_scores(case):
+    run_attend(case)
+
+
 def test_attend_without_pages_or_sequences():
     lay = R.Layout(2, 2, 64, 16, BF, 1)
     cache = lay.cache(torch.zeros(lay.pool_bytes, dtype=torch.uint8, device="cuda"))
@@ -678,6 +695,14 @@ def test_evict(case, pad):
                 b = np.arange(lay.row)
                 want[torch.from_numpy((d[:, None] + b).reshape(-1))] = host[torch.from_numpy((s[:, None] + b).reshape(-1))]
     assert torch.equal(pool.cpu(), want)
+
+
+@pytest.mark.parametrize("case", [(FP, 1, 16, 64, [400001], 3000, 4, 1000, "special", False),
+                                  (FP, 2, 16, 64, [200001] + [9] * 9, 2000, 4, 100, "random", False),
+                                  (FP, 1, 16, 64, [410000], 200000, 0, 0, "ties", False)], ids=["eight", "four", "ties"])
+def test_evict_clusters_with_more_keys_than_they_hold(case):
+    test_evict(case, 1)
+    test_evict(case, 4)
 
 
 def test_evict_bad_pages():
