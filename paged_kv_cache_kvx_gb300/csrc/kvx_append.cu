@@ -294,13 +294,15 @@ extern "C" kvx_status kvx_append_tokens(const kvx_cache *cache, const void *q, u
     const uint32_t lanes = cache->dim <= 64 ? 8 : cache->dim <= 128 ? 16 : 32;
     const uint32_t per_block = kThreads / lanes, rows = q_heads + 2 * cache->heads;
     // A token's rows go to several blocks while those fit on the device
-    // together.  Beyond that, to two where the last wave is short of blocks: a
-    // block's start costs as much as about kStart of its rounds.
+    // together, and to two up to half a wave beyond that: three waves of halves
+    // in place of two of wholes (32 + 8 heads of 128: 4999 tokens 26.9 us in one
+    // block each, 24.1 in two; 7000 tokens 31.8 and 30.4; 8000, which stay in
+    // one, 34.5 and 35.5, 12,000 49.8 and 50.1).  With eight rounds or fewer a
+    // block's start costs as much as that saves (12 + 2 heads: 4865 tokens 11.1
+    // and 11.4 us; 16 + 2 heads, ten rounds, 13.0 and 12.2).
     const uint64_t most = ceil_div(rows, per_block), fit = (uint64_t)kMinBlocks * sm_count();
-    uint64_t parts = T < fit ? fit / T : 1;
-    constexpr uint64_t kStart = 4;
-    if (parts == 1 && ceil_div(2 * (uint64_t)T, fit) * (kStart + ceil_div(most, 2)) < ceil_div(T, fit) * (kStart + most))
-        parts = 2;
+    const bool halves = T > fit && 2 * (uint64_t)T <= 3 * fit && most > 8;
+    const uint64_t parts = T < fit ? fit / T : halves ? 2 : 1;
     const dim3 grid(T, (uint32_t)(most < parts ? most : parts));
     if (dtype == KVX_BF16)
         cache->dtype == KVX_E4M3 ? launch<__nv_bfloat16, true>(a, grid, interleaved != 0, as_stream(stream))
