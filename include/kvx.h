@@ -529,7 +529,8 @@ kvx_status kvx_pack_noalloc(const uint8_t *pool, uint64_t pool_bytes,
 
 /* ------------------------------------------------- the cache's operators */
 
-/* Element types of the cache operators. */
+/* Element types of the cache and its operators (KVX_F32 stands for what is float
+ * in their descriptions; none of them takes it as a `dtype`). */
 #define KVX_F32  0u
 #define KVX_BF16 1u
 #define KVX_F16  2u
@@ -661,7 +662,7 @@ size_t kvx_attend_workspace_size(const kvx_cache *cache, uint32_t num_seqs,
  *                  added to element j of every visible token, in a fixed
  *                  order.  scores_stride >= blocks_per_seq * page_tokens.
  * Results depend on nothing but the arguments and the device's SM count: no
- * atomics.  One launch, another where blocks_per_seq and the window let a
+ * atomics.  After KVX_S_TIMEOUT out, lse and scores are unspecified.  One launch, another where blocks_per_seq and the window let a
  * sequence show more than 256 tokens (it may be split over blocks and is then
  * joined), another where scores are added; num_seqs == 0 enqueues nothing.
  */
@@ -698,7 +699,9 @@ size_t kvx_evict_workspace_size(const kvx_cache *cache, uint32_t num_seqs,
  *   kept           [num_seqs][heads][budget] uint32 out: the kept tokens'
  *                  indices, ascending; 0xFFFFFFFF after the last.
  *   kept_scores    [num_seqs][heads][budget] float out: their scores; 0 after
- *                  the last.
+ *                  the last.  (kvx_attend adds to rows of its scores_stride,
+ *                  which is more once there is a page for new tokens: copy
+ *                  them there to go on adding.)
  *   new_lens       [num_seqs] uint32 out: min(lens[s], budget), where a length
  *                  beyond its pages counts as full pages.  It may be lens
  *                  itself: lengths are then cut in place.

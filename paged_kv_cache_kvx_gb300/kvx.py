@@ -658,7 +658,8 @@ class Cache:
     def evict(self, blocks, lens, scores, dst_blocks, kept, kept_scores, new_lens, ws, sinks: int = 0, recent: int = 0,
               stream=None):
         """kvx_evict: kept int32 and kept_scores float [num_seqs, heads, budget];
-        dst_blocks int32 [num_seqs, dst_per_seq]; new_lens int32 [num_seqs]."""
+        dst_blocks int32 [num_seqs, dst_per_seq]; new_lens int32 [num_seqs], or
+        lens itself."""
         _need(blocks.dim() == 2 and dst_blocks.dim() == 2 and kept.dim() == 3, "evict: blocks and dst_blocks are "
               "[num_seqs, pages], kept is [num_seqs, heads, budget]")
         (N, per), dper, heads, budget, stride = blocks.shape, dst_blocks.shape[1], self.heads, kept.shape[2], scores.shape[-1]
