@@ -314,13 +314,18 @@ def _rotated(x, cos, sin, pairs):
     return torch.cat([torch.stack([a * cos - b * sin, b * cos + a * sin], dim=-1).flatten(-2), rest], dim=-1)
 
 
+def _power(e):
+    """2 to whole numbers from -126 to 127, exactly."""
+    return (e + 127 << 23).to(torch.int32).view(torch.float32)
+
+
 def _quantised(x):
     """Rows as e4m3 (their bytes) and the exponent, biased by 127, of the smallest power of two that they fit over."""
     top = x.abs().amax(-1, keepdim=True)
     mantissa, exponent = torch.frexp(top)  # in [0.5, 1)
     e = (exponent - 9 + (mantissa > 0.875)).clamp(min=-126)
     e = torch.where(top > 0, e, -126)
-    stored = torch.ldexp(x, -e).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
+    stored = (x * _power(-e)).clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
     return stored.view(torch.uint8), (e[..., 0] + 127).to(torch.uint8)
 
 
@@ -355,7 +360,7 @@ def _loaded(s, block, place):
     x = s["pool"].view(torch.int32).view(-1, 4)[at].flatten(-2).view(STORE[c["store"]]).float()
     if c["store"] == "rows":
         e = s["pool"][seg + s["scale_offset"] + place[..., None]]
-        x = torch.ldexp(x, e.int()[..., None] - 127)
+        x = x * _power(e.int()[..., None] - 127)
     return x[..., 0::2, :] * s["k_scale"], x[..., 1::2, :] * s["v_scale"]
 
 
@@ -458,9 +463,10 @@ def _exact_append(s):
     block = s["addr"][block, 0] // size
     for kv, x in ((0, head(s["k"], s["k_weight"])[has]), (1, s["v"].double()[has])):
         top = x.abs().amax(-1)
-        e = torch.ceil(torch.log2(top / E4M3_MAX)).clamp(min=-126.0)
-        e = torch.where(top > 2.0 ** e * E4M3_MAX, e + 1, torch.where(top <= 2.0 ** (e - 1) * E4M3_MAX, e - 1, e))
-        scale = 2.0 ** e.clamp(min=-126.0)
+        e = torch.ceil(torch.log2(top / E4M3_MAX)).clamp(min=-126.0) + 127
+        power = lambda b: b.clamp(1, 254).to(torch.uint8).view(torch.float8_e8m0fnu).double()  # noqa: E731
+        e = torch.where(top > power(e) * E4M3_MAX, e + 1, torch.where(top <= power(e - 1) * E4M3_MAX, e - 1, e))
+        scale = power(e)
         for j in range(h):
             if rows.dim() == 4:  # [blocks, lanes, tokens, dim]
                 rows[block, 2 * j + kv, place] = x[:, j] / scale[:, j, None]
@@ -479,7 +485,7 @@ def _head64(s, block, place, head, kv):
     raw = s["pool"][(seg + place * s["stride"])[:, None] + torch.arange(row, device="cuda")]
     x = raw.view(STORE[c["store"]] if size == 2 else torch.float8_e4m3fn).double()
     if c["store"] == "rows":
-        return x * 2.0 ** (s["pool"][seg + s["scale_offset"] + place].double()[:, None] - 127)
+        return x * s["pool"][seg + s["scale_offset"] + place].view(torch.float8_e8m0fnu).double()[:, None]
     return x * (s["v_scale"] if kv else s["k_scale"])
 
 
