@@ -550,8 +550,18 @@ kvx_status kvx_pack_noalloc(const uint8_t *pool, uint64_t pool_bytes,
  * first_lane + 2*heads - 1 within L; token_stride a multiple of 16 bytes and
  * at least a row; pool 16-byte aligned; k_scale and v_scale (the values that a
  * stored 1 stands for) finite and > 0, and 1 unless dtype is KVX_E4M3.
+ * Row scales: with scale_offset != 0 (dtype KVX_E4M3, k_scale = v_scale = 1; a
+ * multiple of 16, behind the segment's last row) every row has a scale of its
+ * own, a power of two: byte e at scale_offset + i of a segment says that token
+ * i's row stands for its values times 2^(e - 127); e = 255 makes it NaN.  (For
+ * token-major pages a place for one token more holds the scales of all heads:
+ * scale_offset = page_tokens * token_stride, where page_tokens <= dim.)  The
+ * scales lie in their segment and are transferred with it.  kvx_append_tokens
+ * writes such caches, kvx_read_tokens and kvx_attend_shared read them;
+ * kvx_attend and kvx_evict refuse them (KVX_EINVAL).
  * On the device: a segment whose address is not a multiple of 16 raises
- * KVX_S_ALIGN, one that leaves the pool (all page_tokens rows of it counted)
+ * KVX_S_ALIGN, one that leaves the pool (all page_tokens rows of it counted, and
+ * scales)
  * or whose block id is >= B raises KVX_S_BOUNDS; it is neither read nor
  * written.
  */
@@ -565,7 +575,7 @@ typedef struct kvx_cache {
     uint32_t dim;
     uint32_t dtype;
     uint32_t page_tokens;
-    uint32_t reserved;     /* 0 */
+    uint32_t scale_offset; /* of a segment's row scales; 0 (reserved to mean none) */
     uint64_t token_stride; /* bytes */
     float k_scale, v_scale;
 } kvx_cache;
@@ -580,7 +590,8 @@ typedef struct kvx_cache {
  * i < rot_dim / 2: a = i and b = i + rot_dim/2, or with interleaved != 0
  * a = 2i and b = 2i + 1.  Everything is computed in 32 bits and rounded once,
  * to the nearest even; KVX_E4M3 stores value / scale and limits it to +-448
- * (a NaN stays NaN).
+ * (a NaN stays NaN).  With row scales a row's scale is the smallest power of
+ * two, from 2^-126 on, over which its largest finite magnitude is at most 448.
  *
  *   q, k, v        [T][q_heads|heads|heads][dim] of `dtype` (KVX_BF16 or
  *                  KVX_F16; the cache's type is the same one or KVX_E4M3); a
@@ -674,6 +685,82 @@ kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t q_stride,
                       float *lse, float *scores, uint64_t scores_stride,
                       uint32_t *status, void *ws, size_t ws_bytes,
                       void *stream);
+
+/*
+ * Attention of one new token per sequence for a batch whose sequences share
+ * prefixes: sequence n sees first the prefix_lens[g] tokens of the group g that
+ * it belongs to, whose pages are read once for all of the group's sequences,
+ * and then the lens[n] tokens of its own pages.  Logits, outputs and lse are
+ * those of kvx_attend over both; without groups it is kvx_attend (without
+ * window, sinks and scores) over any cache, one with row scales too.
+ *
+ *   q, out, lse, scale, blocks, lens  as for kvx_attend.  lens may be 0, of a
+ *                  sequence that sees its prefix alone.
+ *   group_first    [num_groups + 1] uint32, not decreasing: the sequences of
+ *                  group g are group_first[g] .. group_first[g+1] - 1; those
+ *                  before the first group and behind the last see their own
+ *                  tokens only.  A group that decreases or reaches beyond
+ *                  num_seqs raises KVX_S_BOUNDS, and the outputs of the
+ *                  sequences it names are unspecified.
+ *   prefix_blocks  [num_groups][blocks_per_prefix] uint32.
+ *   prefix_lens    [num_groups] uint32; like lens, one that exceeds its pages
+ *                  raises KVX_S_BOUNDS and counts as full pages.
+ * Keys and values enter the tensor cores in `dtype`: 16-bit ones as they are,
+ * 8-bit ones exactly (row-scaled ones in fp16 rounded to it, where they are
+ * under 2^-14 or from 65520 on).  Logits, softmax and sums are held in 32 bits;
+ * the weights that multiply V are rounded to `dtype`, as V and the output are.
+ * An infinite value in V makes its column of the output infinite, or NaN where
+ * its weight counts as 0 (in fp16 one under 2^-32 of a head's largest).
+ * Results depend on nothing but the arguments and the device's SM count: no
+ * atomics.  After KVX_S_TIMEOUT out and lse are unspecified.  Two launches;
+ * num_seqs == 0 enqueues nothing.
+ */
+size_t kvx_attend_shared_workspace_size(const kvx_cache *cache,
+                                        uint32_t num_seqs, uint32_t q_heads,
+                                        uint32_t blocks_per_seq,
+                                        uint32_t num_groups,
+                                        uint32_t blocks_per_prefix);
+kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q,
+                             uint64_t q_stride, uint32_t dtype,
+                             uint32_t num_seqs, uint32_t q_heads,
+                             const uint32_t *prefix_blocks,
+                             uint32_t blocks_per_prefix,
+                             const uint32_t *prefix_lens,
+                             const uint32_t *group_first, uint32_t num_groups,
+                             const uint32_t *blocks, uint32_t blocks_per_seq,
+                             const uint32_t *lens, float scale, void *out,
+                             uint64_t out_stride, float *lse,
+                             uint32_t *status, void *ws, size_t ws_bytes,
+                             void *stream);
+
+/*
+ * Read tokens of the cache back into dense tensors: rows starts[n] ..
+ * starts[n+1] - 1 of k_out and v_out get the keys and values, in all heads, of
+ * sequence n's tokens first[n], first[n] + 1, ...  16-bit caches are copied;
+ * 8-bit values are multiplied by their scale (k_scale and v_scale, or the
+ * row's) and rounded once to `dtype`, to the nearest even.
+ *
+ *   blocks         [num_seqs][blocks_per_seq] uint32, as for kvx_attend; only
+ *                  entries of pages that hold tokens to be read are read.
+ *   first          [num_seqs] uint32, or NULL for zeros.
+ *   starts         [num_seqs + 1] uint32, not decreasing, starts[num_seqs] <= T
+ *                  (else KVX_S_BOUNDS, and the rows that exist are unspecified).
+ *                  Rows before starts[0] and from starts[num_seqs] on are left
+ *                  as they were.
+ *   k_out, v_out   [T][heads][dim] of `dtype` (KVX_BF16 or KVX_F16; of a 16-bit
+ *                  cache its own type), a token's heads contiguous, tokens
+ *                  k_stride, v_stride elements apart, 16-byte aligned as in
+ *                  kvx_append_tokens.
+ * A token beyond blocks_per_seq * page_tokens raises KVX_S_BOUNDS; its rows, like
+ * those of a page or segment that the cache's rules exclude, are left as they
+ * were.  One launch; T == 0 or num_seqs == 0 enqueues nothing.
+ */
+kvx_status kvx_read_tokens(const kvx_cache *cache, const uint32_t *blocks,
+                           uint32_t num_seqs, uint32_t blocks_per_seq,
+                           const uint32_t *first, const uint32_t *starts,
+                           uint32_t T, uint32_t dtype, void *k_out,
+                           uint64_t k_stride, void *v_out, uint64_t v_stride,
+                           uint32_t *status, void *stream);
 
 /* Scratch of kvx_evict; 0 for arguments it refuses.  (The present kernels keep
  * what they need in shared memory: it is a small constant.) */

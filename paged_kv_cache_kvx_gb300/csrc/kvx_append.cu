@@ -74,6 +74,19 @@ __device__ __forceinline__ void divide(float *x, float scale, float inverse) {
     }
 }
 
+// Rows with a scale of their own (kvx_cache.scale_offset): the smallest power of
+// two, from 2^-126 on, over which the row's largest finite magnitude is at most
+// 448, as its exponent biased by 127.  In floats with a mantissa of 1.75 at most
+// 448 = 1.75 * 2^8 takes eight octaves off the exponent, with a larger one seven.
+// Such a scale costs no accuracy beside amax / 448 (the values are floating
+// point), takes one byte, and divides, multiplies and reads back without a
+// rounding of its own.
+__device__ __forceinline__ uint32_t row_exponent(float top) {
+    const uint32_t bits = __float_as_uint(top);
+    const int e = (int)(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u);
+    return e < 1 ? 1 : e;
+}
+
 // 1 / scale where that is exact, else 0.
 float exact_inverse(float scale) {
     int e;  // scale = 2^(e-1)
@@ -94,9 +107,10 @@ struct Lane {
 };
 
 enum Kind { kQuery, kKey, kValue };
+enum Store { kSame, kScaled, kRowScaled };  // the queries' type; e4m3 with one scale; e4m3 with one a row
 
 // All of a token's rows of one kind.  Loads run a round ahead.
-template <class T, bool FP8, int LANES, bool NEIGHBOURS, Kind KIND>
+template <class T, Store STORE, int LANES, bool NEIGHBOURS, Kind KIND>
 struct Section {
     const AppendArgs &a;
     const Lane &l;
@@ -119,7 +133,7 @@ struct Section {
     }
     // entry: the block's address-table entries from head 0's K on, or NULL
     __device__ __forceinline__ void run(const void *weight, T *q_out, const uint64_t *entry, uint64_t place, uint64_t room,
-                                        uint32_t &bad) {
+                                        uint64_t scale_place, uint32_t &bad) {
         float w[8];
 #pragma unroll
         for (int e = 0; e < 8; e++) w[e] = 1.0f;
@@ -166,6 +180,15 @@ struct Section {
                         x[j + other] = fmaf(ya, sn[i], yb * cc[i]);
                     }
                 }
+                uint32_t exponent = 0;
+                if constexpr (STORE == kRowScaled && KIND != kQuery) {
+                    float top = 0;  // an infinite value is limited to 448 as it would be by any scale
+#pragma unroll
+                    for (int e = 0; e < 8; e++) top = fmaxf(top, fabsf(x[e]) < INFINITY ? fabsf(x[e]) : 0.0f);
+#pragma unroll
+                    for (int o = LANES / 2; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, o));
+                    exponent = row_exponent(top);
+                }
                 if (!l.in || r >= rows) continue;
                 if constexpr (KIND == kQuery) {
                     T *o = q_out + r * a.c.dim;
@@ -177,7 +200,14 @@ struct Section {
                         continue;
                     }
                     uint8_t *o = a.c.pool + (seg[u] + place);
-                    if constexpr (FP8) {
+                    if constexpr (STORE == kRowScaled) {
+                        const float inverse = __uint_as_float((254 - exponent) << 23);
+#pragma unroll
+                        for (int e = 0; e < 8; e++) x[e] *= inverse;
+                        *reinterpret_cast<uint32_t *>(o + l.da) = e4m3x4(x);
+                        *reinterpret_cast<uint32_t *>(o + l.db) = e4m3x4(x + 4);
+                        if (l.da == 0) a.c.pool[seg[u] + scale_place] = (uint8_t)exponent;
+                    } else if constexpr (STORE == kScaled) {
                         divide(x, KIND == kValue ? a.c.v_scale : a.c.k_scale, KIND == kValue ? a.inv_v_scale : a.inv_k_scale);
                         *reinterpret_cast<uint32_t *>(o + l.da) = e4m3x4(x);
                         *reinterpret_cast<uint32_t *>(o + l.db) = e4m3x4(x + 4);
@@ -195,7 +225,7 @@ struct Section {
 };
 
 // Lanes of a row: a power of two with 8 * LANES >= dim.
-template <class T, bool FP8, int LANES, bool NEIGHBOURS>
+template <class T, Store STORE, int LANES, bool NEIGHBOURS>
 __global__ void __launch_bounds__(kThreads, kMinBlocks) k_append(const __grid_constant__ AppendArgs a) {
     constexpr uint32_t kRows = kThreads / LANES, kWarpRows = 32 / LANES;
     const uint64_t t = blockIdx.x;
@@ -214,9 +244,9 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) k_append(const __grid_co
 
     // Two rounds of latency to the first store: the values, the slot and the
     // position, then the angles and the segments' addresses.
-    Section<T, FP8, LANES, NEIGHBOURS, kQuery> q(a, l, static_cast<const T *>(a.q) + t * a.q_stride, a.q_heads);
-    Section<T, FP8, LANES, NEIGHBOURS, kKey> k(a, l, static_cast<const T *>(a.k) + t * a.k_stride, heads);
-    Section<T, FP8, LANES, NEIGHBOURS, kValue> v(a, l, static_cast<const T *>(a.v) + t * a.v_stride, heads);
+    Section<T, STORE, LANES, NEIGHBOURS, kQuery> q(a, l, static_cast<const T *>(a.q) + t * a.q_stride, a.q_heads);
+    Section<T, STORE, LANES, NEIGHBOURS, kKey> k(a, l, static_cast<const T *>(a.k) + t * a.k_stride, heads);
+    Section<T, STORE, LANES, NEIGHBOURS, kValue> v(a, l, static_cast<const T *>(a.v) + t * a.v_stride, heads);
     q.load(l.first);
     const int64_t slot = a.slots[t];
     const uint32_t pos = a.rot ? a.positions[t] : 0;
@@ -230,10 +260,12 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) k_append(const __grid_co
         l.s = __ldg(reinterpret_cast<const float4 *>(row + a.rot / 2));
     }
     const uint64_t *entry = nullptr;
-    uint64_t place = 0;
+    uint64_t place = 0, scale_place = 0;
     if (slot >= 0) {
         const uint64_t b = (uint64_t)slot < (1ull << 31) ? a.c.page.div((uint32_t)slot) : (uint64_t)slot / a.c.page.d;
-        place = ((uint64_t)slot - b * a.c.page.d) * a.c.token_stride;
+        const uint64_t token = (uint64_t)slot - b * a.c.page.d;
+        place = token * a.c.token_stride;
+        scale_place = token + a.c.scale_offset;
         if (b < a.c.B)
             entry = a.c.lane_addr((uint32_t)b, 0, 0);
         else
@@ -245,26 +277,26 @@ __global__ void __launch_bounds__(kThreads, kMinBlocks) k_append(const __grid_co
         entry = nullptr;
     }
     k.load(l.first);
-    q.run(a.q_weight, static_cast<T *>(a.q_out) + t * a.q_out_stride, nullptr, 0, 0, bad);
+    q.run(a.q_weight, static_cast<T *>(a.q_out) + t * a.q_out_stride, nullptr, 0, 0, 0, bad);
     v.load(l.first);
-    k.run(a.k_weight, nullptr, entry, place, room, bad);
-    v.run(nullptr, nullptr, entry, place, room, bad);
+    k.run(a.k_weight, nullptr, entry, place, room, scale_place, bad);
+    v.run(nullptr, nullptr, entry, place, room, scale_place, bad);
     raise(a.status, bad);
 }
 
-template <class T, bool FP8, bool NEIGHBOURS>
+template <class T, Store STORE, bool NEIGHBOURS>
 void launch_one(const AppendArgs &a, dim3 grid, cudaStream_t s) {
     if (a.c.dim <= 64)
-        k_append<T, FP8, 8, NEIGHBOURS><<<grid, kThreads, 0, s>>>(a);
+        k_append<T, STORE, 8, NEIGHBOURS><<<grid, kThreads, 0, s>>>(a);
     else if (a.c.dim <= 128)
-        k_append<T, FP8, 16, NEIGHBOURS><<<grid, kThreads, 0, s>>>(a);
+        k_append<T, STORE, 16, NEIGHBOURS><<<grid, kThreads, 0, s>>>(a);
     else
-        k_append<T, FP8, 32, NEIGHBOURS><<<grid, kThreads, 0, s>>>(a);
+        k_append<T, STORE, 32, NEIGHBOURS><<<grid, kThreads, 0, s>>>(a);
 }
 
-template <class T, bool FP8>
+template <class T, Store STORE>
 void launch(const AppendArgs &a, dim3 grid, bool neighbours, cudaStream_t s) {
-    neighbours ? launch_one<T, FP8, true>(a, grid, s) : launch_one<T, FP8, false>(a, grid, s);
+    neighbours ? launch_one<T, STORE, true>(a, grid, s) : launch_one<T, STORE, false>(a, grid, s);
 }
 
 }  // namespace
@@ -304,12 +336,16 @@ extern "C" kvx_status kvx_append_tokens(const kvx_cache *cache, const void *q, u
     const bool halves = T > fit && 2 * (uint64_t)T <= 3 * fit && most > 8;
     const uint64_t parts = T < fit ? fit / T : halves ? 2 : 1;
     const dim3 grid(T, (uint32_t)(most < parts ? most : parts));
+    const Store store = cache->scale_offset ? kRowScaled : cache->dtype == KVX_E4M3 ? kScaled : kSame;
+    const cudaStream_t s = as_stream(stream);
     if (dtype == KVX_BF16)
-        cache->dtype == KVX_E4M3 ? launch<__nv_bfloat16, true>(a, grid, interleaved != 0, as_stream(stream))
-                                 : launch<__nv_bfloat16, false>(a, grid, interleaved != 0, as_stream(stream));
+        store == kRowScaled ? launch<__nv_bfloat16, kRowScaled>(a, grid, interleaved != 0, s)
+        : store == kScaled  ? launch<__nv_bfloat16, kScaled>(a, grid, interleaved != 0, s)
+                            : launch<__nv_bfloat16, kSame>(a, grid, interleaved != 0, s);
     else
-        cache->dtype == KVX_E4M3 ? launch<__half, true>(a, grid, interleaved != 0, as_stream(stream))
-                                 : launch<__half, false>(a, grid, interleaved != 0, as_stream(stream));
+        store == kRowScaled ? launch<__half, kRowScaled>(a, grid, interleaved != 0, s)
+        : store == kScaled  ? launch<__half, kScaled>(a, grid, interleaved != 0, s)
+                            : launch<__half, kSame>(a, grid, interleaved != 0, s);
     KVX_LAUNCHED();
     return KVX_OK;
 }

@@ -179,7 +179,7 @@ struct Plan {
 // Sizes that follow from the host's arguments; false where they are refused.
 bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t blocks_per_seq, uint32_t window,
           uint32_t sinks, bool scores, Plan &p) {
-    if (!cache_ok(c) || !q_heads || q_heads % c->heads || q_heads / c->heads > kMaxGroup) return false;
+    if (!cache_ok(c) || c->scale_offset || !q_heads || q_heads % c->heads || q_heads / c->heads > kMaxGroup) return false;
     const uint64_t max_len = (uint64_t)blocks_per_seq * c->page_tokens;
     if (q_heads > 65536u || max_len >= (1ull << 31) || num_seqs >= (1u << 24) || (uint64_t)num_seqs * q_heads >= (1ull << 30)) return false;
     const uint32_t group = q_heads / c->heads;

@@ -1,5 +1,6 @@
-// What the cache operators (kvx_append_tokens, kvx_attend, kvx_evict) share:
-// the checked kvx_cache as kernels see it, and the 16-bit types' conversions.
+// What the cache operators (kvx_append_tokens, kvx_read_tokens, kvx_attend,
+// kvx_attend_shared, kvx_evict) share: the checked kvx_cache as kernels see it,
+// and the 16-bit types' conversions.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -29,7 +30,8 @@ struct CacheView {
     uint64_t pool_bytes;
     const uint64_t *addr;
     uint64_t token_stride;
-    uint64_t span;  // bytes from a segment's first row to the end of its last one
+    uint64_t span;  // bytes from a segment's first row to the end of its last one, or of its scales
+    uint64_t scale_offset;  // of a segment's scales, one byte a token; 0: none
     uint32_t B, L, first_lane, heads, dim;
     uint32_t row_bytes;
     FastDiv page;
@@ -56,11 +58,15 @@ inline bool cache_ok(const kvx_cache *c) {
     if (!c || !c->pool || !c->addr || !aligned16(c->pool)) return false;
     if (c->dtype != KVX_BF16 && c->dtype != KVX_F16 && c->dtype != KVX_E4M3) return false;
     if (!c->dim || c->dim % 16 || c->dim > 256) return false;
-    if (!c->page_tokens || c->page_tokens >= (1u << 31) || !c->heads || !c->B || c->reserved) return false;
+    if (!c->page_tokens || c->page_tokens >= (1u << 31) || !c->heads || !c->B) return false;
     if (c->first_lane > c->L || 2 * (uint64_t)c->heads > c->L - c->first_lane) return false;
     const uint64_t row = (uint64_t)c->dim * elem_size(c->dtype);
     if (c->token_stride % 16 || c->token_stride < row || c->token_stride > (1ull << 31)) return false;
     if (!(c->k_scale > 0 && c->k_scale < INFINITY && c->v_scale > 0 && c->v_scale < INFINITY)) return false;
+    if (c->scale_offset) {  // behind the rows, in place of k_scale and v_scale
+        if (c->dtype != KVX_E4M3 || c->scale_offset % 16 || c->k_scale != 1 || c->v_scale != 1) return false;
+        if (c->scale_offset < (uint64_t)(c->page_tokens - 1) * c->token_stride + row) return false;
+    }
     if (c->dtype != KVX_E4M3 && (c->k_scale != 1 || c->v_scale != 1)) return false;
     return true;
 }
@@ -73,6 +79,8 @@ inline CacheView cache_view(const kvx_cache *c) {
     v.token_stride = c->token_stride;
     v.row_bytes = c->dim * elem_size(c->dtype);
     v.span = (uint64_t)(c->page_tokens - 1) * c->token_stride + v.row_bytes;
+    if (c->scale_offset) v.span = (uint64_t)c->scale_offset + c->page_tokens;
+    v.scale_offset = c->scale_offset;
     v.B = c->B;
     v.L = c->L;
     v.first_lane = c->first_lane;

@@ -404,7 +404,7 @@ bool launch_select(const EvictArgs &a, uint32_t rows, uint32_t size, uint32_t he
 }
 
 bool sizes_ok(const kvx_cache *c, uint32_t num_seqs, uint32_t blocks_per_seq, uint32_t budget) {
-    if (!cache_ok(c) || !budget || budget >= (1u << 31)) return false;
+    if (!cache_ok(c) || c->scale_offset || !budget || budget >= (1u << 31)) return false;
     if ((uint64_t)blocks_per_seq * c->page_tokens >= (1ull << 31)) return false;
     return (ceil_div(budget, kRows) + kMaxCluster) * c->heads * (uint64_t)num_seqs < (1ull << 31);
 }

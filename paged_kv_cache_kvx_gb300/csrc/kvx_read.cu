@@ -1,0 +1,155 @@
+// kvx_read_tokens: tokens of a paged cache read back into dense 16-bit tensors.
+//
+// out[t] = stored * scale, rounded once: the product of an 8-bit value and a
+// scale is taken in 32 bits.  A warp takes one token, whose sequence, page and
+// segment addresses it looks up once for all heads; a lane takes 16 stored bytes
+// at a time.
+#include "kvx_cache.cuh"
+
+namespace kvx {
+namespace {
+
+constexpr int kWarps = 4;   // of a block
+constexpr int kUnroll = 4;  // pieces of a lane on their way
+
+struct ReadArgs {
+    CacheView c;
+    const uint32_t *blocks, *first, *starts;
+    void *out[2];
+    uint64_t stride[2];
+    uint32_t *status;
+    uint32_t num_seqs, blocks_per_seq, T;
+    uint32_t pieces;  // 16-byte pieces of a row
+    FastDiv by_pieces;
+    uint64_t max_len;
+};
+
+// How many of starts[0 .. count-1], which do not decrease, are at most t: by the
+// whole warp, 32 of them at a time.
+__device__ __forceinline__ uint32_t rank_of(const uint32_t *starts, uint32_t count, uint32_t t, uint32_t lane) {
+    uint32_t lo = 0;
+    while (count > 32) {
+        const uint32_t step = (count + 31) / 32;
+        const uint32_t i = lane * step;
+        const uint32_t below = __popc(__ballot_sync(0xFFFFFFFFu, i < count && __ldg(starts + lo + i) <= t));
+        if (!below) return lo;
+        const uint32_t at = (below - 1) * step;
+        lo += at;
+        count = count - at < step ? count - at : step;
+    }
+    return lo + __popc(__ballot_sync(0xFFFFFFFFu, lane < count && __ldg(starts + lo + lane) <= t));
+}
+
+__device__ __forceinline__ float row_scale(uint32_t e) {
+    return __uint_as_float(e == 255 ? 0x7FFFFFFFu : e ? e << 23 : 0x400000u);
+}
+
+// Four stored 8-bit values times a scale, as 16-bit ones.
+template <class T>
+__device__ __forceinline__ uint2 scaled4(uint32_t four, float scale) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
+    const float2 x = Pair<__half>::unpack(lo), y = Pair<__half>::unpack(hi);
+    return make_uint2(Pair<T>::pack(x.x * scale, x.y * scale), Pair<T>::pack(y.x * scale, y.y * scale));
+}
+
+template <class T, bool FP8>
+__global__ void __launch_bounds__(32 * kWarps) k_read(const __grid_constant__ ReadArgs a) {
+    const uint32_t lane = threadIdx.x & 31;
+    const uint32_t t = blockIdx.x * kWarps + threadIdx.x / 32;
+    uint32_t bad = 0;
+    if (blockIdx.x == 0)  // the table itself
+        for (uint32_t n = threadIdx.x; n < a.num_seqs; n += 32 * kWarps)
+            if (a.starts[n] > a.starts[n + 1] || a.starts[n + 1] > a.T) bad |= KVX_S_BOUNDS;
+    uint32_t seq = kNone;
+    if (t < a.T) seq = rank_of(a.starts, a.num_seqs + 1, t, lane) - 1;  // none: t is before the first start
+    if (seq < a.num_seqs) {
+        const uint32_t start = __ldg(a.starts + seq);
+        const uint64_t pos = (uint64_t)(a.first ? __ldg(a.first + seq) : 0) + (t - start);
+        uint32_t id = kNone;
+        if (start <= t && pos < a.max_len) {
+            const uint32_t page = a.c.page.div((uint32_t)pos);
+            id = __ldg(a.blocks + (uint64_t)seq * a.blocks_per_seq + page);
+            const uint32_t token = (uint32_t)pos - page * a.c.page.d;
+            if (id < a.c.B) {
+                const uint64_t *entry = a.c.lane_addr(id, 0, 0);
+                const uint32_t total = 2 * a.c.heads * a.pieces;
+                const uint64_t place = token * a.c.token_stride;
+                for (uint32_t i0 = lane; i0 < total; i0 += 32 * kUnroll) {
+                    uint32_t lane_of[kUnroll], piece[kUnroll];
+                    bool ok[kUnroll];
+                    uint64_t seg[kUnroll];
+                    uint4 raw[kUnroll];
+                    uint32_t e[kUnroll];
+#pragma unroll
+                    for (int u = 0; u < kUnroll; u++) {
+                        const uint32_t i = i0 + 32 * u;
+                        lane_of[u] = a.by_pieces.div(i);
+                        piece[u] = i - lane_of[u] * a.pieces;
+                        ok[u] = i < total;
+                        seg[u] = ok[u] ? __ldg(entry + lane_of[u]) : 0;
+                    }
+#pragma unroll
+                    for (int u = 0; u < kUnroll; u++) {
+                        ok[u] = ok[u] && a.c.ok(seg[u], bad);
+                        raw[u] = ok[u] ? __ldg(reinterpret_cast<const uint4 *>(a.c.pool + seg[u] + place) + piece[u]) : make_uint4(0, 0, 0, 0);
+                        e[u] = FP8 && ok[u] && a.c.scale_offset ? __ldg(a.c.pool + seg[u] + a.c.scale_offset + token) : 127;
+                    }
+#pragma unroll
+                    for (int u = 0; u < kUnroll; u++) {
+                        if (!ok[u]) continue;
+                        const uint32_t kv = lane_of[u] & 1, head = lane_of[u] >> 1;
+                        T *o = static_cast<T *>(a.out[kv]) + t * a.stride[kv] + (uint64_t)head * a.c.dim + piece[u] * (FP8 ? 16 : 8);
+                        if constexpr (FP8) {
+                            const float scale = a.c.scale_offset ? row_scale(e[u]) : kv ? a.c.v_scale : a.c.k_scale;
+                            const uint2 w0 = scaled4<T>(raw[u].x, scale), w1 = scaled4<T>(raw[u].y, scale);
+                            const uint2 w2 = scaled4<T>(raw[u].z, scale), w3 = scaled4<T>(raw[u].w, scale);
+                            reinterpret_cast<uint4 *>(o)[0] = make_uint4(w0.x, w0.y, w1.x, w1.y);
+                            reinterpret_cast<uint4 *>(o)[1] = make_uint4(w2.x, w2.y, w3.x, w3.y);
+                        } else {
+                            *reinterpret_cast<uint4 *>(o) = raw[u];
+                        }
+                    }
+                }
+            } else {
+                bad |= KVX_S_BOUNDS;
+            }
+        } else {
+            bad |= KVX_S_BOUNDS;
+        }
+    }
+    raise(a.status, bad);
+}
+
+}  // namespace
+}  // namespace kvx
+
+extern "C" kvx_status kvx_read_tokens(const kvx_cache *cache, const uint32_t *blocks, uint32_t num_seqs,
+                                      uint32_t blocks_per_seq, const uint32_t *first, const uint32_t *starts, uint32_t T,
+                                      uint32_t dtype, void *k_out, uint64_t k_stride, void *v_out, uint64_t v_stride,
+                                      uint32_t *status, void *stream) {
+    using namespace kvx;
+    if (!cache_ok(cache) || (dtype != KVX_BF16 && dtype != KVX_F16) || !status) return KVX_EINVAL;
+    if (cache->dtype != dtype && cache->dtype != KVX_E4M3) return KVX_EINVAL;
+    const uint64_t max_len = (uint64_t)blocks_per_seq * cache->page_tokens;
+    if (T > 0x7FFFFFFFu || num_seqs > 0x7FFFFFFFu || max_len >= (1ull << 31) || cache->heads > 65536u) return KVX_EINVAL;
+    if ((k_stride | v_stride) % 8 || !aligned16(k_out) || !aligned16(v_out)) return KVX_EINVAL;
+    if (!T || !num_seqs) return KVX_OK;
+    if (!k_out || !v_out || !starts || (max_len && !blocks)) return KVX_EINVAL;
+    ReadArgs a = {cache_view(cache), blocks, first, starts, {k_out, v_out}, {k_stride, v_stride}, status, num_seqs,
+                  blocks_per_seq, T, 0, FastDiv(1), max_len};
+    a.pieces = a.c.row_bytes / 16;
+    a.by_pieces = FastDiv(a.pieces);
+    const uint32_t grid = (uint32_t)ceil_div(T, kWarps);
+    const cudaStream_t s = as_stream(stream);
+    const bool fp8 = cache->dtype == KVX_E4M3;
+    if (dtype == KVX_BF16)
+        fp8 ? k_read<__nv_bfloat16, true><<<grid, 32 * kWarps, 0, s>>>(a)
+            : k_read<__nv_bfloat16, false><<<grid, 32 * kWarps, 0, s>>>(a);
+    else
+        fp8 ? k_read<__half, true><<<grid, 32 * kWarps, 0, s>>>(a) : k_read<__half, false><<<grid, 32 * kWarps, 0, s>>>(a);
+    KVX_LAUNCHED();
+    return KVX_OK;
+}

@@ -46,7 +46,7 @@ _F = ctypes.c_float
 
 
 class CacheStruct(ctypes.Structure):
-    """struct kvx_cache (include/kvx.h)"""
+    """struct kvx_cache (include/kvx.h); its scale_offset is the field `reserved`"""
     _fields_ = [("pool", _P), ("pool_bytes", _U64), ("addr", _P), ("B", _U32), ("L", _U32), ("first_lane", _U32),
                 ("heads", _U32), ("dim", _U32), ("dtype", _U32), ("page_tokens", _U32), ("reserved", _U32),
                 ("token_stride", _U64), ("k_scale", _F), ("v_scale", _F)]
@@ -86,6 +86,9 @@ _SIGS = {
     "kvx_append_tokens": (ctypes.c_int, [_P] * 12 + [_F] + [_P] * 10),
     "kvx_attend_workspace_size": (_SZ, [_P, _U32, _U32, _U32, _U32, _U32, _U32]),
     "kvx_attend": (ctypes.c_int, [_P] * 9 + [_F] + [_P] * 11),
+    "kvx_attend_shared_workspace_size": (_SZ, [_P, _U32, _U32, _U32, _U32, _U32]),
+    "kvx_attend_shared": (ctypes.c_int, [_P] * 14 + [_F] + [_P] * 7),
+    "kvx_read_tokens": (ctypes.c_int, [_P] * 14),
     "kvx_evict_workspace_size": (_SZ, [_P, _U32, _U32, _U32]),
     "kvx_evict": (ctypes.c_int, [_P] * 19),
     "kvx_selftest_timeouts": (ctypes.c_int, [_P, _P]),
@@ -313,6 +316,26 @@ def kvx_attend(cache, q, q_stride, dtype, num_seqs, q_heads, blocks, blocks_per_
                             blocks_per_seq, _ptr(lens), scale, window, sinks, _ptr(out), out_stride, _ptr(lse),
                             _ptr(scores), scores_stride, _ptr(status), _ptr(ws), ws.numel(), _stream(stream)),
            "kvx_attend")
+
+
+def kvx_attend_shared_workspace_size(cache, num_seqs: int, q_heads: int, blocks_per_seq: int, num_groups: int,
+                                     blocks_per_prefix: int) -> int:
+    return int(lib().kvx_attend_shared_workspace_size(ctypes.byref(cache), num_seqs, q_heads, blocks_per_seq, num_groups,
+                                                      blocks_per_prefix))
+
+
+def kvx_attend_shared(cache, q, q_stride, dtype, num_seqs, q_heads, prefix_blocks, blocks_per_prefix, prefix_lens, group_first,
+                      num_groups, blocks, blocks_per_seq, lens, scale, out, out_stride, lse, status, ws, ws_bytes, stream=None):
+    _check(lib().kvx_attend_shared(ctypes.byref(cache), _ptr(q), q_stride, dtype, num_seqs, q_heads, _ptr(prefix_blocks),
+                                   blocks_per_prefix, _ptr(prefix_lens), _ptr(group_first), num_groups, _ptr(blocks),
+                                   blocks_per_seq, _ptr(lens), scale, _ptr(out), out_stride, _ptr(lse), _ptr(status), _ptr(ws),
+                                   ws_bytes, _stream(stream)), "kvx_attend_shared")
+
+
+def kvx_read_tokens(cache, blocks, num_seqs, blocks_per_seq, first, starts, T, dtype, k_out, k_stride, v_out, v_stride, status,
+                    stream=None):
+    _check(lib().kvx_read_tokens(ctypes.byref(cache), _ptr(blocks), num_seqs, blocks_per_seq, _ptr(first), _ptr(starts), T, dtype,
+                                 _ptr(k_out), k_stride, _ptr(v_out), v_stride, _ptr(status), _stream(stream)), "kvx_read_tokens")
 
 
 def kvx_evict_workspace_size(cache, num_seqs: int, blocks_per_seq: int, budget: int) -> int:
@@ -568,13 +591,15 @@ class Cache:
     """One layer's paged cache in a pool (struct kvx_cache): block b's K and V
     segments of head h start at the bytes addr[b, first_lane + 2*h] and
     addr[b, first_lane + 2*h + 1], so the address table of a transfer serves as it is.
+    With scale_offset (float8_e4m3fn) each row has a scale of its own, one byte of
+    float8_e8m0fnu per token from that byte of the segment on.
     The object keeps the pool and the table alive and owns one status word;
-    workspaces are the caller's (attend_workspace, evict_workspace: uint8
-    tensors, one per stream that calls concurrently).  Every tensor of a call is
+    workspaces are the caller's (attend_workspace, attend_shared_workspace,
+    evict_workspace: uint8 tensors, one per stream that calls concurrently).  Every tensor of a call is
     on the pool's GPU, which is the current device."""
 
     def __init__(self, pool, addr, heads: int, dim: int, dtype, page_tokens: int, first_lane: int = 0,
-                 token_stride: int | None = None, k_scale: float = 1.0, v_scale: float = 1.0):
+                 token_stride: int | None = None, k_scale: float = 1.0, v_scale: float = 1.0, scale_offset: int = 0):
         _need(pool.dtype == torch.uint8 and pool.is_contiguous(), "pool: contiguous uint8")
         _need(addr.dim() == 2 and addr.dtype in (torch.int64, torch.uint64) and addr.is_contiguous(),
               "addr: contiguous [blocks, lanes] of 64-bit byte offsets")
@@ -585,8 +610,8 @@ class Cache:
         row = self.dim * dtype.itemsize
         self.c = CacheStruct(pool=pool.data_ptr(), pool_bytes=pool.numel(), addr=addr.data_ptr(), B=addr.size(0),
                              L=addr.size(1), first_lane=first_lane, heads=heads, dim=dim, dtype=_DTYPES[dtype],
-                             page_tokens=page_tokens, token_stride=row if token_stride is None else token_stride,
-                             k_scale=k_scale, v_scale=v_scale)
+                             page_tokens=page_tokens, reserved=scale_offset,
+                             token_stride=row if token_stride is None else token_stride, k_scale=k_scale, v_scale=v_scale)
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self._ref, self._status, self._device = ctypes.byref(self.c), self.status.data_ptr(), pool.get_device()
 
@@ -649,6 +674,49 @@ class Cache:
                                 dim ** -0.5 if scale is None else scale, window, sinks, out.data_ptr(),
                                 _heads(out, "out", queries, act, dev), sums, weights, stride, self._status,
                                 _scratch(ws, dev), ws.numel(), self._stream(stream)), "kvx_attend")
+
+    def attend_shared_workspace(self, num_seqs: int, q_heads: int, blocks_per_seq: int, num_groups: int,
+                                blocks_per_prefix: int):
+        n = kvx_attend_shared_workspace_size(self.c, num_seqs, q_heads, blocks_per_seq, num_groups, blocks_per_prefix)
+        _need(n > 0, "attend_shared: refused sizes")
+        return torch.empty(n, dtype=torch.uint8, device=self.pool.device)
+
+    def attend_shared(self, q, prefix_blocks, prefix_lens, group_first, blocks, lens, out, ws, scale: float | None = None,
+                      lse=None, stream=None):
+        """kvx_attend_shared: as attend, with prefix_blocks int32 [num_groups,
+        blocks_per_prefix] and prefix_lens int32 [num_groups] of the prefixes that
+        the sequences group_first[g] .. group_first[g+1] - 1 share; group_first
+        int32 [num_groups + 1]."""
+        _need(q.dim() == 3 and blocks.dim() == 2 and prefix_blocks.dim() == 2, "q: [num_seqs, q_heads, dim], blocks: "
+              "[num_seqs, blocks_per_seq], prefix_blocks: [num_groups, blocks_per_prefix]")
+        (N, q_heads, _), act, dim, dev, per = q.shape, q.dtype, self.dim, self._device, blocks.shape[1]
+        groups, pper = prefix_blocks.shape
+        _need(act in _ACTS, "q: bfloat16 or float16")
+        queries = (N, q_heads, dim)
+        _check(lib().kvx_attend_shared(self._ref, q.data_ptr(), _heads(q, "q", queries, act, dev), _DTYPES[act], N, q_heads,
+                                       _table(prefix_blocks, "prefix_blocks", _IDS, (groups, pper), dev), pper,
+                                       _table(prefix_lens, "prefix_lens", _IDS, (groups,), dev),
+                                       _table(group_first, "group_first", _IDS, (groups + 1,), dev), groups,
+                                       _table(blocks, "blocks", _IDS, (N, per), dev), per, _table(lens, "lens", _IDS, (N,), dev),
+                                       dim ** -0.5 if scale is None else scale, out.data_ptr(),
+                                       _heads(out, "out", queries, act, dev),
+                                       None if lse is None else _table(lse, "lse", _FLOAT, (N, q_heads), dev), self._status,
+                                       _scratch(ws, dev), ws.numel(), self._stream(stream)), "kvx_attend_shared")
+
+    def read(self, blocks, starts, k_out, v_out, first=None, stream=None):
+        """kvx_read_tokens: rows starts[n] .. starts[n+1] - 1 of k_out and v_out
+        [T, heads, dim] get sequence n's tokens from first[n] (or 0) on; blocks int32
+        [num_seqs, blocks_per_seq]; starts int32 [num_seqs + 1]; first int32
+        [num_seqs]."""
+        _need(blocks.dim() == 2 and k_out.dim() == 3, "blocks: [num_seqs, blocks_per_seq], k_out: [tokens, heads, dim]")
+        (N, per), T, act, dev = blocks.shape, k_out.shape[0], k_out.dtype, self._device
+        _need(act in _ACTS, "k_out: bfloat16 or float16")
+        rows = (T, self.heads, self.dim)
+        ks, vs = _heads(k_out, "k_out", rows, act, dev), _heads(v_out, "v_out", rows, act, dev)
+        _check(lib().kvx_read_tokens(self._ref, _table(blocks, "blocks", _IDS, (N, per), dev), N, per,
+                                     None if first is None else _table(first, "first", _IDS, (N,), dev),
+                                     _table(starts, "starts", _IDS, (N + 1,), dev), T, _DTYPES[act], k_out.data_ptr(), ks,
+                                     v_out.data_ptr(), vs, self._status, self._stream(stream)), "kvx_read_tokens")
 
     def evict_workspace(self, num_seqs: int, blocks_per_seq: int, budget: int):
         n = kvx_evict_workspace_size(self.c, num_seqs, blocks_per_seq, budget)
