@@ -92,6 +92,11 @@ inline CacheView cache_view(const kvx_cache *c) {
     return v;
 }
 
+// The power of two that a row's scale byte stands for (kvx_cache.scale_offset).
+__device__ __forceinline__ float row_scale(uint32_t e) {
+    return __uint_as_float(e == 255 ? 0x7FFFFFFFu : e ? e << 23 : 0x400000u);
+}
+
 // Pairs of 16-bit values and floats.
 template <class T>
 struct Pair;

@@ -40,10 +40,6 @@ __device__ __forceinline__ uint32_t rank_of(const uint32_t *starts, uint32_t cou
     return lo + __popc(__ballot_sync(0xFFFFFFFFu, lane < count && __ldg(starts + lo + lane) <= t));
 }
 
-__device__ __forceinline__ float row_scale(uint32_t e) {
-    return __uint_as_float(e == 255 ? 0x7FFFFFFFu : e ? e << 23 : 0x400000u);
-}
-
 // Four stored 8-bit values times a scale, as 16-bit ones.
 template <class T>
 __device__ __forceinline__ uint2 scaled4(uint32_t four, float scale) {

@@ -1,96 +1,196 @@
 // kvx_attend_shared: attention of one new token per sequence over a prefix that
 // a group of sequences shares, and the sequence's own tokens.
-#include "kvx_cache.cuh"
+//
+// k_shared (kvx_shared.cuh) leaves partial results o_c = sum 2^(x_j - m_c) v_j,
+// l_c = sum 2^(x_j - m_c) of prefixes and of own tokens, logits x in powers of
+// two; k_join puts a query's together,
+//     M = max m_c,  L = sum l_c 2^(m_c - M),  out = sum o_c 2^(m_c - M) / L
+// in a fixed order.
+#include "kvx_shared.cuh"
 
 namespace kvx {
 namespace shared {
+
+// instantiated in kvx_shared_<types>.cu, a file each so that they compile in parallel
+extern template bool launch<__nv_bfloat16, 2>(const Args &, cudaStream_t);
+extern template bool launch<__nv_bfloat16, 1>(const Args &, cudaStream_t);
+extern template bool launch<__half, 2>(const Args &, cudaStream_t);
+extern template bool launch<__half, 1>(const Args &, cudaStream_t);
+
 namespace {
 
 constexpr uint32_t kMaxGroup = 128;
+constexpr uint32_t kJoinWarps = 4;
+constexpr uint32_t kJoinParts = 128;  // whose weights a block holds
+constexpr int kJoinUnroll = 4;        // parts whose loads a warp has in flight
 
-struct Args {
-    CacheView c;
-    const void *q;
-    uint64_t q_stride;
-    const uint32_t *prefix_blocks, *prefix_lens, *group_first, *blocks, *lens;
-    uint32_t blocks_per_prefix, num_groups, blocks_per_seq, num_seqs, q_heads, group;
-    uint32_t max_prefix, max_len;
-    float scale;
-    void *out;
-    uint64_t out_stride;
-    float *lse;
-    uint32_t *status;
+// The parts of a query's results over one set of keys: `subs` rows for each block
+// first .. first + blocks-1.
+struct Parts {
+    uint32_t row, cap, off_b, subs, blocks;
+    __device__ __forceinline__ uint32_t count() const { return blocks * subs; }
+    __device__ __forceinline__ uint64_t at(uint32_t i) const {
+        return subs == 2 ? row + (uint64_t)(i >> 1) * cap + (i & 1) * off_b : row + (uint64_t)i * cap;
+    }
 };
 
-// One warp for each query head: a lane has eight values of it.
-template <class T, int ES>
-__global__ void __launch_bounds__(32) k_simple(const __grid_constant__ Args a) {
-    const uint32_t n = blockIdx.x, head = blockIdx.y, lane = threadIdx.x, h = head / a.group;
-    const bool in = lane * 8 < a.c.dim;
-    uint32_t bad = 0;
-    float q[8] = {}, o[8] = {}, m = -INFINITY, l = 0;
-    if (in)
-        for (int i = 0; i < 8; i++)
-            q[i] = (float)static_cast<const T *>(a.q)[n * a.q_stride + (uint64_t)head * a.c.dim + lane * 8 + i] * a.scale;
-    uint32_t g = kNone;
-    for (uint32_t i = 0; i < a.num_groups; i++) {
-        const uint32_t from = a.group_first[i], to = a.group_first[i + 1];
-        if (from > to || to > a.num_seqs) bad |= KVX_S_BOUNDS;
-        if (from <= n && n < to && to <= a.num_seqs) g = i;
+// A block for each query.
+template <class T>
+__global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant__ Args a) {
+    __shared__ float sh_m[kJoinWarps], sh_l[kJoinWarps], sh_w[kJoinParts];
+    __shared__ float4 sh_o[kJoinWarps][64];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
+    const uint32_t n = blockIdx.x / a.q_heads, x = blockIdx.x - n * a.q_heads, head = x / a.group, in = x - head * a.group;
+    // the group: the last that starts at n or before
+    uint32_t lo = 0, hi = a.num_groups;
+    while (lo < hi) {
+        const uint32_t mid = (lo + hi) / 2;
+        if (__ldg(a.group_first + mid) <= n)
+            lo = mid + 1;
+        else
+            hi = mid;
     }
-    for (int part = 0; part < 2; part++) {
-        if (!part && g == kNone) continue;
-        uint32_t len = part ? a.lens[n] : a.prefix_lens[g];
-        const uint32_t most = part ? a.max_len : a.max_prefix;
-        if (len > most) len = most, bad |= KVX_S_BOUNDS;
-        const uint32_t *table = part ? a.blocks + (uint64_t)n * a.blocks_per_seq : a.prefix_blocks + (uint64_t)g * a.blocks_per_prefix;
-        for (uint32_t j = 0; j < len; j++) {
-            const uint32_t page = a.c.page.div(j), id = table[page], token = j - page * a.c.page.d;
-            float x[2][8] = {};
-            if (id >= a.c.B) {
-                bad |= KVX_S_BOUNDS;
-            } else {
-                for (int kv = 0; kv < 2; kv++) {
-                    const uint64_t seg = *a.c.lane_addr(id, h, kv);
-                    if (!a.c.ok(seg, bad) || !in) continue;
-                    const uint8_t *row = a.c.pool + seg + token * a.c.token_stride + lane * 8 * ES;
-                    const uint32_t e = ES == 1 && a.c.scale_offset ? a.c.pool[seg + a.c.scale_offset + token] : 127;
-                    const float s = a.c.scale_offset ? __uint_as_float(e == 255 ? 0x7FFFFFFFu : e ? e << 23 : 0x400000u) : kv ? a.c.v_scale : a.c.k_scale;
-                    for (int i = 0; i < 8; i++) {
-                        if (ES == 1) {
-                            uint32_t v;
-                            asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v) : "h"((uint16_t)row[i]));
-                            x[kv][i] = Pair<__half>::unpack(v).x * s;
-                        } else {
-                            x[kv][i] = (float)reinterpret_cast<const T *>(row)[i];
-                        }
-                    }
-                }
-            }
-            float s = 0;
-            for (int i = 0; i < 8; i++) s += q[i] * x[0][i];
-            for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-            const float top = fmaxf(m, s);
-            if (top == -INFINITY) continue;
-            const float r = expf(m - top), p = expf(s - top);
-            m = top;
-            l = l * r + p;
-            for (int i = 0; i < 8; i++) o[i] = o[i] * r + p * x[1][i];
+    const bool wide = a.c.dim > 128;
+    Parts parts[2] = {};
+    uint2 const *where[2] = {};
+    if (lo) {
+        const Entry e = entry_of(a, lo - 1);
+        if (e.len && n - e.seq0 < e.rows / a.group) {
+            const uint32_t row = (n - e.seq0) * a.group + in, mt = row / a.tile_rows;
+            const uint32_t rows = e.rows - mt * a.tile_rows;
+            const uint32_t u = (prefix_tile(a, e.seq0, lo - 1) + mt) * a.c.heads + head;
+            where[0] = a.prefix_parts + u;
+            parts[0] = Parts{u * a.prefix_cap + row - mt * a.tile_rows, a.prefix_cap, a.prefix_off_b,
+                             wide || rows > kRows ? 1u : 2u, 0};
         }
     }
-    const float inv = l != 0 ? 1.0f / l : 0.0f;
-    if (in)
-        for (int i = 0; i < 8; i++)
-            static_cast<T *>(a.out)[n * a.out_stride + (uint64_t)head * a.c.dim + lane * 8 + i] = (T)(o[i] * inv);
-    if (a.lse && lane == 0) a.lse[(uint64_t)n * a.q_heads + head] = l != 0 ? m + logf(l) : -INFINITY;
-    raise(a.status, bad);
+    const Entry own = entry_of(a, a.num_groups + n);
+    if (own.len) {
+        const uint32_t u = n * a.c.heads + head;
+        where[1] = a.own_parts + u;
+        parts[1] = Parts{a.own_first_row + u * a.own_cap + in, a.own_cap, a.own_off_b, wide ? 1u : 2u, 0};
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    for (int k = 0; k < 2; k++) {
+        if (!where[k]) continue;
+        const uint2 w = __ldcg(where[k]);
+        if (w.x > w.y || w.y >= a.grid) continue;  // left by a block whose wait ran out
+        parts[k].blocks = w.y - w.x + 1;
+        parts[k].row += w.x * parts[k].cap;
+    }
+    const uint32_t first = parts[0].count(), all = first + parts[1].count();
+    auto at = [&](uint32_t i) { return i < first ? parts[0].at(i) : parts[1].at(i - first); };
+    float top = -INFINITY, sum = 0;
+    float4 o[2] = {};
+    for (uint32_t i0 = 0; i0 < all; i0 += kJoinParts) {
+        // the parts' bases and sums; 0 stands for none, whose outputs do not exist
+        const uint32_t here = all - i0 < kJoinParts ? all - i0 : kJoinParts;
+        float2 ml = make_float2(-INFINITY, 0);
+        if (threadIdx.x < here) ml = __ldcg(a.part_ml + at(i0 + threadIdx.x));
+        if (ml.y == 0) ml.x = -INFINITY;
+        float higher = ml.x;
+        for (int d = 16; d; d >>= 1) higher = fmaxf(higher, __shfl_xor_sync(0xFFFFFFFFu, higher, d));
+        if (lane == 0) sh_m[warp] = higher;
+        __syncthreads();
+        higher = top;
+        for (uint32_t w = 0; w < kJoinWarps; w++) higher = fmaxf(higher, sh_m[w]);
+        const float old = top == -INFINITY ? 0.0f : exp2_fast(top - higher);
+        // (an infinite base comes with a NaN sum, which stays one)
+        const float weight = ml.y == 0 ? 0.0f : exp2_fast(ml.x - higher);
+        top = higher;
+        sh_w[threadIdx.x] = weight;
+        float s = ml.y == 0 ? 0.0f : ml.y * weight;
+        for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
+        if (lane == 0) sh_l[warp] = s;
+        __syncthreads();
+        sum *= old;
+        for (uint32_t w = 0; w < kJoinWarps; w++) sum += sh_l[w];
+#pragma unroll
+        for (int k = 0; k < 2; k++) o[k].x *= old, o[k].y *= old, o[k].z *= old, o[k].w *= old;
+        for (uint32_t i = warp; i < here; i += kJoinWarps * kJoinUnroll) {
+            float4 v[kJoinUnroll][2] = {};
+            float w[kJoinUnroll];
+#pragma unroll
+            for (int u = 0; u < kJoinUnroll; u++) {
+                const uint32_t j = i + u * kJoinWarps;
+                w[u] = j < here ? sh_w[j] : 0.0f;
+                if (w[u] == 0) continue;  // (a NaN is none)
+                const float *from = a.part_o + at(i0 + j) * a.c.dim;
+#pragma unroll
+                for (int k = 0; k < 2; k++)
+                    if (k * 128 + lane * 4 < a.c.dim) v[u][k] = __ldcg(reinterpret_cast<const float4 *>(from + k * 128) + lane);
+            }
+#pragma unroll
+            for (int u = 0; u < kJoinUnroll; u++)
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    o[k].x += v[u][k].x * w[u], o[k].y += v[u][k].y * w[u];
+                    o[k].z += v[u][k].z * w[u], o[k].w += v[u][k].w * w[u];
+                }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int k = 0; k < 2; k++) sh_o[warp][k * 32 + lane] = o[k];
+    __syncthreads();
+    const uint32_t d = threadIdx.x * 4;
+    if (d < a.c.dim) {
+        float4 v = sh_o[0][threadIdx.x];
+        for (uint32_t w = 1; w < kJoinWarps; w++) {
+            const float4 y = sh_o[w][threadIdx.x];
+            v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+        }
+        const float inv = sum == 0 ? 0.0f : a.c.v_scale / sum;
+        T *to = static_cast<T *>(a.out) + (uint64_t)n * a.out_stride + (uint64_t)x * a.c.dim + d;
+        *reinterpret_cast<uint2 *>(to) = make_uint2(Pair<T>::pack(v.x * inv, v.y * inv), Pair<T>::pack(v.z * inv, v.w * inv));
+    }
+    if (a.lse && threadIdx.x == 0)
+        a.lse[blockIdx.x] = sum == 0 ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
-bool sizes_ok(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t blocks_per_seq, uint32_t num_groups,
-              uint32_t blocks_per_prefix) {
+// Sizes of the call, known on the host: the lengths are not, so every bound is the tables'.
+struct Plan {
+    uint32_t max_len, max_prefix, grid;
+    uint32_t tile_rows, prefix_cap, prefix_off_b, own_cap, own_off_b;
+    uint64_t prefix_units, own_units, own_first_row, rows;
+};
+
+bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t blocks_per_seq, uint32_t num_groups,
+          uint32_t blocks_per_prefix, Plan &p) {
     if (!cache_ok(c) || !q_heads || q_heads % c->heads || q_heads / c->heads > kMaxGroup) return false;
     const uint64_t len = (uint64_t)blocks_per_seq * c->page_tokens, prefix = (uint64_t)blocks_per_prefix * c->page_tokens;
-    return len < (1ull << 31) && prefix < (1ull << 31) && num_seqs < (1u << 31) && num_groups < (1u << 31);
+    if (len >= (1ull << 31) || prefix >= (1ull << 31)) return false;
+    if (num_seqs >= (1u << 30) || num_groups >= (1u << 30) || (uint64_t)num_seqs * q_heads >= (1ull << 31)) return false;
+    const uint32_t group = q_heads / c->heads, keys = c->dim > 128 ? 64 : 128;
+    const bool wide = c->dim > 128;
+    const uint64_t queries = (uint64_t)num_seqs * group;
+    p.max_len = (uint32_t)len, p.max_prefix = (uint32_t)prefix;
+    p.tile_rows = wide ? 128 : 256;
+    // a part's rows: both slots', where they have the same ones
+    const uint32_t few = queries < kRows ? (uint32_t)queries : kRows;
+    p.prefix_off_b = wide ? 0 : few;
+    p.prefix_cap = wide ? few : 2 * few;
+    p.own_off_b = wide ? 0 : group;
+    p.own_cap = wide ? group : 2 * group;
+    const uint64_t tiles = num_groups ? queries / p.tile_rows + num_groups : 0;
+    p.prefix_units = tiles * c->heads;
+    p.own_units = (uint64_t)num_seqs * c->heads;
+    const uint64_t most = p.prefix_units * (ceil_div(prefix, keys) + kExtra) + p.own_units * (ceil_div(len, keys) + kExtra);
+    if (tiles >= (1ull << 31) || p.prefix_units >= (1ull << 31) || most >= (1ull << 31)) return false;
+    const uint64_t want = ceil_div(most, kMinShare);
+    p.grid = want < (uint64_t)sm_count() ? (want ? (uint32_t)want : 1) : (uint32_t)sm_count();
+    p.own_first_row = num_groups ? (p.prefix_units + p.grid) * p.prefix_cap : 0;
+    p.rows = p.own_first_row + (p.own_units + p.grid) * p.own_cap;
+    return p.rows < (1ull << 32);
+}
+
+size_t carve(const Plan &p, const kvx_cache *c, void *ws, Args *a) {
+    Carver w(ws);
+    float *o = w.take<float>(p.rows * c->dim);
+    float2 *ml = w.take<float2>(p.rows);
+    uint2 *prefix = w.take<uint2>(p.prefix_units), *own = w.take<uint2>(p.own_units);
+    if (a) a->part_o = o, a->part_ml = ml, a->prefix_parts = prefix, a->own_parts = own;
+    return w.off;
 }
 
 }  // namespace
@@ -100,7 +200,9 @@ bool sizes_ok(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t 
 extern "C" size_t kvx_attend_shared_workspace_size(const kvx_cache *cache, uint32_t num_seqs, uint32_t q_heads,
                                                    uint32_t blocks_per_seq, uint32_t num_groups,
                                                    uint32_t blocks_per_prefix) {
-    return kvx::shared::sizes_ok(cache, num_seqs, q_heads, blocks_per_seq, num_groups, blocks_per_prefix) ? 256 : 0;
+    using namespace kvx::shared;
+    Plan p;
+    return plan(cache, num_seqs, q_heads, blocks_per_seq, num_groups, blocks_per_prefix, p) ? carve(p, cache, nullptr, nullptr) : 0;
 }
 
 extern "C" kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q, uint64_t q_stride, uint32_t dtype,
@@ -112,26 +214,50 @@ extern "C" kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q, u
                                         void *stream) {
     using namespace kvx;
     using namespace kvx::shared;
-    if (!sizes_ok(cache, num_seqs, q_heads, blocks_per_seq, num_groups, blocks_per_prefix)) return KVX_EINVAL;
+    Plan p;
+    if (!plan(cache, num_seqs, q_heads, blocks_per_seq, num_groups, blocks_per_prefix, p)) return KVX_EINVAL;
     if ((dtype != KVX_BF16 && dtype != KVX_F16) || (cache->dtype != dtype && cache->dtype != KVX_E4M3)) return KVX_EINVAL;
     if (!status || !(scale > -INFINITY && scale < INFINITY)) return KVX_EINVAL;
     if ((q_stride | out_stride) % 8 || !aligned16(q) || !aligned16(out)) return KVX_EINVAL;
     if (!num_seqs) return KVX_OK;
-    const uint32_t max_len = blocks_per_seq * cache->page_tokens, max_prefix = blocks_per_prefix * cache->page_tokens;
-    if (!q || !out || !lens || (max_len && !blocks)) return KVX_EINVAL;
-    if (num_groups && (!prefix_lens || !group_first || (max_prefix && !prefix_blocks))) return KVX_EINVAL;
-    if (!ws || !aligned16(ws) ||
-        ws_bytes < kvx_attend_shared_workspace_size(cache, num_seqs, q_heads, blocks_per_seq, num_groups, blocks_per_prefix))
-        return KVX_EINVAL;
-    Args a = {cache_view(cache), q, q_stride, prefix_blocks, prefix_lens, group_first, blocks, lens, blocks_per_prefix,
-              num_groups, blocks_per_seq, num_seqs, q_heads, q_heads / cache->heads, max_prefix, max_len, scale, out,
-              out_stride, lse, status};
-    const dim3 grid(num_seqs, q_heads);
+    if (!q || !out || !lens || (p.max_len && !blocks)) return KVX_EINVAL;
+    if (num_groups && (!prefix_lens || !group_first || (p.max_prefix && !prefix_blocks))) return KVX_EINVAL;
+    if (!ws || !aligned16(ws) || ws_bytes < carve(p, cache, nullptr, nullptr)) return KVX_EINVAL;
+    Args a = {};
+    a.c = cache_view(cache);
+    a.q = q, a.q_stride = q_stride;
+    a.prefix_blocks = prefix_blocks, a.prefix_lens = prefix_lens, a.group_first = group_first;
+    a.blocks = blocks, a.lens = lens;
+    a.blocks_per_prefix = blocks_per_prefix, a.num_groups = num_groups;
+    a.blocks_per_seq = blocks_per_seq, a.num_seqs = num_seqs;
+    a.q_heads = q_heads, a.group = q_heads / cache->heads;
+    a.max_prefix = p.max_prefix, a.max_len = p.max_len;
+    a.by_group = FastDiv(a.group);
+    a.scale2 = fabsf(scale) * cache->k_scale * 1.4426950408889634f;
+    a.negate = scale < 0;
+    a.out = out, a.out_stride = out_stride, a.lse = lse, a.status = status;
+    a.tile_rows = p.tile_rows;
+    a.prefix_cap = p.prefix_cap, a.prefix_off_b = p.prefix_off_b;
+    a.own_cap = p.own_cap, a.own_off_b = p.own_off_b, a.own_first_row = (uint32_t)p.own_first_row;
+    a.grid = p.grid;
+    carve(p, cache, ws, &a);
     const cudaStream_t s = as_stream(stream);
-    if (cache->dtype == KVX_E4M3)
-        dtype == KVX_BF16 ? k_simple<__nv_bfloat16, 1><<<grid, 32, 0, s>>>(a) : k_simple<__half, 1><<<grid, 32, 0, s>>>(a);
-    else
-        dtype == KVX_BF16 ? k_simple<__nv_bfloat16, 2><<<grid, 32, 0, s>>>(a) : k_simple<__half, 2><<<grid, 32, 0, s>>>(a);
+    const bool ok = dtype == KVX_BF16
+                        ? (cache->dtype == KVX_E4M3 ? launch<__nv_bfloat16, 1>(a, s) : launch<__nv_bfloat16, 2>(a, s))
+                        : (cache->dtype == KVX_E4M3 ? launch<__half, 1>(a, s) : launch<__half, 2>(a, s));
+    if (!ok) return KVX_ECUDA;
+    KVX_LAUNCHED();
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_seqs * q_heads);
+    cfg.blockDim = dim3(32 * kJoinWarps);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    const cudaError_t e = dtype == KVX_BF16 ? cudaLaunchKernelEx(&cfg, k_join<__nv_bfloat16>, a) : cudaLaunchKernelEx(&cfg, k_join<__half>, a);
+    if (e != cudaSuccess) return KVX_ECUDA;
     KVX_LAUNCHED();
     return KVX_OK;
 }

@@ -1,0 +1,892 @@
+// The attention kernel of kvx_attend_shared, as a template on the element types
+// and the head size; kvx_shared_*.cu instantiate it, kvx_shared.cu has the entry
+// point and the joining kernel.
+#pragma once
+
+#include <type_traits>
+
+#include "kvx_cache.cuh"
+
+namespace kvx {
+namespace shared {
+
+// Warps of a block: 0-3 and 4-7 take softmaxes, each thread one row of a slot;
+// 8-11 copy; one issues the tensor cores' instructions; one walks the schedule.
+constexpr int kSoftWarps = 8, kCopyWarps = 4, kMmaWarp = 12, kWalkWarp = 13, kWarps = 14;
+constexpr int kThreads = 32 * kWarps;
+constexpr uint32_t kCopyThreads = 32 * kCopyWarps;
+// Descriptors that the walking warp may be ahead: more than the tiles that the
+// copying warps hold back (Shape::kPending, two to a piece of one tile) and look
+// up ahead reach back.
+constexpr int kPieces = 16;
+constexpr uint32_t kRows = 128;  // of a slot: the tensor cores' M, a query row for each lane of tensor memory
+constexpr uint32_t kExtra = 1;   // tiles that a unit's own overhead counts as
+constexpr uint32_t kMinShare = 2;
+
+struct Args {
+    CacheView c;
+    const void *q;
+    uint64_t q_stride;
+    const uint32_t *prefix_blocks, *prefix_lens, *group_first, *blocks, *lens;
+    uint32_t blocks_per_prefix, num_groups, blocks_per_seq, num_seqs, q_heads, group;
+    uint32_t max_prefix, max_len;
+    FastDiv by_group;
+    float scale2;     // |scale| * k_scale * log2(e)
+    uint32_t negate;  // scale < 0
+    void *out;
+    uint64_t out_stride;
+    float *lse;
+    uint32_t *status;
+    // workspace
+    float *part_o;        // [rows of parts][dim]: unnormalised outputs
+    float2 *part_ml;      // [rows of parts]: base (of powers of two) and sum
+    uint2 *prefix_parts;  // [units of prefixes], [num_seqs * heads]: the first and the last block with a part
+    uint2 *own_parts;
+    uint32_t tile_rows;                          // query rows of a unit of a prefix
+    uint32_t prefix_cap, prefix_off_b;           // rows of a part of a prefix; where those of slot B start
+    uint32_t own_cap, own_off_b, own_first_row;  // of a sequence's own tokens; the first such part's first row
+    uint32_t grid;
+};
+
+// Units.  A prefix's are its group's query rows of a KV head, kTileRows at a
+// time; their numbers grow with the group, the tile and the head, with gaps.
+__host__ __device__ __forceinline__ uint32_t prefix_tile(const Args &a, uint32_t first_seq, uint32_t g) {
+    return (uint32_t)((uint64_t)first_seq * a.group / a.tile_rows) + g;
+}
+
+// What is shared out: a group's prefix, or a sequence's own tokens.
+struct Entry {
+    uint32_t seq0, rows, len, bad;
+};
+__device__ __forceinline__ Entry entry_of(const Args &a, uint32_t i) {
+    Entry e = {};
+    uint32_t most;
+    if (i < a.num_groups) {
+        const uint32_t from = __ldg(a.group_first + i), to = __ldg(a.group_first + i + 1);
+        e.len = __ldg(a.prefix_lens + i);
+        most = a.max_prefix;
+        e.seq0 = from;
+        if (from > to || to > a.num_seqs)
+            e.bad = KVX_S_BOUNDS;
+        else
+            e.rows = (to - from) * a.group;
+    } else {
+        e.seq0 = i - a.num_groups;
+        e.rows = a.group;
+        e.len = __ldg(a.lens + e.seq0);
+        most = a.max_len;
+    }
+    if (e.len > most) e.len = most, e.bad |= KVX_S_BOUNDS;
+    if (!e.rows) e.len = 0;
+    return e;
+}
+
+// A part of a unit that one block works on.
+struct Piece {
+    const uint32_t *table;                    // its pages
+    uint32_t seq0, row0, rows, head, k0, k1;  // query rows row0 .. row0 + rows-1 of seq0's group on; 0 rows end the stream
+    uint32_t both;                            // both slots take every tile, or tiles in turn
+    uint32_t part_row, off_b;                 // of the partial result
+};
+
+template <int DP, int ES>
+struct Shape {
+    static constexpr uint32_t kKeys = DP == 256 ? 64 : 128;  // of a tile
+    static constexpr uint32_t kTileRows = DP == 256 ? 128 : 256;
+    static constexpr uint32_t kStage = kKeys * DP * 2;  // bytes of a tile of keys or values in 16 bits
+    static constexpr uint32_t kQ = kRows * DP * 2;
+    static constexpr uint32_t kQBufs = DP == 256 ? 1 : 2;
+    static constexpr uint32_t kStages = ES == 2 ? (DP == 64 ? 11 : 5) : (DP == 64 ? 6 : 3);
+    static constexpr uint32_t kHeld = ES == 2 ? 0 : DP == 64 ? 8 : 4;  // 8-bit tiles on their way
+    static constexpr uint32_t kPending = ES == 2 ? kStages - 1 : kHeld;
+    static constexpr uint32_t kSmem = 1024 + kQ * kQBufs + kStages * kStage + kHeld * (kStage / 2);
+};
+
+struct Shared {  // behind the tiles
+    uint64_t kv_full[11], kv_empty[11];
+    uint64_t q_empty[2];
+    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+    uint64_t pc_full[kPieces], pc_empty[kPieces];
+    uint64_t drained;
+    Piece pieces[kPieces];
+    uint32_t sums[kWarps];
+    uint32_t tmem;
+};
+
+// ------------------------------------------------------------- instructions
+
+__device__ __forceinline__ void mbar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tmbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+// mbar_wait by a whole warp, which goes on together.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, mbar_wait(bar, parity));
+}
+__device__ __forceinline__ bool warp_test(uint64_t *bar, uint32_t parity) {
+    return __all_sync(0xFFFFFFFFu, mbar_test(bar, parity));
+}
+// 16 bytes, or zeros where there is nothing to read.
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+__device__ __forceinline__ void copies_wait(uint32_t most) {  // until at most that many groups are on their way
+    switch (most) {
+        case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
+        case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
+        case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
+        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
+        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
+        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
+        case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
+        case 7: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
+        case 8: asm volatile("cp.async.wait_group 8;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 9;" ::: "memory"); break;
+    }
+}
+// What this thread wrote to shared memory becomes visible to the tensor cores.
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+// Arrives when the tensor instructions issued so far are complete.
+__device__ __forceinline__ void mma_commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+          "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16(uint32_t (&r)[16], uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(at)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+        "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+
+// Shared-memory operands lie in rows of 128 bytes whose 16-byte pieces are
+// exchanged within groups of eight rows (the 128-byte swizzle): bits 0-13 the
+// address / 16, 16-29 and 32-45 the leading and the stride byte offsets / 16,
+// 46 the version, 61-63 the swizzle.
+__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading, uint32_t stride) {
+    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
+           1ull << 46 | 2ull << 61;
+}
+// M = 128; both operands bf16 or fp16, results 32 bits.
+template <class T>
+__device__ __forceinline__ uint32_t instruction(uint32_t n, bool b_by_columns, bool negate) {
+    constexpr uint32_t type = std::is_same<T, __nv_bfloat16>::value ? 1 : 0;
+    return 1u << 4 | type << 7 | type << 10 | (uint32_t)negate << 13 | (uint32_t)b_by_columns << 16 | n / 8 << 17 |
+           kRows / 16 << 24;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// a / b for b > 0; small quotients go through the reciprocal: a < 2^22 is exact
+// as a float, and a * (1/b) is off by less than one.
+__device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t b) {
+    if (a >= 1u << 22) return a / b;
+    uint32_t q = (uint32_t)__fmul_rz((float)a, __frcp_rz((float)b));
+    q += a - q * b >= b;
+    return q;
+}
+
+// ------------------------------------------------------------- the schedule
+
+// The walking warp: the block's share of all units' tiles, piece by piece.
+template <int DP, int ES>
+__device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *cum, uint32_t total, uint32_t per,
+                                     uint32_t lane) {
+    using S = Shape<DP, ES>;
+    const uint32_t entries = a.num_groups + a.num_seqs;
+    uint32_t share = (total + a.grid - 1) / a.grid;
+    if (share < kMinShare) share = kMinShare;
+    const uint64_t begin64 = (uint64_t)blockIdx.x * share;
+    uint32_t at = begin64 < total ? (uint32_t)begin64 : total;
+    const uint32_t end = total - at > share ? at + share : total;
+    auto units_of = [&](const Entry &e) { return a.c.heads * ((e.rows + S::kTileRows - 1) / S::kTileRows); };
+    auto unit_len = [&](const Entry &e) { return e.len ? (e.len + S::kKeys - 1) / S::kKeys + kExtra : 0; };
+    uint32_t i = 0, off = 0, np = 0;
+    Entry e = {};
+    if (at < end) {
+        // the thread that counted the first entry: the first whose sum passes `at`
+        uint32_t t = 0;
+        for (uint32_t j = 0; j < kThreads; j += 32) t += __popc(__ballot_sync(0xFFFFFFFFu, cum[j + lane] <= at));
+        uint32_t before = t ? cum[t - 1] : 0;
+        for (i = t * per;; i++) {
+            e = entry_of(a, i);
+            const uint32_t n = unit_len(e) * units_of(e);
+            if (at - before < n) break;
+            before += n;
+        }
+        off = at - before;
+    }
+    __syncthreads();  // cum's place is the copies' from here on
+    Entry next = {};
+    if (at < end && i + 1 < entries) next = entry_of(a, i + 1);
+    while (at < end) {
+        const uint32_t len = unit_len(e), units = units_of(e);
+        if (off >= len * units) {
+            off -= len * units;
+            e = next;
+            i++;
+            next = Entry{};
+            if (i + 1 < entries) next = entry_of(a, i + 1);
+            continue;
+        }
+        const uint32_t unit = quotient(off, len), from = off - unit * len;
+        const uint32_t to = len - from < end - at ? len : from + (end - at);
+        const uint32_t start = at - from;  // the unit's
+        at += to - from;
+        off += to - from;
+        if (to <= kExtra) continue;  // the overhead's tiles come first
+        const uint32_t t0 = from > kExtra ? from - kExtra : 0, t1 = to - kExtra;
+        if (np >= kPieces && !warp_wait(&sh.pc_empty[np % kPieces], (np / kPieces & 1) ^ 1)) return false;
+        if (lane == 0) {
+            Piece p;
+            const uint32_t mt = unit / a.c.heads, head = unit - mt * a.c.heads;
+            const bool prefix = i < a.num_groups;
+            p.seq0 = e.seq0;
+            p.row0 = mt * S::kTileRows;
+            p.rows = e.rows - p.row0 < S::kTileRows ? e.rows - p.row0 : S::kTileRows;
+            p.head = head;
+            p.k0 = t0 * S::kKeys;
+            p.k1 = t1 * S::kKeys < e.len ? t1 * S::kKeys : e.len;
+            p.both = DP == 256 || p.rows > kRows;
+            const uint2 parts = make_uint2((start + kExtra) / share, (start + len - 1) / share);
+            if (prefix) {
+                const uint32_t u = (prefix_tile(a, e.seq0, i) + mt) * a.c.heads + head;
+                p.table = a.prefix_blocks + (uint64_t)i * a.blocks_per_prefix;
+                p.part_row = (u + blockIdx.x) * a.prefix_cap;
+                p.off_b = a.prefix_off_b;
+                if (!t0) a.prefix_parts[u] = parts;
+            } else {
+                const uint32_t u = e.seq0 * a.c.heads + head;
+                p.table = a.blocks + (uint64_t)e.seq0 * a.blocks_per_seq;
+                p.part_row = a.own_first_row + (u + blockIdx.x) * a.own_cap;
+                p.off_b = a.own_off_b;
+                if (!t0) a.own_parts[u] = parts;
+            }
+            sh.pieces[np % kPieces] = p;
+            mbar_arrive(&sh.pc_full[np % kPieces]);
+        }
+        __syncwarp();
+        np++;
+    }
+    if (np >= kPieces && !warp_wait(&sh.pc_empty[np % kPieces], (np / kPieces & 1) ^ 1)) return false;
+    if (lane == 0) {
+        sh.pieces[np % kPieces].rows = 0;
+        mbar_arrive(&sh.pc_full[np % kPieces]);
+    }
+    return true;
+}
+
+// --------------------------------------------------------------- the copies
+
+// Four stored 8-bit values times a power of two (or, of a cache with one scale,
+// as they are), as 16-bit ones.
+template <class T>
+struct Widen;
+template <>
+struct Widen<__nv_bfloat16> {  // exact
+    float s;
+    __device__ __forceinline__ explicit Widen(uint32_t e) { s = row_scale(e); }
+    __device__ __forceinline__ uint32_t two(uint32_t f16x2) const {
+        const float2 x = Pair<__half>::unpack(f16x2);
+        return Pair<__nv_bfloat16>::pack(x.x * s, x.y * s);
+    }
+};
+template <>
+struct Widen<__half> {  // by two factors: the first product is exact (an 8-bit value's last bit is 2^-9 or more)
+    __half2 a, b;
+    __device__ __forceinline__ explicit Widen(uint32_t e) {
+        const int k = (int)e - 127, ka = k < -12 ? -12 : k > 15 ? 15 : k;
+        const int kb = k - ka < -24 ? -40 : k - ka > 15 ? 15 : k - ka;
+        const uint32_t wa = e == 255 ? 0x7FFF7FFFu : (uint32_t)(ka + 15) * 0x04000400u;
+        const uint32_t wb = kb < -24 ? 0u : kb < -14 ? 0x00010001u << (kb + 24) : (uint32_t)(kb + 15) * 0x04000400u;
+        a = *reinterpret_cast<const __half2 *>(&wa), b = *reinterpret_cast<const __half2 *>(&wb);
+    }
+    __device__ __forceinline__ uint32_t two(uint32_t f16x2) const {
+        const __half2 r = __hmul2(__hmul2(*reinterpret_cast<const __half2 *>(&f16x2), a), b);
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
+};
+template <class T>
+__device__ __forceinline__ uint2 widen4(uint32_t four, const Widen<T> &w) {
+    uint32_t lo, hi;
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(four));
+    return make_uint2(w.two(lo), w.two(hi));
+}
+
+// The copying warps.  A warp looks up and copies a quarter of a tile's rows: a
+// lane has one token's segment addresses, which the copying lanes take from it.
+// Tiles go keys of tile e, values of tile e-1, as the tensor cores take them.
+template <class T, int DP, int ES>
+__device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q_smem, uint8_t *ring, uint8_t *held, uint32_t thread,
+                                           uint32_t &bad) {
+    using S = Shape<DP, ES>;
+    constexpr uint32_t kWarpKeys = S::kKeys / kCopyWarps;
+    constexpr uint32_t kParts = DP * ES / 16;  // 16-byte pieces of a row
+    constexpr uint32_t kCopies = kWarpKeys * kParts / 32;
+    const uint32_t warp = thread / 32, lane = thread & 31;
+    const uint32_t key = warp * kWarpKeys + lane % kWarpKeys;  // this lane's, within the tile
+    const uint32_t parts = a.c.row_bytes / 16;
+    const uint64_t room = a.c.pool_bytes - a.c.span;
+    const bool fits = a.c.pool_bytes >= a.c.span, row_scales = ES == 1 && a.c.scale_offset;
+
+    // Tiles whose copies have been issued and not yet handed over.
+    uint32_t issued = 0, done = 0;
+    uint64_t scales = 0;   // a byte for each of the last eight tiles: this lane's row's
+    auto hand_over = [&]() -> bool {
+        const uint32_t t = done, stage = t % S::kStages;
+        if constexpr (ES == 1) {
+            if (t >= S::kStages && !warp_wait(&sh.kv_empty[stage], (t / S::kStages & 1) ^ 1)) return false;
+            const uint4 *from = reinterpret_cast<const uint4 *>(held + t % S::kHeld * (S::kStage / 2)) + thread;
+            uint8_t *to = ring + stage * S::kStage;
+            const uint32_t mine = (uint32_t)(scales >> (t % 8 * 8)) & 0xFF;
+#pragma unroll
+            for (uint32_t c = 0; c < kCopies; c++) {
+                const uint32_t j = c * 32 + lane, row = j / kParts, part = j % kParts;
+                const uint32_t at = warp * kWarpKeys + row;
+                const uint4 raw = from[c * kCopyThreads];
+                const Widen<T> w(__shfl_sync(0xFFFFFFFFu, mine, row));
+                const uint2 x0 = widen4<T>(raw.x, w), x1 = widen4<T>(raw.y, w), x2 = widen4<T>(raw.z, w), x3 = widen4<T>(raw.w, w);
+                uint8_t *line = to + (part / 4) * (S::kKeys * 128) + at * 128;
+                const uint32_t p0 = part % 4 * 2;
+                *reinterpret_cast<uint4 *>(line + ((p0 ^ (at & 7)) * 16)) = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                *reinterpret_cast<uint4 *>(line + (((p0 + 1) ^ (at & 7)) * 16)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
+            }
+        }
+        fence_async();
+        mbar_arrive(&sh.kv_full[stage]);
+        done++;
+        return true;
+    };
+    // Hands over all that is held back, before a wait for another warp.
+    auto drain = [&]() -> bool {
+        copies_wait(0);
+        while (done < issued)
+            if (!hand_over()) return false;
+        return true;
+    };
+    // A tile on its way through the look-up: its block ids, then its segments'
+    // addresses, then its rows' scales are loaded, each while the tile before
+    // is a step further.
+    struct Look {
+        uint32_t any, first, last, piece;
+        uint32_t valid, token, head;
+    };
+    uint32_t np = 0, k = 0, k1 = 0, head = 0;  // where the look-up is
+    const uint32_t *table = nullptr;
+    bool over = false, alive = true;
+    uint32_t id = 0;
+    uint64_t seg[2] = {};
+    auto find = [&]() -> Look {
+        Look l = {};
+        if (over || !alive) return l;
+        if (k >= k1) {
+            uint64_t *bar = &sh.pc_full[np % kPieces];
+            if (!warp_test(bar, np / kPieces & 1) && !(drain() && warp_wait(bar, np / kPieces & 1))) {
+                alive = false;
+                return l;
+            }
+            const Piece &p = sh.pieces[np % kPieces];
+            if (!p.rows) {
+                over = true;
+                return l;
+            }
+            k = p.k0, k1 = p.k1, head = p.head, table = p.table;
+            l.first = 1;
+            np++;
+        }
+        l.any = 1;
+        l.piece = np - 1;
+        l.head = head;
+        const uint32_t pos = k + key;
+        l.valid = pos < k1;
+        const uint32_t page = a.c.page.div(l.valid ? pos : k);
+        l.token = pos - page * a.c.page.d;
+        id = 0;
+        if (l.valid) id = __ldg(table + page);
+        k += S::kKeys;
+        l.last = k >= k1;
+        return l;
+    };
+    auto find_segments = [&](Look &l) {
+        if (l.valid && id >= a.c.B) bad |= KVX_S_BOUNDS, l.valid = 0;
+        if (l.valid) {
+            const uint64_t *entry = a.c.lane_addr(id, l.head, 0);
+            seg[0] = __ldg(entry), seg[1] = __ldg(entry + 1);
+        }
+    };
+
+    // Room for the next tile.
+    auto make_room = [&]() -> bool {
+        if (issued - done >= S::kPending) {
+            copies_wait(S::kPending - 1);
+            if (!hand_over()) return false;
+        }
+        if constexpr (ES == 2) {
+            const uint32_t stage = issued % S::kStages;
+            const uint32_t parity = (issued / S::kStages & 1) ^ 1;
+            if (issued >= S::kStages && !warp_test(&sh.kv_empty[stage], parity) &&
+                !(drain() && warp_wait(&sh.kv_empty[stage], parity)))
+                return false;
+        }
+        return true;
+    };
+    auto set_scale = [&](uint32_t t, uint32_t exponent) {
+        if (ES == 1) scales = (scales & ~(0xFFull << (t % 8 * 8))) | (uint64_t)exponent << (t % 8 * 8);
+    };
+    auto issue = [&](uint64_t row) {  // an offset from the pool; odd: no row
+        const uint32_t t = issued;
+        uint8_t *to = ES == 2 ? ring + t % S::kStages * S::kStage : held + t % (S::kHeld ? S::kHeld : 1) * (S::kStage / 2) + thread * 16;
+        const uint32_t base = smem_u32(to);
+#pragma unroll
+        for (uint32_t c = 0; c < kCopies; c++) {
+            const uint32_t j = c * 32 + lane, r = j / kParts, part = j % kParts;
+            const uint64_t from = __shfl_sync(0xFFFFFFFFu, row, r);
+            const uint32_t at = warp * kWarpKeys + r;
+            const bool in = !(from & 1) && part < parts;
+            const uint32_t dst = ES == 2 ? base + (part / 8) * (S::kKeys * 128) + at * 128 + ((part % 8 ^ (at & 7)) * 16)
+                                         : base + c * (kCopyThreads * 16);
+            copy16(dst, a.c.pool + (in ? from + part * 16 : 0), in);
+        }
+        copies_commit();
+        issued++;
+    };
+    uint32_t q_used[2] = {};
+    auto issue_q = [&](uint32_t b, uint32_t piece) -> bool {  // rows of a piece into buffer b
+        const Piece p = sh.pieces[piece % kPieces];
+        const uint32_t r0 = DP != 256 && p.both ? b * kRows : 0;
+        const uint32_t rows = p.rows - r0 < kRows ? p.rows - r0 : kRows;
+        const uint32_t parity = (q_used[b] & 1) ^ 1;
+        if (q_used[b] && !warp_test(&sh.q_empty[b], parity) && !(drain() && warp_wait(&sh.q_empty[b], parity))) return false;
+        q_used[b]++;
+        constexpr uint32_t kQParts = DP / 8;
+        const uint32_t base = smem_u32(q_smem + b * S::kQ), q_parts = a.c.dim / 8;
+        for (uint32_t j = thread; j < rows * kQParts; j += kCopyThreads) {
+            const uint32_t r = j / kQParts, part = j % kQParts;
+            const uint32_t rr = p.row0 + r0 + r, s = a.by_group.div(rr);
+            const uint64_t from = (uint64_t)(p.seq0 + s) * a.q_stride + (uint64_t)(p.head * a.group + rr - s * a.group) * a.c.dim;
+            if (part < q_parts)
+                copy16(base + (part / 8) * (kRows * 128) + r * 128 + ((part % 8 ^ (r & 7)) * 16),
+                       static_cast<const T *>(a.q) + from + part * 8, true);
+        }
+        return true;
+    };
+
+    Look one = find();
+    find_segments(one);
+    Look two = one.any ? find() : Look{};
+    uint64_t v_row = 1;
+    uint32_t k_tile = 0, k_exponent = 127, v_exponent = 127;  // scales come a step later
+    bool v_any = false;
+    while (one.any && alive) {
+        // `one` has its addresses on their way, `two` its block ids
+        const Look now = one;
+        uint64_t row[2];
+        uint32_t exponent[2] = {127, 127};
+#pragma unroll
+        for (int kv = 0; kv < 2; kv++) {
+            const uint64_t s = seg[kv];
+            const bool good = fits && s <= room && !((uint32_t)s & 15);
+            if (now.valid && !good) a.c.ok(s, bad);
+            row[kv] = now.valid && good ? s + now.token * a.c.token_stride : 1;
+            if (row_scales && now.valid && good) exponent[kv] = __ldg(a.c.pool + s + a.c.scale_offset + now.token);
+        }
+        find_segments(two);
+        one = two;
+        two = one.any ? find() : Look{};
+        if (!alive) return false;
+
+        if (v_any) set_scale(k_tile, k_exponent);  // of the tile before
+        if (!make_room()) return false;
+        if (now.first) {
+            const uint32_t both = sh.pieces[now.piece % kPieces].both;
+            for (uint32_t b = 0; b < S::kQBufs; b++)
+                if ((DP == 256 || both || b == (now.piece & 1)) && !issue_q(b, now.piece)) return false;
+        }
+        k_tile = issued;
+        issue(row[0]);
+        if (v_any) {
+            if (!make_room()) return false;
+            set_scale(issued, v_exponent);
+            issue(v_row);
+        }
+        v_row = row[1], v_any = true;
+        k_exponent = exponent[0], v_exponent = exponent[1];
+        if (now.last) {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.pc_empty[now.piece % kPieces]);
+        }
+    }
+    if (!alive) return false;
+    if (v_any) {
+        set_scale(k_tile, k_exponent);
+        if (!make_room()) return false;
+        set_scale(issued, v_exponent);
+        issue(v_row);
+    }
+    return drain();
+}
+
+// --------------------------------------------------------- the tensor cores
+
+template <class T, int DP, int ES>
+__device__ __forceinline__ bool multiply(const Args &a, Shared &sh, const uint8_t *q_smem, const uint8_t *ring, uint32_t tmem) {
+    using S = Shape<DP, ES>;
+    const uint32_t steps = a.c.dim / 16;
+    const uint32_t qk = instruction<T>(S::kKeys, false, a.negate);
+    const uint32_t q0 = smem_u32(q_smem), r0 = smem_u32(ring);
+    // a slot's product with V still to come
+    bool pending[2] = {}, has_v[2] = {}, fresh[2] = {};
+    uint32_t v_tile[2] = {}, rounds[2] = {}, outs[2] = {};
+    auto finish = [&](uint32_t s) -> bool {
+        if (!mbar_wait(&sh.p_full[s], (rounds[s] & 1) ^ 1)) return false;  // of round rounds[s] - 1
+        const uint32_t stage = v_tile[s] % S::kStages;
+        if (!mbar_wait(&sh.kv_full[stage], v_tile[s] / S::kStages & 1)) return false;
+        if (fresh[s]) {
+            if (outs[s] && !mbar_wait(&sh.o_free[s], (outs[s] & 1) ^ 1)) return false;
+            outs[s]++;
+        }
+        tmem_after();
+        const uint32_t col = DP == 256 ? s * 128 : 0;
+        const uint32_t n = DP == 256 ? (s ? a.c.dim - 128 : 128) : a.c.dim;
+        const uint32_t pv = instruction<T>(n, true, false);
+        const uint32_t v = r0 + stage * S::kStage + col / 64 * (S::kKeys * 128);
+        const uint32_t o = tmem + 256 + s * 128, p = tmem + s * 128;
+#pragma unroll
+        for (uint32_t i = 0; i < S::kKeys / 16; i++)
+            mma_ts(o, p + i * 8, operand(v + i * 2048, S::kKeys * 128, 1024), pv, i > 0 || !fresh[s]);
+        mma_commit(&sh.pv_done[s]);
+        pending[s] = false;
+        if (!(pending[s ^ 1] && has_v[s ^ 1] && v_tile[s ^ 1] == v_tile[s])) mma_commit(&sh.kv_empty[stage]);
+        return true;
+    };
+    uint32_t tile = 0, event = 0;
+    for (uint32_t np = 0;; np++) {
+        if (!mbar_wait(&sh.pc_full[np % kPieces], np / kPieces & 1)) return false;
+        const Piece p = sh.pieces[np % kPieces];
+        if (!p.rows) break;
+        const uint32_t nt = (p.k1 - p.k0 + S::kKeys - 1) / S::kKeys;
+        bool started[2] = {};
+        for (uint32_t t = 0; t < nt; t++, event++) {
+            const uint32_t k_tile = tile++, stage = k_tile % S::kStages;
+            if (event) {
+                for (uint32_t s = 0; s < 2; s++)
+                    if (pending[s] && !has_v[s]) v_tile[s] = tile, has_v[s] = true;
+                tile++;
+            }
+            const uint32_t s_first = p.both ? 0 : event & 1, s_last = p.both ? 1 : s_first;
+            for (uint32_t s = s_first; s <= s_last; s++) {
+                if (pending[s] && !finish(s)) return false;
+                const uint32_t b = DP == 256 ? 0 : p.both ? s : np & 1;
+                // (a piece's queries come with its first keys)
+                if (s == s_first && !mbar_wait(&sh.kv_full[stage], k_tile / S::kStages & 1)) return false;
+                tmem_after();
+                const uint32_t q = q0 + b * S::kQ, kk = r0 + stage * S::kStage;
+                for (uint32_t i = 0; i < steps; i++)
+                    mma_ss(tmem + s * 128, operand(q + i / 4 * (kRows * 128) + i % 4 * 32, 16, 1024),
+                           operand(kk + i / 4 * (S::kKeys * 128) + i % 4 * 32, 16, 1024), qk, i > 0);
+                mma_commit(&sh.s_full[s]);
+                pending[s] = true, has_v[s] = false, fresh[s] = !started[s];
+                started[s] = true;
+                rounds[s]++;
+            }
+            mma_commit(&sh.kv_empty[stage]);
+        }
+        if (DP == 256 || p.both || !(np & 1)) mma_commit(&sh.q_empty[0]);
+        if (DP != 256 && (p.both || (np & 1))) mma_commit(&sh.q_empty[1]);
+        mbar_arrive(&sh.pc_empty[np % kPieces]);
+    }
+    if (event) {
+        for (uint32_t s = 0; s < 2; s++)
+            if (pending[s] && !has_v[s]) v_tile[s] = tile, has_v[s] = true;
+        for (uint32_t s = 0; s < 2; s++)
+            if (pending[s] && !finish(s)) return false;
+    }
+    return true;
+}
+
+// -------------------------------------------------------------- the softmax
+
+template <class T, int DP, int ES>
+__device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem, uint32_t slot, uint32_t warp, uint32_t lane) {
+    using S = Shape<DP, ES>;
+    // Weights are 2^(logit - base).  The base follows the running maximum only when
+    // a logit exceeds it by more than kSlack + kBoost: sums and outputs are
+    // divided by the same power in the end.  It lies kBoost below that maximum,
+    // so that in fp16, whose smallest step is 2^-24, small weights keep some
+    // bits more beside a large one.
+    constexpr float kSlack = 8.0f, kBoost = std::is_same<T, __half>::value ? 7.0f : 0.0f;
+    const uint32_t r = warp * 32 + lane;  // row of the slot
+    const uint32_t lanes = (warp * 32) << 16;
+    const uint32_t s_at = tmem + lanes + slot * 128, o_at = tmem + lanes + 256 + slot * 128;
+    const uint32_t col = DP == 256 ? slot * 128 : 0;
+    const uint32_t cols = DP == 256 ? (slot ? a.c.dim - 128 : 128) : a.c.dim;  // of the output, a multiple of 16
+    uint32_t event = 0, rounds = 0;
+    for (uint32_t np = 0;; np++) {
+        if (!warp_wait(&sh.pc_full[np % kPieces], np / kPieces & 1)) return false;
+        const Piece p = sh.pieces[np % kPieces];
+        if (!p.rows) return true;
+        const uint32_t nt = (p.k1 - p.k0 + S::kKeys - 1) / S::kKeys;
+        const uint32_t first_row = DP != 256 && p.both ? slot * kRows : 0;
+        const bool busy = first_row + warp * 32 < p.rows, mine = first_row + r < p.rows;
+        const uint32_t step = p.both ? 1 : 2;
+        uint32_t t = p.both ? 0 : (event & 1) ^ slot;
+        event += nt;
+        const bool any = t < nt;
+        float base = 0, limit = -INFINITY, sum = 0;
+        for (bool fresh = true; t < nt; t += step, fresh = false) {
+            if (!warp_wait(&sh.s_full[slot], rounds & 1)) return false;
+            rounds++;
+            if (busy) {
+                tmem_after();
+                const uint32_t left = p.k1 - p.k0 - t * S::kKeys, n = left < S::kKeys ? left : S::kKeys;
+                float top = -INFINITY;
+                uint32_t x[32];
+#pragma unroll
+                for (uint32_t c = 0; c < S::kKeys; c += 32) {
+                    tmem_ld32(x, s_at + c);
+                    tmem_wait_ld();
+                    if (c + 32 <= n) {
+#pragma unroll
+                        for (int i = 0; i < 32; i++) top = fmaxf(top, __uint_as_float(x[i]));
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 32; i++)
+                            if (c + i < n) top = fmaxf(top, __uint_as_float(x[i]));
+                    }
+                }
+                top *= a.scale2;
+                const bool over = top > limit;
+                if (__any_sync(0xFFFFFFFFu, over)) {
+                    float factor = 1.0f;
+                    if (over) {
+                        const float to = top - kBoost;
+                        factor = fresh ? 0.0f : exp2_fast(base - to);
+                        if (limit == -INFINITY) factor = 0.0f;  // nothing was added so far
+                        base = to;
+                        limit = top + kSlack;
+                        sum *= factor;
+                    }
+                    if (!fresh) {
+                        // the product before has to be in the sums
+                        if (!warp_wait(&sh.pv_done[slot], rounds & 1)) return false;
+                        tmem_after();
+                        uint32_t y[16];
+                        for (uint32_t c = 0; c < cols; c += 16) {
+                            tmem_ld16(y, o_at + c);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int i = 0; i < 16; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * factor);
+                            tmem_st16(o_at + c, y);
+                        }
+                        tmem_wait_st();
+                    }
+                }
+                float sums[4] = {};
+#pragma unroll
+                for (uint32_t c = 0; c < S::kKeys; c += 32) {
+                    tmem_ld32(x, s_at + c);
+                    tmem_wait_ld();
+                    uint32_t w[16];
+                    if (c + 32 <= n) {
+#pragma unroll
+                        for (int i = 0; i < 16; i++) {
+                            const float e0 = exp2_fast(fmaf(__uint_as_float(x[2 * i]), a.scale2, -base));
+                            const float e1 = exp2_fast(fmaf(__uint_as_float(x[2 * i + 1]), a.scale2, -base));
+                            sums[i % 2 * 2] += e0, sums[i % 2 * 2 + 1] += e1;
+                            w[i] = Pair<T>::pack(e0, e1);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 16; i++) {
+                            const float e0 = c + 2 * i < n ? exp2_fast(fmaf(__uint_as_float(x[2 * i]), a.scale2, -base)) : 0.0f;
+                            const float e1 = c + 2 * i + 1 < n ? exp2_fast(fmaf(__uint_as_float(x[2 * i + 1]), a.scale2, -base)) : 0.0f;
+                            sums[i % 2 * 2] += e0, sums[i % 2 * 2 + 1] += e1;
+                            w[i] = Pair<T>::pack(e0, e1);
+                        }
+                    }
+                    tmem_st16(s_at + c / 2, w);
+                }
+                sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+                tmem_wait_st();
+                tmem_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.p_full[slot]);
+        }
+        const uint64_t row = p.part_row + (slot && DP != 256 ? p.off_b : 0) + r;
+        if (any) {
+            if (!warp_wait(&sh.pv_done[slot], (rounds & 1) ^ 1)) return false;
+            if (busy) {
+                tmem_after();
+                uint32_t y[16];
+                for (uint32_t c = 0; c < cols; c += 16) {
+                    tmem_ld16(y, o_at + c);
+                    tmem_wait_ld();
+                    if (mine) {
+                        uint4 *to = reinterpret_cast<uint4 *>(a.part_o + row * a.c.dim + col + c);
+#pragma unroll
+                        for (int i = 0; i < 4; i++) to[i] = make_uint4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
+                    }
+                }
+                tmem_before();
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.o_free[slot]);
+        }
+        if (mine && (DP != 256 || !slot)) a.part_ml[row] = make_float2(base, any ? sum : 0.0f);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.pc_empty[np % kPieces]);
+    }
+}
+
+template <class T, int DP, int ES>
+__global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ Args a) {
+    using S = Shape<DP, ES>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    uint8_t *ring = smem, *q_smem = smem + S::kStages * S::kStage, *held = q_smem + S::kQBufs * S::kQ;
+    __shared__ Shared sh;
+    const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    // ---- count all tiles
+    const uint32_t entries = a.num_groups + a.num_seqs, per = (entries + kThreads - 1) / kThreads;
+    uint32_t *cum = reinterpret_cast<uint32_t *>(smem);
+    uint32_t mine = 0, bad = 0;
+    for (uint32_t i = threadIdx.x * per; i < (threadIdx.x + 1) * per && i < entries; i++) {
+        const Entry e = entry_of(a, i);
+        bad |= e.bad;
+        if (e.len) mine += a.c.heads * ((e.rows + S::kTileRows - 1) / S::kTileRows) * ((e.len + S::kKeys - 1) / S::kKeys + kExtra);
+    }
+    uint32_t upto = warp_incl_sum(mine);
+    if (lane == 31) sh.sums[warp] = upto;
+    if (threadIdx.x == 0) {
+        for (uint32_t i = 0; i < S::kStages; i++) mbar_init(&sh.kv_full[i], kCopyThreads), mbar_init(&sh.kv_empty[i], 1);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&sh.q_empty[i], 1);
+            mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 4);
+            mbar_init(&sh.pv_done[i], 1), mbar_init(&sh.o_free[i], 4);
+        }
+        for (int i = 0; i < kPieces; i++) mbar_init(&sh.pc_full[i], 1), mbar_init(&sh.pc_empty[i], kSoftWarps + kCopyWarps + 1);
+        mbar_init(&sh.drained, 1);
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    __syncthreads();
+    uint32_t total = 0;
+    for (uint32_t w = 0; w < kWarps; w++) {
+        if (w < warp) upto += sh.sums[w];
+        total += sh.sums[w];
+    }
+    cum[threadIdx.x] = upto;
+    raise(a.status, bad);
+    bad = 0;
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)) : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+        tmem_before();
+    }
+    __syncthreads();
+    tmem_after();
+    const uint32_t tmem = sh.tmem;
+    bool ok = true;
+    if (warp == kWalkWarp) {
+        ok = walk<DP, ES>(a, sh, cum, total, per, lane);
+    } else {
+        __syncthreads();  // the walking warp has found its first entry
+        if (warp < kSoftWarps) {
+            ok = soften<T, DP, ES>(a, sh, tmem, warp / 4, warp % 4, lane);
+        } else if (warp < kSoftWarps + kCopyWarps) {
+            ok = copy_tiles<T, DP, ES>(a, sh, q_smem, ring, held, threadIdx.x - 32 * kSoftWarps, bad);
+            copies_wait(0);
+        } else if (lane == 0) {
+            ok = multiply<T, DP, ES>(a, sh, q_smem, ring, tmem);
+            mma_commit(&sh.drained);  // no instruction outlives its operands
+            if (!mbar_wait(&sh.drained, 0)) ok = false;
+        }
+    }
+    if (!ok) bad |= KVX_S_TIMEOUT;
+    raise(a.status, bad);
+    tmem_before();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tmem_after();
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem) : "memory");
+    }
+}
+
+// Launches one variant on a.grid blocks; false where that failed.
+template <class T, int DP, int ES>
+bool launch_kernel(const Args &a, cudaStream_t s) {
+    using S = Shape<DP, ES>;
+    static bool done[64];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return false;
+    if (dev < 0 || dev >= 64 || !done[dev]) {
+        if (cudaFuncSetAttribute(k_shared<T, DP, ES>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
+            return false;
+        if (dev >= 0 && dev < 64) done[dev] = true;
+    }
+    k_shared<T, DP, ES><<<a.grid, kThreads, S::kSmem, s>>>(a);
+    return true;
+}
+
+template <class T, int ES>
+bool launch(const Args &a, cudaStream_t s) {
+    return a.c.dim <= 64 ? launch_kernel<T, 64, ES>(a, s) : a.c.dim <= 128 ? launch_kernel<T, 128, ES>(a, s)
+                                                                            : launch_kernel<T, 256, ES>(a, s);
+}
+
+}  // namespace shared
+}  // namespace kvx
