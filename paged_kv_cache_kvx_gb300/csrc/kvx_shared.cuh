@@ -11,8 +11,8 @@ namespace kvx {
 namespace shared {
 
 // Warps of a block: 0-3 and 4-7 take softmaxes, each thread one row of a slot;
-// 8-11 copy; one issues the tensor cores' instructions; one walks the schedule.
-constexpr int kSoftWarps = 8, kCopyWarps = 4, kMmaWarp = 12, kWalkWarp = 13, kWarps = 14;
+// 8-15 copy; one for each slot issues the tensor cores' instructions; one walks the schedule.
+constexpr int kSoftWarps = 8, kCopyWarps = 8, kMmaWarp = 16, kWalkWarp = 18, kWarps = 20;
 constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kCopyThreads = 32 * kCopyWarps;
 // Descriptors that the walking warp may be ahead: more than the tiles that the
@@ -85,7 +85,7 @@ __device__ __forceinline__ Entry entry_of(const Args &a, uint32_t i) {
 struct Piece {
     const uint32_t *table;                    // its pages
     uint32_t seq0, row0, rows, head, k0, k1;  // query rows row0 .. row0 + rows-1 of seq0's group on; 0 rows end the stream
-    uint32_t both;                            // both slots take every tile, or tiles in turn
+    uint32_t both, event;                     // both slots take every tile, or tiles in turn: slot `event` & 1 the first
     uint32_t part_row, off_b;                 // of the partial result
 };
 
@@ -164,18 +164,27 @@ __device__ __forceinline__ void mma_commit(uint64_t *bar) {
     asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
                  : "memory");
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+// One of a warp's threads issues; all of them go the same way.
+__device__ __forceinline__ bool elected() {
+    uint32_t ok;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
+    return ok != 0;
+}
+// Operands by the low words of their descriptors (Operand); d += or, without
+// `add`, d = a b.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t a_high, uint32_t b, uint32_t b_high, uint32_t idesc,
+                                       uint32_t add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\tsetp.ne.u32 p, %6, 0;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(a_high), "r"(b), "r"(b_high), "r"(idesc), "r"(add)
         : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t add) {
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t b_high, uint32_t idesc, uint32_t add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"(add)
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\tsetp.ne.u32 p, %5, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(b_high), "r"(idesc), "r"(add)
         : "memory");
 }
 __device__ __forceinline__ void tmem_ld32(uint32_t (&r)[32], uint32_t at) {
@@ -206,13 +215,13 @@ __device__ __forceinline__ void tmem_st16(uint32_t at, const uint32_t (&r)[16]) 
 }
 
 // Shared-memory operands lie in rows of 128 bytes whose 16-byte pieces are
-// exchanged within groups of eight rows (the 128-byte swizzle): bits 0-13 the
-// address / 16, 16-29 and 32-45 the leading and the stride byte offsets / 16,
-// 46 the version, 61-63 the swizzle.
-__device__ __forceinline__ uint64_t operand(uint32_t addr, uint32_t leading, uint32_t stride) {
-    return (uint64_t)((addr & 0x3FFFF) >> 4) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
-           1ull << 46 | 2ull << 61;
+// exchanged within groups of eight rows (the 128-byte swizzle).  Descriptor:
+// bits 0-13 the address / 16, 16-29 and 32-45 the leading and the stride byte
+// offsets / 16, 46 the version, 61-63 the swizzle.
+__device__ __forceinline__ constexpr uint32_t operand_low(uint32_t addr, uint32_t leading) {
+    return (addr & 0x3FFFF) >> 4 | (leading >> 4) << 16;
 }
+constexpr uint32_t kOperandHigh = 1024 >> 4 | 1u << 14 | 2u << 29;  // a stride of 1024 bytes from eight rows to the next
 // M = 128; both operands bf16 or fp16, results 32 bits.
 template <class T>
 __device__ __forceinline__ uint32_t instruction(uint32_t n, bool b_by_columns, bool negate) {
@@ -251,7 +260,7 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
     const uint32_t end = total - at > share ? at + share : total;
     auto units_of = [&](const Entry &e) { return a.c.heads * ((e.rows + S::kTileRows - 1) / S::kTileRows); };
     auto unit_len = [&](const Entry &e) { return e.len ? (e.len + S::kKeys - 1) / S::kKeys + kExtra : 0; };
-    uint32_t i = 0, off = 0, np = 0;
+    uint32_t i = 0, off = 0, np = 0, event = 0;
     Entry e = {};
     if (at < end) {
         // the thread that counted the first entry: the first whose sum passes `at`
@@ -298,6 +307,7 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
             p.k0 = t0 * S::kKeys;
             p.k1 = t1 * S::kKeys < e.len ? t1 * S::kKeys : e.len;
             p.both = DP == 256 || p.rows > kRows;
+            p.event = event;
             const uint2 parts = make_uint2((start + kExtra) / share, (start + len - 1) / share);
             if (prefix) {
                 const uint32_t u = (prefix_tile(a, e.seq0, i) + mt) * a.c.heads + head;
@@ -317,6 +327,7 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
         }
         __syncwarp();
         np++;
+        event += t1 - t0;
     }
     if (np >= kPieces && !warp_wait(&sh.pc_empty[np % kPieces], (np / kPieces & 1) ^ 1)) return false;
     if (lane == 0) {
@@ -328,42 +339,77 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
 
 // --------------------------------------------------------------- the copies
 
-// Four stored 8-bit values times a power of two (or, of a cache with one scale,
-// as they are), as 16-bit ones.
+// Stored 8-bit values times a power of two (1 in a cache with one scale, which
+// enters with the logits and the sums), as 16-bit ones.  bf16, exactly: an e4m3
+// value's bits, moved to a bf16's, are the value times 2^-120, normal and
+// subnormal numbers alike; one product brings the scale as well.  A NaN, whose
+// bits would be 480's, and scales above 2^7, whose factor bf16 does not hold, take
+// the way through 32 bits (any()).
+__device__ __forceinline__ void halves(uint32_t v, uint32_t &lo, uint32_t &hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(v));
+}
 template <class T>
 struct Widen;
 template <>
-struct Widen<__nv_bfloat16> {  // exact
-    float s;
-    __device__ __forceinline__ explicit Widen(uint32_t e) { s = row_scale(e); }
-    __device__ __forceinline__ uint32_t two(uint32_t f16x2) const {
-        const float2 x = Pair<__half>::unpack(f16x2);
-        return Pair<__nv_bfloat16>::pack(x.x * s, x.y * s);
+struct Widen<__nv_bfloat16> {
+    uint32_t e, factor;
+    __device__ __forceinline__ explicit Widen(uint32_t exponent) : e(exponent), factor((exponent + 120) * 0x00800080u) {}
+    __device__ __forceinline__ bool simple() const { return e - 1 <= 133; }
+    // Another lane's.
+    __device__ __forceinline__ Widen of(uint32_t from) const { return Widen(__shfl_sync(0xFFFFFFFFu, e, from)); }
+    __device__ __forceinline__ static uint32_t check(const uint4 &v) {  // bits 7, 15, ...: there is a NaN
+        auto nan = [](uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; };
+        return nan(v.x) | nan(v.y) | nan(v.z) | nan(v.w);
+    }
+    __device__ __forceinline__ uint32_t two(uint32_t w) const {  // bytes 1 and 3
+        const uint32_t v = (w >> 4 & 0x07F007F0u) | (w & 0x80008000u);
+        uint32_t r;
+        asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(factor));
+        return r;
+    }
+    __device__ __forceinline__ uint2 four(uint32_t v) const {
+        return make_uint2(two(__byte_perm(v, 0, 0x1404)), two(__byte_perm(v, 0, 0x3424)));
+    }
+    __device__ __forceinline__ uint2 any(uint32_t v) const {
+        uint32_t lo, hi;
+        halves(v, lo, hi);
+        const float s = row_scale(e);
+        const float2 x = Pair<__half>::unpack(lo), y = Pair<__half>::unpack(hi);
+        return make_uint2(Pair<__nv_bfloat16>::pack(x.x * s, x.y * s), Pair<__nv_bfloat16>::pack(y.x * s, y.y * s));
     }
 };
+// fp16: the conversion is exact, and a product by 2^-12 to 2^15 is as exact as
+// fp16 can be; others come in two steps, of which the first is exact (an 8-bit
+// value's last bit is 2^-9 or more).
 template <>
-struct Widen<__half> {  // by two factors: the first product is exact (an 8-bit value's last bit is 2^-9 or more)
-    __half2 a, b;
-    __device__ __forceinline__ explicit Widen(uint32_t e) {
+struct Widen<__half> {
+    uint32_t e, a;
+    __device__ __forceinline__ explicit Widen(uint32_t exponent) : e(exponent) {
         const int k = (int)e - 127, ka = k < -12 ? -12 : k > 15 ? 15 : k;
-        const int kb = k - ka < -24 ? -40 : k - ka > 15 ? 15 : k - ka;
-        const uint32_t wa = e == 255 ? 0x7FFF7FFFu : (uint32_t)(ka + 15) * 0x04000400u;
-        const uint32_t wb = kb < -24 ? 0u : kb < -14 ? 0x00010001u << (kb + 24) : (uint32_t)(kb + 15) * 0x04000400u;
-        a = *reinterpret_cast<const __half2 *>(&wa), b = *reinterpret_cast<const __half2 *>(&wb);
+        a = (uint32_t)(ka + 15) * 0x04000400u;
     }
-    __device__ __forceinline__ uint32_t two(uint32_t f16x2) const {
-        const __half2 r = __hmul2(__hmul2(*reinterpret_cast<const __half2 *>(&f16x2), a), b);
+    __device__ __forceinline__ bool simple() const { return e - 115 <= 27; }
+    __device__ __forceinline__ Widen of(uint32_t from) const { return Widen(__shfl_sync(0xFFFFFFFFu, e, from)); }
+    __device__ __forceinline__ static uint32_t check(const uint4 &) { return 0; }  // a NaN stays one
+    __device__ __forceinline__ static uint32_t times(uint32_t x, uint32_t y) {
+        const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
         return *reinterpret_cast<const uint32_t *>(&r);
     }
+    __device__ __forceinline__ uint2 four(uint32_t v) const {
+        uint32_t lo, hi;
+        halves(v, lo, hi);
+        return make_uint2(times(lo, a), times(hi, a));
+    }
+    __device__ __forceinline__ uint2 any(uint32_t v) const {
+        const int k = (int)e - 127, kb = k < -12 ? k + 12 : k > 15 ? k - 15 : 0;
+        const uint32_t b = e == 255 ? 0x7FFF7FFFu : kb < -24 ? 0u : kb < -14 ? 0x00010001u << (kb + 24)
+                                                 : (uint32_t)((kb > 15 ? 15 : kb) + 15) * 0x04000400u;
+        const uint2 w = four(v);
+        return make_uint2(times(w.x, b), times(w.y, b));
+    }
 };
-template <class T>
-__device__ __forceinline__ uint2 widen4(uint32_t four, const Widen<T> &w) {
-    uint32_t lo, hi;
-    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(four));
-    return make_uint2(w.two(lo), w.two(hi));
-}
 
 // The copying warps.  A warp looks up and copies a quarter of a tile's rows: a
 // lane has one token's segment addresses, which the copying lanes take from it.
@@ -374,10 +420,21 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     using S = Shape<DP, ES>;
     constexpr uint32_t kWarpKeys = S::kKeys / kCopyWarps;
     constexpr uint32_t kParts = DP * ES / 16;  // 16-byte pieces of a row
-    constexpr uint32_t kCopies = kWarpKeys * kParts / 32;
+    constexpr uint32_t kAtOnce = 32 / kParts;  // rows that a warp copies with one instruction
+    constexpr uint32_t kCopies = kWarpKeys / kAtOnce;
     const uint32_t warp = thread / 32, lane = thread & 31;
-    const uint32_t key = warp * kWarpKeys + lane % kWarpKeys;  // this lane's, within the tile
-    const uint32_t parts = a.c.row_bytes / 16;
+    const uint32_t key = warp * kWarpKeys + lane % kWarpKeys;  // whose addresses this lane looks up, within the tile
+    const uint32_t part = lane % kParts, row0 = lane / kParts;  // what it copies: that piece of rows row0 + kAtOnce * i
+    const bool in = part < a.c.row_bytes / 16;
+    // Where those go: the pattern of the swizzle comes again after eight rows.
+    constexpr uint32_t kPeriod = 8 / kAtOnce ? 8 / kAtOnce : 1;
+    uint32_t place[kPeriod];
+#pragma unroll
+    for (uint32_t i = 0; i < kPeriod; i++) {
+        const uint32_t r = i * kAtOnce + row0, p16 = ES == 2 ? part : 2 * part;  // piece in 16 bits
+        place[i] = p16 / 8 * (S::kKeys * 128) + (warp * kWarpKeys + r) * 128 + ((p16 % 8 ^ (r & 7)) * 16);
+    }
+    auto place_of = [&](uint32_t c) { return place[c % kPeriod] + c / kPeriod * 1024; };
     const uint64_t room = a.c.pool_bytes - a.c.span;
     const bool fits = a.c.pool_bytes >= a.c.span, row_scales = ES == 1 && a.c.scale_offset;
 
@@ -390,22 +447,36 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
             if (t >= S::kStages && !warp_wait(&sh.kv_empty[stage], (t / S::kStages & 1) ^ 1)) return false;
             const uint4 *from = reinterpret_cast<const uint4 *>(held + t % S::kHeld * (S::kStage / 2)) + thread;
             uint8_t *to = ring + stage * S::kStage;
-            const uint32_t mine = (uint32_t)(scales >> (t % 8 * 8)) & 0xFF;
+            const Widen<T> own((uint32_t)(scales >> (t % 8 * 8)) & 0xFF);
+            bool odd = !__all_sync(0xFFFFFFFFu, own.simple());
+            uint32_t check = 0;
 #pragma unroll
             for (uint32_t c = 0; c < kCopies; c++) {
-                const uint32_t j = c * 32 + lane, row = j / kParts, part = j % kParts;
-                const uint32_t at = warp * kWarpKeys + row;
                 const uint4 raw = from[c * kCopyThreads];
-                const Widen<T> w(__shfl_sync(0xFFFFFFFFu, mine, row));
-                const uint2 x0 = widen4<T>(raw.x, w), x1 = widen4<T>(raw.y, w), x2 = widen4<T>(raw.z, w), x3 = widen4<T>(raw.w, w);
-                uint8_t *line = to + (part / 4) * (S::kKeys * 128) + at * 128;
-                const uint32_t p0 = part % 4 * 2;
-                *reinterpret_cast<uint4 *>(line + ((p0 ^ (at & 7)) * 16)) = make_uint4(x0.x, x0.y, x1.x, x1.y);
-                *reinterpret_cast<uint4 *>(line + (((p0 + 1) ^ (at & 7)) * 16)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                const Widen<T> w = own.of(c * kAtOnce + row0);
+                check |= Widen<T>::check(raw);
+                const uint2 x0 = w.four(raw.x), x1 = w.four(raw.y), x2 = w.four(raw.z), x3 = w.four(raw.w);
+                const uint32_t at = place_of(c);
+                *reinterpret_cast<uint4 *>(to + at) = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                *reinterpret_cast<uint4 *>(to + (at ^ 16)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
+            }
+            odd |= __any_sync(0xFFFFFFFFu, check & 0x80808080u);
+            if (odd) {
+#pragma unroll 1
+                for (uint32_t c = 0; c < kCopies; c++) {
+                    const uint4 raw = from[c * kCopyThreads];
+                    const Widen<T> w = own.of(c * kAtOnce + row0);
+                    const uint2 x0 = w.any(raw.x), x1 = w.any(raw.y), x2 = w.any(raw.z), x3 = w.any(raw.w);
+                    const uint32_t r = c * kAtOnce + row0, p0 = 2 * part;
+                    const uint32_t at = p0 / 8 * (S::kKeys * 128) + (warp * kWarpKeys + r) * 128 + ((p0 % 8 ^ (r & 7)) * 16);
+                    *reinterpret_cast<uint4 *>(to + at) = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                    *reinterpret_cast<uint4 *>(to + (at ^ 16)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                }
             }
         }
         fence_async();
-        mbar_arrive(&sh.kv_full[stage]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.kv_full[stage]);
         done++;
         return true;
     };
@@ -485,19 +556,26 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     auto set_scale = [&](uint32_t t, uint32_t exponent) {
         if (ES == 1) scales = (scales & ~(0xFFull << (t % 8 * 8))) | (uint64_t)exponent << (t % 8 * 8);
     };
-    auto issue = [&](uint64_t row) {  // an offset from the pool; odd: no row
+    auto issue = [&](uint64_t row) {  // this lane's row; odd: there is none
         const uint32_t t = issued;
         uint8_t *to = ES == 2 ? ring + t % S::kStages * S::kStage : held + t % (S::kHeld ? S::kHeld : 1) * (S::kStage / 2) + thread * 16;
         const uint32_t base = smem_u32(to);
+        const uint32_t rows = __ballot_sync(0xFFFFFFFFu, !(row & 1)) >> row0;
+        const uint64_t shift = (uint64_t)part * 16;
+        if (__all_sync(0xFFFFFFFFu, !(row & 1))) {
 #pragma unroll
-        for (uint32_t c = 0; c < kCopies; c++) {
-            const uint32_t j = c * 32 + lane, r = j / kParts, part = j % kParts;
-            const uint64_t from = __shfl_sync(0xFFFFFFFFu, row, r);
-            const uint32_t at = warp * kWarpKeys + r;
-            const bool in = !(from & 1) && part < parts;
-            const uint32_t dst = ES == 2 ? base + (part / 8) * (S::kKeys * 128) + at * 128 + ((part % 8 ^ (at & 7)) * 16)
-                                         : base + c * (kCopyThreads * 16);
-            copy16(dst, a.c.pool + (in ? from + part * 16 : 0), in);
+            for (uint32_t c = 0; c < kCopies; c++) {
+                const uint64_t from = __shfl_sync(0xFFFFFFFFu, row, c * kAtOnce + row0) + shift;
+                if (in) copy16(base + (ES == 2 ? place_of(c) : c * (kCopyThreads * 16)), reinterpret_cast<const void *>(from), true);
+            }
+        } else {
+#pragma unroll 1
+            for (uint32_t c = 0; c < kCopies; c++) {
+                const uint64_t from = (__shfl_sync(0xFFFFFFFFu, row, c * kAtOnce + row0) & ~1ull) + shift;
+                const uint32_t r = c * kAtOnce + row0;
+                const uint32_t at = part / 8 * (S::kKeys * 128) + (warp * kWarpKeys + r) * 128 + ((part % 8 ^ (r & 7)) * 16);
+                if (in) copy16(base + (ES == 2 ? at : c * (kCopyThreads * 16)), reinterpret_cast<const void *>(from), rows >> (c * kAtOnce) & 1);
+            }
         }
         copies_commit();
         issued++;
@@ -539,7 +617,7 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
             const uint64_t s = seg[kv];
             const bool good = fits && s <= room && !((uint32_t)s & 15);
             if (now.valid && !good) a.c.ok(s, bad);
-            row[kv] = now.valid && good ? s + now.token * a.c.token_stride : 1;
+            row[kv] = reinterpret_cast<uint64_t>(a.c.pool) + (now.valid && good ? s + now.token * a.c.token_stride : 1);
             if (row_scales && now.valid && good) exponent[kv] = __ldg(a.c.pool + s + a.c.scale_offset + now.token);
         }
         find_segments(two);
@@ -580,83 +658,106 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
 
 // --------------------------------------------------------- the tensor cores
 
+// One warp a slot.  A warp waits for tiles that only the other slot takes, too,
+// and lets go of them: so no barrier counts it twice in one phase.
 template <class T, int DP, int ES>
-__device__ __forceinline__ bool multiply(const Args &a, Shared &sh, const uint8_t *q_smem, const uint8_t *ring, uint32_t tmem) {
+__device__ __forceinline__ bool multiply(const Args &a, Shared &sh, const uint8_t *q_smem, const uint8_t *ring, uint32_t tmem,
+                                         uint32_t slot) {
     using S = Shape<DP, ES>;
     const uint32_t steps = a.c.dim / 16;
     const uint32_t qk = instruction<T>(S::kKeys, false, a.negate);
-    const uint32_t q0 = smem_u32(q_smem), r0 = smem_u32(ring);
-    // a slot's product with V still to come
-    bool pending[2] = {}, has_v[2] = {}, fresh[2] = {};
-    uint32_t v_tile[2] = {}, rounds[2] = {}, outs[2] = {};
-    auto finish = [&](uint32_t s) -> bool {
-        if (!mbar_wait(&sh.p_full[s], (rounds[s] & 1) ^ 1)) return false;  // of round rounds[s] - 1
-        const uint32_t stage = v_tile[s] % S::kStages;
-        if (!mbar_wait(&sh.kv_full[stage], v_tile[s] / S::kStages & 1)) return false;
-        if (fresh[s]) {
-            if (outs[s] && !mbar_wait(&sh.o_free[s], (outs[s] & 1) ^ 1)) return false;
-            outs[s]++;
+    const uint32_t pv = instruction<T>(DP == 256 ? (slot ? a.c.dim - 128 : 128) : a.c.dim, true, false);
+    const uint32_t q0 = operand_low(smem_u32(q_smem), 16), k0 = operand_low(smem_u32(ring), 16);
+    const uint32_t v0 = operand_low(smem_u32(ring) + (DP == 256 ? slot * 2 * (S::kKeys * 128) : 0), S::kKeys * 128);
+    const uint32_t s_at = tmem + slot * 128, o_at = tmem + 256 + slot * 128;
+    uint32_t tile = 0, rounds = 0, outs = 0;
+    bool pending = false, fresh = false, any = false;  // a product with V is due; it is the piece's first; there was a tile
+    // The values of the tile before.
+    auto finish = [&](uint32_t v_tile) -> bool {
+        const uint32_t stage = v_tile % S::kStages;
+        if (!warp_wait(&sh.kv_full[stage], v_tile / S::kStages & 1)) return false;
+        if (!pending) {
+            if (elected()) mbar_arrive(&sh.kv_empty[stage]);
+            return true;
         }
+        if (fresh) {
+            if (outs && !warp_wait(&sh.o_free[slot], (outs & 1) ^ 1)) return false;
+            outs++;
+        }
+        if (!warp_wait(&sh.p_full[slot], (rounds & 1) ^ 1)) return false;  // of round rounds - 1
         tmem_after();
-        const uint32_t col = DP == 256 ? s * 128 : 0;
-        const uint32_t n = DP == 256 ? (s ? a.c.dim - 128 : 128) : a.c.dim;
-        const uint32_t pv = instruction<T>(n, true, false);
-        const uint32_t v = r0 + stage * S::kStage + col / 64 * (S::kKeys * 128);
-        const uint32_t o = tmem + 256 + s * 128, p = tmem + s * 128;
+        const uint32_t low = v0 + stage * (S::kStage / 16), add = !fresh;
+        if (elected()) {
 #pragma unroll
-        for (uint32_t i = 0; i < S::kKeys / 16; i++)
-            mma_ts(o, p + i * 8, operand(v + i * 2048, S::kKeys * 128, 1024), pv, i > 0 || !fresh[s]);
-        mma_commit(&sh.pv_done[s]);
-        pending[s] = false;
-        if (!(pending[s ^ 1] && has_v[s ^ 1] && v_tile[s ^ 1] == v_tile[s])) mma_commit(&sh.kv_empty[stage]);
-        return true;
-    };
-    uint32_t tile = 0, event = 0;
-    for (uint32_t np = 0;; np++) {
-        if (!mbar_wait(&sh.pc_full[np % kPieces], np / kPieces & 1)) return false;
-        const Piece p = sh.pieces[np % kPieces];
-        if (!p.rows) break;
-        const uint32_t nt = (p.k1 - p.k0 + S::kKeys - 1) / S::kKeys;
-        bool started[2] = {};
-        for (uint32_t t = 0; t < nt; t++, event++) {
-            const uint32_t k_tile = tile++, stage = k_tile % S::kStages;
-            if (event) {
-                for (uint32_t s = 0; s < 2; s++)
-                    if (pending[s] && !has_v[s]) v_tile[s] = tile, has_v[s] = true;
-                tile++;
-            }
-            const uint32_t s_first = p.both ? 0 : event & 1, s_last = p.both ? 1 : s_first;
-            for (uint32_t s = s_first; s <= s_last; s++) {
-                if (pending[s] && !finish(s)) return false;
-                const uint32_t b = DP == 256 ? 0 : p.both ? s : np & 1;
-                // (a piece's queries come with its first keys)
-                if (s == s_first && !mbar_wait(&sh.kv_full[stage], k_tile / S::kStages & 1)) return false;
-                tmem_after();
-                const uint32_t q = q0 + b * S::kQ, kk = r0 + stage * S::kStage;
-                for (uint32_t i = 0; i < steps; i++)
-                    mma_ss(tmem + s * 128, operand(q + i / 4 * (kRows * 128) + i % 4 * 32, 16, 1024),
-                           operand(kk + i / 4 * (S::kKeys * 128) + i % 4 * 32, 16, 1024), qk, i > 0);
-                mma_commit(&sh.s_full[s]);
-                pending[s] = true, has_v[s] = false, fresh[s] = !started[s];
-                started[s] = true;
-                rounds[s]++;
-            }
+            for (uint32_t i = 0; i < S::kKeys / 16; i++) mma_ts(o_at, s_at + i * 8, low + i * 128, kOperandHigh, pv, i ? 1 : add);
+            mma_commit(&sh.pv_done[slot]);
             mma_commit(&sh.kv_empty[stage]);
         }
-        if (DP == 256 || p.both || !(np & 1)) mma_commit(&sh.q_empty[0]);
-        if (DP != 256 && (p.both || (np & 1))) mma_commit(&sh.q_empty[1]);
-        mbar_arrive(&sh.pc_empty[np % kPieces]);
+        pending = false;
+        return true;
+    };
+    for (uint32_t np = 0;; np++) {
+        if (!warp_wait(&sh.pc_full[np % kPieces], np / kPieces & 1)) return false;
+        const Piece &p = sh.pieces[np % kPieces];
+        if (!p.rows) break;
+        const uint32_t nt = (p.k1 - p.k0 + S::kKeys - 1) / S::kKeys;
+        const bool both = p.both;
+        bool started = false;
+        for (uint32_t t = 0; t < nt; t++) {
+            const uint32_t k_tile = tile, stage = k_tile % S::kStages;
+            const bool mine = both || ((p.event + t) & 1) == slot;
+            tile += any ? 2 : 1;
+            if (!mine) {  // (its keys come before the values of the tile before)
+                if (!warp_wait(&sh.kv_full[stage], k_tile / S::kStages & 1)) return false;
+                if (elected()) mbar_arrive(&sh.kv_empty[stage]);
+            }
+            if (any && !finish(k_tile + 1)) return false;
+            any = true;
+            if (mine) {  // (a piece's queries come with its first keys)
+                if (!warp_wait(&sh.kv_full[stage], k_tile / S::kStages & 1)) return false;
+                tmem_after();
+                const uint32_t q = q0 + (DP == 256 ? 0 : both ? slot : np & 1) * (S::kQ / 16), kk = k0 + stage * (S::kStage / 16);
+                if (elected()) {
+#pragma unroll
+                    for (uint32_t i = 0; i < DP / 16; i++)
+                        if (i < steps)
+                            mma_ss(s_at, q + i / 4 * (kRows * 8) + i % 4 * 2, kOperandHigh,
+                                   kk + i / 4 * (S::kKeys * 8) + i % 4 * 2, kOperandHigh, qk, i > 0);
+                    mma_commit(&sh.s_full[slot]);
+                    mma_commit(&sh.kv_empty[stage]);
+                }
+                pending = true, fresh = !started, started = true;
+                rounds++;
+            }
+        }
+        if (elected()) {
+            if (DP == 256 || both || !(np & 1)) mma_commit(&sh.q_empty[0]);
+            if (DP != 256 && (both || (np & 1))) mma_commit(&sh.q_empty[1]);
+            mbar_arrive(&sh.pc_empty[np % kPieces]);
+        }
     }
-    if (event) {
-        for (uint32_t s = 0; s < 2; s++)
-            if (pending[s] && !has_v[s]) v_tile[s] = tile, has_v[s] = true;
-        for (uint32_t s = 0; s < 2; s++)
-            if (pending[s] && !finish(s)) return false;
-    }
-    return true;
+    return !any || finish(tile);
 }
 
 // -------------------------------------------------------------- the softmax
+
+// Pairs of floats: two results an instruction.
+__device__ __forceinline__ uint64_t pair(float x, float y) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ void unpair(uint64_t v, float &x, float &y) { asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(v)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
 
 template <class T, int DP, int ES>
 __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem, uint32_t slot, uint32_t warp, uint32_t lane) {
@@ -672,48 +773,56 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
     const uint32_t s_at = tmem + lanes + slot * 128, o_at = tmem + lanes + 256 + slot * 128;
     const uint32_t col = DP == 256 ? slot * 128 : 0;
     const uint32_t cols = DP == 256 ? (slot ? a.c.dim - 128 : 128) : a.c.dim;  // of the output, a multiple of 16
-    uint32_t event = 0, rounds = 0;
+    const uint64_t scale = pair(a.scale2, a.scale2);
+    uint32_t rounds = 0;
     for (uint32_t np = 0;; np++) {
         if (!warp_wait(&sh.pc_full[np % kPieces], np / kPieces & 1)) return false;
-        const Piece p = sh.pieces[np % kPieces];
+        const Piece &p = sh.pieces[np % kPieces];
         if (!p.rows) return true;
-        const uint32_t nt = (p.k1 - p.k0 + S::kKeys - 1) / S::kKeys;
-        const uint32_t first_row = DP != 256 && p.both ? slot * kRows : 0;
+        const uint32_t keys = p.k1 - p.k0, nt = (keys + S::kKeys - 1) / S::kKeys;
+        const bool both = p.both;
+        const uint32_t first_row = DP != 256 && both ? slot * kRows : 0;
         const bool busy = first_row + warp * 32 < p.rows, mine = first_row + r < p.rows;
-        const uint32_t step = p.both ? 1 : 2;
-        uint32_t t = p.both ? 0 : (event & 1) ^ slot;
-        event += nt;
+        uint32_t t = both ? 0 : (p.event & 1) ^ slot;
         const bool any = t < nt;
         float base = 0, limit = -INFINITY, sum = 0;
-        for (bool fresh = true; t < nt; t += step, fresh = false) {
+        for (bool fresh = true; t < nt; t += both ? 1 : 2, fresh = false) {
             if (!warp_wait(&sh.s_full[slot], rounds & 1)) return false;
             rounds++;
             if (busy) {
                 tmem_after();
-                const uint32_t left = p.k1 - p.k0 - t * S::kKeys, n = left < S::kKeys ? left : S::kKeys;
-                float top = -INFINITY;
                 uint32_t x[32];
+                const uint32_t left = keys - t * S::kKeys;
+                if (left < S::kKeys) {  // what lies behind the last key weighs nothing
+#pragma unroll 1
+                    for (uint32_t c = left & ~15u; c < S::kKeys; c += 16) {
+                        uint32_t y[16];
+                        tmem_ld16(y, s_at + c);
+                        tmem_wait_ld();
 #pragma unroll
+                        for (int i = 0; i < 16; i++) y[i] = c + i < left ? y[i] : 0xFF800000u;
+                        tmem_st16(s_at + c, y);
+                    }
+                    tmem_wait_st();
+                }
+                float top = -INFINITY, top2 = -INFINITY;
+#pragma unroll 1
                 for (uint32_t c = 0; c < S::kKeys; c += 32) {
                     tmem_ld32(x, s_at + c);
                     tmem_wait_ld();
-                    if (c + 32 <= n) {
 #pragma unroll
-                        for (int i = 0; i < 32; i++) top = fmaxf(top, __uint_as_float(x[i]));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 32; i++)
-                            if (c + i < n) top = fmaxf(top, __uint_as_float(x[i]));
+                    for (int i = 0; i < 32; i += 4) {
+                        top = fmaxf(top, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
+                        top2 = fmaxf(top2, fmaxf(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])));
                     }
                 }
-                top *= a.scale2;
+                top = fmaxf(top, top2) * a.scale2;
                 const bool over = top > limit;
                 if (__any_sync(0xFFFFFFFFu, over)) {
                     float factor = 1.0f;
                     if (over) {
                         const float to = top - kBoost;
-                        factor = fresh ? 0.0f : exp2_fast(base - to);
-                        if (limit == -INFINITY) factor = 0.0f;  // nothing was added so far
+                        factor = limit == -INFINITY ? 0.0f : exp2_fast(base - to);  // 0: nothing was added so far
                         base = to;
                         limit = top + kSlack;
                         sum *= factor;
@@ -722,8 +831,9 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
                         // the product before has to be in the sums
                         if (!warp_wait(&sh.pv_done[slot], rounds & 1)) return false;
                         tmem_after();
-                        uint32_t y[16];
+#pragma unroll 1
                         for (uint32_t c = 0; c < cols; c += 16) {
+                            uint32_t y[16];
                             tmem_ld16(y, o_at + c);
                             tmem_wait_ld();
 #pragma unroll
@@ -733,32 +843,26 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
                         tmem_wait_st();
                     }
                 }
-                float sums[4] = {};
-#pragma unroll
+                const uint64_t shift = pair(-base, -base);
+                uint64_t sums[2] = {};
+#pragma unroll 1
                 for (uint32_t c = 0; c < S::kKeys; c += 32) {
                     tmem_ld32(x, s_at + c);
                     tmem_wait_ld();
                     uint32_t w[16];
-                    if (c + 32 <= n) {
 #pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            const float e0 = exp2_fast(fmaf(__uint_as_float(x[2 * i]), a.scale2, -base));
-                            const float e1 = exp2_fast(fmaf(__uint_as_float(x[2 * i + 1]), a.scale2, -base));
-                            sums[i % 2 * 2] += e0, sums[i % 2 * 2 + 1] += e1;
-                            w[i] = Pair<T>::pack(e0, e1);
-                        }
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 16; i++) {
-                            const float e0 = c + 2 * i < n ? exp2_fast(fmaf(__uint_as_float(x[2 * i]), a.scale2, -base)) : 0.0f;
-                            const float e1 = c + 2 * i + 1 < n ? exp2_fast(fmaf(__uint_as_float(x[2 * i + 1]), a.scale2, -base)) : 0.0f;
-                            sums[i % 2 * 2] += e0, sums[i % 2 * 2 + 1] += e1;
-                            w[i] = Pair<T>::pack(e0, e1);
-                        }
+                    for (int i = 0; i < 16; i++) {
+                        float e0, e1;
+                        unpair(fma2(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale, shift), e0, e1);
+                        e0 = exp2_fast(e0), e1 = exp2_fast(e1);
+                        sums[i & 1] = add2(sums[i & 1], pair(e0, e1));
+                        w[i] = Pair<T>::pack(e0, e1);
                     }
                     tmem_st16(s_at + c / 2, w);
                 }
-                sum += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+                float s0, s1;
+                unpair(add2(sums[0], sums[1]), s0, s1);
+                sum += s0 + s1;
                 tmem_wait_st();
                 tmem_before();
             }
@@ -770,8 +874,9 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
             if (!warp_wait(&sh.pv_done[slot], (rounds & 1) ^ 1)) return false;
             if (busy) {
                 tmem_after();
-                uint32_t y[16];
+#pragma unroll 1
                 for (uint32_t c = 0; c < cols; c += 16) {
+                    uint32_t y[16];
                     tmem_ld16(y, o_at + c);
                     tmem_wait_ld();
                     if (mine) {
@@ -813,14 +918,14 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
     uint32_t upto = warp_incl_sum(mine);
     if (lane == 31) sh.sums[warp] = upto;
     if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < S::kStages; i++) mbar_init(&sh.kv_full[i], kCopyThreads), mbar_init(&sh.kv_empty[i], 1);
+        for (uint32_t i = 0; i < S::kStages; i++) mbar_init(&sh.kv_full[i], kCopyWarps), mbar_init(&sh.kv_empty[i], 2);
         for (int i = 0; i < 2; i++) {
-            mbar_init(&sh.q_empty[i], 1);
+            mbar_init(&sh.q_empty[i], 2);
             mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 4);
             mbar_init(&sh.pv_done[i], 1), mbar_init(&sh.o_free[i], 4);
         }
-        for (int i = 0; i < kPieces; i++) mbar_init(&sh.pc_full[i], 1), mbar_init(&sh.pc_empty[i], kSoftWarps + kCopyWarps + 1);
-        mbar_init(&sh.drained, 1);
+        for (int i = 0; i < kPieces; i++) mbar_init(&sh.pc_full[i], 1), mbar_init(&sh.pc_empty[i], kSoftWarps + kCopyWarps + 2);
+        mbar_init(&sh.drained, 2);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
@@ -850,10 +955,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
         } else if (warp < kSoftWarps + kCopyWarps) {
             ok = copy_tiles<T, DP, ES>(a, sh, q_smem, ring, held, threadIdx.x - 32 * kSoftWarps, bad);
             copies_wait(0);
-        } else if (lane == 0) {
-            ok = multiply<T, DP, ES>(a, sh, q_smem, ring, tmem);
-            mma_commit(&sh.drained);  // no instruction outlives its operands
-            if (!mbar_wait(&sh.drained, 0)) ok = false;
+        } else if (warp < kWalkWarp) {
+            ok = multiply<T, DP, ES>(a, sh, q_smem, ring, tmem, warp - kMmaWarp);
+            if (elected()) mma_commit(&sh.drained);  // no instruction outlives its operands
+            __syncwarp();
+            if (!warp_wait(&sh.drained, 0)) ok = false;
         }
     }
     if (!ok) bad |= KVX_S_TIMEOUT;
