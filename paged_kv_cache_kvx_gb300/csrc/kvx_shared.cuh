@@ -19,6 +19,7 @@ constexpr uint32_t kCopyThreads = 32 * kCopyWarps;
 // copying warps hold back (Shape::kPending, two to a piece of one tile) and look
 // up ahead reach back.
 constexpr int kPieces = 16;
+constexpr uint32_t kRound = 64;  // keys that a slot's softmax takes at a time
 constexpr uint32_t kRows = 128;  // of a slot: the tensor cores' M, a query row for each lane of tensor memory
 constexpr uint32_t kExtra = 1;   // tiles that a unit's own overhead counts as
 constexpr uint32_t kMinShare = 2;
@@ -98,14 +99,14 @@ struct Shape {
     static constexpr uint32_t kQBufs = DP == 256 ? 1 : 2;
     static constexpr uint32_t kStages = ES == 2 ? (DP == 64 ? 11 : 5) : (DP == 64 ? 6 : 3);
     static constexpr uint32_t kHeld = ES == 2 ? 0 : DP == 64 ? 8 : 4;  // 8-bit tiles on their way
-    static constexpr uint32_t kPending = ES == 2 ? kStages - 1 : kHeld;
     static constexpr uint32_t kSmem = 1024 + kQ * kQBufs + kStages * kStage + kHeld * (kStage / 2);
 };
 
 struct Shared {  // behind the tiles
     uint64_t kv_full[11], kv_empty[11];
     uint64_t q_empty[2];
-    uint64_t s_full[2], p_full[2], pv_done[2], o_free[2];
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // by slot and round & 1
+    uint64_t o_free[2];
     uint64_t pc_full[kPieces], pc_empty[kPieces];
     uint64_t drained;
     Piece pieces[kPieces];
@@ -138,6 +139,10 @@ __device__ __forceinline__ bool warp_test(uint64_t *bar, uint32_t parity) {
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, bool there) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(there ? 16 : 0) : "memory");
 }
+// Arrives when this thread's copies so far are complete.
+__device__ __forceinline__ void mbar_arrive_copies(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 __device__ __forceinline__ void copies_wait(uint32_t most) {  // until at most that many groups are on their way
     switch (most) {
@@ -153,11 +158,20 @@ __device__ __forceinline__ void copies_wait(uint32_t most) {  // until at most t
         default: asm volatile("cp.async.wait_group 9;" ::: "memory"); break;
     }
 }
-// What this thread wrote to shared memory becomes visible to the tensor cores.
+// What this thread wrote to shared memory, or has seen others write, is there for
+// the tensor cores.
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void tmem_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void tmem_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tmem_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// Until loads so far are in their registers; nothing that uses these comes before it.
+template <int N>
+__device__ __forceinline__ void tmem_wait_ld(uint32_t (&r)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; i += 8)
+        asm volatile("" : "+r"(r[i]), "+r"(r[i + 1]), "+r"(r[i + 2]), "+r"(r[i + 3]), "+r"(r[i + 4]), "+r"(r[i + 5]),
+                     "+r"(r[i + 6]), "+r"(r[i + 7]));
+}
 __device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 // Arrives when the tensor instructions issued so far are complete.
 __device__ __forceinline__ void mma_commit(uint64_t *bar) {
@@ -438,13 +452,15 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     const uint64_t room = a.c.pool_bytes - a.c.span;
     const bool fits = a.c.pool_bytes >= a.c.span, row_scales = ES == 1 && a.c.scale_offset;
 
-    // Tiles whose copies have been issued and not yet handed over.
+    // 16-bit tiles are copied to where the tensor cores take them, and count as
+    // there when the copies arrive.  8-bit ones come to a place of the thread's own
+    // first and are handed over as 16-bit ones.
     uint32_t issued = 0, done = 0;
-    uint64_t scales = 0;   // a byte for each of the last eight tiles: this lane's row's
+    uint64_t scales = 0;  // a byte for each of the last eight tiles: this lane's row's
     auto hand_over = [&]() -> bool {
         const uint32_t t = done, stage = t % S::kStages;
+        if (t >= S::kStages && !warp_wait(&sh.kv_empty[stage], (t / S::kStages & 1) ^ 1)) return false;
         if constexpr (ES == 1) {
-            if (t >= S::kStages && !warp_wait(&sh.kv_empty[stage], (t / S::kStages & 1) ^ 1)) return false;
             const uint4 *from = reinterpret_cast<const uint4 *>(held + t % S::kHeld * (S::kStage / 2)) + thread;
             uint8_t *to = ring + stage * S::kStage;
             const Widen<T> own((uint32_t)(scales >> (t % 8 * 8)) & 0xFF);
@@ -482,6 +498,7 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     };
     // Hands over all that is held back, before a wait for another warp.
     auto drain = [&]() -> bool {
+        if (ES == 2) return true;
         copies_wait(0);
         while (done < issued)
             if (!hand_over()) return false;
@@ -540,18 +557,14 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
 
     // Room for the next tile.
     auto make_room = [&]() -> bool {
-        if (issued - done >= S::kPending) {
-            copies_wait(S::kPending - 1);
-            if (!hand_over()) return false;
-        }
         if constexpr (ES == 2) {
             const uint32_t stage = issued % S::kStages;
-            const uint32_t parity = (issued / S::kStages & 1) ^ 1;
-            if (issued >= S::kStages && !warp_test(&sh.kv_empty[stage], parity) &&
-                !(drain() && warp_wait(&sh.kv_empty[stage], parity)))
-                return false;
+            return issued < S::kStages || warp_wait(&sh.kv_empty[stage], (issued / S::kStages & 1) ^ 1);
+        } else {
+            if (issued - done < S::kHeld) return true;
+            copies_wait(S::kHeld - 1);
+            return hand_over();
         }
-        return true;
     };
     auto set_scale = [&](uint32_t t, uint32_t exponent) {
         if (ES == 1) scales = (scales & ~(0xFFull << (t % 8 * 8))) | (uint64_t)exponent << (t % 8 * 8);
@@ -577,7 +590,10 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
                 if (in) copy16(base + (ES == 2 ? at : c * (kCopyThreads * 16)), reinterpret_cast<const void *>(from), rows >> (c * kAtOnce) & 1);
             }
         }
-        copies_commit();
+        if (ES == 2)
+            mbar_arrive_copies(&sh.kv_full[t % S::kStages]);
+        else
+            copies_commit();
         issued++;
     };
     uint32_t q_used[2] = {};
@@ -601,142 +617,177 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
         return true;
     };
 
-    Look one = find();
-    find_segments(one);
-    Look two = one.any ? find() : Look{};
-    uint64_t v_row = 1;
-    uint32_t k_tile = 0, k_exponent = 127, v_exponent = 127;  // scales come a step later
-    bool v_any = false;
-    while (one.any && alive) {
-        // `one` has its addresses on their way, `two` its block ids
-        const Look now = one;
+    // Rows of the tile after a look-up's, with their scales on their way.
+    struct Rows {
         uint64_t row[2];
-        uint32_t exponent[2] = {127, 127};
+        uint32_t exponent[2];
+        uint32_t any, first, last, piece;
+    };
+    auto find_rows = [&](const Look &l) -> Rows {
+        Rows r = {};
+        r.any = l.any, r.first = l.first, r.last = l.last, r.piece = l.piece;
+        if (!l.any) return r;
 #pragma unroll
         for (int kv = 0; kv < 2; kv++) {
             const uint64_t s = seg[kv];
-            const bool good = fits && s <= room && !((uint32_t)s & 15);
-            if (now.valid && !good) a.c.ok(s, bad);
-            row[kv] = reinterpret_cast<uint64_t>(a.c.pool) + (now.valid && good ? s + now.token * a.c.token_stride : 1);
-            if (row_scales && now.valid && good) exponent[kv] = __ldg(a.c.pool + s + a.c.scale_offset + now.token);
+            const bool good = l.valid && fits && s <= room && !((uint32_t)s & 15);
+            if (l.valid && !good) a.c.ok(s, bad);
+            r.row[kv] = reinterpret_cast<uint64_t>(a.c.pool) + (good ? s + l.token * a.c.token_stride : 1);
+            r.exponent[kv] = 127;
+            if (row_scales && good) r.exponent[kv] = __ldg(a.c.pool + s + a.c.scale_offset + l.token);
         }
-        find_segments(two);
+        return r;
+    };
+    Look one = find();
+    find_segments(one);
+    Look two = one.any ? find() : Look{};
+    Rows next = find_rows(one);
+    one = two;
+    find_segments(one);
+    two = one.any ? find() : Look{};
+    while (next.any && alive) {
+        // the next tile's scales, the addresses of the one after and the block ids
+        // of the one after that are loaded meanwhile
+        const Rows now = next;
+        next = find_rows(one);
         one = two;
+        find_segments(one);
         two = one.any ? find() : Look{};
-        if (!alive) return false;
-
-        if (v_any) set_scale(k_tile, k_exponent);  // of the tile before
-        if (!make_room()) return false;
+        if (!alive || !make_room()) return false;
         if (now.first) {
             const uint32_t both = sh.pieces[now.piece % kPieces].both;
             for (uint32_t b = 0; b < S::kQBufs; b++)
                 if ((DP == 256 || both || b == (now.piece & 1)) && !issue_q(b, now.piece)) return false;
         }
-        k_tile = issued;
-        issue(row[0]);
-        if (v_any) {
-            if (!make_room()) return false;
-            set_scale(issued, v_exponent);
-            issue(v_row);
-        }
-        v_row = row[1], v_any = true;
-        k_exponent = exponent[0], v_exponent = exponent[1];
+        set_scale(issued, now.exponent[0]);
+        issue(now.row[0]);
+        if (!make_room()) return false;
+        set_scale(issued, now.exponent[1]);
+        issue(now.row[1]);
         if (now.last) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.pc_empty[now.piece % kPieces]);
         }
     }
-    if (!alive) return false;
-    if (v_any) {
-        set_scale(k_tile, k_exponent);
-        if (!make_room()) return false;
-        set_scale(issued, v_exponent);
-        issue(v_row);
-    }
-    return drain();
+    return alive && drain();
 }
 
 // --------------------------------------------------------- the tensor cores
 
-// One warp a slot.  A warp waits for tiles that only the other slot takes, too,
-// and lets go of them: so no barrier counts it twice in one phase.
+// One warp a slot.  A slot goes by rounds of kRound keys, whose logits and weights
+// have two places: the next round's logits are there when the softmax has done
+// one.  Its warp takes the next product Q K^T as soon as a place is free and keys
+// are there, else the oldest product with V.  One thread does it all: without
+// votes and branches that a warp would have to come together after.
 template <class T, int DP, int ES>
 __device__ __forceinline__ bool multiply(const Args &a, Shared &sh, const uint8_t *q_smem, const uint8_t *ring, uint32_t tmem,
                                          uint32_t slot) {
     using S = Shape<DP, ES>;
     const uint32_t steps = a.c.dim / 16;
-    const uint32_t qk = instruction<T>(S::kKeys, false, a.negate);
+    const uint32_t qk = instruction<T>(kRound, false, a.negate);
     const uint32_t pv = instruction<T>(DP == 256 ? (slot ? a.c.dim - 128 : 128) : a.c.dim, true, false);
     const uint32_t q0 = operand_low(smem_u32(q_smem), 16), k0 = operand_low(smem_u32(ring), 16);
     const uint32_t v0 = operand_low(smem_u32(ring) + (DP == 256 ? slot * 2 * (S::kKeys * 128) : 0), S::kKeys * 128);
     const uint32_t s_at = tmem + slot * 128, o_at = tmem + 256 + slot * 128;
-    uint32_t tile = 0, rounds = 0, outs = 0;
-    bool pending = false, fresh = false, any = false;  // a product with V is due; it is the piece's first; there was a tile
-    // The values of the tile before.
-    auto finish = [&](uint32_t v_tile) -> bool {
-        const uint32_t stage = v_tile % S::kStages;
-        if (!warp_wait(&sh.kv_full[stage], v_tile / S::kStages & 1)) return false;
-        if (!pending) {
-            if (elected()) mbar_arrive(&sh.kv_empty[stage]);
-            return true;
-        }
-        if (fresh) {
-            if (outs && !warp_wait(&sh.o_free[slot], (outs & 1) ^ 1)) return false;
+    uint32_t tile = 0;                        // its keys are the copies' number 2 * tile, its values the next
+    uint32_t started = 0, done = 0, outs = 0;  // rounds, and pieces with one
+    struct Round {  // a product with V that is due
+        uint32_t v;  // the values' number
+        uint32_t half;
+        bool fresh, last, twice;  // the piece's first; the tile's last round; lets go of the values for both slots
+    };
+    Round due = {}, then = {};
+    // Copies are looked at in their order, the other slot's too: a barrier's parity
+    // says nothing about a tile before the one that was in its place is known to
+    // have come.
+    uint32_t seen = 0;  // copies known to be there
+    auto there = [&](uint32_t copy) -> bool {
+        while (seen <= copy && mbar_test(&sh.kv_full[seen % S::kStages], seen / S::kStages & 1)) seen++;
+        return seen > copy;
+    };
+    auto await = [&](uint32_t copy) -> bool {
+        for (; seen <= copy; seen++)
+            if (!mbar_wait(&sh.kv_full[seen % S::kStages], seen / S::kStages & 1)) return false;
+        return true;
+    };
+    auto finish = [&]() -> bool {
+        const uint32_t stage = due.v % S::kStages, buffer = done & 1;
+        if (!await(due.v)) return false;
+        if (due.fresh) {
+            if (outs && !mbar_wait(&sh.o_free[slot], (outs & 1) ^ 1)) return false;
             outs++;
         }
-        if (!warp_wait(&sh.p_full[slot], (rounds & 1) ^ 1)) return false;  // of round rounds - 1
+        if (!mbar_wait(&sh.p_full[slot][buffer], done >> 1 & 1)) return false;
         tmem_after();
-        const uint32_t low = v0 + stage * (S::kStage / 16), add = !fresh;
-        if (elected()) {
+        fence_async();  // the copies' writes, too, are before what follows
+        const uint32_t low = v0 + stage * (S::kStage / 16) + due.half * (kRound * 8), add = !due.fresh, p = s_at + buffer * kRound;
 #pragma unroll
-            for (uint32_t i = 0; i < S::kKeys / 16; i++) mma_ts(o_at, s_at + i * 8, low + i * 128, kOperandHigh, pv, i ? 1 : add);
-            mma_commit(&sh.pv_done[slot]);
-            mma_commit(&sh.kv_empty[stage]);
-        }
-        pending = false;
+        for (uint32_t i = 0; i < kRound / 16; i++) mma_ts(o_at, p + i * 8, low + i * 128, kOperandHigh, pv, i ? 1 : add);
+        mma_commit(&sh.pv_done[slot][buffer]);
+        if (due.last) mma_commit(&sh.kv_empty[stage]);
+        if (due.last && due.twice) mma_commit(&sh.kv_empty[stage]);
+        due = then;
+        done++;
         return true;
     };
     for (uint32_t np = 0;; np++) {
-        if (!warp_wait(&sh.pc_full[np % kPieces], np / kPieces & 1)) return false;
+        if (!mbar_test(&sh.pc_full[np % kPieces], np / kPieces & 1)) {
+            while (done != started)  // nothing waits for the next piece
+                if (!finish()) return false;
+            if (!mbar_wait(&sh.pc_full[np % kPieces], np / kPieces & 1)) return false;
+        }
         const Piece &p = sh.pieces[np % kPieces];
         if (!p.rows) break;
-        const uint32_t nt = (p.k1 - p.k0 + S::kKeys - 1) / S::kKeys;
+        const uint32_t keys = p.k1 - p.k0, nt = (keys + S::kKeys - 1) / S::kKeys;
         const bool both = p.both;
-        bool started = false;
-        for (uint32_t t = 0; t < nt; t++) {
-            const uint32_t k_tile = tile, stage = k_tile % S::kStages;
-            const bool mine = both || ((p.event + t) & 1) == slot;
-            tile += any ? 2 : 1;
-            if (!mine) {  // (its keys come before the values of the tile before)
-                if (!warp_wait(&sh.kv_full[stage], k_tile / S::kStages & 1)) return false;
-                if (elected()) mbar_arrive(&sh.kv_empty[stage]);
-            }
-            if (any && !finish(k_tile + 1)) return false;
-            any = true;
-            if (mine) {  // (a piece's queries come with its first keys)
-                if (!warp_wait(&sh.kv_full[stage], k_tile / S::kStages & 1)) return false;
-                tmem_after();
-                const uint32_t q = q0 + (DP == 256 ? 0 : both ? slot : np & 1) * (S::kQ / 16), kk = k0 + stage * (S::kStage / 16);
-                if (elected()) {
-#pragma unroll
-                    for (uint32_t i = 0; i < DP / 16; i++)
-                        if (i < steps)
-                            mma_ss(s_at, q + i / 4 * (kRows * 8) + i % 4 * 2, kOperandHigh,
-                                   kk + i / 4 * (S::kKeys * 8) + i % 4 * 2, kOperandHigh, qk, i > 0);
-                    mma_commit(&sh.s_full[slot]);
-                    mma_commit(&sh.kv_empty[stage]);
+        uint32_t t = both ? 0 : (p.event & 1) ^ slot;
+        const bool any = t < nt;
+        bool fresh = true;
+        for (; t < nt; t += both ? 1 : 2) {
+            const uint32_t k = 2 * (tile + t), stage = k % S::kStages;
+            const uint32_t halves = S::kKeys == kRound || keys - t * S::kKeys <= kRound ? 1 : 2;
+            for (uint32_t h = 0; h < halves; h++) {
+                if (started - done == 2 && !finish()) return false;
+                if (!h) {  // (a piece's queries come with its first keys)
+                    while (done != started && !there(k))
+                        if (!finish()) return false;
+                    if (!await(k)) return false;
                 }
-                pending = true, fresh = !started, started = true;
-                rounds++;
+                tmem_after();
+                fence_async();
+                const uint32_t q = q0 + (DP == 256 ? 0 : both ? slot : np & 1) * (S::kQ / 16);
+                const uint32_t kk = k0 + stage * (S::kStage / 16) + h * (kRound * 8);
+                const uint32_t buffer = started & 1, d = s_at + buffer * kRound;
+                const bool last = h + 1 == halves;
+#pragma unroll
+                for (uint32_t i = 0; i < DP / 16; i++)
+                    if (i < steps)
+                        mma_ss(d, q + i / 4 * (kRows * 8) + i % 4 * 2, kOperandHigh,
+                               kk + i / 4 * (S::kKeys * 8) + i % 4 * 2, kOperandHigh, qk, i > 0);
+                mma_commit(&sh.s_full[slot][buffer]);
+                if (last) mma_commit(&sh.kv_empty[stage]);
+                if (last && !both) mma_commit(&sh.kv_empty[stage]);
+                const Round r = {k + 1, h, fresh, last, !both};
+                if (started == done)
+                    due = r;
+                else
+                    then = r;
+                fresh = false;
+                started++;
             }
         }
-        if (elected()) {
-            if (DP == 256 || both || !(np & 1)) mma_commit(&sh.q_empty[0]);
-            if (DP != 256 && (both || (np & 1))) mma_commit(&sh.q_empty[1]);
-            mbar_arrive(&sh.pc_empty[np % kPieces]);
-        }
+        tile += nt;
+        // both slots let go of a query, or the only one that took it twice
+        if (any)
+            for (int i = 0; i < (both || nt > 1 ? 1 : 2); i++) {
+                if (DP == 256 || both || !(np & 1)) mma_commit(&sh.q_empty[0]);
+                if (DP != 256 && (both || (np & 1))) mma_commit(&sh.q_empty[1]);
+            }
+        mbar_arrive(&sh.pc_empty[np % kPieces]);
     }
-    return !any || finish(tile);
+    while (done != started)
+        if (!finish()) return false;
+    return true;
 }
 
 // -------------------------------------------------------------- the softmax
@@ -786,56 +837,56 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
         uint32_t t = both ? 0 : (p.event & 1) ^ slot;
         const bool any = t < nt;
         float base = 0, limit = -INFINITY, sum = 0;
-        for (bool fresh = true; t < nt; t += both ? 1 : 2, fresh = false) {
-            if (!warp_wait(&sh.s_full[slot], rounds & 1)) return false;
-            rounds++;
+        uint32_t at = t * S::kKeys;  // the round's first key
+        for (bool fresh = true; at < keys; fresh = false) {
+            const uint32_t buffer = rounds & 1, left = keys - at;
+            if (!warp_wait(&sh.s_full[slot][buffer], rounds >> 1 & 1)) return false;
             if (busy) {
                 tmem_after();
-                uint32_t x[32];
-                const uint32_t left = keys - t * S::kKeys;
-                if (left < S::kKeys) {  // what lies behind the last key weighs nothing
+                const uint32_t s = s_at + buffer * kRound;
+                if (left < kRound) {  // what lies behind the last key weighs nothing
 #pragma unroll 1
-                    for (uint32_t c = left & ~15u; c < S::kKeys; c += 16) {
+                    for (uint32_t c = left & ~15u; c < kRound; c += 16) {
                         uint32_t y[16];
-                        tmem_ld16(y, s_at + c);
-                        tmem_wait_ld();
+                        tmem_ld16(y, s + c);
+                        tmem_wait_ld(y);
 #pragma unroll
                         for (int i = 0; i < 16; i++) y[i] = c + i < left ? y[i] : 0xFF800000u;
-                        tmem_st16(s_at + c, y);
+                        tmem_st16(s + c, y);
                     }
                     tmem_wait_st();
                 }
-                float top = -INFINITY, top2 = -INFINITY;
-#pragma unroll 1
-                for (uint32_t c = 0; c < S::kKeys; c += 32) {
-                    tmem_ld32(x, s_at + c);
-                    tmem_wait_ld();
+                uint32_t x[2][32];
+                tmem_ld32(x[0], s);
+                tmem_ld32(x[1], s + 32);
+                tmem_wait_ld(x[0]);
+                tmem_wait_ld(x[1]);
+                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int i = 0; i < 32; i += 4) {
-                        top = fmaxf(top, fmaxf(__uint_as_float(x[i]), __uint_as_float(x[i + 1])));
-                        top2 = fmaxf(top2, fmaxf(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3])));
-                    }
-                }
-                top = fmaxf(top, top2) * a.scale2;
-                const bool over = top > limit;
+                for (int i = 0; i < 64; i += 8)
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[i / 32][i % 32 + 2 * k]), __uint_as_float(x[i / 32][i % 32 + 2 * k + 1])));
+                top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale2;
+                const bool over = top[0] > limit;
                 if (__any_sync(0xFFFFFFFFu, over)) {
                     float factor = 1.0f;
                     if (over) {
-                        const float to = top - kBoost;
+                        const float to = top[0] - kBoost;
                         factor = limit == -INFINITY ? 0.0f : exp2_fast(base - to);  // 0: nothing was added so far
                         base = to;
-                        limit = top + kSlack;
+                        limit = top[0] + kSlack;
                         sum *= factor;
                     }
                     if (!fresh) {
-                        // the product before has to be in the sums
-                        if (!warp_wait(&sh.pv_done[slot], rounds & 1)) return false;
+                        // the product before has to be in the outputs
+                        if (!warp_wait(&sh.pv_done[slot][buffer ^ 1], (rounds - 1) >> 1 & 1)) return false;
                         tmem_after();
 #pragma unroll 1
                         for (uint32_t c = 0; c < cols; c += 16) {
                             uint32_t y[16];
                             tmem_ld16(y, o_at + c);
-                            tmem_wait_ld();
+                            tmem_wait_ld(y);
 #pragma unroll
                             for (int i = 0; i < 16; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * factor);
                             tmem_st16(o_at + c, y);
@@ -845,20 +896,18 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
                 }
                 const uint64_t shift = pair(-base, -base);
                 uint64_t sums[2] = {};
-#pragma unroll 1
-                for (uint32_t c = 0; c < S::kKeys; c += 32) {
-                    tmem_ld32(x, s_at + c);
-                    tmem_wait_ld();
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
                     uint32_t w[16];
 #pragma unroll
                     for (int i = 0; i < 16; i++) {
                         float e0, e1;
-                        unpair(fma2(pair(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1])), scale, shift), e0, e1);
+                        unpair(fma2(pair(__uint_as_float(x[h][2 * i]), __uint_as_float(x[h][2 * i + 1])), scale, shift), e0, e1);
                         e0 = exp2_fast(e0), e1 = exp2_fast(e1);
                         sums[i & 1] = add2(sums[i & 1], pair(e0, e1));
                         w[i] = Pair<T>::pack(e0, e1);
                     }
-                    tmem_st16(s_at + c / 2, w);
+                    tmem_st16(s + h * 16, w);
                 }
                 float s0, s1;
                 unpair(add2(sums[0], sums[1]), s0, s1);
@@ -867,18 +916,21 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
                 tmem_before();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[slot]);
+            if (lane == 0) mbar_arrive(&sh.p_full[slot][buffer]);
+            rounds++;
+            at += kRound;
+            if (at % S::kKeys == 0 && !both) at += S::kKeys;  // the other slot's tile
         }
         const uint64_t row = p.part_row + (slot && DP != 256 ? p.off_b : 0) + r;
         if (any) {
-            if (!warp_wait(&sh.pv_done[slot], (rounds & 1) ^ 1)) return false;
+            if (!warp_wait(&sh.pv_done[slot][(rounds - 1) & 1], (rounds - 1) >> 1 & 1)) return false;
             if (busy) {
                 tmem_after();
 #pragma unroll 1
                 for (uint32_t c = 0; c < cols; c += 16) {
                     uint32_t y[16];
                     tmem_ld16(y, o_at + c);
-                    tmem_wait_ld();
+                    tmem_wait_ld(y);
                     if (mine) {
                         uint4 *to = reinterpret_cast<uint4 *>(a.part_o + row * a.c.dim + col + c);
 #pragma unroll
@@ -918,11 +970,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
     uint32_t upto = warp_incl_sum(mine);
     if (lane == 31) sh.sums[warp] = upto;
     if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < S::kStages; i++) mbar_init(&sh.kv_full[i], kCopyWarps), mbar_init(&sh.kv_empty[i], 2);
+        for (uint32_t i = 0; i < S::kStages; i++) mbar_init(&sh.kv_full[i], ES == 2 ? kCopyThreads : kCopyWarps), mbar_init(&sh.kv_empty[i], 2);
         for (int i = 0; i < 2; i++) {
             mbar_init(&sh.q_empty[i], 2);
-            mbar_init(&sh.s_full[i], 1), mbar_init(&sh.p_full[i], 4);
-            mbar_init(&sh.pv_done[i], 1), mbar_init(&sh.o_free[i], 4);
+            for (int k = 0; k < 2; k++) mbar_init(&sh.s_full[i][k], 1), mbar_init(&sh.p_full[i][k], 4), mbar_init(&sh.pv_done[i][k], 1);
+            mbar_init(&sh.o_free[i], 4);
         }
         for (int i = 0; i < kPieces; i++) mbar_init(&sh.pc_full[i], 1), mbar_init(&sh.pc_empty[i], kSoftWarps + kCopyWarps + 2);
         mbar_init(&sh.drained, 2);
@@ -956,10 +1008,12 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
             ok = copy_tiles<T, DP, ES>(a, sh, q_smem, ring, held, threadIdx.x - 32 * kSoftWarps, bad);
             copies_wait(0);
         } else if (warp < kWalkWarp) {
-            ok = multiply<T, DP, ES>(a, sh, q_smem, ring, tmem, warp - kMmaWarp);
-            if (elected()) mma_commit(&sh.drained);  // no instruction outlives its operands
+            if (elected()) {
+                ok = multiply<T, DP, ES>(a, sh, q_smem, ring, tmem, warp - kMmaWarp);
+                mma_commit(&sh.drained);  // no instruction outlives its operands
+                if (!mbar_wait(&sh.drained, 0)) ok = false;
+            }
             __syncwarp();
-            if (!warp_wait(&sh.drained, 0)) ok = false;
         }
     }
     if (!ok) bad |= KVX_S_TIMEOUT;
