@@ -21,7 +21,6 @@ namespace {
 
 constexpr uint32_t kMaxGroup = 128;
 constexpr uint32_t kJoinWarps = 4;
-constexpr uint32_t kJoinParts = 128;  // whose weights a block holds
 constexpr int kJoinUnroll = 4;        // parts whose loads a warp has in flight
 
 // The parts of a query's results over one set of keys: `subs` rows for each block
@@ -34,13 +33,19 @@ struct Parts {
     }
 };
 
-// A block for each query.
-template <class T>
+// A query's parts by WARPS warps, blocks of kJoinWarps.  Bound by the chain of its
+// reads (group, lengths, which blocks, bases and sums, outputs), so few waves of
+// many warps: one warp a query takes 8192 queries of 7 parts in .. us, four in ..;
+// one query of 300 parts in .. and ...
+template <class T, uint32_t WARPS>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant__ Args a) {
-    __shared__ float sh_m[kJoinWarps], sh_l[kJoinWarps], sh_w[kJoinParts];
-    __shared__ float4 sh_o[kJoinWarps][64];
-    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32;
-    const uint32_t n = blockIdx.x / a.q_heads, x = blockIdx.x - n * a.q_heads, head = x / a.group, in = x - head * a.group;
+    __shared__ float sh_m[WARPS > 1 ? kJoinWarps : 1], sh_l[WARPS > 1 ? kJoinWarps : 1];
+    __shared__ float4 sh_o[WARPS > 1 ? kJoinWarps : 1][WARPS > 1 ? 64 : 1];
+    const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32, turn = warp % WARPS;
+    const uint64_t query = (uint64_t)blockIdx.x * (kJoinWarps / WARPS) + warp / WARPS;
+    const bool has = query < (uint64_t)a.num_seqs * a.q_heads;
+    const uint32_t n = has ? (uint32_t)(query / a.q_heads) : 0, x = has ? (uint32_t)(query - (uint64_t)n * a.q_heads) : 0;
+    const uint32_t head = a.by_group.div(x), in = x - head * a.group;
     // the group: the last that starts at n or before
     uint32_t lo = 0, hi = a.num_groups;
     while (lo < hi) {
@@ -71,51 +76,49 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
         parts[1] = Parts{a.own_first_row + u * a.own_cap + in, a.own_cap, a.own_off_b, wide ? 1u : 2u, 0};
     }
     asm volatile("griddepcontrol.wait;" ::: "memory");
+    uint2 w[2] = {make_uint2(1, 0), make_uint2(1, 0)};
+    for (int k = 0; k < 2; k++)
+        if (where[k]) w[k] = __ldcg(where[k]);
     for (int k = 0; k < 2; k++) {
-        if (!where[k]) continue;
-        const uint2 w = __ldcg(where[k]);
-        if (w.x > w.y || w.y >= a.grid) continue;  // left by a block whose wait ran out
-        parts[k].blocks = w.y - w.x + 1;
-        parts[k].row += w.x * parts[k].cap;
+        if (w[k].x > w[k].y || w[k].y >= a.grid) continue;  // none, or left by a block whose wait ran out
+        parts[k].blocks = w[k].y - w[k].x + 1;
+        parts[k].row += w[k].x * parts[k].cap;
     }
     const uint32_t first = parts[0].count(), all = first + parts[1].count();
     auto at = [&](uint32_t i) { return i < first ? parts[0].at(i) : parts[1].at(i - first); };
+    // A warp's share, 32 parts at a time: a lane has one's base and sum; 0 stands
+    // for none, whose outputs do not exist.
     float top = -INFINITY, sum = 0;
     float4 o[2] = {};
-    for (uint32_t i0 = 0; i0 < all; i0 += kJoinParts) {
-        // the parts' bases and sums; 0 stands for none, whose outputs do not exist
-        const uint32_t here = all - i0 < kJoinParts ? all - i0 : kJoinParts;
+    for (uint32_t i0 = turn * 32; i0 < all; i0 += 32 * WARPS) {
+        const uint32_t here = all - i0 < 32 ? all - i0 : 32;
         float2 ml = make_float2(-INFINITY, 0);
-        if (threadIdx.x < here) ml = __ldcg(a.part_ml + at(i0 + threadIdx.x));
+        uint32_t row = 0;  // (rows are below 2^32)
+        if (lane < here) {
+            row = (uint32_t)at(i0 + lane);
+            ml = __ldcg(a.part_ml + row);
+        }
         if (ml.y == 0) ml.x = -INFINITY;
         float higher = ml.x;
         for (int d = 16; d; d >>= 1) higher = fmaxf(higher, __shfl_xor_sync(0xFFFFFFFFu, higher, d));
-        if (lane == 0) sh_m[warp] = higher;
-        __syncthreads();
-        higher = top;
-        for (uint32_t w = 0; w < kJoinWarps; w++) higher = fmaxf(higher, sh_m[w]);
+        higher = fmaxf(higher, top);
         const float old = top == -INFINITY ? 0.0f : exp2_fast(top - higher);
         // (an infinite base comes with a NaN sum, which stays one)
         const float weight = ml.y == 0 ? 0.0f : exp2_fast(ml.x - higher);
         top = higher;
-        sh_w[threadIdx.x] = weight;
         float s = ml.y == 0 ? 0.0f : ml.y * weight;
         for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
-        if (lane == 0) sh_l[warp] = s;
-        __syncthreads();
-        sum *= old;
-        for (uint32_t w = 0; w < kJoinWarps; w++) sum += sh_l[w];
+        sum = sum * old + s;
 #pragma unroll
         for (int k = 0; k < 2; k++) o[k].x *= old, o[k].y *= old, o[k].z *= old, o[k].w *= old;
-        for (uint32_t i = warp; i < here; i += kJoinWarps * kJoinUnroll) {
+        for (uint32_t i = 0; i < here; i += kJoinUnroll) {
             float4 v[kJoinUnroll][2] = {};
-            float w[kJoinUnroll];
+            float f[kJoinUnroll];
 #pragma unroll
             for (int u = 0; u < kJoinUnroll; u++) {
-                const uint32_t j = i + u * kJoinWarps;
-                w[u] = j < here ? sh_w[j] : 0.0f;
-                if (w[u] == 0) continue;  // (a NaN is none)
-                const float *from = a.part_o + at(i0 + j) * a.c.dim;
+                f[u] = __shfl_sync(0xFFFFFFFFu, weight, i + u);  // 0 behind the last
+                const float *from = a.part_o + (uint64_t)__shfl_sync(0xFFFFFFFFu, row, i + u) * a.c.dim;
+                if (f[u] == 0) continue;  // (a NaN is none)
 #pragma unroll
                 for (int k = 0; k < 2; k++)
                     if (k * 128 + lane * 4 < a.c.dim) v[u][k] = __ldcg(reinterpret_cast<const float4 *>(from + k * 128) + lane);
@@ -124,28 +127,43 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
             for (int u = 0; u < kJoinUnroll; u++)
 #pragma unroll
                 for (int k = 0; k < 2; k++) {
-                    o[k].x += v[u][k].x * w[u], o[k].y += v[u][k].y * w[u];
-                    o[k].z += v[u][k].z * w[u], o[k].w += v[u][k].w * w[u];
+                    o[k].x += v[u][k].x * f[u], o[k].y += v[u][k].y * f[u];
+                    o[k].z += v[u][k].z * f[u], o[k].w += v[u][k].w * f[u];
                 }
         }
-        __syncthreads();
     }
+    if constexpr (WARPS > 1) {
+        if (lane == 0) sh_m[warp] = top, sh_l[warp] = sum;
 #pragma unroll
-    for (int k = 0; k < 2; k++) sh_o[warp][k * 32 + lane] = o[k];
-    __syncthreads();
-    const uint32_t d = threadIdx.x * 4;
-    if (d < a.c.dim) {
-        float4 v = sh_o[0][threadIdx.x];
-        for (uint32_t w = 1; w < kJoinWarps; w++) {
-            const float4 y = sh_o[w][threadIdx.x];
-            v.x += y.x, v.y += y.y, v.z += y.z, v.w += y.w;
+        for (int k = 0; k < 2; k++) sh_o[warp][k * 32 + lane] = o[k];
+        __syncthreads();
+        if (turn) return;
+        top = -INFINITY, sum = 0;
+        for (uint32_t k = 0; k < WARPS; k++) top = fmaxf(top, sh_m[warp + k]);
+#pragma unroll
+        for (int h = 0; h < 2; h++) o[h] = make_float4(0, 0, 0, 0);
+        for (uint32_t k = 0; k < WARPS; k++) {
+            const float f = sh_m[warp + k] == -INFINITY ? 0.0f : exp2_fast(sh_m[warp + k] - top);
+            if (f == 0) continue;
+            sum += sh_l[warp + k] * f;
+#pragma unroll
+            for (int h = 0; h < 2; h++) {
+                const float4 v = sh_o[warp + k][h * 32 + lane];
+                o[h].x += v.x * f, o[h].y += v.y * f, o[h].z += v.z * f, o[h].w += v.w * f;
+            }
         }
-        const float inv = sum == 0 ? 0.0f : a.c.v_scale / sum;
-        T *to = static_cast<T *>(a.out) + (uint64_t)n * a.out_stride + (uint64_t)x * a.c.dim + d;
-        *reinterpret_cast<uint2 *>(to) = make_uint2(Pair<T>::pack(v.x * inv, v.y * inv), Pair<T>::pack(v.z * inv, v.w * inv));
     }
-    if (a.lse && threadIdx.x == 0)
-        a.lse[blockIdx.x] = sum == 0 ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+    if (!has) return;
+    const float inv = sum == 0 ? 0.0f : a.c.v_scale / sum;
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const uint32_t d = k * 128 + lane * 4;
+        if (d >= a.c.dim) continue;
+        T *to = static_cast<T *>(a.out) + (uint64_t)n * a.out_stride + (uint64_t)x * a.c.dim + d;
+        *reinterpret_cast<uint2 *>(to) =
+            make_uint2(Pair<T>::pack(o[k].x * inv, o[k].y * inv), Pair<T>::pack(o[k].z * inv, o[k].w * inv));
+    }
+    if (a.lse && lane == 0) a.lse[query] = sum == 0 ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
 }
 
 // Sizes of the call, known on the host: the lengths are not, so every bound is the tables'.
@@ -235,6 +253,7 @@ extern "C" kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q, u
     a.by_group = FastDiv(a.group);
     a.scale2 = fabsf(scale) * cache->k_scale * 1.4426950408889634f;
     a.negate = scale < 0;
+    a.paged16 = cache->page_tokens % 16 == 0;
     a.out = out, a.out_stride = out_stride, a.lse = lse, a.status = status;
     a.tile_rows = p.tile_rows;
     a.prefix_cap = p.prefix_cap, a.prefix_off_b = p.prefix_off_b;
@@ -248,7 +267,10 @@ extern "C" kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q, u
     if (!ok) return KVX_ECUDA;
     KVX_LAUNCHED();
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_seqs * q_heads);
+    // four warps a query where that many fit on the device together
+    const uint64_t queries = (uint64_t)num_seqs * q_heads;
+    const bool four = queries <= 4ull * sm_count();
+    cfg.gridDim = dim3((uint32_t)ceil_div(queries, four ? 1 : kJoinWarps));
     cfg.blockDim = dim3(32 * kJoinWarps);
     cfg.stream = s;
     cudaLaunchAttribute attr[1];
@@ -256,7 +278,8 @@ extern "C" kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q, u
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = dtype == KVX_BF16 ? cudaLaunchKernelEx(&cfg, k_join<__nv_bfloat16>, a) : cudaLaunchKernelEx(&cfg, k_join<__half>, a);
+    const cudaError_t e = dtype == KVX_BF16 ? cudaLaunchKernelEx(&cfg, four ? k_join<__nv_bfloat16, 4> : k_join<__nv_bfloat16, 1>, a)
+                                            : cudaLaunchKernelEx(&cfg, four ? k_join<__half, 4> : k_join<__half, 1>, a);
     if (e != cudaSuccess) return KVX_ECUDA;
     KVX_LAUNCHED();
     return KVX_OK;

@@ -11,14 +11,13 @@ namespace kvx {
 namespace shared {
 
 // Warps of a block: 0-3 and 4-7 take softmaxes, each thread one row of a slot;
-// 8-15 copy; one for each slot issues the tensor cores' instructions; one walks the schedule.
-constexpr int kSoftWarps = 8, kCopyWarps = 8, kMmaWarp = 16, kWalkWarp = 18, kWarps = 20;
+// 8-15 copy; one for each slot issues the tensor cores' instructions; one walks the
+// schedule; one looks up pages of whole groups of 16 tokens (of others each
+// copying warp looks up its own).
+constexpr int kSoftWarps = 8, kCopyWarps = 8, kMmaWarp = 16, kWalkWarp = 18, kLookWarp = 19, kWarps = 20;
 constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kCopyThreads = 32 * kCopyWarps;
-// Descriptors that the walking warp may be ahead: more than the tiles that the
-// copying warps hold back (Shape::kPending, two to a piece of one tile) and look
-// up ahead reach back.
-constexpr int kPieces = 16;
+constexpr int kPieces = 8;  // descriptors that the walking warp may be ahead
 constexpr uint32_t kRound = 64;  // keys that a slot's softmax takes at a time
 constexpr uint32_t kRows = 128;  // of a slot: the tensor cores' M, a query row for each lane of tensor memory
 constexpr uint32_t kExtra = 1;   // tiles that a unit's own overhead counts as
@@ -34,6 +33,7 @@ struct Args {
     FastDiv by_group;
     float scale2;     // |scale| * k_scale * log2(e)
     uint32_t negate;  // scale < 0
+    uint32_t paged16;  // pages are whole groups of 16 tokens
     void *out;
     uint64_t out_stride;
     float *lse;
@@ -99,20 +99,33 @@ struct Shape {
     static constexpr uint32_t kQBufs = DP == 256 ? 1 : 2;
     static constexpr uint32_t kStages = ES == 2 ? (DP == 64 ? 11 : 5) : (DP == 64 ? 6 : 3);
     static constexpr uint32_t kHeld = ES == 2 ? 0 : DP == 64 ? 8 : 4;  // 8-bit tiles on their way
-    static constexpr uint32_t kSmem = 1024 + kQ * kQBufs + kStages * kStage + kHeld * (kStage / 2);
+    static constexpr uint32_t kTiles = kQ * kQBufs + kStages * kStage + kHeld * (kStage / 2);
+    static constexpr uint32_t kGroups = kKeys / 16;        // of 16 tokens in a tile
+    static constexpr uint32_t kFound = 64 / (2 * kGroups);  // tiles whose look-ups may be ahead
 };
 
-struct Shared {  // behind the tiles
+// 16 tokens' rows of keys or values: where the first is, and its scale from there.
+struct alignas(16) Group {
+    uint64_t row;
+    uint32_t scale, count;  // rows that exist
+};
+
+struct alignas(16) Shared {  // behind the tiles
     uint64_t kv_full[11], kv_empty[11];
     uint64_t q_empty[2];
     uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // by slot and round & 1
     uint64_t o_free[2];
     uint64_t pc_full[kPieces], pc_empty[kPieces];
+    uint64_t found[8], taken[8];
     uint64_t drained;
     Piece pieces[kPieces];
+    Group groups[64];        // [tile][group][keys, values]
     uint32_t sums[kWarps];
     uint32_t tmem;
 };
+constexpr uint32_t kTileScales = kCopyWarps * 16;  // bytes of an 8-bit tile on its way, behind Shared: [warp][row]
+template <int DP, int ES>
+constexpr uint32_t kSmem = Shape<DP, ES>::kTiles + sizeof(Shared) + Shape<DP, ES>::kHeld * kTileScales;
 
 // ------------------------------------------------------------- instructions
 
@@ -371,8 +384,6 @@ struct Widen<__nv_bfloat16> {
     uint32_t e, factor;
     __device__ __forceinline__ explicit Widen(uint32_t exponent) : e(exponent), factor((exponent + 120) * 0x00800080u) {}
     __device__ __forceinline__ bool simple() const { return e - 1 <= 133; }
-    // Another lane's.
-    __device__ __forceinline__ Widen of(uint32_t from) const { return Widen(__shfl_sync(0xFFFFFFFFu, e, from)); }
     __device__ __forceinline__ static uint32_t check(const uint4 &v) {  // bits 7, 15, ...: there is a NaN
         auto nan = [](uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; };
         return nan(v.x) | nan(v.y) | nan(v.z) | nan(v.w);
@@ -405,7 +416,6 @@ struct Widen<__half> {
         a = (uint32_t)(ka + 15) * 0x04000400u;
     }
     __device__ __forceinline__ bool simple() const { return e - 115 <= 27; }
-    __device__ __forceinline__ Widen of(uint32_t from) const { return Widen(__shfl_sync(0xFFFFFFFFu, e, from)); }
     __device__ __forceinline__ static uint32_t check(const uint4 &) { return 0; }  // a NaN stays one
     __device__ __forceinline__ static uint32_t times(uint32_t x, uint32_t y) {
         const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
@@ -451,39 +461,40 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     auto place_of = [&](uint32_t c) { return place[c % kPeriod] + c / kPeriod * 1024; };
     const uint64_t room = a.c.pool_bytes - a.c.span;
     const bool fits = a.c.pool_bytes >= a.c.span, row_scales = ES == 1 && a.c.scale_offset;
+    uint8_t *scales = reinterpret_cast<uint8_t *>(&sh + 1);
+    const uint32_t first_scale = a.paged16 ? warp * kWarpKeys % 16 : 0;
 
     // 16-bit tiles are copied to where the tensor cores take them, and count as
     // there when the copies arrive.  8-bit ones come to a place of the thread's own
     // first and are handed over as 16-bit ones.
     uint32_t issued = 0, done = 0;
-    uint64_t scales = 0;  // a byte for each of the last eight tiles: this lane's row's
     auto hand_over = [&]() -> bool {
         const uint32_t t = done, stage = t % S::kStages;
         if (t >= S::kStages && !warp_wait(&sh.kv_empty[stage], (t / S::kStages & 1) ^ 1)) return false;
         if constexpr (ES == 1) {
             const uint4 *from = reinterpret_cast<const uint4 *>(held + t % S::kHeld * (S::kStage / 2)) + thread;
             uint8_t *to = ring + stage * S::kStage;
-            const Widen<T> own((uint32_t)(scales >> (t % 8 * 8)) & 0xFF);
-            bool odd = !__all_sync(0xFFFFFFFFu, own.simple());
-            uint32_t check = 0;
+            const uint8_t *exponents = scales + t % S::kHeld * kTileScales + warp * 16;
+            __syncwarp();  // each lane has waited for its copies
+            uint32_t odd = 0, check = 0;
 #pragma unroll
             for (uint32_t c = 0; c < kCopies; c++) {
                 const uint4 raw = from[c * kCopyThreads];
-                const Widen<T> w = own.of(c * kAtOnce + row0);
+                const Widen<T> w(row_scales ? exponents[first_scale + c * kAtOnce + row0] : 127);
                 check |= Widen<T>::check(raw);
+                odd |= !w.simple();
                 const uint2 x0 = w.four(raw.x), x1 = w.four(raw.y), x2 = w.four(raw.z), x3 = w.four(raw.w);
                 const uint32_t at = place_of(c);
                 *reinterpret_cast<uint4 *>(to + at) = make_uint4(x0.x, x0.y, x1.x, x1.y);
                 *reinterpret_cast<uint4 *>(to + (at ^ 16)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
             }
-            odd |= __any_sync(0xFFFFFFFFu, check & 0x80808080u);
-            if (odd) {
+            if (odd | (check & 0x80808080u)) {
 #pragma unroll 1
                 for (uint32_t c = 0; c < kCopies; c++) {
                     const uint4 raw = from[c * kCopyThreads];
-                    const Widen<T> w = own.of(c * kAtOnce + row0);
-                    const uint2 x0 = w.any(raw.x), x1 = w.any(raw.y), x2 = w.any(raw.z), x3 = w.any(raw.w);
                     const uint32_t r = c * kAtOnce + row0, p0 = 2 * part;
+                    const Widen<T> w(row_scales ? exponents[first_scale + r] : 127);
+                    const uint2 x0 = w.any(raw.x), x1 = w.any(raw.y), x2 = w.any(raw.z), x3 = w.any(raw.w);
                     const uint32_t at = p0 / 8 * (S::kKeys * 128) + (warp * kWarpKeys + r) * 128 + ((p0 % 8 ^ (r & 7)) * 16);
                     *reinterpret_cast<uint4 *>(to + at) = make_uint4(x0.x, x0.y, x1.x, x1.y);
                     *reinterpret_cast<uint4 *>(to + (at ^ 16)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
@@ -504,6 +515,123 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
             if (!hand_over()) return false;
         return true;
     };
+    // Room for the next tile.
+    auto make_room = [&]() -> bool {
+        if constexpr (ES == 2) {
+            const uint32_t stage = issued % S::kStages;
+            return issued < S::kStages || warp_wait(&sh.kv_empty[stage], (issued / S::kStages & 1) ^ 1);
+        } else {
+            if (issued - done < S::kHeld) return true;
+            copies_wait(S::kHeld - 1);
+            return hand_over();
+        }
+    };
+    auto set_scale = [&](uint32_t t, uint32_t exponent) {
+        if (row_scales && lane < kWarpKeys) scales[t % (S::kHeld ? S::kHeld : 1) * kTileScales + warp * 16 + lane] = (uint8_t)exponent;
+    };
+    auto issue = [&](uint64_t row) {  // this lane's row; odd: there is none
+        const uint32_t t = issued;
+        uint8_t *to = ES == 2 ? ring + t % S::kStages * S::kStage : held + t % (S::kHeld ? S::kHeld : 1) * (S::kStage / 2) + thread * 16;
+        const uint32_t base = smem_u32(to);
+        const uint32_t rows = __ballot_sync(0xFFFFFFFFu, !(row & 1)) >> row0;
+        const uint64_t shift = (uint64_t)part * 16;
+        if (__all_sync(0xFFFFFFFFu, !(row & 1))) {
+#pragma unroll
+            for (uint32_t c = 0; c < kCopies; c++) {
+                const uint64_t from = __shfl_sync(0xFFFFFFFFu, row, c * kAtOnce + row0) + shift;
+                if (in) copy16(base + (ES == 2 ? place_of(c) : c * (kCopyThreads * 16)), reinterpret_cast<const void *>(from), true);
+            }
+        } else {
+#pragma unroll 1
+            for (uint32_t c = 0; c < kCopies; c++) {
+                const uint64_t from = (__shfl_sync(0xFFFFFFFFu, row, c * kAtOnce + row0) & ~1ull) + shift;
+                const uint32_t r = c * kAtOnce + row0;
+                const uint32_t at = part / 8 * (S::kKeys * 128) + (warp * kWarpKeys + r) * 128 + ((part % 8 ^ (r & 7)) * 16);
+                if (in) copy16(base + (ES == 2 ? at : c * (kCopyThreads * 16)), reinterpret_cast<const void *>(from), rows >> (c * kAtOnce) & 1);
+            }
+        }
+        if (ES == 2)
+            mbar_arrive_copies(&sh.kv_full[t % S::kStages]);
+        else
+            copies_commit();
+        issued++;
+    };
+    uint32_t q_used[2] = {};
+    auto issue_q = [&](uint32_t b, uint32_t piece) -> bool {  // rows of a piece into buffer b
+        const Piece p = sh.pieces[piece % kPieces];
+        const uint32_t r0 = DP != 256 && p.both ? b * kRows : 0;
+        const uint32_t rows = p.rows - r0 < kRows ? p.rows - r0 : kRows;
+        const uint32_t parity = (q_used[b] & 1) ^ 1;
+        if (q_used[b] && !warp_test(&sh.q_empty[b], parity) && !(drain() && warp_wait(&sh.q_empty[b], parity))) return false;
+        q_used[b]++;
+        constexpr uint32_t kQParts = DP / 8;
+        const uint32_t base = smem_u32(q_smem + b * S::kQ), q_parts = a.c.dim / 8;
+        for (uint32_t j = thread; j < rows * kQParts; j += kCopyThreads) {
+            const uint32_t r = j / kQParts, part = j % kQParts;
+            const uint32_t rr = p.row0 + r0 + r, s = a.by_group.div(rr);
+            const uint64_t from = (uint64_t)(p.seq0 + s) * a.q_stride + (uint64_t)(p.head * a.group + rr - s * a.group) * a.c.dim;
+            if (part < q_parts)
+                copy16(base + (part / 8) * (kRows * 128) + r * 128 + ((part % 8 ^ (r & 7)) * 16),
+                       static_cast<const T *>(a.q) + from + part * 8, true);
+        }
+        return true;
+    };
+
+    if (a.paged16) {
+        constexpr uint32_t kOff = 16 % kWarpKeys;  // (0: a warp's rows are one group's, or half of one's)
+        static_assert(kOff == 0);
+        const uint32_t group = warp * kWarpKeys / 16, off = warp * kWarpKeys % 16;
+        const uint64_t stride = a.c.token_stride, shift = (off + row0) * stride + part * 16;
+        auto issue_group = [&](const Group &g) {
+            const uint32_t t = issued;
+            uint8_t *to = ES == 2 ? ring + t % S::kStages * S::kStage : held + t % (S::kHeld ? S::kHeld : 1) * (S::kStage / 2) + thread * 16;
+            const uint32_t base = smem_u32(to);
+            const uint8_t *from = reinterpret_cast<const uint8_t *>(g.row + shift);
+            if (g.count == 16) {
+#pragma unroll
+                for (uint32_t c = 0; c < kCopies; c++, from += kAtOnce * stride)
+                    if (in) copy16(base + (ES == 2 ? place_of(c) : c * (kCopyThreads * 16)), from, true);
+            } else {
+#pragma unroll
+                for (uint32_t c = 0; c < kCopies; c++, from += kAtOnce * stride) {
+                    const bool there = off + row0 + c * kAtOnce < g.count;
+                    if (in) copy16(base + (ES == 2 ? place_of(c) : c * (kCopyThreads * 16)), there ? from : a.c.pool, there);
+                }
+            }
+            if (row_scales && lane == 0)  // 16 bytes, wherever a warp's rows begin among them
+                copy16(smem_u32(scales + t % (S::kHeld ? S::kHeld : 1) * kTileScales + warp * 16), reinterpret_cast<const uint8_t *>(g.row + g.scale), g.count > 0);
+            if (ES == 2)
+                mbar_arrive_copies(&sh.kv_full[t % S::kStages]);
+            else
+                copies_commit();
+            issued++;
+        };
+        uint32_t tile = 0;
+        for (uint32_t np = 0;; np++) {
+            uint64_t *bar = &sh.pc_full[np % kPieces];
+            if (!warp_test(bar, np / kPieces & 1) && !(drain() && warp_wait(bar, np / kPieces & 1))) return false;
+            const Piece &p = sh.pieces[np % kPieces];
+            if (!p.rows) return drain();
+            const uint32_t nt = (p.k1 - p.k0 + S::kKeys - 1) / S::kKeys, both = p.both;
+            for (uint32_t b = 0; b < S::kQBufs; b++)
+                if ((DP == 256 || both || b == (np & 1)) && !issue_q(b, np)) return false;
+            for (uint32_t t = 0; t < nt; t++, tile++) {
+                const uint32_t slot = tile % S::kFound, parity = tile / S::kFound & 1;
+                if (!warp_test(&sh.found[slot], parity) && !(drain() && warp_wait(&sh.found[slot], parity))) return false;
+                const Group *g = sh.groups + (slot * S::kGroups + group) * 2;
+                const Group keys = g[0], values = g[1];
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.taken[slot]);
+                if (!make_room()) return false;
+                issue_group(keys);
+                if (!make_room()) return false;
+                issue_group(values);
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.pc_empty[np % kPieces]);
+        }
+    }
+
     // A tile on its way through the look-up: its block ids, then its segments'
     // addresses, then its rows' scales are loaded, each while the tile before
     // is a step further.
@@ -553,68 +681,6 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
             const uint64_t *entry = a.c.lane_addr(id, l.head, 0);
             seg[0] = __ldg(entry), seg[1] = __ldg(entry + 1);
         }
-    };
-
-    // Room for the next tile.
-    auto make_room = [&]() -> bool {
-        if constexpr (ES == 2) {
-            const uint32_t stage = issued % S::kStages;
-            return issued < S::kStages || warp_wait(&sh.kv_empty[stage], (issued / S::kStages & 1) ^ 1);
-        } else {
-            if (issued - done < S::kHeld) return true;
-            copies_wait(S::kHeld - 1);
-            return hand_over();
-        }
-    };
-    auto set_scale = [&](uint32_t t, uint32_t exponent) {
-        if (ES == 1) scales = (scales & ~(0xFFull << (t % 8 * 8))) | (uint64_t)exponent << (t % 8 * 8);
-    };
-    auto issue = [&](uint64_t row) {  // this lane's row; odd: there is none
-        const uint32_t t = issued;
-        uint8_t *to = ES == 2 ? ring + t % S::kStages * S::kStage : held + t % (S::kHeld ? S::kHeld : 1) * (S::kStage / 2) + thread * 16;
-        const uint32_t base = smem_u32(to);
-        const uint32_t rows = __ballot_sync(0xFFFFFFFFu, !(row & 1)) >> row0;
-        const uint64_t shift = (uint64_t)part * 16;
-        if (__all_sync(0xFFFFFFFFu, !(row & 1))) {
-#pragma unroll
-            for (uint32_t c = 0; c < kCopies; c++) {
-                const uint64_t from = __shfl_sync(0xFFFFFFFFu, row, c * kAtOnce + row0) + shift;
-                if (in) copy16(base + (ES == 2 ? place_of(c) : c * (kCopyThreads * 16)), reinterpret_cast<const void *>(from), true);
-            }
-        } else {
-#pragma unroll 1
-            for (uint32_t c = 0; c < kCopies; c++) {
-                const uint64_t from = (__shfl_sync(0xFFFFFFFFu, row, c * kAtOnce + row0) & ~1ull) + shift;
-                const uint32_t r = c * kAtOnce + row0;
-                const uint32_t at = part / 8 * (S::kKeys * 128) + (warp * kWarpKeys + r) * 128 + ((part % 8 ^ (r & 7)) * 16);
-                if (in) copy16(base + (ES == 2 ? at : c * (kCopyThreads * 16)), reinterpret_cast<const void *>(from), rows >> (c * kAtOnce) & 1);
-            }
-        }
-        if (ES == 2)
-            mbar_arrive_copies(&sh.kv_full[t % S::kStages]);
-        else
-            copies_commit();
-        issued++;
-    };
-    uint32_t q_used[2] = {};
-    auto issue_q = [&](uint32_t b, uint32_t piece) -> bool {  // rows of a piece into buffer b
-        const Piece p = sh.pieces[piece % kPieces];
-        const uint32_t r0 = DP != 256 && p.both ? b * kRows : 0;
-        const uint32_t rows = p.rows - r0 < kRows ? p.rows - r0 : kRows;
-        const uint32_t parity = (q_used[b] & 1) ^ 1;
-        if (q_used[b] && !warp_test(&sh.q_empty[b], parity) && !(drain() && warp_wait(&sh.q_empty[b], parity))) return false;
-        q_used[b]++;
-        constexpr uint32_t kQParts = DP / 8;
-        const uint32_t base = smem_u32(q_smem + b * S::kQ), q_parts = a.c.dim / 8;
-        for (uint32_t j = thread; j < rows * kQParts; j += kCopyThreads) {
-            const uint32_t r = j / kQParts, part = j % kQParts;
-            const uint32_t rr = p.row0 + r0 + r, s = a.by_group.div(rr);
-            const uint64_t from = (uint64_t)(p.seq0 + s) * a.q_stride + (uint64_t)(p.head * a.group + rr - s * a.group) * a.c.dim;
-            if (part < q_parts)
-                copy16(base + (part / 8) * (kRows * 128) + r * 128 + ((part % 8 ^ (r & 7)) * 16),
-                       static_cast<const T *>(a.q) + from + part * 8, true);
-        }
-        return true;
     };
 
     // Rows of the tile after a look-up's, with their scales on their way.
@@ -670,6 +736,82 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
         }
     }
     return alive && drain();
+}
+
+// The looking-up warp, for pages of whole groups of 16 tokens: a lane has the keys'
+// or the values' segment of one group; several tiles at a time.  Block ids of a
+// step are loaded while the segment addresses of the step before are.
+template <int DP, int ES>
+__device__ __forceinline__ bool look_up(const Args &a, Shared &sh, uint32_t lane, uint32_t &bad) {
+    using S = Shape<DP, ES>;
+    constexpr uint32_t kLanes = 2 * S::kGroups, kTilesAtOnce = 32 / kLanes;
+    const uint32_t which = lane / kLanes, group = lane % kLanes / 2, kv = lane & 1;
+    const uint64_t room = a.c.pool_bytes - a.c.span;
+    const bool fits = a.c.pool_bytes >= a.c.span;
+    uint32_t np = 0, k = 0, k1 = 0, head = 0;
+    const uint32_t *table = nullptr;
+    bool over = false, alive = true;
+    struct Step {
+        uint32_t tiles, count, token, head;
+    };
+    uint32_t id = 0;
+    uint64_t seg = 0;
+    auto find = [&]() -> Step {
+        Step s = {};
+        if (over || !alive) return s;
+        if (k >= k1) {
+            alive = warp_wait(&sh.pc_full[np % kPieces], np / kPieces & 1);
+            if (!alive) return s;
+            const Piece p = sh.pieces[np % kPieces];
+            __syncwarp();
+            if (!p.rows) {
+                over = true;
+                return s;
+            }
+            if (lane == 0) mbar_arrive(&sh.pc_empty[np % kPieces]);
+            k = p.k0, k1 = p.k1, head = p.head, table = p.table;
+            np++;
+        }
+        const uint32_t left = (k1 - k + S::kKeys - 1) / S::kKeys, pos = k + which * S::kKeys + group * 16;
+        s.tiles = left < kTilesAtOnce ? left : kTilesAtOnce;
+        s.head = head;
+        s.count = pos < k1 ? (k1 - pos < 16 ? k1 - pos : 16) : 0;
+        const uint32_t page = a.c.page.div(s.count ? pos : k);
+        s.token = pos - page * a.c.page.d;
+        id = __ldg(table + page);
+        k += s.tiles * S::kKeys;
+        return s;
+    };
+    auto find_segment = [&](Step &s) {
+        if (s.count && id >= a.c.B) bad |= KVX_S_BOUNDS, s.count = 0;
+        seg = 0;
+        if (s.count) seg = __ldg(a.c.lane_addr(id, s.head, kv));
+    };
+    Step one = find();
+    find_segment(one);
+    Step two = one.tiles ? find() : Step{};
+    uint32_t tile = 0;
+    while (one.tiles && alive) {
+        Group g;
+        const bool good = fits && seg <= room && !((uint32_t)seg & 15);
+        if (one.count && !good) a.c.ok(seg, bad);
+        g.count = good ? one.count : 0;
+        g.row = reinterpret_cast<uint64_t>(a.c.pool) + (g.count ? seg + one.token * a.c.token_stride : 0);
+        g.scale = (uint32_t)(a.c.scale_offset + one.token - one.token * a.c.token_stride);
+        const Step now = one;
+        find_segment(two);
+        one = two;
+        for (uint32_t t = 0; t < now.tiles; t++) {
+            const uint32_t slot = (tile + t) % S::kFound, use = (tile + t) / S::kFound;
+            if (use && !warp_wait(&sh.taken[slot], (use & 1) ^ 1)) return false;
+        }
+        if (which < now.tiles) sh.groups[((tile + which) % S::kFound * S::kGroups + group) * 2 + kv] = g;
+        __syncwarp();
+        if (lane < now.tiles) mbar_arrive(&sh.found[(tile + lane) % S::kFound]);
+        tile += now.tiles;
+        two = one.tiles ? find() : Step{};
+    }
+    return alive;
 }
 
 // --------------------------------------------------------- the tensor cores
@@ -951,10 +1093,9 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
 template <class T, int DP, int ES>
 __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ Args a) {
     using S = Shape<DP, ES>;
-    extern __shared__ __align__(1024) uint8_t smem_raw[];
-    uint8_t *smem = smem_raw + ((1024 - (smem_u32(smem_raw) & 1023)) & 1023);
+    extern __shared__ __align__(1024) uint8_t smem[];  // (without others it starts on a multiple of 1024)
     uint8_t *ring = smem, *q_smem = smem + S::kStages * S::kStage, *held = q_smem + S::kQBufs * S::kQ;
-    __shared__ Shared sh;
+    Shared &sh = *reinterpret_cast<Shared *>(smem + S::kTiles);
     const uint32_t warp = threadIdx.x / 32, lane = threadIdx.x & 31;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -976,7 +1117,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
             for (int k = 0; k < 2; k++) mbar_init(&sh.s_full[i][k], 1), mbar_init(&sh.p_full[i][k], 4), mbar_init(&sh.pv_done[i][k], 1);
             mbar_init(&sh.o_free[i], 4);
         }
-        for (int i = 0; i < kPieces; i++) mbar_init(&sh.pc_full[i], 1), mbar_init(&sh.pc_empty[i], kSoftWarps + kCopyWarps + 2);
+        for (int i = 0; i < kPieces; i++)
+            mbar_init(&sh.pc_full[i], 1), mbar_init(&sh.pc_empty[i], kSoftWarps + kCopyWarps + 2 + (a.paged16 ? 1 : 0));
+        for (int i = 0; i < 8; i++) mbar_init(&sh.found[i], 1), mbar_init(&sh.taken[i], kCopyWarps);
         mbar_init(&sh.drained, 2);
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -1007,7 +1150,9 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
         } else if (warp < kSoftWarps + kCopyWarps) {
             ok = copy_tiles<T, DP, ES>(a, sh, q_smem, ring, held, threadIdx.x - 32 * kSoftWarps, bad);
             copies_wait(0);
-        } else if (warp < kWalkWarp) {
+        } else if (warp == kLookWarp) {
+            if (a.paged16) ok = look_up<DP, ES>(a, sh, lane, bad);
+        } else {
             if (elected()) {
                 ok = multiply<T, DP, ES>(a, sh, q_smem, ring, tmem, warp - kMmaWarp);
                 mma_commit(&sh.drained);  // no instruction outlives its operands
@@ -1034,11 +1179,11 @@ bool launch_kernel(const Args &a, cudaStream_t s) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return false;
     if (dev < 0 || dev >= 64 || !done[dev]) {
-        if (cudaFuncSetAttribute(k_shared<T, DP, ES>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem) != cudaSuccess)
+        if (cudaFuncSetAttribute(k_shared<T, DP, ES>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem<DP, ES>) != cudaSuccess)
             return false;
         if (dev >= 0 && dev < 64) done[dev] = true;
     }
-    k_shared<T, DP, ES><<<a.grid, kThreads, S::kSmem, s>>>(a);
+    k_shared<T, DP, ES><<<a.grid, kThreads, kSmem<DP, ES>, s>>>(a);
     return true;
 }
 
