@@ -23,13 +23,37 @@ constexpr uint32_t kMaxGroup = 128;
 constexpr uint32_t kJoinWarps = 4;
 constexpr int kJoinUnroll = 4;        // parts whose loads a warp has in flight
 
-// The parts of a query's results over one set of keys: `subs` rows for each block
-// first .. first + blocks-1.
+// The parts of a query's results over one set of keys, by number 0 .. count()-1:
+// `subs` rows for each pair of a block of columns and a block of k_shared that
+// works on it, of which there may be fewer than `each`.
 struct Parts {
-    uint32_t row, cap, off_b, subs, blocks;
-    __device__ __forceinline__ uint32_t count() const { return blocks * subs; }
-    __device__ __forceinline__ uint64_t at(uint32_t i) const {
-        return subs == 2 ? row + (uint64_t)(i >> 1) * cap + (i & 1) * off_b : row + (uint64_t)i * cap;
+    Region r;
+    uint32_t row, head, c0, c1;     // the columns c0 .. c1-1 of a row
+    uint32_t start, share;          // of the entry; of a block
+    uint32_t first_row, cap, off_b, subs;
+    uint32_t b0, blocks, each;
+    __device__ __forceinline__ void find() {
+        b0 = c0 / r.block;
+        blocks = (c1 - 1) / r.block - b0 + 1;
+        uint32_t from, to;
+        span(b0, from, to);
+        each = blocks > 1 || r.rows > 1 ? 2 : to / share - from / share + 1;
+    }
+    // First and last place of the columns in a block.
+    __device__ __forceinline__ void span(uint32_t b, uint32_t &from, uint32_t &to) const {
+        const uint32_t n = r.columns(b), begin = b * r.block, at = start + begin * r.rows + row * n;
+        from = at + (c0 > begin ? c0 - begin : 0);
+        to = at + (c1 - begin < n ? c1 - begin : n) - 1;
+    }
+    __device__ __forceinline__ uint32_t count() const { return blocks * each * subs; }
+    // The row of a part, kNone where there is none.
+    __device__ __forceinline__ uint32_t at(uint32_t i) const {
+        const uint32_t sub = subs == 2 ? i & 1 : 0, k = subs == 2 ? i >> 1 : i, b = k / each;
+        uint32_t from, to;
+        span(b0 + b, from, to);
+        const uint32_t c = from / share + (k - b * each);
+        if (c > to / share) return kNone;
+        return first_row + (r.rank(b0 + b, row, head) + c) * cap + sub * off_b;
     }
 };
 
@@ -56,36 +80,53 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
             hi = mid;
     }
     const bool wide = a.c.dim > 128;
+    const uint32_t keys = wide ? 64 : 128;
     Parts parts[2] = {};
     uint2 const *where[2] = {};
+    Entry entry[2] = {};
     if (lo) {
         const Entry e = entry_of(a, lo - 1);
         if (e.len && n - e.seq0 < e.rows / a.group) {
-            const uint32_t row = (n - e.seq0) * a.group + in, mt = row / a.tile_rows;
-            const uint32_t rows = e.rows - mt * a.tile_rows;
-            const uint32_t u = (prefix_tile(a, e.seq0, lo - 1) + mt) * a.c.heads + head;
-            where[0] = a.prefix_parts + u;
-            parts[0] = Parts{u * a.prefix_cap + row - mt * a.tile_rows, a.prefix_cap, a.prefix_off_b,
-                             wide || rows > kRows ? 1u : 2u, 0};
+            entry[0] = e;
+            where[0] = a.group_at + lo - 1;
         }
     }
-    const Entry own = entry_of(a, a.num_groups + n);
-    if (own.len) {
-        const uint32_t u = n * a.c.heads + head;
-        where[1] = a.own_parts + u;
-        parts[1] = Parts{a.own_first_row + u * a.own_cap + in, a.own_cap, a.own_off_b, wide ? 1u : 2u, 0};
-    }
+    entry[1] = entry_of(a, a.num_groups + n);
+    if (entry[1].len) where[1] = a.own_parts + (uint64_t)n * a.c.heads + head;
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    uint2 w[2] = {make_uint2(1, 0), make_uint2(1, 0)};
+    uint2 w[2] = {};
     for (int k = 0; k < 2; k++)
         if (where[k]) w[k] = __ldcg(where[k]);
-    for (int k = 0; k < 2; k++) {
-        if (w[k].x > w[k].y || w[k].y >= a.grid) continue;  // none, or left by a block whose wait ran out
-        parts[k].blocks = w[k].y - w[k].x + 1;
-        parts[k].row += w[k].x * parts[k].cap;
+    if (where[0] && w[0].y) {
+        const Entry &e = entry[0];
+        Parts &p = parts[0];
+        p.start = w[0].x, p.share = w[0].y;
+        p.r = region_of(a, e, p.share, keys);
+        const uint32_t query_row = (n - e.seq0) * a.group + in;
+        p.row = query_row / a.tile_rows, p.head = head;
+        p.c0 = head * p.r.len + kExtra, p.c1 = (head + 1) * p.r.len;
+        const uint32_t at = query_row - p.row * a.tile_rows, rows = e.rows - p.row * a.tile_rows;
+        p.first_row = group_parts(a, p.start, p.share, e.seq0, lo - 1) * a.prefix_cap + at;
+        p.cap = a.prefix_cap, p.off_b = a.prefix_off_b;
+        p.subs = wide || rows > kRows ? 1 : 2;
+        p.find();
+    }
+    if (where[1] && w[1].x <= w[1].y && w[1].y < a.grid) {  // (else left by a block whose wait ran out)
+        Parts &p = parts[1];  // one column a block
+        p.r.len = p.r.rows = p.r.block = 1, p.r.width = w[1].y + 1;
+        p.share = 1, p.c0 = w[1].x, p.c1 = w[1].y + 1;
+        p.first_row = a.own_first_row + (n * a.c.heads + head) * a.own_cap + in;
+        p.cap = a.own_cap, p.off_b = a.own_off_b, p.subs = wide ? 1 : 2;
+        p.b0 = w[1].x, p.blocks = w[1].y - w[1].x + 1, p.each = 1;
     }
     const uint32_t first = parts[0].count(), all = first + parts[1].count();
-    auto at = [&](uint32_t i) { return i < first ? parts[0].at(i) : parts[1].at(i - first); };
+    const uint32_t most = (uint32_t)(a.rows < kNone ? a.rows : kNone);
+    auto at = [&](uint32_t i) {
+        const uint32_t row = i < first ? parts[0].at(i)
+                                       : parts[1].first_row + (parts[1].c0 + (i - first) / parts[1].subs) * parts[1].cap +
+                                             (i - first) % parts[1].subs * parts[1].off_b;
+        return row < most ? row : kNone;  // (a group that a block left in disorder)
+    };
     // A warp's share, 32 parts at a time: a lane has one's base and sum; 0 stands
     // for none, whose outputs do not exist.
     float top = -INFINITY, sum = 0;
@@ -94,10 +135,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
         const uint32_t here = all - i0 < 32 ? all - i0 : 32;
         float2 ml = make_float2(-INFINITY, 0);
         uint32_t row = 0;  // (rows are below 2^32)
-        if (lane < here) {
-            row = (uint32_t)at(i0 + lane);
-            ml = __ldcg(a.part_ml + row);
-        }
+        if (lane < here) row = at(i0 + lane);
+        if (lane < here && row != kNone) ml = __ldcg(a.part_ml + row);
         if (ml.y == 0) ml.x = -INFINITY;
         float higher = ml.x;
         for (int d = 16; d; d >>= 1) higher = fmaxf(higher, __shfl_xor_sync(0xFFFFFFFFu, higher, d));
@@ -170,7 +209,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
 struct Plan {
     uint32_t max_len, max_prefix, grid;
     uint32_t tile_rows, prefix_cap, prefix_off_b, own_cap, own_off_b;
-    uint64_t prefix_units, own_units, own_first_row, rows;
+    uint64_t own_units, own_first_row, rows;
 };
 
 bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t blocks_per_seq, uint32_t num_groups,
@@ -191,23 +230,22 @@ bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t bloc
     p.own_off_b = wide ? 0 : group;
     p.own_cap = wide ? group : 2 * group;
     const uint64_t tiles = num_groups ? queries / p.tile_rows + num_groups : 0;
-    p.prefix_units = tiles * c->heads;
     p.own_units = (uint64_t)num_seqs * c->heads;
-    const uint64_t most = p.prefix_units * (ceil_div(prefix, keys) + kExtra) + p.own_units * (ceil_div(len, keys) + kExtra);
-    if (tiles >= (1ull << 31) || p.prefix_units >= (1ull << 31) || most >= (1ull << 31)) return false;
+    const uint64_t most = tiles * c->heads * (ceil_div(prefix, keys) + kExtra) + p.own_units * (ceil_div(len, keys) + kExtra);
+    if (tiles * (c->heads + 2) >= (1ull << 31) || most >= (1ull << 31)) return false;
     const uint64_t want = ceil_div(most, kMinShare);
     p.grid = want < (uint64_t)sm_count() ? (want ? (uint32_t)want : 1) : (uint32_t)sm_count();
-    p.own_first_row = num_groups ? (p.prefix_units + p.grid) * p.prefix_cap : 0;
+    p.own_first_row = num_groups ? (tiles * (c->heads + 2) + 2 * p.grid) * p.prefix_cap : 0;
     p.rows = p.own_first_row + (p.own_units + p.grid) * p.own_cap;
     return p.rows < (1ull << 32);
 }
 
-size_t carve(const Plan &p, const kvx_cache *c, void *ws, Args *a) {
+size_t carve(const Plan &p, const kvx_cache *c, uint32_t num_groups, void *ws, Args *a) {
     Carver w(ws);
     float *o = w.take<float>(p.rows * c->dim);
     float2 *ml = w.take<float2>(p.rows);
-    uint2 *prefix = w.take<uint2>(p.prefix_units), *own = w.take<uint2>(p.own_units);
-    if (a) a->part_o = o, a->part_ml = ml, a->prefix_parts = prefix, a->own_parts = own;
+    uint2 *groups = w.take<uint2>(num_groups), *own = w.take<uint2>(p.own_units);
+    if (a) a->part_o = o, a->part_ml = ml, a->group_at = groups, a->own_parts = own, a->rows = p.rows;
     return w.off;
 }
 
@@ -220,7 +258,7 @@ extern "C" size_t kvx_attend_shared_workspace_size(const kvx_cache *cache, uint3
                                                    uint32_t blocks_per_prefix) {
     using namespace kvx::shared;
     Plan p;
-    return plan(cache, num_seqs, q_heads, blocks_per_seq, num_groups, blocks_per_prefix, p) ? carve(p, cache, nullptr, nullptr) : 0;
+    return plan(cache, num_seqs, q_heads, blocks_per_seq, num_groups, blocks_per_prefix, p) ? carve(p, cache, num_groups, nullptr, nullptr) : 0;
 }
 
 extern "C" kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q, uint64_t q_stride, uint32_t dtype,
@@ -240,7 +278,7 @@ extern "C" kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q, u
     if (!num_seqs) return KVX_OK;
     if (!q || !out || !lens || (p.max_len && !blocks)) return KVX_EINVAL;
     if (num_groups && (!prefix_lens || !group_first || (p.max_prefix && !prefix_blocks))) return KVX_EINVAL;
-    if (!ws || !aligned16(ws) || ws_bytes < carve(p, cache, nullptr, nullptr)) return KVX_EINVAL;
+    if (!ws || !aligned16(ws) || ws_bytes < carve(p, cache, num_groups, nullptr, nullptr)) return KVX_EINVAL;
     Args a = {};
     a.c = cache_view(cache);
     a.q = q, a.q_stride = q_stride;
@@ -259,7 +297,7 @@ extern "C" kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q, u
     a.prefix_cap = p.prefix_cap, a.prefix_off_b = p.prefix_off_b;
     a.own_cap = p.own_cap, a.own_off_b = p.own_off_b, a.own_first_row = (uint32_t)p.own_first_row;
     a.grid = p.grid;
-    carve(p, cache, ws, &a);
+    carve(p, cache, num_groups, ws, &a);
     const cudaStream_t s = as_stream(stream);
     const bool ok = dtype == KVX_BF16
                         ? (cache->dtype == KVX_E4M3 ? launch<__nv_bfloat16, 1>(a, s) : launch<__nv_bfloat16, 2>(a, s))

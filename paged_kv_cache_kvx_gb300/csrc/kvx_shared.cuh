@@ -41,19 +41,14 @@ struct Args {
     // workspace
     float *part_o;        // [rows of parts][dim]: unnormalised outputs
     float2 *part_ml;      // [rows of parts]: base (of powers of two) and sum
-    uint2 *prefix_parts;  // [units of prefixes], [num_seqs * heads]: the first and the last block with a part
-    uint2 *own_parts;
+    uint2 *group_at;      // [num_groups]: where a group's columns start, and a block's share
+    uint2 *own_parts;     // [num_seqs * heads]: the first and the last block with a part
     uint32_t tile_rows;                          // query rows of a unit of a prefix
     uint32_t prefix_cap, prefix_off_b;           // rows of a part of a prefix; where those of slot B start
     uint32_t own_cap, own_off_b, own_first_row;  // of a sequence's own tokens; the first such part's first row
     uint32_t grid;
+    uint64_t rows;  // of all parts
 };
-
-// Units.  A prefix's are its group's query rows of a KV head, kTileRows at a
-// time; their numbers grow with the group, the tile and the head, with gaps.
-__host__ __device__ __forceinline__ uint32_t prefix_tile(const Args &a, uint32_t first_seq, uint32_t g) {
-    return (uint32_t)((uint64_t)first_seq * a.group / a.tile_rows) + g;
-}
 
 // What is shared out: a group's prefix, or a sequence's own tokens.
 struct Entry {
@@ -80,6 +75,41 @@ __device__ __forceinline__ Entry entry_of(const Args &a, uint32_t i) {
     if (e.len > most) e.len = most, e.bad |= KVX_S_BOUNDS;
     if (!e.rows) e.len = 0;
     return e;
+}
+
+// How an entry's work is shared out.  It has heads * len columns, a tile of keys in
+// one head each (kExtra at a head's start stand for what a part costs beside its
+// keys), and tile_rows query rows at a time make `rows` rows of them.  Blocks of
+// `block` columns, a share each where there are several rows, are gone through row
+// by row: so the blocks that work on different rows of the same columns do so at
+// the same time, and keys and values come from memory once (100,000 tokens, 8
+// heads, 4 rows: 1.71 GB of DRAM reads with the rows one after the other, 0.4 GB
+// so; .. us and ..).
+struct Region {
+    uint32_t len, width, rows, block;
+    __device__ __forceinline__ uint32_t columns(uint32_t b) const {  // of block b
+        return width - b * block < block ? width - b * block : block;
+    }
+    // Number of the parts of a row's columns of one head in a block, by which parts
+    // are laid out: it grows in the order in which these are gone through.
+    __device__ __forceinline__ uint32_t rank(uint32_t b, uint32_t row, uint32_t head) const {
+        const uint32_t first = b * block / len, last = (b * block + columns(b) - 1) / len;
+        return rows * (b + first) + row * (last - first + 1) + head - first;
+    }
+};
+__device__ __forceinline__ Region region_of(const Args &a, const Entry &e, uint32_t share, uint32_t keys) {
+    Region r;
+    r.len = e.len ? (e.len + keys - 1) / keys + kExtra : 0;
+    r.width = a.c.heads * r.len;
+    r.rows = (e.rows + a.tile_rows - 1) / a.tile_rows;
+    r.block = r.rows > 1 ? share : r.width;
+    return r;
+}
+// The first part of a group's, by number.  Its parts are at most rows * (blocks + heads),
+// and one for each border of a share: blocks * rows is its columns over the share,
+// and tiles of query rows of all groups before it, g for rounding, count the rest.
+__device__ __forceinline__ uint32_t group_parts(const Args &a, uint32_t start, uint32_t share, uint32_t first_seq, uint32_t g) {
+    return start / share + ((uint32_t)((uint64_t)first_seq * a.group / a.tile_rows) + g) * (a.c.heads + 2);
 }
 
 // A part of a unit that one block works on.
@@ -285,8 +315,6 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
     const uint64_t begin64 = (uint64_t)blockIdx.x * share;
     uint32_t at = begin64 < total ? (uint32_t)begin64 : total;
     const uint32_t end = total - at > share ? at + share : total;
-    auto units_of = [&](const Entry &e) { return a.c.heads * ((e.rows + S::kTileRows - 1) / S::kTileRows); };
-    auto unit_len = [&](const Entry &e) { return e.len ? (e.len + S::kKeys - 1) / S::kKeys + kExtra : 0; };
     uint32_t i = 0, off = 0, np = 0, event = 0;
     Entry e = {};
     if (at < end) {
@@ -296,7 +324,8 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
         uint32_t before = t ? cum[t - 1] : 0;
         for (i = t * per;; i++) {
             e = entry_of(a, i);
-            const uint32_t n = unit_len(e) * units_of(e);
+            const Region r = region_of(a, e, share, S::kKeys);
+            const uint32_t n = r.width * r.rows;
             if (at - before < n) break;
             before += n;
         }
@@ -306,48 +335,48 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
     Entry next = {};
     if (at < end && i + 1 < entries) next = entry_of(a, i + 1);
     while (at < end) {
-        const uint32_t len = unit_len(e), units = units_of(e);
-        if (off >= len * units) {
-            off -= len * units;
+        const Region r = region_of(a, e, share, S::kKeys);
+        if (off >= r.width * r.rows) {
+            off -= r.width * r.rows;
             e = next;
             i++;
             next = Entry{};
             if (i + 1 < entries) next = entry_of(a, i + 1);
             continue;
         }
-        const uint32_t unit = quotient(off, len), from = off - unit * len;
-        const uint32_t to = len - from < end - at ? len : from + (end - at);
-        const uint32_t start = at - from;  // the unit's
+        const uint32_t b = quotient(off, r.block * r.rows), in_block = off - b * r.block * r.rows;
+        const uint32_t columns = r.columns(b), mt = quotient(in_block, columns), in_row = in_block - mt * columns;
+        const uint32_t column = b * r.block + in_row, head = quotient(column, r.len), from = column - head * r.len;
+        uint32_t to = from + (columns - in_row);
+        if (to > r.len) to = r.len;
+        if (to - from > end - at) to = from + (end - at);
+        const uint32_t start = at - off;  // the entry's
         at += to - from;
         off += to - from;
-        if (to <= kExtra) continue;  // the overhead's tiles come first
+        if (to <= kExtra) continue;
         const uint32_t t0 = from > kExtra ? from - kExtra : 0, t1 = to - kExtra;
         if (np >= kPieces && !warp_wait(&sh.pc_empty[np % kPieces], (np / kPieces & 1) ^ 1)) return false;
         if (lane == 0) {
             Piece p;
-            const uint32_t mt = unit / a.c.heads, head = unit - mt * a.c.heads;
-            const bool prefix = i < a.num_groups;
             p.seq0 = e.seq0;
-            p.row0 = mt * S::kTileRows;
-            p.rows = e.rows - p.row0 < S::kTileRows ? e.rows - p.row0 : S::kTileRows;
+            p.row0 = mt * a.tile_rows;
+            p.rows = e.rows - p.row0 < a.tile_rows ? e.rows - p.row0 : a.tile_rows;
             p.head = head;
             p.k0 = t0 * S::kKeys;
             p.k1 = t1 * S::kKeys < e.len ? t1 * S::kKeys : e.len;
             p.both = DP == 256 || p.rows > kRows;
             p.event = event;
-            const uint2 parts = make_uint2((start + kExtra) / share, (start + len - 1) / share);
-            if (prefix) {
-                const uint32_t u = (prefix_tile(a, e.seq0, i) + mt) * a.c.heads + head;
+            if (i < a.num_groups) {
                 p.table = a.prefix_blocks + (uint64_t)i * a.blocks_per_prefix;
-                p.part_row = (u + blockIdx.x) * a.prefix_cap;
+                p.part_row = (group_parts(a, start, share, e.seq0, i) + r.rank(b, mt, head) + blockIdx.x) * a.prefix_cap;
                 p.off_b = a.prefix_off_b;
-                if (!t0) a.prefix_parts[u] = parts;
+                a.group_at[i] = make_uint2(start, share);  // the same from all blocks
             } else {
-                const uint32_t u = e.seq0 * a.c.heads + head;
+                const uint32_t u = e.seq0 * a.c.heads + head, first = start + head * r.len;
                 p.table = a.blocks + (uint64_t)e.seq0 * a.blocks_per_seq;
                 p.part_row = a.own_first_row + (u + blockIdx.x) * a.own_cap;
                 p.off_b = a.own_off_b;
-                if (!t0) a.own_parts[u] = parts;
+                if (!t0) a.own_parts[u] = make_uint2((first + kExtra) / share, (first + r.len - 1) / share);
             }
             sh.pieces[np % kPieces] = p;
             mbar_arrive(&sh.pc_full[np % kPieces]);
@@ -1106,7 +1135,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
     for (uint32_t i = threadIdx.x * per; i < (threadIdx.x + 1) * per && i < entries; i++) {
         const Entry e = entry_of(a, i);
         bad |= e.bad;
-        if (e.len) mine += a.c.heads * ((e.rows + S::kTileRows - 1) / S::kTileRows) * ((e.len + S::kKeys - 1) / S::kKeys + kExtra);
+        const Region r = region_of(a, e, 1, S::kKeys);
+        mine += r.width * r.rows;
     }
     uint32_t upto = warp_incl_sum(mine);
     if (lane == 31) sh.sums[warp] = upto;
