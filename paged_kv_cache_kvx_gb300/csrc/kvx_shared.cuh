@@ -18,7 +18,7 @@ constexpr int kSoftWarps = 8, kCopyWarps = 8, kMmaWarp = 16, kWalkWarp = 18, kLo
 constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kCopyThreads = 32 * kCopyWarps;
 constexpr int kPieces = 8;  // descriptors that the walking warp may be ahead
-constexpr uint32_t kRound = 64;  // keys that a slot's softmax takes at a time
+constexpr uint32_t kHalf = 64;  // keys that a slot's softmax takes at a time
 constexpr uint32_t kRows = 128;  // of a slot: the tensor cores' M, a query row for each lane of tensor memory
 constexpr uint32_t kExtra = 1;   // tiles that a unit's own overhead counts as
 constexpr uint32_t kMinShare = 2;
@@ -124,6 +124,12 @@ template <int DP, int ES>
 struct Shape {
     static constexpr uint32_t kKeys = DP == 256 ? 64 : 128;  // of a tile
     static constexpr uint32_t kTileRows = DP == 256 ? 128 : 256;
+    // A slot has room for the logits of 128 keys: of a tile's two halves, or of
+    // two tiles.  (Two halves that the tensor cores fill one by one, the next
+    // while the softmax works on the other, take longer: a product with 64 keys
+    // reads as many bytes of the queries as one with 128, and is bound by shared
+    // memory's bandwidth.  100,000 tokens, 4 x 256 rows: 370 and .. us.)
+    static constexpr uint32_t kHalves = kKeys / kHalf, kPlaces = 2 / kHalves;
     static constexpr uint32_t kStage = kKeys * DP * 2;  // bytes of a tile of keys or values in 16 bits
     static constexpr uint32_t kQ = kRows * DP * 2;
     static constexpr uint32_t kQBufs = DP == 256 ? 1 : 2;
@@ -143,10 +149,12 @@ struct alignas(16) Group {
 struct alignas(16) Shared {  // behind the tiles
     uint64_t kv_full[11], kv_empty[11];
     uint64_t q_empty[2];
-    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // by slot and round & 1
+    uint64_t s_full[2][2], p_full[2][2], pv_done[2][2];  // by slot and place (s_full: the tile's)
     uint64_t o_free[2];
     uint64_t pc_full[kPieces], pc_empty[kPieces];
     uint64_t found[8], taken[8];
+    uint64_t turn[2];
+    uint32_t begun;  // tiles of keys and of values whose copies to their places have begun
     uint64_t drained;
     Piece pieces[kPieces];
     Group groups[64];        // [tile][group][keys, values]
@@ -170,6 +178,14 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
         : "r"(smem_u32(bar)), "r"(parity)
         : "memory");
     return ok != 0;
+}
+__device__ __forceinline__ uint32_t ld_acquire(const uint32_t *p) {
+    uint32_t v;
+    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
+    return v;
+}
+__device__ __forceinline__ void st_release(uint32_t *p, uint32_t v) {
+    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
 }
 // mbar_wait by a whole warp, which goes on together.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
@@ -500,6 +516,7 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     auto hand_over = [&]() -> bool {
         const uint32_t t = done, stage = t % S::kStages;
         if (t >= S::kStages && !warp_wait(&sh.kv_empty[stage], (t / S::kStages & 1) ^ 1)) return false;
+        if (thread == 0) st_release(&sh.begun, t + 1);
         if constexpr (ES == 1) {
             const uint4 *from = reinterpret_cast<const uint4 *>(held + t % S::kHeld * (S::kStage / 2)) + thread;
             uint8_t *to = ring + stage * S::kStage;
@@ -548,7 +565,9 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     auto make_room = [&]() -> bool {
         if constexpr (ES == 2) {
             const uint32_t stage = issued % S::kStages;
-            return issued < S::kStages || warp_wait(&sh.kv_empty[stage], (issued / S::kStages & 1) ^ 1);
+            if (issued >= S::kStages && !warp_wait(&sh.kv_empty[stage], (issued / S::kStages & 1) ^ 1)) return false;
+            if (thread == 0) st_release(&sh.begun, issued + 1);
+            return true;
         } else {
             if (issued - done < S::kHeld) return true;
             copies_wait(S::kHeld - 1);
@@ -845,62 +864,81 @@ __device__ __forceinline__ bool look_up(const Args &a, Shared &sh, uint32_t lane
 
 // --------------------------------------------------------- the tensor cores
 
-// One warp a slot.  A slot goes by rounds of kRound keys, whose logits and weights
-// have two places: the next round's logits are there when the softmax has done
-// one.  Its warp takes the next product Q K^T as soon as a place is free and keys
-// are there, else the oldest product with V.  One thread does it all: without
-// votes and branches that a warp would have to come together after.
+// One warp a slot, of which one thread does it all: without votes and branches
+// that a warp would have to come together after.  It takes the next product Q K^T
+// as soon as there is room for its logits and keys are there, else the oldest
+// product with V.
 template <class T, int DP, int ES>
 __device__ __forceinline__ bool multiply(const Args &a, Shared &sh, const uint8_t *q_smem, const uint8_t *ring, uint32_t tmem,
                                          uint32_t slot) {
     using S = Shape<DP, ES>;
     const uint32_t steps = a.c.dim / 16;
-    const uint32_t qk = instruction<T>(kRound, false, a.negate);
+    const uint32_t qk = instruction<T>(S::kKeys, false, a.negate), qk_half = instruction<T>(kHalf, false, a.negate);
     const uint32_t pv = instruction<T>(DP == 256 ? (slot ? a.c.dim - 128 : 128) : a.c.dim, true, false);
     const uint32_t q0 = operand_low(smem_u32(q_smem), 16), k0 = operand_low(smem_u32(ring), 16);
     const uint32_t v0 = operand_low(smem_u32(ring) + (DP == 256 ? slot * 2 * (S::kKeys * 128) : 0), S::kKeys * 128);
     const uint32_t s_at = tmem + slot * 128, o_at = tmem + 256 + slot * 128;
-    uint32_t tile = 0;                        // its keys are the copies' number 2 * tile, its values the next
-    uint32_t started = 0, done = 0, outs = 0;  // rounds, and pieces with one
-    struct Round {  // a product with V that is due
+    uint32_t tile = 0;                         // its keys are the copies' number 2 * tile, its values the next
+    uint32_t started = 0, done = 0, outs = 0;  // this slot's tiles, and pieces with one
+    struct Due {    // a product with V
         uint32_t v;  // the values' number
-        uint32_t half;
-        bool fresh, last, twice;  // the piece's first; the tile's last round; lets go of the values for both slots
+        bool fresh, second, twice;  // the piece's first; the tile has a second half; lets go of the values for both slots
     };
-    Round due = {}, then = {};
-    // Copies are looked at in their order, the other slot's too: a barrier's parity
-    // says nothing about a tile before the one that was in its place is known to
-    // have come.
-    uint32_t seen = 0;  // copies known to be there
+    Due due = {}, then = {};
+    // A barrier's parity tells a tile from the one before in its place, but not from
+    // earlier ones, which may be the other slot's: so its copy has to have begun,
+    // for which the tile before must have come and gone.
+    uint32_t begun = 0;
     auto there = [&](uint32_t copy) -> bool {
-        while (seen <= copy && mbar_test(&sh.kv_full[seen % S::kStages], seen / S::kStages & 1)) seen++;
-        return seen > copy;
+        if (begun <= copy) begun = ld_acquire(&sh.begun);
+        return begun > copy && mbar_test(&sh.kv_full[copy % S::kStages], copy / S::kStages & 1);
     };
     auto await = [&](uint32_t copy) -> bool {
-        for (; seen <= copy; seen++)
-            if (!mbar_wait(&sh.kv_full[seen % S::kStages], seen / S::kStages & 1)) return false;
+        if (begun <= copy) begun = ld_acquire(&sh.begun);
+        if (begun <= copy) {
+            const uint64_t t0 = global_ns();
+            for (uint32_t i = 0; (begun = ld_acquire(&sh.begun)) <= copy; i++)
+                if (i >= kSpinLimit || global_ns() - t0 > kWaitNs) return false;
+        }
+        return mbar_wait(&sh.kv_full[copy % S::kStages], copy / S::kStages & 1);
+    };
+    auto times_v = [&](uint32_t h) -> bool {  // with the values of a half
+        const uint32_t stage = due.v % S::kStages, place = S::kHalves == 2 ? h : done & 1;
+        if (!mbar_wait(&sh.p_full[slot][place], (S::kHalves == 2 ? done : done >> 1) & 1)) return false;
+        tmem_after();
+        if (!h) fence_async();  // the copies' writes, too, are before what follows
+        if (!h || due.second) {
+            const uint32_t low = v0 + stage * (S::kStage / 16);
+#pragma unroll
+            for (uint32_t i = 0; i < kHalf / 16; i++)
+                mma_ts(o_at, s_at + place * kHalf + i * 8, low + (h * kHalf / 16 + i) * 128, kOperandHigh, pv, h || i ? 1 : !due.fresh);
+        }
+        mma_commit(&sh.pv_done[slot][place]);
         return true;
     };
-    auto finish = [&]() -> bool {
-        const uint32_t stage = due.v % S::kStages, buffer = done & 1;
+    auto finish_most = [&]() -> bool {  // but for the last half
         if (!await(due.v)) return false;
         if (due.fresh) {
             if (outs && !mbar_wait(&sh.o_free[slot], (outs & 1) ^ 1)) return false;
             outs++;
         }
-        if (!mbar_wait(&sh.p_full[slot][buffer], done >> 1 & 1)) return false;
-        tmem_after();
-        fence_async();  // the copies' writes, too, are before what follows
-        const uint32_t low = v0 + stage * (S::kStage / 16) + due.half * (kRound * 8), add = !due.fresh, p = s_at + buffer * kRound;
-#pragma unroll
-        for (uint32_t i = 0; i < kRound / 16; i++) mma_ts(o_at, p + i * 8, low + i * 128, kOperandHigh, pv, i ? 1 : add);
-        mma_commit(&sh.pv_done[slot][buffer]);
-        if (due.last) mma_commit(&sh.kv_empty[stage]);
-        if (due.last && due.twice) mma_commit(&sh.kv_empty[stage]);
+        return S::kHalves == 1 || times_v(0);
+    };
+    auto finish_rest = [&]() -> bool {
+        if (!times_v(S::kHalves - 1)) return false;
+        mma_commit(&sh.kv_empty[due.v % S::kStages]);
+        if (due.twice) mma_commit(&sh.kv_empty[due.v % S::kStages]);
         due = then;
         done++;
         return true;
     };
+    auto finish = [&]() -> bool { return finish_most() && finish_rest(); };
+    // Where both slots take every tile they take turns: what one gives the tensor
+    // cores at a time, the rest of a tile and the next one's logits, is not mixed
+    // with the other's.  Mixed, both end together, and both softmaxes want the same
+    // units at the same time while the tensor cores wait (425 us against ..).
+    uint32_t turns = 0;
+    auto take_turn = [&]() -> bool { return slot ? mbar_wait(&sh.turn[1], turns & 1) : !turns || mbar_wait(&sh.turn[0], (turns & 1) ^ 1); };
     for (uint32_t np = 0;; np++) {
         if (!mbar_test(&sh.pc_full[np % kPieces], np / kPieces & 1)) {
             while (done != started)  // nothing waits for the next piece
@@ -913,39 +951,47 @@ __device__ __forceinline__ bool multiply(const Args &a, Shared &sh, const uint8_
         const bool both = p.both;
         uint32_t t = both ? 0 : (p.event & 1) ^ slot;
         const bool any = t < nt;
-        bool fresh = true;
-        for (; t < nt; t += both ? 1 : 2) {
+        const uint32_t q = q0 + (DP == 256 ? 0 : both ? slot : np & 1) * (S::kQ / 16);
+        for (bool fresh = true; t < nt; t += both ? 1 : 2, fresh = false) {
             const uint32_t k = 2 * (tile + t), stage = k % S::kStages;
-            const uint32_t halves = S::kKeys == kRound || keys - t * S::kKeys <= kRound ? 1 : 2;
-            for (uint32_t h = 0; h < halves; h++) {
-                if (started - done == 2 && !finish()) return false;
-                if (!h) {  // (a piece's queries come with its first keys)
+            // (a piece's queries come with its first keys)
+            if (started - done == S::kPlaces) {
+                if (!finish_most()) return false;
+                const bool now = both && there(k);
+                if (now && !take_turn()) return false;
+                if (!finish_rest()) return false;
+                if (!now) {
                     while (done != started && !there(k))
                         if (!finish()) return false;
                     if (!await(k)) return false;
+                    if (both && !take_turn()) return false;
                 }
-                tmem_after();
-                fence_async();
-                const uint32_t q = q0 + (DP == 256 ? 0 : both ? slot : np & 1) * (S::kQ / 16);
-                const uint32_t kk = k0 + stage * (S::kStage / 16) + h * (kRound * 8);
-                const uint32_t buffer = started & 1, d = s_at + buffer * kRound;
-                const bool last = h + 1 == halves;
-#pragma unroll
-                for (uint32_t i = 0; i < DP / 16; i++)
-                    if (i < steps)
-                        mma_ss(d, q + i / 4 * (kRows * 8) + i % 4 * 2, kOperandHigh,
-                               kk + i / 4 * (S::kKeys * 8) + i % 4 * 2, kOperandHigh, qk, i > 0);
-                mma_commit(&sh.s_full[slot][buffer]);
-                if (last) mma_commit(&sh.kv_empty[stage]);
-                if (last && !both) mma_commit(&sh.kv_empty[stage]);
-                const Round r = {k + 1, h, fresh, last, !both};
-                if (started == done)
-                    due = r;
-                else
-                    then = r;
-                fresh = false;
-                started++;
+            } else {
+                while (done != started && !there(k))
+                    if (!finish()) return false;
+                if (!await(k)) return false;
+                if (both && !take_turn()) return false;
             }
+            tmem_after();
+            fence_async();
+            const bool second = S::kHalves == 2 && keys - t * S::kKeys > kHalf;
+            const uint32_t kk = k0 + stage * (S::kStage / 16), place = S::kPlaces == 2 ? started & 1 : 0, d = s_at + place * kHalf;
+            const uint32_t what = S::kHalves == 1 || second ? qk : qk_half;
+#pragma unroll
+            for (uint32_t i = 0; i < DP / 16; i++)
+                if (i < steps)
+                    mma_ss(d, q + i / 4 * (kRows * 8) + i % 4 * 2, kOperandHigh, kk + i / 4 * (S::kKeys * 8) + i % 4 * 2,
+                           kOperandHigh, what, i > 0);
+            if (both) mbar_arrive(&sh.turn[slot ^ 1]), turns++;
+            mma_commit(&sh.s_full[slot][place]);
+            mma_commit(&sh.kv_empty[stage]);
+            if (!both) mma_commit(&sh.kv_empty[stage]);
+            const Due r = {k + 1, fresh, second, !both};
+            if (started == done)
+                due = r;
+            else
+                then = r;
+            started++;
         }
         tile += nt;
         // both slots let go of a query, or the only one that took it twice
@@ -996,7 +1042,7 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
     const uint32_t col = DP == 256 ? slot * 128 : 0;
     const uint32_t cols = DP == 256 ? (slot ? a.c.dim - 128 : 128) : a.c.dim;  // of the output, a multiple of 16
     const uint64_t scale = pair(a.scale2, a.scale2);
-    uint32_t rounds = 0;
+    uint32_t tiles = 0;  // of this slot
     for (uint32_t np = 0;; np++) {
         if (!warp_wait(&sh.pc_full[np % kPieces], np / kPieces & 1)) return false;
         const Piece &p = sh.pieces[np % kPieces];
@@ -1008,16 +1054,20 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
         uint32_t t = both ? 0 : (p.event & 1) ^ slot;
         const bool any = t < nt;
         float base = 0, limit = -INFINITY, sum = 0;
-        uint32_t at = t * S::kKeys;  // the round's first key
-        for (bool fresh = true; at < keys; fresh = false) {
-            const uint32_t buffer = rounds & 1, left = keys - at;
-            if (!warp_wait(&sh.s_full[slot][buffer], rounds >> 1 & 1)) return false;
-            if (busy) {
-                tmem_after();
-                const uint32_t s = s_at + buffer * kRound;
-                if (left < kRound) {  // what lies behind the last key weighs nothing
+        bool fresh = true;
+        for (; t < nt; t += both ? 1 : 2, tiles++) {
+            const uint32_t left_tile = keys - t * S::kKeys, tile_place = S::kPlaces == 2 ? tiles & 1 : 0;
+            if (!warp_wait(&sh.s_full[slot][tile_place], (S::kPlaces == 2 ? tiles >> 1 : tiles) & 1)) return false;
 #pragma unroll 1
-                    for (uint32_t c = left & ~15u; c < kRound; c += 16) {
+            for (uint32_t h = 0; h < S::kHalves; h++) {
+            const uint32_t place = S::kHalves == 2 ? h : tiles & 1;
+            const uint32_t left = left_tile > h * kHalf ? left_tile - h * kHalf : 0;
+            if (busy && left) {
+                tmem_after();
+                const uint32_t s = s_at + place * kHalf;
+                if (left < kHalf) {  // what lies behind the last key weighs nothing
+#pragma unroll 1
+                    for (uint32_t c = left & ~15u; c < kHalf; c += 16) {
                         uint32_t y[16];
                         tmem_ld16(y, s + c);
                         tmem_wait_ld(y);
@@ -1051,7 +1101,8 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
                     }
                     if (!fresh) {
                         // the product before has to be in the outputs
-                        if (!warp_wait(&sh.pv_done[slot][buffer ^ 1], (rounds - 1) >> 1 & 1)) return false;
+                        const uint32_t use = S::kHalves == 2 ? (h ? tiles : tiles - 1) : (tiles - 1) >> 1;
+                        if (!warp_wait(&sh.pv_done[slot][place ^ 1], use & 1)) return false;
                         tmem_after();
 #pragma unroll 1
                         for (uint32_t c = 0; c < cols; c += 16) {
@@ -1087,14 +1138,14 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
                 tmem_before();
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[slot][buffer]);
-            rounds++;
-            at += kRound;
-            if (at % S::kKeys == 0 && !both) at += S::kKeys;  // the other slot's tile
+            if (lane == 0) mbar_arrive(&sh.p_full[slot][place]);
+            fresh = false;
+            }
         }
         const uint64_t row = p.part_row + (slot && DP != 256 ? p.off_b : 0) + r;
         if (any) {
-            if (!warp_wait(&sh.pv_done[slot][(rounds - 1) & 1], (rounds - 1) >> 1 & 1)) return false;
+            const uint32_t last = tiles - 1;
+            if (!warp_wait(&sh.pv_done[slot][S::kHalves == 2 ? 1 : last & 1], (S::kHalves == 2 ? last : last >> 1) & 1)) return false;
             if (busy) {
                 tmem_after();
 #pragma unroll 1
@@ -1151,6 +1202,8 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
             mbar_init(&sh.pc_full[i], 1), mbar_init(&sh.pc_empty[i], kSoftWarps + kCopyWarps + 2 + (a.paged16 ? 1 : 0));
         for (int i = 0; i < 8; i++) mbar_init(&sh.found[i], 1), mbar_init(&sh.taken[i], kCopyWarps);
         mbar_init(&sh.drained, 2);
+        mbar_init(&sh.turn[0], 1), mbar_init(&sh.turn[1], 1);
+        sh.begun = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     __syncthreads();
