@@ -179,13 +179,16 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ uint32_t ld_acquire(const uint32_t *p) {
+// A word of shared memory that says how far its writer is.  (Relaxed: a release
+// would wait for the writer's copies on their way.  What a reader does next, it
+// asks of a barrier that the writer had seen pass.)
+__device__ __forceinline__ uint32_t progress(const uint32_t *p) {
     uint32_t v;
-    asm volatile("ld.acquire.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
+    asm volatile("ld.relaxed.cta.shared::cta.u32 %0, [%1];" : "=r"(v) : "r"(smem_u32(p)) : "memory");
     return v;
 }
-__device__ __forceinline__ void st_release(uint32_t *p, uint32_t v) {
-    asm volatile("st.release.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
+__device__ __forceinline__ void set_progress(uint32_t *p, uint32_t v) {
+    asm volatile("st.relaxed.cta.shared::cta.u32 [%0], %1;" ::"r"(smem_u32(p)), "r"(v) : "memory");
 }
 // mbar_wait by a whole warp, which goes on together.
 __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity) {
@@ -430,17 +433,25 @@ struct Widen<__nv_bfloat16> {
     __device__ __forceinline__ explicit Widen(uint32_t exponent) : e(exponent), factor((exponent + 120) * 0x00800080u) {}
     __device__ __forceinline__ bool simple() const { return e - 1 <= 133; }
     __device__ __forceinline__ static uint32_t check(const uint4 &v) {  // bits 7, 15, ...: there is a NaN
-        auto nan = [](uint32_t w) { return (w & 0x7F7F7F7Fu) + 0x01010101u; };
+        auto nan = [](uint32_t w) {
+            uint32_t r;
+            asm("mad.lo.u32 %0, %1, 1, %2;" : "=r"(r) : "r"(w & 0x7F7F7F7Fu), "r"(0x01010101u));
+            return r;
+        };
         return nan(v.x) | nan(v.y) | nan(v.z) | nan(v.w);
     }
-    __device__ __forceinline__ uint32_t two(uint32_t w) const {  // bytes 1 and 3
-        const uint32_t v = (w >> 4 & 0x07F007F0u) | (w & 0x80008000u);
-        uint32_t r;
+    // Bytes 0 and 2, by products that shift them by four places and their signs by
+    // four more: the units for logic have half the rate and the most to do (shifts
+    // and masks in their place: .. us against ..).
+    __device__ __forceinline__ uint32_t two(uint32_t w) const {
+        uint32_t v, r;
+        asm("mul.lo.u32 %0, %1, 16;" : "=r"(v) : "r"(w));
+        asm("mad.lo.u32 %0, %1, 240, %2;" : "=r"(v) : "r"(w & 0x00800080u), "r"(v));
         asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(v), "r"(factor));
         return r;
     }
     __device__ __forceinline__ uint2 four(uint32_t v) const {
-        return make_uint2(two(__byte_perm(v, 0, 0x1404)), two(__byte_perm(v, 0, 0x3424)));
+        return make_uint2(two(__byte_perm(v, 0, 0x4140)), two(__byte_perm(v, 0, 0x4342)));
     }
     __device__ __forceinline__ uint2 any(uint32_t v) const {
         uint32_t lo, hi;
@@ -493,7 +504,11 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     constexpr uint32_t kCopies = kWarpKeys / kAtOnce;
     const uint32_t warp = thread / 32, lane = thread & 31;
     const uint32_t key = warp * kWarpKeys + lane % kWarpKeys;  // whose addresses this lane looks up, within the tile
-    const uint32_t part = lane % kParts, row0 = lane / kParts;  // what it copies: that piece of rows row0 + kAtOnce * i
+    // What it copies: that piece of rows row0 + kAtOnce * i.  Eight lanes that write
+    // 8-bit rows' pieces in 16 bits, two pieces each, do so to four of a row and
+    // four of the next, whose places in 128 bytes differ.
+    const uint32_t part = ES == 2 ? lane % kParts : (lane & 3) | ((lane >> 3 << 2) & (kParts - 1));
+    const uint32_t row0 = ES == 2 ? lane / kParts : kParts == 4 ? lane >> 2 : (lane >> 2 & 1) | (kParts == 8 ? lane >> 4 << 1 : 0);
     const bool in = part < a.c.row_bytes / 16;
     // Where those go: the pattern of the swizzle comes again after eight rows.
     constexpr uint32_t kPeriod = 8 / kAtOnce ? 8 / kAtOnce : 1;
@@ -516,17 +531,23 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     auto hand_over = [&]() -> bool {
         const uint32_t t = done, stage = t % S::kStages;
         if (t >= S::kStages && !warp_wait(&sh.kv_empty[stage], (t / S::kStages & 1) ^ 1)) return false;
-        if (thread == 0) st_release(&sh.begun, t + 1);
+        if (thread == 0) set_progress(&sh.begun, t + 1);
         if constexpr (ES == 1) {
             const uint4 *from = reinterpret_cast<const uint4 *>(held + t % S::kHeld * (S::kStage / 2)) + thread;
             uint8_t *to = ring + stage * S::kStage;
             const uint8_t *exponents = scales + t % S::kHeld * kTileScales + warp * 16;
             __syncwarp();  // each lane has waited for its copies
-            uint32_t odd = 0, check = 0;
+            uint32_t odd = 0, check = 0, e[kCopies];
+            uint4 v[kCopies];
+#pragma unroll
+            for (uint32_t c = 0; c < kCopies; c++) {  // all reads before the first write, which they could not pass
+                v[c] = from[c * kCopyThreads];
+                e[c] = row_scales ? exponents[first_scale + c * kAtOnce + row0] : 127;
+            }
 #pragma unroll
             for (uint32_t c = 0; c < kCopies; c++) {
-                const uint4 raw = from[c * kCopyThreads];
-                const Widen<T> w(row_scales ? exponents[first_scale + c * kAtOnce + row0] : 127);
+                const uint4 raw = v[c];
+                const Widen<T> w(e[c]);
                 check |= Widen<T>::check(raw);
                 odd |= !w.simple();
                 const uint2 x0 = w.four(raw.x), x1 = w.four(raw.y), x2 = w.four(raw.z), x3 = w.four(raw.w);
@@ -566,7 +587,7 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
         if constexpr (ES == 2) {
             const uint32_t stage = issued % S::kStages;
             if (issued >= S::kStages && !warp_wait(&sh.kv_empty[stage], (issued / S::kStages & 1) ^ 1)) return false;
-            if (thread == 0) st_release(&sh.begun, issued + 1);
+            if (thread == 0) set_progress(&sh.begun, issued + 1);
             return true;
         } else {
             if (issued - done < S::kHeld) return true;
@@ -890,14 +911,14 @@ __device__ __forceinline__ bool multiply(const Args &a, Shared &sh, const uint8_
     // for which the tile before must have come and gone.
     uint32_t begun = 0;
     auto there = [&](uint32_t copy) -> bool {
-        if (begun <= copy) begun = ld_acquire(&sh.begun);
+        if (begun <= copy) begun = progress(&sh.begun);
         return begun > copy && mbar_test(&sh.kv_full[copy % S::kStages], copy / S::kStages & 1);
     };
     auto await = [&](uint32_t copy) -> bool {
-        if (begun <= copy) begun = ld_acquire(&sh.begun);
+        if (begun <= copy) begun = progress(&sh.begun);
         if (begun <= copy) {
             const uint64_t t0 = global_ns();
-            for (uint32_t i = 0; (begun = ld_acquire(&sh.begun)) <= copy; i++)
+            for (uint32_t i = 0; (begun = progress(&sh.begun)) <= copy; i++)
                 if (i >= kSpinLimit || global_ns() - t0 > kWaitNs) return false;
         }
         return mbar_wait(&sh.kv_full[copy % S::kStages], copy / S::kStages & 1);
