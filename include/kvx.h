@@ -699,9 +699,8 @@ kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t q_stride,
  *   group_first    [num_groups + 1] uint32, not decreasing: the sequences of
  *                  group g are group_first[g] .. group_first[g+1] - 1; those
  *                  before the first group and behind the last see their own
- *                  tokens only.  A group that decreases or reaches beyond
- *                  num_seqs raises KVX_S_BOUNDS, and the outputs of the
- *                  sequences it names are unspecified.
+ *                  tokens only.  A table that decreases or reaches beyond
+ *                  num_seqs raises KVX_S_BOUNDS, and out and lse are unspecified.
  *   prefix_blocks  [num_groups][blocks_per_prefix] uint32.
  *   prefix_lens    [num_groups] uint32; like lens, one that exceeds its pages
  *                  raises KVX_S_BOUNDS and counts as full pages.
@@ -710,7 +709,8 @@ kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t q_stride,
  * under 2^-14 or from 65520 on).  Logits, softmax and sums are held in 32 bits;
  * the weights that multiply V are rounded to `dtype`, as V and the output are.
  * An infinite value in V makes its column of the output infinite, or NaN where
- * its weight counts as 0 (in fp16 one under 2^-32 of a head's largest).
+ * its weight counts as 0 (in fp16 one under 2^-32 of a head's largest); in bf16
+ * values from about 2^100 on may overflow on the way.
  * Results depend on nothing but the arguments and the device's SM count: no
  * atomics.  After KVX_S_TIMEOUT out and lse are unspecified.  Two launches;
  * num_seqs == 0 enqueues nothing.

@@ -119,13 +119,17 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
         p.cap = a.own_cap, p.off_b = a.own_off_b, p.subs = wide ? 1 : 2;
         p.b0 = w[1].x, p.blocks = w[1].y - w[1].x + 1, p.each = 1;
     }
-    const uint32_t first = parts[0].count(), all = first + parts[1].count();
+    // A call that ended early, by a table in disorder or a wait that ran out, may
+    // leave anything: parts are at most 2 * (grid + 2) pairs of a prefix, and as many
+    // as blocks of own tokens.
+    const uint64_t counted = (uint64_t)parts[0].blocks * parts[0].each * parts[0].subs + parts[1].count();
+    const uint32_t first = parts[0].count(), all = counted > 8ull * (a.grid + 2) ? 0 : (uint32_t)counted;
     const uint32_t most = (uint32_t)(a.rows < kNone ? a.rows : kNone);
     auto at = [&](uint32_t i) {
         const uint32_t row = i < first ? parts[0].at(i)
                                        : parts[1].first_row + (parts[1].c0 + (i - first) / parts[1].subs) * parts[1].cap +
                                              (i - first) % parts[1].subs * parts[1].off_b;
-        return row < most ? row : kNone;  // (a group that a block left in disorder)
+        return row < most ? row : kNone;
     };
     // A warp's share, 32 parts at a time: a lane has one's base and sum; 0 stands
     // for none, whose outputs do not exist.
@@ -290,6 +294,7 @@ extern "C" kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q, u
     a.max_prefix = p.max_prefix, a.max_len = p.max_len;
     a.by_group = FastDiv(a.group);
     a.scale2 = fabsf(scale) * cache->k_scale * 1.4426950408889634f;
+    if (a.scale2 == 0) a.scale2 = 1.4e-45f;  // the smallest: what is masked by -infinity stays masked
     a.negate = scale < 0;
     a.paged16 = cache->page_tokens % 16 == 0;
     a.out = out, a.out_stride = out_stride, a.lse = lse, a.status = status;

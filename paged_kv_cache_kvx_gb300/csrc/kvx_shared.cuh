@@ -52,7 +52,8 @@ struct Args {
 
 // What is shared out: a group's prefix, or a sequence's own tokens.
 struct Entry {
-    uint32_t seq0, rows, len, bad;
+    uint32_t seq0, rows, len;
+    bool disorder, beyond;  // a group whose sequences do not exist; more tokens than pages
 };
 __device__ __forceinline__ Entry entry_of(const Args &a, uint32_t i) {
     Entry e = {};
@@ -63,7 +64,7 @@ __device__ __forceinline__ Entry entry_of(const Args &a, uint32_t i) {
         most = a.max_prefix;
         e.seq0 = from;
         if (from > to || to > a.num_seqs)
-            e.bad = KVX_S_BOUNDS;
+            e.disorder = true;
         else
             e.rows = (to - from) * a.group;
     } else {
@@ -72,7 +73,7 @@ __device__ __forceinline__ Entry entry_of(const Args &a, uint32_t i) {
         e.len = __ldg(a.lens + e.seq0);
         most = a.max_len;
     }
-    if (e.len > most) e.len = most, e.bad |= KVX_S_BOUNDS;
+    if (e.len > most) e.len = most, e.beyond = true;
     if (!e.rows) e.len = 0;
     return e;
 }
@@ -87,17 +88,17 @@ __device__ __forceinline__ Entry entry_of(const Args &a, uint32_t i) {
 // so; .. us and ..).
 struct Region {
     uint32_t len, width, rows, block;
-    __device__ __forceinline__ uint32_t columns(uint32_t b) const {  // of block b
+    __host__ __device__ __forceinline__ uint32_t columns(uint32_t b) const {  // of block b
         return width - b * block < block ? width - b * block : block;
     }
     // Number of the parts of a row's columns of one head in a block, by which parts
     // are laid out: it grows in the order in which these are gone through.
-    __device__ __forceinline__ uint32_t rank(uint32_t b, uint32_t row, uint32_t head) const {
+    __host__ __device__ __forceinline__ uint32_t rank(uint32_t b, uint32_t row, uint32_t head) const {
         const uint32_t first = b * block / len, last = (b * block + columns(b) - 1) / len;
         return rows * (b + first) + row * (last - first + 1) + head - first;
     }
 };
-__device__ __forceinline__ Region region_of(const Args &a, const Entry &e, uint32_t share, uint32_t keys) {
+__host__ __device__ __forceinline__ Region region_of(const Args &a, const Entry &e, uint32_t share, uint32_t keys) {
     Region r;
     r.len = e.len ? (e.len + keys - 1) / keys + kExtra : 0;
     r.width = a.c.heads * r.len;
@@ -108,7 +109,7 @@ __device__ __forceinline__ Region region_of(const Args &a, const Entry &e, uint3
 // The first part of a group's, by number.  Its parts are at most rows * (blocks + heads),
 // and one for each border of a share: blocks * rows is its columns over the share,
 // and tiles of query rows of all groups before it, g for rounding, count the rest.
-__device__ __forceinline__ uint32_t group_parts(const Args &a, uint32_t start, uint32_t share, uint32_t first_seq, uint32_t g) {
+__host__ __device__ __forceinline__ uint32_t group_parts(const Args &a, uint32_t start, uint32_t share, uint32_t first_seq, uint32_t g) {
     return start / share + ((uint32_t)((uint64_t)first_seq * a.group / a.tile_rows) + g) * (a.c.heads + 2);
 }
 
@@ -528,6 +529,7 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     // there when the copies arrive.  8-bit ones come to a place of the thread's own
     // first and are handed over as 16-bit ones.
     uint32_t issued = 0, done = 0;
+    uint64_t exist = 0;  // a byte for each of the last eight tiles: rows up to which this warp's have scales
     auto hand_over = [&]() -> bool {
         const uint32_t t = done, stage = t % S::kStages;
         if (t >= S::kStages && !warp_wait(&sh.kv_empty[stage], (t / S::kStages & 1) ^ 1)) return false;
@@ -537,12 +539,14 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
             uint8_t *to = ring + stage * S::kStage;
             const uint8_t *exponents = scales + t % S::kHeld * kTileScales + warp * 16;
             __syncwarp();  // each lane has waited for its copies
+            const uint32_t rows = (uint32_t)(exist >> (t % 8 * 8)) & 0xFF;
             uint32_t odd = 0, check = 0, e[kCopies];
             uint4 v[kCopies];
 #pragma unroll
             for (uint32_t c = 0; c < kCopies; c++) {  // all reads before the first write, which they could not pass
                 v[c] = from[c * kCopyThreads];
                 e[c] = row_scales ? exponents[first_scale + c * kAtOnce + row0] : 127;
+                if (row_scales && first_scale + c * kAtOnce + row0 >= rows) e[c] = 127;  // zeros, whatever its scale says
             }
 #pragma unroll
             for (uint32_t c = 0; c < kCopies; c++) {
@@ -560,7 +564,7 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
                 for (uint32_t c = 0; c < kCopies; c++) {
                     const uint4 raw = from[c * kCopyThreads];
                     const uint32_t r = c * kAtOnce + row0, p0 = 2 * part;
-                    const Widen<T> w(row_scales ? exponents[first_scale + r] : 127);
+                    const Widen<T> w(row_scales && first_scale + r < rows ? exponents[first_scale + r] : 127);
                     const uint2 x0 = w.any(raw.x), x1 = w.any(raw.y), x2 = w.any(raw.z), x3 = w.any(raw.w);
                     const uint32_t at = p0 / 8 * (S::kKeys * 128) + (warp * kWarpKeys + r) * 128 + ((p0 % 8 ^ (r & 7)) * 16);
                     *reinterpret_cast<uint4 *>(to + at) = make_uint4(x0.x, x0.y, x1.x, x1.y);
@@ -595,7 +599,11 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
             return hand_over();
         }
     };
+    auto set_rows = [&](uint32_t t, uint32_t rows) {
+        if (ES == 1) exist = (exist & ~(0xFFull << (t % 8 * 8))) | (uint64_t)rows << (t % 8 * 8);
+    };
     auto set_scale = [&](uint32_t t, uint32_t exponent) {
+        set_rows(t, kWarpKeys);
         if (row_scales && lane < kWarpKeys) scales[t % (S::kHeld ? S::kHeld : 1) * kTileScales + warp * 16 + lane] = (uint8_t)exponent;
     };
     auto issue = [&](uint64_t row) {  // this lane's row; odd: there is none
@@ -667,6 +675,7 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
                     if (in) copy16(base + (ES == 2 ? place_of(c) : c * (kCopyThreads * 16)), there ? from : a.c.pool, there);
                 }
             }
+            set_rows(t, g.count);
             if (row_scales && lane == 0)  // 16 bytes, wherever a warp's rows begin among them
                 copy16(smem_u32(scales + t % (S::kHeld ? S::kHeld : 1) * kTileScales + warp * 16), reinterpret_cast<const uint8_t *>(g.row + g.scale), g.count > 0);
             if (ES == 2)
@@ -1204,9 +1213,11 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
     const uint32_t entries = a.num_groups + a.num_seqs, per = (entries + kThreads - 1) / kThreads;
     uint32_t *cum = reinterpret_cast<uint32_t *>(smem);
     uint32_t mine = 0, bad = 0;
+    bool disorder = false;
     for (uint32_t i = threadIdx.x * per; i < (threadIdx.x + 1) * per && i < entries; i++) {
         const Entry e = entry_of(a, i);
-        bad |= e.bad;
+        if (e.disorder || e.beyond) bad |= KVX_S_BOUNDS;
+        disorder |= e.disorder;
         const Region r = region_of(a, e, 1, S::kKeys);
         mine += r.width * r.rows;
     }
@@ -1227,7 +1238,10 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
         sh.begun = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    __syncthreads();
+    if (__syncthreads_or(disorder)) {  // (groups may overlap: their parts, and all tiles, would be more than there is room for)
+        raise(a.status, bad);
+        return;
+    }
     uint32_t total = 0;
     for (uint32_t w = 0; w < kWarps; w++) {
         if (w < warp) upto += sh.sums[w];
