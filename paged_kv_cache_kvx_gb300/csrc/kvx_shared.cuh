@@ -16,7 +16,8 @@ namespace shared {
 // copying warp looks up its own).
 constexpr int kSoftWarps = 8, kCopyWarps = 8, kMmaWarp = 16, kWalkWarp = 18, kLookWarp = 19, kWarps = 20;
 constexpr int kThreads = 32 * kWarps;
-constexpr uint32_t kCopyThreads = 32 * kCopyWarps;
+constexpr uint32_t kKindWarps = kCopyWarps / 2;  // that copy keys; the others copy values
+constexpr uint32_t kKindThreads = 32 * kKindWarps;
 constexpr int kPieces = 8;  // descriptors that the walking warp may be ahead
 constexpr uint32_t kHalf = 64;  // keys that a slot's softmax takes at a time
 constexpr uint32_t kRows = 128;  // of a slot: the tensor cores' M, a query row for each lane of tensor memory
@@ -155,14 +156,14 @@ struct alignas(16) Shared {  // behind the tiles
     uint64_t pc_full[kPieces], pc_empty[kPieces];
     uint64_t found[8], taken[8];
     uint64_t turn[2];
-    uint32_t begun;  // tiles of keys and of values whose copies to their places have begun
+    uint32_t begun[2];  // tiles of keys and of values whose copies to their places have begun
     uint64_t drained;
     Piece pieces[kPieces];
     Group groups[64];        // [tile][group][keys, values]
     uint32_t sums[kWarps];
     uint32_t tmem;
 };
-constexpr uint32_t kTileScales = kCopyWarps * 16;  // bytes of an 8-bit tile on its way, behind Shared: [warp][row]
+constexpr uint32_t kTileScales = 128;  // bytes of an 8-bit tile on its way, behind Shared: [row]
 template <int DP, int ES>
 constexpr uint32_t kSmem = Shape<DP, ES>::kTiles + sizeof(Shared) + Shape<DP, ES>::kHeld * kTileScales;
 
@@ -492,19 +493,41 @@ struct Widen<__half> {
     }
 };
 
-// The copying warps.  A warp looks up and copies a quarter of a tile's rows: a
-// lane has one token's segment addresses, which the copying lanes take from it.
-// Tiles go keys of tile e, values of tile e-1, as the tensor cores take them.
+// Whether a copy has begun.  A barrier's parity tells a tile from the one before in
+// its place, but not from earlier ones, which may be another warp's business: so
+// its copy has to have begun before the barrier is asked, for which the tile
+// before must have come and gone.  `known`: what was read last.
+__device__ __forceinline__ bool has_begun(const Shared &sh, uint32_t &known, uint32_t copy) {
+    if (known <= copy / 2) known = progress(&sh.begun[copy & 1]);
+    return known > copy / 2;
+}
+__device__ __forceinline__ bool await_begun(const Shared &sh, uint32_t &known, uint32_t copy) {
+    if (has_begun(sh, known, copy)) return true;
+    const uint64_t t0 = global_ns();
+    for (uint32_t i = 0; i < kSpinLimit; i++) {
+        if (has_begun(sh, known, copy)) return true;
+        if (global_ns() - t0 > kWaitNs) return false;
+    }
+    return false;
+}
+
+// The copying warps: four for keys, four for values, a quarter of a tile's rows
+// each.  Copies are numbered 2 * tile and 2 * tile + 1 and take their places in
+// turn.  Without groups of 16 tokens a lane looks up one token's segment, which
+// the copying lanes take from it.
 template <class T, int DP, int ES>
 __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q_smem, uint8_t *ring, uint8_t *held, uint32_t thread,
                                            uint32_t &bad) {
     using S = Shape<DP, ES>;
-    constexpr uint32_t kWarpKeys = S::kKeys / kCopyWarps;
+    constexpr uint32_t kWarpKeys = S::kKeys / kKindWarps;
     constexpr uint32_t kParts = DP * ES / 16;  // 16-byte pieces of a row
     constexpr uint32_t kAtOnce = 32 / kParts;  // rows that a warp copies with one instruction
     constexpr uint32_t kCopies = kWarpKeys / kAtOnce;
-    const uint32_t warp = thread / 32, lane = thread & 31;
-    const uint32_t key = warp * kWarpKeys + lane % kWarpKeys;  // whose addresses this lane looks up, within the tile
+    constexpr uint32_t kHeld = S::kHeld ? S::kHeld / 2 : 1;  // of a kind
+    const uint32_t kind = thread / kKindThreads, lane = thread & 31;
+    thread %= kKindThreads;
+    const uint32_t warp = thread / 32;
+    const uint32_t key = warp * kWarpKeys + lane % kWarpKeys;  // whose address this lane looks up, within the tile
     // What it copies: that piece of rows row0 + kAtOnce * i.  Eight lanes that write
     // 8-bit rows' pieces in 16 bits, two pieces each, do so to four of a row and
     // four of the next, whose places in 128 bytes differ.
@@ -523,48 +546,65 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     const uint64_t room = a.c.pool_bytes - a.c.span;
     const bool fits = a.c.pool_bytes >= a.c.span, row_scales = ES == 1 && a.c.scale_offset;
     uint8_t *scales = reinterpret_cast<uint8_t *>(&sh + 1);
-    const uint32_t first_scale = a.paged16 ? warp * kWarpKeys % 16 : 0;
 
     // 16-bit tiles are copied to where the tensor cores take them, and count as
     // there when the copies arrive.  8-bit ones come to a place of the thread's own
     // first and are handed over as 16-bit ones.
-    uint32_t issued = 0, done = 0;
-    uint64_t exist = 0;  // a byte for each of the last eight tiles: rows up to which this warp's have scales
+    uint32_t issued = 0, done = 0;  // of this kind
+    uint64_t exist = 0;             // 16 bits for each of the last four tiles: a bit less than 17 for each group, rows that exist
+    auto held_at = [&](uint32_t n) { return held + (n % kHeld * 2 + kind) * (S::kStage / 2); };
+    auto scales_at = [&](uint32_t n) { return scales + (n % kHeld * 2 + kind) * kTileScales + warp * kWarpKeys; };
+    // Waits for room for copy n of this kind, and says that it begins.  (The copy
+    // before in its place has to have begun, too, before its barrier is asked: see
+    // has_begun.  With an odd number of places that is one of the other kind.)
+    uint32_t others = 0;
+    auto begin = [&](uint32_t n) -> bool {
+        const uint32_t t = 2 * n + kind, use = t / S::kStages;
+        if (use && S::kStages % 2 && !await_begun(sh, others, t - S::kStages)) return false;
+        if (use && !warp_wait(&sh.kv_empty[t % S::kStages], (use & 1) ^ 1)) return false;
+        if (thread == 0) set_progress(&sh.begun[kind], n + 1);
+        return true;
+    };
     auto hand_over = [&]() -> bool {
-        const uint32_t t = done, stage = t % S::kStages;
-        if (t >= S::kStages && !warp_wait(&sh.kv_empty[stage], (t / S::kStages & 1) ^ 1)) return false;
-        if (thread == 0) set_progress(&sh.begun, t + 1);
+        const uint32_t n = done, stage = (2 * n + kind) % S::kStages;
+        if (!begin(n)) return false;
         if constexpr (ES == 1) {
-            const uint4 *from = reinterpret_cast<const uint4 *>(held + t % S::kHeld * (S::kStage / 2)) + thread;
+            const uint4 *from = reinterpret_cast<const uint4 *>(held_at(n)) + thread;
             uint8_t *to = ring + stage * S::kStage;
-            const uint8_t *exponents = scales + t % S::kHeld * kTileScales + warp * 16;
+            const uint8_t *exponents = scales_at(n);
             __syncwarp();  // each lane has waited for its copies
-            const uint32_t rows = (uint32_t)(exist >> (t % 8 * 8)) & 0xFF;
-            uint32_t odd = 0, check = 0, e[kCopies];
-            uint4 v[kCopies];
+            const uint32_t groups = (uint32_t)(exist >> (n % 4 * 16)) & 0xFFFF;
+            auto exists = [&](uint32_t r) { return r % 16 < (groups >> (r / 16 * 8) & 0xFF); };
+            uint32_t odd = 0, check = 0;
+            constexpr uint32_t kBatch = kCopies < 4 ? kCopies : 4;
 #pragma unroll
-            for (uint32_t c = 0; c < kCopies; c++) {  // all reads before the first write, which they could not pass
-                v[c] = from[c * kCopyThreads];
-                e[c] = row_scales ? exponents[first_scale + c * kAtOnce + row0] : 127;
-                if (row_scales && first_scale + c * kAtOnce + row0 >= rows) e[c] = 127;  // zeros, whatever its scale says
-            }
+            for (uint32_t c0 = 0; c0 < kCopies; c0 += kBatch) {
+                uint32_t e[kBatch];
+                uint4 v[kBatch];
 #pragma unroll
-            for (uint32_t c = 0; c < kCopies; c++) {
-                const uint4 raw = v[c];
-                const Widen<T> w(e[c]);
-                check |= Widen<T>::check(raw);
-                odd |= !w.simple();
-                const uint2 x0 = w.four(raw.x), x1 = w.four(raw.y), x2 = w.four(raw.z), x3 = w.four(raw.w);
-                const uint32_t at = place_of(c);
-                *reinterpret_cast<uint4 *>(to + at) = make_uint4(x0.x, x0.y, x1.x, x1.y);
-                *reinterpret_cast<uint4 *>(to + (at ^ 16)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                for (uint32_t i = 0; i < kBatch; i++) {  // all reads before the first write, which they could not pass
+                    const uint32_t r = (c0 + i) * kAtOnce + row0;
+                    v[i] = from[(c0 + i) * kKindThreads];
+                    e[i] = row_scales ? exponents[r] : 127;
+                    if (row_scales && !exists(r)) e[i] = 127;  // zeros, whatever its scale says
+                }
+#pragma unroll
+                for (uint32_t i = 0; i < kBatch; i++) {
+                    const Widen<T> w(e[i]);
+                    check |= Widen<T>::check(v[i]);
+                    odd |= !w.simple();
+                    const uint2 x0 = w.four(v[i].x), x1 = w.four(v[i].y), x2 = w.four(v[i].z), x3 = w.four(v[i].w);
+                    const uint32_t at = place_of(c0 + i);
+                    *reinterpret_cast<uint4 *>(to + at) = make_uint4(x0.x, x0.y, x1.x, x1.y);
+                    *reinterpret_cast<uint4 *>(to + (at ^ 16)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
+                }
             }
             if (odd | (check & 0x80808080u)) {
 #pragma unroll 1
                 for (uint32_t c = 0; c < kCopies; c++) {
-                    const uint4 raw = from[c * kCopyThreads];
+                    const uint4 raw = from[c * kKindThreads];
                     const uint32_t r = c * kAtOnce + row0, p0 = 2 * part;
-                    const Widen<T> w(row_scales && first_scale + r < rows ? exponents[first_scale + r] : 127);
+                    const Widen<T> w(row_scales && exists(r) ? exponents[r] : 127);
                     const uint2 x0 = w.any(raw.x), x1 = w.any(raw.y), x2 = w.any(raw.z), x3 = w.any(raw.w);
                     const uint32_t at = p0 / 8 * (S::kKeys * 128) + (warp * kWarpKeys + r) * 128 + ((p0 % 8 ^ (r & 7)) * 16);
                     *reinterpret_cast<uint4 *>(to + at) = make_uint4(x0.x, x0.y, x1.x, x1.y);
@@ -588,35 +628,37 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     };
     // Room for the next tile.
     auto make_room = [&]() -> bool {
-        if constexpr (ES == 2) {
-            const uint32_t stage = issued % S::kStages;
-            if (issued >= S::kStages && !warp_wait(&sh.kv_empty[stage], (issued / S::kStages & 1) ^ 1)) return false;
-            if (thread == 0) set_progress(&sh.begun, issued + 1);
-            return true;
-        } else {
-            if (issued - done < S::kHeld) return true;
-            copies_wait(S::kHeld - 1);
-            return hand_over();
-        }
+        if (ES == 2) return begin(issued);
+        if (issued - done < kHeld) return true;
+        copies_wait(kHeld - 1);
+        return hand_over();
     };
-    auto set_rows = [&](uint32_t t, uint32_t rows) {
-        if (ES == 1) exist = (exist & ~(0xFFull << (t % 8 * 8))) | (uint64_t)rows << (t % 8 * 8);
+    auto set_rows = [&](uint32_t first, uint32_t second) {
+        if (ES == 1) exist = (exist & ~(0xFFFFull << (issued % 4 * 16))) | (uint64_t)(first | second << 8) << (issued % 4 * 16);
     };
-    auto set_scale = [&](uint32_t t, uint32_t exponent) {
-        set_rows(t, kWarpKeys);
-        if (row_scales && lane < kWarpKeys) scales[t % (S::kHeld ? S::kHeld : 1) * kTileScales + warp * 16 + lane] = (uint8_t)exponent;
+    auto set_scale = [&](uint32_t exponent) {
+        set_rows(16, 16);
+        if (row_scales && lane < kWarpKeys) scales_at(issued)[lane] = (uint8_t)exponent;
+    };
+    auto issued_one = [&]() {
+        if (ES == 2)
+            mbar_arrive_copies(&sh.kv_full[(2 * issued + kind) % S::kStages]);
+        else
+            copies_commit();
+        issued++;
+    };
+    auto place_now = [&]() {  // where the next copy's pieces go
+        return smem_u32(ES == 2 ? ring + (2 * issued + kind) % S::kStages * S::kStage : held_at(issued) + thread * 16);
     };
     auto issue = [&](uint64_t row) {  // this lane's row; odd: there is none
-        const uint32_t t = issued;
-        uint8_t *to = ES == 2 ? ring + t % S::kStages * S::kStage : held + t % (S::kHeld ? S::kHeld : 1) * (S::kStage / 2) + thread * 16;
-        const uint32_t base = smem_u32(to);
+        const uint32_t base = place_now();
         const uint32_t rows = __ballot_sync(0xFFFFFFFFu, !(row & 1)) >> row0;
         const uint64_t shift = (uint64_t)part * 16;
         if (__all_sync(0xFFFFFFFFu, !(row & 1))) {
 #pragma unroll
             for (uint32_t c = 0; c < kCopies; c++) {
                 const uint64_t from = __shfl_sync(0xFFFFFFFFu, row, c * kAtOnce + row0) + shift;
-                if (in) copy16(base + (ES == 2 ? place_of(c) : c * (kCopyThreads * 16)), reinterpret_cast<const void *>(from), true);
+                if (in) copy16(base + (ES == 2 ? place_of(c) : c * (kKindThreads * 16)), reinterpret_cast<const void *>(from), true);
             }
         } else {
 #pragma unroll 1
@@ -624,17 +666,14 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
                 const uint64_t from = (__shfl_sync(0xFFFFFFFFu, row, c * kAtOnce + row0) & ~1ull) + shift;
                 const uint32_t r = c * kAtOnce + row0;
                 const uint32_t at = part / 8 * (S::kKeys * 128) + (warp * kWarpKeys + r) * 128 + ((part % 8 ^ (r & 7)) * 16);
-                if (in) copy16(base + (ES == 2 ? at : c * (kCopyThreads * 16)), reinterpret_cast<const void *>(from), rows >> (c * kAtOnce) & 1);
+                if (in) copy16(base + (ES == 2 ? at : c * (kKindThreads * 16)), reinterpret_cast<const void *>(from), rows >> (c * kAtOnce) & 1);
             }
         }
-        if (ES == 2)
-            mbar_arrive_copies(&sh.kv_full[t % S::kStages]);
-        else
-            copies_commit();
-        issued++;
+        issued_one();
     };
     uint32_t q_used[2] = {};
-    auto issue_q = [&](uint32_t b, uint32_t piece) -> bool {  // rows of a piece into buffer b
+    auto issue_q = [&](uint32_t b, uint32_t piece) -> bool {  // rows of a piece into buffer b: they come with its first keys
+        if (kind) return true;
         const Piece p = sh.pieces[piece % kPieces];
         const uint32_t r0 = DP != 256 && p.both ? b * kRows : 0;
         const uint32_t rows = p.rows - r0 < kRows ? p.rows - r0 : kRows;
@@ -643,7 +682,7 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
         q_used[b]++;
         constexpr uint32_t kQParts = DP / 8;
         const uint32_t base = smem_u32(q_smem + b * S::kQ), q_parts = a.c.dim / 8;
-        for (uint32_t j = thread; j < rows * kQParts; j += kCopyThreads) {
+        for (uint32_t j = thread; j < rows * kQParts; j += kKindThreads) {
             const uint32_t r = j / kQParts, part = j % kQParts;
             const uint32_t rr = p.row0 + r0 + r, s = a.by_group.div(rr);
             const uint64_t from = (uint64_t)(p.seq0 + s) * a.q_stride + (uint64_t)(p.head * a.group + rr - s * a.group) * a.c.dim;
@@ -655,34 +694,29 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     };
 
     if (a.paged16) {
-        constexpr uint32_t kOff = 16 % kWarpKeys;  // (0: a warp's rows are one group's, or half of one's)
-        static_assert(kOff == 0);
-        const uint32_t group = warp * kWarpKeys / 16, off = warp * kWarpKeys % 16;
-        const uint64_t stride = a.c.token_stride, shift = (off + row0) * stride + part * 16;
-        auto issue_group = [&](const Group &g) {
-            const uint32_t t = issued;
-            uint8_t *to = ES == 2 ? ring + t % S::kStages * S::kStage : held + t % (S::kHeld ? S::kHeld : 1) * (S::kStage / 2) + thread * 16;
-            const uint32_t base = smem_u32(to);
-            const uint8_t *from = reinterpret_cast<const uint8_t *>(g.row + shift);
-            if (g.count == 16) {
+        constexpr uint32_t kWarpGroups = kWarpKeys / 16;
+        static_assert(kWarpKeys % 16 == 0 && kWarpGroups <= 2 && 16 % kAtOnce == 0);
+        const uint64_t stride = a.c.token_stride, shift = row0 * stride + part * 16;
+        auto issue_groups = [&](const Group (&g)[kWarpGroups]) {
+            const uint32_t base = place_now();
+            const bool whole = g[0].count == 16 && g[kWarpGroups - 1].count == 16;
 #pragma unroll
-                for (uint32_t c = 0; c < kCopies; c++, from += kAtOnce * stride)
-                    if (in) copy16(base + (ES == 2 ? place_of(c) : c * (kCopyThreads * 16)), from, true);
-            } else {
+            for (uint32_t k = 0; k < kWarpGroups; k++) {
+                const uint8_t *from = reinterpret_cast<const uint8_t *>(g[k].row + shift);
 #pragma unroll
-                for (uint32_t c = 0; c < kCopies; c++, from += kAtOnce * stride) {
-                    const bool there = off + row0 + c * kAtOnce < g.count;
-                    if (in) copy16(base + (ES == 2 ? place_of(c) : c * (kCopyThreads * 16)), there ? from : a.c.pool, there);
+                for (uint32_t i = 0; i < 16 / kAtOnce; i++, from += kAtOnce * stride) {
+                    const uint32_t c = k * (16 / kAtOnce) + i, to = base + (ES == 2 ? place_of(c) : c * (kKindThreads * 16));
+                    const bool there = whole || row0 + i * kAtOnce < g[k].count;
+                    if (in) copy16(to, there ? from : a.c.pool, there);
                 }
             }
-            set_rows(t, g.count);
-            if (row_scales && lane == 0)  // 16 bytes, wherever a warp's rows begin among them
-                copy16(smem_u32(scales + t % (S::kHeld ? S::kHeld : 1) * kTileScales + warp * 16), reinterpret_cast<const uint8_t *>(g.row + g.scale), g.count > 0);
-            if (ES == 2)
-                mbar_arrive_copies(&sh.kv_full[t % S::kStages]);
-            else
-                copies_commit();
-            issued++;
+            set_rows(g[0].count, g[kWarpGroups - 1].count);
+            if (row_scales && lane < kWarpGroups) {  // a group's 16 scales lie together
+                const Group &last = g[kWarpGroups - 1];
+                const uint64_t from = lane ? last.row + last.scale : g[0].row + g[0].scale;
+                copy16(smem_u32(scales_at(issued) + lane * 16), reinterpret_cast<const uint8_t *>(from), (lane ? last.count : g[0].count) > 0);
+            }
+            issued_one();
         };
         uint32_t tile = 0;
         for (uint32_t np = 0;; np++) {
@@ -696,14 +730,13 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
             for (uint32_t t = 0; t < nt; t++, tile++) {
                 const uint32_t slot = tile % S::kFound, parity = tile / S::kFound & 1;
                 if (!warp_test(&sh.found[slot], parity) && !(drain() && warp_wait(&sh.found[slot], parity))) return false;
-                const Group *g = sh.groups + (slot * S::kGroups + group) * 2;
-                const Group keys = g[0], values = g[1];
+                Group g[kWarpGroups];
+#pragma unroll
+                for (uint32_t k = 0; k < kWarpGroups; k++) g[k] = sh.groups[(slot * S::kGroups + warp * kWarpGroups + k) * 2 + kind];
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&sh.taken[slot]);
                 if (!make_room()) return false;
-                issue_group(keys);
-                if (!make_room()) return false;
-                issue_group(values);
+                issue_groups(g);
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.pc_empty[np % kPieces]);
@@ -721,7 +754,7 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     const uint32_t *table = nullptr;
     bool over = false, alive = true;
     uint32_t id = 0;
-    uint64_t seg[2] = {};
+    uint64_t seg = 0;
     auto find = [&]() -> Look {
         Look l = {};
         if (over || !alive) return l;
@@ -755,45 +788,38 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
     };
     auto find_segments = [&](Look &l) {
         if (l.valid && id >= a.c.B) bad |= KVX_S_BOUNDS, l.valid = 0;
-        if (l.valid) {
-            const uint64_t *entry = a.c.lane_addr(id, l.head, 0);
-            seg[0] = __ldg(entry), seg[1] = __ldg(entry + 1);
-        }
+        if (l.valid) seg = __ldg(a.c.lane_addr(id, l.head, kind));
     };
 
-    // Rows of the tile after a look-up's, with their scales on their way.
-    struct Rows {
-        uint64_t row[2];
-        uint32_t exponent[2];
+    // The row of the tile after a look-up's, with its scale on its way.
+    struct Row {
+        uint64_t row;
+        uint32_t exponent;
         uint32_t any, first, last, piece;
     };
-    auto find_rows = [&](const Look &l) -> Rows {
-        Rows r = {};
+    auto find_row = [&](const Look &l) -> Row {
+        Row r = {};
         r.any = l.any, r.first = l.first, r.last = l.last, r.piece = l.piece;
         if (!l.any) return r;
-#pragma unroll
-        for (int kv = 0; kv < 2; kv++) {
-            const uint64_t s = seg[kv];
-            const bool good = l.valid && fits && s <= room && !((uint32_t)s & 15);
-            if (l.valid && !good) a.c.ok(s, bad);
-            r.row[kv] = reinterpret_cast<uint64_t>(a.c.pool) + (good ? s + l.token * a.c.token_stride : 1);
-            r.exponent[kv] = 127;
-            if (row_scales && good) r.exponent[kv] = __ldg(a.c.pool + s + a.c.scale_offset + l.token);
-        }
+        const bool good = l.valid && fits && seg <= room && !((uint32_t)seg & 15);
+        if (l.valid && !good) a.c.ok(seg, bad);
+        r.row = reinterpret_cast<uint64_t>(a.c.pool) + (good ? seg + l.token * a.c.token_stride : 1);
+        r.exponent = 127;
+        if (row_scales && good) r.exponent = __ldg(a.c.pool + seg + a.c.scale_offset + l.token);
         return r;
     };
     Look one = find();
     find_segments(one);
     Look two = one.any ? find() : Look{};
-    Rows next = find_rows(one);
+    Row next = find_row(one);
     one = two;
     find_segments(one);
     two = one.any ? find() : Look{};
     while (next.any && alive) {
         // the next tile's scales, the addresses of the one after and the block ids
         // of the one after that are loaded meanwhile
-        const Rows now = next;
-        next = find_rows(one);
+        const Row now = next;
+        next = find_row(one);
         one = two;
         find_segments(one);
         two = one.any ? find() : Look{};
@@ -803,11 +829,8 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
             for (uint32_t b = 0; b < S::kQBufs; b++)
                 if ((DP == 256 || both || b == (now.piece & 1)) && !issue_q(b, now.piece)) return false;
         }
-        set_scale(issued, now.exponent[0]);
-        issue(now.row[0]);
-        if (!make_room()) return false;
-        set_scale(issued, now.exponent[1]);
-        issue(now.row[1]);
+        set_scale(now.exponent);
+        issue(now.row);
         if (now.last) {
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.pc_empty[now.piece % kPieces]);
@@ -915,22 +938,12 @@ __device__ __forceinline__ bool multiply(const Args &a, Shared &sh, const uint8_
         bool fresh, second, twice;  // the piece's first; the tile has a second half; lets go of the values for both slots
     };
     Due due = {}, then = {};
-    // A barrier's parity tells a tile from the one before in its place, but not from
-    // earlier ones, which may be the other slot's: so its copy has to have begun,
-    // for which the tile before must have come and gone.
-    uint32_t begun = 0;
-    auto there = [&](uint32_t copy) -> bool {
-        if (begun <= copy) begun = progress(&sh.begun);
-        return begun > copy && mbar_test(&sh.kv_full[copy % S::kStages], copy / S::kStages & 1);
+    uint32_t keys_begun = 0, values_begun = 0;
+    auto there = [&](uint32_t &known, uint32_t copy) -> bool {
+        return has_begun(sh, known, copy) && mbar_test(&sh.kv_full[copy % S::kStages], copy / S::kStages & 1);
     };
-    auto await = [&](uint32_t copy) -> bool {
-        if (begun <= copy) begun = progress(&sh.begun);
-        if (begun <= copy) {
-            const uint64_t t0 = global_ns();
-            for (uint32_t i = 0; (begun = progress(&sh.begun)) <= copy; i++)
-                if (i >= kSpinLimit || global_ns() - t0 > kWaitNs) return false;
-        }
-        return mbar_wait(&sh.kv_full[copy % S::kStages], copy / S::kStages & 1);
+    auto await = [&](uint32_t &known, uint32_t copy) -> bool {
+        return await_begun(sh, known, copy) && mbar_wait(&sh.kv_full[copy % S::kStages], copy / S::kStages & 1);
     };
     auto times_v = [&](uint32_t h) -> bool {  // with the values of a half
         const uint32_t stage = due.v % S::kStages, place = S::kHalves == 2 ? h : done & 1;
@@ -947,7 +960,7 @@ __device__ __forceinline__ bool multiply(const Args &a, Shared &sh, const uint8_
         return true;
     };
     auto finish_most = [&]() -> bool {  // but for the last half
-        if (!await(due.v)) return false;
+        if (!await(values_begun, due.v)) return false;
         if (due.fresh) {
             if (outs && !mbar_wait(&sh.o_free[slot], (outs & 1) ^ 1)) return false;
             outs++;
@@ -987,19 +1000,19 @@ __device__ __forceinline__ bool multiply(const Args &a, Shared &sh, const uint8_
             // (a piece's queries come with its first keys)
             if (started - done == S::kPlaces) {
                 if (!finish_most()) return false;
-                const bool now = both && there(k);
+                const bool now = both && there(keys_begun, k);
                 if (now && !take_turn()) return false;
                 if (!finish_rest()) return false;
                 if (!now) {
-                    while (done != started && !there(k))
+                    while (done != started && !there(keys_begun, k))
                         if (!finish()) return false;
-                    if (!await(k)) return false;
+                    if (!await(keys_begun, k)) return false;
                     if (both && !take_turn()) return false;
                 }
             } else {
-                while (done != started && !there(k))
+                while (done != started && !there(keys_begun, k))
                     if (!finish()) return false;
-                if (!await(k)) return false;
+                if (!await(keys_begun, k)) return false;
                 if (both && !take_turn()) return false;
             }
             tmem_after();
@@ -1224,7 +1237,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
     uint32_t upto = warp_incl_sum(mine);
     if (lane == 31) sh.sums[warp] = upto;
     if (threadIdx.x == 0) {
-        for (uint32_t i = 0; i < S::kStages; i++) mbar_init(&sh.kv_full[i], ES == 2 ? kCopyThreads : kCopyWarps), mbar_init(&sh.kv_empty[i], 2);
+        for (uint32_t i = 0; i < S::kStages; i++) mbar_init(&sh.kv_full[i], ES == 2 ? kKindThreads : kKindWarps), mbar_init(&sh.kv_empty[i], 2);
         for (int i = 0; i < 2; i++) {
             mbar_init(&sh.q_empty[i], 2);
             for (int k = 0; k < 2; k++) mbar_init(&sh.s_full[i][k], 1), mbar_init(&sh.p_full[i][k], 4), mbar_init(&sh.pv_done[i][k], 1);
@@ -1235,7 +1248,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
         for (int i = 0; i < 8; i++) mbar_init(&sh.found[i], 1), mbar_init(&sh.taken[i], kCopyWarps);
         mbar_init(&sh.drained, 2);
         mbar_init(&sh.turn[0], 1), mbar_init(&sh.turn[1], 1);
-        sh.begun = 0;
+        sh.begun[0] = sh.begun[1] = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (__syncthreads_or(disorder)) {  // (groups may overlap: their parts, and all tiles, would be more than there is room for)
