@@ -44,6 +44,9 @@
  *   kvx_attend       attention of one new token per sequence over its pages,
  *                    with a sliding window and sinks, and the attention
  *                    weights added up per token
+ *   kvx_attend_shared  the same for a batch whose sequences share prefixes, each
+ *                    prefix's pages read once
+ *   kvx_read_tokens  tokens of the cache read back into dense 16-bit tensors
  *   kvx_evict        the tokens of a sequence with the most added-up weight
  *                    chosen and copied into fresh pages
  *
@@ -66,7 +69,7 @@
  *     bounded by one second of wall time, after which the kernel ORs
  *     KVX_S_TIMEOUT and returns, and at the hardware barrier of a cluster
  *     (kvx_evict), whose blocks are always resident together; waits within a
- *     block for copies (copies, kvx_attend) are bounded likewise: bad input
+ *     block (copies, kvx_attend, kvx_attend_shared) are bounded likewise: bad input
  *     cannot hang or fault the GPU;
  *     every global access is checked against the capacities passed in.
  *   - Co-scheduling: the grid of a cooperative launch is sized to fit on
@@ -713,7 +716,16 @@ kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t q_stride,
  * values from about 2^100 on may overflow on the way.
  * Results depend on nothing but the arguments and the device's SM count: no
  * atomics.  After KVX_S_TIMEOUT out and lse are unspecified.  Two launches;
- * num_seqs == 0 enqueues nothing.
+ * num_seqs == 0 enqueues nothing.  The sizes refused beside those of kvx_attend:
+ * heads * (2 * num_seqs * group / 256 + num_groups) * blocks_per_prefix * page_tokens
+ * and heads * num_seqs * blocks_per_seq * page_tokens from about 2^37 on.
+ *
+ * Scratch, 16-byte aligned; 0 for arguments it refuses.  It holds partial results
+ * in 32 bits, whatever the lengths will be; for heads of up to 128 values
+ *     2 * group * (num_seqs * heads + SMs) rows for own tokens and
+ *     256 * ((num_seqs * group / 256 + num_groups) * (heads + 2) + 2 * SMs)
+ * for prefixes, of dim + 2 floats each, and half as many rows for wider heads: 57 MB
+ * for 128 sequences of 64 query heads of 128, 8 KV heads and one prefix.
  */
 size_t kvx_attend_shared_workspace_size(const kvx_cache *cache,
                                         uint32_t num_seqs, uint32_t q_heads,

@@ -58,9 +58,10 @@ struct Parts {
 };
 
 // A query's parts by WARPS warps, blocks of kJoinWarps.  Bound by the chain of its
-// reads (group, lengths, which blocks, bases and sums, outputs), so few waves of
-// many warps: one warp a query takes 8192 queries of 7 parts in .. us, four in ..;
-// one query of 300 parts in .. and ...
+// reads (group, lengths, which blocks, bases and sums, outputs), so many warps in
+// one wave: 8192 queries of about seven parts by one warp each 16 us, by four 35;
+// but 8 queries over 131,071 tokens of one KV head, 300 parts each, in all 67 us by
+// one, 41 by four.
 template <class T, uint32_t WARPS>
 __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant__ Args a) {
     __shared__ float sh_m[WARPS > 1 ? kJoinWarps : 1], sh_l[WARPS > 1 ? kJoinWarps : 1];
@@ -235,7 +236,7 @@ bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t bloc
     p.own_cap = wide ? group : 2 * group;
     const uint64_t tiles = num_groups ? queries / p.tile_rows + num_groups : 0;
     p.own_units = (uint64_t)num_seqs * c->heads;
-    const uint64_t most = tiles * c->heads * (ceil_div(prefix, keys) + kExtra) + p.own_units * (ceil_div(len, keys) + kExtra);
+    const uint64_t most = tiles * c->heads * (ceil_div(prefix, kHalf) + kExtra) + p.own_units * (ceil_div(len, keys) + kExtra);
     if (tiles * (c->heads + 2) >= (1ull << 31) || most >= (1ull << 31)) return false;
     const uint64_t want = ceil_div(most, kMinShare);
     p.grid = want < (uint64_t)sm_count() ? (want ? (uint32_t)want : 1) : (uint32_t)sm_count();

@@ -21,7 +21,7 @@ constexpr uint32_t kKindThreads = 32 * kKindWarps;
 constexpr int kPieces = 8;  // descriptors that the walking warp may be ahead
 constexpr uint32_t kHalf = 64;  // keys that a slot's softmax takes at a time
 constexpr uint32_t kRows = 128;  // of a slot: the tensor cores' M, a query row for each lane of tensor memory
-constexpr uint32_t kExtra = 1;   // tiles that a unit's own overhead counts as
+constexpr uint32_t kExtra = 2;   // columns (Region) that a head's own overhead counts as
 constexpr uint32_t kMinShare = 2;
 
 struct Args {
@@ -34,7 +34,7 @@ struct Args {
     FastDiv by_group;
     float scale2;     // |scale| * k_scale * log2(e)
     uint32_t negate;  // scale < 0
-    uint32_t paged16;  // pages are whole groups of 16 tokens
+    uint32_t paged16; // pages are whole groups of 16 tokens
     void *out;
     uint64_t out_stride;
     float *lse;
@@ -79,16 +79,19 @@ __device__ __forceinline__ Entry entry_of(const Args &a, uint32_t i) {
     return e;
 }
 
-// How an entry's work is shared out.  It has heads * len columns, a tile of keys in
+// How an entry's work is shared out.  It has heads * len columns, `keys` keys in
 // one head each (kExtra at a head's start stand for what a part costs beside its
-// keys), and tile_rows query rows at a time make `rows` rows of them.  Blocks of
+// keys), and tile_rows query rows at a time make `rows` rows of them.  Where both
+// slots work on a tile it takes twice the time of one, and makes two columns (128
+// sequences with 2000 shared tokens and one of their own: 76 us with one column,
+// 62 with two).  Blocks of
 // `block` columns, a share each where there are several rows, are gone through row
 // by row: so the blocks that work on different rows of the same columns do so at
 // the same time, and keys and values come from memory once (100,000 tokens, 8
 // heads, 4 rows: 1.71 GB of DRAM reads with the rows one after the other, 0.4 GB
-// so; .. us and ..).
+// so; 382 us and 370).
 struct Region {
-    uint32_t len, width, rows, block;
+    uint32_t keys, len, width, rows, block;
     __host__ __device__ __forceinline__ uint32_t columns(uint32_t b) const {  // of block b
         return width - b * block < block ? width - b * block : block;
     }
@@ -101,7 +104,8 @@ struct Region {
 };
 __host__ __device__ __forceinline__ Region region_of(const Args &a, const Entry &e, uint32_t share, uint32_t keys) {
     Region r;
-    r.len = e.len ? (e.len + keys - 1) / keys + kExtra : 0;
+    r.keys = keys > kHalf && e.rows > kRows ? keys / 2 : keys;
+    r.len = e.len ? (e.len + r.keys - 1) / r.keys + kExtra : 0;
     r.width = a.c.heads * r.len;
     r.rows = (e.rows + a.tile_rows - 1) / a.tile_rows;
     r.block = r.rows > 1 ? share : r.width;
@@ -128,9 +132,10 @@ struct Shape {
     static constexpr uint32_t kTileRows = DP == 256 ? 128 : 256;
     // A slot has room for the logits of 128 keys: of a tile's two halves, or of
     // two tiles.  (Two halves that the tensor cores fill one by one, the next
-    // while the softmax works on the other, take longer: a product with 64 keys
-    // reads as many bytes of the queries as one with 128, and is bound by shared
-    // memory's bandwidth.  100,000 tokens, 4 x 256 rows: 370 and .. us.)
+    // while the softmax works on the other, keep the tensor cores longer: a product
+    // with 64 keys reads as many bytes of the queries as one with 128, and is bound
+    // by shared memory's bandwidth.  100,000 tokens, 4 x 256 rows, the products
+    // alone: 327 us and 233.)
     static constexpr uint32_t kHalves = kKeys / kHalf, kPlaces = 2 / kHalves;
     static constexpr uint32_t kStage = kKeys * DP * 2;  // bytes of a tile of keys or values in 16 bits
     static constexpr uint32_t kQ = kRows * DP * 2;
@@ -213,13 +218,7 @@ __device__ __forceinline__ void copies_wait(uint32_t most) {  // until at most t
         case 0: asm volatile("cp.async.wait_group 0;" ::: "memory"); break;
         case 1: asm volatile("cp.async.wait_group 1;" ::: "memory"); break;
         case 2: asm volatile("cp.async.wait_group 2;" ::: "memory"); break;
-        case 3: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
-        case 4: asm volatile("cp.async.wait_group 4;" ::: "memory"); break;
-        case 5: asm volatile("cp.async.wait_group 5;" ::: "memory"); break;
-        case 6: asm volatile("cp.async.wait_group 6;" ::: "memory"); break;
-        case 7: asm volatile("cp.async.wait_group 7;" ::: "memory"); break;
-        case 8: asm volatile("cp.async.wait_group 8;" ::: "memory"); break;
-        default: asm volatile("cp.async.wait_group 9;" ::: "memory"); break;
+        default: asm volatile("cp.async.wait_group 3;" ::: "memory"); break;
     }
 }
 // What this thread wrote to shared memory, or has seen others write, is there for
@@ -383,8 +382,8 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
             p.row0 = mt * a.tile_rows;
             p.rows = e.rows - p.row0 < a.tile_rows ? e.rows - p.row0 : a.tile_rows;
             p.head = head;
-            p.k0 = t0 * S::kKeys;
-            p.k1 = t1 * S::kKeys < e.len ? t1 * S::kKeys : e.len;
+            p.k0 = t0 * r.keys;
+            p.k1 = t1 * r.keys < e.len ? t1 * r.keys : e.len;
             p.both = DP == 256 || p.rows > kRows;
             p.event = event;
             if (i < a.num_groups) {
@@ -404,7 +403,7 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
         }
         __syncwarp();
         np++;
-        event += t1 - t0;
+        event += ((t1 - t0) * r.keys + S::kKeys - 1) / S::kKeys;
     }
     if (np >= kPieces && !warp_wait(&sh.pc_empty[np % kPieces], (np / kPieces & 1) ^ 1)) return false;
     if (lane == 0) {
@@ -443,8 +442,8 @@ struct Widen<__nv_bfloat16> {
         return nan(v.x) | nan(v.y) | nan(v.z) | nan(v.w);
     }
     // Bytes 0 and 2, by products that shift them by four places and their signs by
-    // four more: the units for logic have half the rate and the most to do (shifts
-    // and masks in their place: .. us against ..).
+    // four more: the units for logic have half the rate and the most to do (a tile's
+    // keys and values 2040 clocks so, 2320 with shifts and masks).
     __device__ __forceinline__ uint32_t two(uint32_t w) const {
         uint32_t v, r;
         asm("mul.lo.u32 %0, %1, 16;" : "=r"(v) : "r"(w));
@@ -979,7 +978,8 @@ __device__ __forceinline__ bool multiply(const Args &a, Shared &sh, const uint8_
     // Where both slots take every tile they take turns: what one gives the tensor
     // cores at a time, the rest of a tile and the next one's logits, is not mixed
     // with the other's.  Mixed, both end together, and both softmaxes want the same
-    // units at the same time while the tensor cores wait (425 us against ..).
+    // units at the same time while the tensor cores wait (100,000
+    // tokens, 4 x 256 rows: 425 us and 368).
     uint32_t turns = 0;
     auto take_turn = [&]() -> bool { return slot ? mbar_wait(&sh.turn[1], turns & 1) : !turns || mbar_wait(&sh.turn[0], (turns & 1) ^ 1); };
     for (uint32_t np = 0;; np++) {
@@ -1103,86 +1103,86 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
             if (!warp_wait(&sh.s_full[slot][tile_place], (S::kPlaces == 2 ? tiles >> 1 : tiles) & 1)) return false;
 #pragma unroll 1
             for (uint32_t h = 0; h < S::kHalves; h++) {
-            const uint32_t place = S::kHalves == 2 ? h : tiles & 1;
-            const uint32_t left = left_tile > h * kHalf ? left_tile - h * kHalf : 0;
-            if (busy && left) {
-                tmem_after();
-                const uint32_t s = s_at + place * kHalf;
-                if (left < kHalf) {  // what lies behind the last key weighs nothing
+                const uint32_t place = S::kHalves == 2 ? h : tiles & 1;
+                const uint32_t left = left_tile > h * kHalf ? left_tile - h * kHalf : 0;
+                if (busy && left) {
+                    tmem_after();
+                    const uint32_t s = s_at + place * kHalf;
+                    if (left < kHalf) {  // what lies behind the last key weighs nothing
 #pragma unroll 1
-                    for (uint32_t c = left & ~15u; c < kHalf; c += 16) {
-                        uint32_t y[16];
-                        tmem_ld16(y, s + c);
-                        tmem_wait_ld(y);
-#pragma unroll
-                        for (int i = 0; i < 16; i++) y[i] = c + i < left ? y[i] : 0xFF800000u;
-                        tmem_st16(s + c, y);
-                    }
-                    tmem_wait_st();
-                }
-                uint32_t x[2][32];
-                tmem_ld32(x[0], s);
-                tmem_ld32(x[1], s + 32);
-                tmem_wait_ld(x[0]);
-                tmem_wait_ld(x[1]);
-                float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-                for (int i = 0; i < 64; i += 8)
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[i / 32][i % 32 + 2 * k]), __uint_as_float(x[i / 32][i % 32 + 2 * k + 1])));
-                top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale2;
-                const bool over = top[0] > limit;
-                if (__any_sync(0xFFFFFFFFu, over)) {
-                    float factor = 1.0f;
-                    if (over) {
-                        const float to = top[0] - kBoost;
-                        factor = limit == -INFINITY ? 0.0f : exp2_fast(base - to);  // 0: nothing was added so far
-                        base = to;
-                        limit = top[0] + kSlack;
-                        sum *= factor;
-                    }
-                    if (!fresh) {
-                        // the product before has to be in the outputs
-                        const uint32_t use = S::kHalves == 2 ? (h ? tiles : tiles - 1) : (tiles - 1) >> 1;
-                        if (!warp_wait(&sh.pv_done[slot][place ^ 1], use & 1)) return false;
-                        tmem_after();
-#pragma unroll 1
-                        for (uint32_t c = 0; c < cols; c += 16) {
+                        for (uint32_t c = left & ~15u; c < kHalf; c += 16) {
                             uint32_t y[16];
-                            tmem_ld16(y, o_at + c);
+                            tmem_ld16(y, s + c);
                             tmem_wait_ld(y);
 #pragma unroll
-                            for (int i = 0; i < 16; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * factor);
-                            tmem_st16(o_at + c, y);
+                            for (int i = 0; i < 16; i++) y[i] = c + i < left ? y[i] : 0xFF800000u;
+                            tmem_st16(s + c, y);
                         }
                         tmem_wait_st();
                     }
-                }
-                const uint64_t shift = pair(-base, -base);
-                uint64_t sums[2] = {};
+                    uint32_t x[2][32];
+                    tmem_ld32(x[0], s);
+                    tmem_ld32(x[1], s + 32);
+                    tmem_wait_ld(x[0]);
+                    tmem_wait_ld(x[1]);
+                    float top[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    uint32_t w[16];
+                    for (int i = 0; i < 64; i += 8)
 #pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        float e0, e1;
-                        unpair(fma2(pair(__uint_as_float(x[h][2 * i]), __uint_as_float(x[h][2 * i + 1])), scale, shift), e0, e1);
-                        e0 = exp2_fast(e0), e1 = exp2_fast(e1);
-                        sums[i & 1] = add2(sums[i & 1], pair(e0, e1));
-                        w[i] = Pair<T>::pack(e0, e1);
+                        for (int k = 0; k < 4; k++)
+                            top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[i / 32][i % 32 + 2 * k]), __uint_as_float(x[i / 32][i % 32 + 2 * k + 1])));
+                    top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale2;
+                    const bool over = top[0] > limit;
+                    if (__any_sync(0xFFFFFFFFu, over)) {
+                        float factor = 1.0f;
+                        if (over) {
+                            const float to = top[0] - kBoost;
+                            factor = limit == -INFINITY ? 0.0f : exp2_fast(base - to);  // 0: nothing was added so far
+                            base = to;
+                            limit = top[0] + kSlack;
+                            sum *= factor;
+                        }
+                        if (!fresh) {
+                            // the product before has to be in the outputs
+                            const uint32_t use = S::kHalves == 2 ? (h ? tiles : tiles - 1) : (tiles - 1) >> 1;
+                            if (!warp_wait(&sh.pv_done[slot][place ^ 1], use & 1)) return false;
+                            tmem_after();
+#pragma unroll 1
+                            for (uint32_t c = 0; c < cols; c += 16) {
+                                uint32_t y[16];
+                                tmem_ld16(y, o_at + c);
+                                tmem_wait_ld(y);
+#pragma unroll
+                                for (int i = 0; i < 16; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * factor);
+                                tmem_st16(o_at + c, y);
+                            }
+                            tmem_wait_st();
+                        }
                     }
-                    tmem_st16(s + h * 16, w);
+                    const uint64_t shift = pair(-base, -base);
+                    uint64_t sums[2] = {};
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        uint32_t w[16];
+#pragma unroll
+                        for (int i = 0; i < 16; i++) {
+                            float e0, e1;
+                            unpair(fma2(pair(__uint_as_float(x[h][2 * i]), __uint_as_float(x[h][2 * i + 1])), scale, shift), e0, e1);
+                            e0 = exp2_fast(e0), e1 = exp2_fast(e1);
+                            sums[i & 1] = add2(sums[i & 1], pair(e0, e1));
+                            w[i] = Pair<T>::pack(e0, e1);
+                        }
+                        tmem_st16(s + h * 16, w);
+                    }
+                    float s0, s1;
+                    unpair(add2(sums[0], sums[1]), s0, s1);
+                    sum += s0 + s1;
+                    tmem_wait_st();
+                    tmem_before();
                 }
-                float s0, s1;
-                unpair(add2(sums[0], sums[1]), s0, s1);
-                sum += s0 + s1;
-                tmem_wait_st();
-                tmem_before();
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&sh.p_full[slot][place]);
-            fresh = false;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&sh.p_full[slot][place]);
+                fresh = false;
             }
         }
         const uint64_t row = p.part_row + (slot && DP != 256 ? p.off_b : 0) + r;
@@ -1213,6 +1213,34 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
     }
 }
 
+// Units are a KV head's query rows of a group (128 or 256 at a time) over the
+// group's prefix, and a sequence's query heads over its own tokens; a block goes
+// through an equal share of all units' columns, piece by piece (Region). For a tile
+// of keys and the 128 rows of a slot
+//     S = Q K^T          128 x keys, in tensor memory
+//     P = 2^(S - base)   in 16 bits, in place of S
+//     O += P V           128 x dim, in tensor memory
+// with tcgen05.mma: queries and tiles come from shared memory (128-byte swizzle), P
+// from tensor memory.  A block has two slots, each with its softmax warps and its
+// issuing thread, so that one's products run beside the other's softmax: of more
+// than 128 rows both take every tile, else they take tiles in turn.  Bases, sums
+// and outputs go to k_join, a row of floats each.
+//
+// Weights are rounded to 16 bits for the second product (as V and the output are):
+// beside the output's own rounding that adds as much again, 1.4 times the error.
+// Their sums are of the unrounded ones.
+//
+// Keys and values are copied by cp.async, 16 bytes at a time: a page may lie at any
+// multiple of 16 bytes, which no tensor map describes.  8-bit rows come to a place
+// of their own and are widened with their scale on the way to the tile.
+//
+// Bound, for many rows, by the softmax and the latency from product to product (a
+// tile takes two slots 2050 clocks of the tensor cores and 3900 in all): 128 x
+// 64 heads over 100,000 tokens of 8 KV heads of 128, bf16, 375 us, 1120 TFLOP/s, 58 %
+// of the measured rate of matrix products, with 490 MB of DRAM reads for 433 MB of
+// cache.  For few rows by the copies: 8 x 16,000 own tokens, bf16, 95 us at 5.5 TB/s;
+// in 8 bits by their widening, for whose 62 instructions per 16 values a tile has
+// too few warps: 132 us at 2.0 TB/s.
 template <class T, int DP, int ES>
 __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ Args a) {
     using S = Shape<DP, ES>;
@@ -1280,7 +1308,7 @@ __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ 
             ok = soften<T, DP, ES>(a, sh, tmem, warp / 4, warp % 4, lane);
         } else if (warp < kSoftWarps + kCopyWarps) {
             ok = copy_tiles<T, DP, ES>(a, sh, q_smem, ring, held, threadIdx.x - 32 * kSoftWarps, bad);
-            copies_wait(0);
+            asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (warp == kLookWarp) {
             if (a.paged16) ok = look_up<DP, ES>(a, sh, lane, bad);
         } else {
