@@ -9,7 +9,7 @@ There is no fallback: if the library is missing, loading raises.
 torch, sized from the library's capacity and workspace queries) and runs the
 five calls in order on one stream, with no host synchronisation in between.
 ``Cache`` describes one layer's paged cache in a pool and runs the operators
-that a decoding server applies to it: append, attend, evict.
+that a decoding server applies to it: append, read, attend, attend_shared, evict.
 """
 from __future__ import annotations
 
