@@ -610,7 +610,8 @@ typedef struct kvx_cache {
  *                  negative slot writes nothing into the cache (its query is
  *                  computed all the same); one beyond the cache's blocks
  *                  raises KVX_S_BOUNDS likewise.  Two tokens with the same
- *                  slot leave either one's bytes.
+ *                  slot leave either one's bytes (with row scales perhaps one's
+ *                  values under the other's scale).
  *   q_out          [T][q_heads][dim] of `dtype`, tokens q_out_stride elements
  *                  apart.  It may be q itself (with the same stride).
  * Pointers and strides of q, k, v, q_out, the weights and cos_sin keep 16-byte
@@ -707,6 +708,7 @@ kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t q_stride,
  *   prefix_blocks  [num_groups][blocks_per_prefix] uint32.
  *   prefix_lens    [num_groups] uint32; like lens, one that exceeds its pages
  *                  raises KVX_S_BOUNDS and counts as full pages.
+ * Tokens of a page or segment that the cache's rules exclude count as zeros.
  * Keys and values enter the tensor cores in `dtype`: 16-bit ones as they are,
  * 8-bit ones exactly (row-scaled ones in fp16 rounded to it, where they are
  * under 2^-14 or from 65520 on).  Logits, softmax and sums are held in 32 bits;

@@ -598,7 +598,7 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
                     *reinterpret_cast<uint4 *>(to + (at ^ 16)) = make_uint4(x2.x, x2.y, x3.x, x3.y);
                 }
             }
-            if (odd | (check & 0x80808080u)) {
+            if (in && (odd | (check & 0x80808080u))) {  // (pieces behind a row's end are whatever was there)
 #pragma unroll 1
                 for (uint32_t c = 0; c < kCopies; c++) {
                     const uint4 raw = from[c * kKindThreads];

@@ -576,6 +576,44 @@ def test_attend_bad_tables():
         p.check(*p.run())
 
 
+@pytest.mark.parametrize("act,store", [(BF, BF), (BF, "rows"), (FP, E4)])
+@pytest.mark.parametrize("page", [16, 7])
+def test_attend_bad_pages_are_zeros(act, store, page):
+    p = Problem(act, store, firsts=[0, 3], prefixes=[100], lens=[40, 5, 0, 70], G=4, H=2, D=80, page=page)
+    own, prefix = int(p.blocks[3, 1]), int(p.prefix_blocks[0, 2])
+    args = list(p.args())
+    args[0], args[3] = args[0].clone(), args[3].clone()
+    args[0][0, 2], args[3][3, 1] = p.cache.addr.shape[0], 2 ** 31 - 1
+    got = [x.clone() for x in p.run(args=args)]
+    assert p.cache.read_status() == kvx.S_BOUNDS
+    p.cache.status.zero_()
+    for b in (own, prefix):
+        for x in p.c.stored:
+            x[b] = 0
+    p.pool.copy_(p.c.pool())
+    want = p.run()
+    assert p.cache.read_status() == 0
+    for x, y in zip(want, got):
+        assert torch.equal(x, y)
+
+
+@pytest.mark.parametrize("dim", [48, 80, 96, 160])
+def test_attend_what_lies_behind_rows_of_odd_widths(dim):
+    """Nothing of it enters: NaN and large values between the rows."""
+    p = Problem(BF, "rows", firsts=[0, 3], prefixes=[300], lens=[40, 5, 0, 270], G=4, H=2, D=dim, page=16)
+    want = [x.clone() for x in p.run()]
+    p.check(*want)
+    # the same call behind one that leaves NaN in all that shared memory may keep
+    other = Problem(BF, "rows", firsts=[0, 3], prefixes=[4000], lens=[400] * 4, G=4, H=2, D=256 if dim > 128 else 128, page=16)
+    for x in other.c.stored:
+        x.fill_(math.nan)
+    other.pool.copy_(other.c.pool())
+    for _ in range(3):
+        other.run()
+        for x, y in zip(want, p.run()):
+            assert torch.equal(x, y)
+
+
 def test_attend_beyond_32_bits():
     """A pool of more than 4 GB, the pages at its end."""
     for store in (BF, "rows"):
