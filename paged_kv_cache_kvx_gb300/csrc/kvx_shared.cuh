@@ -19,6 +19,7 @@ constexpr int kThreads = 32 * kWarps;
 constexpr uint32_t kKindWarps = kCopyWarps / 2;  // that copy keys; the others copy values
 constexpr uint32_t kKindThreads = 32 * kKindWarps;
 constexpr int kPieces = 8;  // descriptors that the walking warp may be ahead
+constexpr uint32_t kFewRows = 16;  // up to so many, four lanes share a row of logits (soften_few)
 constexpr uint32_t kHalf = 64;  // keys that a slot's softmax takes at a time
 constexpr uint32_t kRows = 128;  // of a slot: the tensor cores' M, a query row for each lane of tensor memory
 constexpr uint32_t kExtra = 2;   // columns (Region) that a head's own overhead counts as
@@ -118,11 +119,17 @@ __host__ __device__ __forceinline__ uint32_t group_parts(const Args &a, uint32_t
     return start / share + ((uint32_t)((uint64_t)first_seq * a.group / a.tile_rows) + g) * (a.c.heads + 2);
 }
 
+// Where among the 128 rows a slot's few ones lie, which says which of its warps works:
+// the two slots' not on the same scheduler (59 us on one, 56 on two, neither an
+// issuing warp's).
+__host__ __device__ __forceinline__ constexpr uint32_t few_at(uint32_t slot) { return 64 + 32 * slot; }
+
 // A part of a unit that one block works on.
 struct Piece {
     const uint32_t *table;                    // its pages
     uint32_t seq0, row0, rows, head, k0, k1;  // query rows row0 .. row0 + rows-1 of seq0's group on; 0 rows end the stream
     uint32_t both, event;                     // both slots take every tile, or tiles in turn: slot `event` & 1 the first
+    uint32_t few;                             // no more than kFewRows rows
     uint32_t part_row, off_b;                 // of the partial result
 };
 
@@ -246,6 +253,37 @@ __device__ __forceinline__ bool elected() {
     uint32_t ok;
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(ok));
     return ok != 0;
+}
+// 16 rows of 8 * N columns: a lane has columns 2 * (lane % 4) and the next, of every
+// eight, of rows lane / 4 (the first two of four values) and lane / 4 + 8.
+__device__ __forceinline__ void tmem_ld_rows64(uint32_t (&r)[32], uint32_t at) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, %17, "
+        "%18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]), "=r"(r[9]),
+          "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]), "=r"(r[27]),
+          "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(at));
+}
+__device__ __forceinline__ void tmem_ld_rows16(uint32_t (&r)[8], uint32_t at) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+                 : "r"(at));
+}
+__device__ __forceinline__ void tmem_st_rows16(uint32_t at, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x256b.x2.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(at), "r"(r[0]), "r"(r[1]),
+                 "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// 16 rows of 32 columns: a lane has column lane % 4 of every four, of rows lane / 4
+// and lane / 4 + 8.
+__device__ __forceinline__ void tmem_st_rows32(uint32_t at, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16};" ::"r"(at),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
 }
 // Operands by the low words of their descriptors (Operand); d += or, without
 // `add`, d = a b.
@@ -385,6 +423,7 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
             p.k0 = t0 * r.keys;
             p.k1 = t1 * r.keys < e.len ? t1 * r.keys : e.len;
             p.both = DP == 256 || p.rows > kRows;
+            p.few = p.rows <= kFewRows;
             p.event = event;
             if (i < a.num_groups) {
                 p.table = a.prefix_blocks + (uint64_t)i * a.blocks_per_prefix;
@@ -685,9 +724,11 @@ __device__ __forceinline__ bool copy_tiles(const Args &a, Shared &sh, uint8_t *q
             const uint32_t r = j / kQParts, part = j % kQParts;
             const uint32_t rr = p.row0 + r0 + r, s = a.by_group.div(rr);
             const uint64_t from = (uint64_t)(p.seq0 + s) * a.q_stride + (uint64_t)(p.head * a.group + rr - s * a.group) * a.c.dim;
-            if (part < q_parts)
-                copy16(base + (part / 8) * (kRows * 128) + r * 128 + ((part % 8 ^ (r & 7)) * 16),
-                       static_cast<const T *>(a.q) + from + part * 8, true);
+            const uint32_t to = base + (part / 8) * (kRows * 128) + r * 128 + ((part % 8 ^ (r & 7)) * 16);
+            if (part < q_parts) {
+                copy16(to + (p.few ? few_at(0) * 128 : 0), static_cast<const T *>(a.q) + from + part * 8, true);
+                if (p.few) copy16(to + few_at(1) * 128, static_cast<const T *>(a.q) + from + part * 8, true);
+            }
         }
         return true;
     };
@@ -1070,15 +1111,160 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
+// Weights are 2^(logit - base).  The base follows the running maximum only when
+// a logit exceeds it by more than kSlack + kBoost: sums and outputs are
+// divided by the same power in the end.  It lies kBoost below that maximum,
+// so that in fp16, whose smallest step is 2^-24, small weights keep some
+// bits more beside a large one.
+constexpr float kSlack = 8.0f;
+template <class T>
+constexpr float kBoost = std::is_same<T, __half>::value ? 7.0f : 0.0f;
+struct Running {  // a row's
+    float base, limit, sum;
+    // What sums and outputs are to be multiplied by where a larger maximum has come.
+    __device__ __forceinline__ float follow(float top, float boost) {
+        const float to = top - boost, factor = limit == -INFINITY ? 0.0f : exp2_fast(base - to);  // 0: nothing was added so far
+        base = to;
+        limit = top + kSlack;
+        sum *= factor;
+        return factor;
+    }
+};
+
+// soften's part for a piece of at most kFewRows rows.  One warp of a slot has them all,
+// and a lane 32 logits of a row (of a tile with 128 keys) and, with more than eight
+// rows, of another: its four lanes are of one mind.  With a row a lane, as in soften,
+// 24 lanes of 32 idle over eight rows (48 sequences of up to 8000 tokens, 8-bit rows,
+// 8 heads of 64: 72 us, and 53 so).  A loop of its own, whose registers soften's does
+// not spill (100,000 tokens behind 4 x 256 rows 386 us in one loop, 373 in two).
+template <class T, int DP, int ES>
+__device__ __forceinline__ bool soften_few(Shared &sh, uint32_t s_at, uint32_t o_at, uint32_t slot, bool mine, uint32_t t, uint32_t tiles,
+                                        uint32_t keys, uint32_t step, uint32_t rows, uint32_t cols, float scale2, float *part_o,
+                                        float2 *part_ml, uint32_t dim) {
+    using S = Shape<DP, ES>;
+    constexpr int kN = S::kKeys / kHalf;
+    const uint32_t lane = threadIdx.x & 31, nt = (keys + S::kKeys - 1) / S::kKeys;
+    const uint64_t scale = pair(scale2, scale2);
+    const bool more = rows > 8, any = t < nt;
+    Running run[2] = {{0, -INFINITY, 0}, {0, -INFINITY, 0}};
+    bool fresh = true;
+    for (; t < nt; t += step, tiles++) {
+        const uint32_t left_tile = keys - t * S::kKeys, tile_place = S::kPlaces == 2 ? tiles & 1 : 0;
+        if (!warp_wait(&sh.s_full[slot][tile_place], (S::kPlaces == 2 ? tiles >> 1 : tiles) & 1)) return false;
+        if (mine) {
+            const uint32_t s = s_at + (S::kPlaces == 2 ? tile_place * kHalf : 0);
+            uint32_t x[kN][32];
+            tmem_after();
+#pragma unroll
+            for (int n = 0; n < kN; n++) tmem_ld_rows64(x[n], s + n * kHalf);
+#pragma unroll
+            for (int n = 0; n < kN; n++) tmem_wait_ld(x[n]);
+            if (left_tile < S::kKeys) {
+#pragma unroll
+                for (int n = 0; n < kN; n++)
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        if (n * kHalf + i / 4 * 8 + lane % 4 * 2 + i % 2 >= left_tile) x[n][i] = 0xFF800000u;
+            }
+            float factor[2] = {1.0f, 1.0f};
+            bool over = false;
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                if (k && !more) break;
+                float tops[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                for (int n = 0; n < kN; n++)
+#pragma unroll
+                    for (int i = 0; i < 8; i++)
+                        tops[i % 4] = fmaxf(tops[i % 4], fmaxf(__uint_as_float(x[n][4 * i + 2 * k]), __uint_as_float(x[n][4 * i + 2 * k + 1])));
+                float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3]));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xFFFFFFFFu, top, 2)) * scale2;
+                if (lane / 4 + 8 * k < rows && top > run[k].limit) factor[k] = run[k].follow(top, kBoost<T>), over = true;
+            }
+            if (__any_sync(0xFFFFFFFFu, over) && !fresh) {
+                // the product before has to be in the outputs: with one place for
+                // logits it came before this tile's first one
+                if (S::kPlaces == 2 && !warp_wait(&sh.pv_done[slot][tile_place ^ 1], (tiles - 1) >> 1 & 1)) return false;
+                tmem_after();
+#pragma unroll 1
+                for (uint32_t c = 0; c < cols; c += 16) {
+                    uint32_t y[8];
+                    tmem_ld_rows16(y, o_at + c);
+                    tmem_wait_ld(y);
+#pragma unroll
+                    for (int i = 0; i < 8; i++) y[i] = __float_as_uint(__uint_as_float(y[i]) * factor[i / 2 % 2]);
+                    tmem_st_rows16(o_at + c, y);
+                }
+                tmem_wait_st();
+            }
+            uint32_t w[kN][16] = {};
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                if (k && !more) break;
+                const uint64_t shift = pair(-run[k].base, -run[k].base);
+                uint64_t sums[2] = {};
+#pragma unroll
+                for (int n = 0; n < kN; n++)
+#pragma unroll
+                    for (int i = 0; i < 8; i++) {
+                        float e0, e1;
+                        unpair(fma2(pair(__uint_as_float(x[n][4 * i + 2 * k]), __uint_as_float(x[n][4 * i + 2 * k + 1])), scale, shift), e0, e1);
+                        e0 = exp2_fast(e0), e1 = exp2_fast(e1);
+                        sums[i & 1] = add2(sums[i & 1], pair(e0, e1));
+                        w[n][2 * i + k] = Pair<T>::pack(e0, e1);
+                    }
+                float s0, s1;
+                unpair(add2(sums[0], sums[1]), s0, s1);
+                run[k].sum += s0 + s1;
+            }
+#pragma unroll
+            for (int n = 0; n < kN; n++) tmem_st_rows32(s + n * kHalf, w[n]);
+            tmem_wait_st();
+            tmem_before();
+        }
+        __syncwarp();
+        if (lane < S::kHalves) mbar_arrive(&sh.p_full[slot][S::kHalves == 2 ? lane : tile_place]);
+        fresh = false;
+    }
+    if (any) {
+        const uint32_t last = tiles - 1;
+        if (!warp_wait(&sh.pv_done[slot][S::kHalves == 2 ? 1 : last & 1], (S::kHalves == 2 ? last : last >> 1) & 1)) return false;
+        if (mine) {
+            tmem_after();
+#pragma unroll 1
+            for (uint32_t c = 0; c < cols; c += 16) {
+                uint32_t y[8];
+                tmem_ld_rows16(y, o_at + c);
+                tmem_wait_ld(y);
+#pragma unroll
+                for (int i = 0; i < 8; i += 2) {
+                    const uint32_t x = lane / 4 + i / 2 % 2 * 8;
+                    if (x < rows)
+                        *reinterpret_cast<uint2 *>(part_o + (uint64_t)x * dim + c + i / 4 * 8 + lane % 4 * 2) = make_uint2(y[i], y[i + 1]);
+                }
+            }
+            tmem_before();
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.o_free[slot]);
+    }
+    if (mine && part_ml) {
+#pragma unroll
+        for (int k = 0; k < 2; k++) {
+            float l = any ? run[k].sum : 0.0f;
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 1);
+            l += __shfl_xor_sync(0xFFFFFFFFu, l, 2);
+            const uint32_t x = lane / 4 + 8 * k;
+            if (lane % 4 == 0 && x < rows) part_ml[x] = make_float2(run[k].base, l);
+        }
+    }
+    return true;
+}
+
 template <class T, int DP, int ES>
 __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem, uint32_t slot, uint32_t warp, uint32_t lane) {
     using S = Shape<DP, ES>;
-    // Weights are 2^(logit - base).  The base follows the running maximum only when
-    // a logit exceeds it by more than kSlack + kBoost: sums and outputs are
-    // divided by the same power in the end.  It lies kBoost below that maximum,
-    // so that in fp16, whose smallest step is 2^-24, small weights keep some
-    // bits more beside a large one.
-    constexpr float kSlack = 8.0f, kBoost = std::is_same<T, __half>::value ? 7.0f : 0.0f;
     const uint32_t r = warp * 32 + lane;  // row of the slot
     const uint32_t lanes = (warp * 32) << 16;
     const uint32_t s_at = tmem + lanes + slot * 128, o_at = tmem + lanes + 256 + slot * 128;
@@ -1096,8 +1282,19 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
         const bool busy = first_row + warp * 32 < p.rows, mine = first_row + r < p.rows;
         uint32_t t = both ? 0 : (p.event & 1) ^ slot;
         const bool any = t < nt;
-        float base = 0, limit = -INFINITY, sum = 0;
+        if (p.few) {
+            const uint32_t step = both ? 1 : 2;
+            const uint64_t row = p.part_row + (slot && DP != 256 ? p.off_b : 0);
+            if (!soften_few<T, DP, ES>(sh, s_at, o_at, slot, warp == few_at(slot) / 32, t, tiles, keys, step, p.rows, cols, a.scale2,
+                                       a.part_o + row * a.c.dim + col, DP == 256 && slot ? nullptr : a.part_ml + row, a.c.dim))
+                return false;
+            if (any) tiles += (nt - t + step - 1) / step;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sh.pc_empty[np % kPieces]);
+            continue;
+        }
         bool fresh = true;
+        Running run = {0, -INFINITY, 0};
         for (; t < nt; t += both ? 1 : 2, tiles++) {
             const uint32_t left_tile = keys - t * S::kKeys, tile_place = S::kPlaces == 2 ? tiles & 1 : 0;
             if (!warp_wait(&sh.s_full[slot][tile_place], (S::kPlaces == 2 ? tiles >> 1 : tiles) & 1)) return false;
@@ -1132,16 +1329,9 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
                         for (int k = 0; k < 4; k++)
                             top[k] = fmaxf(top[k], fmaxf(__uint_as_float(x[i / 32][i % 32 + 2 * k]), __uint_as_float(x[i / 32][i % 32 + 2 * k + 1])));
                     top[0] = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * a.scale2;
-                    const bool over = top[0] > limit;
+                    const bool over = top[0] > run.limit;
                     if (__any_sync(0xFFFFFFFFu, over)) {
-                        float factor = 1.0f;
-                        if (over) {
-                            const float to = top[0] - kBoost;
-                            factor = limit == -INFINITY ? 0.0f : exp2_fast(base - to);  // 0: nothing was added so far
-                            base = to;
-                            limit = top[0] + kSlack;
-                            sum *= factor;
-                        }
+                        const float factor = over ? run.follow(top[0], kBoost<T>) : 1.0f;
                         if (!fresh) {
                             // the product before has to be in the outputs
                             const uint32_t use = S::kHalves == 2 ? (h ? tiles : tiles - 1) : (tiles - 1) >> 1;
@@ -1159,7 +1349,7 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
                             tmem_wait_st();
                         }
                     }
-                    const uint64_t shift = pair(-base, -base);
+                    const uint64_t shift = pair(-run.base, -run.base);
                     uint64_t sums[2] = {};
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
@@ -1176,7 +1366,7 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
                     }
                     float s0, s1;
                     unpair(add2(sums[0], sums[1]), s0, s1);
-                    sum += s0 + s1;
+                    run.sum += s0 + s1;
                     tmem_wait_st();
                     tmem_before();
                 }
@@ -1207,7 +1397,7 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
             __syncwarp();
             if (lane == 0) mbar_arrive(&sh.o_free[slot]);
         }
-        if (mine && (DP != 256 || !slot)) a.part_ml[row] = make_float2(base, any ? sum : 0.0f);
+        if (mine && (DP != 256 || !slot)) a.part_ml[row] = make_float2(run.base, any ? run.sum : 0.0f);
         __syncwarp();
         if (lane == 0) mbar_arrive(&sh.pc_empty[np % kPieces]);
     }
