@@ -360,6 +360,24 @@ def test_attend_rising_logits():
         p.check(*p.run())
 
 
+@pytest.mark.parametrize("act,store,G,D,n", [(BF, BF, 1, 128, 48), (BF, "rows", 8, 128, 48), (FP, FP, 9, 64, 48), (BF, E4, 16, 64, 48),
+                                             (FP, "rows", 17, 64, 48), (BF, BF, 8, 256, 24), (FP, FP, 16, 160, 24)])
+def test_attend_rising_logits_of_few_rows(act, store, G, D, n):
+    """Up to 16 rows, and 17, over many tiles of a piece, the last of every kind; every other row rises, the others fall."""
+    lens = [2500 - 37 * i for i in range(n)]
+    p = Problem(act, store, [0], [], lens, G, 1, D, 16, v_mean=0.0 if store == "rows" else 0.5)
+    k = p.c.stored[0]
+    for i, length in enumerate(lens):
+        pos = torch.arange(length)
+        b = p.blocks[i].long()[pos // 16]
+        rise = torch.linspace(0, 20, length)[:, None]
+        k[b, 0, pos % 16] = k[b, 0, pos % 16] * 0.2 + rise * (1 if store in (BF, FP) else 4)
+    p.q = p.q.abs()
+    p.q[:, 1::2] *= -1
+    p.pool.copy_(p.c.pool())
+    p.check(*p.run())
+
+
 def test_attend_many_small_weights():
     """One key with all but a little of the weight and many with the rest: 20,000 keys of 2^-22 of the largest."""
     for act in (BF, FP):
