@@ -61,11 +61,14 @@ struct Parts {
 // reads (group, lengths, which blocks, bases and sums, outputs), so many warps in
 // one wave: 8192 queries of about seven parts by one warp each 16 us, by four 35;
 // but 8 queries over 131,071 tokens of one KV head, 300 parts each, in all 67 us by
-// one, 41 by four.
-template <class T, uint32_t WARPS>
-__global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant__ Args a) {
+// one, 41 by four.  For the same reason heads of up to 128 have kernels of their own,
+// with 72 registers for 88: 28 warps an SM (8192 queries, 100,000 shared tokens, in all
+// 372 us with 88, 368 with 72, 369 with 64, which spills; 32,768 of one piece 84 and 78).
+template <class T, uint32_t WARPS, bool WIDE>
+__global__ void __launch_bounds__(32 * kJoinWarps, WIDE ? 5 : 7) k_join(const __grid_constant__ Args a) {
     __shared__ float sh_m[WARPS > 1 ? kJoinWarps : 1], sh_l[WARPS > 1 ? kJoinWarps : 1];
-    __shared__ float4 sh_o[WARPS > 1 ? kJoinWarps : 1][WARPS > 1 ? 64 : 1];
+    constexpr int kQuads = WIDE ? 2 : 1;  // four outputs that a lane has, and those 128 further
+    __shared__ float4 sh_o[WARPS > 1 ? kJoinWarps : 1][WARPS > 1 ? 32 * kQuads : 1];
     const uint32_t lane = threadIdx.x & 31, warp = threadIdx.x / 32, turn = warp % WARPS;
     const uint64_t query = (uint64_t)blockIdx.x * (kJoinWarps / WARPS) + warp / WARPS;
     const bool has = query < (uint64_t)a.num_seqs * a.q_heads;
@@ -80,7 +83,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
         else
             hi = mid;
     }
-    const bool wide = a.c.dim > 128;
+    constexpr bool wide = WIDE;
     const uint32_t keys = wide ? 64 : 128;
     Parts parts[2] = {};
     uint2 const *where[2] = {};
@@ -135,7 +138,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
     // A warp's share, 32 parts at a time: a lane has one's base and sum; 0 stands
     // for none, whose outputs do not exist.
     float top = -INFINITY, sum = 0;
-    float4 o[2] = {};
+    float4 o[kQuads] = {};
     for (uint32_t i0 = turn * 32; i0 < all; i0 += 32 * WARPS) {
         const uint32_t here = all - i0 < 32 ? all - i0 : 32;
         float2 ml = make_float2(-INFINITY, 0);
@@ -154,9 +157,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
         for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(0xFFFFFFFFu, s, d);
         sum = sum * old + s;
 #pragma unroll
-        for (int k = 0; k < 2; k++) o[k].x *= old, o[k].y *= old, o[k].z *= old, o[k].w *= old;
+        for (int k = 0; k < kQuads; k++) o[k].x *= old, o[k].y *= old, o[k].z *= old, o[k].w *= old;
         for (uint32_t i = 0; i < here; i += kJoinUnroll) {
-            float4 v[kJoinUnroll][2] = {};
+            float4 v[kJoinUnroll][kQuads] = {};
             float f[kJoinUnroll];
 #pragma unroll
             for (int u = 0; u < kJoinUnroll; u++) {
@@ -164,13 +167,13 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
                 const float *from = a.part_o + (uint64_t)__shfl_sync(0xFFFFFFFFu, row, i + u) * a.c.dim;
                 if (f[u] == 0) continue;  // (a NaN is none)
 #pragma unroll
-                for (int k = 0; k < 2; k++)
+                for (int k = 0; k < kQuads; k++)
                     if (k * 128 + lane * 4 < a.c.dim) v[u][k] = __ldcg(reinterpret_cast<const float4 *>(from + k * 128) + lane);
             }
 #pragma unroll
             for (int u = 0; u < kJoinUnroll; u++)
 #pragma unroll
-                for (int k = 0; k < 2; k++) {
+                for (int k = 0; k < kQuads; k++) {
                     o[k].x += v[u][k].x * f[u], o[k].y += v[u][k].y * f[u];
                     o[k].z += v[u][k].z * f[u], o[k].w += v[u][k].w * f[u];
                 }
@@ -179,19 +182,19 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
     if constexpr (WARPS > 1) {
         if (lane == 0) sh_m[warp] = top, sh_l[warp] = sum;
 #pragma unroll
-        for (int k = 0; k < 2; k++) sh_o[warp][k * 32 + lane] = o[k];
+        for (int k = 0; k < kQuads; k++) sh_o[warp][k * 32 + lane] = o[k];
         __syncthreads();
         if (turn) return;
         top = -INFINITY, sum = 0;
         for (uint32_t k = 0; k < WARPS; k++) top = fmaxf(top, sh_m[warp + k]);
 #pragma unroll
-        for (int h = 0; h < 2; h++) o[h] = make_float4(0, 0, 0, 0);
+        for (int h = 0; h < kQuads; h++) o[h] = make_float4(0, 0, 0, 0);
         for (uint32_t k = 0; k < WARPS; k++) {
             const float f = sh_m[warp + k] == -INFINITY ? 0.0f : exp2_fast(sh_m[warp + k] - top);
             if (f == 0) continue;
             sum += sh_l[warp + k] * f;
 #pragma unroll
-            for (int h = 0; h < 2; h++) {
+            for (int h = 0; h < kQuads; h++) {
                 const float4 v = sh_o[warp + k][h * 32 + lane];
                 o[h].x += v.x * f, o[h].y += v.y * f, o[h].z += v.z * f, o[h].w += v.w * f;
             }
@@ -200,7 +203,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
     if (!has) return;
     const float inv = sum == 0 ? 0.0f : a.c.v_scale / sum;
 #pragma unroll
-    for (int k = 0; k < 2; k++) {
+    for (int k = 0; k < kQuads; k++) {
         const uint32_t d = k * 128 + lane * 4;
         if (d >= a.c.dim) continue;
         T *to = static_cast<T *>(a.out) + (uint64_t)n * a.out_stride + (uint64_t)x * a.c.dim + d;
@@ -208,6 +211,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) k_join(const __grid_constant_
             make_uint2(Pair<T>::pack(o[k].x * inv, o[k].y * inv), Pair<T>::pack(o[k].z * inv, o[k].w * inv));
     }
     if (a.lse && lane == 0) a.lse[query] = sum == 0 ? -INFINITY : (top + log2f(sum)) * 0.6931471805599453f;
+}
+
+template <class T>
+cudaError_t launch_join(const cudaLaunchConfig_t &cfg, bool four, bool wide, const Args &a) {
+    return wide ? cudaLaunchKernelEx(&cfg, four ? k_join<T, 4, true> : k_join<T, 1, true>, a)
+                : cudaLaunchKernelEx(&cfg, four ? k_join<T, 4, false> : k_join<T, 1, false>, a);
 }
 
 // Sizes of the call, known on the host: the lengths are not, so every bound is the tables'.
@@ -322,8 +331,7 @@ extern "C" kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q, u
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    const cudaError_t e = dtype == KVX_BF16 ? cudaLaunchKernelEx(&cfg, four ? k_join<__nv_bfloat16, 4> : k_join<__nv_bfloat16, 1>, a)
-                                            : cudaLaunchKernelEx(&cfg, four ? k_join<__half, 4> : k_join<__half, 1>, a);
+    const cudaError_t e = dtype == KVX_BF16 ? launch_join<__nv_bfloat16>(cfg, four, cache->dim > 128, a) : launch_join<__half>(cfg, four, cache->dim > 128, a);
     if (e != cudaSuccess) return KVX_ECUDA;
     KVX_LAUNCHED();
     return KVX_OK;
