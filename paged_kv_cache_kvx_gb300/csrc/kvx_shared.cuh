@@ -1426,7 +1426,7 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
 //
 // Bound, for many rows, by the softmax and the latency from product to product (a
 // tile takes two slots 2050 clocks of the tensor cores and 3900 in all): 128 x
-// 64 heads over 100,000 tokens of 8 KV heads of 128, bf16, 373 us, 1130 TFLOP/s, 58 %
+// 64 heads over 100,000 tokens of 8 KV heads of 128, bf16, 368 us, 1140 TFLOP/s, 59 %
 // of the measured rate of matrix products, with 490 MB of DRAM reads for 433 MB of
 // cache.  For few rows by the copies: 8 x 16,000 own tokens, bf16, 91 us at 5.8 TB/s;
 // in 8 bits by their widening, 62 instructions per 16 values, and a tile's chain:
