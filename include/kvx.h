@@ -752,7 +752,8 @@ kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q,
  * starts[n+1] - 1 of k_out and v_out get the keys and values, in all heads, of
  * sequence n's tokens first[n], first[n] + 1, ...  16-bit caches are copied;
  * 8-bit values are multiplied by their scale (k_scale and v_scale, or the
- * row's) and rounded once to `dtype`, to the nearest even.
+ * row's) and the product is rounded once to `dtype`, to the nearest even (one
+ * under 2^-122, which bf16 reaches, to 32 bits before).
  *
  *   blocks         [num_seqs][blocks_per_seq] uint32, as for kvx_attend; only
  *                  entries of pages that hold tokens to be read are read.

@@ -1,7 +1,9 @@
 // kvx_read_tokens: tokens of a paged cache read back into dense 16-bit tensors.
 //
-// out[t] = stored * scale, rounded once: the product of an 8-bit value and a
-// scale is taken in 32 bits.  A warp takes one token, whose sequence, page and
+// out[t] = stored * scale, rounded once: 32 bits hold the product of an 8-bit value
+// and a power of two, or any scale of up to 20 bits; that with a longer one, up to
+// 28 bits, is cut off to 32 so that rounding it to 16 gives what rounding the
+// product itself would (scaled_odd).  A warp takes one token, whose sequence, page and
 // segment addresses it looks up once for all heads; a lane takes 16 stored bytes
 // at a time and writes 16-bit ones as whole sectors.
 //
@@ -58,19 +60,34 @@ __device__ __forceinline__ uint32_t rank_of(const uint32_t *starts, uint32_t cou
     return lo + __popc(__ballot_sync(0xFFFFFFFFu, lane < count && __ldg(starts + lo + lane) <= t));
 }
 
+// x * scale cut off, with the last bit set where anything was lost: no border or
+// middle of 16-bit values lies between this and the product.  Rounded to 32 bits it
+// could become such a middle (1.125 * 0x1.d38e38p-1: 1.03125 in bf16 by way of 32
+// bits, 1.0234375 is nearer).  The remainder is exact from 2^-122 on.
+__device__ __forceinline__ float scaled_odd(float x, float scale) {
+    const float p = __fmul_rz(x, scale);
+    return fmaf(x, scale, -p) == 0 ? p : __uint_as_float(__float_as_uint(p) | 1);
+}
+
 // Four stored 8-bit values times a scale, as 16-bit ones.
-template <class T>
+template <class T, bool LONG>
 __device__ __forceinline__ uint2 scaled4(uint32_t four, float scale) {
     uint32_t lo, hi;
     asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
         : "=r"(lo), "=r"(hi)
         : "r"(four));
     const float2 x = Pair<__half>::unpack(lo), y = Pair<__half>::unpack(hi);
+    if constexpr (LONG)
+        return make_uint2(Pair<T>::pack(scaled_odd(x.x, scale), scaled_odd(x.y, scale)),
+                          Pair<T>::pack(scaled_odd(y.x, scale), scaled_odd(y.y, scale)));
     return make_uint2(Pair<T>::pack(x.x * scale, x.y * scale), Pair<T>::pack(y.x * scale, y.y * scale));
 }
 
-template <class T, bool FP8>
+enum Store { kSame, kScaled, kScaledLong };  // the outputs' type; e4m3; e4m3 with a scale of more than 20 bits
+
+template <class T, Store STORE>
 __global__ void __launch_bounds__(32 * kWarps, kBlocks) k_read(const __grid_constant__ ReadArgs a) {
+    constexpr bool FP8 = STORE != kSame, LONG = STORE == kScaledLong;
     constexpr int kUnroll = FP8 ? 2 : 4;  // pieces of a lane on their way
     const uint32_t lane = threadIdx.x & 31;
     const uint32_t t = blockIdx.x * kWarps + threadIdx.x / 32;
@@ -119,8 +136,8 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) k_read(const __grid_cons
                         T *o = static_cast<T *>(a.out[kv]) + t * a.stride[kv] + (uint64_t)head * a.c.dim + piece[u] * (FP8 ? 16 : 8);
                         if constexpr (FP8) {
                             const float scale = a.c.scale_offset ? row_scale(e[u]) : kv ? a.c.v_scale : a.c.k_scale;
-                            const uint2 w0 = scaled4<T>(raw[u].x, scale), w1 = scaled4<T>(raw[u].y, scale);
-                            const uint2 w2 = scaled4<T>(raw[u].z, scale), w3 = scaled4<T>(raw[u].w, scale);
+                            const uint2 w0 = scaled4<T, LONG>(raw[u].x, scale), w1 = scaled4<T, LONG>(raw[u].y, scale);
+                            const uint2 w2 = scaled4<T, LONG>(raw[u].z, scale), w3 = scaled4<T, LONG>(raw[u].w, scale);
                             if (a.sectors) {
                                 store_sector(o, w0, w1, w2, w3);
                             } else {
@@ -140,6 +157,20 @@ __global__ void __launch_bounds__(32 * kWarps, kBlocks) k_read(const __grid_cons
         }
     }
     raise(a.status, bad);
+}
+
+// Whether products with an 8-bit value (4 bits) may take more than the 24 bits of a float.
+bool is_long(float scale) {
+    int e;
+    const float m = frexpf(scale, &e) * 1048576.0f;  // 2^20
+    return m != floorf(m);
+}
+
+template <class T>
+void launch(const ReadArgs &a, Store store, uint32_t grid, cudaStream_t s) {
+    store == kSame     ? k_read<T, kSame><<<grid, 32 * kWarps, 0, s>>>(a)
+    : store == kScaled ? k_read<T, kScaled><<<grid, 32 * kWarps, 0, s>>>(a)
+                       : k_read<T, kScaledLong><<<grid, 32 * kWarps, 0, s>>>(a);
 }
 
 }  // namespace
@@ -164,12 +195,11 @@ extern "C" kvx_status kvx_read_tokens(const kvx_cache *cache, const uint32_t *bl
     a.by_pieces = FastDiv(a.pieces);
     const uint32_t grid = (uint32_t)ceil_div(T, kWarps);
     const cudaStream_t s = as_stream(stream);
-    const bool fp8 = cache->dtype == KVX_E4M3;
+    const Store store = cache->dtype != KVX_E4M3 ? kSame : is_long(cache->k_scale) || is_long(cache->v_scale) ? kScaledLong : kScaled;
     if (dtype == KVX_BF16)
-        fp8 ? k_read<__nv_bfloat16, true><<<grid, 32 * kWarps, 0, s>>>(a)
-            : k_read<__nv_bfloat16, false><<<grid, 32 * kWarps, 0, s>>>(a);
+        launch<__nv_bfloat16>(a, store, grid, s);
     else
-        fp8 ? k_read<__half, true><<<grid, 32 * kWarps, 0, s>>>(a) : k_read<__half, false><<<grid, 32 * kWarps, 0, s>>>(a);
+        launch<__half>(a, store, grid, s);
     KVX_LAUNCHED();
     return KVX_OK;
 }
