@@ -578,7 +578,13 @@ typedef struct kvx_cache {
     uint32_t dim;
     uint32_t dtype;
     uint32_t page_tokens;
-    uint32_t scale_offset; /* of a segment's row scales; 0 (reserved to mean none) */
+#ifdef __GNUC__
+    __extension__ /* without a name in C99 too */
+#endif
+    union {
+        uint32_t scale_offset; /* of a segment's row scales; 0: none */
+        uint32_t reserved;     /* the same field, by its name when it was 0 */
+    };
     uint64_t token_stride; /* bytes */
     float k_scale, v_scale;
 } kvx_cache;

@@ -46,10 +46,19 @@ _F = ctypes.c_float
 
 
 class CacheStruct(ctypes.Structure):
-    """struct kvx_cache (include/kvx.h); its scale_offset is the field `reserved`"""
+    """struct kvx_cache (include/kvx.h)"""
     _fields_ = [("pool", _P), ("pool_bytes", _U64), ("addr", _P), ("B", _U32), ("L", _U32), ("first_lane", _U32),
-                ("heads", _U32), ("dim", _U32), ("dtype", _U32), ("page_tokens", _U32), ("reserved", _U32),
+                ("heads", _U32), ("dim", _U32), ("dtype", _U32), ("page_tokens", _U32), ("scale_offset", _U32),
                 ("token_stride", _U64), ("k_scale", _F), ("v_scale", _F)]
+
+    @property
+    def reserved(self):
+        """scale_offset, by its name when it was 0"""
+        return self.scale_offset
+
+    @reserved.setter
+    def reserved(self, value):
+        self.scale_offset = value
 
 
 assert ctypes.sizeof(CacheStruct) == 72
@@ -610,7 +619,7 @@ class Cache:
         row = self.dim * dtype.itemsize
         self.c = CacheStruct(pool=pool.data_ptr(), pool_bytes=pool.numel(), addr=addr.data_ptr(), B=addr.size(0),
                              L=addr.size(1), first_lane=first_lane, heads=heads, dim=dim, dtype=_DTYPES[dtype],
-                             page_tokens=page_tokens, reserved=scale_offset,
+                             page_tokens=page_tokens, scale_offset=scale_offset,
                              token_stride=row if token_stride is None else token_stride, k_scale=k_scale, v_scale=v_scale)
         self.status = torch.zeros(1, dtype=torch.int32, device=pool.device)
         self._ref, self._status, self._device = ctypes.byref(self.c), self.status.data_ptr(), pool.get_device()

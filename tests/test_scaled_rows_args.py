@@ -1,0 +1,47 @@
+"""kvx_cache's place for row scales under both of its names."""
+import os
+import subprocess
+
+import pytest
+
+from conftest import ROOT
+from paged_kv_cache_kvx_gb300 import kvx
+
+PROGRAM = r"""
+#include <stddef.h>
+#include <stdio.h>
+#include "kvx.h"
+int main(void) {
+    kvx_cache by_place = {(uint8_t *)0, 0, (const uint64_t *)0, 1, 2, 0, 1, 64, KVX_BF16, 16, 0, 128, 1, 1};
+    kvx_cache set = by_place;
+%s
+    set.reserved = 0;
+    set.scale_offset = 48;
+    printf("%%d %%d %%d %%d %%u %%u %%d\n", (int)sizeof(kvx_cache), (int)offsetof(kvx_cache, scale_offset),
+           (int)offsetof(kvx_cache, reserved), (int)offsetof(kvx_cache, token_stride), set.reserved, (unsigned)by_place.token_stride,
+           (int)by_place.v_scale);
+    return 0;
+}
+"""
+NAMED = "    kvx_cache named = {.pool = 0, .page_tokens = 16, .reserved = 0, .token_stride = 128}, other = {.scale_offset = 16};\n" \
+        "    set.B += named.reserved + other.scale_offset;\n"
+
+
+@pytest.mark.parametrize("cc", ["gcc -std=c99", "gcc -std=c11", "gcc -std=c17", "g++ -std=c++11", "g++ -std=c++17", "g++ -std=c++20"])
+def test_programs_that_name_the_field_either_way(cc, tmp_path):
+    src = tmp_path / ("p.c" if cc.startswith("gcc") else "p.cpp")
+    src.write_text(PROGRAM % (NAMED if cc.startswith("gcc") or "++20" in cc else ""))
+    res = subprocess.run([*cc.split(), "-Wall", "-Wextra", "-Wno-missing-field-initializers", "-Wno-missing-braces", "-pedantic-errors", "-Werror",
+                          "-I" + os.path.join(ROOT, "include"), "-o", str(tmp_path / "p"), str(src)], capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr
+    out = subprocess.run([str(tmp_path / "p")], capture_output=True, text=True, check=True).stdout
+    S = kvx.CacheStruct
+    assert out.split() == [str(x) for x in (kvx.ctypes.sizeof(S), S.scale_offset.offset, S.scale_offset.offset, S.token_stride.offset,
+                                            48, 128, 1)]
+
+
+def test_python_names_the_field_either_way():
+    for c in (kvx.CacheStruct(scale_offset=64), kvx.CacheStruct(reserved=64)):
+        assert c.reserved == c.scale_offset == 64
+        c.reserved = 32
+        assert c.scale_offset == 32
