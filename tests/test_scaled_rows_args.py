@@ -1,11 +1,14 @@
-"""kvx_cache's place for row scales under both of its names."""
+"""kvx_cache's place for row scales under both of its names, and what the operators make of it, without a GPU."""
 import os
 import subprocess
 
 import pytest
+import torch
 
 from conftest import ROOT
 from paged_kv_cache_kvx_gb300 import kvx
+from test_cache_args import EINVAL, OK, append
+from test_shared_args import read, shared, size
 
 PROGRAM = r"""
 #include <stddef.h>
@@ -45,3 +48,19 @@ def test_python_names_the_field_either_way():
         assert c.reserved == c.scale_offset == 64
         c.reserved = 32
         assert c.scale_offset == 32
+
+
+def quantised(scale_offset):
+    """A cache in host memory, whose address is not that of anything on a device: nothing here gets that far."""
+    raw = torch.zeros((1 << 16) + 16, dtype=torch.uint8)
+    pool = raw[-raw.data_ptr() % 16:][:1 << 16]
+    return kvx.Cache(pool, torch.zeros(4, 4, dtype=torch.int64), heads=2, dim=64, dtype=torch.float8_e4m3fn, page_tokens=16,
+                     scale_offset=scale_offset)
+
+
+def test_the_library_sees_where_the_scales_are():
+    """16 rows of 64 bytes: from byte 1024 on they are behind the rows, before that they are not."""
+    for place, what in ((0, OK), (1024, OK), (1024 + 16, OK), (1024 - 16, EINVAL), (1024 + 8, EINVAL), (16, EINVAL)):
+        c = quantised(place).c
+        assert append(c, cs=None, rot=0) == read(c) == shared(c) == what
+        assert (size(c) > 0) == (what == OK)
