@@ -735,8 +735,12 @@ kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t q_stride,
  * in 32 bits, whatever the lengths will be; for heads of up to 128 values
  *     2 * group * (num_seqs * heads + SMs) rows for own tokens and
  *     256 * ((num_seqs * group / 256 + num_groups) * (heads + 2) + 2 * SMs)
- * for prefixes, of dim + 2 floats each, and half as many rows for wider heads: 57 MB
- * for 128 sequences of 64 query heads of 128, 8 KV heads and one prefix.
+ * for prefixes, of dim + 2 floats each: 57 MB for 128 sequences of 64 query heads
+ * of 128, 8 KV heads and one prefix.  For wider heads
+ *     group * (num_seqs * heads + SMs) and
+ *     128 * ((num_seqs * group / 128 + num_groups) * (heads + 2) + 2 * SMs)
+ * rows.  (Fewer where a call has less than 128 query rows or too few tokens for all
+ * SMs.)  Beside these 8 bytes for each group and for each sequence's KV heads.
  */
 size_t kvx_attend_shared_workspace_size(const kvx_cache *cache,
                                         uint32_t num_seqs, uint32_t q_heads,

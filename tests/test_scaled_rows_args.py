@@ -7,7 +7,7 @@ import torch
 
 from conftest import ROOT
 from paged_kv_cache_kvx_gb300 import kvx
-from test_cache_args import EINVAL, OK, append
+from test_cache_args import EINVAL, OK, append, cache
 from test_shared_args import read, shared, size
 
 PROGRAM = r"""
@@ -64,3 +64,22 @@ def test_the_library_sees_where_the_scales_are():
         c = quantised(place).c
         assert append(c, cs=None, rot=0) == read(c) == shared(c) == what
         assert (size(c) > 0) == (what == OK)
+
+
+@pytest.mark.parametrize("dim", [16, 64, 128, 144, 256])
+def test_scratch_is_what_the_header_says(dim):
+    """Equal, but for rounding to 256 bytes, where a call has 128 rows and more and work for every SM; no more than that where not."""
+    heads, c = 8, cache(dim=dim, token_stride=2 * dim)
+    # (without a GPU the library counts one)
+    sms = torch.cuda.get_device_properties(0).multi_processor_count if torch.cuda.is_available() else 1
+    for n, group, groups, per, pper in ((128, 8, 1, 100, 50), (1024, 8, 1, 100, 50), (8192, 8, 3, 100, 50), (300, 7, 40, 1, 1000),
+                                        (1, 1, 0, 1, 0), (3, 16, 2, 1, 1), (16, 128, 16, 100, 100)):
+        got = size(c, n=n, hq=heads * group, per=per, groups=groups, pper=pper)
+        if dim <= 128:
+            rows = 2 * group * (n * heads + sms) + (256 * ((n * group // 256 + groups) * (heads + 2) + 2 * sms) if groups else 0)
+        else:
+            rows = group * (n * heads + sms) + (128 * ((n * group // 128 + groups) * (heads + 2) + 2 * sms) if groups else 0)
+        said = rows * (dim + 2) * 4 + 8 * groups + 8 * n * heads
+        assert got <= said + 4 * 256
+        if n * group >= 128 and per * n > 100:
+            assert got >= said
