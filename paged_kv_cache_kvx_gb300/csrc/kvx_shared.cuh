@@ -380,7 +380,7 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
         uint32_t t = 0;
         for (uint32_t j = 0; j < kThreads; j += 32) t += __popc(__ballot_sync(0xFFFFFFFFu, cum[j + lane] <= at));
         uint32_t before = t ? cum[t - 1] : 0;
-        for (i = t * per;; i++) {
+        for (i = t * per; i < entries; i++) {
             e = entry_of(a, i);
             const Region r = region_of(a, e, share, S::kKeys);
             const uint32_t n = r.width * r.rows;
@@ -388,6 +388,7 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
             before += n;
         }
         off = at - before;
+        if (i >= entries) at = end;  // (only where lengths changed since they were counted)
     }
     __syncthreads();  // cum's place is the copies' from here on
     Entry next = {};
@@ -398,6 +399,7 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
             off -= r.width * r.rows;
             e = next;
             i++;
+            if (i >= entries) break;  // (as above)
             next = Entry{};
             if (i + 1 < entries) next = entry_of(a, i + 1);
             continue;
