@@ -19,43 +19,8 @@ extern template bool launch<__half, 1>(const Args &, cudaStream_t);
 
 namespace {
 
-constexpr uint32_t kMaxGroup = 128;
 constexpr uint32_t kJoinWarps = 4;
 constexpr int kJoinUnroll = 4;        // parts whose loads a warp has in flight
-
-// The parts of a query's results over one set of keys, by number 0 .. count()-1:
-// `subs` rows for each pair of a block of columns and a block of k_shared that
-// works on it, of which there may be fewer than `each`.
-struct Parts {
-    Region r;
-    uint32_t row, head, c0, c1;     // the columns c0 .. c1-1 of a row
-    uint32_t start, share;          // of the entry; of a block
-    uint32_t first_row, cap, off_b, subs;
-    uint32_t b0, blocks, each;
-    __device__ __forceinline__ void find() {
-        b0 = c0 / r.block;
-        blocks = (c1 - 1) / r.block - b0 + 1;
-        uint32_t from, to;
-        span(b0, from, to);
-        each = blocks > 1 || r.rows > 1 ? 2 : to / share - from / share + 1;
-    }
-    // First and last place of the columns in a block.
-    __device__ __forceinline__ void span(uint32_t b, uint32_t &from, uint32_t &to) const {
-        const uint32_t n = r.columns(b), begin = b * r.block, at = start + begin * r.rows + row * n;
-        from = at + (c0 > begin ? c0 - begin : 0);
-        to = at + (c1 - begin < n ? c1 - begin : n) - 1;
-    }
-    __device__ __forceinline__ uint32_t count() const { return blocks * each * subs; }
-    // The row of a part, kNone where there is none.
-    __device__ __forceinline__ uint32_t at(uint32_t i) const {
-        const uint32_t sub = subs == 2 ? i & 1 : 0, k = subs == 2 ? i >> 1 : i, b = k / each;
-        uint32_t from, to;
-        span(b0 + b, from, to);
-        const uint32_t c = from / share + (k - b * each);
-        if (c > to / share) return kNone;
-        return first_row + (r.rank(b0 + b, row, head) + c) * cap + sub * off_b;
-    }
-};
 
 // A query's parts by WARPS warps, blocks of kJoinWarps.  Bound by the chain of its
 // reads (group, lengths, which blocks, bases and sums, outputs), so many warps in
@@ -83,8 +48,6 @@ __global__ void __launch_bounds__(32 * kJoinWarps, WIDE ? 5 : 7) k_join(const __
         else
             hi = mid;
     }
-    constexpr bool wide = WIDE;
-    const uint32_t keys = wide ? 64 : 128;
     Parts parts[2] = {};
     uint2 const *where[2] = {};
     Entry entry[2] = {};
@@ -102,37 +65,18 @@ __global__ void __launch_bounds__(32 * kJoinWarps, WIDE ? 5 : 7) k_join(const __
     for (int k = 0; k < 2; k++)
         if (where[k]) w[k] = __ldcg(where[k]);
     if (where[0] && w[0].y) {
-        const Entry &e = entry[0];
-        Parts &p = parts[0];
-        p.start = w[0].x, p.share = w[0].y;
-        p.r = region_of(a, e, p.share, keys);
-        const uint32_t query_row = (n - e.seq0) * a.group + in;
-        p.row = query_row / a.tile_rows, p.head = head;
-        p.c0 = head * p.r.len + kExtra, p.c1 = (head + 1) * p.r.len;
-        const uint32_t at = query_row - p.row * a.tile_rows, rows = e.rows - p.row * a.tile_rows;
-        p.first_row = group_parts(a, p.start, p.share, e.seq0, lo - 1) * a.prefix_cap + at;
-        p.cap = a.prefix_cap, p.off_b = a.prefix_off_b;
-        p.subs = wide || rows > kRows ? 1 : 2;
-        p.find();
+        parts[0] = prefix_parts(a, entry[0], w[0], lo - 1, n, head, in, WIDE);
     }
     if (where[1] && w[1].x <= w[1].y && w[1].y < a.grid) {  // (else left by a block whose wait ran out)
-        Parts &p = parts[1];  // one column a block
-        p.r.len = p.r.rows = p.r.block = 1, p.r.width = w[1].y + 1;
-        p.share = 1, p.c0 = w[1].x, p.c1 = w[1].y + 1;
-        p.first_row = a.own_first_row + (n * a.c.heads + head) * a.own_cap + in;
-        p.cap = a.own_cap, p.off_b = a.own_off_b, p.subs = wide ? 1 : 2;
-        p.b0 = w[1].x, p.blocks = w[1].y - w[1].x + 1, p.each = 1;
+        parts[1] = own_parts(a, w[1], n, head, in, WIDE);
     }
     // A call that ended early, by a table in disorder or a wait that ran out, may
-    // leave anything: parts are at most 2 * (grid + 2) pairs of a prefix, and as many
-    // as blocks of own tokens.
+    // leave anything.
     const uint64_t counted = (uint64_t)parts[0].blocks * parts[0].each * parts[0].subs + parts[1].count();
-    const uint32_t first = parts[0].count(), all = counted > 8ull * (a.grid + 2) ? 0 : (uint32_t)counted;
+    const uint32_t first = parts[0].count(), all = counted > most_parts(a) ? 0 : (uint32_t)counted;
     const uint32_t most = (uint32_t)(a.rows < kNone ? a.rows : kNone);
     auto at = [&](uint32_t i) {
-        const uint32_t row = i < first ? parts[0].at(i)
-                                       : parts[1].first_row + (parts[1].c0 + (i - first) / parts[1].subs) * parts[1].cap +
-                                             (i - first) % parts[1].subs * parts[1].off_b;
+        const uint32_t row = i < first ? parts[0].at(i) : parts[1].at_own(i - first);
         return row < most ? row : kNone;
     };
     // A warp's share, 32 parts at a time: a lane has one's base and sum; 0 stands
@@ -219,47 +163,12 @@ cudaError_t launch_join(const cudaLaunchConfig_t &cfg, bool four, bool wide, con
                 : cudaLaunchKernelEx(&cfg, four ? k_join<T, 4, false> : k_join<T, 1, false>, a);
 }
 
-// Sizes of the call, known on the host: the lengths are not, so every bound is the tables'.
-struct Plan {
-    uint32_t max_len, max_prefix, grid;
-    uint32_t tile_rows, prefix_cap, prefix_off_b, own_cap, own_off_b;
-    uint64_t own_units, own_first_row, rows;
-};
-
-bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t blocks_per_seq, uint32_t num_groups,
-          uint32_t blocks_per_prefix, Plan &p) {
-    if (!cache_ok(c) || !q_heads || q_heads % c->heads || q_heads / c->heads > kMaxGroup) return false;
-    const uint64_t len = (uint64_t)blocks_per_seq * c->page_tokens, prefix = (uint64_t)blocks_per_prefix * c->page_tokens;
-    if (len >= (1ull << 31) || prefix >= (1ull << 31)) return false;
-    if (num_seqs >= (1u << 30) || num_groups >= (1u << 30) || (uint64_t)num_seqs * q_heads >= (1ull << 31)) return false;
-    const uint32_t group = q_heads / c->heads, keys = c->dim > 128 ? 64 : 128;
-    const bool wide = c->dim > 128;
-    const uint64_t queries = (uint64_t)num_seqs * group;
-    p.max_len = (uint32_t)len, p.max_prefix = (uint32_t)prefix;
-    p.tile_rows = wide ? 128 : 256;
-    // a part's rows: both slots', where they have the same ones
-    const uint32_t few = queries < kRows ? (uint32_t)queries : kRows;
-    p.prefix_off_b = wide ? 0 : few;
-    p.prefix_cap = wide ? few : 2 * few;
-    p.own_off_b = wide ? 0 : group;
-    p.own_cap = wide ? group : 2 * group;
-    const uint64_t tiles = num_groups ? queries / p.tile_rows + num_groups : 0;
-    p.own_units = (uint64_t)num_seqs * c->heads;
-    const uint64_t most = tiles * c->heads * (ceil_div(prefix, kHalf) + kExtra) + p.own_units * (ceil_div(len, keys) + kExtra);
-    if (tiles * (c->heads + 2) >= (1ull << 31) || most >= (1ull << 31)) return false;
-    const uint64_t want = ceil_div(most, kMinShare);
-    p.grid = want < (uint64_t)sm_count() ? (want ? (uint32_t)want : 1) : (uint32_t)sm_count();
-    p.own_first_row = num_groups ? (tiles * (c->heads + 2) + 2 * p.grid) * p.prefix_cap : 0;
-    p.rows = p.own_first_row + (p.own_units + p.grid) * p.own_cap;
-    return p.rows < (1ull << 32);
-}
-
 size_t carve(const Plan &p, const kvx_cache *c, uint32_t num_groups, void *ws, Args *a) {
     Carver w(ws);
     float *o = w.take<float>(p.rows * c->dim);
     float2 *ml = w.take<float2>(p.rows);
     uint2 *groups = w.take<uint2>(num_groups), *own = w.take<uint2>(p.own_units);
-    if (a) a->part_o = o, a->part_ml = ml, a->group_at = groups, a->own_parts = own, a->rows = p.rows;
+    if (a) a->part_o = o, a->part_ml = ml, a->group_at = groups, a->own_parts = own;
     return w.off;
 }
 
@@ -272,7 +181,7 @@ extern "C" size_t kvx_attend_shared_workspace_size(const kvx_cache *cache, uint3
                                                    uint32_t blocks_per_prefix) {
     using namespace kvx::shared;
     Plan p;
-    return plan(cache, num_seqs, q_heads, blocks_per_seq, num_groups, blocks_per_prefix, p) ? carve(p, cache, num_groups, nullptr, nullptr) : 0;
+    return plan(cache, num_seqs, q_heads, blocks_per_seq, num_groups, blocks_per_prefix, kvx::sm_count(), p) ? carve(p, cache, num_groups, nullptr, nullptr) : 0;
 }
 
 extern "C" kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q, uint64_t q_stride, uint32_t dtype,
@@ -285,7 +194,7 @@ extern "C" kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q, u
     using namespace kvx;
     using namespace kvx::shared;
     Plan p;
-    if (!plan(cache, num_seqs, q_heads, blocks_per_seq, num_groups, blocks_per_prefix, p)) return KVX_EINVAL;
+    if (!plan(cache, num_seqs, q_heads, blocks_per_seq, num_groups, blocks_per_prefix, sm_count(), p)) return KVX_EINVAL;
     if ((dtype != KVX_BF16 && dtype != KVX_F16) || (cache->dtype != dtype && cache->dtype != KVX_E4M3)) return KVX_EINVAL;
     if (!status || !(scale > -INFINITY && scale < INFINITY)) return KVX_EINVAL;
     if ((q_stride | out_stride) % 8 || !aligned16(q) || !aligned16(out)) return KVX_EINVAL;
@@ -293,25 +202,14 @@ extern "C" kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q, u
     if (!q || !out || !lens || (p.max_len && !blocks)) return KVX_EINVAL;
     if (num_groups && (!prefix_lens || !group_first || (p.max_prefix && !prefix_blocks))) return KVX_EINVAL;
     if (!ws || !aligned16(ws) || ws_bytes < carve(p, cache, num_groups, nullptr, nullptr)) return KVX_EINVAL;
-    Args a = {};
-    a.c = cache_view(cache);
+    Args a = args_of(cache, num_seqs, q_heads, blocks_per_seq, num_groups, blocks_per_prefix, p);
     a.q = q, a.q_stride = q_stride;
     a.prefix_blocks = prefix_blocks, a.prefix_lens = prefix_lens, a.group_first = group_first;
     a.blocks = blocks, a.lens = lens;
-    a.blocks_per_prefix = blocks_per_prefix, a.num_groups = num_groups;
-    a.blocks_per_seq = blocks_per_seq, a.num_seqs = num_seqs;
-    a.q_heads = q_heads, a.group = q_heads / cache->heads;
-    a.max_prefix = p.max_prefix, a.max_len = p.max_len;
-    a.by_group = FastDiv(a.group);
     a.scale2 = fabsf(scale) * cache->k_scale * 1.4426950408889634f;
     if (a.scale2 == 0) a.scale2 = 1.4e-45f;  // the smallest: what is masked by -infinity stays masked
     a.negate = scale < 0;
-    a.paged16 = cache->page_tokens % 16 == 0;
     a.out = out, a.out_stride = out_stride, a.lse = lse, a.status = status;
-    a.tile_rows = p.tile_rows;
-    a.prefix_cap = p.prefix_cap, a.prefix_off_b = p.prefix_off_b;
-    a.own_cap = p.own_cap, a.own_off_b = p.own_off_b, a.own_first_row = (uint32_t)p.own_first_row;
-    a.grid = p.grid;
     carve(p, cache, num_groups, ws, &a);
     const cudaStream_t s = as_stream(stream);
     const bool ok = dtype == KVX_BF16

@@ -24,6 +24,10 @@ constexpr uint32_t kHalf = 64;  // keys that a slot's softmax takes at a time
 constexpr uint32_t kRows = 128;  // of a slot: the tensor cores' M, a query row for each lane of tensor memory
 constexpr uint32_t kExtra = 2;   // columns (Region) that a head's own overhead counts as
 constexpr uint32_t kMinShare = 2;
+constexpr uint32_t kMaxGroup = 128;  // query heads of a KV head
+// Keys of a tile and query rows of a unit, of heads wider than 128 and of others.
+__host__ __device__ __forceinline__ constexpr uint32_t keys_of(bool wide) { return wide ? 64 : 128; }
+__host__ __device__ __forceinline__ constexpr uint32_t tile_rows_of(bool wide) { return wide ? 128 : 256; }
 
 struct Args {
     CacheView c;
@@ -57,12 +61,19 @@ struct Entry {
     uint32_t seq0, rows, len;
     bool disorder, beyond;  // a group whose sequences do not exist; more tokens than pages
 };
-__device__ __forceinline__ Entry entry_of(const Args &a, uint32_t i) {
+__host__ __device__ __forceinline__ uint32_t load(const uint32_t *p) {
+#ifdef __CUDA_ARCH__
+    return __ldg(p);
+#else
+    return *p;
+#endif
+}
+__host__ __device__ __forceinline__ Entry entry_of(const Args &a, uint32_t i) {
     Entry e = {};
     uint32_t most;
     if (i < a.num_groups) {
-        const uint32_t from = __ldg(a.group_first + i), to = __ldg(a.group_first + i + 1);
-        e.len = __ldg(a.prefix_lens + i);
+        const uint32_t from = load(a.group_first + i), to = load(a.group_first + i + 1);
+        e.len = load(a.prefix_lens + i);
         most = a.max_prefix;
         e.seq0 = from;
         if (from > to || to > a.num_seqs)
@@ -72,7 +83,7 @@ __device__ __forceinline__ Entry entry_of(const Args &a, uint32_t i) {
     } else {
         e.seq0 = i - a.num_groups;
         e.rows = a.group;
-        e.len = __ldg(a.lens + e.seq0);
+        e.len = load(a.lens + e.seq0);
         most = a.max_len;
     }
     if (e.len > most) e.len = most, e.beyond = true;
@@ -119,6 +130,178 @@ __host__ __device__ __forceinline__ uint32_t group_parts(const Args &a, uint32_t
     return start / share + ((uint32_t)((uint64_t)first_seq * a.group / a.tile_rows) + g) * (a.c.heads + 2);
 }
 
+// a / b for b > 0; small quotients go through the reciprocal: a < 2^22 is exact
+// as a float, and a * (1/b) is off by less than one.
+__host__ __device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t b) {
+#ifdef __CUDA_ARCH__
+    if (a < 1u << 22) {
+        uint32_t q = (uint32_t)__fmul_rz((float)a, __frcp_rz((float)b));
+        q += a - q * b >= b;
+        return q;
+    }
+#endif
+    return a / b;
+}
+
+// What a block does next: columns from .. to-1 of a head's, in a row of a block of columns,
+// from the place `off` of an entry's on, at most `left` of them.
+struct Cut {
+    uint32_t block, row, head, from, to;
+};
+__host__ __device__ __forceinline__ Cut cut(const Region &r, uint32_t off, uint32_t left) {
+    Cut c;
+    c.block = quotient(off, r.block * r.rows);
+    const uint32_t in_block = off - c.block * r.block * r.rows, columns = r.columns(c.block);
+    c.row = quotient(in_block, columns);
+    const uint32_t in_row = in_block - c.row * columns, column = c.block * r.block + in_row;
+    c.head = quotient(column, r.len), c.from = column - c.head * r.len;
+    c.to = c.from + (columns - in_row);
+    if (c.to > r.len) c.to = r.len;
+    if (c.to - c.from > left) c.to = c.from + left;
+    return c;
+}
+// A block's share of all columns.
+__host__ __device__ __forceinline__ uint32_t share_of(const Args &a, uint32_t total) {
+    const uint32_t share = (total + a.grid - 1) / a.grid;
+    return share < kMinShare ? kMinShare : share;
+}
+// The first rows of partial results: of a prefix, of own tokens; and the blocks that
+// have the latter, of a head whose columns start at `first`.
+__host__ __device__ __forceinline__ uint32_t prefix_row(const Args &a, const Region &r, const Cut &c, uint32_t start, uint32_t share,
+                                                        uint32_t first_seq, uint32_t g, uint32_t block) {
+    return (group_parts(a, start, share, first_seq, g) + r.rank(c.block, c.row, c.head) + block) * a.prefix_cap;
+}
+__host__ __device__ __forceinline__ uint32_t own_row(const Args &a, uint32_t unit, uint32_t block) {
+    return a.own_first_row + (unit + block) * a.own_cap;
+}
+__host__ __device__ __forceinline__ uint2 own_blocks(const Region &r, uint32_t first, uint32_t share) {
+    return make_uint2((first + kExtra) / share, (first + r.len - 1) / share);
+}
+
+// The parts of a query's results over one set of keys, by number 0 .. count()-1:
+// `subs` rows for each pair of a block of columns and a block of k_shared that
+// works on it, of which there may be fewer than `each`.
+struct Parts {
+    Region r;
+    uint32_t row, head, c0, c1;     // the columns c0 .. c1-1 of a row
+    uint32_t start, share;          // of the entry; of a block
+    uint32_t first_row, cap, off_b, subs;
+    uint32_t b0, blocks, each;
+    __host__ __device__ __forceinline__ void find() {
+        b0 = c0 / r.block;
+        blocks = (c1 - 1) / r.block - b0 + 1;
+        uint32_t from, to;
+        span(b0, from, to);
+        each = blocks > 1 || r.rows > 1 ? 2 : to / share - from / share + 1;
+    }
+    // First and last place of the columns in a block.
+    __host__ __device__ __forceinline__ void span(uint32_t b, uint32_t &from, uint32_t &to) const {
+        const uint32_t n = r.columns(b), begin = b * r.block, at = start + begin * r.rows + row * n;
+        from = at + (c0 > begin ? c0 - begin : 0);
+        to = at + (c1 - begin < n ? c1 - begin : n) - 1;
+    }
+    __host__ __device__ __forceinline__ uint32_t count() const { return blocks * each * subs; }
+    // The row of a part, kNone where there is none.
+    __host__ __device__ __forceinline__ uint32_t at(uint32_t i) const {
+        const uint32_t sub = subs == 2 ? i & 1 : 0, k = subs == 2 ? i >> 1 : i, b = k / each;
+        uint32_t from, to;
+        span(b0 + b, from, to);
+        const uint32_t c = from / share + (k - b * each);
+        if (c > to / share) return kNone;
+        return first_row + (r.rank(b0 + b, row, head) + c) * cap + sub * off_b;
+    }
+    // The same of own tokens' parts: one column a block of k_shared.
+    __host__ __device__ __forceinline__ uint32_t at_own(uint32_t i) const {
+        return first_row + (c0 + i / subs) * cap + i % subs * off_b;
+    }
+};
+
+// The parts over the prefix of a group g, e, of the query head `in` of sequence n's KV
+// head; w: what the walking warps left in group_at.
+__host__ __device__ __forceinline__ Parts prefix_parts(const Args &a, const Entry &e, uint2 w, uint32_t g, uint32_t n, uint32_t head,
+                                                       uint32_t in, bool wide) {
+    Parts p = {};
+    p.start = w.x, p.share = w.y;
+    p.r = region_of(a, e, p.share, keys_of(wide));
+    const uint32_t query_row = (n - e.seq0) * a.group + in;
+    p.row = query_row / a.tile_rows, p.head = head;
+    p.c0 = head * p.r.len + kExtra, p.c1 = (head + 1) * p.r.len;
+    const uint32_t at = query_row - p.row * a.tile_rows, rows = e.rows - p.row * a.tile_rows;
+    p.first_row = group_parts(a, p.start, p.share, e.seq0, g) * a.prefix_cap + at;
+    p.cap = a.prefix_cap, p.off_b = a.prefix_off_b;
+    p.subs = wide || rows > kRows ? 1 : 2;
+    p.find();
+    return p;
+}
+// Those over its own tokens; w: from own_parts.
+__host__ __device__ __forceinline__ Parts own_parts(const Args &a, uint2 w, uint32_t n, uint32_t head, uint32_t in, bool wide) {
+    Parts p = {};
+    p.r.len = p.r.rows = p.r.block = 1, p.r.width = w.y + 1;
+    p.share = 1, p.c0 = w.x, p.c1 = w.y + 1;
+    p.first_row = a.own_first_row + (n * a.c.heads + head) * a.own_cap + in;
+    p.cap = a.own_cap, p.off_b = a.own_off_b, p.subs = wide ? 1 : 2;
+    p.b0 = w.x, p.blocks = w.y - w.x + 1, p.each = 1;
+    return p;
+}
+
+
+// A query's parts are at most 2 * (grid + 2) pairs over a prefix, and a pair for each
+// block over own tokens.
+__host__ __device__ __forceinline__ uint64_t most_parts(const Args &a) { return 8ull * (a.grid + 2); }
+
+// Sizes of the call, known on the host: the lengths are not, so every bound is the tables'.
+struct Plan {
+    uint32_t max_len, max_prefix, grid;
+    uint32_t tile_rows, prefix_cap, prefix_off_b, own_cap, own_off_b;
+    uint64_t own_units, own_first_row, rows;
+};
+
+inline bool plan(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t blocks_per_seq, uint32_t num_groups,
+                 uint32_t blocks_per_prefix, uint32_t sms, Plan &p) {
+    if (!cache_ok(c) || !q_heads || q_heads % c->heads || q_heads / c->heads > kMaxGroup) return false;
+    const uint64_t len = (uint64_t)blocks_per_seq * c->page_tokens, prefix = (uint64_t)blocks_per_prefix * c->page_tokens;
+    if (len >= (1ull << 31) || prefix >= (1ull << 31)) return false;
+    if (num_seqs >= (1u << 30) || num_groups >= (1u << 30) || (uint64_t)num_seqs * q_heads >= (1ull << 31)) return false;
+    const bool wide = c->dim > 128;
+    const uint32_t group = q_heads / c->heads, keys = keys_of(wide);
+    const uint64_t queries = (uint64_t)num_seqs * group;
+    p.max_len = (uint32_t)len, p.max_prefix = (uint32_t)prefix;
+    p.tile_rows = tile_rows_of(wide);
+    // a part's rows: both slots', where they have the same ones
+    const uint32_t few = queries < kRows ? (uint32_t)queries : kRows;
+    p.prefix_off_b = wide ? 0 : few;
+    p.prefix_cap = wide ? few : 2 * few;
+    p.own_off_b = wide ? 0 : group;
+    p.own_cap = wide ? group : 2 * group;
+    const uint64_t tiles = num_groups ? queries / p.tile_rows + num_groups : 0;
+    p.own_units = (uint64_t)num_seqs * c->heads;
+    const uint64_t most = tiles * c->heads * (ceil_div(prefix, kHalf) + kExtra) + p.own_units * (ceil_div(len, keys) + kExtra);
+    if (tiles * (c->heads + 2) >= (1ull << 31) || most >= (1ull << 31)) return false;
+    const uint64_t want = ceil_div(most, kMinShare);
+    p.grid = want < sms ? (want ? (uint32_t)want : 1) : sms;
+    p.own_first_row = num_groups ? (tiles * (c->heads + 2) + 2 * p.grid) * p.prefix_cap : 0;
+    p.rows = p.own_first_row + (p.own_units + p.grid) * p.own_cap;
+    return p.rows < (1ull << 32);
+}
+
+// What kernels and the join take of it.
+inline Args args_of(const kvx_cache *c, uint32_t num_seqs, uint32_t q_heads, uint32_t blocks_per_seq, uint32_t num_groups,
+                    uint32_t blocks_per_prefix, const Plan &p) {
+    Args a = {};
+    a.c = cache_view(c);
+    a.blocks_per_prefix = blocks_per_prefix, a.num_groups = num_groups;
+    a.blocks_per_seq = blocks_per_seq, a.num_seqs = num_seqs;
+    a.q_heads = q_heads, a.group = q_heads / c->heads;
+    a.max_prefix = p.max_prefix, a.max_len = p.max_len;
+    a.by_group = FastDiv(a.group);
+    a.paged16 = c->page_tokens % 16 == 0;
+    a.tile_rows = p.tile_rows;
+    a.prefix_cap = p.prefix_cap, a.prefix_off_b = p.prefix_off_b;
+    a.own_cap = p.own_cap, a.own_off_b = p.own_off_b, a.own_first_row = (uint32_t)p.own_first_row;
+    a.grid = p.grid, a.rows = p.rows;
+    return a;
+}
+
 // Where among the 128 rows a slot's few ones lie, which says which of its warps works:
 // the two slots' not on the same scheduler (59 us on one, 56 on two, neither an
 // issuing warp's).
@@ -135,8 +318,7 @@ struct Piece {
 
 template <int DP, int ES>
 struct Shape {
-    static constexpr uint32_t kKeys = DP == 256 ? 64 : 128;  // of a tile
-    static constexpr uint32_t kTileRows = DP == 256 ? 128 : 256;
+    static constexpr uint32_t kKeys = keys_of(DP == 256);
     // A slot has room for the logits of 128 keys: of a tile's two halves, or of
     // two tiles.  (Two halves that the tensor cores fill one by one, the next
     // while the softmax works on the other, keep the tensor cores longer: a product
@@ -351,15 +533,6 @@ __device__ __forceinline__ float exp2_fast(float x) {
     return y;
 }
 
-// a / b for b > 0; small quotients go through the reciprocal: a < 2^22 is exact
-// as a float, and a * (1/b) is off by less than one.
-__device__ __forceinline__ uint32_t quotient(uint32_t a, uint32_t b) {
-    if (a >= 1u << 22) return a / b;
-    uint32_t q = (uint32_t)__fmul_rz((float)a, __frcp_rz((float)b));
-    q += a - q * b >= b;
-    return q;
-}
-
 // ------------------------------------------------------------- the schedule
 
 // The walking warp: the block's share of all units' tiles, piece by piece.
@@ -368,8 +541,7 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
                                      uint32_t lane) {
     using S = Shape<DP, ES>;
     const uint32_t entries = a.num_groups + a.num_seqs;
-    uint32_t share = (total + a.grid - 1) / a.grid;
-    if (share < kMinShare) share = kMinShare;
+    const uint32_t share = share_of(a, total);
     const uint64_t begin64 = (uint64_t)blockIdx.x * share;
     uint32_t at = begin64 < total ? (uint32_t)begin64 : total;
     const uint32_t end = total - at > share ? at + share : total;
@@ -413,24 +585,19 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
             if (i + 1 < entries) next = entry_of(a, i + 1);
             continue;
         }
-        const uint32_t b = quotient(off, r.block * r.rows), in_block = off - b * r.block * r.rows;
-        const uint32_t columns = r.columns(b), mt = quotient(in_block, columns), in_row = in_block - mt * columns;
-        const uint32_t column = b * r.block + in_row, head = quotient(column, r.len), from = column - head * r.len;
-        uint32_t to = from + (columns - in_row);
-        if (to > r.len) to = r.len;
-        if (to - from > end - at) to = from + (end - at);
+        const Cut c = cut(r, off, end - at);
         const uint32_t start = at - off;  // the entry's
-        at += to - from;
-        off += to - from;
-        if (to <= kExtra) continue;
-        const uint32_t t0 = from > kExtra ? from - kExtra : 0, t1 = to - kExtra;
+        at += c.to - c.from;
+        off += c.to - c.from;
+        if (c.to <= kExtra) continue;
+        const uint32_t t0 = c.from > kExtra ? c.from - kExtra : 0, t1 = c.to - kExtra;
         if (np >= kPieces && !warp_wait(&sh.pc_empty[np % kPieces], (np / kPieces & 1) ^ 1)) return false;
         if (lane == 0) {
             Piece p;
             p.seq0 = e.seq0;
-            p.row0 = mt * a.tile_rows;
+            p.row0 = c.row * a.tile_rows;
             p.rows = e.rows - p.row0 < a.tile_rows ? e.rows - p.row0 : a.tile_rows;
-            p.head = head;
+            p.head = c.head;
             p.k0 = t0 * r.keys;
             p.k1 = t1 * r.keys < e.len ? t1 * r.keys : e.len;
             p.both = DP == 256 || p.rows > kRows;
@@ -438,15 +605,15 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
             p.event = event;
             if (i < a.num_groups) {
                 p.table = a.prefix_blocks + (uint64_t)i * a.blocks_per_prefix;
-                p.part_row = (group_parts(a, start, share, e.seq0, i) + r.rank(b, mt, head) + blockIdx.x) * a.prefix_cap;
+                p.part_row = prefix_row(a, r, c, start, share, e.seq0, i, blockIdx.x);
                 p.off_b = a.prefix_off_b;
                 a.group_at[i] = make_uint2(start, share);  // the same from all blocks
             } else {
-                const uint32_t u = e.seq0 * a.c.heads + head, first = start + head * r.len;
+                const uint32_t u = e.seq0 * a.c.heads + c.head;
                 p.table = a.blocks + (uint64_t)e.seq0 * a.blocks_per_seq;
-                p.part_row = a.own_first_row + (u + blockIdx.x) * a.own_cap;
+                p.part_row = own_row(a, u, blockIdx.x);
                 p.off_b = a.own_off_b;
-                if (!t0) a.own_parts[u] = make_uint2((first + kExtra) / share, (first + r.len - 1) / share);
+                if (!t0) a.own_parts[u] = own_blocks(r, start + c.head * r.len, share);
             }
             sh.pieces[np % kPieces] = p;
             mbar_arrive(&sh.pc_full[np % kPieces]);
