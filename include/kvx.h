@@ -716,11 +716,8 @@ kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t q_stride,
  *                  raises KVX_S_BOUNDS and counts as full pages.
  * Tokens of a page or segment that the cache's rules exclude count as zeros.
  * Keys and values enter the tensor cores in `dtype`: 16-bit ones as they are,
- * 8-bit ones exactly, but row-scaled ones beyond its range as a cache of `dtype`
- * would hold them.  In fp16 these are values under 2^-14, rounded to multiples of
- * 2^-24, and values from 65536 on: 65536 itself, which kvx_append_tokens makes of a
- * row's values above 63488, counts as 65504, larger ones as infinite.
- * Logits, softmax and sums are held in 32 bits;
+ * 8-bit ones exactly (row-scaled ones in fp16 rounded to it, where they are
+ * under 2^-14 or from 65520 on).  Logits, softmax and sums are held in 32 bits;
  * the weights that multiply V are rounded to `dtype`, as V and the output are.
  * An infinite value in V makes its column of the output infinite, or NaN where
  * its weight counts as 0 (in fp16 one under 2^-32 of a head's largest); in bf16
@@ -766,8 +763,7 @@ kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q,
  * sequence n's tokens first[n], first[n] + 1, ...  16-bit caches are copied;
  * 8-bit values are multiplied by their scale (k_scale and v_scale, or the
  * row's) and the product is rounded once to `dtype`, to the nearest even (one
- * under 2^-122, which bf16 reaches, to 32 bits before).  One beyond `dtype` becomes
- * infinite: so does the 65536 that a row-scaled cache holds for values above 63488.
+ * under 2^-122, which bf16 reaches, to 32 bits before).
  *
  *   blocks         [num_seqs][blocks_per_seq] uint32, as for kvx_attend; only
  *                  entries of pages that hold tokens to be read are read.

@@ -679,32 +679,33 @@ struct Widen<__nv_bfloat16> {
         return make_uint2(Pair<__nv_bfloat16>::pack(x.x * s, x.y * s), Pair<__nv_bfloat16>::pack(y.x * s, y.y * s));
     }
 };
-// fp16: the conversion is exact, and a product by 2^-12 to 2^7 as well.  Smaller
-// scales round values under 2^-14 to fp16's steps.  Larger ones reach beyond fp16:
-// 65536, which a row's values above 63488 become in 8 bits, counts as 65504 (half a
-// step of fp16 away), larger ones are infinite as they are in a cache of 16 bits.
+// fp16: the conversion is exact, and a product by 2^-12 to 2^15 is as exact as
+// fp16 can be; others come in two steps, of which the first is exact (an 8-bit
+// value's last bit is 2^-9 or more).
 template <>
 struct Widen<__half> {
-    uint32_t e, factor;
-    __device__ __forceinline__ explicit Widen(uint32_t exponent) : e(exponent), factor((exponent - 112) * 0x04000400u) {}
-    __device__ __forceinline__ bool simple() const { return e - 115 <= 19; }
+    uint32_t e, a;
+    __device__ __forceinline__ explicit Widen(uint32_t exponent) : e(exponent) {
+        const int k = (int)e - 127, ka = k < -12 ? -12 : k > 15 ? 15 : k;
+        a = (uint32_t)(ka + 15) * 0x04000400u;
+    }
+    __device__ __forceinline__ bool simple() const { return e - 115 <= 27; }
     __device__ __forceinline__ static uint32_t check(const uint4 &) { return 0; }  // a NaN stays one
-    __device__ __forceinline__ uint32_t times(uint32_t x) const {
-        const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&factor));
+    __device__ __forceinline__ static uint32_t times(uint32_t x, uint32_t y) {
+        const __half2 r = __hmul2(*reinterpret_cast<const __half2 *>(&x), *reinterpret_cast<const __half2 *>(&y));
         return *reinterpret_cast<const uint32_t *>(&r);
     }
     __device__ __forceinline__ uint2 four(uint32_t v) const {
         uint32_t lo, hi;
         halves(v, lo, hi);
-        return make_uint2(times(lo), times(hi));
+        return make_uint2(times(lo, a), times(hi, a));
     }
-    __device__ __forceinline__ static float within(float x) { return fabsf(x) == 65536.0f ? copysignf(65504.0f, x) : x; }
-    __device__ __forceinline__ uint2 any(uint32_t v) const {  // products are exact in 32 bits
-        uint32_t lo, hi;
-        halves(v, lo, hi);
-        const float s = row_scale(e);
-        const float2 x = Pair<__half>::unpack(lo), y = Pair<__half>::unpack(hi);
-        return make_uint2(Pair<__half>::pack(within(x.x * s), within(x.y * s)), Pair<__half>::pack(within(y.x * s), within(y.y * s)));
+    __device__ __forceinline__ uint2 any(uint32_t v) const {
+        const int k = (int)e - 127, kb = k < -12 ? k + 12 : k > 15 ? k - 15 : 0;
+        const uint32_t b = e == 255 ? 0x7FFF7FFFu : kb < -24 ? 0u : kb < -14 ? 0x00010001u << (kb + 24)
+                                                 : (uint32_t)((kb > 15 ? 15 : kb) + 15) * 0x04000400u;
+        const uint2 w = four(v);
+        return make_uint2(times(w.x, b), times(w.y, b));
     }
 };
 
