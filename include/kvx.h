@@ -600,7 +600,9 @@ typedef struct kvx_cache {
  * a = 2i and b = 2i + 1.  Everything is computed in 32 bits and rounded once,
  * to the nearest even; KVX_E4M3 stores value / scale and limits it to +-448
  * (a NaN stays NaN).  With row scales a row's scale is the smallest power of
- * two, from 2^-126 on, over which its largest finite magnitude is at most 448.
+ * two, from 2^-126 on, over which its largest finite magnitude is at most 448;
+ * with it KVX_F16 values from 63488 up to the type's largest are stored as 61440,
+ * where the nearest, 65536, would be infinite in that type.
  *
  *   q, k, v        [T][q_heads|heads|heads][dim] of `dtype` (KVX_BF16 or
  *                  KVX_F16; the cache's type is the same one or KVX_E4M3); a

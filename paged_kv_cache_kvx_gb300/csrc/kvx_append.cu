@@ -11,7 +11,7 @@
 // 8-bit rows with a scale each (kRowScaled): the smallest power of two, from 2^-126 on,
 // by which the row's largest value is at most 448, found by one more maximum
 // across the row's lanes.  Stored values are products with its inverse, exact but for
-// the one rounding to 8 bits.
+// the one rounding to 8 bits, which what fp16 holds does not leave (stay_finite).
 //
 // Bound by HBM for prompts (each value read once and written once; the table's
 // row of cosines and sines is read once per block of a token's heads): 16,000
@@ -24,6 +24,7 @@
 // spread over several blocks.
 #include <cmath>
 #include <cuda_fp8.h>
+#include <type_traits>
 
 #include "kvx_cache.cuh"
 
@@ -91,6 +92,16 @@ __device__ __forceinline__ uint32_t row_exponent(float top) {
     const uint32_t bits = __float_as_uint(top);
     const int e = (int)(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u);
     return e < 1 ? 1 : e;
+}
+
+// Values from 63488 on, over a row's scale of 2^8 and from 248 on, would be rounded to
+// 256, which stands for 65536: infinite in fp16, when it is read back and in products.  Those
+// that fp16 holds (under 65520) become 240, of which 61440 is at most 2^-4 away, as
+// half a step of the 8 bits is.  Larger scales are of rows that fp16 does not hold.
+__device__ __forceinline__ void stay_finite(float *x) {
+#pragma unroll
+    for (int e = 0; e < 8; e++)
+        if (fabsf(x[e]) < 65520.0f / 256) x[e] = fminf(fmaxf(x[e], -240.0f), 240.0f);
 }
 
 // 1 / scale where that is exact, else 0.
@@ -210,6 +221,8 @@ struct Section {
                         const float inverse = __uint_as_float((254 - exponent) << 23);
 #pragma unroll
                         for (int e = 0; e < 8; e++) x[e] *= inverse;
+                        if constexpr (std::is_same<T, __half>::value)
+                            if (exponent == 127 + 8) stay_finite(x);
                         *reinterpret_cast<uint32_t *>(o + l.da) = e4m3x4(x);
                         *reinterpret_cast<uint32_t *>(o + l.db) = e4m3x4(x + 4);
                         if (l.da == 0) a.c.pool[seg[u] + scale_place] = (uint8_t)exponent;
