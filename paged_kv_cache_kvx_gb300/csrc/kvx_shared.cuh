@@ -573,14 +573,17 @@ __device__ __forceinline__ bool walk(const Args &a, Shared &sh, const uint32_t *
             i++;
             // Those without columns, the free places of a batch, 32 at a time: one by
             // one they take 235 ns each (5 million between two sequences outlast a wait).
-            while (!e.len && i < entries) {
-                Entry x = {};
-                if (i + 1 + lane < entries) x = entry_of(a, i + 1 + lane);
-                const uint32_t some = __ballot_sync(0xFFFFFFFFu, x.len != 0);
-                i += some ? __ffs(some) : 32;
-                if (some) e = entry_of(a, i);
+            if (!e.len) {
+                do {
+                    Entry x = {};
+                    if (i + 1 + lane < entries) x = entry_of(a, i + 1 + lane);
+                    const uint32_t some = __ballot_sync(0xFFFFFFFFu, x.len != 0);
+                    i += some ? __ffs(some) : 32;
+                    if (some) break;
+                } while (i < entries);
+                if (i >= entries) break;  // (as above)
+                e = entry_of(a, i);
             }
-            if (i >= entries) break;  // (as above)
             next = Entry{};
             if (i + 1 < entries) next = entry_of(a, i + 1);
             continue;
