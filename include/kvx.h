@@ -703,8 +703,10 @@ kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t q_stride,
  * prefixes: sequence n sees first the prefix_lens[g] tokens of the group g that
  * it belongs to, whose pages are read once for all of the group's sequences,
  * and then the lens[n] tokens of its own pages.  Logits, outputs and lse are
- * those of kvx_attend over both; without groups it is kvx_attend (without
- * window, sinks and scores) over any cache, one with row scales too.
+ * defined as those of kvx_attend over both, without window, sinks and scores, and
+ * over any cache, one with row scales too; without groups it is that of own tokens
+ * alone.  Outputs are not kvx_attend's to the last bit: weights are rounded once to
+ * `dtype` here, where kvx_attend takes the sum of two values of that type.
  *
  *   q, out, lse, scale, blocks, lens  as for kvx_attend.  lens may be 0, of a
  *                  sequence that sees its prefix alone.
@@ -718,8 +720,9 @@ kvx_status kvx_attend(const kvx_cache *cache, const void *q, uint64_t q_stride,
  *                  raises KVX_S_BOUNDS and counts as full pages.
  * Tokens of a page or segment that the cache's rules exclude count as zeros.
  * Keys and values enter the tensor cores in `dtype`: 16-bit ones as they are,
- * 8-bit ones exactly (row-scaled ones in fp16 rounded to it, where they are
- * under 2^-14 or from 65520 on).  Logits, softmax and sums are held in 32 bits;
+ * 8-bit ones exactly, but row-scaled ones beyond its range as a cache of `dtype`
+ * would hold them: in fp16 values under 2^-14 are rounded to multiples of 2^-24 and
+ * those from 65520 on are infinite.  Logits, softmax and sums are held in 32 bits;
  * the weights that multiply V are rounded to `dtype`, as V and the output are.
  * An infinite value in V makes its column of the output infinite, or NaN where
  * its weight counts as 0 (in fp16 one under 2^-32 of a head's largest); in bf16
@@ -765,7 +768,9 @@ kvx_status kvx_attend_shared(const kvx_cache *cache, const void *q,
  * sequence n's tokens first[n], first[n] + 1, ...  16-bit caches are copied;
  * 8-bit values are multiplied by their scale (k_scale and v_scale, or the
  * row's) and the product is rounded once to `dtype`, to the nearest even (one
- * under 2^-122, which bf16 reaches, to 32 bits before).
+ * under 2^-122, which bf16 reaches, to 32 bits before).  One beyond `dtype` becomes
+ * infinite: in bf16 so does the 2^128 that row-scaled caches hold for values from
+ * 248 * 2^120 on.
  *
  *   blocks         [num_seqs][blocks_per_seq] uint32, as for kvx_attend; only
  *                  entries of pages that hold tokens to be read are read.

@@ -74,12 +74,6 @@ __device__ __forceinline__ Seen seen(const Args &a, uint32_t len) {
     return v;
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // ----------------------------------------------------------- tensor cores
 
 template <class T>

@@ -1,6 +1,6 @@
 // What the cache operators (kvx_append_tokens, kvx_read_tokens, kvx_attend,
 // kvx_attend_shared, kvx_evict) share: the checked kvx_cache as kernels see it,
-// and the 16-bit types' conversions.
+// the 16-bit types' conversions, and the softmaxes' exponential.
 #pragma once
 
 #include <cuda_bf16.h>
@@ -95,6 +95,12 @@ inline CacheView cache_view(const kvx_cache *c) {
 // The power of two that a row's scale byte stands for (kvx_cache.scale_offset).
 __device__ __forceinline__ float row_scale(uint32_t e) {
     return __uint_as_float(e == 255 ? 0x7FFFFFFFu : e ? e << 23 : 0x400000u);
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
 }
 
 // Pairs of 16-bit values and floats.

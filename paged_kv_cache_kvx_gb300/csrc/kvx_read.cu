@@ -8,8 +8,8 @@
 // at a time and writes 16-bit ones as whole sectors.
 //
 // Bound by HBM, each value read once and written once: eight sequences of 16,000
-// tokens, 8 heads of 128, 8-bit rows with scales into bf16, 119 us, 6650 GB/s
-// (98 % of a copy's rate); 37 sequences of up to 8000, 6 heads of 96, fp16, 52 us,
+// tokens, 8 heads of 128, 8-bit rows with scales into bf16, 120 us, 6580 GB/s
+// (97 % of a copy's rate); 37 sequences of up to 8000, 6 heads of 96, fp16, 52 us,
 // 6085 GB/s.  For one short sequence it is the launch and a chain of four loads:
 // 3.5 us.  What it takes is many warps with few loads each (two pieces a lane and
 // all 64 warps of an SM 119 us, four pieces and 48 warps 137, 40 warps 132): the
@@ -63,7 +63,9 @@ __device__ __forceinline__ uint32_t rank_of(const uint32_t *starts, uint32_t cou
 // x * scale cut off, with the last bit set where anything was lost: no border or
 // middle of 16-bit values lies between this and the product.  Rounded to 32 bits it
 // could become such a middle (1.125 * 0x1.d38e38p-1: 1.03125 in bf16 by way of 32
-// bits, 1.0234375 is nearer).  The remainder is exact from 2^-122 on.
+// bits, 1.0234375 is nearer).  The remainder is exact from 2^-122 on.  For scales that
+// need it only: eight sequences of 16,000 tokens take 121 us with such a scale; with row
+// scales 120 as they are and 122 this way, heads of 64 66 and 70.
 __device__ __forceinline__ float scaled_odd(float x, float scale) {
     const float p = __fmul_rz(x, scale);
     return fmaf(x, scale, -p) == 0 ? p : __uint_as_float(__float_as_uint(p) | 1);

@@ -527,12 +527,6 @@ __device__ __forceinline__ uint32_t instruction(uint32_t n, bool b_by_columns, b
            kRows / 16 << 24;
 }
 
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // ------------------------------------------------------------- the schedule
 
 // The walking warp: the block's share of all units' tiles, piece by piece.
@@ -1594,16 +1588,20 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
 // with tcgen05.mma: queries and tiles come from shared memory (128-byte swizzle), P
 // from tensor memory.  A block has two slots, each with its softmax warps and its
 // issuing thread, so that one's products run beside the other's softmax: of more
-// than 128 rows both take every tile, else they take tiles in turn.  Bases, sums
-// and outputs go to k_join, a row of floats each.
+// than 128 rows both take every tile, else they take tiles in turn.  Of heads wider
+// than 128, whose outputs one slot's part of tensor memory does not hold, both slots
+// take the same rows and tiles, half of V's columns each: Q K^T and its exponentials
+// are done twice.  Bases, sums and outputs go to k_join, a row of floats each.
 //
 // Weights are rounded to 16 bits for the second product (as V and the output are):
-// beside the output's own rounding that adds as much again, 1.4 times the error.
-// Their sums are of the unrounded ones.
+// beside the output's own rounding that adds as much again, 1.4 times the error
+// (kvx_attend, bound by its copies, multiplies the sum of two 16-bit weights; here
+// that would be half as many products again).  Their sums are of the unrounded ones.
 //
-// Keys and values are copied by cp.async, 16 bytes at a time: a page may lie at any
-// multiple of 16 bytes, which no tensor map describes.  8-bit rows come to a place
-// of their own and are widened with their scale on the way to the tile.
+// Keys and values are copied by cp.async, 16 bytes at a time, to where the swizzle has
+// them, from rows at any multiple of 16 bytes; copies by tensor map were not tried.
+// 8-bit rows come to a place of their own and are widened with their scale on the way
+// to the tile.
 //
 // Bound, for many rows, by the softmax and the latency from product to product (a
 // tile takes two slots 2050 clocks of the tensor cores and 3900 in all): 128 x
@@ -1611,7 +1609,9 @@ __device__ __forceinline__ bool soften(const Args &a, Shared &sh, uint32_t tmem,
 // of the measured rate of matrix products, with 490 MB of DRAM reads for 433 MB of
 // cache.  For few rows by the copies: 8 x 16,000 own tokens, bf16, 91 us at 5.8 TB/s;
 // in 8 bits by their widening, 62 instructions per 16 values, and a tile's chain:
-// 106 us at 2.5 TB/s.
+// 106 us at 2.5 TB/s.  Heads of 256, four KV heads: 8 x 16,000 own tokens 93 us, 64 x 16
+// heads over 16,000 shared ones 61 (128, eight: 90 and 57).  Threads have 96 registers,
+// of which every variant spills some (28 to 124 bytes stored, 80 to 116 loaded).
 template <class T, int DP, int ES>
 __global__ void __launch_bounds__(kThreads, 1) k_shared(const __grid_constant__ Args a) {
     using S = Shape<DP, ES>;
